@@ -363,6 +363,120 @@ USP_API int usp_backward(const void *q, const void *k, const void *v, const void
 /* Bytes of workspace usp_backward needs; 0 if the arguments are invalid. */
 USP_API size_t usp_backward_workspace_size(usp_attn_desc d, int head_chunk);
 
+/* ------------------------------------------------------------------------------------------------
+ * Paged K/V cache: what a sequence's K and V become when it goes on token by token. The pages'
+ * subject ends at the attention over a whole sequence; serving the long contexts that it makes
+ * possible needs the three calls below, which have no counterpart there.
+ *
+ * Cache layout: k_cache, v_cache [num_pages][hkv][page_size][hd] (a page holds page_size tokens of
+ * every KV head, one head's rows contiguous). The token at position p of request i lives in page
+ * block_table[i][p / page_size], row p % page_size; its slot is that page * page_size + that row.
+ * block_table: int32 [nreq][table_stride], the first max_pages columns in use.
+ * Lengths and tables are device data that only the kernels read: calls need no host copy of them and
+ * can be captured in a CUDA graph and replayed with other lengths. Values outside their range give
+ * meaningless results, never an access out of bounds: lengths are clamped to what the table and the
+ * tensors hold, and a page outside [0, num_pages) reads as zeros and is never written.
+ * ------------------------------------------------------------------------------------------------ */
+typedef struct {
+    int64_t num_pages;     /* pages in the cache; num_pages * page_size < 2^31 */
+    int64_t k_page_stride; /* elements between consecutive pages of k_cache (0: hkv * page_size * hd); */
+    int64_t v_page_stride; /* a multiple of 16 bytes, e.g. twice that in a cache that interleaves K, V */
+    int32_t page_size;     /* tokens per page: 16, 32, 64, 128 or 256 */
+    int32_t hkv;           /* KV heads */
+    int32_t hd;            /* head dim: 64 or 128 */
+    int32_t dtype;         /* usp_dtype */
+} usp_cache_dims;
+
+typedef struct {
+    int64_t num_pages;    /* pages in the cache */
+    int64_t table_stride; /* entries between consecutive rows of block_table (>= max_pages) */
+    int64_t free_count;   /* entries of free_pages */
+    int64_t max_tokens;   /* entries of slot_map, < 2^31 */
+    int32_t nreq;         /* requests */
+    int32_t max_pages;    /* columns of block_table */
+    int32_t page_size;    /* 16, 32, 64, 128 or 256 */
+} usp_plan_dims;
+
+/*
+ * usp_page_plan -- pages and slots for the next tokens of every request, from the lengths alone.
+ *   ctx_lens, new_lens : int32 [nreq]: tokens request i has in the cache, and tokens it adds now
+ *                        (either may be 0; a negative length counts as 0)
+ *   free_pages         : int32 [free_count], page ids in the order in which they are taken;
+ *   free_head          : int32 [1]: the first entry of free_pages not taken yet
+ *   block_table        : updated in place: with old_i = ceil(ctx_i / page_size), columns
+ *                        [old_i, ceil((ctx_i + new_i) / page_size)) of row i get the next entries of
+ *                        free_pages (request by request, in column order); others are left as they are
+ *   slot_map           : int32 [max_tokens]: the slot of every new token, request by request; -1
+ *                        where there is none: behind the last token, where free_pages or the table's
+ *                        columns run out, where the page is not in [0, num_pages)
+ *   cu_new             : int32 [nreq + 1]: cumulative new lengths (at most max_tokens)
+ *   kv_lens            : int32 [nreq]: ctx_i + new_i
+ *   counts             : int32 [4]: new tokens; the free head after this plan (above free_count when
+ *                        pages ran out); tokens without a slot because free_pages, the table or
+ *                        slot_map ended; the largest kv_lens entry
+ * One launch. Running it again with the same inputs gives the same outputs: to go on, the caller
+ * passes counts + 1 (of another buffer) as free_head and kv_lens as ctx_lens. Outputs must not
+ * overlap inputs (USP_ERR_INVALID_ARG where counts overlaps free_head). Pointers 4-byte aligned.
+ */
+USP_API int usp_page_plan(const int32_t *ctx_lens, const int32_t *new_lens, const int32_t *free_pages,
+                          const int32_t *free_head, int32_t *block_table, int32_t *slot_map, int32_t *cu_new,
+                          int32_t *kv_lens, int32_t *counts, usp_plan_dims d, usp_stream_t stream);
+
+/*
+ * usp_cache_append -- write the K and V rows of `tokens` tokens into the cache.
+ *   k, v       : (tokens, hkv, hd), token t at element t * k_stride / t * v_stride (0: hkv * hd), e.g.
+ *                slices of a fused projection; strides a multiple of 16 bytes
+ *   slot_map   : int32 [tokens]; a token whose slot is not in [0, num_pages * page_size) is skipped
+ * Bit-exact copy; nothing else of the cache changes. Slots must be distinct (where two tokens share
+ * one, its row may hold parts of both). k, v, k_cache, v_cache 16-byte aligned; sources must not
+ * overlap the cache.
+ */
+USP_API int usp_cache_append(const void *k, const void *v, void *k_cache, void *v_cache, const int32_t *slot_map,
+                             int64_t tokens, int64_t k_stride, int64_t v_stride, usp_cache_dims d,
+                             usp_stream_t stream);
+
+typedef struct {
+    usp_cache_dims cache;
+    int64_t tokens;       /* rows of q, out and lse; tokens * hq < 2^31 */
+    int64_t q_stride;     /* elements between consecutive tokens of q (0: hq * hd); a multiple of 16 bytes */
+    int64_t out_stride;   /* the same for out */
+    int64_t table_stride; /* entries between consecutive rows of block_table (>= max_pages) */
+    int32_t nreq;         /* requests */
+    int32_t max_pages;    /* columns of block_table */
+    int32_t hq;           /* query heads; head h reads KV head h / (hq / hkv); hq / hkv <= 128 */
+    int32_t max_new;      /* the most new tokens of one request, as far as the host knows (at most
+                             `tokens`); steers which kernels run, not what they compute: a request
+                             above it costs time, nothing else */
+    int32_t causal;       /* nonzero: a new token sees the keys up to its own position, else all */
+    float scale;          /* softmax scale; <= 0 means 1/sqrt(hd) */
+} usp_paged_desc;
+
+/*
+ * usp_paged_attn -- attention of each request's new tokens over its cached keys (the new ones among
+ * them, appended before): a chunk of a prompt, a whole prompt, or single tokens, mixed in one call.
+ *   q        : (tokens, hq, hd); rows [cu_new[i], cu_new[i + 1]) are request i's new tokens
+ *   cu_new   : int32 [nreq + 1], non-decreasing; kv_lens: int32 [nreq], keys of request i
+ *   out      : (tokens, hq, hd); lse: (tokens, hq) fp32, natural log of the softmax normaliser
+ * New token j of n_i has position kv_i - n_i + j and sees keys 0 .. that position (0 .. kv_i - 1
+ * without the causal mask). A row without a visible key gets o = 0, lse = -inf. Rows outside
+ * [cu_new[0], cu_new[nreq]) are left as they were. Cache rows behind kv_i may hold anything (NaN
+ * among it); rows a request has must be finite where some query of the call sees them: in the bf16
+ * kernels a non-finite V row reaches every query of its 128-key tile. Partials over parts of
+ * a sequence (e.g. one ring rank's keys each) merge with usp_lse_merge.
+ *   workspace : DEVICE buffer, 256-byte aligned, at least usp_paged_attn_workspace_size(d) bytes,
+ *               clobbered; calls that share it must be ordered on one stream (two captured graphs
+ *               that may run at the same time need one each). It needs no initialisation.
+ * q, out, the caches 16-byte aligned. Arithmetic: fp32 softmax statistics and sums; bf16: products on
+ * the tensor cores with the weights rounded to bf16; fp32: fp32 throughout. The result of a call does
+ * not depend on timing: the same inputs give the same bits.
+ */
+USP_API int usp_paged_attn(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_table,
+                           const int32_t *cu_new, const int32_t *kv_lens, void *out, float *lse, usp_paged_desc d,
+                           void *workspace, size_t workspace_bytes, usp_stream_t stream);
+
+/* Bytes of workspace usp_paged_attn needs on the current device; 0 if the arguments are invalid. */
+USP_API size_t usp_paged_attn_workspace_size(usp_paged_desc d);
+
 /* Synchronise `stream`, then report (and clear) the device status word of the current device:
  * USP_OK, USP_ERR_TIMEOUT, or USP_ERR_CUDA if the synchronisation itself failed. */
 USP_API int usp_check(usp_stream_t stream);

@@ -10,6 +10,7 @@ Layouts (all row-major; see include/usp.h for the index formulas):
   local              [rd][ud][bs][Lu][H][hd]             after the zigzag split (Algorithm 2)
   head-sharded       [rd][ud][H/ud][bs][Lr][hd]          after AllToAll4D
   lse (head-sharded) [rd][ud][hq/ud][bs][Lr] fp32; lse (natural) (bs, L, hq)
+  paged K/V cache    [num_pages][hkv][page_size][hd]     what a sequence goes on from, token by token
 """
 from __future__ import annotations
 
@@ -20,14 +21,15 @@ from typing import Optional
 import torch
 
 from . import _abi
-from ._abi import (USP_BF16, USP_F32, USP_MODE_ACCUM, USP_MODE_FUSED, USP_MODE_STEP, UspAttnDesc, UspDims,
-                   UspError)
+from ._abi import (USP_BF16, USP_F32, USP_MODE_ACCUM, USP_MODE_FUSED, USP_MODE_STEP, UspAttnDesc, UspCacheDims,
+                   UspDims, UspError, UspPagedDesc, UspPlanDims)
 
 __all__ = ["usp_extract_local", "usp_a2a4d", "usp_a2a4d_multi", "usp_extract_a2a", "usp_attn_fwd", "usp_lse_merge", "usp_check", "usp_attention",
            "usp_attention_host", "usp_forward", "usp_forward_host", "usp_forward_workspace_size",
            "usp_forward_noalloc", "heads_per_rank",
            "usp_attn_bwd_delta", "usp_attn_bwd", "usp_backward", "usp_backward_workspace_size", "UspAttentionFunction",
-           "UspAttention", "UspError", "USP_MODE_FUSED", "USP_MODE_STEP", "USP_MODE_ACCUM", "lib_path"]
+           "UspAttention", "usp_page_plan", "usp_cache_append", "usp_paged_attn", "usp_paged_attn_workspace_size",
+           "UspError", "USP_MODE_FUSED", "USP_MODE_STEP", "USP_MODE_ACCUM", "lib_path"]
 
 lib_path = _abi.LIB_PATH
 
@@ -514,6 +516,190 @@ class UspAttention:
     def __call__(self, q, k, v, natural_output: bool = True):
         return usp_attention(q, k, v, self.ud, self.rd, causal=self.causal, scale=self.scale,
                              head_chunk=self.head_chunk, natural_output=natural_output)
+
+
+# ---- paged K/V cache ---------------------------------------------------------------------------
+
+
+def _same_device(first: torch.Tensor, *ts):
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError("expected CUDA tensors")
+    for t in ts:
+        if t.device != dev:
+            raise ValueError(f"expected tensors on one device, got {dev} and {t.device}")
+    return dev
+
+
+def _i32(name: str, t: torch.Tensor, n: Optional[int] = None):
+    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 1-D int32 tensor")
+    if n is not None and t.numel() != n:
+        raise ValueError(f"{name} must have {n} entries, got {t.numel()}")
+
+
+def _dense_rows(name: str, t: torch.Tensor) -> int:
+    """The stride of the first axis in elements, 0 where the tensor is contiguous; what an entry of the
+    first axis holds must be contiguous."""
+    if t.is_contiguous():
+        return 0
+    if t.dim() < 2 or not t[0].is_contiguous() or t.stride(0) < t[0].numel():
+        raise ValueError(f"{name}: only the first axis may be strided")
+    return t.stride(0)
+
+
+def _cache_dims(k_cache: torch.Tensor, v_cache: torch.Tensor) -> UspCacheDims:
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must be (num_pages, hkv, page_size, hd), of one shape and dtype")
+    pages, hkv, ps, hd = k_cache.shape
+    return UspCacheDims(pages, _dense_rows("k_cache", k_cache), _dense_rows("v_cache", v_cache), ps, hkv, hd,
+                        _dtype_code(k_cache))
+
+
+def _block_table(t: torch.Tensor, nreq: int) -> int:
+    """The table's row stride; its rows must be contiguous."""
+    if t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] != nreq:
+        raise ValueError(f"block_table must be an int32 tensor of {nreq} rows")
+    return _dense_rows("block_table", t) or t.shape[1]
+
+
+def _with_stream(dev: torch.device, stream, call):
+    """call(raw stream) with the tensors' device current and, where ``stream`` is given, with it as the
+    current stream, so that what the call allocates is ordered on the stream that uses it."""
+    if stream is None:
+        if torch.cuda.current_device() == dev.index:
+            return call(torch.cuda.current_stream().cuda_stream)
+        with torch.cuda.device(dev):
+            return call(torch.cuda.current_stream().cuda_stream)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    _need(stream.device == dev, "the stream belongs to another device than the tensors")
+    with torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
+
+
+def usp_page_plan(ctx_lens, new_lens, free_pages, free_head, block_table, page_size: int, num_pages: int,
+                  max_tokens: int, slot_map=None, cu_new=None, kv_lens=None, counts=None, stream=None):
+    """Pages and slots for the next tokens of every request, from the lengths alone (all int32, on the
+    device; no host copy): ``ctx_lens[i]`` tokens are cached, ``new_lens[i]`` come now. Fresh pages are
+    taken from ``free_pages`` from entry ``free_head[0]`` on and written into ``block_table`` (in place).
+
+    Returns (slot_map, cu_new, kv_lens, counts), allocated where not given: the slot of each of up to
+    ``max_tokens`` new tokens (-1: none), cumulative new lengths, keys per request, and (new tokens, the
+    next free head, tokens left without a slot, largest kv length). The next step passes kv_lens as
+    ctx_lens and counts[1:2] as free_head, with other output tensors than its inputs."""
+    nreq = ctx_lens.numel()
+    for name, t in (("ctx_lens", ctx_lens), ("new_lens", new_lens)):
+        _i32(name, t, nreq)
+    _i32("free_pages", free_pages)
+    _i32("free_head", free_head, 1)
+    dev = _same_device(ctx_lens, new_lens, free_pages, free_head, block_table)
+    d = UspPlanDims(num_pages, _block_table(block_table, nreq), free_pages.numel(), max_tokens, nreq,
+                    block_table.shape[1], page_size)
+
+    def call(raw):
+        outs = []
+        for name, t, n in (("slot_map", slot_map, max_tokens), ("cu_new", cu_new, nreq + 1),
+                           ("kv_lens", kv_lens, nreq), ("counts", counts, 4)):
+            if t is None:
+                t = torch.empty(n, dtype=torch.int32, device=dev)
+            else:
+                _i32(name, t, n)
+                _same_device(ctx_lens, t)
+            outs.append(t)
+        _abi.check("usp_page_plan", _abi.load().usp_page_plan(
+            ctx_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), free_head.data_ptr(),
+            block_table.data_ptr(), outs[0].data_ptr(), outs[1].data_ptr(), outs[2].data_ptr(), outs[3].data_ptr(),
+            d, raw))
+        return tuple(outs)
+
+    _need(max_tokens >= 0, "max_tokens must not be negative")
+    return _with_stream(dev, stream, call)
+
+
+def usp_cache_append(k, v, k_cache, v_cache, slot_map, stream=None):
+    """Write the rows of k and v (tokens, hkv, hd) into their slots of the caches
+    (num_pages, hkv, page_size, hd), in place; a token with slot -1 is skipped. The first axis of every
+    tensor may be strided (slices of a fused projection, a cache that interleaves K and V)."""
+    tokens = k.shape[0]
+    d = _cache_dims(k_cache, v_cache)
+    if k.dim() != 3 or k.shape[1] != d.hkv or k.shape[2] != d.hd or v.shape != k.shape:
+        raise ValueError("k and v must be (tokens, hkv, hd) like the cache")
+    if k.dtype != k_cache.dtype or v.dtype != k_cache.dtype:
+        raise ValueError("dtype mismatch")
+    _i32("slot_map", slot_map, tokens)
+    dev = _same_device(k, v, k_cache, v_cache, slot_map)
+    ks, vs = _dense_rows("k", k), _dense_rows("v", v)
+    _with_stream(dev, stream, lambda raw: _abi.check("usp_cache_append", _abi.load().usp_cache_append(
+        k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), slot_map.data_ptr(), tokens, ks, vs, d,
+        raw)))
+    return k_cache, v_cache
+
+
+def _paged_desc(q, k_cache, v_cache, block_table, nreq, max_new, causal, scale, out):
+    d = _cache_dims(k_cache, v_cache)
+    if q.dim() != 3 or q.shape[2] != d.hd or q.dtype != k_cache.dtype:
+        raise ValueError("q must be (tokens, hq, hd), of the cache's head dim and dtype")
+    T, hq, _ = q.shape
+    if out is not None and (out.shape != q.shape or out.dtype != q.dtype):
+        raise ValueError("out must match q")
+    stride = _block_table(block_table, nreq)
+    return UspPagedDesc(d, T, _dense_rows("q", q), 0 if out is None else _dense_rows("out", out), stride, nreq,
+                        block_table.shape[1], hq, T if max_new is None else max_new, int(bool(causal)),
+                        0.0 if scale is None else scale)
+
+
+def usp_paged_attn_workspace_size(q, k_cache, block_table, max_new: Optional[int] = None) -> int:
+    """Workspace bytes usp_paged_attn needs for these shapes (on q's device)."""
+    d = _paged_desc(q, k_cache, k_cache, block_table, block_table.shape[0], max_new, True, None, None)
+    with torch.cuda.device(q.device):
+        n = _abi.load().usp_paged_attn_workspace_size(d)
+    _need(n > 0, "invalid paged attention shapes")
+    return int(n)
+
+
+def usp_paged_attn(q, k_cache, v_cache, block_table, cu_new, kv_lens, max_new: Optional[int] = None,
+                   causal: bool = True, scale: Optional[float] = None, out=None, lse=None, workspace=None,
+                   stream=None):
+    """Attention of every request's new tokens over its cached keys (its new ones among them): chunks,
+    whole prompts and single tokens in one call. q (tokens, hq, hd), rows [cu_new[i], cu_new[i+1]) of
+    request i; caches (num_pages, hkv, page_size, hd); block_table (nreq, pages); kv_lens[i] keys.
+    Returns (out, lse): (tokens, hq, hd) and fp32 (tokens, hq); rows of no request are left as they
+    were (unset where the call allocates them). ``max_new``: the most new tokens of one request, where
+    the host knows it (1 for a decode step); it saves launches and does not change the result.
+    ``workspace``: at least usp_paged_attn_workspace_size bytes (allocated per call where not given)."""
+    nreq = kv_lens.numel()
+    _i32("cu_new", cu_new, nreq + 1)
+    _i32("kv_lens", kv_lens)
+    d = _paged_desc(q, k_cache, v_cache, block_table, nreq, max_new, causal, scale, out)
+    dev = _same_device(q, k_cache, v_cache, block_table, cu_new, kv_lens)
+    T, hq = q.shape[0], q.shape[1]
+
+    def call(raw):
+        lib = _abi.load()
+        o, l, w = out, lse, workspace
+        if o is None:
+            o = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        else:
+            _same_device(q, o)
+        if l is None:
+            l = torch.empty((T, hq), dtype=torch.float32, device=dev)
+        else:
+            _need(l.shape == (T, hq) and l.dtype == torch.float32 and l.is_contiguous(),
+                  "lse must be contiguous fp32 (tokens, hq)")
+            _same_device(q, l)
+        if w is None:
+            n = lib.usp_paged_attn_workspace_size(d)
+            w = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
+        else:
+            _need(w.is_contiguous(), "workspace must be contiguous")
+            _same_device(q, w)
+        _abi.check("usp_paged_attn", lib.usp_paged_attn(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), cu_new.data_ptr(),
+            kv_lens.data_ptr(), o.data_ptr(), l.data_ptr(), d, w.data_ptr(), w.numel() * w.element_size(), raw))
+        return o, l
+
+    return _with_stream(dev, stream, call)
 
 
 def default_scale(hd: int) -> float:

@@ -45,6 +45,25 @@ class UspAttnDesc(ctypes.Structure):
                 ("nseq", ctypes.c_int32), ("cu_seqlens", ctypes.c_void_p)]
 
 
+class UspCacheDims(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int64), ("k_page_stride", ctypes.c_int64), ("v_page_stride", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("hkv", ctypes.c_int32), ("hd", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class UspPlanDims(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int64), ("table_stride", ctypes.c_int64), ("free_count", ctypes.c_int64),
+                ("max_tokens", ctypes.c_int64), ("nreq", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32)]
+
+
+class UspPagedDesc(ctypes.Structure):
+    _fields_ = [("cache", UspCacheDims), ("tokens", ctypes.c_int64), ("q_stride", ctypes.c_int64),
+                ("out_stride", ctypes.c_int64), ("table_stride", ctypes.c_int64), ("nreq", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("hq", ctypes.c_int32), ("max_new", ctypes.c_int32),
+                ("causal", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
 class UspError(RuntimeError):
     def __init__(self, fn, status, text):
         super().__init__(f"{fn} failed: {text} (status {status})")
@@ -96,6 +115,14 @@ def load():
     lib.usp_backward_workspace_size.restype = ctypes.c_size_t
     lib.usp_lse_merge.argtypes = [vp, vp, vp, vp, i64, i32, i32, vp]
     lib.usp_lse_merge.restype = ctypes.c_int
+    lib.usp_page_plan.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, UspPlanDims, vp]
+    lib.usp_page_plan.restype = ctypes.c_int
+    lib.usp_cache_append.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, UspCacheDims, vp]
+    lib.usp_cache_append.restype = ctypes.c_int
+    lib.usp_paged_attn.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, UspPagedDesc, vp, ctypes.c_size_t, vp]
+    lib.usp_paged_attn.restype = ctypes.c_int
+    lib.usp_paged_attn_workspace_size.argtypes = [UspPagedDesc]
+    lib.usp_paged_attn_workspace_size.restype = ctypes.c_size_t
     lib.usp_check.argtypes = [vp]
     lib.usp_check.restype = ctypes.c_int
     lib.usp_selftest_timeout.argtypes = [i64, vp]

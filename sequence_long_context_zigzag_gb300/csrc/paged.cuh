@@ -1,0 +1,37 @@
+// paged.cuh -- what the paged K/V cache's translation units share (not part of the ABI).
+#pragma once
+
+#include "usp_internal.cuh"
+
+namespace usp {
+
+inline bool valid_page_size(int32_t ps) { return ps >= 16 && ps <= 256 && (ps & (ps - 1)) == 0; }
+
+int check_cache_dims(const usp_cache_dims &d);
+
+// usp_paged_attn's arguments, checked and with the defaults filled in (strides in elements)
+struct PagedArgs {
+    const void *q, *k, *v;
+    const int32_t *table, *cu, *kv;
+    void *out;
+    float *lse;
+    int64_t tokens, q_stride, out_stride, table_stride, num_pages, k_page, v_page;
+    int32_t nreq, max_pages, max_new, hq, hkv, G, hd, log_ps, causal;
+    float scale_log2;  // softmax scale * log2(e)
+};
+
+// The new tokens [t0, t0 + n) and keys of request i, clamped to what the tensors and the table hold.
+struct Request {
+    int64_t t0;
+    int32_t n, kv;
+};
+__device__ __forceinline__ Request paged_request(const int32_t *cu, const int32_t *kv, int32_t i, int64_t tokens,
+                                                 int64_t max_keys) {
+    const int64_t a = min(max((int64_t)__ldg(cu + i), (int64_t)0), tokens);
+    const int64_t b = min(max((int64_t)__ldg(cu + i + 1), a), tokens);
+    return Request{a, (int32_t)(b - a), (int32_t)min(max((int64_t)__ldg(kv + i), (int64_t)0), max_keys)};
+}
+
+int launch_paged_simt(const PagedArgs &a, int dtype, cudaStream_t s);
+
+}  // namespace usp

@@ -246,3 +246,134 @@ def test_packed_samples_rejects():
     assert lib.usp_attn_fwd(BAD, BAD, BAD, BAD, BAD, desc(nseq=3, cu_seqlens=0x1000), None) == _abi.USP_ERR_ALIGN
     assert lib.usp_attn_bwd(*([BAD] * 9), desc(nseq=3, cu_seqlens=None), None) == _abi.USP_ERR_INVALID_ARG
     assert lib.usp_attn_bwd(*([BAD] * 9), desc(nseq=3, cu_seqlens=0x1000), None) == _abi.USP_ERR_ALIGN
+
+
+def cache(**kw):
+    base = dict(num_pages=8, k_page_stride=0, v_page_stride=0, page_size=16, hkv=2, hd=128, dtype=_abi.USP_BF16)
+    base.update(kw)
+    return _abi.UspCacheDims(*[base[f] for f, _ in _abi.UspCacheDims._fields_])
+
+
+GOOD = 0x1000  # aligned, never dereferenced
+BAD_CACHES = [
+    (dict(num_pages=-1), _abi.USP_ERR_INVALID_ARG),
+    (dict(hkv=0), _abi.USP_ERR_INVALID_ARG),
+    (dict(dtype=7), _abi.USP_ERR_DTYPE),
+    (dict(hd=96), _abi.USP_ERR_UNSUPPORTED),
+    (dict(page_size=8), _abi.USP_ERR_UNSUPPORTED),
+    (dict(page_size=48), _abi.USP_ERR_UNSUPPORTED),
+    (dict(page_size=512), _abi.USP_ERR_UNSUPPORTED),
+    (dict(num_pages=2 ** 27), _abi.USP_ERR_UNSUPPORTED),          # 2^31 slots
+    (dict(k_page_stride=2 * 16 * 128 - 8), _abi.USP_ERR_SHAPE),   # shorter than a page
+    (dict(v_page_stride=2 * 16 * 128 + 4), _abi.USP_ERR_ALIGN),   # 8 bytes off
+]
+
+
+@pytest.mark.parametrize("kw,code", BAD_CACHES)
+def test_cache_append_rejects_caches(kw, code):
+    assert _abi.load().usp_cache_append(GOOD, GOOD, GOOD, GOOD, GOOD, 4, 0, 0, cache(**kw), None) == code
+
+
+def test_cache_append_rejects():
+    f = _abi.load().usp_cache_append
+    five = [GOOD] * 5
+    assert f(*five, -1, 0, 0, cache(), None) == _abi.USP_ERR_INVALID_ARG
+    assert f(*five, 4, 255, 0, cache(), None) == _abi.USP_ERR_SHAPE
+    assert f(*five, 4, 0, 260, cache(), None) == _abi.USP_ERR_ALIGN
+    assert f(*five, 2 ** 27, 0, 0, cache(), None) == _abi.USP_ERR_UNSUPPORTED
+    for i in range(5):
+        assert f(*five[:i], None, *five[i + 1:], 4, 0, 0, cache(), None) == _abi.USP_ERR_INVALID_ARG
+        bad = BAD + 1 if i == 4 else BAD
+        assert f(*five[:i], bad, *five[i + 1:], 4, 0, 0, cache(), None) == _abi.USP_ERR_ALIGN
+    assert f(None, None, None, None, None, 0, 0, 0, cache(), None) == _abi.USP_OK
+
+
+def plan(**kw):
+    base = dict(num_pages=8, table_stride=4, free_count=4, max_tokens=32, nreq=2, max_pages=4, page_size=16)
+    base.update(kw)
+    return _abi.UspPlanDims(*[base[f] for f, _ in _abi.UspPlanDims._fields_])
+
+
+def test_page_plan_rejects():
+    f = _abi.load().usp_page_plan
+    nine = [0x10000 * (i + 1) for i in range(9)]
+    for kw, code in [(dict(nreq=-1), _abi.USP_ERR_INVALID_ARG), (dict(max_tokens=-1), _abi.USP_ERR_INVALID_ARG),
+                     (dict(free_count=-1), _abi.USP_ERR_INVALID_ARG), (dict(page_size=24), _abi.USP_ERR_UNSUPPORTED),
+                     (dict(table_stride=3), _abi.USP_ERR_SHAPE), (dict(max_tokens=2 ** 31), _abi.USP_ERR_UNSUPPORTED),
+                     (dict(num_pages=2 ** 27), _abi.USP_ERR_UNSUPPORTED)]:
+        assert f(*nine, plan(**kw), None) == code
+    for i in range(9):
+        assert f(*nine[:i], None, *nine[i + 1:], plan(), None) == _abi.USP_ERR_INVALID_ARG
+        assert f(*nine[:i], nine[i] + 2, *nine[i + 1:], plan(), None) == _abi.USP_ERR_ALIGN
+    # outputs over inputs: counts over the head, kv_lens over ctx_lens, cu_new into new_lens' last entry
+    assert f(*nine[:8], nine[3] - 4, plan(), None) == _abi.USP_ERR_INVALID_ARG
+    assert f(*nine[:7], nine[0], nine[8], plan(), None) == _abi.USP_ERR_INVALID_ARG
+    assert f(*nine[:6], nine[1] + 4, *nine[7:], plan(), None) == _abi.USP_ERR_INVALID_ARG
+
+
+def paged(cache_kw=None, **kw):
+    base = dict(cache=cache(**(cache_kw or {})), tokens=4, q_stride=0, out_stride=0, table_stride=4, nreq=2,
+                max_pages=4, hq=8, max_new=4, causal=1, scale=0.0)
+    base.update(kw)
+    return _abi.UspPagedDesc(*[base[f] for f, _ in _abi.UspPagedDesc._fields_])
+
+
+PAGED_BAD = [
+    (dict(tokens=-1), _abi.USP_ERR_INVALID_ARG), (dict(nreq=-1), _abi.USP_ERR_INVALID_ARG),
+    (dict(max_new=-1), _abi.USP_ERR_INVALID_ARG), (dict(hq=0), _abi.USP_ERR_INVALID_ARG),
+    (dict(scale=float("inf")), _abi.USP_ERR_INVALID_ARG), (dict(scale=float("nan")), _abi.USP_ERR_INVALID_ARG),
+    (dict(hq=7), _abi.USP_ERR_SHAPE), (dict(table_stride=3), _abi.USP_ERR_SHAPE),
+    (dict(q_stride=1000), _abi.USP_ERR_SHAPE), (dict(out_stride=1028), _abi.USP_ERR_ALIGN),
+    (dict(hq=258), _abi.USP_ERR_UNSUPPORTED), (dict(tokens=2 ** 28), _abi.USP_ERR_UNSUPPORTED),
+]
+
+
+@pytest.mark.parametrize("kw,code", PAGED_BAD)
+def test_paged_attn_rejects(kw, code):
+    lib = _abi.load()
+    assert lib.usp_paged_attn(*([GOOD] * 8), paged(**kw), GOOD, 2 ** 30, None) == code
+    assert lib.usp_paged_attn_workspace_size(paged(**kw)) == 0
+
+
+@pytest.mark.parametrize("kw,code", BAD_CACHES)
+def test_paged_attn_rejects_caches(kw, code):
+    assert _abi.load().usp_paged_attn(*([GOOD] * 8), paged(kw), GOOD, 2 ** 30, None) == code
+
+
+def test_paged_attn_rejects_pointers_and_workspace():
+    f = _abi.load().usp_paged_attn
+    eight = [GOOD] * 8
+    for i in range(8):
+        assert f(*eight[:i], None, *eight[i + 1:], paged(), GOOD, 2 ** 30, None) == _abi.USP_ERR_INVALID_ARG
+        assert f(*eight[:i], BAD + 1, *eight[i + 1:], paged(), GOOD, 2 ** 30, None) == _abi.USP_ERR_ALIGN
+    assert f(*eight, paged(), None, 2 ** 30, None) == _abi.USP_ERR_INVALID_ARG
+    assert f(*eight, paged(), GOOD + 128, 2 ** 30, None) == _abi.USP_ERR_ALIGN
+    assert f(*eight, paged(), GOOD, 0, None) == _abi.USP_ERR_INVALID_ARG
+    assert f(*([None] * 8), paged(tokens=0), None, 0, None) == _abi.USP_OK
+    assert f(*([None] * 8), paged(nreq=0), None, 0, None) == _abi.USP_OK
+
+
+def test_paged_binding_rejects():
+    import torch
+    i = torch.zeros(3, dtype=torch.int32)
+    t = torch.zeros(2, 4, dtype=torch.int32)
+    c = torch.zeros(8, 2, 16, 64, dtype=torch.bfloat16)
+    q = torch.zeros(4, 4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        usp.usp_paged_attn(q, c, c, t, i, i[:2])
+    with pytest.raises(ValueError, match="3 entries"):
+        usp.usp_paged_attn(q, c, c, t, i[:2], i[:2])
+    with pytest.raises(ValueError, match="head dim"):
+        usp.usp_paged_attn(q.float(), c, c, t, i, i[:2])
+    with pytest.raises(ValueError, match="first axis"):
+        usp.usp_paged_attn(q.transpose(0, 1), c, c, t, i, i[:2])
+    with pytest.raises(ValueError, match="rows"):
+        usp.usp_paged_attn(q, c, c, t[:1], i, i[:2])
+    with pytest.raises(ValueError, match="CUDA"):
+        usp.usp_cache_append(q[:, :2], q[:, :2], c, c, torch.zeros(4, dtype=torch.int32))
+    with pytest.raises(ValueError, match="like the cache"):
+        usp.usp_cache_append(q, q, c, c, torch.zeros(4, dtype=torch.int32))
+    with pytest.raises(ValueError, match="int32"):
+        usp.usp_page_plan(i.long(), i, i, i[:1], t, 16, 8, 4)
+    with pytest.raises(ValueError, match="CUDA"):
+        usp.usp_page_plan(i[:2], i[:2], i, i[:1], t, 16, 8, 4)

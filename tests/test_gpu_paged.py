@@ -1,0 +1,322 @@
+"""The paged K/V cache: page plan, cache append and the attention over the cache, against plain 64-bit
+definitions with bounds derived from the roundings the kernels make (tests/paged_ref.py)."""
+import math
+import random
+
+import pytest
+import torch
+
+import sequence_long_context_zigzag_gb300 as usp
+from paged_ref import Cache, check_attention, plan_ref
+
+pytestmark = pytest.mark.gpu
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+# ---- plan ----------------------------------------------------------------------------------------
+def run_plan(ctx, new, free, head, table, ps, num_pages, max_tokens):
+    t = i32(table).view(len(ctx), -1)
+    outs = usp.usp_page_plan(i32(ctx), i32(new), i32(free), i32([head]), t, ps, num_pages, max_tokens)
+    usp.usp_check()
+    got = [t.tolist()] + [x.tolist() for x in outs]
+    want = plan_ref(ctx, new, free, head, table, ps, num_pages, max_tokens)
+    for name, g, w in zip(("table", "slots", "cu", "kv", "counts"), got, want):
+        assert list(g) == list(w), name
+
+
+def random_plan(nreq, ctx_hi, new_hi, ps, seed, spare=0, width_less=0, tokens_more=0):
+    r = random.Random(seed)
+    ctx = [r.choice([0, r.randint(0, ctx_hi), ps * r.randint(0, ctx_hi // ps)]) for _ in range(nreq)]
+    new = [r.choice([0, 1, r.randint(0, new_hi)]) for _ in range(nreq)]
+    old = [-(-c // ps) for c in ctx]
+    every = [-(-(c + n) // ps) for c, n in zip(ctx, new)]
+    num = sum(every) + 7
+    ids = list(range(num))
+    r.shuffle(ids)
+    width = max(max(every) - width_less, 1)
+    table, at = [], 0
+    for o in old:
+        row = ids[at:at + o][:width]
+        at += o
+        table.append(row + [-7] * (width - len(row)))
+    fresh = sum(every) - sum(old)
+    free = [99999] * 2 + ids[at:at + max(0, fresh + spare)]
+    return ctx, new, free, 2, table, ps, num, max(0, sum(new) + tokens_more)
+
+
+@pytest.mark.parametrize("nreq,ctx_hi,new_hi,ps", [(1, 40, 3, 16), (3, 0, 70, 16), (64, 900, 1, 64), (64, 900, 200, 32),
+                                                   (256, 3000, 64, 128), (1500, 50, 9, 16), (2049, 600, 3, 256)])
+def test_plan_matches_definition(nreq, ctx_hi, new_hi, ps):
+    run_plan(*random_plan(nreq, ctx_hi, new_hi, ps, seed=nreq, spare=3))
+
+
+@pytest.mark.parametrize("spare,width_less,tokens_more", [(-3, 0, 0), (0, 2, 0), (0, 0, 300), (0, 0, -5), (-100000, 1, 11)])
+def test_plan_shortages(spare, width_less, tokens_more):
+    """Pages, columns or slots that run out: -1 slots, counted; everything else as it would be."""
+    run_plan(*random_plan(70, 500, 40, 16, seed=9, spare=spare, width_less=width_less, tokens_more=tokens_more))
+
+
+def test_plan_odd_values():
+    run_plan([5, -3, 0, 20], [-1, 4, 0, 13], [3, 1, 2, 9, -4, 77], 0, [[50, 51, 52, 53]] * 4, 16, 60, 40)
+    run_plan([0], [1000], list(range(100)), 0, [[-1] * 70], 16, 10, 1000)  # page ids at and above num_pages
+    run_plan([0, 0], [0, 0], [], 0, [[-1], [-1]], 16, 4, 0)
+
+
+def test_plan_runs_again_and_goes_on():
+    """The same inputs give the same outputs, and the outputs are the next step's inputs."""
+    r = random.Random(3)
+    ps, nreq, width = 16, 20, 30
+    free = list(range(400))
+    r.shuffle(free)
+    ctx, table, head = [0] * nreq, [[-1] * width for _ in range(nreq)], 0
+    d_ctx, d_table, d_head, d_free = i32(ctx), i32(table), i32([0]), i32(free)
+    for step in range(4):
+        new = [r.choice([0, 1, r.randint(0, 60)]) for _ in range(nreq)]
+        a = usp.usp_page_plan(d_ctx, i32(new), d_free, d_head, d_table, ps, 400, sum(new) + 3)
+        b = usp.usp_page_plan(d_ctx, i32(new), d_free, d_head, d_table, ps, 400, sum(new) + 3)
+        usp.usp_check()
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+        table, slots, cu, kv, counts = plan_ref(ctx, new, free, head, table, ps, 400, sum(new) + 3)
+        assert d_table.tolist() == table and a[0].tolist() == slots and a[3].tolist() == counts
+        d_ctx, d_head, ctx, head = a[2], a[3][1:2], kv, counts[1]
+
+
+# ---- append ---------------------------------------------------------------------------------------
+@pytest.mark.parametrize("tokens,hkv,hd,ps,dt", [(1, 1, 64, 16, torch.bfloat16), (77, 8, 128, 64, torch.bfloat16),
+                                                 (1001, 3, 64, 32, torch.float32), (5000, 2, 128, 256, torch.float32),
+                                                 (40000, 8, 128, 16, torch.bfloat16)])
+@pytest.mark.parametrize("strided", [False, True])
+def test_append_is_a_bit_exact_scatter(tokens, hkv, hd, ps, dt, strided):
+    g = torch.Generator().manual_seed(tokens)
+    pages = -(-tokens // ps) + 4
+    slots = torch.randperm(pages * ps, generator=g)[:tokens].to(torch.int32)
+    slots[torch.rand(tokens, generator=g) < 0.1] = -1
+    if tokens > 3:
+        slots[1], slots[2] = pages * ps, 2 ** 31 - 1      # one past the cache, and far past it
+    row = hkv * hd
+    both = torch.randn(tokens, 2 * row + (16 if strided else 0), generator=g).to(dt).cuda()
+    k, v = both[:, :row].unflatten(1, (hkv, hd)), both[:, row:2 * row].unflatten(1, (hkv, hd))
+    buf = torch.randn(pages, 2, hkv, ps, hd, generator=g).to(dt).cuda()
+    kc, vc = buf[:, 0], buf[:, 1]
+    if not strided:
+        k, v, kc, vc = k.contiguous(), v.contiguous(), kc.contiguous(), vc.contiguous()
+    want_k, want_v = kc.clone(), vc.clone()
+    ok = (slots >= 0) & (slots < pages * ps)
+    page, at = (slots[ok] // ps).long().cuda(), (slots[ok] % ps).long().cuda()
+    want_k[page, :, at], want_v[page, :, at] = k[ok.cuda()], v[ok.cuda()]
+    usp.usp_cache_append(k, v, kc, vc, slots.cuda())
+    usp.usp_check()
+    assert torch.equal(kc, want_k) and torch.equal(vc, want_v)
+
+
+# ---- attention ------------------------------------------------------------------------------------
+DECODE = [(1, 1), (17, 1), (64, 1), (65, 1), (0, 0), (300, 1), (0, 1), (1000, 1), (5, 0), (128, 1)]
+CHUNKS = [(1, 1), (130, 130), (129, 2), (300, 257), (0, 0), (700, 64), (65, 65), (1000, 1), (400, 33)]
+# fewer keys than new tokens: the first rows see nothing
+SHORT = [(3, 40), (0, 7), (200, 300), (1, 2)]
+
+
+def attend(c, **kw):
+    # poisoned outputs: every row of a request has to be written
+    kw.setdefault("out", torch.full_like(c.q.contiguous(), float("nan")))
+    kw.setdefault("lse", torch.full(c.q.shape[:2], float("nan"), device="cuda"))
+    r = usp.usp_paged_attn(*c.args(), **kw)
+    usp.usp_check()
+    return r
+
+
+@pytest.mark.parametrize("reqs", [DECODE, CHUNKS, SHORT, [(4000, 1)], [(3001, 500)], [(257, 257)]],
+                         ids=["decode", "chunks", "short", "one-decode", "one-chunk", "one-prompt"])
+@pytest.mark.parametrize("hq,hkv,hd,ps,dt", [
+    (8, 2, 128, 16, torch.bfloat16), (4, 4, 64, 64, torch.bfloat16), (8, 1, 128, 128, torch.bfloat16),
+    (10, 2, 64, 32, torch.bfloat16), (7, 1, 128, 256, torch.bfloat16), (32, 1, 64, 16, torch.bfloat16),
+    (128, 1, 128, 64, torch.bfloat16), (4, 2, 64, 16, torch.float32), (3, 1, 128, 256, torch.float32),
+    (16, 1, 64, 32, torch.float32)])
+def test_attention_matches_definition(reqs, hq, hkv, hd, ps, dt):
+    c = Cache(reqs, hq, hkv, hd, ps, dt, seed=hq + hd)
+    out, lse = attend(c, max_new=c.max_new)
+    check_attention(c, out, lse)
+    # without the host's bound, and with one that is too small: the same definition
+    for m in (None, 1):
+        out, lse = attend(c, max_new=m)
+        check_attention(c, out, lse)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("reqs", [DECODE, CHUNKS, SHORT], ids=["decode", "chunks", "short"])
+def test_attention_without_the_causal_mask(reqs, dt):
+    c = Cache(reqs, 8, 2, 64, 32, dt, seed=1)
+    out, lse = attend(c, causal=False, scale=0.3)
+    check_attention(c, out, lse, causal=False, scale=0.3)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("reqs", [DECODE, CHUNKS], ids=["decode", "chunks"])
+def test_attention_strides_and_foreign_rows(reqs, dt):
+    """q and out as slices of wider rows, an interleaved cache, a wider table; rows of no request and the
+    columns beside out keep their bytes."""
+    c = Cache(reqs, 8, 2, 128, 16, dt, seed=2, interleave=True, qpad=64)
+    T, hq, hd = c.q.shape
+    wide = torch.full((T + 9, hq * hd + 32), 7.0, dtype=dt, device="cuda")
+    q = torch.full((T + 9, hq * hd + 64), float("nan"), dtype=dt, device="cuda")
+    q[4:4 + T, :hq * hd] = c.q.flatten(1)
+    lse = torch.full((T + 9, hq), 7.0, device="cuda")
+    table = torch.full((c.table.shape[0], c.table.shape[1] + 5), 2 ** 30, dtype=torch.int32, device="cuda")
+    table[:, :c.table.shape[1]] = c.table
+    out = wide[:, :hq * hd].unflatten(1, (hq, hd))
+    usp.usp_paged_attn(q[:, :hq * hd].unflatten(1, (hq, hd)), c.k_cache, c.v_cache, table[:, :c.table.shape[1]],
+                       c.cu + 4, c.kv, out=out, lse=lse)
+    usp.usp_check()
+    check_attention(c, out[4:4 + T], lse[4:4 + T])
+    assert (wide[:4] == 7).all() and (wide[4 + T:] == 7).all() and (wide[:, hq * hd:] == 7).all()
+    assert (lse[:4] == 7).all() and (lse[4 + T:] == 7).all()
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("new", [1, 150])
+def test_attention_pages_outside_the_cache_read_as_zeros(dt, new):
+    """Wrong page ids and lengths past the table: no fault; such pages hold zero keys and values."""
+    c = Cache([(600, new), (90, 1)], 4, 2, 64, 32, dt, seed=3)
+    bad = {1: -1, 4: c.k_cache.shape[0], 6: 2 ** 31 - 1, 7: -2 ** 31}
+    for col, page in bad.items():
+        c.table[0, col] = page
+        c.k[0][col * 32:(col + 1) * 32] = 0
+        c.v[0][col * 32:(col + 1) * 32] = 0
+    out, lse = attend(c)
+    check_attention(c, out, lse)
+    width = c.table.shape[1]
+    c.kv[1] = 2 ** 31 - 1                      # more keys than the table has room for
+    c.table[1] = c.table[0]
+    c.table[1, -1] = 0
+    out, lse = attend(c)
+    assert out.shape == c.q.shape and width * 32 >= 600
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_attention_many_requests(dt):
+    r = random.Random(4)
+    reqs = [(k, min(k, r.choice([0, 1, 1, 1, 2, 30]))) for k in (r.choice([0, 1, 16, 33, 90]) for _ in range(2500))]
+    c = Cache(reqs, 4, 2, 64, 16, dt, seed=4)
+    out, lse = attend(c)
+    check_attention(c, out, lse)
+
+
+def test_attention_peaked_and_large_scores():
+    """Scores up to some hundred: one key takes all the weight, and the running maximum keeps moving."""
+    for dt in (torch.bfloat16, torch.float32):
+        c = Cache([(900, 1), (500, 200), (64, 64)], 8, 2, 128, 64, dt, seed=5)
+        c.q.mul_(24)
+        out, lse = attend(c)
+        check_attention(c, out, lse)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_attention_same_bits_on_every_run(dt):
+    c = Cache([(5000, 1), (3000, 300), (40, 40), (2500, 1)], 8, 2, 128, 16, dt, seed=6)
+    a = [x.clone() for x in attend(c)]
+    for _ in range(3):
+        b = attend(c)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_attention_on_another_stream_and_in_a_graph():
+    """On a side stream with the call's own allocations; captured, and replayed with other lengths."""
+    c = Cache([(700, 1), (90, 1), (1300, 1)], 8, 2, 128, 16, torch.bfloat16, seed=7)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out, lse = usp.usp_paged_attn(*c.args(), max_new=1, stream=s)
+    s.synchronize()
+    check_attention(c, out, lse)
+    out2, lse2 = usp.usp_paged_attn(*c.args(), max_new=1, stream=s.cuda_stream)
+    s.synchronize()
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        go, gl = usp.usp_paged_attn(*c.args(), max_new=1)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(go, out) and torch.equal(gl, lse)
+    c.kv.copy_(i32([650, 1, 1300]))
+    for i, kv in enumerate((650, 1, 1300)):
+        c.reqs[i] = (kv, 1)
+        c.k[i], c.v[i] = c.k[i][:kv], c.v[i][:kv]
+    g.replay()
+    torch.cuda.synchronize()
+    check_attention(c, go, gl)
+
+
+# ---- together -------------------------------------------------------------------------------------
+@pytest.mark.parametrize("hq,hkv,hd,ps,dt", [(8, 2, 128, 64, torch.bfloat16), (4, 4, 64, 16, torch.float32)])
+def test_prompt_chunks_and_tokens_through_the_cache(hq, hkv, hd, ps, dt):
+    """A serving loop: prompts in chunks, then token by token; plan, append, attention each step. Every
+    step agrees with the definition, and the whole of it with usp_forward over the finished sequences."""
+    from paged_ref import HALF_STEP, attention64
+    g = torch.Generator().manual_seed(8)
+    L = [520, 300]
+    nreq, num = 2, 64
+    r = [[torch.randn(n, h, hd, generator=g).to(dt).cuda() for h in (hq, hkv, hkv)] for n in L]
+    kc = torch.full((num, hkv, ps, hd), float("nan"), dtype=dt, device="cuda")
+    vc = kc.clone()
+    table = torch.full((nreq, 40), -1, dtype=torch.int32, device="cuda")
+    free = torch.randperm(num, generator=g).to(torch.int32).cuda()
+    head, ctx = i32([0]), i32([0, 0])
+    outs, lses, at = [[], []], [[], []], [0, 0]
+    steps = [[257, 100], [200, 0], [60, 199]] + [[1, 1]] + [[1, 0]] * 2
+    for new in steps:
+        T = sum(new)
+        q, k, v = [torch.cat([r[i][x][at[i]:at[i] + new[i]] for i in range(nreq)]) for x in range(3)]
+        slots, cu, kv, counts = usp.usp_page_plan(ctx, i32(new), free, head, table, ps, num, T + 5)
+        usp.usp_cache_append(k, v, kc, vc, slots[:T])
+        o, z = usp.usp_paged_attn(q, kc, vc, table, cu, kv, max(new))
+        usp.usp_check()
+        assert counts.tolist()[0] == T and counts.tolist()[2] == 0
+        t = 0
+        for i in range(nreq):
+            outs[i].append(o[t:t + new[i]])
+            lses[i].append(z[t:t + new[i]])
+            at[i] += new[i]
+            t += new[i]
+        ctx, head = kv, counts[1:2]
+    assert at == L
+
+    class Whole:
+        reqs, q, T = [(n, n) for n in L], torch.cat([x[0] for x in r]), sum(L)
+        k, v = [x[1] for x in r], [x[2] for x in r]
+    Whole.hq, Whole.hkv, Whole.hd, Whole.dtype = hq, hkv, hd, dt
+    out, lse = torch.cat(outs[0] + outs[1]), torch.cat(lses[0] + lses[1])
+    check_attention(Whole, out, lse)
+    _, _, bo, bl = attention64(Whole)
+    t = 0
+    for i, n in enumerate(L):
+        fo, fl = usp.usp_attention(*[x[None] for x in r[i]], ud=1, rd=1)
+        usp.usp_check()
+        # two computations, each within its bound of the definition
+        assert ((fo[0].double() - out[t:t + n].double()).abs() <= 2 * bo[t:t + n] + HALF_STEP[dt]).all()
+        assert ((fl[0].double() - lse[t:t + n].double()).abs() <= 2 * bl[t:t + n] + 1e-5).all()
+        t += n
+
+
+def test_parts_of_a_sequence_merge():
+    """Two caches with half of the keys each: the partials merge (usp_lse_merge) to the whole."""
+    c = Cache([(1000, 1), (640, 1)], 8, 2, 128, 64, torch.float32, seed=9)
+    parts = []
+    for lo, hi in ((0, 320), (320, None)):
+        kv = i32([len(c.k[i][lo:hi]) for i in range(2)])
+        table = c.table[:, lo // 64:].contiguous() if lo else c.table
+        o, z = usp.usp_paged_attn(c.q, c.k_cache, c.v_cache, table, c.cu, kv, 1, causal=False)
+        parts.append((o, z))
+    usp.usp_lse_merge(parts[0][0], parts[0][1], parts[1][0], parts[1][1])
+    usp.usp_check()
+    # the merge adds a few roundings of its own (weights and products in fp32)
+    class Both:
+        pass
+    o, z = parts[0]
+    from paged_ref import attention64
+    ref, lref, bo, bl = attention64(c, causal=False)
+    assert ((o.double() - ref).abs() <= 3 * bo + 2.0 ** -20 * ref.abs()).all()
+    assert ((z.double() - lref).abs() <= 3 * bl + 2.0 ** -20).all()
+    assert math.isfinite(z.sum().item())
