@@ -1,7 +1,10 @@
 // paged_attn.cu -- usp_paged_attn: argument checks and dispatch.
+#include <limits.h>
 #include <math.h>
 
-#include "paged.cuh"
+#include <algorithm>
+
+#include "paged_sched.cuh"
 
 namespace usp {
 namespace {
@@ -45,6 +48,36 @@ PagedArgs paged_args(const usp_paged_desc &d) {
     return a;
 }
 
+// Which kernels run, and the CTAs and rows of their partials.
+struct Route {
+    int decode_rows, decode_ctas;
+};
+
+Route route(const usp_paged_desc &d, int sms) {
+    Route r{};
+    const int G = d.hq / d.cache.hkv;
+    const int64_t rows = G * (int64_t)std::max(1, d.max_new);
+    if (d.cache.dtype == USP_BF16 && G <= 32) {
+        r.decode_rows = rows <= 16 ? 16 : 32;
+        r.decode_ctas = decode_ctas(sms, r.decode_rows);
+    }
+    return r;
+}
+
+size_t workspace_bytes_of(const Route &r, int hd) {
+    return 256 + (r.decode_ctas ? part_bytes(r.decode_ctas, r.decode_rows, hd) : 0);
+}
+
+PartSpace part_space(char *&at, int ctas, int rows, int hd) {
+    PartSpace w{};
+    w.ctas = ctas;
+    w.rows = rows;
+    w.head = reinterpret_cast<PartHeader *>(at);
+    w.data = reinterpret_cast<float *>(at + (size_t)ctas * sizeof(PartHeader));
+    at += part_bytes(ctas, rows, hd);
+    return w;
+}
+
 }  // namespace
 }  // namespace usp
 
@@ -53,8 +86,9 @@ using namespace usp;
 extern "C" {
 
 size_t usp_paged_attn_workspace_size(usp_paged_desc d) {
-    if (check_paged_desc(d)) return 0;
-    return 256;
+    const DeviceInfo *di = nullptr;
+    if (check_paged_desc(d) || !(di = device_info())) return 0;
+    return workspace_bytes_of(route(d, di->sm_count), d.cache.hd);
 }
 
 int usp_paged_attn(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_table,
@@ -63,19 +97,28 @@ int usp_paged_attn(const void *q, const void *k_cache, const void *v_cache, cons
     int rc = check_paged_desc(d);
     if (rc) return rc;
     if (d.tokens == 0 || d.nreq == 0) return USP_OK;
-    if (!q || !cu_new || !kv_lens || !out || !lse || !workspace) return USP_ERR_INVALID_ARG;
-    // a cache without pages and a table without columns may be null: no request has a key then
-    if ((d.cache.num_pages > 0 && (!k_cache || !v_cache)) || (d.max_pages > 0 && !block_table))
-        return USP_ERR_INVALID_ARG;
+    if (!q || !k_cache || !v_cache || !cu_new || !kv_lens || !out || !lse || !workspace) return USP_ERR_INVALID_ARG;
+    if (d.max_pages > 0 && !block_table) return USP_ERR_INVALID_ARG;  // without columns no request has a key
+    if (d.cache.num_pages == 0) return USP_ERR_SHAPE;
     if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
         !aligned(block_table, 4) || !aligned(cu_new, 4) || !aligned(kv_lens, 4) || !aligned(workspace, 256))
         return USP_ERR_ALIGN;
-    if (workspace_bytes < usp_paged_attn_workspace_size(d)) return USP_ERR_INVALID_ARG;
+    const DeviceInfo *di = device_info();
+    if (!di) return USP_ERR_CUDA;
+    const Route r = route(d, di->sm_count);
+    if (workspace_bytes < workspace_bytes_of(r, d.cache.hd)) return USP_ERR_INVALID_ARG;
     PagedArgs a = paged_args(d);
     a.q = q; a.k = k_cache; a.v = v_cache;
     a.table = block_table; a.cu = cu_new; a.kv = kv_lens;
     a.out = out; a.lse = lse;
-    return launch_paged_simt(a, d.cache.dtype, reinterpret_cast<cudaStream_t>(stream));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (!r.decode_ctas) return launch_paged_simt(a, d.cache.dtype, s);
+    char *at = static_cast<char *>(workspace);
+    CombineArgs c{};
+    c.out = out; c.lse = lse; c.out_stride = a.out_stride; c.G = a.G; c.hq = a.hq;
+    c.w[0] = part_space(at, r.decode_ctas, r.decode_rows, a.hd);
+    if ((rc = launch_paged_decode(a, r.decode_rows, INT_MAX, c.w[0], s))) return rc;
+    return launch_paged_combine(c, a.hd, d.cache.dtype, s);
 }
 
 }  // extern "C"

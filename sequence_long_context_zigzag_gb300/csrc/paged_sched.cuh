@@ -1,0 +1,269 @@
+// paged_sched.cuh -- how the work of one usp_paged_attn call is divided among the CTAs of a kernel.
+//
+// A unit is one request, one KV head and one block of `tb` new tokens (tb * G query rows); its cost is
+// the keys its last token sees plus a constant `over` for its start and end. Units are ordered request
+// by request, KV head by KV head, block by block, and the total cost W is cut into equal spans, one per
+// CTA, at key-tile boundaries inside units. So every CTA gets the same number of keys however ragged
+// the lengths are, and a long sequence with few rows is spread over all SMs. The lengths are device
+// data: every CTA sums the costs itself (one scan over the requests, about a microsecond for the first
+// few hundred), which costs less than a planning launch and keeps the call free of host copies.
+// A unit cut by a span's end is finished by paged_combine_kernel: the CTA that opens it writes its
+// partial to its slot 1 with a header, the CTAs that continue it to their slot 0; spans are longer than
+// a tile, so a CTA has at most one of each.
+#pragma once
+
+#include "paged.cuh"
+
+namespace usp {
+
+struct SchedIn {
+    const int32_t *cu, *kv;
+    int64_t tokens, max_keys;
+    int32_t nreq, hkv, G;
+    int32_t tb;          // new tokens per unit
+    int32_t causal;
+    int32_t n_lo, n_hi;  // the requests of this kernel: n_lo < new tokens <= n_hi
+    int32_t over;        // constant cost of a unit, in keys
+    int32_t min_span;    // keys per CTA below which fewer CTAs work (more than a key tile)
+};
+
+// A request's units: block b of each head holds new tokens [b tb, min((b + 1) tb, n)).
+struct ReqUnits {
+    int64_t t0, p0;  // first row of q; position of the first new token
+    int32_t n, kv, nb;
+    int64_t head_cost;
+};
+
+__device__ __forceinline__ int64_t unit_keys(const SchedIn &s, const ReqUnits &r, int32_t b) {
+    if (!s.causal) return r.kv;
+    return max((int64_t)0, r.p0 + min((int64_t)(b + 1) * s.tb, (int64_t)r.n));
+}
+
+// cost of blocks [0, b), b < nb (all of them full): sum of over + max(0, p0 + (b' + 1) tb)
+__device__ __forceinline__ int64_t unit_prefix(const SchedIn &s, const ReqUnits &r, int32_t b) {
+    if (!s.causal) return (int64_t)b * (s.over + (int64_t)r.kv);
+    const int64_t b0 = r.p0 >= 0 ? 0 : min((int64_t)b, -r.p0 / s.tb);  // blocks that see nothing
+    const int64_t nb = b, tri = nb * (nb + 1) / 2 - b0 * (b0 + 1) / 2;
+    return nb * s.over + (nb - b0) * r.p0 + tri * s.tb;
+}
+
+__device__ __forceinline__ ReqUnits req_units(const SchedIn &s, int32_t i) {
+    const Request q = paged_request(s.cu, s.kv, i, s.tokens, s.max_keys);
+    ReqUnits r;
+    r.t0 = q.t0;
+    r.n = q.n > s.n_lo && q.n <= s.n_hi ? q.n : 0;
+    r.kv = q.kv;
+    r.p0 = (int64_t)q.kv - q.n;
+    r.nb = (r.n + s.tb - 1) / s.tb;
+    r.head_cost = r.n > 0 ? unit_prefix(s, r, r.nb - 1) + s.over + unit_keys(s, r, r.nb - 1) : 0;
+    return r;
+}
+
+// A place in the order of units: key tile t of a unit. req == nreq: the end.
+struct UnitPos {
+    int32_t req, head, b, t;
+};
+
+struct SchedShared {
+    int64_t warp_sum[32];
+    int64_t before[2];
+    int32_t req[2];
+};
+
+struct Sched {
+    int64_t W;         // total cost
+    int32_t ctas;      // CTAs that work
+    UnitPos at, end;   // this CTA's span
+    ReqUnits r;        // the request of `at`
+    int64_t before;    // cost before that request
+};
+
+__device__ __forceinline__ int64_t span_start(int64_t W, int32_t ctas, int32_t c) {
+    return W / ctas * c + W % ctas * c / ctas;  // floor(W c / ctas) without overflow
+}
+
+// the last CTA whose span begins before cost x (0 < x <= W)
+__device__ __forceinline__ int32_t span_of(int64_t W, int32_t ctas, int64_t x) {
+    int32_t k = (int32_t)((double)x / (double)W * ctas);
+    k = max(0, min(k, ctas - 1));
+    while (k > 0 && span_start(W, ctas, k) >= x) --k;
+    while (k + 1 < ctas && span_start(W, ctas, k + 1) < x) ++k;
+    return k;
+}
+
+template <int KT>
+__device__ __forceinline__ UnitPos unit_pos(const SchedIn &s, const ReqUnits &r, int32_t req, int64_t off) {
+    UnitPos p;
+    p.req = req;
+    p.head = (int32_t)(off / r.head_cost);
+    off -= p.head * r.head_cost;
+    int32_t lo = 0, hi = r.nb;  // the last block that begins at or before off
+    while (hi - lo > 1) {
+        const int32_t mid = (lo + hi) >> 1;
+        if (unit_prefix(s, r, mid) <= off) lo = mid;
+        else hi = mid;
+    }
+    p.b = lo;
+    off -= unit_prefix(s, r, lo);
+    p.t = off <= s.over ? 0 : (int32_t)((off - s.over) / KT);
+    return p;
+}
+
+// Called by all NT threads of the CTA. False when this CTA has no work.
+template <int NT, int KT>
+__device__ bool sched_init(const SchedIn &s, SchedShared &sh, Sched &o) {
+    static_assert(NT % 32 == 0 && NT <= 1024, "whole warps");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // inclusive scan of x over the CTA; total: the sum
+    auto scan = [&](int64_t x, int64_t &total) {
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d) x += y;
+        }
+        __syncthreads();
+        if (lane == 31) sh.warp_sum[warp] = x;
+        __syncthreads();
+        total = 0;
+        for (int w = 0; w < NT / 32; ++w) {
+            const int64_t y = sh.warp_sum[w];
+            if (w < warp) x += y;
+            total += y;
+        }
+        return x;
+    };
+    if (tid < 2) sh.req[tid] = s.nreq;
+    int64_t mine = 0;
+    for (int32_t i = tid; i < s.nreq; i += NT) mine += req_units(s, i).head_cost * s.hkv;
+    int64_t incl = scan(mine, o.W);
+    if (o.W == 0) return false;
+    o.ctas = (int32_t)min((int64_t)gridDim.x, max((int64_t)1, o.W / s.min_span));
+    const int32_t c = blockIdx.x;
+    if (c >= o.ctas) return false;
+    const int64_t x0 = span_start(o.W, o.ctas, c), x1 = span_start(o.W, o.ctas, c + 1);
+    int64_t carry = 0;
+    for (int32_t base = 0; base < s.nreq; base += NT) {
+        int64_t total = o.W;
+        if (s.nreq > NT) {
+            mine = base + tid < s.nreq ? req_units(s, base + tid).head_cost * s.hkv : 0;
+            incl = scan(mine, total);
+        }
+        const int64_t a = carry + incl - mine;
+        if (mine > 0 && a <= x0 && x0 < a + mine) {
+            sh.req[0] = base + tid;
+            sh.before[0] = a;
+        }
+        if (mine > 0 && a <= x1 && x1 < a + mine) {
+            sh.req[1] = base + tid;
+            sh.before[1] = a;
+        }
+        carry += total;
+        if (carry > x1) break;
+    }
+    __syncthreads();
+    const int32_t i0 = sh.req[0], i1 = sh.req[1];
+    o.before = sh.before[0];
+    o.r = req_units(s, i0);
+    o.at = unit_pos<KT>(s, o.r, i0, x0 - o.before);
+    o.end = UnitPos{s.nreq, 0, 0, 0};
+    if (i1 < s.nreq) o.end = unit_pos<KT>(s, i1 == i0 ? o.r : req_units(s, i1), i1, x1 - sh.before[1]);
+    return true;
+}
+
+// One stretch of a unit's key tiles [t0, t1), of `tiles` in all, that this CTA computes.
+struct Segment {
+    int64_t tok0;        // first row of q
+    int32_t ntok, head;  // tokens of the block; KV head
+    int32_t req, b;
+    int32_t p0, kv;      // position of the block's first token; keys of the request
+    int32_t t0, t1, tiles;
+};
+
+// the next segment of the span; false at its end
+template <int KT>
+__device__ __forceinline__ bool sched_next(const SchedIn &s, Sched &o, Segment &g) {
+    for (;;) {
+        const bool last = o.at.req == o.end.req && o.at.head == o.end.head && o.at.b == o.end.b;
+        if (o.at.req >= s.nreq || (last && o.end.t <= o.at.t)) return false;
+        g.tiles = (int32_t)((unit_keys(s, o.r, o.at.b) + KT - 1) / KT);
+        g.t0 = o.at.t;
+        g.t1 = last ? o.end.t : g.tiles;
+        g.head = o.at.head;
+        g.req = o.at.req;
+        g.b = o.at.b;
+        const int32_t first = o.at.b * s.tb;
+        g.tok0 = o.r.t0 + first;
+        g.ntok = min(s.tb, o.r.n - first);
+        g.p0 = (int32_t)(o.r.p0 + first);
+        g.kv = o.r.kv;
+        // step to the next unit (the end of the span when this one is cut)
+        if (last) {
+            o.at = o.end;
+        } else {
+            o.at.t = 0;
+            if (++o.at.b == o.r.nb) {
+                o.at.b = 0;
+                if (++o.at.head == s.hkv) {
+                    o.at.head = 0;
+                    o.before += o.r.head_cost * s.hkv;
+                    do {
+                        if (++o.at.req >= s.nreq) break;
+                        o.r = req_units(s, o.at.req);
+                    } while (o.r.n == 0);
+                }
+            }
+        }
+        return true;
+    }
+}
+
+// What the CTA that opens a unit and does not finish it leaves for the combine.
+struct PartHeader {
+    int64_t tok0;
+    int32_t rows;  // valid rows (ntok * G); 0: this CTA opens no cut unit
+    int32_t head;
+    int32_t last;  // the CTA that finishes the unit
+    int32_t pad[3];
+};
+
+// The header of a segment with t0 == 0 and t1 < tiles. Such a segment is the span's last one, so `o`
+// still holds its request.
+__device__ __forceinline__ PartHeader part_header(const SchedIn &s, const Sched &o, const Segment &g) {
+    PartHeader h{};
+    h.tok0 = g.tok0;
+    h.rows = g.ntok * s.G;
+    h.head = g.head;
+    const int64_t end = o.before + (int64_t)g.head * o.r.head_cost +
+                        (g.b + 1 < o.r.nb ? unit_prefix(s, o.r, g.b + 1) : o.r.head_cost);
+    h.last = span_of(o.W, o.ctas, end);
+    return h;
+}
+
+// ---- partials: per CTA two slots of `rows` rows: o (rows x hd, relative to the maximum m), m, l ------
+struct PartSpace {
+    PartHeader *head;  // [ctas]
+    float *data;       // [ctas][2][rows * (hd + 2)]
+    int32_t ctas, rows;
+};
+__host__ __device__ inline size_t part_bytes(int ctas, int rows, int hd) {
+    const size_t b = (size_t)ctas * (sizeof(PartHeader) + 2 * (size_t)rows * (hd + 2) * 4);
+    return (b + 255) / 256 * 256;
+}
+__device__ __forceinline__ float *part_slot(const PartSpace &w, int hd, int cta, int slot) {
+    return w.data + ((size_t)cta * 2 + slot) * (size_t)w.rows * (hd + 2);
+}
+
+struct CombineArgs {
+    PartSpace w[2];  // one per kernel of the call (ctas == 0: not launched)
+    void *out;
+    float *lse;
+    int64_t out_stride;
+    int32_t G, hq;
+};
+int launch_paged_combine(const CombineArgs &a, int hd, int dtype, cudaStream_t s);
+
+// bf16, units of up to `rows` (16 or 32) query rows; requests with at most n_hi new tokens
+int launch_paged_decode(const PagedArgs &a, int rows, int n_hi, const PartSpace &w, cudaStream_t s);
+int decode_ctas(int sms, int rows);
+
+}  // namespace usp

@@ -348,7 +348,7 @@ def test_paged_attn_rejects_pointers_and_workspace():
         assert f(*eight[:i], BAD + 1, *eight[i + 1:], paged(), GOOD, 2 ** 30, None) == _abi.USP_ERR_ALIGN
     assert f(*eight, paged(), None, 2 ** 30, None) == _abi.USP_ERR_INVALID_ARG
     assert f(*eight, paged(), GOOD + 128, 2 ** 30, None) == _abi.USP_ERR_ALIGN
-    assert f(*eight, paged(), GOOD, 0, None) == _abi.USP_ERR_INVALID_ARG
+    assert f(*eight, paged(dict(num_pages=0)), GOOD, 2 ** 30, None) == _abi.USP_ERR_SHAPE
     assert f(*([None] * 8), paged(tokens=0), None, 0, None) == _abi.USP_OK
     assert f(*([None] * 8), paged(nreq=0), None, 0, None) == _abi.USP_OK
 
