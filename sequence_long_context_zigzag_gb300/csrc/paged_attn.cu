@@ -50,14 +50,22 @@ PagedArgs paged_args(const usp_paged_desc &d) {
 
 // Which kernels run, and the CTAs and rows of their partials.
 struct Route {
-    int decode_rows, decode_ctas;
+    int decode_rows, decode_ctas;  // units of few rows (CTAs 0: not launched)
+    int chunk_ctas;                // units of many rows
+    int split;                     // the most new tokens of a request that the decode kernel takes
 };
 
 Route route(const usp_paged_desc &d, int sms) {
     Route r{};
     const int G = d.hq / d.cache.hkv;
     const int64_t rows = G * (int64_t)std::max(1, d.max_new);
-    if (d.cache.dtype == USP_BF16 && G <= 32) {
+    if (d.cache.dtype != USP_BF16) return r;
+    r.split = INT_MAX;
+    if (rows > 32) {
+        r.chunk_ctas = sms;
+        r.split = 32 / G;
+    }
+    if (r.split > 0) {
         r.decode_rows = rows <= 16 ? 16 : 32;
         r.decode_ctas = decode_ctas(sms, r.decode_rows);
     }
@@ -65,7 +73,8 @@ Route route(const usp_paged_desc &d, int sms) {
 }
 
 size_t workspace_bytes_of(const Route &r, int hd) {
-    return 256 + (r.decode_ctas ? part_bytes(r.decode_ctas, r.decode_rows, hd) : 0);
+    return 256 + (r.decode_ctas ? part_bytes(r.decode_ctas, r.decode_rows, hd) : 0) +
+           (r.chunk_ctas ? part_bytes(r.chunk_ctas, kChunkRows, hd) : 0);
 }
 
 PartSpace part_space(char *&at, int ctas, int rows, int hd) {
@@ -112,12 +121,18 @@ int usp_paged_attn(const void *q, const void *k_cache, const void *v_cache, cons
     a.table = block_table; a.cu = cu_new; a.kv = kv_lens;
     a.out = out; a.lse = lse;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (!r.decode_ctas) return launch_paged_simt(a, d.cache.dtype, s);
+    if (d.cache.dtype != USP_BF16) return launch_paged_simt(a, d.cache.dtype, s);
     char *at = static_cast<char *>(workspace);
     CombineArgs c{};
     c.out = out; c.lse = lse; c.out_stride = a.out_stride; c.G = a.G; c.hq = a.hq;
-    c.w[0] = part_space(at, r.decode_ctas, r.decode_rows, a.hd);
-    if ((rc = launch_paged_decode(a, r.decode_rows, INT_MAX, c.w[0], s))) return rc;
+    if (r.chunk_ctas) {
+        c.w[0] = part_space(at, r.chunk_ctas, kChunkRows, a.hd);
+        if ((rc = launch_paged_chunk(a, r.split, c.w[0], s))) return rc;
+    }
+    if (r.decode_ctas) {
+        c.w[1] = part_space(at, r.decode_ctas, r.decode_rows, a.hd);
+        if ((rc = launch_paged_decode(a, r.decode_rows, r.split, c.w[1], s))) return rc;
+    }
     return launch_paged_combine(c, a.hd, d.cache.dtype, s);
 }
 

@@ -1,0 +1,619 @@
+// paged_chunk.cu -- bf16 attention of many query rows per KV head over the paged cache, on the
+// 5th-generation tensor cores (sm_103a): chunks of a prompt, whole prompts.
+//
+// Mathematics: as paged_decode.cu (online softmax, lazy rescale). A unit is two tiles of up to 128 query
+// rows of one request and KV head: a tile packs TQ = 128 / G tokens x the G query heads of the KV head,
+// so grouped heads share every K/V tile that is loaded, and a chunk of 128 / G tokens fills a tile.
+//
+// What bounds it: from about 290 rows per KV head on, the tensor cores and the exponentials (the
+// unit's two tiles keep both busy in turn); below that, HBM. Roles of a CTA (one per SM), each walking the
+// CTA's span of the work (paged_sched.cuh) without a CTA-wide barrier:
+//   warps 0-3, 4-7  softmax of Q tile 0 / 1, one thread per query row: S from tensor memory, mask, running
+//                   maximum, P = 2^(S scale log2(e) - m) as bf16 back over S (the A operand of P V), rescale
+//                   of O when the maximum grows by more than 2^8; at a segment's end out and lse, or the
+//                   fp32 partial of a cut unit;
+//   warp 8          TMA: Q per segment (a box of 64 columns x G heads x TQ tokens), K and V tiles of 128 keys
+//                   through a ring of stages, one box of a page per lane, page numbers read ahead;
+//   warps 9, 10     one MMA issuer per Q tile: S_i = Q_i K^T, O_i += P_i V, taking turns so that one tile's
+//                   products run under the other tile's softmax;
+//   warp 11         idle; with 8-10 the warpgroup that gives registers to the softmax (setmaxnreg).
+//   TMEM: S0 [0,128) S1 [128,256) O0 [256,256+hd) O1 [256+hd,256+2hd); P_i lies over S_i.
+// Rows of the last page behind the request's last key may hold NaN, and 0 x NaN would spread in P V: the
+// softmax warps clear those rows of V's stage in shared memory before they hand P over.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "paged_sched.cuh"
+#include "paged_tma.cuh"
+#include "tc_ptx.cuh"
+#include "usp_device.cuh"
+
+namespace usp {
+namespace {
+
+constexpr int kM = 128;  // rows of a Q tile
+constexpr int kN = 128;  // keys of a tile
+constexpr int kSoftmaxWarps = 8;
+constexpr int kWarps = kSoftmaxWarps + 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kProducerWarp = kSoftmaxWarps;
+constexpr int kMmaWarp = kSoftmaxWarps + 1;  // Q tile 0's issuer; allocates and frees tensor memory
+constexpr int kMmaWarp1 = kSoftmaxWarps + 2;
+// the warpgroups' shares (setmaxnreg) add up to exactly the launch's registers
+constexpr int kLaunchRegs = (65536 / kThreads) / 8 * 8;
+constexpr int kSoftmaxRegs = 208;
+constexpr int kControlRegs = kLaunchRegs * kWarps / 4 - 2 * kSoftmaxRegs;
+static_assert(kControlRegs >= 24 && kControlRegs % 8 == 0 &&
+                  2 * kSoftmaxRegs + kControlRegs == kLaunchRegs * kWarps / 4,
+              "register split must use exactly the launch's registers");
+constexpr int kOver = 192;     // a unit's constant cost, in keys
+constexpr int kMinSpan = 768;  // keys per CTA below which fewer CTAs work
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr float kRescale = 8.0f;  // log2 units
+constexpr float kLn2 = 0.69314718055994531f;
+
+template <int HD> struct Cfg {
+    static constexpr int kBoxes = HD / 64;
+    static constexpr int kBoxBytes = kM * 128;
+    static constexpr int kTileBytes = kM * HD * 2;
+    static constexpr int kStages = HD == 128 ? 2 : 4;
+    static constexpr int kQ = 0;
+    static constexpr int kK = kQ + 2 * kTileBytes;
+    static constexpr int kV = kK + kStages * kTileBytes;
+    static constexpr int kBar = kV + kStages * kTileBytes;
+    static constexpr int Q_FULL = 0;
+    static constexpr int K_FULL = 1;
+    static constexpr int K_EMPTY = K_FULL + kStages;
+    static constexpr int V_FULL = K_EMPTY + kStages;
+    static constexpr int V_EMPTY = V_FULL + kStages;
+    static constexpr int S_FULL = V_EMPTY + kStages;  // [2]
+    static constexpr int P_FULL = S_FULL + 2;         // [2]
+    static constexpr int O_FULL = P_FULL + 2;         // [2]
+    static constexpr int DONE = O_FULL + 2;           // [2]
+    static constexpr int TURN = DONE + 2;             // [2]
+    static constexpr int Q_EMPTY = TURN + 2;
+    static constexpr int O_EMPTY = Q_EMPTY + 1;       // [2]
+    static constexpr int kNumBars = O_EMPTY + 2;
+    static constexpr int kSlot = kBar + kNumBars * 8;  // tensor memory address, skip flag
+    static constexpr int kSmem = kSlot + 16 + 1024;    // + slack for the 1024-byte alignment
+};
+
+struct ChunkParams {
+    CUtensorMap tq, tk, tv;
+    SchedIn s;
+    PartSpace w;
+    __nv_bfloat16 *out;
+    float *lse;
+    const int32_t *table;
+    int *status;
+    int64_t out_stride, table_stride;
+    int32_t num_pages, log_ps, hq;
+    int32_t tq_tokens;  // tokens per Q tile
+    float scale_log2;
+};
+
+// What a Q tile needs of a key tile: nothing, all of it, or its part under the mask.
+struct TileRange {
+    int32_t last;  // keys the tile's last token sees (0: no token)
+    int32_t all;   // keys every token of it sees
+};
+__device__ __forceinline__ TileRange tile_range(const ChunkParams &p, const Segment &g, int i) {
+    const int32_t a = i * p.tq_tokens, b = min(g.ntok, a + p.tq_tokens);
+    TileRange r{0, 0};
+    if (a >= b) return r;
+    r.last = p.s.causal ? max(0, min(g.kv, g.p0 + b)) : g.kv;
+    r.all = p.s.causal ? max(0, min(g.kv, g.p0 + a + 1)) : g.kv;
+    return r;
+}
+
+// The CTA's key tiles as one stream across its segments (segments without a tile are passed over).
+struct Cursor {
+    Sched sc;
+    Segment g;
+    int32_t kt;
+    bool live;
+};
+struct Tile {
+    bool act[2];
+    bool first;  // first tile of its segment
+};
+__device__ __forceinline__ bool cursor_next(const ChunkParams &p, Cursor &c, Tile &t) {
+    t.first = false;
+    while (!(c.live && c.kt < c.g.t1)) {
+        c.live = sched_next<kN>(p.s, c.sc, c.g);
+        if (!c.live) return false;
+        c.kt = c.g.t0;
+        t.first = true;
+    }
+    for (int i = 0; i < 2; ++i) t.act[i] = c.kt * kN < tile_range(p, c.g, i).last;
+    ++c.kt;
+    return true;
+}
+
+// The producer warp. Lane l < boxes loads box l of each K and V tile: column half l / pieces, page piece
+// l % pieces; lane 0 loads Q too.
+template <int HD>
+__device__ void producer_role(const ChunkParams &p, Sched &sc, uint32_t sbase, uint32_t bar0) {
+    using C = Cfg<HD>;
+    const int lane = threadIdx.x & 31;
+    auto BAR = [&](int i) { return bar0 + 8u * i; };
+    auto wait = [&](int bar, uint32_t parity) {
+        const bool r = tc::mbar_wait(BAR(bar), parity, p.status, USP_ERR_TIMEOUT, kWaitLimitNs);
+        return (bool)__all_sync(0xffffffffu, r);
+    };
+    const int ps = 1 << p.log_ps, piece = min(ps, kN), pieces = kN / piece, nbox = pieces * C::kBoxes;
+    const int half = lane / pieces, pc = lane % pieces;
+    const uint32_t in_tile = half * C::kBoxBytes + pc * piece * 128;
+    uint32_t kfills = 0, vfills = 0, nq = 0;
+    bool ok = true;
+    Segment g;
+    while (ok && sched_next<kN>(p.s, sc, g)) {
+        if (g.t0 >= g.t1) continue;
+        if (nq > 0 && !(ok = wait(C::Q_EMPTY, (nq - 1) & 1u))) break;
+        if (lane == 0) {
+            const uint32_t box = (uint32_t)(p.tq_tokens * p.s.G) * 128;
+            tc::mbar_arrive_expect_tx(BAR(C::Q_FULL), 2 * C::kBoxes * box);
+            for (int i = 0; i < 2; ++i)
+                for (int bx = 0; bx < C::kBoxes; ++bx)
+                    tma_load_3d(sbase + C::kQ + i * C::kTileBytes + bx * C::kBoxBytes, &p.tq, bx * 64, g.head * p.s.G,
+                                (int32_t)(g.tok0 + i * p.tq_tokens), BAR(C::Q_FULL));
+        }
+        ++nq;
+        const int32_t *row = p.table + (int64_t)g.req * p.table_stride;
+        // page of this lane's piece of tile t; num_pages (a box of zeros) behind the request's keys
+        auto page_of = [&](int t) {
+            const int64_t key = (int64_t)t * kN + pc * piece;
+            if (lane >= nbox || key >= g.kv) return p.num_pages;
+            const int32_t x = __ldg(row + (key >> p.log_ps));
+            return x >= 0 && x < p.num_pages ? x : p.num_pages;
+        };
+        int32_t page = page_of(g.t0);
+        for (int t = g.t0; t < g.t1; ++t) {
+            const int32_t next = t + 1 < g.t1 ? page_of(t + 1) : 0;
+            const int32_t c1 = g.head * ps + (int)(((int64_t)t * kN + pc * piece) & (ps - 1));
+            const uint32_t st = kfills % C::kStages, ph = ((kfills / C::kStages) & 1u) ^ 1u;
+            if (!(ok = wait(C::K_EMPTY + st, ph))) break;
+            if (lane == 0) tc::mbar_arrive_expect_tx(BAR(C::K_FULL + st), C::kTileBytes);
+            __syncwarp();
+            if (lane < nbox)
+                tma_load_3d(sbase + C::kK + st * C::kTileBytes + in_tile, &p.tk, half * 64, c1, page, BAR(C::K_FULL + st));
+            ++kfills;
+            if (!(ok = wait(C::V_EMPTY + st, ph))) break;
+            if (lane == 0) tc::mbar_arrive_expect_tx(BAR(C::V_FULL + st), C::kTileBytes);
+            __syncwarp();
+            if (lane < nbox)
+                tma_load_3d(sbase + C::kV + st * C::kTileBytes + in_tile, &p.tv, half * 64, c1, page, BAR(C::V_FULL + st));
+            ++vfills;
+            page = next;
+        }
+    }
+    if (!ok) {
+        // drain (bounded), so that no copy lands after the CTA has gone
+        if (nq > 0) wait(C::Q_FULL, (nq - 1) & 1u);
+        for (uint32_t f = kfills > C::kStages ? kfills - C::kStages : 0; f < kfills; ++f)
+            wait(C::K_FULL + f % C::kStages, (f / C::kStages) & 1u);
+        for (uint32_t f = vfills > C::kStages ? vfills - C::kStages : 0; f < vfills; ++f)
+            wait(C::V_FULL + f % C::kStages, (f / C::kStages) & 1u);
+    }
+}
+
+template <int HD>
+__device__ __forceinline__ void issue_s(uint32_t d_tmem, uint64_t qdesc, uint64_t kdesc) {
+    using C = Cfg<HD>;
+    constexpr uint32_t id = tc::idesc_bf16_f32(kM, kN, 0, 0);
+#pragma unroll
+    for (int k = 0; k < HD / 16; ++k) {
+        const uint64_t off = (uint64_t)(((k / 4) * C::kBoxBytes + (k % 4) * 32) >> 4);
+        tc::mma_ss(d_tmem, qdesc + off, kdesc + off, id, k > 0 ? 1u : 0u);
+    }
+}
+// V as (N = hd) x (K = keys), MN-major: 64-column blocks kBoxBytes apart, 8-key groups 1024 bytes apart
+template <int HD>
+__device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint64_t vdesc, uint32_t accumulate) {
+    constexpr uint32_t id = tc::idesc_bf16_f32(kM, HD, 0, 1);
+#pragma unroll
+    for (int k = 0; k < kN / 16; ++k)
+        tc::mma_ts(d_tmem, p_tmem + k * 8, vdesc + (uint64_t)((k * 2048) >> 4), id, (accumulate || k > 0) ? 1u : 0u);
+}
+
+// One thread per Q tile. Burst j of issuer i: PV_i(j), then S_i(j+1) unless tile j+1 opens a segment (its
+// first S leaves the turn order, so that it runs while the other tile finishes the old segment). Every
+// burst waits for its operands first and for its turn last. PV_i(j) and S_i(j+1) come from one thread, so
+// S_i(j+1) overwrites P_i(j) only after PV_i(j) has read it. Stages are released by both issuers; each
+// waits for a stage's fill before releasing it, also when its Q tile skips the tile.
+template <int HD>
+__device__ void mma_role(const ChunkParams &p, Cursor &cs, uint32_t sbase, uint32_t bar0, uint32_t tmem, int i) {
+    using C = Cfg<HD>;
+    auto BAR = [&](int k) { return bar0 + 8u * k; };
+    auto wait = [&](int bar, uint32_t parity) {
+        return tc::mbar_wait(BAR(bar), parity, p.status, USP_ERR_TIMEOUT, kWaitLimitNs);
+    };
+    const uint64_t qdesc = tc::sw128_desc(sbase + C::kQ + (uint32_t)i * C::kTileBytes, 16, 1024);
+    const uint64_t kdesc0 = tc::sw128_desc(sbase + C::kK, 16, 1024);
+    const uint64_t vdesc0 = tc::sw128_desc(sbase + C::kV, C::kBoxBytes, 1024);
+    auto stage_off = [](uint32_t st) { return (uint64_t)((st * C::kTileBytes) >> 4); };
+    const uint32_t tS = tmem + 128u * i, tO = tmem + 256u + (uint32_t)(HD * i);
+    const int my_turn = C::TURN + i, other_turn = C::TURN + (1 - i);
+    uint32_t turns = 0;
+    Tile cur, nxt;
+    bool have = false, ok = true;
+    uint32_t pc = 0, started = 0;  // P waits; a PV of the current segment has been issued
+    uint32_t nq = 0, no = 0;       // Q loads consumed; O_i read-outs handed to the softmax
+    uint32_t j = 0;                // tiles of the stream
+    if (i == 1) tc::mbar_arrive(BAR(other_turn));  // issuer 1's empty "burst -1"
+    while (ok) {
+        const bool have_n = cursor_next(p, cs, nxt);
+        const bool boundary = have_n && nxt.first;
+        const uint32_t jn = have ? j + 1 : 0;
+        const uint32_t stn = jn % C::kStages, phn = (jn / C::kStages) & 1u;
+        bool turn_after_s = false;
+        if (have) {
+            const bool last = !have_n || nxt.first;
+            const uint32_t st = j % C::kStages, ph = (j / C::kStages) & 1u;
+            const bool act = i ? cur.act[1] : cur.act[0];
+            if (last) tc::mma_commit(BAR(C::Q_EMPTY));  // this issuer's S products of the segment are issued
+            if (!(ok = wait(C::V_FULL + st, ph))) break;
+            if (act && !(ok = wait(C::P_FULL + i, pc & 1u))) break;
+            if (act && !started && no > 0 && !(ok = wait(C::O_EMPTY + i, (no - 1) & 1u))) break;
+            if (have_n && !boundary && !(ok = wait(C::K_FULL + stn, phn))) break;
+            if (!(ok = wait(my_turn, (turns++) & 1u))) break;
+            if (act) {
+                ++pc;
+                tc::fence_after_sync();
+                issue_pv<HD>(tO, tS, vdesc0 + stage_off(st), started);
+                started = 1;
+            }
+            tc::mma_commit(BAR(C::V_EMPTY + st));
+            if (last) {
+                if (started) {
+                    tc::mma_commit(BAR(C::O_FULL + i));
+                    ++no;
+                }
+                started = 0;
+            }
+            turn_after_s = have_n && !boundary;
+            if (!turn_after_s) tc::mbar_arrive(BAR(other_turn));
+        }
+        if (!have_n) break;
+        if (boundary) {
+            if (!(ok = wait(C::Q_FULL, nq & 1u))) break;
+            ++nq;
+            if (!(ok = wait(C::K_FULL + stn, phn))) break;
+        }
+        if (i ? nxt.act[1] : nxt.act[0]) {
+            issue_s<HD>(tS, qdesc, kdesc0 + stage_off(stn));
+            tc::mma_commit(BAR(C::S_FULL + i));
+        }
+        tc::mma_commit(BAR(C::K_EMPTY + stn));
+        if (turn_after_s) tc::mbar_arrive(BAR(other_turn));
+        cur = nxt;
+        have = true;
+        j = jn;
+    }
+    if (!ok) tc::mbar_arrive(BAR(other_turn));  // let the other issuer reach its own bounded exit
+    tc::mma_commit(BAR(C::DONE + i));           // every MMA of this issuer ends before tensor memory is freed
+    wait(C::DONE + i, 0);
+}
+
+__device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
+
+// One segment of the softmax of Q tile i; ns (S tiles), no (O read-outs) and nt (tiles of the stream) run
+// on across segments. False after a failed wait (the whole warp leaves; the others' waits end by the
+// recorded status).
+template <int HD>
+__device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const Segment &g, uint8_t *smem, uint32_t bar0,
+                                                uint32_t tmem, int i, uint32_t &ns, uint32_t &no, uint32_t &nt) {
+    using C = Cfg<HD>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wq = warp & 3;
+    const int row = wq * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
+    const uint32_t tS = tmem + lane_off + 128u * (uint32_t)i;
+    const uint32_t tO = tmem + lane_off + 256u + (uint32_t)(HD * i);
+    const TileRange range = tile_range(p, g, i);
+    const int tok = i * p.tq_tokens + row / p.s.G;  // token of the segment's block
+    const bool row_ok = row < p.tq_tokens * p.s.G && tok < g.ntok;
+    const int lim = p.s.causal ? max(0, min(g.kv, g.p0 + min(tok, g.ntok - 1) + 1)) : g.kv;
+    const float sl2 = p.scale_log2;
+    const uint64_t sl22 = tc::pack2(sl2, sl2);
+    float m = -INFINITY, l = 0.f;
+    bool any = false, ok = true;
+    const uint32_t nt0 = nt;
+    nt += (uint32_t)(g.t1 - g.t0);
+    const int act_end = min(g.t1, (range.last + kN - 1) / kN);
+    for (int kt = g.t0; kt < act_end; ++kt) {
+        const bool full = (kt + 1) * kN <= range.all;
+        ok = tc::mbar_wait(bar0 + 8u * (C::S_FULL + i), ns & 1u, p.status, USP_ERR_TIMEOUT, kWaitLimitNs);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        uint32_t sr[4][32];
+        tc::fence_after_sync();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tc::tmem_ld32(tS + c * 32, sr[c]);
+        tc::tmem_ld_wait();
+        if (!full) {
+            const int ll = lim - kt * kN;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if (c * 32 + e >= ll) sr[c][e] = __float_as_uint(-INFINITY);
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            float a = u2f(sr[c][0]), b = u2f(sr[c][1]);
+#pragma unroll
+            for (int e = 2; e < 30; e += 4) {
+                a = tc::max3(a, u2f(sr[c][e]), u2f(sr[c][e + 1]));
+                b = tc::max3(b, u2f(sr[c][e + 2]), u2f(sr[c][e + 3]));
+            }
+            mx = tc::max3(mx, tc::max3(a, u2f(sr[c][30]), u2f(sr[c][31])), b);
+        }
+        mx *= sl2;
+        const bool need = mx > m + kRescale;
+        if (__any_sync(0xffffffffu, need)) {
+            const float mn = fmaxf(m, mx);
+            const float alpha = need ? tc::ex2(m - mn) : 1.f;  // 0 on the first visible tile
+            if (need) m = mn;
+            if (any) {
+#pragma unroll 1
+                for (int c = 0; c < HD / 32; ++c) {
+                    uint32_t o[32];
+                    tc::tmem_ld32(tO + c * 32, o);
+                    tc::tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(u2f(o[e]) * alpha);
+                    tc::tmem_st32(tO + c * 32, o);
+                }
+            }
+            l *= alpha;
+        }
+        const float mb = m == -INFINITY ? 0.f : m;
+        const uint64_t nmb2 = tc::pack2(-mb, -mb);
+        uint64_t sum = tc::pack2(0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const uint64_t y = tc::fma2(tc::pack2(u2f(sr[c][2 * e]), u2f(sr[c][2 * e + 1])), sl22, nmb2);
+                float y0, y1;
+                tc::unpack2(y, y0, y1);
+                const float p0 = tc::ex2(y0), p1 = tc::ex2(y1);
+                sum = tc::add2(sum, tc::pack2(p0, p1));
+                pk[e] = float2_to_bf16x2(p0, p1);
+            }
+            tc::tmem_st16(tS + c * 16, pk);
+        }
+        float s0, s1;
+        tc::unpack2(sum, s0, s1);
+        l += s0 + s1;
+        if ((kt + 1) * kN > g.kv) {
+            // keys behind the request's last one: their V rows become zeros (each softmax warpgroup that
+            // uses the tile clears them; the values written are the same)
+            const uint32_t jt = nt0 + (uint32_t)(kt - g.t0), st = jt % C::kStages;
+            ok = tc::mbar_wait(bar0 + 8u * (C::V_FULL + st), (jt / C::kStages) & 1u, p.status, USP_ERR_TIMEOUT,
+                               kWaitLimitNs);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            uint8_t *v = smem + C::kV + st * C::kTileBytes;
+            for (int x = (g.kv - kt * kN) * 8 + row; x < kN * 8; x += 128)
+#pragma unroll
+                for (int bx = 0; bx < C::kBoxes; ++bx)
+                    *reinterpret_cast<uint4 *>(v + bx * C::kBoxBytes + x * 16) = make_uint4(0, 0, 0, 0);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        tc::tmem_st_wait();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar0 + 8u * (C::P_FULL + i));
+        any = true;
+        ++ns;
+    }
+    if (!ok) return false;
+    // ---- end of the segment -----------------------------------------------------------------------
+    const bool whole = g.t0 == 0 && g.t1 == g.tiles;
+    const int r = i * p.tq_tokens * p.s.G + row;  // row of the unit
+    float *slot = part_slot(p.w, HD, blockIdx.x, g.t0 == 0 ? 1 : 0);
+    const int head = g.head * p.s.G + row % p.s.G;
+    __nv_bfloat16 *orow = p.out + (g.tok0 + tok) * p.out_stride + (int64_t)head * HD;
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    if (any) {
+        ok = tc::mbar_wait(bar0 + 8u * (C::O_FULL + i), no & 1u, p.status, USP_ERR_TIMEOUT, kWaitLimitNs);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return false;
+        ++no;
+        tc::fence_after_sync();
+        uint32_t o[HD / 32][32];
+#pragma unroll
+        for (int c = 0; c < HD / 32; ++c) tc::tmem_ld32(tO + c * 32, o[c]);
+        tc::tmem_ld_wait();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar0 + 8u * (C::O_EMPTY + i));
+        if (row_ok && whole) {
+#pragma unroll
+            for (int c = 0; c < HD / 32; ++c)
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                    uint4 x;
+                    x.x = float2_to_bf16x2(u2f(o[c][e]) * inv, u2f(o[c][e + 1]) * inv);
+                    x.y = float2_to_bf16x2(u2f(o[c][e + 2]) * inv, u2f(o[c][e + 3]) * inv);
+                    x.z = float2_to_bf16x2(u2f(o[c][e + 4]) * inv, u2f(o[c][e + 5]) * inv);
+                    x.w = float2_to_bf16x2(u2f(o[c][e + 6]) * inv, u2f(o[c][e + 7]) * inv);
+                    *reinterpret_cast<uint4 *>(orow + c * 32 + e) = x;
+                }
+        } else if (row_ok) {
+#pragma unroll
+            for (int c = 0; c < HD / 32; ++c)
+#pragma unroll
+                for (int e = 0; e < 32; e += 4)
+                    *reinterpret_cast<uint4 *>(slot + (size_t)r * HD + c * 32 + e) =
+                        make_uint4(o[c][e], o[c][e + 1], o[c][e + 2], o[c][e + 3]);
+        }
+    } else if (row_ok && whole) {
+        for (int e = 0; e < HD; e += 8) *reinterpret_cast<uint4 *>(orow + e) = make_uint4(0, 0, 0, 0);
+    }
+    if (row_ok) {
+        if (whole) {
+            p.lse[(g.tok0 + tok) * p.hq + head] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+        } else {
+            // a part without a visible key has m = -inf: the combine gives its (unwritten) o no weight
+            slot[(size_t)p.w.rows * HD + r] = m;
+            slot[(size_t)p.w.rows * (HD + 1) + r] = l;
+        }
+    }
+    return true;
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_constant__ ChunkParams p) {
+    using C = Cfg<HD>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ SchedShared sh;
+    const uint32_t raw = tc::smem_u32(smem_raw);
+    const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
+    uint8_t *smem = smem_raw + pad;
+    const uint32_t sbase = raw + pad;
+    const uint32_t bar0 = sbase + C::kBar;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kSlot);
+    volatile uint32_t *skip_flag = tmem_slot + 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    Sched sc;
+    if (!sched_init<kThreads, kN>(p.s, sh, sc)) {  // the same for every thread
+        if (threadIdx.x == 0) p.w.head[blockIdx.x] = PartHeader{};
+        return;
+    }
+    if (threadIdx.x == 0) {
+        // a bounded wait of an earlier kernel ran out: do no work until usp_check clears it
+        *skip_flag = (*reinterpret_cast<volatile int *>(p.status) != 0) ? 1u : 0u;
+        for (int s = 0; s < C::kStages; ++s) {
+            tc::mbar_init(bar0 + 8u * (C::K_FULL + s), 1);
+            tc::mbar_init(bar0 + 8u * (C::K_EMPTY + s), 2);
+            tc::mbar_init(bar0 + 8u * (C::V_FULL + s), 1);
+            tc::mbar_init(bar0 + 8u * (C::V_EMPTY + s), 2);
+        }
+        tc::mbar_init(bar0 + 8u * C::Q_FULL, 1);
+        tc::mbar_init(bar0 + 8u * C::Q_EMPTY, 2);
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(bar0 + 8u * (C::S_FULL + i), 1);
+            tc::mbar_init(bar0 + 8u * (C::P_FULL + i), 4);
+            tc::mbar_init(bar0 + 8u * (C::O_FULL + i), 1);
+            tc::mbar_init(bar0 + 8u * (C::O_EMPTY + i), 4);
+            tc::mbar_init(bar0 + 8u * (C::DONE + i), 1);
+            tc::mbar_init(bar0 + 8u * (C::TURN + i), 1);
+        }
+        tc::fence_barrier_init();
+    }
+    if (warp == kMmaWarp) {
+        tc::tmem_alloc(tc::smem_u32(tmem_slot), 512);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    const bool skip = *skip_flag != 0;
+    if (warp >= kSoftmaxWarps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
+        if (!skip) {
+            if (warp == kProducerWarp) {
+                producer_role<HD>(p, sc, sbase, bar0);
+            } else if ((warp == kMmaWarp || warp == kMmaWarp1) && lane == 0) {
+                Cursor cs;
+                cs.sc = sc;
+                cs.kt = 0;
+                cs.live = false;
+                mma_role<HD>(p, cs, sbase, bar0, tmem, warp - kMmaWarp);
+            }
+            __syncwarp();
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        PartHeader opened{};
+        if (!skip) {
+            uint32_t ns = 0, no = 0, nt = 0;
+            Segment g;
+            while (sched_next<kN>(p.s, sc, g)) {
+                if (!softmax_segment<HD>(p, g, smem, bar0, tmem, warp >> 2, ns, no, nt)) break;
+                if (threadIdx.x == 0 && g.t0 == 0 && g.t1 < g.tiles) opened = part_header(p.s, sc, g);
+            }
+        }
+        if (threadIdx.x == 0) p.w.head[blockIdx.x] = opened;
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int HD>
+int launch_typed(const ChunkParams &p, int grid, cudaStream_t s) {
+    constexpr int kSmem = Cfg<HD>::kSmem;
+    static_assert(kSmem <= 226 * 1024, "shared memory per CTA");
+    static std::mutex mu;
+    static bool attr_set[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return USP_ERR_CUDA;
+    {
+        std::lock_guard<std::mutex> lk(mu);
+        if (dev < 0 || dev >= 64) return USP_ERR_UNSUPPORTED;
+        if (!attr_set[dev]) {
+            // setmaxnreg.inc is granted only from registers the launch holds: never launch a build whose
+            // register count would make the split wait forever
+            cudaFuncAttributes fa{};
+            if (cudaFuncGetAttributes(&fa, paged_chunk_kernel<HD>) != cudaSuccess) return USP_ERR_CUDA;
+            if ((long)fa.numRegs * kThreads < 2L * 128 * kSoftmaxRegs + 128L * kControlRegs) return USP_ERR_UNSUPPORTED;
+            if (cudaFuncSetAttribute(paged_chunk_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
+                cudaSuccess)
+                return USP_ERR_CUDA;
+            attr_set[dev] = true;
+        }
+    }
+    paged_chunk_kernel<HD><<<grid, kThreads, kSmem, s>>>(p);
+    return cudaGetLastError() == cudaSuccess ? USP_OK : USP_ERR_CUDA;
+}
+
+}  // namespace
+
+int launch_paged_chunk(const PagedArgs &a, int n_lo, const PartSpace &w, cudaStream_t s) {
+    const DeviceInfo *di = device_info();
+    if (!di) return USP_ERR_CUDA;
+    ChunkParams p{};
+    const int ps = 1 << a.log_ps;
+    const uint32_t box = (uint32_t)std::min(ps, kN);
+    p.tq_tokens = kM / a.G;
+    // q as (hd, hq, tokens) in boxes of 64 columns x G heads x the tile's tokens
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return USP_ERR_CUDA;
+    const cuuint64_t dims[3] = {(cuuint64_t)a.hd, (cuuint64_t)a.hq, (cuuint64_t)a.tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)a.hd * 2, (cuuint64_t)a.q_stride * 2};
+    const cuuint32_t qbox[3] = {64, (cuuint32_t)a.G, (cuuint32_t)p.tq_tokens}, estr[3] = {1, 1, 1};
+    if (enc(&p.tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(a.q), dims, strides, qbox, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
+        !make_cache_tmap(&p.tk, a.k, a.num_pages, a.k_page, a.hkv, ps, a.hd, box) ||
+        !make_cache_tmap(&p.tv, a.v, a.num_pages, a.v_page, a.hkv, ps, a.hd, box))
+        return USP_ERR_CUDA;
+    p.s.cu = a.cu; p.s.kv = a.kv;
+    p.s.tokens = a.tokens; p.s.max_keys = (int64_t)a.max_pages << a.log_ps;
+    p.s.nreq = a.nreq; p.s.hkv = a.hkv; p.s.G = a.G;
+    p.s.tb = 2 * p.tq_tokens; p.s.causal = a.causal;
+    p.s.n_lo = n_lo; p.s.n_hi = INT32_MAX;
+    p.s.over = kOver; p.s.min_span = kMinSpan;
+    p.w = w;
+    p.out = static_cast<__nv_bfloat16 *>(a.out);
+    p.lse = a.lse;
+    p.table = a.table;
+    p.status = di->status;
+    p.out_stride = a.out_stride; p.table_stride = a.table_stride;
+    p.num_pages = (int32_t)a.num_pages; p.log_ps = a.log_ps; p.hq = a.hq;
+    p.scale_log2 = a.scale_log2;
+    return a.hd == 128 ? launch_typed<128>(p, w.ctas, s) : launch_typed<64>(p, w.ctas, s);
+}
+
+}  // namespace usp

@@ -404,9 +404,9 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 2 : 1) paged_decode_kernel
 // ------------------------------------------------------------------------------------------------
 // combine: out and lse of the units that spans cut
 // ------------------------------------------------------------------------------------------------
-// One CTA per (span, 8 rows): a warp per row, the columns over its lanes. The parts' maxima and sums are
-// read a part per lane; o = sum_i 2^(m_i - M) o_i / l in the parts' order, so the result does not depend
-// on timing. An empty part has m = -inf, l = 0, o = 0.
+// A CTA per span and up to 8 rows at a time: a warp per row, the columns over its lanes. The parts' maxima
+// and sums are read a part per lane; o = sum_i 2^(m_i - M) o_i / l in the parts' order, so the result does
+// not depend on timing. A part whose rows saw nothing has m = -inf, and its o (perhaps unwritten) no part.
 template <typename T, int HD>
 __global__ void __launch_bounds__(256) paged_combine_kernel(const CombineArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -416,42 +416,43 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const CombineArgs a)
     if (which) c -= a.w[0].ctas;
     const PartSpace w = which ? a.w[1] : a.w[0];
     const PartHeader h = w.head[c];
-    const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
-    if (r >= h.rows) return;
+    const int lane = threadIdx.x & 31;
     const int parts = h.last - c + 1;
     auto slot = [&](int i) { return part_slot(w, HD, c + i, i == 0 ? 1 : 0); };
-    float M = -INFINITY;
-    for (int i = lane; i < parts; i += 32) M = fmaxf(M, slot(i)[(size_t)w.rows * HD + r]);
+    for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < h.rows; r += gridDim.y * 8) {
+        float M = -INFINITY;
+        for (int i = lane; i < parts; i += 32) M = fmaxf(M, slot(i)[(size_t)w.rows * HD + r]);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float Mb = M == -INFINITY ? 0.f : M;
-    float L = 0.f, acc[E] = {};
-    for (int base = 0; base < parts; base += 32) {
-        float wgt = 0.f, l = 0.f;
-        if (base + lane < parts) {
-            const float *s = slot(base + lane);
-            wgt = tc::ex2(s[(size_t)w.rows * HD + r] - Mb);
-            l = wgt * s[(size_t)w.rows * (HD + 1) + r];
-        }
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        const float Mb = M == -INFINITY ? 0.f : M;
+        float L = 0.f, acc[E] = {};
+        for (int base = 0; base < parts; base += 32) {
+            float wgt = 0.f, l = 0.f;
+            if (base + lane < parts) {
+                const float *s = slot(base + lane);
+                wgt = tc::ex2(s[(size_t)w.rows * HD + r] - Mb);
+                l = wgt * s[(size_t)w.rows * (HD + 1) + r];
+            }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        L += l;
-        const int n = min(32, parts - base);
+            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            L += l;
+            const int n = min(32, parts - base);
 #pragma unroll 8
-        for (int i = 0; i < n; ++i) {
-            const float wi = __shfl_sync(0xffffffffu, wgt, i);
-            const float *s = slot(base + i) + (size_t)r * HD + lane * E;
+            for (int i = 0; i < n; ++i) {
+                const float wi = __shfl_sync(0xffffffffu, wgt, i);
+                const float *s = slot(base + i) + (size_t)r * HD + lane * E;
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = fmaf(wi, s[e], acc[e]);
+                for (int e = 0; e < E; ++e) acc[e] = wi > 0.f ? fmaf(wi, s[e], acc[e]) : acc[e];
+            }
         }
-    }
-    const float inv = L > 0.f ? 1.f / L : 0.f;
-    const int64_t tok = h.tok0 + r / a.G;
-    const int head = h.head * a.G + r % a.G;
-    T *o = static_cast<T *>(a.out) + tok * a.out_stride + (int64_t)head * HD + lane * E;
+        const float inv = L > 0.f ? 1.f / L : 0.f;
+        const int64_t tok = h.tok0 + r / a.G;
+        const int head = h.head * a.G + r % a.G;
+        T *o = static_cast<T *>(a.out) + tok * a.out_stride + (int64_t)head * HD + lane * E;
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = (T)(acc[e] * inv);
-    if (lane == 0) a.lse[tok * a.hq + head] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
+        for (int e = 0; e < E; ++e) o[e] = (T)(acc[e] * inv);
+        if (lane == 0) a.lse[tok * a.hq + head] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
+    }
 }
 
 template <int HD, int MT>
@@ -513,7 +514,7 @@ int launch_paged_combine(const CombineArgs &a, int hd, int dtype, cudaStream_t s
     // launched while the kernel before it still runs; griddepcontrol.wait is its first instruction
     cudaLaunchConfig_t cfg{};
     const int rows = std::max(a.w[0].ctas ? a.w[0].rows : 0, a.w[1].ctas ? a.w[1].rows : 0);
-    cfg.gridDim = dim3((unsigned)(a.w[0].ctas + a.w[1].ctas), (unsigned)((rows + 7) / 8));
+    cfg.gridDim = dim3((unsigned)(a.w[0].ctas + a.w[1].ctas), (unsigned)std::min(8, (rows + 7) / 8));
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     cudaLaunchAttribute at{};

@@ -266,4 +266,8 @@ int launch_paged_combine(const CombineArgs &a, int hd, int dtype, cudaStream_t s
 int launch_paged_decode(const PagedArgs &a, int rows, int n_hi, const PartSpace &w, cudaStream_t s);
 int decode_ctas(int sms, int rows);
 
+// bf16, units of up to kChunkRows query rows, one CTA per SM; requests with more than n_lo new tokens
+constexpr int kChunkRows = 256;
+int launch_paged_chunk(const PagedArgs &a, int n_lo, const PartSpace &w, cudaStream_t s);
+
 }  // namespace usp
