@@ -312,7 +312,9 @@ __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const Segm
     const uint32_t tS = tmem + lane_off + 128u * (uint32_t)i;
     const uint32_t tO = tmem + lane_off + 256u + (uint32_t)(HD * i);
     const TileRange range = tile_range(p, g, i);
-    const int tok = i * p.tq_tokens + row / p.s.G;  // token of the segment's block
+    uint32_t rt, rh;
+    p.s.by_G.divmod((uint32_t)row, rt, rh);
+    const int tok = i * p.tq_tokens + (int)rt;  // token of the segment's block
     const bool row_ok = row < p.tq_tokens * p.s.G && tok < g.ntok;
     const int lim = p.s.causal ? max(0, min(g.kv, g.p0 + min(tok, g.ntok - 1) + 1)) : g.kv;
     const float sl2 = p.scale_log2;
@@ -417,7 +419,7 @@ __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const Segm
     const bool whole = g.t0 == 0 && g.t1 == g.tiles;
     const int r = i * p.tq_tokens * p.s.G + row;  // row of the unit
     float *slot = part_slot(p.w, HD, blockIdx.x, g.t0 == 0 ? 1 : 0);
-    const int head = g.head * p.s.G + row % p.s.G;
+    const int head = g.head * p.s.G + (int)rh;
     __nv_bfloat16 *orow = p.out + (g.tok0 + tok) * p.out_stride + (int64_t)head * HD;
     const float inv = l > 0.f ? 1.f / l : 0.f;
     if (any) {
@@ -487,6 +489,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         return;
     }
     if (threadIdx.x == 0) {
+        tc::prefetch_tmap(&p.tq);
+        tc::prefetch_tmap(&p.tk);
+        tc::prefetch_tmap(&p.tv);
         // a bounded wait of an earlier kernel ran out: do no work until usp_check clears it
         *skip_flag = (*reinterpret_cast<volatile int *>(p.status) != 0) ? 1u : 0u;
         for (int s = 0; s < C::kStages; ++s) {
@@ -605,6 +610,8 @@ int launch_paged_chunk(const PagedArgs &a, int n_lo, const PartSpace &w, cudaStr
     p.s.tb = 2 * p.tq_tokens; p.s.causal = a.causal;
     p.s.n_lo = n_lo; p.s.n_hi = INT32_MAX;
     p.s.over = kOver; p.s.min_span = kMinSpan;
+    p.s.inv_ctas = 1.0f / (float)w.ctas;
+    p.s.by_tb = FastDiv((uint32_t)p.s.tb); p.s.by_G = FastDiv((uint32_t)a.G);
     p.w = w;
     p.out = static_cast<__nv_bfloat16 *>(a.out);
     p.lse = a.lse;

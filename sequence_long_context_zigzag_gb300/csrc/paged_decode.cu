@@ -159,7 +159,9 @@ __device__ void consumer(const DecodeParams &p, Sched &sc, uint8_t *smem, uint32
         uint32_t qf[MT > 1 ? 1 : kKS][4];
         auto q_word = [&](int r, int c) -> uint32_t {
             if (r >= rows) return 0u;
-            const int tok = r / p.s.G, head = g.head * p.s.G + r % p.s.G;
+            uint32_t tok, h;
+            p.s.by_G.divmod((uint32_t)r, tok, h);
+            const int head = g.head * p.s.G + (int)h;
             return __ldg(reinterpret_cast<const uint32_t *>(p.q + (g.tok0 + tok) * p.q_stride + (int64_t)head * HD + c));
         };
         if constexpr (MT == 1) {
@@ -195,7 +197,7 @@ __device__ void consumer(const DecodeParams &p, Sched &sc, uint8_t *smem, uint32
         for (int t = 0; t < MT; ++t)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int tok = min(t * 16 + qr + h * 8, rows - 1) / p.s.G;
+                const int tok = (int)p.s.by_G.div((uint32_t)min(t * 16 + qr + h * 8, rows - 1));
                 lim[t][h] = p.s.causal ? max(0, min(g.kv, g.p0 + tok + 1)) : g.kv;
             }
         const int lim_all = p.s.causal ? max(0, min(g.kv, g.p0 + 1)) : g.kv;  // keys that every row sees
@@ -329,7 +331,9 @@ __device__ void consumer(const DecodeParams &p, Sched &sc, uint8_t *smem, uint32
                 a[h] = mm == -INFINITY ? 0.f : tc::ex2(m[i][h] - mm);
             }
             const float inv = whole ? (L > 0.f ? 1.f / L : 0.f) : 1.f;
-            const int tok = r / p.s.G, head = g.head * p.s.G + r % p.s.G;
+            uint32_t tok, hr;
+            p.s.by_G.divmod((uint32_t)r, tok, hr);
+            const int head = g.head * p.s.G + (int)hr;
 #pragma unroll
             for (int c = 0; c < HD / 32; ++c) {
                 consumer_sync();  // the exchange buffer is free
@@ -381,7 +385,11 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 2 : 1) paged_decode_kernel
     __shared__ SchedShared sh;
     __shared__ uint32_t skip;
     const uint32_t full = sbase + C::kBar, empty = full + 8 * C::kStages;
+    // the combine may take its place on the SMs already; it waits for this kernel's end before it reads
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
+        tc::prefetch_tmap(&p.tk);
+        tc::prefetch_tmap(&p.tv);
         // a bounded wait of an earlier kernel ran out: do no work until usp_check clears it
         skip = *reinterpret_cast<volatile int *>(p.status) != 0;
         for (int i = 0; i < C::kStages; ++i) {
@@ -496,6 +504,8 @@ int launch_paged_decode(const PagedArgs &a, int rows, int n_hi, const PartSpace 
     p.s.tb = rows / a.G; p.s.causal = a.causal;
     p.s.n_lo = 0; p.s.n_hi = n_hi;
     p.s.over = kOver; p.s.min_span = kMinSpan;
+    p.s.inv_ctas = 1.0f / (float)w.ctas;
+    p.s.by_tb = FastDiv((uint32_t)p.s.tb); p.s.by_G = FastDiv((uint32_t)a.G);
     p.w = w;
     p.q = static_cast<const __nv_bfloat16 *>(a.q);
     p.out = static_cast<__nv_bfloat16 *>(a.out);

@@ -2,8 +2,8 @@
 //
 // A unit is one request, one KV head and one block of `tb` new tokens (tb * G query rows); its cost is
 // the keys its last token sees plus a constant `over` for its start and end. Units are ordered request
-// by request, KV head by KV head, block by block, and the total cost W is cut into equal spans, one per
-// CTA, at key-tile boundaries inside units. So every CTA gets the same number of keys however ragged
+// by request, KV head by KV head, block by block, and the total cost W is cut into spans of one length, a
+// span per CTA, at key-tile boundaries inside units. So every CTA gets the same number of keys however ragged
 // the lengths are, and a long sequence with few rows is spread over all SMs. The lengths are device
 // data: every CTA sums the costs itself (one scan over the requests, about a microsecond for the first
 // few hundred), which costs less than a planning launch and keeps the call free of host copies.
@@ -24,7 +24,9 @@ struct SchedIn {
     int32_t causal;
     int32_t n_lo, n_hi;  // the requests of this kernel: n_lo < new tokens <= n_hi
     int32_t over;        // constant cost of a unit, in keys
-    int32_t min_span;    // keys per CTA below which fewer CTAs work (more than a key tile)
+    int32_t min_span;    // keys per CTA below which fewer CTAs work (more than over + a key tile)
+    float inv_ctas;      // 1 / CTAs of the launch
+    FastDiv by_tb, by_G;
 };
 
 // A request's units: block b of each head holds new tokens [b tb, min((b + 1) tb, n)).
@@ -54,7 +56,7 @@ __device__ __forceinline__ ReqUnits req_units(const SchedIn &s, int32_t i) {
     r.n = q.n > s.n_lo && q.n <= s.n_hi ? q.n : 0;
     r.kv = q.kv;
     r.p0 = (int64_t)q.kv - q.n;
-    r.nb = (r.n + s.tb - 1) / s.tb;
+    r.nb = (int32_t)s.by_tb.div((uint32_t)(r.n + s.tb - 1));
     r.head_cost = r.n > 0 ? unit_prefix(s, r, r.nb - 1) + s.over + unit_keys(s, r, r.nb - 1) : 0;
     return r;
 }
@@ -67,27 +69,34 @@ struct UnitPos {
 struct SchedShared {
     int64_t warp_sum[32];
     int64_t before[2];
+    ReqUnits r[2];
     int32_t req[2];
 };
 
+// One stretch of a unit's key tiles [t0, t1), of `tiles` in all, that this CTA computes.
+struct Segment {
+    int64_t tok0;        // first row of q
+    int32_t ntok, head;  // tokens of the block; KV head
+    int32_t req, b;
+    int32_t p0, kv;      // position of the block's first token; keys of the request
+    int32_t t0, t1, tiles;
+};
+
 struct Sched {
-    int64_t W;         // total cost
-    int32_t ctas;      // CTAs that work
+    int64_t span;      // cost per CTA: CTA c covers [c span, (c + 1) span)
     UnitPos at, end;   // this CTA's span
     ReqUnits r;        // the request of `at`
     int64_t before;    // cost before that request
+    Segment tail;      // a segment put off to the end (put_off; see sched_init)
+    bool put_off;
 };
 
-__device__ __forceinline__ int64_t span_start(int64_t W, int32_t ctas, int32_t c) {
-    return W / ctas * c + W % ctas * c / ctas;  // floor(W c / ctas) without overflow
-}
-
-// the last CTA whose span begins before cost x (0 < x <= W)
-__device__ __forceinline__ int32_t span_of(int64_t W, int32_t ctas, int64_t x) {
-    int32_t k = (int32_t)((double)x / (double)W * ctas);
-    k = max(0, min(k, ctas - 1));
-    while (k > 0 && span_start(W, ctas, k) >= x) --k;
-    while (k + 1 < ctas && span_start(W, ctas, k + 1) < x) ++k;
+// floor(x / d), 0 <= x, 0 < d, for quotients below 2^20: a rounded estimate and its correction (a 64-bit
+// division costs a few hundred cycles, and the start of a short call is a chain of these)
+__device__ __forceinline__ int32_t div_small(int64_t x, int64_t d) {
+    int32_t k = (int32_t)__fdividef((float)x, (float)d);
+    while ((int64_t)k * d > x) --k;
+    while ((int64_t)(k + 1) * d <= x) ++k;
     return k;
 }
 
@@ -95,7 +104,7 @@ template <int KT>
 __device__ __forceinline__ UnitPos unit_pos(const SchedIn &s, const ReqUnits &r, int32_t req, int64_t off) {
     UnitPos p;
     p.req = req;
-    p.head = (int32_t)(off / r.head_cost);
+    p.head = div_small(off, r.head_cost);  // fewer than 2^16 heads
     off -= p.head * r.head_cost;
     int32_t lo = 0, hi = r.nb;  // the last block that begins at or before off
     while (hi - lo > 1) {
@@ -109,79 +118,9 @@ __device__ __forceinline__ UnitPos unit_pos(const SchedIn &s, const ReqUnits &r,
     return p;
 }
 
-// Called by all NT threads of the CTA. False when this CTA has no work.
-template <int NT, int KT>
-__device__ bool sched_init(const SchedIn &s, SchedShared &sh, Sched &o) {
-    static_assert(NT % 32 == 0 && NT <= 1024, "whole warps");
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    // inclusive scan of x over the CTA; total: the sum
-    auto scan = [&](int64_t x, int64_t &total) {
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
-            if (lane >= d) x += y;
-        }
-        __syncthreads();
-        if (lane == 31) sh.warp_sum[warp] = x;
-        __syncthreads();
-        total = 0;
-        for (int w = 0; w < NT / 32; ++w) {
-            const int64_t y = sh.warp_sum[w];
-            if (w < warp) x += y;
-            total += y;
-        }
-        return x;
-    };
-    if (tid < 2) sh.req[tid] = s.nreq;
-    int64_t mine = 0;
-    for (int32_t i = tid; i < s.nreq; i += NT) mine += req_units(s, i).head_cost * s.hkv;
-    int64_t incl = scan(mine, o.W);
-    if (o.W == 0) return false;
-    o.ctas = (int32_t)min((int64_t)gridDim.x, max((int64_t)1, o.W / s.min_span));
-    const int32_t c = blockIdx.x;
-    if (c >= o.ctas) return false;
-    const int64_t x0 = span_start(o.W, o.ctas, c), x1 = span_start(o.W, o.ctas, c + 1);
-    int64_t carry = 0;
-    for (int32_t base = 0; base < s.nreq; base += NT) {
-        int64_t total = o.W;
-        if (s.nreq > NT) {
-            mine = base + tid < s.nreq ? req_units(s, base + tid).head_cost * s.hkv : 0;
-            incl = scan(mine, total);
-        }
-        const int64_t a = carry + incl - mine;
-        if (mine > 0 && a <= x0 && x0 < a + mine) {
-            sh.req[0] = base + tid;
-            sh.before[0] = a;
-        }
-        if (mine > 0 && a <= x1 && x1 < a + mine) {
-            sh.req[1] = base + tid;
-            sh.before[1] = a;
-        }
-        carry += total;
-        if (carry > x1) break;
-    }
-    __syncthreads();
-    const int32_t i0 = sh.req[0], i1 = sh.req[1];
-    o.before = sh.before[0];
-    o.r = req_units(s, i0);
-    o.at = unit_pos<KT>(s, o.r, i0, x0 - o.before);
-    o.end = UnitPos{s.nreq, 0, 0, 0};
-    if (i1 < s.nreq) o.end = unit_pos<KT>(s, i1 == i0 ? o.r : req_units(s, i1), i1, x1 - sh.before[1]);
-    return true;
-}
-
-// One stretch of a unit's key tiles [t0, t1), of `tiles` in all, that this CTA computes.
-struct Segment {
-    int64_t tok0;        // first row of q
-    int32_t ntok, head;  // tokens of the block; KV head
-    int32_t req, b;
-    int32_t p0, kv;      // position of the block's first token; keys of the request
-    int32_t t0, t1, tiles;
-};
-
-// the next segment of the span; false at its end
+// the next segment in the order of the units
 template <int KT>
-__device__ __forceinline__ bool sched_next(const SchedIn &s, Sched &o, Segment &g) {
+__device__ __forceinline__ bool sched_step(const SchedIn &s, Sched &o, Segment &g) {
     for (;;) {
         const bool last = o.at.req == o.end.req && o.at.head == o.end.head && o.at.b == o.end.b;
         if (o.at.req >= s.nreq || (last && o.end.t <= o.at.t)) return false;
@@ -217,6 +156,96 @@ __device__ __forceinline__ bool sched_next(const SchedIn &s, Sched &o, Segment &
     }
 }
 
+// Called by all NT threads of the CTA. False when this CTA has no work.
+template <int NT, int KT>
+__device__ bool sched_init(const SchedIn &s, SchedShared &sh, Sched &o) {
+    static_assert(NT % 32 == 0 && NT <= 1024, "whole warps");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // inclusive scan of x over the CTA; total: the sum
+    auto scan = [&](int64_t x, int64_t &total) {
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d) x += y;
+        }
+        __syncthreads();
+        if (lane == 31) sh.warp_sum[warp] = x;
+        __syncthreads();
+        total = 0;
+        for (int w = 0; w < NT / 32; ++w) {
+            const int64_t y = sh.warp_sum[w];
+            if (w < warp) x += y;
+            total += y;
+        }
+        return x;
+    };
+    if (tid < 2) sh.req[tid] = s.nreq;
+    int64_t mine = 0, W;
+    ReqUnits r{};
+    for (int32_t i = tid; i < s.nreq; i += NT) {
+        r = req_units(s, i);
+        mine += r.head_cost * s.hkv;
+    }
+    int64_t incl = scan(mine, W);
+    // one length for all spans; the factor covers the estimate's roundings, so that they cover W
+    o.span = max((int64_t)s.min_span, (int64_t)((float)W * s.inv_ctas * 1.000001f) + 1);
+    const int64_t x0 = blockIdx.x * o.span, x1 = x0 + o.span;
+    if (x0 >= W) return false;
+    int64_t carry = 0;
+    for (int32_t base = 0; base < s.nreq; base += NT) {
+        int64_t total = W;
+        if (s.nreq > NT) {
+            mine = 0;
+            if (base + tid < s.nreq) {
+                r = req_units(s, base + tid);
+                mine = r.head_cost * s.hkv;
+            }
+            incl = scan(mine, total);
+        }
+        const int64_t a = carry + incl - mine;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int64_t x = k ? x1 : x0;
+            if (mine > 0 && a <= x && x < a + mine) {
+                sh.req[k] = base + tid;
+                sh.before[k] = a;
+                sh.r[k] = r;
+            }
+        }
+        carry += total;
+        if (carry > x1) break;
+    }
+    __syncthreads();
+    const int32_t i0 = sh.req[0], i1 = sh.req[1];
+    o.before = sh.before[0];
+    o.r = sh.r[0];
+    o.at = unit_pos<KT>(s, o.r, i0, x0 - o.before);
+    o.end = UnitPos{s.nreq, 0, 0, 0};
+    if (i1 < s.nreq) o.end = unit_pos<KT>(s, sh.r[1], i1, x1 - sh.before[1]);
+    // A span that begins inside a unit takes that unit's rest last, if there is more: so all CTAs sweep
+    // the keys from the front at the same time, and those that share a KV head read it from L2 (chunk
+    // of 900 tokens over 64000 keys, 152 spans: every span at its own place re-reads 4 GB from HBM).
+    o.put_off = false;
+    if (o.at.t > 0 && !(o.end.req == o.at.req && o.end.head == o.at.head && o.end.b == o.at.b)) {
+        Segment g;
+        sched_step<KT>(s, o, g);
+        o.tail = g;
+        o.put_off = true;
+    }
+    return true;
+}
+
+// the next segment of the span; false at its end
+template <int KT>
+__device__ __forceinline__ bool sched_next(const SchedIn &s, Sched &o, Segment &g) {
+    if (sched_step<KT>(s, o, g)) return true;
+    if (!o.put_off) return false;
+    o.put_off = false;
+    g = o.tail;
+    return true;
+}
+
+
 // What the CTA that opens a unit and does not finish it leaves for the combine.
 struct PartHeader {
     int64_t tok0;
@@ -226,8 +255,8 @@ struct PartHeader {
     int32_t pad[3];
 };
 
-// The header of a segment with t0 == 0 and t1 < tiles. Such a segment is the span's last one, so `o`
-// still holds its request.
+// The header of the segment just returned, with t0 == 0 and t1 < tiles: the last one in the order of
+// the units, so `o` still holds its request.
 __device__ __forceinline__ PartHeader part_header(const SchedIn &s, const Sched &o, const Segment &g) {
     PartHeader h{};
     h.tok0 = g.tok0;
@@ -235,7 +264,7 @@ __device__ __forceinline__ PartHeader part_header(const SchedIn &s, const Sched 
     h.head = g.head;
     const int64_t end = o.before + (int64_t)g.head * o.r.head_cost +
                         (g.b + 1 < o.r.nb ? unit_prefix(s, o.r, g.b + 1) : o.r.head_cost);
-    h.last = span_of(o.W, o.ctas, end);
+    h.last = div_small(end - 1, o.span);  // fewer than 2^16 CTAs
     return h;
 }
 
