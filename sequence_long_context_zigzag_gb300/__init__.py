@@ -519,6 +519,22 @@ class UspAttention:
 
 
 # ---- paged K/V cache ---------------------------------------------------------------------------
+# Serving calls these once per layer and token, where a short call's GPU work is a few microseconds: the
+# checks of an argument layout (shapes, strides, dtypes, devices: nothing of its data) run once, and the
+# descriptor they end in is kept for the next call with the same layout.
+_layouts: dict = {}
+_MAX_LAYOUTS = 4096
+
+
+def _layout(*ts):
+    return [(t.shape, t.stride(), t.dtype, t.get_device()) for t in ts]
+
+
+def _keep(key, value):
+    if len(_layouts) >= _MAX_LAYOUTS:
+        _layouts.clear()
+    _layouts[key] = value
+    return value
 
 
 def _same_device(first: torch.Tensor, *ts):
@@ -563,17 +579,22 @@ def _block_table(t: torch.Tensor, nreq: int) -> int:
     return _dense_rows("block_table", t) or t.shape[1]
 
 
-def _with_stream(dev: torch.device, stream, call):
+# the raw handle of a device's current stream, without the Stream object where torch has the call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _with_stream(index: int, stream, call):
     """call(raw stream) with the tensors' device current and, where ``stream`` is given, with it as the
     current stream, so that what the call allocates is ordered on the stream that uses it."""
     if stream is None:
-        if torch.cuda.current_device() == dev.index:
-            return call(torch.cuda.current_stream().cuda_stream)
-        with torch.cuda.device(dev):
-            return call(torch.cuda.current_stream().cuda_stream)
+        if torch.cuda.current_device() == index:
+            return call(_raw_stream(index))
+        with torch.cuda.device(index):
+            return call(_raw_stream(index))
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=dev)
-    _need(stream.device == dev, "the stream belongs to another device than the tensors")
+        stream = torch.cuda.ExternalStream(int(stream), device=index)
+    _need(stream.device.index == index, "the stream belongs to another device than the tensors")
     with torch.cuda.stream(stream):
         return call(stream.cuda_stream)
 
@@ -588,70 +609,71 @@ def usp_page_plan(ctx_lens, new_lens, free_pages, free_head, block_table, page_s
     ``max_tokens`` new tokens (-1: none), cumulative new lengths, keys per request, and (new tokens, the
     next free head, tokens left without a slot, largest kv length). The next step passes kv_lens as
     ctx_lens and counts[1:2] as free_head, with other output tensors than its inputs."""
-    nreq = ctx_lens.numel()
-    for name, t in (("ctx_lens", ctx_lens), ("new_lens", new_lens)):
-        _i32(name, t, nreq)
-    _i32("free_pages", free_pages)
-    _i32("free_head", free_head, 1)
-    dev = _same_device(ctx_lens, new_lens, free_pages, free_head, block_table)
-    d = UspPlanDims(num_pages, _block_table(block_table, nreq), free_pages.numel(), max_tokens, nreq,
-                    block_table.shape[1], page_size)
+    key = ("plan", *_layout(ctx_lens, new_lens, free_pages, free_head, block_table), page_size, num_pages, max_tokens)
+    d = _layouts.get(key)
+    if d is None:
+        nreq = ctx_lens.numel()
+        for name, t in (("ctx_lens", ctx_lens), ("new_lens", new_lens)):
+            _i32(name, t, nreq)
+        _i32("free_pages", free_pages)
+        _i32("free_head", free_head, 1)
+        _need(max_tokens >= 0, "max_tokens must not be negative")
+        stride = _block_table(block_table, nreq)
+        _same_device(ctx_lens, new_lens, free_pages, free_head, block_table)
+        d = _keep(key, UspPlanDims(num_pages, stride, free_pages.numel(), max_tokens, nreq, block_table.shape[1],
+                                   page_size))
+    dev = ctx_lens.device
 
     def call(raw):
-        outs = []
-        for name, t, n in (("slot_map", slot_map, max_tokens), ("cu_new", cu_new, nreq + 1),
-                           ("kv_lens", kv_lens, nreq), ("counts", counts, 4)):
+        def output(name, t, n):
             if t is None:
-                t = torch.empty(n, dtype=torch.int32, device=dev)
-            else:
-                _i32(name, t, n)
-                _same_device(ctx_lens, t)
-            outs.append(t)
+                return torch.empty(n, dtype=torch.int32, device=dev)
+            _i32(name, t, n)
+            _same_device(ctx_lens, t)
+            return t
+        slots, cu = output("slot_map", slot_map, max_tokens), output("cu_new", cu_new, d.nreq + 1)
+        kv, cnt = output("kv_lens", kv_lens, d.nreq), output("counts", counts, 4)
         _abi.check("usp_page_plan", _abi.load().usp_page_plan(
             ctx_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), free_head.data_ptr(),
-            block_table.data_ptr(), outs[0].data_ptr(), outs[1].data_ptr(), outs[2].data_ptr(), outs[3].data_ptr(),
-            d, raw))
-        return tuple(outs)
+            block_table.data_ptr(), slots.data_ptr(), cu.data_ptr(), kv.data_ptr(), cnt.data_ptr(), d, raw))
+        return slots, cu, kv, cnt
 
-    _need(max_tokens >= 0, "max_tokens must not be negative")
-    return _with_stream(dev, stream, call)
+    return _with_stream(dev.index, stream, call)
 
 
 def usp_cache_append(k, v, k_cache, v_cache, slot_map, stream=None):
     """Write the rows of k and v (tokens, hkv, hd) into their slots of the caches
     (num_pages, hkv, page_size, hd), in place; a token with slot -1 is skipped. The first axis of every
     tensor may be strided (slices of a fused projection, a cache that interleaves K and V)."""
-    tokens = k.shape[0]
-    d = _cache_dims(k_cache, v_cache)
-    if k.dim() != 3 or k.shape[1] != d.hkv or k.shape[2] != d.hd or v.shape != k.shape:
-        raise ValueError("k and v must be (tokens, hkv, hd) like the cache")
-    if k.dtype != k_cache.dtype or v.dtype != k_cache.dtype:
-        raise ValueError("dtype mismatch")
-    _i32("slot_map", slot_map, tokens)
-    dev = _same_device(k, v, k_cache, v_cache, slot_map)
-    ks, vs = _dense_rows("k", k), _dense_rows("v", v)
-    _with_stream(dev, stream, lambda raw: _abi.check("usp_cache_append", _abi.load().usp_cache_append(
-        k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), slot_map.data_ptr(), tokens, ks, vs, d,
-        raw)))
+    key = ("append", *_layout(k, v, k_cache, v_cache, slot_map))
+    spec = _layouts.get(key)
+    if spec is None:
+        d = _cache_dims(k_cache, v_cache)
+        if k.dim() != 3 or k.shape[1] != d.hkv or k.shape[2] != d.hd or v.shape != k.shape:
+            raise ValueError("k and v must be (tokens, hkv, hd) like the cache")
+        if k.dtype != k_cache.dtype or v.dtype != k_cache.dtype:
+            raise ValueError("dtype mismatch")
+        _i32("slot_map", slot_map, k.shape[0])
+        strides = _dense_rows("k", k), _dense_rows("v", v)
+        _same_device(k, v, k_cache, v_cache, slot_map)
+        spec = _keep(key, (k.shape[0], *strides, d))
+    _with_stream(k.get_device(), stream, lambda raw: _abi.check("usp_cache_append", _abi.load().usp_cache_append(
+        k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), slot_map.data_ptr(), *spec, raw)))
     return k_cache, v_cache
 
 
-def _paged_desc(q, k_cache, v_cache, block_table, nreq, max_new, causal, scale, out):
+def _paged_desc(q, k_cache, v_cache, block_table, nreq, max_new, causal, scale, out_stride):
     d = _cache_dims(k_cache, v_cache)
     if q.dim() != 3 or q.shape[2] != d.hd or q.dtype != k_cache.dtype:
         raise ValueError("q must be (tokens, hq, hd), of the cache's head dim and dtype")
-    T, hq, _ = q.shape
-    if out is not None and (out.shape != q.shape or out.dtype != q.dtype):
-        raise ValueError("out must match q")
     stride = _block_table(block_table, nreq)
-    return UspPagedDesc(d, T, _dense_rows("q", q), 0 if out is None else _dense_rows("out", out), stride, nreq,
-                        block_table.shape[1], hq, T if max_new is None else max_new, int(bool(causal)),
-                        0.0 if scale is None else scale)
+    return UspPagedDesc(d, q.shape[0], _dense_rows("q", q), out_stride, stride, nreq, block_table.shape[1], q.shape[1],
+                        q.shape[0] if max_new is None else max_new, int(bool(causal)), 0.0 if scale is None else scale)
 
 
 def usp_paged_attn_workspace_size(q, k_cache, block_table, max_new: Optional[int] = None) -> int:
     """Workspace bytes usp_paged_attn needs for these shapes (on q's device)."""
-    d = _paged_desc(q, k_cache, k_cache, block_table, block_table.shape[0], max_new, True, None, None)
+    d = _paged_desc(q, k_cache, k_cache, block_table, block_table.shape[0], max_new, True, None, 0)
     with torch.cuda.device(q.device):
         n = _abi.load().usp_paged_attn_workspace_size(d)
     _need(n > 0, "invalid paged attention shapes")
@@ -666,40 +688,46 @@ def usp_paged_attn(q, k_cache, v_cache, block_table, cu_new, kv_lens, max_new: O
     request i; caches (num_pages, hkv, page_size, hd); block_table (nreq, pages); kv_lens[i] keys.
     Returns (out, lse): (tokens, hq, hd) and fp32 (tokens, hq); rows of no request are left as they
     were (unset where the call allocates them). ``max_new``: the most new tokens of one request, where
-    the host knows it (1 for a decode step); it saves launches and does not change the result.
+    the host knows it (1 for a decode step); it saves launches and does not change what is computed.
     ``workspace``: at least usp_paged_attn_workspace_size bytes (allocated per call where not given)."""
-    nreq = kv_lens.numel()
-    _i32("cu_new", cu_new, nreq + 1)
-    _i32("kv_lens", kv_lens)
-    d = _paged_desc(q, k_cache, v_cache, block_table, nreq, max_new, causal, scale, out)
-    dev = _same_device(q, k_cache, v_cache, block_table, cu_new, kv_lens)
-    T, hq = q.shape[0], q.shape[1]
+    out_stride = 0
+    if out is not None:
+        if out.shape != q.shape or out.dtype != q.dtype:
+            raise ValueError("out must match q")
+        out_stride = _dense_rows("out", out)
+        _same_device(q, out)
+    key = ("attn", *_layout(q, k_cache, v_cache, block_table, cu_new, kv_lens), max_new, causal, scale, out_stride)
+    d = _layouts.get(key)
+    if d is None:
+        nreq = kv_lens.numel()
+        _i32("cu_new", cu_new, nreq + 1)
+        _i32("kv_lens", kv_lens)
+        d = _paged_desc(q, k_cache, v_cache, block_table, nreq, max_new, causal, scale, out_stride)
+        _same_device(q, k_cache, v_cache, block_table, cu_new, kv_lens)
+        _keep(key, d)
+    dev = q.device
 
     def call(raw):
         lib = _abi.load()
         o, l, w = out, lse, workspace
         if o is None:
             o = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        else:
-            _same_device(q, o)
         if l is None:
-            l = torch.empty((T, hq), dtype=torch.float32, device=dev)
+            l = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
         else:
-            _need(l.shape == (T, hq) and l.dtype == torch.float32 and l.is_contiguous(),
+            _need(l.shape == q.shape[:2] and l.dtype == torch.float32 and l.is_contiguous(),
                   "lse must be contiguous fp32 (tokens, hq)")
             _same_device(q, l)
         if w is None:
-            n = lib.usp_paged_attn_workspace_size(d)
-            w = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
-        else:
-            _need(w.is_contiguous(), "workspace must be contiguous")
-            _same_device(q, w)
+            w = torch.empty(max(lib.usp_paged_attn_workspace_size(d), 1), dtype=torch.uint8, device=dev)
+        elif w.get_device() != dev.index or not w.is_contiguous():
+            raise ValueError("workspace must be contiguous, on the tensors' device")
         _abi.check("usp_paged_attn", lib.usp_paged_attn(
             q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), cu_new.data_ptr(),
             kv_lens.data_ptr(), o.data_ptr(), l.data_ptr(), d, w.data_ptr(), w.numel() * w.element_size(), raw))
         return o, l
 
-    return _with_stream(dev, stream, call)
+    return _with_stream(dev.index, stream, call)
 
 
 def default_scale(hd: int) -> float:

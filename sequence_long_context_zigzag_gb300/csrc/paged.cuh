@@ -32,6 +32,4 @@ __device__ __forceinline__ Request paged_request(const int32_t *cu, const int32_
     return Request{a, (int32_t)(b - a), (int32_t)min(max((int64_t)__ldg(kv + i), (int64_t)0), max_keys)};
 }
 
-int launch_paged_simt(const PagedArgs &a, int dtype, cudaStream_t s);
-
 }  // namespace usp

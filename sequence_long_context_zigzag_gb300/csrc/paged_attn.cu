@@ -48,33 +48,36 @@ PagedArgs paged_args(const usp_paged_desc &d) {
     return a;
 }
 
-// Which kernels run, and the CTAs and rows of their partials.
+// Which kernels run: one for units of few query rows (a request's new tokens x G), one for units of many,
+// or both, each with the CTAs (0: not launched) and unit rows of its partials.
 struct Route {
-    int decode_rows, decode_ctas;  // units of few rows (CTAs 0: not launched)
-    int chunk_ctas;                // units of many rows
-    int split;                     // the most new tokens of a request that the decode kernel takes
+    int few_ctas, few_rows, many_ctas, many_rows;
+    int split;  // the most new tokens of a request that the kernel for few rows takes
 };
 
+// Up to 32 rows of a KV head (bf16; 16 in fp32) a call is bound by reading the cache, and the kernels for
+// few rows read it at the HBM rate; above, their re-reading of K/V per unit costs more than the others' idle rows.
 Route route(const usp_paged_desc &d, int sms) {
     Route r{};
-    const int G = d.hq / d.cache.hkv;
+    const bool bf16 = d.cache.dtype == USP_BF16;
+    const int G = d.hq / d.cache.hkv, most = bf16 ? 32 : 16;
     const int64_t rows = G * (int64_t)std::max(1, d.max_new);
-    if (d.cache.dtype != USP_BF16) return r;
     r.split = INT_MAX;
-    if (rows > 32) {
-        r.chunk_ctas = sms;
-        r.split = 32 / G;
+    if (rows > most || G > (bf16 ? 32 : f32_rows(false))) {
+        r.many_ctas = bf16 ? sms : f32_ctas(sms, true, d.cache.hd);
+        r.many_rows = bf16 ? kChunkRows : f32_rows(true);
+        r.split = G > (bf16 ? 32 : f32_rows(false)) ? 0 : most / G;
     }
     if (r.split > 0) {
-        r.decode_rows = rows <= 16 ? 16 : 32;
-        r.decode_ctas = decode_ctas(sms, r.decode_rows);
+        r.few_rows = bf16 ? (rows <= 16 ? 16 : 32) : f32_rows(false);
+        r.few_ctas = bf16 ? decode_ctas(sms, r.few_rows) : f32_ctas(sms, false, d.cache.hd);
     }
     return r;
 }
 
 size_t workspace_bytes_of(const Route &r, int hd) {
-    return 256 + (r.decode_ctas ? part_bytes(r.decode_ctas, r.decode_rows, hd) : 0) +
-           (r.chunk_ctas ? part_bytes(r.chunk_ctas, kChunkRows, hd) : 0);
+    return (r.few_ctas ? part_bytes(r.few_ctas, r.few_rows, hd) : 0) +
+           (r.many_ctas ? part_bytes(r.many_ctas, r.many_rows, hd) : 0);
 }
 
 PartSpace part_space(char *&at, int ctas, int rows, int hd) {
@@ -121,17 +124,20 @@ int usp_paged_attn(const void *q, const void *k_cache, const void *v_cache, cons
     a.table = block_table; a.cu = cu_new; a.kv = kv_lens;
     a.out = out; a.lse = lse;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (d.cache.dtype != USP_BF16) return launch_paged_simt(a, d.cache.dtype, s);
+    const bool bf16 = d.cache.dtype == USP_BF16;
     char *at = static_cast<char *>(workspace);
     CombineArgs c{};
     c.out = out; c.lse = lse; c.out_stride = a.out_stride; c.G = a.G; c.hq = a.hq;
-    if (r.chunk_ctas) {
-        c.w[0] = part_space(at, r.chunk_ctas, kChunkRows, a.hd);
-        if ((rc = launch_paged_chunk(a, r.split, c.w[0], s))) return rc;
+    if (r.many_ctas) {
+        c.w[0] = part_space(at, r.many_ctas, r.many_rows, a.hd);
+        rc = bf16 ? launch_paged_chunk(a, r.split, c.w[0], s) : launch_paged_f32(a, true, r.split, INT_MAX, c.w[0], s);
+        if (rc) return rc;
     }
-    if (r.decode_ctas) {
-        c.w[1] = part_space(at, r.decode_ctas, r.decode_rows, a.hd);
-        if ((rc = launch_paged_decode(a, r.decode_rows, r.split, c.w[1], s))) return rc;
+    if (r.few_ctas) {
+        c.w[1] = part_space(at, r.few_ctas, r.few_rows, a.hd);
+        rc = bf16 ? launch_paged_decode(a, r.few_rows, r.split, c.w[1], s)
+                  : launch_paged_f32(a, false, 0, r.split, c.w[1], s);
+        if (rc) return rc;
     }
     return launch_paged_combine(c, a.hd, d.cache.dtype, s);
 }

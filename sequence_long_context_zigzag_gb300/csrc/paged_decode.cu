@@ -438,7 +438,8 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const CombineArgs a)
             float wgt = 0.f, l = 0.f;
             if (base + lane < parts) {
                 const float *s = slot(base + lane);
-                wgt = tc::ex2(s[(size_t)w.rows * HD + r] - Mb);
+                const float d = s[(size_t)w.rows * HD + r] - Mb;
+                wgt = sizeof(T) == 4 ? exp2f(d) : tc::ex2(d);  // the fp32 path has no fast functions
                 l = wgt * s[(size_t)w.rows * (HD + 1) + r];
             }
 #pragma unroll
@@ -459,7 +460,7 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const CombineArgs a)
         T *o = static_cast<T *>(a.out) + tok * a.out_stride + (int64_t)head * HD + lane * E;
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] = (T)(acc[e] * inv);
-        if (lane == 0) a.lse[tok * a.hq + head] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
+        if (lane == 0) a.lse[tok * a.hq + head] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
     }
 }
 
