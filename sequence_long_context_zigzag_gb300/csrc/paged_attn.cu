@@ -127,7 +127,8 @@ int usp_paged_attn(const void *q, const void *k_cache, const void *v_cache, cons
     const bool bf16 = d.cache.dtype == USP_BF16;
     char *at = static_cast<char *>(workspace);
     CombineArgs c{};
-    c.out = out; c.lse = lse; c.out_stride = a.out_stride; c.G = a.G; c.hq = a.hq;
+    c.out = out; c.lse = lse; c.out_stride = a.out_stride;
+    c.G = a.G; c.hq = a.hq; c.by_G = FastDiv((uint32_t)a.G);
     if (r.many_ctas) {
         c.w[0] = part_space(at, r.many_ctas, r.many_rows, a.hd);
         rc = bf16 ? launch_paged_chunk(a, r.split, c.w[0], s) : launch_paged_f32(a, true, r.split, INT_MAX, c.w[0], s);

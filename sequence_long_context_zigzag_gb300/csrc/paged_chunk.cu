@@ -6,8 +6,8 @@
 // so grouped heads share every K/V tile that is loaded, and a chunk of 128 / G tokens fills a tile.
 //
 // What bounds it: from about 290 rows per KV head on, the tensor cores and the exponentials (the
-// unit's two tiles keep both busy in turn); below that, HBM. Roles of a CTA (one per SM), each walking the
-// CTA's span of the work (paged_sched.cuh) without a CTA-wide barrier:
+// unit's two tiles keep both busy in turn); below that, HBM. Roles of a CTA (one per SM), which run through
+// the CTA's span of the work (paged_sched.cuh) without a CTA-wide barrier:
 //   warps 0-3, 4-7  softmax of Q tile 0 / 1, one thread per query row: S from tensor memory, mask, running
 //                   maximum, P = 2^(S scale log2(e) - m) as bf16 back over S (the A operand of P V), rescale
 //                   of O when the maximum grows by more than 2^8; at a segment's end out and lse, or the
@@ -16,7 +16,8 @@
 //                   through a ring of stages, one box of a page per lane, page numbers read ahead;
 //   warps 9, 10     one MMA issuer per Q tile: S_i = Q_i K^T, O_i += P_i V, taking turns so that one tile's
 //                   products run under the other tile's softmax;
-//   warp 11         idle; with 8-10 the warpgroup that gives registers to the softmax (setmaxnreg).
+//   warp 11         walks the span and hands its segments to the other roles through a ring; with 8-10 it
+//                   is the warpgroup that gives registers to the softmax (setmaxnreg).
 //   TMEM: S0 [0,128) S1 [128,256) O0 [256,256+hd) O1 [256+hd,256+2hd); P_i lies over S_i.
 // Rows of the last page behind the request's last key may hold NaN, and 0 x NaN would spread in P V: the
 // softmax warps clear those rows of V's stage in shared memory before they hand P over.
@@ -39,8 +40,9 @@ constexpr int kSoftmaxWarps = 8;
 constexpr int kWarps = kSoftmaxWarps + 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kProducerWarp = kSoftmaxWarps;
-constexpr int kMmaWarp = kSoftmaxWarps + 1;  // Q tile 0's issuer; allocates and frees tensor memory
-constexpr int kMmaWarp1 = kSoftmaxWarps + 2;
+constexpr int kMmaWarp = kSoftmaxWarps + 1;  // Q tile 0's issuer (tile 1's follows); allocates and frees tensor memory
+constexpr int kWalkWarp = kSoftmaxWarps + 3;
+constexpr int kSegReaders = kSoftmaxWarps + 3;  // the softmax warps, the producer and the issuers
 // the warpgroups' shares (setmaxnreg) add up to exactly the launch's registers
 constexpr int kLaunchRegs = (65536 / kThreads) / 8 * 8;
 constexpr int kSoftmaxRegs = 208;
@@ -75,9 +77,12 @@ template <int HD> struct Cfg {
     static constexpr int TURN = DONE + 2;             // [2]
     static constexpr int Q_EMPTY = TURN + 2;
     static constexpr int O_EMPTY = Q_EMPTY + 1;       // [2]
-    static constexpr int kNumBars = O_EMPTY + 2;
-    static constexpr int kSlot = kBar + kNumBars * 8;  // tensor memory address, skip flag
-    static constexpr int kSmem = kSlot + 16 + 1024;    // + slack for the 1024-byte alignment
+    static constexpr int SEG_FULL = O_EMPTY + 2;      // [kSegSlots]
+    static constexpr int SEG_EMPTY = SEG_FULL + kSegSlots;
+    static constexpr int kNumBars = SEG_EMPTY + kSegSlots;
+    static constexpr int kSlot = kBar + (kNumBars * 8 + 15) / 16 * 16;  // tensor memory address, skip flag
+    static constexpr int kSeg = kSlot + 16;
+    static constexpr int kSmem = kSeg + kSegSlots * (int)sizeof(SegMsg) + 1024;  // + slack for the alignment
 };
 
 struct ChunkParams {
@@ -94,48 +99,64 @@ struct ChunkParams {
     float scale_log2;
 };
 
-// What a Q tile needs of a key tile: nothing, all of it, or its part under the mask.
-struct TileRange {
-    int32_t last;  // keys the tile's last token sees (0: no token)
-    int32_t all;   // keys every token of it sees
-};
-__device__ __forceinline__ TileRange tile_range(const ChunkParams &p, const Segment &g, int i) {
-    const int32_t a = i * p.tq_tokens, b = min(g.ntok, a + p.tq_tokens);
-    TileRange r{0, 0};
-    if (a >= b) return r;
-    r.last = p.s.causal ? max(0, min(g.kv, g.p0 + b)) : g.kv;
-    r.all = p.s.causal ? max(0, min(g.kv, g.p0 + a + 1)) : g.kv;
-    return r;
+// The walk: one thread hands out the segments and, at the end, the header of a unit left open.
+template <int HD>
+__device__ void walk_role(const ChunkParams &p, const SchedShared &sh, uint8_t *smem, uint32_t bar0) {
+    using C = Cfg<HD>;
+    SegMsg *ring = reinterpret_cast<SegMsg *>(smem + C::kSeg);
+    Sched sc;
+    sched_begin<kN>(p.s, sh, sc);
+    PartHeader opened{};
+    for (uint32_t n = 0;; ++n) {
+        Segment g;
+        const bool more = sched_next<kN>(p.s, sc, g);
+        if (!tc::mbar_wait(bar0 + 8u * (C::SEG_EMPTY + n % kSegSlots), ((n / kSegSlots) & 1u) ^ 1u, p.status,
+                           USP_ERR_TIMEOUT, kWaitLimitNs)) {
+            opened = PartHeader{};
+            break;
+        }
+        SegMsg m{};
+        if (more) {
+            m.tok0 = g.tok0; m.ntok = g.ntok; m.head = g.head; m.req = g.req; m.p0 = g.p0; m.kv = g.kv;
+            m.t0 = g.t0; m.t1 = g.t1; m.tiles = g.tiles;
+            for (int i = 0; i < 2; ++i) {
+                const int a = i * p.tq_tokens, b = min(g.ntok, a + p.tq_tokens);  // the Q tile's tokens
+                if (a >= b) continue;
+                const int last = p.s.causal ? max(0, min(g.kv, g.p0 + b)) : g.kv;
+                const int all = p.s.causal ? max(0, min(g.kv, g.p0 + a + 1)) : g.kv;
+                m.act[i] = (last + kN - 1) / kN;
+                m.full[i] = all / kN;
+            }
+        }
+        ring[n % kSegSlots] = m;
+        tc::mbar_arrive(bar0 + 8u * (C::SEG_FULL + n % kSegSlots));
+        if (!more) break;
+        if (g.t0 == 0 && g.t1 < g.tiles) opened = part_header(p.s, sc, g);
+    }
+    p.w.head[blockIdx.x] = opened;
 }
 
-// The CTA's key tiles as one stream across its segments (segments without a tile are passed over).
-struct Cursor {
-    Sched sc;
-    Segment g;
-    int32_t kt;
-    bool live;
-};
-struct Tile {
-    bool act[2];
-    bool first;  // first tile of its segment
-};
-__device__ __forceinline__ bool cursor_next(const ChunkParams &p, Cursor &c, Tile &t) {
-    t.first = false;
-    while (!(c.live && c.kt < c.g.t1)) {
-        c.live = sched_next<kN>(p.s, c.sc, c.g);
-        if (!c.live) return false;
-        c.kt = c.g.t0;
-        t.first = true;
-    }
-    for (int i = 0; i < 2; ++i) t.act[i] = c.kt * kN < tile_range(p, c.g, i).last;
-    ++c.kt;
+// The next segment, for a whole warp (all lanes call) or a single thread; ntok == 0 at the end. False
+// after a failed wait.
+template <int HD, bool kWarp>
+__device__ __forceinline__ bool next_segment(const ChunkParams &p, const uint8_t *smem, uint32_t bar0, uint32_t &n,
+                                             SegMsg &g) {
+    using C = Cfg<HD>;
+    bool ok = tc::mbar_wait(bar0 + 8u * (C::SEG_FULL + n % kSegSlots), (n / kSegSlots) & 1u, p.status, USP_ERR_TIMEOUT,
+                            kWaitLimitNs);
+    if (kWarp) ok = __all_sync(0xffffffffu, ok);
+    if (!ok) return false;
+    g = reinterpret_cast<const SegMsg *>(smem + C::kSeg)[n % kSegSlots];
+    if (kWarp) __syncwarp();
+    if (!kWarp || (threadIdx.x & 31) == 0) tc::mbar_arrive(bar0 + 8u * (C::SEG_EMPTY + n % kSegSlots));
+    ++n;
     return true;
 }
 
 // The producer warp. Lane l < boxes loads box l of each K and V tile: column half l / pieces, page piece
 // l % pieces; lane 0 loads Q too.
 template <int HD>
-__device__ void producer_role(const ChunkParams &p, Sched &sc, uint32_t sbase, uint32_t bar0) {
+__device__ void producer_role(const ChunkParams &p, const uint8_t *smem, uint32_t sbase, uint32_t bar0) {
     using C = Cfg<HD>;
     const int lane = threadIdx.x & 31;
     auto BAR = [&](int i) { return bar0 + 8u * i; };
@@ -146,10 +167,10 @@ __device__ void producer_role(const ChunkParams &p, Sched &sc, uint32_t sbase, u
     const int ps = 1 << p.log_ps, piece = min(ps, kN), pieces = kN / piece, nbox = pieces * C::kBoxes;
     const int half = lane / pieces, pc = lane % pieces;
     const uint32_t in_tile = half * C::kBoxBytes + pc * piece * 128;
-    uint32_t kfills = 0, vfills = 0, nq = 0;
+    uint32_t kfills = 0, vfills = 0, nq = 0, nseg = 0;
     bool ok = true;
-    Segment g;
-    while (ok && sched_next<kN>(p.s, sc, g)) {
+    SegMsg g;
+    while (ok && (ok = next_segment<HD, true>(p, smem, bar0, nseg, g)) && g.ntok > 0) {
         if (g.t0 >= g.t1) continue;
         if (nq > 0 && !(ok = wait(C::Q_EMPTY, (nq - 1) & 1u))) break;
         if (lane == 0) {
@@ -224,7 +245,7 @@ __device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint6
 // S_i(j+1) overwrites P_i(j) only after PV_i(j) has read it. Stages are released by both issuers; each
 // waits for a stage's fill before releasing it, also when its Q tile skips the tile.
 template <int HD>
-__device__ void mma_role(const ChunkParams &p, Cursor &cs, uint32_t sbase, uint32_t bar0, uint32_t tmem, int i) {
+__device__ void mma_role(const ChunkParams &p, const uint8_t *smem, uint32_t sbase, uint32_t bar0, uint32_t tmem, int i) {
     using C = Cfg<HD>;
     auto BAR = [&](int k) { return bar0 + 8u * k; };
     auto wait = [&](int bar, uint32_t parity) {
@@ -236,23 +257,38 @@ __device__ void mma_role(const ChunkParams &p, Cursor &cs, uint32_t sbase, uint3
     auto stage_off = [](uint32_t st) { return (uint64_t)((st * C::kTileBytes) >> 4); };
     const uint32_t tS = tmem + 128u * i, tO = tmem + 256u + (uint32_t)(HD * i);
     const int my_turn = C::TURN + i, other_turn = C::TURN + (1 - i);
-    uint32_t turns = 0;
-    Tile cur, nxt;
-    bool have = false, ok = true;
+    uint32_t turns = 0, nseg = 0;
+    // the tiles of all segments as one stream (segments without a tile are passed over): the next tile is
+    // kt of [kt, t1); this issuer's Q tile needs those below act_end
+    int kt = 0, t1 = 0, act_end = 0;
+    bool more = true;
+    bool have = false, cur_act = false, ok = true;
     uint32_t pc = 0, started = 0;  // P waits; a PV of the current segment has been issued
     uint32_t nq = 0, no = 0;       // Q loads consumed; O_i read-outs handed to the softmax
     uint32_t j = 0;                // tiles of the stream
     if (i == 1) tc::mbar_arrive(BAR(other_turn));  // issuer 1's empty "burst -1"
     while (ok) {
-        const bool have_n = cursor_next(p, cs, nxt);
-        const bool boundary = have_n && nxt.first;
+        bool boundary = false;  // the next tile opens a segment
+        while (ok && more && kt >= t1) {
+            SegMsg g;
+            if (!(ok = next_segment<HD, false>(p, smem, bar0, nseg, g))) break;
+            if (!(more = g.ntok > 0)) break;
+            kt = g.t0;
+            t1 = g.t1;
+            act_end = i ? g.act[1] : g.act[0];
+            boundary = true;
+        }
+        if (!ok) break;
+        const bool have_n = more;
+        const bool nxt_act = have_n && kt < act_end;
+        ++kt;
         const uint32_t jn = have ? j + 1 : 0;
         const uint32_t stn = jn % C::kStages, phn = (jn / C::kStages) & 1u;
         bool turn_after_s = false;
         if (have) {
-            const bool last = !have_n || nxt.first;
+            const bool last = !have_n || boundary;
             const uint32_t st = j % C::kStages, ph = (j / C::kStages) & 1u;
-            const bool act = i ? cur.act[1] : cur.act[0];
+            const bool act = cur_act;
             if (last) tc::mma_commit(BAR(C::Q_EMPTY));  // this issuer's S products of the segment are issued
             if (!(ok = wait(C::V_FULL + st, ph))) break;
             if (act && !(ok = wait(C::P_FULL + i, pc & 1u))) break;
@@ -282,13 +318,13 @@ __device__ void mma_role(const ChunkParams &p, Cursor &cs, uint32_t sbase, uint3
             ++nq;
             if (!(ok = wait(C::K_FULL + stn, phn))) break;
         }
-        if (i ? nxt.act[1] : nxt.act[0]) {
+        if (nxt_act) {
             issue_s<HD>(tS, qdesc, kdesc0 + stage_off(stn));
             tc::mma_commit(BAR(C::S_FULL + i));
         }
         tc::mma_commit(BAR(C::K_EMPTY + stn));
         if (turn_after_s) tc::mbar_arrive(BAR(other_turn));
-        cur = nxt;
+        cur_act = nxt_act;
         have = true;
         j = jn;
     }
@@ -303,7 +339,7 @@ __device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
 // on across segments. False after a failed wait (the whole warp leaves; the others' waits end by the
 // recorded status).
 template <int HD>
-__device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const Segment &g, uint8_t *smem, uint32_t bar0,
+__device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegMsg &g, uint8_t *smem, uint32_t bar0,
                                                 uint32_t tmem, int i, uint32_t &ns, uint32_t &no, uint32_t &nt) {
     using C = Cfg<HD>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wq = warp & 3;
@@ -311,7 +347,6 @@ __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const Segm
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     const uint32_t tS = tmem + lane_off + 128u * (uint32_t)i;
     const uint32_t tO = tmem + lane_off + 256u + (uint32_t)(HD * i);
-    const TileRange range = tile_range(p, g, i);
     uint32_t rt, rh;
     p.s.by_G.divmod((uint32_t)row, rt, rh);
     const int tok = i * p.tq_tokens + (int)rt;  // token of the segment's block
@@ -323,9 +358,9 @@ __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const Segm
     bool any = false, ok = true;
     const uint32_t nt0 = nt;
     nt += (uint32_t)(g.t1 - g.t0);
-    const int act_end = min(g.t1, (range.last + kN - 1) / kN);
+    const int act_end = min(g.t1, i ? g.act[1] : g.act[0]), full_end = i ? g.full[1] : g.full[0];
     for (int kt = g.t0; kt < act_end; ++kt) {
-        const bool full = (kt + 1) * kN <= range.all;
+        const bool full = kt < full_end;
         ok = tc::mbar_wait(bar0 + 8u * (C::S_FULL + i), ns & 1u, p.status, USP_ERR_TIMEOUT, kWaitLimitNs);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -483,8 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kSlot);
     volatile uint32_t *skip_flag = tmem_slot + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    Sched sc;
-    if (!sched_init<kThreads, kN>(p.s, sh, sc)) {  // the same for every thread
+    if (!sched_scan<kThreads>(p.s, sh)) {  // the same for every thread
         if (threadIdx.x == 0) p.w.head[blockIdx.x] = PartHeader{};
         return;
     }
@@ -502,6 +536,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         }
         tc::mbar_init(bar0 + 8u * C::Q_FULL, 1);
         tc::mbar_init(bar0 + 8u * C::Q_EMPTY, 2);
+        for (int i = 0; i < kSegSlots; ++i) {
+            tc::mbar_init(bar0 + 8u * (C::SEG_FULL + i), 1);
+            tc::mbar_init(bar0 + 8u * (C::SEG_EMPTY + i), kSegReaders);
+        }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(bar0 + 8u * (C::S_FULL + i), 1);
             tc::mbar_init(bar0 + 8u * (C::P_FULL + i), 4);
@@ -524,30 +562,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     if (warp >= kSoftmaxWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
         if (!skip) {
-            if (warp == kProducerWarp) {
-                producer_role<HD>(p, sc, sbase, bar0);
-            } else if ((warp == kMmaWarp || warp == kMmaWarp1) && lane == 0) {
-                Cursor cs;
-                cs.sc = sc;
-                cs.kt = 0;
-                cs.live = false;
-                mma_role<HD>(p, cs, sbase, bar0, tmem, warp - kMmaWarp);
-            }
+            if (warp == kProducerWarp) producer_role<HD>(p, smem, sbase, bar0);
+            else if (warp == kWalkWarp && lane == 0) walk_role<HD>(p, sh, smem, bar0);
+            else if (warp != kWalkWarp && lane == 0) mma_role<HD>(p, smem, sbase, bar0, tmem, warp - kMmaWarp);
             __syncwarp();
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-        PartHeader opened{};
-        if (!skip) {
-            uint32_t ns = 0, no = 0, nt = 0;
-            Segment g;
-            while (sched_next<kN>(p.s, sc, g)) {
-                if (!softmax_segment<HD>(p, g, smem, bar0, tmem, warp >> 2, ns, no, nt)) break;
-                if (threadIdx.x == 0 && g.t0 == 0 && g.t1 < g.tiles) opened = part_header(p.s, sc, g);
-            }
-        }
-        if (threadIdx.x == 0) p.w.head[blockIdx.x] = opened;
+        uint32_t ns = 0, no = 0, nt = 0, nseg = 0;
+        SegMsg g;
+        while (!skip && next_segment<HD, true>(p, smem, bar0, nseg, g) && g.ntok > 0)
+            if (!softmax_segment<HD>(p, g, smem, bar0, tmem, warp >> 2, ns, no, nt)) break;
     }
+    if (skip && threadIdx.x == 0) p.w.head[blockIdx.x] = PartHeader{};
     tc::fence_before_sync();
     __syncthreads();
     if (warp == kMmaWarp) {

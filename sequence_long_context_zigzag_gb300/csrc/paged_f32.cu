@@ -69,11 +69,22 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_f32_few_kernel(const __g
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int srow = lane >> 2, skey = lane & 3;  // the score this lane ends up with
-    Sched sc;
-    PartHeader opened{};
-    if (sched_init<kFewThreads, kFewKT>(p.s, sh, sc)) {
-        Segment g;
-        while (sched_next<kFewKT>(p.s, sc, g)) {
+    // thread 0 walks the span; its state stays in shared memory, out of the products' registers
+    __shared__ Sched sc;
+    __shared__ Segment seg;
+    __shared__ PartHeader opened;
+    if (tid == 0) opened = PartHeader{};
+    if (sched_scan<kFewThreads>(p.s, sh)) {
+        __syncthreads();
+        if (tid == 0) sched_begin<kFewKT>(p.s, sh, sc);
+        for (;;) {
+            if (tid == 0) {
+                if (!sched_next<kFewKT>(p.s, sc, seg)) seg.ntok = 0;
+                else if (seg.t0 == 0 && seg.t1 < seg.tiles) opened = part_header(p.s, sc, seg);
+            }
+            __syncthreads();
+            const Segment g = seg;
+            if (g.ntok == 0) break;
             const int rows = g.ntok * p.s.G;
             __syncthreads();  // the previous unit's reads of qs, xch and ml are done
             for (int x = tid; x < kFewRows * HD; x += kFewThreads) {
@@ -203,7 +214,6 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_f32_few_kernel(const __g
                     }
                 }
             }
-            if (!whole && g.t0 == 0) opened = part_header(p.s, sc, g);
         }
     }
     if (tid == 0) p.w.head[blockIdx.x] = opened;
@@ -242,11 +252,22 @@ __global__ void __launch_bounds__(kManyThreads, HD == 64 ? 2 : 1) paged_f32_many
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     float *qt = sm + C::kQ, *kt = sm + C::kK, *vs = sm + C::kV, *pt = sm + C::kP;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    Sched sc;
-    PartHeader opened{};
-    if (sched_init<kManyThreads, kManyKT>(p.s, sh, sc)) {
-        Segment g;
-        while (sched_next<kManyKT>(p.s, sc, g)) {
+    // thread 0 walks the span; its state stays in shared memory, out of the products' registers
+    __shared__ Sched sc;
+    __shared__ Segment seg;
+    __shared__ PartHeader opened;
+    if (tid == 0) opened = PartHeader{};
+    if (sched_scan<kManyThreads>(p.s, sh)) {
+        __syncthreads();
+        if (tid == 0) sched_begin<kManyKT>(p.s, sh, sc);
+        for (;;) {
+            if (tid == 0) {
+                if (!sched_next<kManyKT>(p.s, sc, seg)) seg.ntok = 0;
+                else if (seg.t0 == 0 && seg.t1 < seg.tiles) opened = part_header(p.s, sc, seg);
+            }
+            __syncthreads();
+            const Segment g = seg;
+            if (g.ntok == 0) break;
             const int rows = g.ntok * p.s.G;
             __syncthreads();  // the previous unit's products are done
             // Q scaled and transposed; lanes along the rows, so that the writes are free of conflicts
@@ -436,7 +457,6 @@ __global__ void __launch_bounds__(kManyThreads, HD == 64 ? 2 : 1) paged_f32_many
                     }
                 }
             }
-            if (!whole && g.t0 == 0) opened = part_header(p.s, sc, g);
         }
     }
     if (tid == 0) p.w.head[blockIdx.x] = opened;

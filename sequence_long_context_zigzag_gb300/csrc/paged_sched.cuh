@@ -68,9 +68,10 @@ struct UnitPos {
 
 struct SchedShared {
     int64_t warp_sum[32];
-    int64_t before[2];
+    int64_t before[2];  // of the span's first request [0], and of the one after its end [1]
     ReqUnits r[2];
     int32_t req[2];
+    int64_t span;
 };
 
 // One stretch of a unit's key tiles [t0, t1), of `tiles` in all, that this CTA computes.
@@ -87,7 +88,7 @@ struct Sched {
     UnitPos at, end;   // this CTA's span
     ReqUnits r;        // the request of `at`
     int64_t before;    // cost before that request
-    Segment tail;      // a segment put off to the end (put_off; see sched_init)
+    Segment tail;      // a segment put off to the end (see sched_begin)
     bool put_off;
 };
 
@@ -156,9 +157,10 @@ __device__ __forceinline__ bool sched_step(const SchedIn &s, Sched &o, Segment &
     }
 }
 
-// Called by all NT threads of the CTA. False when this CTA has no work.
-template <int NT, int KT>
-__device__ bool sched_init(const SchedIn &s, SchedShared &sh, Sched &o) {
+// Called by all NT threads of the CTA: finds the requests in which the CTA's span begins and ends. False
+// when this CTA has no work. `sh` is complete after the caller's next barrier.
+template <int NT>
+__device__ bool sched_scan(const SchedIn &s, SchedShared &sh) {
     static_assert(NT % 32 == 0 && NT <= 1024, "whole warps");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // inclusive scan of x over the CTA; total: the sum
@@ -188,8 +190,9 @@ __device__ bool sched_init(const SchedIn &s, SchedShared &sh, Sched &o) {
     }
     int64_t incl = scan(mine, W);
     // one length for all spans; the factor covers the estimate's roundings, so that they cover W
-    o.span = max((int64_t)s.min_span, (int64_t)((float)W * s.inv_ctas * 1.000001f) + 1);
-    const int64_t x0 = blockIdx.x * o.span, x1 = x0 + o.span;
+    const int64_t span = max((int64_t)s.min_span, (int64_t)((float)W * s.inv_ctas * 1.000001f) + 1);
+    const int64_t x0 = blockIdx.x * span, x1 = x0 + span;
+    if (tid == 0) sh.span = span;
     if (x0 >= W) return false;
     int64_t carry = 0;
     for (int32_t base = 0; base < s.nreq; base += NT) {
@@ -215,13 +218,20 @@ __device__ bool sched_init(const SchedIn &s, SchedShared &sh, Sched &o) {
         carry += total;
         if (carry > x1) break;
     }
-    __syncthreads();
+    return true;
+}
+
+// The CTA's span as a walk, from what sched_scan found: for the one thread (or warp) that hands out the
+// segments.
+template <int KT>
+__device__ __forceinline__ void sched_begin(const SchedIn &s, const SchedShared &sh, Sched &o) {
     const int32_t i0 = sh.req[0], i1 = sh.req[1];
+    o.span = sh.span;
     o.before = sh.before[0];
     o.r = sh.r[0];
-    o.at = unit_pos<KT>(s, o.r, i0, x0 - o.before);
+    o.at = unit_pos<KT>(s, o.r, i0, blockIdx.x * o.span - o.before);
     o.end = UnitPos{s.nreq, 0, 0, 0};
-    if (i1 < s.nreq) o.end = unit_pos<KT>(s, sh.r[1], i1, x1 - sh.before[1]);
+    if (i1 < s.nreq) o.end = unit_pos<KT>(s, sh.r[1], i1, (blockIdx.x + 1) * o.span - sh.before[1]);
     // A span that begins inside a unit takes that unit's rest last, if there is more: so all CTAs sweep
     // the keys from the front at the same time, and those that share a KV head read it from L2 (chunk
     // of 900 tokens over 64000 keys, 152 spans: every span at its own place re-reads 4 GB from HBM).
@@ -232,7 +242,6 @@ __device__ bool sched_init(const SchedIn &s, SchedShared &sh, Sched &o) {
         o.tail = g;
         o.put_off = true;
     }
-    return true;
 }
 
 // the next segment of the span; false at its end
@@ -245,6 +254,21 @@ __device__ __forceinline__ bool sched_next(const SchedIn &s, Sched &o, Segment &
     return true;
 }
 
+
+// ---- handing segments to a CTA's roles ---------------------------------------------------------------
+// One warp walks the span and passes each segment on through a small ring in shared memory, so that the
+// other roles hold none of the walk's state (whose registers would spill in the softmax) and never wait
+// for its arithmetic at a unit's end.
+constexpr int kSegSlots = 4;
+struct SegMsg {
+    int64_t tok0;
+    int32_t ntok, head;  // ntok == 0: the end
+    int32_t req, p0, kv, t0;
+    int32_t t1, tiles;
+    int32_t act[2], full[2];  // per tile of rows (paged_chunk.cu): key tiles needed; key tiles without a mask
+    int32_t pad[2];
+};
+static_assert(sizeof(SegMsg) == 64, "four 16-byte words");
 
 // What the CTA that opens a unit and does not finish it leaves for the combine.
 struct PartHeader {
@@ -287,7 +311,8 @@ struct CombineArgs {
     void *out;
     float *lse;
     int64_t out_stride;
-    int32_t G, hq;
+    int32_t hq, G;
+    FastDiv by_G;
 };
 int launch_paged_combine(const CombineArgs &a, int hd, int dtype, cudaStream_t s);
 
