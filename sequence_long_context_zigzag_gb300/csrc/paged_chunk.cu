@@ -136,19 +136,18 @@ __device__ void walk_role(const ChunkParams &p, const SchedShared &sh, uint8_t *
     p.w.head[blockIdx.x] = opened;
 }
 
-// The next segment, for a whole warp (all lanes call) or a single thread; ntok == 0 at the end. False
-// after a failed wait.
-template <int HD, bool kWarp>
+// The next segment, for a whole warp; ntok == 0 at the end. False after a failed wait.
+template <int HD>
 __device__ __forceinline__ bool next_segment(const ChunkParams &p, const uint8_t *smem, uint32_t bar0, uint32_t &n,
                                              SegMsg &g) {
     using C = Cfg<HD>;
     bool ok = tc::mbar_wait(bar0 + 8u * (C::SEG_FULL + n % kSegSlots), (n / kSegSlots) & 1u, p.status, USP_ERR_TIMEOUT,
                             kWaitLimitNs);
-    if (kWarp) ok = __all_sync(0xffffffffu, ok);
+    ok = __all_sync(0xffffffffu, ok);
     if (!ok) return false;
     g = reinterpret_cast<const SegMsg *>(smem + C::kSeg)[n % kSegSlots];
-    if (kWarp) __syncwarp();
-    if (!kWarp || (threadIdx.x & 31) == 0) tc::mbar_arrive(bar0 + 8u * (C::SEG_EMPTY + n % kSegSlots));
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar0 + 8u * (C::SEG_EMPTY + n % kSegSlots));
     ++n;
     return true;
 }
@@ -170,7 +169,7 @@ __device__ void producer_role(const ChunkParams &p, const uint8_t *smem, uint32_
     uint32_t kfills = 0, vfills = 0, nq = 0, nseg = 0;
     bool ok = true;
     SegMsg g;
-    while (ok && (ok = next_segment<HD, true>(p, smem, bar0, nseg, g)) && g.ntok > 0) {
+    while (ok && (ok = next_segment<HD>(p, smem, bar0, nseg, g)) && g.ntok > 0) {
         if (g.t0 >= g.t1) continue;
         if (nq > 0 && !(ok = wait(C::Q_EMPTY, (nq - 1) & 1u))) break;
         if (lane == 0) {
@@ -220,36 +219,94 @@ __device__ void producer_role(const ChunkParams &p, const uint8_t *smem, uint32_
     }
 }
 
+// The issuing warps stay converged and predicate each tensor-core instruction on one elected lane: the
+// descriptors are then warp-uniform values in uniform registers. Issued from a branch that one lane takes,
+// every product first moves its descriptors there: 75 to 100 cycles per m128n128k16 product (64 at the
+// tensor core's rate), and the issue bounds the kernel (measured: a burst of 16 products 1420 cycles).
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void mma_ss_if(uint32_t elected, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts_if(uint32_t elected, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
+        : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t elected, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(elected)
+        : "memory");
+}
+__device__ __forceinline__ void arrive_if(uint32_t elected, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar),
+        "r"(elected)
+        : "memory");
+}
+// a wait of a whole warp, with a warp-uniform result
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int *status) {
+    if (__all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity))) return true;
+    return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, status, USP_ERR_TIMEOUT, kWaitLimitNs));
+}
+
 template <int HD>
-__device__ __forceinline__ void issue_s(uint32_t d_tmem, uint64_t qdesc, uint64_t kdesc) {
+__device__ __forceinline__ void issue_s(uint32_t el, uint32_t d_tmem, uint64_t qdesc, uint64_t kdesc) {
     using C = Cfg<HD>;
     constexpr uint32_t id = tc::idesc_bf16_f32(kM, kN, 0, 0);
 #pragma unroll
     for (int k = 0; k < HD / 16; ++k) {
         const uint64_t off = (uint64_t)(((k / 4) * C::kBoxBytes + (k % 4) * 32) >> 4);
-        tc::mma_ss(d_tmem, qdesc + off, kdesc + off, id, k > 0 ? 1u : 0u);
+        mma_ss_if(el, d_tmem, qdesc + off, kdesc + off, id, k > 0 ? 1u : 0u);
     }
 }
 // V as (N = hd) x (K = keys), MN-major: 64-column blocks kBoxBytes apart, 8-key groups 1024 bytes apart
 template <int HD>
-__device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint64_t vdesc, uint32_t accumulate) {
+__device__ __forceinline__ void issue_pv(uint32_t el, uint32_t d_tmem, uint32_t p_tmem, uint64_t vdesc,
+                                         uint32_t accumulate) {
     constexpr uint32_t id = tc::idesc_bf16_f32(kM, HD, 0, 1);
 #pragma unroll
     for (int k = 0; k < kN / 16; ++k)
-        tc::mma_ts(d_tmem, p_tmem + k * 8, vdesc + (uint64_t)((k * 2048) >> 4), id, (accumulate || k > 0) ? 1u : 0u);
+        mma_ts_if(el, d_tmem, p_tmem + k * 8, vdesc + (uint64_t)((k * 2048) >> 4), id, (accumulate || k > 0) ? 1u : 0u);
 }
 
-// One thread per Q tile. Burst j of issuer i: PV_i(j), then S_i(j+1) unless tile j+1 opens a segment (its
-// first S leaves the turn order, so that it runs while the other tile finishes the old segment). Every
-// burst waits for its operands first and for its turn last. PV_i(j) and S_i(j+1) come from one thread, so
-// S_i(j+1) overwrites P_i(j) only after PV_i(j) has read it. Stages are released by both issuers; each
-// waits for a stage's fill before releasing it, also when its Q tile skips the tile.
+// One warp per Q tile. Burst j of issuer i: PV_i(j), then S_i(j+1) unless tile j+1 opens a segment (its
+// S leaves the turn order, so that it runs while the other tile finishes the old segment). Every burst
+// waits for its operands first and for its turn last, so it issues the moment the other's burst is
+// queued. PV_i(j) and S_i(j+1) come from one lane, so S_i(j+1) overwrites P_i(j) only after PV_i(j) has
+// read it. Stages are released by both issuers; each waits for a stage's fill before releasing it, also
+// when its Q tile skips the tile.
 template <int HD>
 __device__ void mma_role(const ChunkParams &p, const uint8_t *smem, uint32_t sbase, uint32_t bar0, uint32_t tmem, int i) {
     using C = Cfg<HD>;
+    const uint32_t el = elect_one();
     auto BAR = [&](int k) { return bar0 + 8u * k; };
     auto wait = [&](int bar, uint32_t parity) {
-        return tc::mbar_wait(BAR(bar), parity, p.status, USP_ERR_TIMEOUT, kWaitLimitNs);
+        return warp_wait(BAR(bar), parity, p.status);
     };
     const uint64_t qdesc = tc::sw128_desc(sbase + C::kQ + (uint32_t)i * C::kTileBytes, 16, 1024);
     const uint64_t kdesc0 = tc::sw128_desc(sbase + C::kK, 16, 1024);
@@ -258,78 +315,92 @@ __device__ void mma_role(const ChunkParams &p, const uint8_t *smem, uint32_t sba
     const uint32_t tS = tmem + 128u * i, tO = tmem + 256u + (uint32_t)(HD * i);
     const int my_turn = C::TURN + i, other_turn = C::TURN + (1 - i);
     uint32_t turns = 0, nseg = 0;
+    bool ok = true;
     // the tiles of all segments as one stream (segments without a tile are passed over): the next tile is
     // kt of [kt, t1); this issuer's Q tile needs those below act_end
+    struct Tile {
+        bool have, first, act;  // there is one; it opens a segment; the Q tile needs it
+    };
     int kt = 0, t1 = 0, act_end = 0;
-    bool more = true;
-    bool have = false, cur_act = false, ok = true;
+    auto next_tile = [&]() {
+        Tile t{true, false, false};
+        while (kt >= t1) {
+            SegMsg g;
+            ok = next_segment<HD>(p, smem, bar0, nseg, g);
+            if (!ok || __reduce_max_sync(0xffffffffu, g.ntok) == 0) {
+                t.have = false;
+                return t;
+            }
+            // (reductions over equal values: the compiler then knows that they are uniform)
+            kt = __reduce_max_sync(0xffffffffu, g.t0);
+            t1 = __reduce_max_sync(0xffffffffu, g.t1);
+            act_end = __reduce_max_sync(0xffffffffu, i ? g.act[1] : g.act[0]);
+            t.first = true;
+        }
+        t.act = kt < act_end;
+        ++kt;
+        return t;
+    };
+    auto s_burst = [&](bool act, uint32_t st) {
+        if (act) {
+            issue_s<HD>(el, tS, qdesc, kdesc0 + stage_off(st));
+            commit_if(el, BAR(C::S_FULL + i));
+        }
+        commit_if(el, BAR(C::K_EMPTY + st));
+    };
     uint32_t pc = 0, started = 0;  // P waits; a PV of the current segment has been issued
     uint32_t nq = 0, no = 0;       // Q loads consumed; O_i read-outs handed to the softmax
     uint32_t j = 0;                // tiles of the stream
-    if (i == 1) tc::mbar_arrive(BAR(other_turn));  // issuer 1's empty "burst -1"
-    while (ok) {
-        bool boundary = false;  // the next tile opens a segment
-        while (ok && more && kt >= t1) {
-            SegMsg g;
-            if (!(ok = next_segment<HD, false>(p, smem, bar0, nseg, g))) break;
-            if (!(more = g.ntok > 0)) break;
-            kt = g.t0;
-            t1 = g.t1;
-            act_end = i ? g.act[1] : g.act[0];
-            boundary = true;
+    Tile cur = next_tile();
+    if (ok && cur.have) {
+        ok = wait(C::Q_FULL, 0) && wait(C::K_FULL, 0);
+        nq = 1;
+        if (ok && i == 1) ok = wait(my_turn, (turns++) & 1u);
+        if (ok) {
+            s_burst(cur.act, 0);
+            arrive_if(el, BAR(other_turn));
         }
+    }
+    while (ok && cur.have) {
+        const Tile nxt = next_tile();
         if (!ok) break;
-        const bool have_n = more;
-        const bool nxt_act = have_n && kt < act_end;
-        ++kt;
-        const uint32_t jn = have ? j + 1 : 0;
-        const uint32_t stn = jn % C::kStages, phn = (jn / C::kStages) & 1u;
-        bool turn_after_s = false;
-        if (have) {
-            const bool last = !have_n || boundary;
-            const uint32_t st = j % C::kStages, ph = (j / C::kStages) & 1u;
-            const bool act = cur_act;
-            if (last) tc::mma_commit(BAR(C::Q_EMPTY));  // this issuer's S products of the segment are issued
-            if (!(ok = wait(C::V_FULL + st, ph))) break;
-            if (act && !(ok = wait(C::P_FULL + i, pc & 1u))) break;
-            if (act && !started && no > 0 && !(ok = wait(C::O_EMPTY + i, (no - 1) & 1u))) break;
-            if (have_n && !boundary && !(ok = wait(C::K_FULL + stn, phn))) break;
-            if (!(ok = wait(my_turn, (turns++) & 1u))) break;
-            if (act) {
-                ++pc;
-                tc::fence_after_sync();
-                issue_pv<HD>(tO, tS, vdesc0 + stage_off(st), started);
-                started = 1;
-            }
-            tc::mma_commit(BAR(C::V_EMPTY + st));
-            if (last) {
-                if (started) {
-                    tc::mma_commit(BAR(C::O_FULL + i));
-                    ++no;
-                }
-                started = 0;
-            }
-            turn_after_s = have_n && !boundary;
-            if (!turn_after_s) tc::mbar_arrive(BAR(other_turn));
+        const bool last = !nxt.have || nxt.first, boundary = nxt.have && nxt.first;
+        const uint32_t st = j % C::kStages, ph = (j / C::kStages) & 1u;
+        const uint32_t stn = (j + 1) % C::kStages, phn = ((j + 1) / C::kStages) & 1u;
+        if (last) commit_if(el, BAR(C::Q_EMPTY));  // this issuer's S products of the segment are issued
+        if (!(ok = wait(C::V_FULL + st, ph))) break;
+        if (cur.act && !(ok = wait(C::P_FULL + i, pc & 1u))) break;
+        if (cur.act && !started && no > 0 && !(ok = wait(C::O_EMPTY + i, (no - 1) & 1u))) break;
+        if (!last && !(ok = wait(C::K_FULL + stn, phn))) break;
+        if (!(ok = wait(my_turn, (turns++) & 1u))) break;
+        if (cur.act) {
+            ++pc;
+            tc::fence_after_sync();
+            issue_pv<HD>(el, tO, tS, vdesc0 + stage_off(st), started);
+            started = 1;
         }
-        if (!have_n) break;
+        commit_if(el, BAR(C::V_EMPTY + st));
+        if (last) {
+            if (started) {
+                commit_if(el, BAR(C::O_FULL + i));
+                ++no;
+            }
+            started = 0;
+        } else {
+            s_burst(nxt.act, stn);
+        }
+        arrive_if(el, BAR(other_turn));
         if (boundary) {
             if (!(ok = wait(C::Q_FULL, nq & 1u))) break;
             ++nq;
             if (!(ok = wait(C::K_FULL + stn, phn))) break;
+            s_burst(nxt.act, stn);
         }
-        if (nxt_act) {
-            issue_s<HD>(tS, qdesc, kdesc0 + stage_off(stn));
-            tc::mma_commit(BAR(C::S_FULL + i));
-        }
-        tc::mma_commit(BAR(C::K_EMPTY + stn));
-        if (turn_after_s) tc::mbar_arrive(BAR(other_turn));
-        cur_act = nxt_act;
-        have = true;
-        j = jn;
+        cur = nxt;
+        ++j;
     }
-    if (!ok) tc::mbar_arrive(BAR(other_turn));  // let the other issuer reach its own bounded exit
-    tc::mma_commit(BAR(C::DONE + i));           // every MMA of this issuer ends before tensor memory is freed
+    if (!ok) arrive_if(el, BAR(other_turn));  // let the other issuer reach its own bounded exit
+    commit_if(el, BAR(C::DONE + i));           // every MMA of this issuer ends before tensor memory is freed
     wait(C::DONE + i, 0);
 }
 
@@ -564,14 +635,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         if (!skip) {
             if (warp == kProducerWarp) producer_role<HD>(p, smem, sbase, bar0);
             else if (warp == kWalkWarp && lane == 0) walk_role<HD>(p, sh, smem, bar0);
-            else if (warp != kWalkWarp && lane == 0) mma_role<HD>(p, smem, sbase, bar0, tmem, warp - kMmaWarp);
+            else if (warp != kWalkWarp) mma_role<HD>(p, smem, sbase, bar0, tmem, warp - kMmaWarp);
             __syncwarp();
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         uint32_t ns = 0, no = 0, nt = 0, nseg = 0;
         SegMsg g;
-        while (!skip && next_segment<HD, true>(p, smem, bar0, nseg, g) && g.ntok > 0)
+        while (!skip && next_segment<HD>(p, smem, bar0, nseg, g) && g.ntok > 0)
             if (!softmax_segment<HD>(p, g, smem, bar0, tmem, warp >> 2, ns, no, nt)) break;
     }
     if (skip && threadIdx.x == 0) p.w.head[blockIdx.x] = PartHeader{};
