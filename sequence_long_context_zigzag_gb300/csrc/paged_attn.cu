@@ -131,13 +131,13 @@ int usp_paged_attn(const void *q, const void *k_cache, const void *v_cache, cons
     c.G = a.G; c.hq = a.hq; c.by_G = FastDiv((uint32_t)a.G);
     if (r.many_ctas) {
         c.w[0] = part_space(at, r.many_ctas, r.many_rows, a.hd);
-        rc = bf16 ? launch_paged_chunk(a, r.split, c.w[0], s) : launch_paged_f32(a, true, r.split, INT_MAX, c.w[0], s);
+        rc = bf16 ? launch_paged_chunk(a, r.split, c.w[0], s) : launch_paged_f32(a, true, r.split, INT_MAX, false, c.w[0], s);
         if (rc) return rc;
     }
     if (r.few_ctas) {
         c.w[1] = part_space(at, r.few_ctas, r.few_rows, a.hd);
-        rc = bf16 ? launch_paged_decode(a, r.few_rows, r.split, c.w[1], s)
-                  : launch_paged_f32(a, false, 0, r.split, c.w[1], s);
+        rc = bf16 ? launch_paged_decode(a, r.few_rows, r.split, r.many_ctas > 0, c.w[1], s)
+                  : launch_paged_f32(a, false, 0, r.split, r.many_ctas > 0, c.w[1], s);
         if (rc) return rc;
     }
     return launch_paged_combine(c, a.hd, d.cache.dtype, s);

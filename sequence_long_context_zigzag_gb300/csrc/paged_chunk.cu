@@ -17,10 +17,10 @@
 //   warps 9, 10     one MMA issuer per Q tile: S_i = Q_i K^T, O_i += P_i V, taking turns so that one tile's
 //                   products run under the other tile's softmax;
 //   warp 11         walks the span and hands its segments to the other roles through a ring; with 8-10 it
-//                   is the warpgroup that gives registers to the softmax (setmaxnreg).
+//                   is the warpgroup that gives registers to the softmax (setmaxnreg). Rows of the last page
+//                   behind the request's last key may hold NaN, and 0 x NaN would spread in P V: this warp
+//                   clears them in V's stage before the issuers see it.
 //   TMEM: S0 [0,128) S1 [128,256) O0 [256,256+hd) O1 [256+hd,256+2hd); P_i lies over S_i.
-// Rows of the last page behind the request's last key may hold NaN, and 0 x NaN would spread in P V: the
-// softmax warps clear those rows of V's stage in shared memory before they hand P over.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -79,10 +79,14 @@ template <int HD> struct Cfg {
     static constexpr int O_EMPTY = Q_EMPTY + 1;       // [2]
     static constexpr int SEG_FULL = O_EMPTY + 2;      // [kSegSlots]
     static constexpr int SEG_EMPTY = SEG_FULL + kSegSlots;
-    static constexpr int kNumBars = SEG_EMPTY + kSegSlots;
+    static constexpr int TAIL = SEG_EMPTY + kSegSlots;  // [2]: V tiles that the walk warp has to clear the end of
+    static constexpr int kNumBars = TAIL + 2;
     static constexpr int kSlot = kBar + (kNumBars * 8 + 15) / 16 * 16;  // tensor memory address, skip flag
     static constexpr int kSeg = kSlot + 16;
-    static constexpr int kSmem = kSeg + kSegSlots * (int)sizeof(SegMsg) + 1024;  // + slack for the alignment
+    // a staging slot per softmax warp for its stores: 32 rows x 64 bytes
+    static constexpr int kStgSlot = 32 * 64;
+    static constexpr int kStg = kSeg + kSegSlots * (int)sizeof(SegMsg);
+    static constexpr int kSmem = kStg + kSoftmaxWarps * kStgSlot + 1024;  // + slack for the alignment
 };
 
 struct ChunkParams {
@@ -99,41 +103,74 @@ struct ChunkParams {
     float scale_log2;
 };
 
-// The walk: one thread hands out the segments and, at the end, the header of a unit left open.
+// does key tile t hold rows behind the request's last key? (only a unit's last tile can)
+__device__ __forceinline__ bool is_tail(const int32_t t, const int32_t kv) { return (t + 1) * kN > kv; }
+
+// The walk warp hands out the segments and, at the end, the header of a unit left open. It is a segment
+// ahead when it clears the end of a segment's last V tile.
 template <int HD>
 __device__ void walk_role(const ChunkParams &p, const SchedShared &sh, uint8_t *smem, uint32_t bar0) {
     using C = Cfg<HD>;
+    const int lane = threadIdx.x & 31;
+    auto wait = [&](int bar, uint32_t parity) {
+        const bool r = tc::mbar_wait(bar0 + 8u * bar, parity, p.status, USP_ERR_TIMEOUT, kWaitLimitNs);
+        return (bool)__all_sync(0xffffffffu, r);
+    };
     SegMsg *ring = reinterpret_cast<SegMsg *>(smem + C::kSeg);
     Sched sc;
     sched_begin<kN>(p.s, sh, sc);
     PartHeader opened{};
-    for (uint32_t n = 0;; ++n) {
+    uint32_t tiles = 0, ntail = 0;  // tiles and tails of the segments handed out
+    int tail_row = -1;              // first row to clear in the pending tail tile
+    uint32_t tail_stage = 0;
+    bool ok = true, more = true;
+    for (uint32_t n = 0; ok && more; ++n) {
         Segment g;
-        const bool more = sched_next<kN>(p.s, sc, g);
-        if (!tc::mbar_wait(bar0 + 8u * (C::SEG_EMPTY + n % kSegSlots), ((n / kSegSlots) & 1u) ^ 1u, p.status,
-                           USP_ERR_TIMEOUT, kWaitLimitNs)) {
-            opened = PartHeader{};
-            break;
+        more = sched_next<kN>(p.s, sc, g);
+        if (!(ok = wait(C::SEG_EMPTY + n % kSegSlots, ((n / kSegSlots) & 1u) ^ 1u))) break;
+        if (lane == 0) {
+            SegMsg m{};
+            if (more) {
+                m.tok0 = g.tok0; m.ntok = g.ntok; m.head = g.head; m.req = g.req; m.p0 = g.p0; m.kv = g.kv;
+                m.t0 = g.t0; m.t1 = g.t1; m.tiles = g.tiles;
+                for (int i = 0; i < 2; ++i) {
+                    const int a = i * p.tq_tokens, b = min(g.ntok, a + p.tq_tokens);  // the Q tile's tokens
+                    if (a >= b) continue;
+                    const int last = p.s.causal ? max(0, min(g.kv, g.p0 + b)) : g.kv;
+                    const int all = p.s.causal ? max(0, min(g.kv, g.p0 + a + 1)) : g.kv;
+                    m.act[i] = (last + kN - 1) / kN;
+                    m.full[i] = all / kN;
+                }
+            }
+            ring[n % kSegSlots] = m;
+            tc::mbar_arrive(bar0 + 8u * (C::SEG_FULL + n % kSegSlots));
         }
-        SegMsg m{};
-        if (more) {
-            m.tok0 = g.tok0; m.ntok = g.ntok; m.head = g.head; m.req = g.req; m.p0 = g.p0; m.kv = g.kv;
-            m.t0 = g.t0; m.t1 = g.t1; m.tiles = g.tiles;
-            for (int i = 0; i < 2; ++i) {
-                const int a = i * p.tq_tokens, b = min(g.ntok, a + p.tq_tokens);  // the Q tile's tokens
-                if (a >= b) continue;
-                const int last = p.s.causal ? max(0, min(g.kv, g.p0 + b)) : g.kv;
-                const int all = p.s.causal ? max(0, min(g.kv, g.p0 + a + 1)) : g.kv;
-                m.act[i] = (last + kN - 1) / kN;
-                m.full[i] = all / kN;
+        __syncwarp();
+        if (tail_row >= 0) {
+            // the last V tile of the segment before: landed, cleared, handed to the issuers
+            if (!(ok = wait(C::TAIL + (ntail & 1u), (ntail >> 1) & 1u))) break;
+            uint8_t *v = smem + C::kV + tail_stage * C::kTileBytes;
+            for (int x = tail_row * 8 + lane; x < kN * 8; x += 32)
+#pragma unroll
+                for (int bx = 0; bx < C::kBoxes; ++bx)
+                    *reinterpret_cast<uint4 *>(v + bx * C::kBoxBytes + x * 16) = make_uint4(0, 0, 0, 0);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(bar0 + 8u * (C::V_FULL + tail_stage));
+            ++ntail;
+            tail_row = -1;
+        }
+        if (more && g.t0 < g.t1) {
+            tiles += (uint32_t)(g.t1 - g.t0);
+            if (is_tail(g.t1 - 1, g.kv)) {
+                tail_row = g.kv - (g.t1 - 1) * kN;
+                tail_stage = (tiles - 1) % C::kStages;
             }
         }
-        ring[n % kSegSlots] = m;
-        tc::mbar_arrive(bar0 + 8u * (C::SEG_FULL + n % kSegSlots));
-        if (!more) break;
-        if (g.t0 == 0 && g.t1 < g.tiles) opened = part_header(p.s, sc, g);
+        if (more && g.t0 == 0 && g.t1 < g.tiles) opened = part_header(p.s, sc, g);
     }
-    p.w.head[blockIdx.x] = opened;
+    if (!ok) opened = PartHeader{};
+    if (lane == 0) p.w.head[blockIdx.x] = opened;
 }
 
 // The next segment, for a whole warp; ntok == 0 at the end. False after a failed wait.
@@ -166,21 +203,18 @@ __device__ void producer_role(const ChunkParams &p, const uint8_t *smem, uint32_
     const int ps = 1 << p.log_ps, piece = min(ps, kN), pieces = kN / piece, nbox = pieces * C::kBoxes;
     const int half = lane / pieces, pc = lane % pieces;
     const uint32_t in_tile = half * C::kBoxBytes + pc * piece * 128;
-    uint32_t kfills = 0, vfills = 0, nq = 0, nseg = 0;
+    uint32_t kfills = 0, vfills = 0, nq = 0, nseg = 0, ntail = 0;
     bool ok = true;
     SegMsg g;
     while (ok && (ok = next_segment<HD>(p, smem, bar0, nseg, g)) && g.ntok > 0) {
         if (g.t0 >= g.t1) continue;
-        if (nq > 0 && !(ok = wait(C::Q_EMPTY, (nq - 1) & 1u))) break;
-        if (lane == 0) {
-            const uint32_t box = (uint32_t)(p.tq_tokens * p.s.G) * 128;
-            tc::mbar_arrive_expect_tx(BAR(C::Q_FULL), 2 * C::kBoxes * box);
+        // Q comes from HBM and its buffer frees late: into L2 meanwhile
+        auto q_boxes = [&](auto &&f) {
             for (int i = 0; i < 2; ++i)
                 for (int bx = 0; bx < C::kBoxes; ++bx)
-                    tma_load_3d(sbase + C::kQ + i * C::kTileBytes + bx * C::kBoxBytes, &p.tq, bx * 64, g.head * p.s.G,
-                                (int32_t)(g.tok0 + i * p.tq_tokens), BAR(C::Q_FULL));
-        }
-        ++nq;
+                    f(C::kQ + i * C::kTileBytes + bx * C::kBoxBytes, bx * 64, (int32_t)(g.tok0 + i * p.tq_tokens));
+        };
+        if (lane == 0) q_boxes([&](int, int c, int32_t tok) { tma_prefetch_3d(&p.tq, c, g.head * p.s.G, tok); });
         const int32_t *row = p.table + (int64_t)g.req * p.table_stride;
         // page of this lane's piece of tile t; num_pages (a box of zeros) behind the request's keys
         auto page_of = [&](int t) {
@@ -200,12 +234,25 @@ __device__ void producer_role(const ChunkParams &p, const uint8_t *smem, uint32_
             if (lane < nbox)
                 tma_load_3d(sbase + C::kK + st * C::kTileBytes + in_tile, &p.tk, half * 64, c1, page, BAR(C::K_FULL + st));
             ++kfills;
+            if (t == g.t0) {
+                if (nq > 0 && !(ok = wait(C::Q_EMPTY, (nq - 1) & 1u))) break;
+                if (lane == 0) {
+                    tc::mbar_arrive_expect_tx(BAR(C::Q_FULL), 2 * C::kBoxes * (uint32_t)(p.tq_tokens * p.s.G) * 128);
+                    q_boxes([&](int dst, int c, int32_t tok) {
+                        tma_load_3d(sbase + dst, &p.tq, c, g.head * p.s.G, tok, BAR(C::Q_FULL));
+                    });
+                }
+                ++nq;
+            }
             if (!(ok = wait(C::V_EMPTY + st, ph))) break;
-            if (lane == 0) tc::mbar_arrive_expect_tx(BAR(C::V_FULL + st), C::kTileBytes);
+            // a tile with rows behind the last key goes to the walk warp first
+            const bool tail = is_tail(t, g.kv);
+            const uint32_t full = BAR(tail ? C::TAIL + (int)(ntail & 1u) : C::V_FULL + (int)st);
+            if (lane == 0) tc::mbar_arrive_expect_tx(full, C::kTileBytes);
             __syncwarp();
-            if (lane < nbox)
-                tma_load_3d(sbase + C::kV + st * C::kTileBytes + in_tile, &p.tv, half * 64, c1, page, BAR(C::V_FULL + st));
+            if (lane < nbox) tma_load_3d(sbase + C::kV + st * C::kTileBytes + in_tile, &p.tv, half * 64, c1, page, full);
             ++vfills;
+            ntail += tail;
             page = next;
         }
     }
@@ -216,6 +263,7 @@ __device__ void producer_role(const ChunkParams &p, const uint8_t *smem, uint32_
             wait(C::K_FULL + f % C::kStages, (f / C::kStages) & 1u);
         for (uint32_t f = vfills > C::kStages ? vfills - C::kStages : 0; f < vfills; ++f)
             wait(C::V_FULL + f % C::kStages, (f / C::kStages) & 1u);
+        if (ntail > 0) wait(C::TAIL + ((ntail - 1) & 1u), ((ntail - 1) >> 1) & 1u);
     }
 }
 
@@ -295,11 +343,12 @@ __device__ __forceinline__ void issue_pv(uint32_t el, uint32_t d_tmem, uint32_t 
 }
 
 // One warp per Q tile. Burst j of issuer i: PV_i(j), then S_i(j+1) unless tile j+1 opens a segment (its
-// S leaves the turn order, so that it runs while the other tile finishes the old segment). Every burst
-// waits for its operands first and for its turn last, so it issues the moment the other's burst is
-// queued. PV_i(j) and S_i(j+1) come from one lane, so S_i(j+1) overwrites P_i(j) only after PV_i(j) has
-// read it. Stages are released by both issuers; each waits for a stage's fill before releasing it, also
-// when its Q tile skips the tile.
+// S leaves the turn order, so that it runs while the other tile finishes the old segment). Every wait
+// costs 100 cycles or more even when it need not wait, so the one for P, which comes last in the steady
+// state, is the last (with the turn last, 16384 tokens without the mask ran 6% slower). PV_i(j) and
+// S_i(j+1) come from one lane, so S_i(j+1) overwrites P_i(j) only after PV_i(j) has read it. Stages are
+// released by both issuers; each waits for a stage's fill before releasing it, also when its Q tile skips
+// the tile.
 template <int HD>
 __device__ void mma_role(const ChunkParams &p, const uint8_t *smem, uint32_t sbase, uint32_t bar0, uint32_t tmem, int i) {
     using C = Cfg<HD>;
@@ -369,10 +418,10 @@ __device__ void mma_role(const ChunkParams &p, const uint8_t *smem, uint32_t sba
         const uint32_t stn = (j + 1) % C::kStages, phn = ((j + 1) / C::kStages) & 1u;
         if (last) commit_if(el, BAR(C::Q_EMPTY));  // this issuer's S products of the segment are issued
         if (!(ok = wait(C::V_FULL + st, ph))) break;
-        if (cur.act && !(ok = wait(C::P_FULL + i, pc & 1u))) break;
-        if (cur.act && !started && no > 0 && !(ok = wait(C::O_EMPTY + i, (no - 1) & 1u))) break;
         if (!last && !(ok = wait(C::K_FULL + stn, phn))) break;
+        if (cur.act && !started && no > 0 && !(ok = wait(C::O_EMPTY + i, (no - 1) & 1u))) break;
         if (!(ok = wait(my_turn, (turns++) & 1u))) break;
+        if (cur.act && !(ok = wait(C::P_FULL + i, pc & 1u))) break;
         if (cur.act) {
             ++pc;
             tc::fence_after_sync();
@@ -405,13 +454,21 @@ __device__ void mma_role(const ChunkParams &p, const uint8_t *smem, uint32_t sba
 }
 
 __device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr)
+                 : "memory");
+    return v;
+}
 
-// One segment of the softmax of Q tile i; ns (S tiles), no (O read-outs) and nt (tiles of the stream) run
-// on across segments. False after a failed wait (the whole warp leaves; the others' waits end by the
+// One segment of the softmax of Q tile i; ns (S tiles) and no (O read-outs) run on across segments. False after a failed wait (the whole warp leaves; the others' waits end by the
 // recorded status).
 template <int HD>
 __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegMsg &g, uint8_t *smem, uint32_t bar0,
-                                                uint32_t tmem, int i, uint32_t &ns, uint32_t &no, uint32_t &nt) {
+                                                uint32_t tmem, int i, uint32_t &ns, uint32_t &no) {
     using C = Cfg<HD>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wq = warp & 3;
     const int row = wq * 32 + lane;
@@ -427,8 +484,6 @@ __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegM
     const uint64_t sl22 = tc::pack2(sl2, sl2);
     float m = -INFINITY, l = 0.f;
     bool any = false, ok = true;
-    const uint32_t nt0 = nt;
-    nt += (uint32_t)(g.t1 - g.t0);
     const int act_end = min(g.t1, i ? g.act[1] : g.act[0]), full_end = i ? g.full[1] : g.full[0];
     for (int kt = g.t0; kt < act_end; ++kt) {
         const bool full = kt < full_end;
@@ -441,12 +496,16 @@ __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegM
         for (int c = 0; c < 4; ++c) tc::tmem_ld32(tS + c * 32, sr[c]);
         tc::tmem_ld_wait();
         if (!full) {
-            const int ll = lim - kt * kN;
+            // (a warp's rows are a few tokens with limits close together: whole chunks are visible to all)
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < 4; ++c) {
+                const int lc = lim - kt * kN - c * 32;
+                if (__any_sync(0xffffffffu, lc < 32)) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    if (c * 32 + e >= ll) sr[c][e] = __float_as_uint(-INFINITY);
+                    for (int e = 0; e < 32; ++e)
+                        if (e >= lc) sr[c][e] = __float_as_uint(-INFINITY);
+                }
+            }
         }
         float mx = -INFINITY;
 #pragma unroll
@@ -498,21 +557,6 @@ __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegM
         float s0, s1;
         tc::unpack2(sum, s0, s1);
         l += s0 + s1;
-        if ((kt + 1) * kN > g.kv) {
-            // keys behind the request's last one: their V rows become zeros (each softmax warpgroup that
-            // uses the tile clears them; the values written are the same)
-            const uint32_t jt = nt0 + (uint32_t)(kt - g.t0), st = jt % C::kStages;
-            ok = tc::mbar_wait(bar0 + 8u * (C::V_FULL + st), (jt / C::kStages) & 1u, p.status, USP_ERR_TIMEOUT,
-                               kWaitLimitNs);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            uint8_t *v = smem + C::kV + st * C::kTileBytes;
-            for (int x = (g.kv - kt * kN) * 8 + row; x < kN * 8; x += 128)
-#pragma unroll
-                for (int bx = 0; bx < C::kBoxes; ++bx)
-                    *reinterpret_cast<uint4 *>(v + bx * C::kBoxBytes + x * 16) = make_uint4(0, 0, 0, 0);
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        }
         tc::tmem_st_wait();
         tc::fence_before_sync();
         __syncwarp();
@@ -526,7 +570,6 @@ __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegM
     const int r = i * p.tq_tokens * p.s.G + row;  // row of the unit
     float *slot = part_slot(p.w, HD, blockIdx.x, g.t0 == 0 ? 1 : 0);
     const int head = g.head * p.s.G + (int)rh;
-    __nv_bfloat16 *orow = p.out + (g.tok0 + tok) * p.out_stride + (int64_t)head * HD;
     const float inv = l > 0.f ? 1.f / l : 0.f;
     if (any) {
         ok = tc::mbar_wait(bar0 + 8u * (C::O_FULL + i), no & 1u, p.status, USP_ERR_TIMEOUT, kWaitLimitNs);
@@ -541,27 +584,58 @@ __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegM
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar0 + 8u * (C::O_EMPTY + i));
-        if (row_ok && whole) {
+        // A lane holds a row, and rows lie apart in memory: each 64 bytes of the 32 rows go through the warp's
+        // staging slot, 16-byte pieces swizzled by (row / 2) % 4 against bank conflicts, so that a store
+        // instruction writes 8 whole 64-byte pieces of rows instead of 32 scattered 16-byte ones (measured:
+        // a segment's end took 5000 cycles with a store per lane and row).
+        const uint32_t stg = tc::smem_u32(smem) + C::kStg + warp * C::kStgSlot;
+        const int sub = lane >> 2, pc = lane & 3;  // row of 8 and piece of 4 that this lane stores
+        char *dst[4];
 #pragma unroll
-            for (int c = 0; c < HD / 32; ++c)
+        for (int x = 0; x < 4; ++x) {
+            const uint32_t rr = wq * 32 + x * 8 + sub;
+            uint32_t t, h;
+            p.s.by_G.divmod(rr, t, h);
+            const int tk = i * p.tq_tokens + (int)t;
+            const bool in = (int)rr < p.tq_tokens * p.s.G && tk < g.ntok;
+            char *to = whole ? reinterpret_cast<char *>(p.out + (g.tok0 + tk) * p.out_stride +
+                                                        (int64_t)(g.head * p.s.G + (int)h) * HD)
+                             : reinterpret_cast<char *>(slot + (size_t)(i * p.tq_tokens * p.s.G + (int)rr) * HD);
+            dst[x] = in ? to + pc * 16 : nullptr;
+        }
+        auto stage_out = [&](const uint32_t (&w)[16], int at) {  // 64 bytes of the lane's row, to byte `at`
 #pragma unroll
-                for (int e = 0; e < 32; e += 8) {
-                    uint4 x;
-                    x.x = float2_to_bf16x2(u2f(o[c][e]) * inv, u2f(o[c][e + 1]) * inv);
-                    x.y = float2_to_bf16x2(u2f(o[c][e + 2]) * inv, u2f(o[c][e + 3]) * inv);
-                    x.z = float2_to_bf16x2(u2f(o[c][e + 4]) * inv, u2f(o[c][e + 5]) * inv);
-                    x.w = float2_to_bf16x2(u2f(o[c][e + 6]) * inv, u2f(o[c][e + 7]) * inv);
-                    *reinterpret_cast<uint4 *>(orow + c * 32 + e) = x;
+            for (int c4 = 0; c4 < 4; ++c4)
+                st_shared_v4(stg + (uint32_t)lane * 64u + (((uint32_t)c4 ^ (((uint32_t)lane >> 1) & 3u)) << 4),
+                             w[4 * c4], w[4 * c4 + 1], w[4 * c4 + 2], w[4 * c4 + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const uint32_t rr = (uint32_t)x * 8u + (uint32_t)sub;
+                const uint4 v = ld_shared_v4(stg + rr * 64u + (((uint32_t)pc ^ ((rr >> 1) & 3u)) << 4));
+                if (dst[x]) *reinterpret_cast<uint4 *>(dst[x] + at) = v;
+            }
+            __syncwarp();
+        };
+#pragma unroll
+        for (int c = 0; c < HD / 32; ++c) {
+            uint32_t w[16];
+            if (whole) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    w[e] = float2_to_bf16x2(u2f(o[c][2 * e]) * inv, u2f(o[c][2 * e + 1]) * inv);
+                stage_out(w, c * 64);
+            } else {
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) w[e] = o[c][hf * 16 + e];
+                    stage_out(w, c * 128 + hf * 64);
                 }
-        } else if (row_ok) {
-#pragma unroll
-            for (int c = 0; c < HD / 32; ++c)
-#pragma unroll
-                for (int e = 0; e < 32; e += 4)
-                    *reinterpret_cast<uint4 *>(slot + (size_t)r * HD + c * 32 + e) =
-                        make_uint4(o[c][e], o[c][e + 1], o[c][e + 2], o[c][e + 3]);
+            }
         }
     } else if (row_ok && whole) {
+        __nv_bfloat16 *orow = p.out + (g.tok0 + tok) * p.out_stride + (int64_t)head * HD;
         for (int e = 0; e < HD; e += 8) *reinterpret_cast<uint4 *>(orow + e) = make_uint4(0, 0, 0, 0);
     }
     if (row_ok) {
@@ -588,11 +662,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     const uint32_t bar0 = sbase + C::kBar;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kSlot);
     volatile uint32_t *skip_flag = tmem_slot + 1;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5;
     if (!sched_scan<kThreads>(p.s, sh)) {  // the same for every thread
         if (threadIdx.x == 0) p.w.head[blockIdx.x] = PartHeader{};
         return;
     }
+    // the next kernels of the call may take their places as SMs come free
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
         tc::prefetch_tmap(&p.tq);
         tc::prefetch_tmap(&p.tk);
@@ -618,6 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             tc::mbar_init(bar0 + 8u * (C::O_EMPTY + i), 4);
             tc::mbar_init(bar0 + 8u * (C::DONE + i), 1);
             tc::mbar_init(bar0 + 8u * (C::TURN + i), 1);
+            tc::mbar_init(bar0 + 8u * (C::TAIL + i), 1);
         }
         tc::fence_barrier_init();
     }
@@ -634,16 +711,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
         if (!skip) {
             if (warp == kProducerWarp) producer_role<HD>(p, smem, sbase, bar0);
-            else if (warp == kWalkWarp && lane == 0) walk_role<HD>(p, sh, smem, bar0);
-            else if (warp != kWalkWarp) mma_role<HD>(p, smem, sbase, bar0, tmem, warp - kMmaWarp);
+            else if (warp == kWalkWarp) walk_role<HD>(p, sh, smem, bar0);
+            else mma_role<HD>(p, smem, sbase, bar0, tmem, warp - kMmaWarp);
             __syncwarp();
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-        uint32_t ns = 0, no = 0, nt = 0, nseg = 0;
+        uint32_t ns = 0, no = 0, nseg = 0;
         SegMsg g;
         while (!skip && next_segment<HD>(p, smem, bar0, nseg, g) && g.ntok > 0)
-            if (!softmax_segment<HD>(p, g, smem, bar0, tmem, warp >> 2, ns, no, nt)) break;
+            if (!softmax_segment<HD>(p, g, smem, bar0, tmem, warp >> 2, ns, no)) break;
     }
     if (skip && threadIdx.x == 0) p.w.head[blockIdx.x] = PartHeader{};
     tc::fence_before_sync();

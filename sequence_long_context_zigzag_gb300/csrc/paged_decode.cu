@@ -428,6 +428,7 @@ __global__ void __launch_bounds__(Cfg<HD, RT>::kThreads, RT == 1 ? 2 : 1)
     } else {
         consumer<HD, RT>(p, smem, sbase);
     }
+    follow_grid_before();
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -498,7 +499,7 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Co
 }
 
 template <int HD, int RT>
-int launch_typed(const DecodeParams &p, int grid, cudaStream_t s) {
+int launch_typed(const DecodeParams &p, int grid, bool second, cudaStream_t s) {
     using C = Cfg<HD, RT>;
     constexpr int kSmem = C::kSmem;
     static_assert(kSmem + 2048 <= (RT == 1 ? 114 : 227) * 1024, "shared memory per CTA");
@@ -516,15 +517,14 @@ int launch_typed(const DecodeParams &p, int grid, cudaStream_t s) {
             attr_set[dev] = true;
         }
     }
-    paged_decode_kernel<HD, RT><<<grid, C::kThreads, kSmem, s>>>(p);
-    return cudaGetLastError() == cudaSuccess ? USP_OK : USP_ERR_CUDA;
+    return launch_overlapped(paged_decode_kernel<HD, RT>, dim3((unsigned)grid), C::kThreads, kSmem, s, p, second);
 }
 
 }  // namespace
 
 int decode_ctas(int sms, int rows) { return rows == 16 ? 2 * sms : sms; }
 
-int launch_paged_decode(const PagedArgs &a, int rows, int n_hi, const PartSpace &w, cudaStream_t s) {
+int launch_paged_decode(const PagedArgs &a, int rows, int n_hi, bool second, const PartSpace &w, cudaStream_t s) {
     const DeviceInfo *di = device_info();
     if (!di) return USP_ERR_CUDA;
     DecodeParams p{};
@@ -551,30 +551,17 @@ int launch_paged_decode(const PagedArgs &a, int rows, int n_hi, const PartSpace 
     p.num_pages = (int32_t)a.num_pages; p.log_ps = a.log_ps; p.hq = a.hq;
     p.scale_log2 = a.scale_log2;
     if (rows == 16)
-        return a.hd == 128 ? launch_typed<128, 1>(p, w.ctas, s) : launch_typed<64, 1>(p, w.ctas, s);
-    return a.hd == 128 ? launch_typed<128, 2>(p, w.ctas, s) : launch_typed<64, 2>(p, w.ctas, s);
+        return a.hd == 128 ? launch_typed<128, 1>(p, w.ctas, second, s) : launch_typed<64, 1>(p, w.ctas, second, s);
+    return a.hd == 128 ? launch_typed<128, 2>(p, w.ctas, second, s) : launch_typed<64, 2>(p, w.ctas, second, s);
 }
 
 int launch_paged_combine(const CombineArgs &a, int hd, int dtype, cudaStream_t s) {
-    // launched while the kernel before it still runs; griddepcontrol.wait is its first instruction
-    cudaLaunchConfig_t cfg{};
     const int per = combine_rows(hd);
-    cfg.gridDim = dim3((unsigned)(a.w[0].ctas * ((a.w[0].rows + per - 1) / per) + a.w[1].ctas * ((a.w[1].rows + per - 1) / per)));
-    cfg.blockDim = dim3(kCombineThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    cudaError_t e;
+    const dim3 grid((unsigned)(a.w[0].ctas * ((a.w[0].rows + per - 1) / per) + a.w[1].ctas * ((a.w[1].rows + per - 1) / per)));
+    auto go = [&](auto kernel) { return launch_overlapped(kernel, grid, kCombineThreads, 0, s, a, true); };
     if (dtype == USP_BF16)
-        e = hd == 128 ? cudaLaunchKernelEx(&cfg, paged_combine_kernel<__nv_bfloat16, 128>, a)
-                      : cudaLaunchKernelEx(&cfg, paged_combine_kernel<__nv_bfloat16, 64>, a);
-    else
-        e = hd == 128 ? cudaLaunchKernelEx(&cfg, paged_combine_kernel<float, 128>, a)
-                      : cudaLaunchKernelEx(&cfg, paged_combine_kernel<float, 64>, a);
-    return e == cudaSuccess ? USP_OK : USP_ERR_CUDA;
+        return hd == 128 ? go(paged_combine_kernel<__nv_bfloat16, 128>) : go(paged_combine_kernel<__nv_bfloat16, 64>);
+    return hd == 128 ? go(paged_combine_kernel<float, 128>) : go(paged_combine_kernel<float, 64>);
 }
 
 }  // namespace usp

@@ -217,6 +217,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_f32_few_kernel(const __g
         }
     }
     if (tid == 0) p.w.head[blockIdx.x] = opened;
+    follow_grid_before();
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -489,7 +490,8 @@ int launch_many(const F32Params &p, int grid, cudaStream_t s) {
 int f32_ctas(int sms, bool many, int hd) { return many && hd == 128 ? sms : 2 * sms; }
 int f32_rows(bool many) { return many ? kManyRows : kFewRows; }
 
-int launch_paged_f32(const PagedArgs &a, bool many, int n_lo, int n_hi, const PartSpace &w, cudaStream_t s) {
+int launch_paged_f32(const PagedArgs &a, bool many, int n_lo, int n_hi, bool second, const PartSpace &w,
+                     cudaStream_t s) {
     F32Params p{};
     p.s.cu = a.cu; p.s.kv = a.kv;
     p.s.tokens = a.tokens; p.s.max_keys = (int64_t)a.max_pages << a.log_ps;
@@ -509,9 +511,8 @@ int launch_paged_f32(const PagedArgs &a, bool many, int n_lo, int n_hi, const Pa
     p.num_pages = (int32_t)a.num_pages; p.log_ps = a.log_ps; p.hq = a.hq;
     p.scale_log2 = a.scale_log2;
     if (many) return a.hd == 128 ? launch_many<128>(p, w.ctas, s) : launch_many<64>(p, w.ctas, s);
-    if (a.hd == 128) paged_f32_few_kernel<128><<<w.ctas, kFewThreads, 0, s>>>(p);
-    else paged_f32_few_kernel<64><<<w.ctas, kFewThreads, 0, s>>>(p);
-    return cudaGetLastError() == cudaSuccess ? USP_OK : USP_ERR_CUDA;
+    return launch_overlapped(a.hd == 128 ? paged_f32_few_kernel<128> : paged_f32_few_kernel<64>, dim3((unsigned)w.ctas),
+                             kFewThreads, 0, s, p, second);
 }
 
 }  // namespace usp

@@ -306,6 +306,26 @@ __device__ __forceinline__ float *part_slot(const PartSpace &w, int hd, int cta,
     return w.data + ((size_t)cta * 2 + slot) * (size_t)w.rows * (hd + 2);
 }
 
+// Launch of a call's later kernels: they may start while the one before still runs (as SMs come free), and
+// order themselves with griddepcontrol.wait where they need its results, at their end at the latest.
+template <typename K, typename P>
+inline int launch_overlapped(K kernel, dim3 grid, int threads, int smem, cudaStream_t s, const P &p, bool overlap) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = overlap ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? USP_OK : USP_ERR_CUDA;
+}
+// the end of a kernel that may have been launched early: the grid before has completed when this one has,
+// so that the combine, which waits for this one only, follows both
+__device__ __forceinline__ void follow_grid_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 struct CombineArgs {
     PartSpace w[2];  // one per kernel of the call (ctas == 0: not launched)
     void *out;
@@ -316,8 +336,9 @@ struct CombineArgs {
 };
 int launch_paged_combine(const CombineArgs &a, int hd, int dtype, cudaStream_t s);
 
-// bf16, units of up to `rows` (16 or 32) query rows; requests with at most n_hi new tokens
-int launch_paged_decode(const PagedArgs &a, int rows, int n_hi, const PartSpace &w, cudaStream_t s);
+// bf16, units of up to `rows` (16 or 32) query rows; requests with at most n_hi new tokens. `second`: the
+// call's other kernel is in the stream before it
+int launch_paged_decode(const PagedArgs &a, int rows, int n_hi, bool second, const PartSpace &w, cudaStream_t s);
 int decode_ctas(int sms, int rows);
 
 // bf16, units of up to kChunkRows query rows, one CTA per SM; requests with more than n_lo new tokens
@@ -325,7 +346,8 @@ constexpr int kChunkRows = 256;
 int launch_paged_chunk(const PagedArgs &a, int n_lo, const PartSpace &w, cudaStream_t s);
 
 // fp32: units of few (8) or many (128) query rows; requests with n_lo < new tokens <= n_hi
-int launch_paged_f32(const PagedArgs &a, bool many, int n_lo, int n_hi, const PartSpace &w, cudaStream_t s);
+int launch_paged_f32(const PagedArgs &a, bool many, int n_lo, int n_hi, bool second, const PartSpace &w,
+                     cudaStream_t s);
 int f32_ctas(int sms, bool many, int hd);
 int f32_rows(bool many);
 
