@@ -83,8 +83,8 @@ template <int HD> struct Cfg {
     static constexpr int kNumBars = TAIL + 2;
     static constexpr int kSlot = kBar + (kNumBars * 8 + 15) / 16 * 16;  // tensor memory address, skip flag
     static constexpr int kSeg = kSlot + 16;
-    // a staging slot per softmax warp for its stores: 32 rows x 64 bytes
-    static constexpr int kStgSlot = 32 * 64;
+    // a staging slot per softmax warp for its stores: 32 rows x 128 bytes
+    static constexpr int kStgSlot = 32 * 128;
     static constexpr int kStg = kSeg + kSegSlots * (int)sizeof(SegMsg);
     static constexpr int kSmem = kStg + kSoftmaxWarps * kStgSlot + 1024;  // + slack for the alignment
 };
@@ -490,23 +490,30 @@ __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegM
         ok = tc::mbar_wait(bar0 + 8u * (C::S_FULL + i), ns & 1u, p.status, USP_ERR_TIMEOUT, kWaitLimitNs);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        uint32_t sr[4][32];
         tc::fence_after_sync();
+        if (!full) {
+            // Mask S in place, only the 32-key chunks that some row of the warp sees not all of (a warp's
+            // rows are a few tokens with limits close together). A rolled loop of its own keeps 128 selects
+            // out of the code that every tile runs through: what runs once per unit mostly waits for its
+            // instructions.
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                const int lc = lim - kt * kN - c * 32;
+                if (__all_sync(0xffffffffu, lc >= 32)) continue;
+                uint32_t x[32];
+                tc::tmem_ld32(tS + c * 32, x);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if (e >= lc) x[e] = __float_as_uint(-INFINITY);
+                tc::tmem_st32(tS + c * 32, x);
+                tc::tmem_st_wait();
+            }
+        }
+        uint32_t sr[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tc::tmem_ld32(tS + c * 32, sr[c]);
         tc::tmem_ld_wait();
-        if (!full) {
-            // (a warp's rows are a few tokens with limits close together: whole chunks are visible to all)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int lc = lim - kt * kN - c * 32;
-                if (__any_sync(0xffffffffu, lc < 32)) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (e >= lc) sr[c][e] = __float_as_uint(-INFINITY);
-                }
-            }
-        }
         float mx = -INFINITY;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -570,6 +577,7 @@ __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegM
     const int r = i * p.tq_tokens * p.s.G + row;  // row of the unit
     float *slot = part_slot(p.w, HD, blockIdx.x, g.t0 == 0 ? 1 : 0);
     const int head = g.head * p.s.G + (int)rh;
+    __nv_bfloat16 *orow = p.out + (g.tok0 + tok) * p.out_stride + (int64_t)head * HD;
     const float inv = l > 0.f ? 1.f / l : 0.f;
     if (any) {
         ok = tc::mbar_wait(bar0 + 8u * (C::O_FULL + i), no & 1u, p.status, USP_ERR_TIMEOUT, kWaitLimitNs);
@@ -577,65 +585,59 @@ __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegM
         if (!ok) return false;
         ++no;
         tc::fence_after_sync();
-        uint32_t o[HD / 32][32];
-#pragma unroll
-        for (int c = 0; c < HD / 32; ++c) tc::tmem_ld32(tO + c * 32, o[c]);
-        tc::tmem_ld_wait();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bar0 + 8u * (C::O_EMPTY + i));
-        // A lane holds a row, and rows lie apart in memory: each 64 bytes of the 32 rows go through the warp's
-        // staging slot, 16-byte pieces swizzled by (row / 2) % 4 against bank conflicts, so that a store
-        // instruction writes 8 whole 64-byte pieces of rows instead of 32 scattered 16-byte ones (measured:
-        // a segment's end took 5000 cycles with a store per lane and row).
+        // A lane holds a row, and rows lie apart in memory: 128 bytes of each of the 32 rows go through the
+        // warp's staging slot, 16-byte pieces swizzled by row % 8 against bank conflicts, so that a store
+        // instruction writes four whole lines instead of 32 scattered pieces.
         const uint32_t stg = tc::smem_u32(smem) + C::kStg + warp * C::kStgSlot;
-        const int sub = lane >> 2, pc = lane & 3;  // row of 8 and piece of 4 that this lane stores
-        char *dst[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const uint32_t rr = wq * 32 + x * 8 + sub;
-            uint32_t t, h;
-            p.s.by_G.divmod(rr, t, h);
-            const int tk = i * p.tq_tokens + (int)t;
-            const bool in = (int)rr < p.tq_tokens * p.s.G && tk < g.ntok;
-            char *to = whole ? reinterpret_cast<char *>(p.out + (g.tok0 + tk) * p.out_stride +
-                                                        (int64_t)(g.head * p.s.G + (int)h) * HD)
-                             : reinterpret_cast<char *>(slot + (size_t)(i * p.tq_tokens * p.s.G + (int)rr) * HD);
-            dst[x] = in ? to + pc * 16 : nullptr;
-        }
-        auto stage_out = [&](const uint32_t (&w)[16], int at) {  // 64 bytes of the lane's row, to byte `at`
-#pragma unroll
-            for (int c4 = 0; c4 < 4; ++c4)
-                st_shared_v4(stg + (uint32_t)lane * 64u + (((uint32_t)c4 ^ (((uint32_t)lane >> 1) & 3u)) << 4),
-                             w[4 * c4], w[4 * c4 + 1], w[4 * c4 + 2], w[4 * c4 + 3]);
+        const int sub = lane >> 3, pc = lane & 7;  // row of 4 and piece of 8 that this lane stores
+        const uint64_t mine = !row_ok ? 0
+                              : whole ? reinterpret_cast<uint64_t>(orow)
+                                      : reinterpret_cast<uint64_t>(slot + (size_t)r * HD);
+        auto stage_in = [&](int c, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+            st_shared_v4(stg + (uint32_t)lane * 128u + (((uint32_t)c ^ ((uint32_t)lane & 7u)) << 4), x, y, z, w);
+        };
+        auto stage_out = [&](uint32_t at) {  // the staged 128 bytes of every row, to byte `at` of the rows
             __syncwarp();
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const uint32_t rr = (uint32_t)x * 8u + (uint32_t)sub;
-                const uint4 v = ld_shared_v4(stg + rr * 64u + (((uint32_t)pc ^ ((rr >> 1) & 3u)) << 4));
-                if (dst[x]) *reinterpret_cast<uint4 *>(dst[x] + at) = v;
+            for (int x = 0; x < 8; ++x) {
+                const uint32_t rr = (uint32_t)x * 4u + (uint32_t)sub;
+                const uint4 v = ld_shared_v4(stg + rr * 128u + (((uint32_t)pc ^ (rr & 7u)) << 4));
+                const uint64_t to = __shfl_sync(0xffffffffu, mine, (int)rr);
+                if (to) *reinterpret_cast<uint4 *>(to + at + (uint32_t)pc * 16u) = v;
             }
             __syncwarp();
         };
-#pragma unroll
-        for (int c = 0; c < HD / 32; ++c) {
-            uint32_t w[16];
+#pragma unroll 1
+        for (uint32_t c = 0; c < HD / 64; ++c) {
+            uint32_t o[2][32];
+            tc::tmem_ld32(tO + c * 64, o[0]);
+            tc::tmem_ld32(tO + c * 64 + 32, o[1]);
+            tc::tmem_ld_wait();
             if (whole) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    w[e] = float2_to_bf16x2(u2f(o[c][2 * e]) * inv, u2f(o[c][2 * e + 1]) * inv);
-                stage_out(w, c * 64);
+                for (int c8 = 0; c8 < 8; ++c8) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        w[e] = float2_to_bf16x2(u2f(o[c8 / 4][c8 % 4 * 8 + 2 * e]) * inv,
+                                                u2f(o[c8 / 4][c8 % 4 * 8 + 2 * e + 1]) * inv);
+                    stage_in(c8, w[0], w[1], w[2], w[3]);
+                }
+                stage_out(c * 128);
             } else {
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
+                for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) w[e] = o[c][hf * 16 + e];
-                    stage_out(w, c * 128 + hf * 64);
+                    for (int c8 = 0; c8 < 8; ++c8)
+                        stage_in(c8, o[h][c8 * 4], o[h][c8 * 4 + 1], o[h][c8 * 4 + 2], o[h][c8 * 4 + 3]);
+                    stage_out(c * 256 + h * 128);
                 }
             }
         }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar0 + 8u * (C::O_EMPTY + i));
     } else if (row_ok && whole) {
-        __nv_bfloat16 *orow = p.out + (g.tok0 + tok) * p.out_stride + (int64_t)head * HD;
         for (int e = 0; e < HD; e += 8) *reinterpret_cast<uint4 *>(orow + e) = make_uint4(0, 0, 0, 0);
     }
     if (row_ok) {
