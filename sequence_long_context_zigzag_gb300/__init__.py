@@ -526,10 +526,6 @@ _layouts: dict = {}
 _MAX_LAYOUTS = 4096
 
 
-def _layout(*ts):
-    return [(t.shape, t.stride(), t.dtype, t.get_device()) for t in ts]
-
-
 def _keep(key, value):
     if len(_layouts) >= _MAX_LAYOUTS:
         _layouts.clear()
@@ -582,13 +578,14 @@ def _block_table(t: torch.Tensor, nreq: int) -> int:
 # the raw handle of a device's current stream, without the Stream object where torch has the call
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _with_stream(index: int, stream, call):
     """call(raw stream) with the tensors' device current and, where ``stream`` is given, with it as the
     current stream, so that what the call allocates is ordered on the stream that uses it."""
     if stream is None:
-        if torch.cuda.current_device() == index:
+        if _current_device() == index:
             return call(_raw_stream(index))
         with torch.cuda.device(index):
             return call(_raw_stream(index))
@@ -609,7 +606,10 @@ def usp_page_plan(ctx_lens, new_lens, free_pages, free_head, block_table, page_s
     ``max_tokens`` new tokens (-1: none), cumulative new lengths, keys per request, and (new tokens, the
     next free head, tokens left without a slot, largest kv length). The next step passes kv_lens as
     ctx_lens and counts[1:2] as free_head, with other output tensors than its inputs."""
-    key = ("plan", *_layout(ctx_lens, new_lens, free_pages, free_head, block_table), page_size, num_pages, max_tokens)
+    key = (ctx_lens.shape, ctx_lens.stride(), ctx_lens.dtype, ctx_lens.device, new_lens.shape, new_lens.stride(),
+           new_lens.dtype, new_lens.device, free_pages.shape, free_pages.stride(), free_pages.dtype, free_pages.device,
+           free_head.shape, free_head.stride(), free_head.dtype, free_head.device, block_table.shape,
+           block_table.stride(), block_table.dtype, block_table.device, page_size, num_pages, max_tokens)
     d = _layouts.get(key)
     if d is None:
         nreq = ctx_lens.numel()
@@ -633,9 +633,11 @@ def usp_page_plan(ctx_lens, new_lens, free_pages, free_head, block_table, page_s
             return t
         slots, cu = output("slot_map", slot_map, max_tokens), output("cu_new", cu_new, d.nreq + 1)
         kv, cnt = output("kv_lens", kv_lens, d.nreq), output("counts", counts, 4)
-        _abi.check("usp_page_plan", _abi.load().usp_page_plan(
+        rc = _abi.load().usp_page_plan(
             ctx_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), free_head.data_ptr(),
-            block_table.data_ptr(), slots.data_ptr(), cu.data_ptr(), kv.data_ptr(), cnt.data_ptr(), d, raw))
+            block_table.data_ptr(), slots.data_ptr(), cu.data_ptr(), kv.data_ptr(), cnt.data_ptr(), d, raw)
+        if rc:
+            _abi.check("usp_page_plan", rc)
         return slots, cu, kv, cnt
 
     return _with_stream(dev.index, stream, call)
@@ -645,7 +647,9 @@ def usp_cache_append(k, v, k_cache, v_cache, slot_map, stream=None):
     """Write the rows of k and v (tokens, hkv, hd) into their slots of the caches
     (num_pages, hkv, page_size, hd), in place; a token with slot -1 is skipped. The first axis of every
     tensor may be strided (slices of a fused projection, a cache that interleaves K and V)."""
-    key = ("append", *_layout(k, v, k_cache, v_cache, slot_map))
+    key = (k.shape, k.stride(), k.dtype, k.device, v.shape, v.stride(), v.dtype, v.device, k_cache.shape,
+           k_cache.stride(), k_cache.dtype, k_cache.device, v_cache.shape, v_cache.stride(), v_cache.dtype,
+           v_cache.device, slot_map.shape, slot_map.stride(), slot_map.dtype, slot_map.device)
     spec = _layouts.get(key)
     if spec is None:
         d = _cache_dims(k_cache, v_cache)
@@ -696,7 +700,11 @@ def usp_paged_attn(q, k_cache, v_cache, block_table, cu_new, kv_lens, max_new: O
             raise ValueError("out must match q")
         out_stride = _dense_rows("out", out)
         _same_device(q, out)
-    key = ("attn", *_layout(q, k_cache, v_cache, block_table, cu_new, kv_lens), max_new, causal, scale, out_stride)
+    dev = q.device
+    key = (q.shape, q.stride(), q.dtype, dev, k_cache.shape, k_cache.stride(), k_cache.dtype, k_cache.device,
+           v_cache.shape, v_cache.stride(), v_cache.dtype, v_cache.device, block_table.shape, block_table.stride(),
+           block_table.dtype, block_table.device, cu_new.shape, cu_new.stride(), cu_new.dtype, cu_new.device,
+           kv_lens.shape, kv_lens.stride(), kv_lens.dtype, kv_lens.device, max_new, causal, scale, out_stride)
     d = _layouts.get(key)
     if d is None:
         nreq = kv_lens.numel()
@@ -705,7 +713,6 @@ def usp_paged_attn(q, k_cache, v_cache, block_table, cu_new, kv_lens, max_new: O
         d = _paged_desc(q, k_cache, v_cache, block_table, nreq, max_new, causal, scale, out_stride)
         _same_device(q, k_cache, v_cache, block_table, cu_new, kv_lens)
         _keep(key, d)
-    dev = q.device
 
     def call(raw):
         lib = _abi.load()
@@ -720,11 +727,13 @@ def usp_paged_attn(q, k_cache, v_cache, block_table, cu_new, kv_lens, max_new: O
             _same_device(q, l)
         if w is None:
             w = torch.empty(max(lib.usp_paged_attn_workspace_size(d), 1), dtype=torch.uint8, device=dev)
-        elif w.get_device() != dev.index or not w.is_contiguous():
+        elif w.device != dev or not w.is_contiguous():
             raise ValueError("workspace must be contiguous, on the tensors' device")
-        _abi.check("usp_paged_attn", lib.usp_paged_attn(
+        rc = lib.usp_paged_attn(
             q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), cu_new.data_ptr(),
-            kv_lens.data_ptr(), o.data_ptr(), l.data_ptr(), d, w.data_ptr(), w.numel() * w.element_size(), raw))
+            kv_lens.data_ptr(), o.data_ptr(), l.data_ptr(), d, w.data_ptr(), w.nbytes, raw)
+        if rc:
+            _abi.check("usp_paged_attn", rc)
         return o, l
 
     return _with_stream(dev.index, stream, call)

@@ -66,10 +66,12 @@ Route route(const usp_paged_desc &d, int sms) {
     if (rows > most || G > (bf16 ? 32 : f32_rows(false))) {
         r.many_ctas = bf16 ? sms : f32_ctas(sms, true, d.cache.hd);
         r.many_rows = bf16 ? kChunkRows : f32_rows(true);
-        r.split = G > (bf16 ? 32 : f32_rows(false)) ? 0 : most / G;
+        // beside chunks, the few-row requests are mostly single tokens: the 16-row kernel (two CTAs per SM)
+        // takes those, the other one all chunks (33 requests, 26 of one token: 49 -> 40 us)
+        r.split = G > (bf16 ? 32 : f32_rows(false)) ? 0 : (G <= 16 ? 16 : most) / G;
     }
     if (r.split > 0) {
-        r.few_rows = bf16 ? (rows <= 16 ? 16 : 32) : f32_rows(false);
+        r.few_rows = bf16 ? (std::min<int64_t>(rows, (int64_t)r.split * G) <= 16 ? 16 : 32) : f32_rows(false);
         r.few_ctas = bf16 ? decode_ctas(sms, r.few_rows) : f32_ctas(sms, false, d.cache.hd);
     }
     return r;

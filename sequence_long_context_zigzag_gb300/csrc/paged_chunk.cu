@@ -51,7 +51,7 @@ static_assert(kControlRegs >= 24 && kControlRegs % 8 == 0 &&
                   2 * kSoftmaxRegs + kControlRegs == kLaunchRegs * kWarps / 4,
               "register split must use exactly the launch's registers");
 constexpr int kOver = 192;     // a unit's constant cost, in keys
-constexpr int kMinSpan = 768;  // keys per CTA below which fewer CTAs work
+constexpr int kMinSpan = 448;  // keys per CTA below which fewer CTAs work
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr float kRescale = 8.0f;  // log2 units
 constexpr float kLn2 = 0.69314718055994531f;

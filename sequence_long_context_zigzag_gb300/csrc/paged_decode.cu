@@ -434,68 +434,85 @@ __global__ void __launch_bounds__(Cfg<HD, RT>::kThreads, RT == 1 ? 2 : 1)
 // ------------------------------------------------------------------------------------------------
 // combine: out and lse of the units that spans cut
 // ------------------------------------------------------------------------------------------------
-// A thread computes 4 columns of a row over all parts of its unit: o = sum_i 2^(m_i - M) o_i / l, in the
-// parts' order, so the result does not depend on timing. Bound by latency (the header, the parts' maxima,
-// the parts), so the first two parts' rows (most units have no more) are fetched with the maxima. A part
-// whose rows saw nothing has m = -inf, and its o (perhaps unwritten) is not used.
-constexpr int kCombineThreads = 256;
-__host__ __device__ constexpr int combine_rows(int hd) { return kCombineThreads / (hd / 4); }  // rows per CTA
+// A thread computes 4 columns of a row over all parts of its unit: o = sum_i 2^(m_i - M) o_i / l, online,
+// in the parts' order, so the result does not depend on timing. Bound by latency (the header, then the
+// parts), so the maxima, sums and rows of 8 parts are fetched at once, which is all of them for most
+// units. A part whose rows saw nothing has m = -inf, and its o (perhaps unwritten) is not used. Small CTAs:
+// some fit beside the decode kernel's and are in place when it ends.
+constexpr int kCombineThreads = 128;
+constexpr int kCombineRows = 16;  // rows per CTA
+constexpr int kBatch = 8;
 
 template <typename T, int HD>
 __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const CombineArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr bool kExact = sizeof(T) == 4;  // the fp32 path has no fast functions
+    constexpr int kStep = kCombineThreads / (HD / 4);
     auto exp2_of = [](float x) { return kExact ? exp2f(x) : tc::ex2(x); };
-    const int per0 = (a.w[0].rows + combine_rows(HD) - 1) / combine_rows(HD);
-    const int per1 = (a.w[1].rows + combine_rows(HD) - 1) / combine_rows(HD);
+    const int per0 = (a.w[0].rows + kCombineRows - 1) / kCombineRows;
+    const int per1 = (a.w[1].rows + kCombineRows - 1) / kCombineRows;
     const bool second = (int)blockIdx.x >= a.w[0].ctas * per0;
     const PartSpace w = second ? a.w[1] : a.w[0];
     const int x = (int)blockIdx.x - (second ? a.w[0].ctas * per0 : 0), per = second ? per1 : per0;
-    const int c = x / per, r = x % per * combine_rows(HD) + (int)threadIdx.x / (HD / 4);
+    const int c = x / per, r0 = x % per * kCombineRows;
     const int col = (int)threadIdx.x % (HD / 4) * 4;
     const PartHeader h = w.head[c];
-    if (r >= h.rows) return;
     const int parts = h.last - c + 1;
     const size_t step = 2 * (size_t)w.rows * (HD + 2);  // from a CTA's slot to the next CTA's
     const float *cont = part_slot(w, HD, c + 1, 0);       // parts 1, 2, ...
     const float *open = part_slot(w, HD, c, 1);           // part 0
-    auto part = [&](int i) { return i == 0 ? open : cont + (i - 1) * step; };
-    const size_t at_m = (size_t)w.rows * HD + r, at_l = at_m + w.rows, at_o = (size_t)r * HD + col;
-    auto load4 = [&](int i) { return *reinterpret_cast<const float4 *>(part(i) + at_o); };
-    const float4 o0 = load4(0), o1 = load4(1);  // a unit that was cut has two parts at least
-    float M = -INFINITY;
-#pragma unroll 4
-    for (int i = 0; i < parts; ++i) M = fmaxf(M, part(i)[at_m]);
-    const float Mb = M == -INFINITY ? 0.f : M;
-    float L = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](int i, float4 v) {
-        const float g = exp2_of(part(i)[at_m] - Mb);
-        L = fmaf(g, part(i)[at_l], L);
-        if (g > 0.f) {
-            acc.x = fmaf(g, v.x, acc.x);
-            acc.y = fmaf(g, v.y, acc.y);
-            acc.z = fmaf(g, v.z, acc.z);
-            acc.w = fmaf(g, v.w, acc.w);
+    for (int r = r0 + (int)threadIdx.x / (HD / 4); r < min(r0 + kCombineRows, h.rows); r += kStep) {
+        const size_t at_m = (size_t)w.rows * HD + r, at_l = at_m + w.rows, at_o = (size_t)r * HD + col;
+        float M = -INFINITY, L = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int base = 0; base < parts; base += kBatch) {
+            float m[kBatch], l[kBatch];
+            float4 o[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                m[i] = -INFINITY;
+                l[i] = 0.f;
+                o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (base + i < parts) {
+                    const float *s = base + i == 0 ? open : cont + (base + i - 1) * step;
+                    m[i] = s[at_m];
+                    l[i] = s[at_l];
+                    o[i] = *reinterpret_cast<const float4 *>(s + at_o);
+                }
+            }
+            float mx = M;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) mx = fmaxf(mx, m[i]);
+            const float mb = mx == -INFINITY ? 0.f : mx, g0 = exp2_of(M - mb);
+            M = mx;
+            L *= g0;
+            acc.x *= g0; acc.y *= g0; acc.z *= g0; acc.w *= g0;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const float g = exp2_of(m[i] - mb);
+                if (g > 0.f) {
+                    L = fmaf(g, l[i], L);
+                    acc.x = fmaf(g, o[i].x, acc.x);
+                    acc.y = fmaf(g, o[i].y, acc.y);
+                    acc.z = fmaf(g, o[i].z, acc.z);
+                    acc.w = fmaf(g, o[i].w, acc.w);
+                }
+            }
         }
-    };
-    add(0, o0);
-    add(1, o1);
-#pragma unroll 4
-    for (int i = 2; i < parts; ++i) add(i, load4(i));
-    const float inv = L > 0.f ? 1.f / L : 0.f;
-    uint32_t tok, hr;
-    a.by_G.divmod((uint32_t)r, tok, hr);
-    const int head = h.head * a.G + (int)hr;
-    T *o = static_cast<T *>(a.out) + (h.tok0 + tok) * a.out_stride + (int64_t)head * HD + col;
-    if constexpr (kExact) {
-        *reinterpret_cast<float4 *>(o) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    } else {
-        *reinterpret_cast<uint2 *>(o) =
-            make_uint2(float2_to_bf16x2(acc.x * inv, acc.y * inv), float2_to_bf16x2(acc.z * inv, acc.w * inv));
+        const float inv = L > 0.f ? 1.f / L : 0.f;
+        uint32_t tok, hr;
+        a.by_G.divmod((uint32_t)r, tok, hr);
+        const int head = h.head * a.G + (int)hr;
+        T *to = static_cast<T *>(a.out) + (h.tok0 + tok) * a.out_stride + (int64_t)head * HD + col;
+        if constexpr (kExact) {
+            *reinterpret_cast<float4 *>(to) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        } else {
+            *reinterpret_cast<uint2 *>(to) =
+                make_uint2(float2_to_bf16x2(acc.x * inv, acc.y * inv), float2_to_bf16x2(acc.z * inv, acc.w * inv));
+        }
+        if (col == 0)
+            a.lse[(h.tok0 + tok) * a.hq + head] = L > 0.f ? (M + (kExact ? log2f(L) : __log2f(L))) * kLn2 : -INFINITY;
     }
-    if (col == 0)
-        a.lse[(h.tok0 + tok) * a.hq + head] = L > 0.f ? (M + (kExact ? log2f(L) : __log2f(L))) * kLn2 : -INFINITY;
 }
 
 template <int HD, int RT>
@@ -556,7 +573,7 @@ int launch_paged_decode(const PagedArgs &a, int rows, int n_hi, bool second, con
 }
 
 int launch_paged_combine(const CombineArgs &a, int hd, int dtype, cudaStream_t s) {
-    const int per = combine_rows(hd);
+    const int per = kCombineRows;
     const dim3 grid((unsigned)(a.w[0].ctas * ((a.w[0].rows + per - 1) / per) + a.w[1].ctas * ((a.w[1].rows + per - 1) / per)));
     auto go = [&](auto kernel) { return launch_overlapped(kernel, grid, kCombineThreads, 0, s, a, true); };
     if (dtype == USP_BF16)
