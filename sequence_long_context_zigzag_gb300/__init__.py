@@ -625,14 +625,24 @@ def usp_page_plan(ctx_lens, new_lens, free_pages, free_head, block_table, page_s
     dev = ctx_lens.device
 
     def call(raw):
-        def output(name, t, n):
-            if t is None:
-                return torch.empty(n, dtype=torch.int32, device=dev)
-            _i32(name, t, n)
-            _same_device(ctx_lens, t)
-            return t
-        slots, cu = output("slot_map", slot_map, max_tokens), output("cu_new", cu_new, d.nreq + 1)
-        kv, cnt = output("kv_lens", kv_lens, d.nreq), output("counts", counts, 4)
+        nreq = d.nreq
+        if slot_map is None and cu_new is None and kv_lens is None and counts is None:
+            # one allocation, in four views
+            buf = torch.empty(max_tokens + 2 * nreq + 5, dtype=torch.int32, device=dev)
+            one = (1,)
+            cnt = buf.as_strided((4,), one, 0)
+            slots = buf.as_strided((max_tokens,), one, 4)
+            cu = buf.as_strided((nreq + 1,), one, 4 + max_tokens)
+            kv = buf.as_strided((nreq,), one, 5 + max_tokens + nreq)
+        else:
+            def output(name, t, n):
+                if t is None:
+                    return torch.empty(n, dtype=torch.int32, device=dev)
+                _i32(name, t, n)
+                _same_device(ctx_lens, t)
+                return t
+            slots, cu = output("slot_map", slot_map, max_tokens), output("cu_new", cu_new, nreq + 1)
+            kv, cnt = output("kv_lens", kv_lens, nreq), output("counts", counts, 4)
         rc = _abi.load().usp_page_plan(
             ctx_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), free_head.data_ptr(),
             block_table.data_ptr(), slots.data_ptr(), cu.data_ptr(), kv.data_ptr(), cnt.data_ptr(), d, raw)

@@ -10,9 +10,11 @@
 //   score per lane (row lane / 4, key lane % 4): 31 shuffles for 32 sums.
 // many rows (paged_f32_many_kernel, units of up to 128 query rows): bound by the fp32 pipes
 //   (128 lanes per SM). 256 threads compute 128 x 64 scores, 8 x 4 each, and 128 x hd outputs, 8 x hd / 16
-//   each, from shared memory in which the summed index is the slow one (Q, K transposed, P written
-//   transposed), so a thread reads its 8 and 4 operands as 16-byte words and gets 32 multiply-adds from
-//   three of them. Products run two rows at a time (packed fp32 pairs: half the issue slots).
+//   each, from shared memory: Q and P lie transposed (the summed index is the slow one), K and V as they
+//   come, so a thread reads its 8 rows, and 4 elements of each of its 4 keys, as 16-byte words and gets 128
+//   multiply-adds from twelve of them. Products run two rows at a time (packed fp32 pairs: half the issue
+//   slots). K and V come by asynchronous copies: V during a tile's scores, the next K during its outputs,
+//   so the copies hold no registers (with register prefetch the loop had none left to run its loads ahead).
 #include <math.h>
 
 #include <algorithm>
@@ -230,13 +232,20 @@ constexpr int kManyOver = 64, kManyMinSpan = 256;
 
 template <int HD> struct Many {
     static constexpr int kQRow = kManyRows + 4;  // floats per row of the transposed Q and P
-    static constexpr int kKRow = kManyKT + 4;    // of the transposed K
+    static constexpr int kKRow = HD + 4;         // of K: 16 keys' pieces of a column then lie on all banks
     static constexpr int kQ = 0;                        // [HD][kQRow]
-    static constexpr int kK = kQ + HD * kQRow;          // [HD][kKRow]
-    static constexpr int kV = kK + HD * kKRow;          // [kManyKT][HD]
+    static constexpr int kK = kQ + HD * kQRow;          // [kManyKT][kKRow]
+    static constexpr int kV = kK + kManyKT * kKRow;     // [kManyKT][HD]
     static constexpr int kP = kV + kManyKT * HD;        // [kManyKT][kQRow]
     static constexpr int kFloats = kP + kManyKT * kQRow;
 };
+
+// 16 bytes global -> shared; zeros when !ok (src is not read then)
+__device__ __forceinline__ void copy16(uint32_t dst, const float *src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ void load_pairs(const float *p, uint64_t (&x)[4]) {  // 8 floats as 4 pairs
     const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(p), b = *reinterpret_cast<const ulonglong2 *>(p + 4);
@@ -247,11 +256,11 @@ template <int HD>
 __global__ void __launch_bounds__(kManyThreads, HD == 64 ? 2 : 1) paged_f32_many_kernel(const __grid_constant__ F32Params p) {
     using C = Many<HD>;
     constexpr int kCols = HD / 64;             // groups of 4 output columns per thread
-    constexpr int kLd = kManyKT * HD / 4 / kManyThreads;  // 16-byte loads of K (and V) per thread
+    constexpr int kLd = kManyKT * HD / 4 / kManyThreads;  // 16-byte copies of K (and V) per thread
     extern __shared__ __align__(16) float sm[];
     __shared__ SchedShared sh;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    float *qt = sm + C::kQ, *kt = sm + C::kK, *vs = sm + C::kV, *pt = sm + C::kP;
+    float *qt = sm + C::kQ, *ks = sm + C::kK, *vs = sm + C::kV, *pt = sm + C::kP;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     // thread 0 walks the span; its state stays in shared memory, out of the products' registers
     __shared__ Sched sc;
@@ -288,26 +297,19 @@ __global__ void __launch_bounds__(kManyThreads, HD == 64 ? 2 : 1) paged_f32_many
             }
             const int32_t *row = p.table + (int64_t)g.req * p.table_stride;
             const int ps = 1 << p.log_ps;
-            auto src = [&](const float *base, int64_t stride, int key) -> const float * {
-                if (key >= g.kv) return nullptr;
-                const int32_t page = __ldg(row + (key >> p.log_ps));
-                if (page < 0 || page >= p.num_pages) return nullptr;
-                return base + page * stride + ((int64_t)g.head * ps + (key & (ps - 1))) * HD;
-            };
-            // K: thread = key tid % 64, a run of 16-byte pieces; V: whole rows over consecutive threads
-            float4 kr[kLd], vr[kLd];
-            auto fetch = [&](int t) {
-                const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-                const float *a = src(p.k, p.k_page, t * kManyKT + (tid & 63));
-#pragma unroll
-                for (int i = 0; i < kLd; ++i)
-                    kr[i] = a ? __ldg(reinterpret_cast<const float4 *>(a) + (tid >> 6) * kLd + i) : zero;
+            // whole rows over consecutive threads; zeros behind the request's keys and for pages outside the cache
+            auto fetch = [&](int t, const float *base, int64_t stride, const float *to, int to_row) {
 #pragma unroll
                 for (int i = 0; i < kLd; ++i) {
-                    const int x = tid + i * kManyThreads;
-                    const float *b = src(p.v, p.v_page, t * kManyKT + x / (HD / 4));
-                    vr[i] = b ? __ldg(reinterpret_cast<const float4 *>(b) + x % (HD / 4)) : zero;
+                    const int x = tid + i * kManyThreads, r = x / (HD / 4), c = x % (HD / 4) * 4;
+                    const int key = t * kManyKT + r;
+                    int32_t page = -1;
+                    if (key < g.kv) page = __ldg(row + (key >> p.log_ps));
+                    const bool ok = page >= 0 && page < p.num_pages;
+                    const float *from = ok ? base + page * stride + ((int64_t)g.head * ps + (key & (ps - 1))) * HD + c : base;
+                    copy16(tc::smem_u32(to + r * to_row + c), from, ok);
                 }
+                copies_commit();
             };
             // keys each of this thread's rows sees
             int lim[8];
@@ -325,38 +327,35 @@ __global__ void __launch_bounds__(kManyThreads, HD == 64 ? 2 : 1) paged_f32_many
 #pragma unroll
                 for (int c = 0; c < 4 * kCols; ++c) o[i][c] = 0;
             const int lim_all = p.s.causal ? max(0, min(g.kv, g.p0 + 1)) : g.kv;
-            if (g.t0 < g.t1) fetch(g.t0);
+            if (g.t0 < g.t1) fetch(g.t0, p.k, p.k_page, ks, C::kKRow);
             for (int t = g.t0; t < g.t1; ++t) {
-                __syncthreads();  // the previous tile's products are done
-#pragma unroll
-                for (int i = 0; i < kLd; ++i) {
-                    float *d = kt + ((tid >> 6) * kLd + i) * 4 * C::kKRow + (tid & 63);
-                    d[0] = kr[i].x;
-                    d[C::kKRow] = kr[i].y;
-                    d[2 * C::kKRow] = kr[i].z;
-                    d[3 * C::kKRow] = kr[i].w;
-                    reinterpret_cast<float4 *>(vs)[tid + i * kManyThreads] = vr[i];
-                }
-                __syncthreads();
-                if (t + 1 < g.t1) fetch(t + 1);
+                copies_wait_all();  // K of this tile
+                __syncthreads();    // everyone's; and the previous tile's outputs are done with V
+                fetch(t, p.v, p.v_page, vs, HD);
                 uint64_t s[4][4];  // [row pair][key]
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) s[i][j] = 0;
-#pragma unroll 8
-                for (int d = 0; d < HD; ++d) {
-                    uint64_t q2[4];
-                    load_pairs(qt + d * C::kQRow + ty * 8, q2);
-                    const float4 k4 = *reinterpret_cast<const float4 *>(kt + d * C::kKRow + tx * 4);
-                    const uint64_t kk[4] = {tc::pack2(k4.x, k4.x), tc::pack2(k4.y, k4.y), tc::pack2(k4.z, k4.z),
-                                            tc::pack2(k4.w, k4.w)};
+#pragma unroll 2
+                for (int d = 0; d < HD; d += 4) {
+                    float k4[4][4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                    for (int j = 0; j < 4; ++j)
+                        *reinterpret_cast<float4 *>(k4[j]) = *reinterpret_cast<const float4 *>(ks + (tx + 16 * j) * C::kKRow + d);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) s[i][j] = tc::fma2(q2[i], kk[j], s[i][j]);
+                    for (int e = 0; e < 4; ++e) {
+                        uint64_t q2[4];
+                        load_pairs(qt + (d + e) * C::kQRow + ty * 8, q2);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint64_t kk = tc::pack2(k4[j][e], k4[j][e]);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) s[i][j] = tc::fma2(q2[i], kk, s[i][j]);
+                        }
+                    }
                 }
-                const int key0 = t * kManyKT + tx * 4;
+                const int key0 = t * kManyKT + tx;  // this thread's keys: key0 + 16 j
                 const bool edge = (t + 1) * kManyKT > lim_all;
                 float w[8][4];
 #pragma unroll
@@ -370,7 +369,7 @@ __global__ void __launch_bounds__(kManyThreads, HD == 64 ? 2 : 1) paged_f32_many
                     if (edge) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            if (key0 + j >= lim[i]) w[i][j] = -INFINITY;
+                            if (key0 + 16 * j >= lim[i]) w[i][j] = -INFINITY;
                     }
                     float x = fmaxf(fmaxf(w[i][0], w[i][1]), fmaxf(w[i][2], w[i][3]));
 #pragma unroll
@@ -403,12 +402,13 @@ __global__ void __launch_bounds__(kManyThreads, HD == 64 ? 2 : 1) paged_f32_many
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    float4 *d = reinterpret_cast<float4 *>(pt + (tx * 4 + j) * C::kQRow + ty * 8);
+                    float4 *d = reinterpret_cast<float4 *>(pt + (tx + 16 * j) * C::kQRow + ty * 8);
                     d[0] = make_float4(w[0][j], w[1][j], w[2][j], w[3][j]);
                     d[1] = make_float4(w[4][j], w[5][j], w[6][j], w[7][j]);
                 }
-                // a warp reads only the rows it wrote (its two ty), for all keys: 16 lanes each
-                __syncwarp();
+                copies_wait_all();  // V
+                __syncthreads();    // everyone's; and all are done with K
+                if (t + 1 < g.t1) fetch(t + 1, p.k, p.k_page, ks, C::kKRow);
 #pragma unroll 4
                 for (int d = 0; d < kManyKT; ++d) {
                     uint64_t p2[4];
