@@ -261,18 +261,17 @@ __device__ void consumer(const DecodeParams &p, uint8_t *smem, uint32_t sbase) {
                         for (int e = 0; e < 4; ++e)
                             if (key0 + n * 8 + qc + (e & 1) >= lim[e >> 1]) s[n][e] = -INFINITY;
                 }
+                // a row's maximum over its four lanes is needed only when some lane's own exceeds the bound
                 float mx[2];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float x = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                    mx[h] = x * p.scale_log2;
-                }
+                for (int h = 0; h < 2; ++h)
+                    mx[h] = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1])) * p.scale_log2;
                 const bool need = mx[0] > m[0] + kRescale || mx[1] > m[1] + kRescale;
                 if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
+                        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+                        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
                         const float mn = fmaxf(m[h], mx[h]);
                         const float a = mn == -INFINITY ? 1.f : tc::ex2(m[h] - mn);
                         m[h] = mn;

@@ -1,4 +1,5 @@
-// paged_f32.cu -- fp32 attention over the paged cache on the CUDA cores, fp32 throughout.
+// paged_f32.cu -- fp32 attention over the paged cache on the CUDA cores, fp32 throughout (weights by the
+// special-function unit's 2^x, whose error of 2^-22 is that of the scores' own sums).
 //
 // Mathematics and division of the work as in the bf16 kernels (online softmax with lazy rescale, spans of
 // equal cost, cut units merged by the combine). Two kernels:
@@ -155,10 +156,10 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_f32_few_kernel(const __g
                     }
                 }
                 const float score = key0 + skey < lim ? s[0] : -INFINITY;
-                float mx = fmaxf(score, __shfl_xor_sync(0xffffffffu, score, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                if (__any_sync(0xffffffffu, mx > m + kRescale)) {
-                    const float mn = fmaxf(m, mx), a = mn == -INFINITY ? 1.f : exp2f(m - mn);
+                if (__any_sync(0xffffffffu, score > m + kRescale)) {
+                    float mx = fmaxf(score, __shfl_xor_sync(0xffffffffu, score, 1));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                    const float mn = fmaxf(m, mx), a = mn == -INFINITY ? 1.f : tc::ex2(m - mn);
                     m = mn;
                     l *= a;
 #pragma unroll
@@ -168,7 +169,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_f32_few_kernel(const __g
                         for (int e = 0; e < E; ++e) o[r][e] *= ar;
                     }
                 }
-                const float w = exp2f(score - finite_or_0(m));
+                const float w = tc::ex2(score - finite_or_0(m));
                 l += w;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -371,18 +372,18 @@ __global__ void __launch_bounds__(kManyThreads, HD == 64 ? 2 : 1) paged_f32_many
                         for (int j = 0; j < 4; ++j)
                             if (key0 + 16 * j >= lim[i]) w[i][j] = -INFINITY;
                     }
-                    float x = fmaxf(fmaxf(w[i][0], w[i][1]), fmaxf(w[i][2], w[i][3]));
-#pragma unroll
-                    for (int d = 8; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-                    mx[i] = x;
-                    need |= x > m[i] + kRescale;
+                    // the row's maximum over its 16 lanes is needed only when some lane's own exceeds the bound
+                    mx[i] = fmaxf(fmaxf(w[i][0], w[i][1]), fmaxf(w[i][2], w[i][3]));
+                    need |= mx[i] > m[i] + kRescale;
                 }
                 if (__any_sync(0xffffffffu, need)) {
                     float a[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
+#pragma unroll
+                        for (int d = 8; d > 0; d >>= 1) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], d));
                         const float mn = fmaxf(m[i], mx[i]);
-                        a[i] = mn == -INFINITY ? 1.f : exp2f(m[i] - mn);
+                        a[i] = mn == -INFINITY ? 1.f : tc::ex2(m[i] - mn);
                         m[i] = mn;
                         l[i] *= a[i];
                     }
@@ -397,7 +398,7 @@ __global__ void __launch_bounds__(kManyThreads, HD == 64 ? 2 : 1) paged_f32_many
                 for (int i = 0; i < 8; ++i) {
                     const float mb = finite_or_0(m[i]);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) w[i][j] = exp2f(w[i][j] - mb);
+                    for (int j = 0; j < 4; ++j) w[i][j] = tc::ex2(w[i][j] - mb);
                     l[i] += (w[i][0] + w[i][1]) + (w[i][2] + w[i][3]);
                 }
 #pragma unroll
