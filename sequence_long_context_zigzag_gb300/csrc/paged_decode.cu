@@ -8,11 +8,13 @@
 // What bounds it: every K/V row is read once for 2 x rows multiply-adds per element, so HBM is the limit
 // (an SM's share of the copy rate is about 23 bytes per clock). Layout of the work:
 //  - spans of equal key counts per CTA (paged_sched.cuh); two CTAs per SM for 16 rows, one for 32;
-//  - one producer warp walks the span, hands its segments to the others, and streams K and V tiles of 64
-//    keys through a ring of shared-memory stages with TMA: one box of a page per lane, 128-byte swizzle,
+//  - one producer warp walks the span, hands its segments to the others, and streams K and V tiles of 64 or
+//    128 keys through a ring of shared-memory stages with TMA: one box of a page per lane, 128-byte swizzle,
 //    the next tile's page numbers read ahead;
-//  - four consumer warps per 16 rows, each with 16 of the tile's 64 keys and a softmax state of its own:
-//    no synchronisation among them inside a unit. S = Q K^T and O += P V run as m16n8k16 products
+//  - four consumer warps per 16 rows, each with a quarter of the tile's keys and a softmax state of its own:
+//    no synchronisation among them inside a unit. A tile is a chain of about 1000 cycles per warp (products,
+//    maximum, exponentials, products), so a warp takes 32 keys of it, as two interleaved chains, where 16
+//    would not keep HBM busy: rows of 64 elements, or one CTA per SM. S = Q K^T and O += P V run as m16n8k16 products
 //    (mma.sync: at 16 rows a product uses an eighth of a tcgen05 tile, and the rate needed is far below
 //    the legacy pipe's); P goes from S's registers straight into the next product;
 //  - the four states merge through shared memory at a unit's end.
@@ -31,21 +33,22 @@
 namespace usp {
 namespace {
 
-constexpr int kKT = 64;           // keys per tile
 constexpr int kOver = 64;         // a unit's constant cost, in keys
-constexpr int kMinSpan = 192;     // keys per CTA below which fewer CTAs work
+constexpr int kMinSpan = 194;     // keys per CTA below which fewer CTAs work
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr float kRescale = 8.0f;  // log2 units
 constexpr float kLn2 = 0.69314718055994531f;
 
 // RT: row tiles of 16 rows, each with four consumer warps
 template <int HD, int RT> struct Cfg {
+    static constexpr int kW = HD == 128 && RT == 1 ? 1 : 2;  // 16-key steps per warp and tile
+    static constexpr int kKT = 64 * kW;                      // keys per tile
     static constexpr int kConsumers = 4 * RT;
     static constexpr int kThreads = (kConsumers + 1) * 32;
     static constexpr int kBoxes = HD / 64;
     static constexpr int kTile = kKT * HD * 2;  // bytes of K (or V) of one tile
-    // 96 KB in flight per CTA at two CTAs per SM, 160 KB at one
-    static constexpr int kStages = (HD == 128 ? 3 : 6) * (RT == 1 ? 3 : 5) / 3;
+    static constexpr int kStages = RT == 1 ? 3 : HD == 128 ? 3 : 5;  // 96 KB per CTA at two per SM, 160-192 KB at one
+    static_assert(kMinSpan > kOver + kKT, "a span holds more than a tile");
     static constexpr int kXRow = 36;            // exchange row: 32 columns + padding
     static constexpr int kXGroup = 4 * 16 * kXRow * 4;
     static constexpr int kX = kStages * 2 * kTile;
@@ -113,20 +116,20 @@ __device__ void producer(const DecodeParams &p, const SchedShared &sh, uint8_t *
         return (bool)__all_sync(0xffffffffu, r);
     };
     SegMsg *ring = reinterpret_cast<SegMsg *>(smem + C::kSeg);
-    const int ps = 1 << p.log_ps, piece = min(ps, kKT), pieces = kKT / piece;
-    const int nbox = pieces * C::kBoxes * 2;  // at most 16
+    const int ps = 1 << p.log_ps, piece = min(ps, C::kKT), pieces = C::kKT / piece;
+    const int nbox = pieces * C::kBoxes * 2;  // at most 32
     const int kv = lane >= nbox / 2, within = lane - kv * (nbox / 2);
     const int half = within / pieces, pc = within % pieces;
-    const uint32_t dst0 = sbase + kv * C::kTile + half * (kKT * 128) + pc * piece * 128;
+    const uint32_t dst0 = sbase + kv * C::kTile + half * (C::kKT * 128) + pc * piece * 128;
     const void *map = kv ? &p.tv : &p.tk;
     Sched sc;
-    sched_begin<kKT>(p.s, sh, sc);
+    sched_begin<C::kKT>(p.s, sh, sc);
     PartHeader opened{};
     uint32_t fill = 0, nseg = 0;
     bool ok = true, more = true;
     while (more) {
         Segment g;
-        more = sched_next<kKT>(p.s, sc, g);
+        more = sched_next<C::kKT>(p.s, sc, g);
         if (!(ok = wait(C::SEG_EMPTY + nseg % kSegSlots, ((nseg / kSegSlots) & 1u) ^ 1u))) break;
         if (lane == 0) {
             SegMsg m{};
@@ -142,7 +145,7 @@ __device__ void producer(const DecodeParams &p, const SchedShared &sh, uint8_t *
         const int32_t *row = p.table + (int64_t)g.req * p.table_stride;
         // page of this lane's piece of tile t; num_pages (a box of zeros) behind the request's keys
         auto page_of = [&](int t) {
-            const int64_t key = (int64_t)t * kKT + pc * piece;
+            const int64_t key = (int64_t)t * C::kKT + pc * piece;
             if (lane >= nbox || key >= g.kv) return p.num_pages;
             const int32_t x = __ldg(row + (key >> p.log_ps));
             return x >= 0 && x < p.num_pages ? x : p.num_pages;
@@ -156,7 +159,7 @@ __device__ void producer(const DecodeParams &p, const SchedShared &sh, uint8_t *
             __syncwarp();
             if (lane < nbox)
                 tma_load_3d(dst0 + st * 2 * C::kTile, map, half * 64,
-                            g.head * ps + (int)(((int64_t)t * kKT + pc * piece) & (ps - 1)), page, BAR(C::FULL + st));
+                            g.head * ps + (int)(((int64_t)t * C::kKT + pc * piece) & (ps - 1)), page, BAR(C::FULL + st));
             ++fill;
             page = next;
         }
@@ -186,12 +189,12 @@ __device__ void consumer(const DecodeParams &p, uint8_t *smem, uint32_t sbase) {
     float *xch = reinterpret_cast<float *>(smem + C::kX + group * C::kXGroup);
     float2 *ml = reinterpret_cast<float2 *>(smem + C::kML) + group * 64;  // [warp][16]
     const int qr = lane >> 2, qc = (lane & 3) * 2;  // fragment row and column of this lane
-    // ldmatrix addresses inside a tile: 16-byte piece c of key row r lies at (c / 8) * 64 rows + r * 128 +
+    // ldmatrix addresses inside a tile: 16-byte piece c of key row r lies at (c / 8) * kKT * 128 + r * 128 +
     // ((c % 8) ^ (r % 8)) * 16
     const int mi = lane >> 3, mr = lane & 7;
-    const int krow = warp * 16 + (mi >> 1) * 8 + mr, kc0 = mi & 1;
-    const int vrow = warp * 16 + (mi & 1) * 8 + mr, vc0 = mi >> 1;
-    auto piece_at = [](int row, int c) { return (uint32_t)((c >> 3) * (kKT * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)); };
+    const int krow = warp * 16 * C::kW + (mi >> 1) * 8 + mr, kc0 = mi & 1;
+    const int vrow = warp * 16 * C::kW + (mi & 1) * 8 + mr, vc0 = mi >> 1;
+    auto piece_at = [](int row, int c) { return (uint32_t)((c >> 3) * (C::kKT * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)); };
     uint32_t fill = 0;
     for (uint32_t nseg = 0;; ++nseg) {
         // Every warp of the group reaches exactly one group_all per segment, also after a failed wait and
@@ -240,23 +243,25 @@ __device__ void consumer(const DecodeParams &p, uint8_t *smem, uint32_t sbase) {
             const uint32_t st = fill % C::kStages;
             if (!(ok = wait(C::FULL + st, (fill / C::kStages) & 1u))) break;
             const uint32_t sk = sbase + st * 2 * C::kTile, sv = sk + C::kTile;
-            const int key0 = t * kKT + warp * 16;  // this warp's first key
+            const int key0 = t * C::kKT + warp * 16 * C::kW;  // this warp's first key
             if (RT == 1 || rows > 0) {
-                float s[2][4];
+                float s[2 * C::kW][4];
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int n = 0; n < 2 * C::kW; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
 #pragma unroll
-                for (int k = 0; k < kKS; ++k) {
-                    uint32_t b[4];
-                    ldsm4(sk + piece_at(krow, k * 2 + kc0), b);
-                    mma16816(s[0], qf[k], b[0], b[1]);
-                    mma16816(s[1], qf[k], b[2], b[3]);
-                }
-                if (key0 + 16 > lim_all) {
+                for (int k = 0; k < kKS; ++k)
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
+                    for (int w = 0; w < C::kW; ++w) {
+                        uint32_t b[4];
+                        ldsm4(sk + piece_at(krow + w * 16, k * 2 + kc0), b);
+                        mma16816(s[2 * w], qf[k], b[0], b[1]);
+                        mma16816(s[2 * w + 1], qf[k], b[2], b[3]);
+                    }
+                if (key0 + 16 * C::kW > lim_all) {
+#pragma unroll
+                    for (int n = 0; n < 2 * C::kW; ++n)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             if (key0 + n * 8 + qc + (e & 1) >= lim[e >> 1]) s[n][e] = -INFINITY;
@@ -264,8 +269,12 @@ __device__ void consumer(const DecodeParams &p, uint8_t *smem, uint32_t sbase) {
                 // a row's maximum over its four lanes is needed only when some lane's own exceeds the bound
                 float mx[2];
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    mx[h] = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1])) * p.scale_log2;
+                for (int h = 0; h < 2; ++h) {
+                    mx[h] = fmaxf(s[0][2 * h], s[0][2 * h + 1]);
+#pragma unroll
+                    for (int n = 1; n < 2 * C::kW; ++n) mx[h] = tc::max3(mx[h], s[n][2 * h], s[n][2 * h + 1]);
+                    mx[h] *= p.scale_log2;
+                }
                 const bool need = mx[0] > m[0] + kRescale || mx[1] > m[1] + kRescale;
                 if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
@@ -283,35 +292,41 @@ __device__ void consumer(const DecodeParams &p, uint8_t *smem, uint32_t sbase) {
                         }
                     }
                 }
-                uint32_t pf[4];
+                uint32_t pf[C::kW][4], keep[C::kW][2];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float mb = m[h] == -INFINITY ? 0.f : m[h];
-                    float w[4];
-#pragma unroll
-                    for (int n = 0; n < 2; ++n)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) w[2 * n + e] = tc::ex2(fmaf(s[n][2 * h + e], p.scale_log2, -mb));
-                    l[h] += (w[0] + w[1]) + (w[2] + w[3]);
-                    pf[h] = float2_to_bf16x2(w[0], w[1]);
-                    pf[2 + h] = float2_to_bf16x2(w[2], w[3]);
-                }
-                // keys behind the request's last one: cleared in V's fragments (this lane's keys qc, qc+1, +8)
-                uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
-                if (key0 + 16 > g.kv) {
+                for (int w = 0; w < C::kW; ++w) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const int k = key0 + h * 8 + qc;
-                        keep[h] = (k < g.kv ? 0xffffu : 0u) | (k + 1 < g.kv ? 0xffff0000u : 0u);
+                        const float mb = m[h] == -INFINITY ? 0.f : m[h];
+                        float x[4];
+#pragma unroll
+                        for (int n = 0; n < 2; ++n)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                x[2 * n + e] = tc::ex2(fmaf(s[2 * w + n][2 * h + e], p.scale_log2, -mb));
+                        l[h] += (x[0] + x[1]) + (x[2] + x[3]);
+                        pf[w][h] = float2_to_bf16x2(x[0], x[1]);
+                        pf[w][2 + h] = float2_to_bf16x2(x[2], x[3]);
+                    }
+                    // keys behind the request's last one: cleared in V's fragments (this lane's keys qc, qc+1, +8)
+                    keep[w][0] = keep[w][1] = 0xffffffffu;
+                    if (key0 + w * 16 + 16 > g.kv) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int k = key0 + w * 16 + h * 8 + qc;
+                            keep[w][h] = (k < g.kv ? 0xffffu : 0u) | (k + 1 < g.kv ? 0xffff0000u : 0u);
+                        }
                     }
                 }
 #pragma unroll
-                for (int c = 0; c < kNT; c += 2) {
-                    uint32_t b[4];
-                    ldsm4t(sv + piece_at(vrow, c + vc0), b);
-                    mma16816(o[c], pf, b[0] & keep[0], b[1] & keep[1]);
-                    mma16816(o[c + 1], pf, b[2] & keep[0], b[3] & keep[1]);
-                }
+                for (int c = 0; c < kNT; c += 2)
+#pragma unroll
+                    for (int w = 0; w < C::kW; ++w) {
+                        uint32_t b[4];
+                        ldsm4t(sv + piece_at(vrow + w * 16, c + vc0), b);
+                        mma16816(o[c], pf[w], b[0] & keep[w][0], b[1] & keep[w][1]);
+                        mma16816(o[c + 1], pf[w], b[2] & keep[w][0], b[3] & keep[w][1]);
+                    }
             }
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(BAR(C::EMPTY + st));
@@ -545,7 +560,8 @@ int launch_paged_decode(const PagedArgs &a, int rows, int n_hi, bool second, con
     if (!di) return USP_ERR_CUDA;
     DecodeParams p{};
     const int ps = 1 << a.log_ps;
-    const uint32_t box = (uint32_t)std::min(ps, kKT);
+    const uint32_t box = (uint32_t)std::min(ps, a.hd == 128 && rows == 16 ? Cfg<128, 1>::kKT : Cfg<64, 1>::kKT);
+    static_assert(Cfg<64, 1>::kKT == Cfg<64, 2>::kKT && Cfg<64, 1>::kKT == Cfg<128, 2>::kKT, "one box height for these");
     if (!make_cache_tmap(&p.tk, a.k, a.num_pages, a.k_page, a.hkv, ps, a.hd, box) ||
         !make_cache_tmap(&p.tv, a.v, a.num_pages, a.v_page, a.hkv, ps, a.hd, box))
         return USP_ERR_CUDA;
