@@ -627,13 +627,9 @@ def usp_page_plan(ctx_lens, new_lens, free_pages, free_head, block_table, page_s
     def call(raw):
         nreq = d.nreq
         if slot_map is None and cu_new is None and kv_lens is None and counts is None:
-            # one allocation, in four views
-            buf = torch.empty(max_tokens + 2 * nreq + 5, dtype=torch.int32, device=dev)
-            one = (1,)
-            cnt = buf.as_strided((4,), one, 0)
-            slots = buf.as_strided((max_tokens,), one, 4)
-            cu = buf.as_strided((nreq + 1,), one, 4 + max_tokens)
-            kv = buf.as_strided((nreq,), one, 5 + max_tokens + nreq)
+            # one allocation, in four parts
+            cnt, slots, cu, kv = torch.empty(max_tokens + 2 * nreq + 5, dtype=torch.int32, device=dev) \
+                .unsafe_split_with_sizes((4, max_tokens, nreq + 1, nreq))
         else:
             def output(name, t, n):
                 if t is None:
