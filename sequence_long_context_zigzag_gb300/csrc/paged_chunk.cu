@@ -208,13 +208,22 @@ __device__ void producer_role(const ChunkParams &p, const uint8_t *smem, uint32_
     SegMsg g;
     while (ok && (ok = next_segment<HD>(p, smem, bar0, nseg, g)) && g.ntok > 0) {
         if (g.t0 >= g.t1) continue;
-        // Q comes from HBM and its buffer frees late: into L2 meanwhile
+        // Q: the first one at once; later ones when the buffer is free, into L2 meanwhile
         auto q_boxes = [&](auto &&f) {
             for (int i = 0; i < 2; ++i)
                 for (int bx = 0; bx < C::kBoxes; ++bx)
                     f(C::kQ + i * C::kTileBytes + bx * C::kBoxBytes, bx * 64, (int32_t)(g.tok0 + i * p.tq_tokens));
         };
-        if (lane == 0) q_boxes([&](int, int c, int32_t tok) { tma_prefetch_3d(&p.tq, c, g.head * p.s.G, tok); });
+        auto load_q = [&]() {
+            if (lane != 0) return;
+            tc::mbar_arrive_expect_tx(BAR(C::Q_FULL), 2 * C::kBoxes * (uint32_t)(p.tq_tokens * p.s.G) * 128);
+            q_boxes([&](int dst, int c, int32_t tok) {
+                tma_load_3d(sbase + dst, &p.tq, c, g.head * p.s.G, tok, BAR(C::Q_FULL));
+            });
+        };
+        if (nq == 0) load_q();
+        else if (lane == 0) q_boxes([&](int, int c, int32_t tok) { tma_prefetch_3d(&p.tq, c, g.head * p.s.G, tok); });
+        ++nq;
         const int32_t *row = p.table + (int64_t)g.req * p.table_stride;
         // page of this lane's piece of tile t; num_pages (a box of zeros) behind the request's keys
         auto page_of = [&](int t) {
@@ -234,15 +243,9 @@ __device__ void producer_role(const ChunkParams &p, const uint8_t *smem, uint32_
             if (lane < nbox)
                 tma_load_3d(sbase + C::kK + st * C::kTileBytes + in_tile, &p.tk, half * 64, c1, page, BAR(C::K_FULL + st));
             ++kfills;
-            if (t == g.t0) {
-                if (nq > 0 && !(ok = wait(C::Q_EMPTY, (nq - 1) & 1u))) break;
-                if (lane == 0) {
-                    tc::mbar_arrive_expect_tx(BAR(C::Q_FULL), 2 * C::kBoxes * (uint32_t)(p.tq_tokens * p.s.G) * 128);
-                    q_boxes([&](int dst, int c, int32_t tok) {
-                        tma_load_3d(sbase + dst, &p.tq, c, g.head * p.s.G, tok, BAR(C::Q_FULL));
-                    });
-                }
-                ++nq;
+            if (t == g.t0 && nq > 1) {
+                if (!(ok = wait(C::Q_EMPTY, (nq - 2) & 1u))) break;
+                load_q();
             }
             if (!(ok = wait(C::V_EMPTY + st, ph))) break;
             // a tile with rows behind the last key goes to the walk warp first
@@ -258,7 +261,7 @@ __device__ void producer_role(const ChunkParams &p, const uint8_t *smem, uint32_
     }
     if (!ok) {
         // drain (bounded), so that no copy lands after the CTA has gone
-        if (nq > 0) wait(C::Q_FULL, (nq - 1) & 1u);
+        if (nq > 0) wait(C::Q_FULL, (nq - 1) & 1u);  // (a load that was not issued ends by the recorded status)
         for (uint32_t f = kfills > C::kStages ? kfills - C::kStages : 0; f < kfills; ++f)
             wait(C::K_FULL + f % C::kStages, (f / C::kStages) & 1u);
         for (uint32_t f = vfills > C::kStages ? vfills - C::kStages : 0; f < vfills; ++f)
@@ -665,10 +668,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kSlot);
     volatile uint32_t *skip_flag = tmem_slot + 1;
     const int warp = threadIdx.x >> 5;
-    if (!sched_scan<kThreads>(p.s, sh)) {  // the same for every thread
-        if (threadIdx.x == 0) p.w.head[blockIdx.x] = PartHeader{};
-        return;
-    }
     // the next kernels of the call may take their places as SMs come free
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
@@ -704,11 +703,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         tc::tmem_alloc(tc::smem_u32(tmem_slot), 512);
         tc::tmem_relinquish();
     }
+    const bool work = sched_scan<kThreads, kN>(p.s, sh);  // the same for every thread
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    const bool skip = *skip_flag != 0;
+    const bool skip = !work || *skip_flag != 0;
     if (warp >= kSoftmaxWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
         if (!skip) {

@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(Cfg<HD, RT>::kThreads, RT == 1 ? 2 : 1)
         }
         tc::fence_barrier_init();
     }
-    const bool work = sched_scan<C::kThreads>(p.s, sh);
+    const bool work = sched_scan<C::kThreads, C::kKT>(p.s, sh);
     __syncthreads();
     if (!work || skip) {
         if (threadIdx.x == 0) p.w.head[blockIdx.x] = PartHeader{};

@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_f32_few_kernel(const __g
     __shared__ Segment seg;
     __shared__ PartHeader opened;
     if (tid == 0) opened = PartHeader{};
-    if (sched_scan<kFewThreads>(p.s, sh)) {
+    if (sched_scan<kFewThreads, kFewKT>(p.s, sh)) {
         __syncthreads();
         if (tid == 0) sched_begin<kFewKT>(p.s, sh, sc);
         for (;;) {
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(kManyThreads, HD == 64 ? 2 : 1) paged_f32_many
     __shared__ Segment seg;
     __shared__ PartHeader opened;
     if (tid == 0) opened = PartHeader{};
-    if (sched_scan<kManyThreads>(p.s, sh)) {
+    if (sched_scan<kManyThreads, kManyKT>(p.s, sh)) {
         __syncthreads();
         if (tid == 0) sched_begin<kManyKT>(p.s, sh, sc);
         for (;;) {

@@ -68,9 +68,9 @@ struct UnitPos {
 
 struct SchedShared {
     int64_t warp_sum[32];
-    int64_t before[2];  // of the span's first request [0], and of the one after its end [1]
-    ReqUnits r[2];
-    int32_t req[2];
+    UnitPos at, end;  // of this CTA's span
+    ReqUnits r;       // the request of `at`
+    int64_t before;   // cost before that request
     int64_t span;
 };
 
@@ -159,7 +159,7 @@ __device__ __forceinline__ bool sched_step(const SchedIn &s, Sched &o, Segment &
 
 // Called by all NT threads of the CTA: finds the requests in which the CTA's span begins and ends. False
 // when this CTA has no work. `sh` is complete after the caller's next barrier.
-template <int NT>
+template <int NT, int KT>
 __device__ bool sched_scan(const SchedIn &s, SchedShared &sh) {
     static_assert(NT % 32 == 0 && NT <= 1024, "whole warps");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -181,7 +181,7 @@ __device__ bool sched_scan(const SchedIn &s, SchedShared &sh) {
         }
         return x;
     };
-    if (tid < 2) sh.req[tid] = s.nreq;
+    if (tid == 0) sh.end = UnitPos{s.nreq, 0, 0, 0};
     int64_t mine = 0, W;
     ReqUnits r{};
     for (int32_t i = tid; i < s.nreq; i += NT) {
@@ -206,15 +206,13 @@ __device__ bool sched_scan(const SchedIn &s, SchedShared &sh) {
             incl = scan(mine, total);
         }
         const int64_t a = carry + incl - mine;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int64_t x = k ? x1 : x0;
-            if (mine > 0 && a <= x && x < a + mine) {
-                sh.req[k] = base + tid;
-                sh.before[k] = a;
-                sh.r[k] = r;
-            }
+        // the threads of the requests in which the span begins and ends find the places
+        if (mine > 0 && a <= x0 && x0 < a + mine) {
+            sh.at = unit_pos<KT>(s, r, base + tid, x0 - a);
+            sh.before = a;
+            sh.r = r;
         }
+        if (mine > 0 && a <= x1 && x1 < a + mine) sh.end = unit_pos<KT>(s, r, base + tid, x1 - a);
         carry += total;
         if (carry > x1) break;
     }
@@ -225,13 +223,11 @@ __device__ bool sched_scan(const SchedIn &s, SchedShared &sh) {
 // segments.
 template <int KT>
 __device__ __forceinline__ void sched_begin(const SchedIn &s, const SchedShared &sh, Sched &o) {
-    const int32_t i0 = sh.req[0], i1 = sh.req[1];
     o.span = sh.span;
-    o.before = sh.before[0];
-    o.r = sh.r[0];
-    o.at = unit_pos<KT>(s, o.r, i0, blockIdx.x * o.span - o.before);
-    o.end = UnitPos{s.nreq, 0, 0, 0};
-    if (i1 < s.nreq) o.end = unit_pos<KT>(s, sh.r[1], i1, (blockIdx.x + 1) * o.span - sh.before[1]);
+    o.before = sh.before;
+    o.r = sh.r;
+    o.at = sh.at;
+    o.end = sh.end;
     // A span that begins inside a unit takes that unit's rest last, if there is more: so all CTAs sweep
     // the keys from the front at the same time, and those that share a KV head read it from L2 (chunk
     // of 900 tokens over 64000 keys, 152 spans: every span at its own place re-reads 4 GB from HBM).
@@ -323,8 +319,11 @@ inline int launch_overlapped(K kernel, dim3 grid, int threads, int smem, cudaStr
     return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? USP_OK : USP_ERR_CUDA;
 }
 // the end of a kernel that may have been launched early: the grid before has completed when this one has,
-// so that the combine, which waits for this one only, follows both
-__device__ __forceinline__ void follow_grid_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// so that the combine, which waits for this one only, follows both. One CTA waits for that; the others make
+// room on the SMs.
+__device__ __forceinline__ void follow_grid_before() {
+    if (blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
 
 struct CombineArgs {
     PartSpace w[2];  // one per kernel of the call (ctas == 0: not launched)
