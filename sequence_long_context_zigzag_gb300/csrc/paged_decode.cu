@@ -450,83 +450,104 @@ __global__ void __launch_bounds__(Cfg<HD, RT>::kThreads, RT == 1 ? 2 : 1)
 // ------------------------------------------------------------------------------------------------
 // A thread computes 4 columns of a row over all parts of its unit: o = sum_i 2^(m_i - M) o_i / l, online,
 // in the parts' order, so the result does not depend on timing. Bound by latency (the header, then the
-// parts), so the maxima, sums and rows of 8 parts are fetched at once, which is all of them for most
-// units. A part whose rows saw nothing has m = -inf, and its o (perhaps unwritten) is not used. Small CTAs:
-// some fit beside the decode kernel's and are in place when it ends.
+// parts), so a thread fetches the maxima, sums and rows of 8 (row, part) pairs at once: 8 parts of a row in
+// the few-row kernels' units, which long sequences cut into many, 2 parts of 4 rows in the others' (prompts
+// of 16334 tokens: 16 us with a row at a time). A part whose rows saw nothing has m = -inf, and its o
+// (perhaps unwritten) is not used. Small CTAs: some fit beside the decode kernel's and are in place when it
+// ends.
 constexpr int kCombineThreads = 128;
 constexpr int kCombineRows = 16;  // rows per CTA
-constexpr int kBatch = 8;
+
+template <typename T, int HD, int NR, int NP>  // rows and parts fetched at once
+__device__ __forceinline__ void combine_rows(const CombineArgs &a, const PartSpace &w, int c, int r0) {
+    constexpr bool kExact = sizeof(T) == 4;  // log2f for the fp32 path
+    constexpr int kStep = kCombineThreads / (HD / 4);
+    const int col = (int)threadIdx.x % (HD / 4) * 4, row = r0 + (int)threadIdx.x / (HD / 4);
+    const PartHeader h = w.head[c];
+    const int parts = h.last - c + 1, end = min(r0 + kCombineRows, h.rows);
+    const size_t step = 2 * (size_t)w.rows * (HD + 2);  // from a CTA's slot to the next CTA's
+    const float *cont = part_slot(w, HD, c + 1, 0);       // parts 1, 2, ...
+    const float *open = part_slot(w, HD, c, 1);           // part 0
+    for (int first = row; first < end; first += NR * kStep) {
+        float M[NR], L[NR];
+        float4 acc[NR];
+#pragma unroll
+        for (int j = 0; j < NR; ++j) {
+            M[j] = -INFINITY;
+            L[j] = 0.f;
+            acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        for (int base = 0; base < parts; base += NP) {
+            float m[NR][NP], l[NR][NP];
+            float4 o[NR][NP];
+#pragma unroll
+            for (int j = 0; j < NR; ++j)
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+                    const int r = first + j * kStep;
+                    m[j][i] = -INFINITY;
+                    l[j][i] = 0.f;
+                    o[j][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (base + i < parts && r < end) {
+                        const float *s = base + i == 0 ? open : cont + (base + i - 1) * step;
+                        m[j][i] = s[(size_t)w.rows * HD + r];
+                        l[j][i] = s[(size_t)w.rows * (HD + 1) + r];
+                        o[j][i] = *reinterpret_cast<const float4 *>(s + (size_t)r * HD + col);
+                    }
+                }
+#pragma unroll
+            for (int j = 0; j < NR; ++j) {
+                float mx = M[j];
+#pragma unroll
+                for (int i = 0; i < NP; ++i) mx = fmaxf(mx, m[j][i]);
+                const float mb = mx == -INFINITY ? 0.f : mx, g0 = tc::ex2(M[j] - mb);
+                M[j] = mx;
+                L[j] *= g0;
+                acc[j].x *= g0; acc[j].y *= g0; acc[j].z *= g0; acc[j].w *= g0;
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+                    const float g = tc::ex2(m[j][i] - mb);
+                    if (g > 0.f) {
+                        L[j] = fmaf(g, l[j][i], L[j]);
+                        acc[j].x = fmaf(g, o[j][i].x, acc[j].x);
+                        acc[j].y = fmaf(g, o[j][i].y, acc[j].y);
+                        acc[j].z = fmaf(g, o[j][i].z, acc[j].z);
+                        acc[j].w = fmaf(g, o[j][i].w, acc[j].w);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NR; ++j) {
+            const int r = first + j * kStep;
+            if (r >= end) break;
+            const float inv = L[j] > 0.f ? 1.f / L[j] : 0.f;
+            uint32_t tok, hr;
+            a.by_G.divmod((uint32_t)r, tok, hr);
+            const int head = h.head * a.G + (int)hr;
+            T *to = static_cast<T *>(a.out) + (h.tok0 + tok) * a.out_stride + (int64_t)head * HD + col;
+            if constexpr (kExact) {
+                *reinterpret_cast<float4 *>(to) =
+                    make_float4(acc[j].x * inv, acc[j].y * inv, acc[j].z * inv, acc[j].w * inv);
+            } else {
+                *reinterpret_cast<uint2 *>(to) = make_uint2(float2_to_bf16x2(acc[j].x * inv, acc[j].y * inv),
+                                                            float2_to_bf16x2(acc[j].z * inv, acc[j].w * inv));
+            }
+            if (col == 0)
+                a.lse[(h.tok0 + tok) * a.hq + head] =
+                    L[j] > 0.f ? (M[j] + (kExact ? log2f(L[j]) : __log2f(L[j]))) * kLn2 : -INFINITY;
+        }
+    }
+}
 
 template <typename T, int HD>
 __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const CombineArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    constexpr bool kExact = sizeof(T) == 4;  // the fp32 path has no fast functions
-    constexpr int kStep = kCombineThreads / (HD / 4);
-    auto exp2_of = [](float x) { return kExact ? exp2f(x) : tc::ex2(x); };
     const int per0 = (a.w[0].rows + kCombineRows - 1) / kCombineRows;
     const int per1 = (a.w[1].rows + kCombineRows - 1) / kCombineRows;
-    const bool second = (int)blockIdx.x >= a.w[0].ctas * per0;
-    const PartSpace w = second ? a.w[1] : a.w[0];
-    const int x = (int)blockIdx.x - (second ? a.w[0].ctas * per0 : 0), per = second ? per1 : per0;
-    const int c = x / per, r0 = x % per * kCombineRows;
-    const int col = (int)threadIdx.x % (HD / 4) * 4;
-    const PartHeader h = w.head[c];
-    const int parts = h.last - c + 1;
-    const size_t step = 2 * (size_t)w.rows * (HD + 2);  // from a CTA's slot to the next CTA's
-    const float *cont = part_slot(w, HD, c + 1, 0);       // parts 1, 2, ...
-    const float *open = part_slot(w, HD, c, 1);           // part 0
-    for (int r = r0 + (int)threadIdx.x / (HD / 4); r < min(r0 + kCombineRows, h.rows); r += kStep) {
-        const size_t at_m = (size_t)w.rows * HD + r, at_l = at_m + w.rows, at_o = (size_t)r * HD + col;
-        float M = -INFINITY, L = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int base = 0; base < parts; base += kBatch) {
-            float m[kBatch], l[kBatch];
-            float4 o[kBatch];
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                m[i] = -INFINITY;
-                l[i] = 0.f;
-                o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (base + i < parts) {
-                    const float *s = base + i == 0 ? open : cont + (base + i - 1) * step;
-                    m[i] = s[at_m];
-                    l[i] = s[at_l];
-                    o[i] = *reinterpret_cast<const float4 *>(s + at_o);
-                }
-            }
-            float mx = M;
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) mx = fmaxf(mx, m[i]);
-            const float mb = mx == -INFINITY ? 0.f : mx, g0 = exp2_of(M - mb);
-            M = mx;
-            L *= g0;
-            acc.x *= g0; acc.y *= g0; acc.z *= g0; acc.w *= g0;
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const float g = exp2_of(m[i] - mb);
-                if (g > 0.f) {
-                    L = fmaf(g, l[i], L);
-                    acc.x = fmaf(g, o[i].x, acc.x);
-                    acc.y = fmaf(g, o[i].y, acc.y);
-                    acc.z = fmaf(g, o[i].z, acc.z);
-                    acc.w = fmaf(g, o[i].w, acc.w);
-                }
-            }
-        }
-        const float inv = L > 0.f ? 1.f / L : 0.f;
-        uint32_t tok, hr;
-        a.by_G.divmod((uint32_t)r, tok, hr);
-        const int head = h.head * a.G + (int)hr;
-        T *to = static_cast<T *>(a.out) + (h.tok0 + tok) * a.out_stride + (int64_t)head * HD + col;
-        if constexpr (kExact) {
-            *reinterpret_cast<float4 *>(to) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-        } else {
-            *reinterpret_cast<uint2 *>(to) =
-                make_uint2(float2_to_bf16x2(acc.x * inv, acc.y * inv), float2_to_bf16x2(acc.z * inv, acc.w * inv));
-        }
-        if (col == 0)
-            a.lse[(h.tok0 + tok) * a.hq + head] = L > 0.f ? (M + (kExact ? log2f(L) : __log2f(L))) * kLn2 : -INFINITY;
-    }
+    const int x = (int)blockIdx.x - a.w[0].ctas * per0;
+    if (x < 0) combine_rows<T, HD, 4, 2>(a, a.w[0], (int)blockIdx.x / per0, (int)blockIdx.x % per0 * kCombineRows);
+    else combine_rows<T, HD, 1, 8>(a, a.w[1], x / per1, x % per1 * kCombineRows);
 }
 
 template <int HD, int RT>
