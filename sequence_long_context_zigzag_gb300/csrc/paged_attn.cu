@@ -64,7 +64,7 @@ Route route(const usp_paged_desc &d, int sms) {
     const int64_t rows = G * (int64_t)std::max(1, d.max_new);
     r.split = INT_MAX;
     if (rows > most || G > (bf16 ? 32 : f32_rows(false))) {
-        r.many_ctas = bf16 ? sms : f32_ctas(sms, true, d.cache.hd);
+        r.many_ctas = bf16 ? sms : f32_ctas(sms, true);
         r.many_rows = bf16 ? kChunkRows : f32_rows(true);
         // beside chunks, the few-row requests are mostly single tokens: the 16-row kernel (two CTAs per SM)
         // takes those, the other one all chunks (33 requests, 26 of one token: 49 -> 40 us)
@@ -72,7 +72,7 @@ Route route(const usp_paged_desc &d, int sms) {
     }
     if (r.split > 0) {
         r.few_rows = bf16 ? (std::min<int64_t>(rows, (int64_t)r.split * G) <= 16 ? 16 : 32) : f32_rows(false);
-        r.few_ctas = bf16 ? decode_ctas(sms, r.few_rows) : f32_ctas(sms, false, d.cache.hd);
+        r.few_ctas = bf16 ? decode_ctas(sms, r.few_rows) : f32_ctas(sms, false);
     }
     return r;
 }

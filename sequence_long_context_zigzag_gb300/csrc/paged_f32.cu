@@ -11,10 +11,9 @@
 //   score per lane (row lane / 4, key lane % 4): 31 shuffles for 32 sums.
 // many rows (paged_f32_many_kernel, units of up to 128 query rows): bound by the fp32 pipes
 //   (128 lanes per SM). 256 threads compute 128 x 64 scores, 8 x 4 each, and 128 x hd outputs, 8 x hd / 16
-//   each, from shared memory: Q and P lie transposed (the summed index is the slow one), K and V as they
-//   come, so a thread reads its 8 rows, and 4 elements of each of its 4 keys, as 16-byte words and gets 128
-//   multiply-adds from twelve of them. Products run two rows at a time (packed fp32 pairs: half the issue
-//   slots). K and V come by asynchronous copies: V during a tile's scores, the next K during its outputs,
+//   each, from shared memory, with packed fp32 pairs (half the issue slots): a score's pair sums its even and
+//   its odd elements, so that Q's and K's rows serve as they are, 12 16-byte words for 64 pair products; an
+//   output's pair is two rows, from P written transposed. K and V come by asynchronous copies: V during a tile's scores, the next K during its outputs,
 //   so the copies hold no registers (with register prefetch the loop had none left to run its loads ahead).
 #include <math.h>
 
@@ -232,13 +231,13 @@ constexpr int kManyKT = 64;
 constexpr int kManyOver = 64, kManyMinSpan = 256;
 
 template <int HD> struct Many {
-    static constexpr int kQRow = kManyRows + 4;  // floats per row of the transposed Q and P
-    static constexpr int kKRow = HD + 4;         // of K: 16 keys' pieces of a column then lie on all banks
-    static constexpr int kQ = 0;                        // [HD][kQRow]
-    static constexpr int kK = kQ + HD * kQRow;          // [kManyKT][kKRow]
-    static constexpr int kV = kK + kManyKT * kKRow;     // [kManyKT][HD]
-    static constexpr int kP = kV + kManyKT * HD;        // [kManyKT][kQRow]
-    static constexpr int kFloats = kP + kManyKT * kQRow;
+    static constexpr int kRow = HD + 4;          // floats per row of Q and K: 16 keys' pieces then lie on all banks
+    static constexpr int kPRow = kManyRows + 4;  // of the transposed P
+    static constexpr int kQ = 0;                       // [kManyRows][kRow]
+    static constexpr int kK = kQ + kManyRows * kRow;   // [kManyKT][kRow]
+    static constexpr int kV = kK + kManyKT * kRow;     // [kManyKT][HD]
+    static constexpr int kP = kV + kManyKT * HD;       // [kManyKT][kPRow]
+    static constexpr int kFloats = kP + kManyKT * kPRow;
 };
 
 // 16 bytes global -> shared; zeros when !ok (src is not read then)
@@ -254,14 +253,14 @@ __device__ __forceinline__ void load_pairs(const float *p, uint64_t (&x)[4]) {  
 }
 
 template <int HD>
-__global__ void __launch_bounds__(kManyThreads, HD == 64 ? 2 : 1) paged_f32_many_kernel(const __grid_constant__ F32Params p) {
+__global__ void __launch_bounds__(kManyThreads, 1) paged_f32_many_kernel(const __grid_constant__ F32Params p) {
     using C = Many<HD>;
     constexpr int kCols = HD / 64;             // groups of 4 output columns per thread
     constexpr int kLd = kManyKT * HD / 4 / kManyThreads;  // 16-byte copies of K (and V) per thread
     extern __shared__ __align__(16) float sm[];
     __shared__ SchedShared sh;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    float *qt = sm + C::kQ, *ks = sm + C::kK, *vs = sm + C::kV, *pt = sm + C::kP;
+    float *qs = sm + C::kQ, *ks = sm + C::kK, *vs = sm + C::kV, *pt = sm + C::kP;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     // thread 0 walks the span; its state stays in shared memory, out of the products' registers
     __shared__ Sched sc;
@@ -281,9 +280,8 @@ __global__ void __launch_bounds__(kManyThreads, HD == 64 ? 2 : 1) paged_f32_many
             if (g.ntok == 0) break;
             const int rows = g.ntok * p.s.G;
             __syncthreads();  // the previous unit's products are done
-            // Q scaled and transposed; lanes along the rows, so that the writes are free of conflicts
             for (int x = tid; x < kManyRows * (HD / 4); x += kManyThreads) {
-                const int r = x % kManyRows, c = x / kManyRows * 4;
+                const int r = x / (HD / 4), c = x % (HD / 4) * 4;
                 float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (r < rows) {
                     uint32_t tok, h;
@@ -291,10 +289,8 @@ __global__ void __launch_bounds__(kManyThreads, HD == 64 ? 2 : 1) paged_f32_many
                     f = __ldg(reinterpret_cast<const float4 *>(p.q + (g.tok0 + tok) * p.q_stride +
                                                                (int64_t)(g.head * p.s.G + (int)h) * HD + c));
                 }
-                qt[c * C::kQRow + r] = f.x * p.scale_log2;
-                qt[(c + 1) * C::kQRow + r] = f.y * p.scale_log2;
-                qt[(c + 2) * C::kQRow + r] = f.z * p.scale_log2;
-                qt[(c + 3) * C::kQRow + r] = f.w * p.scale_log2;
+                *reinterpret_cast<float4 *>(qs + r * C::kRow + c) =
+                    make_float4(f.x * p.scale_log2, f.y * p.scale_log2, f.z * p.scale_log2, f.w * p.scale_log2);
             }
             const int32_t *row = p.table + (int64_t)g.req * p.table_stride;
             const int ps = 1 << p.log_ps;
@@ -328,41 +324,42 @@ __global__ void __launch_bounds__(kManyThreads, HD == 64 ? 2 : 1) paged_f32_many
 #pragma unroll
                 for (int c = 0; c < 4 * kCols; ++c) o[i][c] = 0;
             const int lim_all = p.s.causal ? max(0, min(g.kv, g.p0 + 1)) : g.kv;
-            if (g.t0 < g.t1) fetch(g.t0, p.k, p.k_page, ks, C::kKRow);
+            if (g.t0 < g.t1) fetch(g.t0, p.k, p.k_page, ks, C::kRow);
             for (int t = g.t0; t < g.t1; ++t) {
                 copies_wait_all();  // K of this tile
                 __syncthreads();    // everyone's; and the previous tile's outputs are done with V
                 fetch(t, p.v, p.v_page, vs, HD);
-                uint64_t s[4][4];  // [row pair][key]
+                uint64_t s[8][4];  // [row][key]: the sums over even and over odd elements
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 8; ++i)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) s[i][j] = 0;
 #pragma unroll 2
                 for (int d = 0; d < HD; d += 4) {
-                    float k4[4][4];
+                    ulonglong2 k2[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        *reinterpret_cast<float4 *>(k4[j]) = *reinterpret_cast<const float4 *>(ks + (tx + 16 * j) * C::kKRow + d);
+                        k2[j] = *reinterpret_cast<const ulonglong2 *>(ks + (tx + 16 * j) * C::kRow + d);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint64_t q2[4];
-                        load_pairs(qt + (d + e) * C::kQRow + ty * 8, q2);
+                    for (int i = 0; i < 8; ++i) {
+                        const ulonglong2 q2 = *reinterpret_cast<const ulonglong2 *>(qs + (ty * 8 + i) * C::kRow + d);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint64_t kk = tc::pack2(k4[j][e], k4[j][e]);
+                        for (int j = 0; j < 4; ++j) s[i][j] = tc::fma2(q2.x, k2[j].x, s[i][j]);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) s[i][j] = tc::fma2(q2[i], kk, s[i][j]);
-                        }
+                        for (int j = 0; j < 4; ++j) s[i][j] = tc::fma2(q2.y, k2[j].y, s[i][j]);
                     }
                 }
                 const int key0 = t * kManyKT + tx;  // this thread's keys: key0 + 16 j
                 const bool edge = (t + 1) * kManyKT > lim_all;
                 float w[8][4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 8; ++i)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) tc::unpack2(s[i][j], w[2 * i][j], w[2 * i + 1][j]);
+                    for (int j = 0; j < 4; ++j) {
+                        float even, odd;
+                        tc::unpack2(s[i][j], even, odd);
+                        w[i][j] = even + odd;
+                    }
                 float mx[8];
                 bool need = false;
 #pragma unroll
@@ -403,17 +400,17 @@ __global__ void __launch_bounds__(kManyThreads, HD == 64 ? 2 : 1) paged_f32_many
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    float4 *d = reinterpret_cast<float4 *>(pt + (tx + 16 * j) * C::kQRow + ty * 8);
+                    float4 *d = reinterpret_cast<float4 *>(pt + (tx + 16 * j) * C::kPRow + ty * 8);
                     d[0] = make_float4(w[0][j], w[1][j], w[2][j], w[3][j]);
                     d[1] = make_float4(w[4][j], w[5][j], w[6][j], w[7][j]);
                 }
                 copies_wait_all();  // V
                 __syncthreads();    // everyone's; and all are done with K
-                if (t + 1 < g.t1) fetch(t + 1, p.k, p.k_page, ks, C::kKRow);
+                if (t + 1 < g.t1) fetch(t + 1, p.k, p.k_page, ks, C::kRow);
 #pragma unroll 4
                 for (int d = 0; d < kManyKT; ++d) {
                     uint64_t p2[4];
-                    load_pairs(pt + d * C::kQRow + ty * 8, p2);
+                    load_pairs(pt + d * C::kPRow + ty * 8, p2);
 #pragma unroll
                     for (int c = 0; c < kCols; ++c) {
                         const float4 v4 = *reinterpret_cast<const float4 *>(vs + d * HD + c * 64 + tx * 4);
@@ -488,7 +485,9 @@ int launch_many(const F32Params &p, int grid, cudaStream_t s) {
 
 }  // namespace
 
-int f32_ctas(int sms, bool many, int hd) { return many && hd == 128 ? sms : 2 * sms; }
+// one CTA per SM for many rows also at hd 64, where two fit: with half the registers the products' operands
+// spill (2048 tokens over 8192: 1196 us against 824)
+int f32_ctas(int sms, bool many) { return many ? sms : 2 * sms; }
 int f32_rows(bool many) { return many ? kManyRows : kFewRows; }
 
 int launch_paged_f32(const PagedArgs &a, bool many, int n_lo, int n_hi, bool second, const PartSpace &w,

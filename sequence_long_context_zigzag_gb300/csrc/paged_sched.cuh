@@ -347,7 +347,7 @@ int launch_paged_chunk(const PagedArgs &a, int n_lo, const PartSpace &w, cudaStr
 // fp32: units of few (8) or many (128) query rows; requests with n_lo < new tokens <= n_hi
 int launch_paged_f32(const PagedArgs &a, bool many, int n_lo, int n_hi, bool second, const PartSpace &w,
                      cudaStream_t s);
-int f32_ctas(int sms, bool many, int hd);
+int f32_ctas(int sms, bool many);
 int f32_rows(bool many);
 
 }  // namespace usp
