@@ -462,7 +462,8 @@ typedef struct {
  * [cu_new[0], cu_new[nreq]) are left as they were. Cache rows behind kv_i may hold anything (NaN
  * among it); rows a request has must be finite where some query of the call sees them: in the bf16
  * kernels a non-finite V row reaches every query of its 128-key tile. Partials over parts of
- * a sequence (e.g. one ring rank's keys each) merge with usp_lse_merge.
+ * a sequence (e.g. one ring rank's keys each) merge with usp_lse_merge. Requests may share pages. out and
+ * lse must not overlap each other or the inputs.
  *   workspace : DEVICE buffer, 256-byte aligned, at least usp_paged_attn_workspace_size(d) bytes,
  *               clobbered; calls that share it must be ordered on one stream (two captured graphs
  *               that may run at the same time need one each). It needs no initialisation.

@@ -590,7 +590,7 @@ def _with_stream(index: int, stream, call):
         with torch.cuda.device(index):
             return call(_raw_stream(index))
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=index)
+        stream = torch.cuda.ExternalStream(int(stream), device=index) if stream else torch.cuda.default_stream(index)
     _need(stream.device.index == index, "the stream belongs to another device than the tensors")
     with torch.cuda.stream(stream):
         return call(stream.cuda_stream)

@@ -20,6 +20,12 @@ struct PagedArgs {
     float scale_log2;  // softmax scale * log2(e)
 };
 
+// Keys a request can have: what the table holds, and 32-bit key tile arithmetic with room for a tile.
+inline int64_t paged_max_keys(const PagedArgs &a) {
+    const int64_t held = (int64_t)a.max_pages << a.log_ps, most = (int64_t(1) << 31) - 1024;
+    return held < most ? held : most;
+}
+
 // The new tokens [t0, t0 + n) and keys of request i, clamped to what the tensors and the table hold.
 struct Request {
     int64_t t0;

@@ -587,7 +587,7 @@ int launch_paged_decode(const PagedArgs &a, int rows, int n_hi, bool second, con
         !make_cache_tmap(&p.tv, a.v, a.num_pages, a.v_page, a.hkv, ps, a.hd, box))
         return USP_ERR_CUDA;
     p.s.cu = a.cu; p.s.kv = a.kv;
-    p.s.tokens = a.tokens; p.s.max_keys = (int64_t)a.max_pages << a.log_ps;
+    p.s.tokens = a.tokens; p.s.max_keys = paged_max_keys(a);
     p.s.nreq = a.nreq; p.s.hkv = a.hkv; p.s.G = a.G;
     p.s.tb = rows / a.G; p.s.causal = a.causal;
     p.s.n_lo = 0; p.s.n_hi = n_hi;

@@ -494,7 +494,7 @@ int launch_paged_f32(const PagedArgs &a, bool many, int n_lo, int n_hi, bool sec
                      cudaStream_t s) {
     F32Params p{};
     p.s.cu = a.cu; p.s.kv = a.kv;
-    p.s.tokens = a.tokens; p.s.max_keys = (int64_t)a.max_pages << a.log_ps;
+    p.s.tokens = a.tokens; p.s.max_keys = paged_max_keys(a);
     p.s.nreq = a.nreq; p.s.hkv = a.hkv; p.s.G = a.G;
     p.s.tb = f32_rows(many) / a.G; p.s.causal = a.causal;
     p.s.n_lo = n_lo; p.s.n_hi = n_hi;

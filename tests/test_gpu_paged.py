@@ -320,3 +320,134 @@ def test_parts_of_a_sequence_merge():
     assert ((o.double() - ref).abs() <= 3 * bo + 2.0 ** -20 * ref.abs()).all()
     assert ((z.double() - lref).abs() <= 3 * bl + 2.0 ** -20).all()
     assert math.isfinite(z.sum().item())
+
+
+# ---- at the edges of what the calls allow ----------------------------------------------------------
+def test_attention_fewer_tokens_than_a_tile_of_queries():
+    """One short chunk alone: the query tile's box is taller than q."""
+    for new, hq, hkv, hd in ((9, 8, 2, 128), (17, 2, 2, 64), (33, 1, 1, 128), (3, 64, 2, 64)):
+        c = Cache([(new + 60, new)], hq, hkv, hd, 16, torch.bfloat16, seed=new)
+        out, lse = attend(c, max_new=new)
+        check_attention(c, out, lse)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_attention_shared_pages(dt):
+    """Requests that begin with the same pages (a shared prompt) and go on in their own."""
+    c = Cache([(300, 1), (290, 40), (256, 1)], 8, 2, 64, 64, dt, seed=21)
+    for i in (1, 2):
+        c.table[i, :4] = c.table[0, :4]
+        c.k[i][:256], c.v[i][:256] = c.k[0][:256], c.v[0][:256]
+    out, lse = attend(c)
+    check_attention(c, out, lse)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("new", [1, 70])
+def test_offsets_past_32_bits(dt, new):
+    """A cache of more than 2^31 elements (and 2^32 bytes): append to and attend over its last pages."""
+    hkv, ps, hd, num = 8, 256, 128, 8300
+    kc, vc = (torch.empty(num, hkv, ps, hd, dtype=dt, device="cuda") for _ in range(2))
+    assert kc.numel() > 2 ** 31
+    c = Cache([(600, new), (256, new)], 16, hkv, hd, ps, dt, seed=22)
+    pages = [[num - 1, num - 5, num - 3], [num - 2]]
+    c.table = i32([pages[0], pages[1] + [-1, -1]])
+    keys = torch.cat(c.k).cuda(), torch.cat(c.v).cuda()
+    slots = i32([pages[i][p // ps] * ps + p % ps for i, (n, _) in enumerate(c.reqs) for p in range(n)])
+    usp.usp_cache_append(*keys, kc, vc, slots)
+    c.k_cache, c.v_cache = kc, vc
+    out, lse = attend(c)
+    check_attention(c, out, lse)
+
+
+def test_two_calls_at_once_with_their_own_workspaces():
+    cs = [Cache([(3000 + 100 * i, 1), (700, 90)], 8, 2, 128, 16, torch.bfloat16, seed=30 + i) for i in range(2)]
+    alone = [[x.clone() for x in attend(c)] for c in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = [usp.usp_paged_attn(*c.args(), stream=s) for c, s in zip(cs, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(alone, got):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_whole_step_in_one_graph():
+    """Plan, append and attention captured together and replayed for other lengths, with -1 slots behind
+    the last token."""
+    hq, hkv, hd, ps, num, cap = 8, 2, 64, 16, 80, 64
+    g = torch.Generator().manual_seed(40)
+    c = Cache([(0, 0), (0, 0)], hq, hkv, hd, ps, torch.bfloat16)
+    kc, vc = (torch.full((num, hkv, ps, hd), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    table, free = torch.full((2, 30), -1, dtype=torch.int32, device="cuda"), torch.arange(num, dtype=torch.int32, device="cuda")
+    ctx, new, head = i32([0, 0]), i32([0, 0]), i32([0])
+    q, k, v = (torch.zeros(cap, h, hd, dtype=torch.bfloat16, device="cuda") for h in (hq, hkv, hkv))
+
+    def step():
+        slots, cu, kv, counts = usp.usp_page_plan(ctx, new, free, head, table, ps, num, cap)
+        usp.usp_cache_append(k, v, kc, vc, slots)
+        return (*usp.usp_paged_attn(q, kc, vc, table, cu, kv), kv, counts)
+    step()
+    usp.usp_check()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse, kv, counts = step()
+    c.k, c.v, c.q = [torch.empty(0, hkv, hd, dtype=torch.bfloat16)] * 2, [torch.empty(0, hkv, hd, dtype=torch.bfloat16)] * 2, q
+    for lens in ([40, 13], [1, 1], [0, 50], [30, 0]):
+        T = sum(lens)
+        for t in (q, k, v):
+            t.copy_(torch.randn(t.shape, generator=g).to(t.dtype))
+        new.copy_(i32(lens))
+        graph.replay()
+        torch.cuda.synchronize()
+        at = 0
+        for i, n in enumerate(lens):
+            c.k[i], c.v[i] = torch.cat([c.k[i], k[at:at + n].cpu()]), torch.cat([c.v[i], v[at:at + n].cpu()])
+            at += n
+        c.reqs, c.T = [(len(c.k[i]), lens[i]) for i in range(2)], T
+        c.q = q[:T]
+        check_attention(c, out[:T], lse[:T])
+        assert counts.tolist()[0] == T and counts.tolist()[2] == 0
+        ctx.copy_(kv)
+        head.copy_(counts[1:2])
+
+
+def test_no_work_after_a_recorded_timeout_until_it_is_checked():
+    from sequence_long_context_zigzag_gb300 import _abi
+    c = Cache([(500, 1), (300, 80)], 8, 2, 128, 16, torch.bfloat16, seed=50)
+    _abi.check("usp_selftest_timeout", _abi.load().usp_selftest_timeout(1000, torch.cuda.current_stream().cuda_stream))
+    with pytest.raises(usp.UspError) as e:
+        attend(c)
+    assert e.value.status == _abi.USP_ERR_TIMEOUT
+    out, lse = attend(c)
+    check_attention(c, out, lse)
+
+
+def test_binding_refuses_on_the_gpu():
+    c = Cache([(50, 2), (20, 1)], 4, 2, 64, 16, torch.bfloat16)
+    q, kc, vc, table, cu, kv = c.args()
+    for bad in (dict(lse=torch.empty(3, 5, device="cuda")), dict(out=torch.empty(3, 4, 128, device="cuda")),
+                dict(workspace=torch.empty(10, dtype=torch.uint8)), dict(lse=torch.empty(c.T, 4))):
+        with pytest.raises(ValueError):
+            usp.usp_paged_attn(*c.args(), **bad)
+    with pytest.raises(ValueError, match="one device"):
+        usp.usp_paged_attn(q, kc, vc, table.cpu(), cu, kv)
+    with pytest.raises(usp.UspError):
+        usp.usp_paged_attn(*c.args(), max_new=-1)
+    with pytest.raises(usp.UspError):
+        usp.usp_paged_attn(*c.args(), workspace=torch.empty(1024, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(usp.UspError):   # pages of 8 tokens
+        usp.usp_paged_attn(q, kc[:, :, :8].contiguous(), vc[:, :, :8].contiguous(), table, cu, kv)
+    with pytest.raises(ValueError):
+        usp.usp_cache_append(q[:, :2], q[:, :2], kc, vc, i32([0]))
+    n = usp.usp_paged_attn_workspace_size(q, kc, table, 2)
+    out, lse = usp.usp_paged_attn(*c.args(), max_new=2, workspace=torch.empty(n, dtype=torch.uint8, device="cuda"), stream=0)
+    usp.usp_check()
+    check_attention(c, out, lse)
+    # no request, no token
+    o, z = usp.usp_paged_attn(q, kc, vc, table[:0], cu[:1], kv[:0], out=torch.full_like(q.contiguous(), 3.0))
+    usp.usp_check()
+    assert (o == 3).all()
+    usp.usp_paged_attn(q[:0], kc, vc, table, cu * 0, kv)
+    usp.usp_check()
