@@ -1,7 +1,8 @@
 """USP-Attention forward (zigzag Ulysses x Ring) on one GB300, over a virtual rank grid.
 
 Thin Python binding of the C ABI in include/usp.h: functions with the ABI's names take torch CUDA
-tensors, check their shapes, and pass raw device pointers and the current CUDA stream to libusp.so.
+tensors, check their shapes, and pass raw device pointers and the current CUDA stream to libusp.so
+(through ctypes; the paged cache's calls through a small C++ module).
 Every step of the path runs in the library's CUDA kernels; torch only allocates memory and supplies
 streams. There is no CPU fallback: if libusp.so cannot be loaded, every call raises.
 
@@ -21,8 +22,8 @@ from typing import Optional
 import torch
 
 from . import _abi
-from ._abi import (USP_BF16, USP_F32, USP_MODE_ACCUM, USP_MODE_FUSED, USP_MODE_STEP, UspAttnDesc, UspCacheDims,
-                   UspDims, UspError, UspPagedDesc, UspPlanDims)
+from ._abi import (USP_BF16, USP_F32, USP_MODE_ACCUM, USP_MODE_FUSED, USP_MODE_STEP, UspAttnDesc, UspDims,
+                   UspError)
 
 __all__ = ["usp_extract_local", "usp_a2a4d", "usp_a2a4d_multi", "usp_extract_a2a", "usp_attn_fwd", "usp_lse_merge", "usp_check", "usp_attention",
            "usp_attention_host", "usp_forward", "usp_forward_host", "usp_forward_workspace_size",
@@ -519,81 +520,26 @@ class UspAttention:
 
 
 # ---- paged K/V cache ---------------------------------------------------------------------------
-# Serving calls these once per layer and token, where a short call's GPU work is a few microseconds: the
-# checks of an argument layout (shapes, strides, dtypes, devices: nothing of its data) run once, and the
-# descriptor they end in is kept for the next call with the same layout.
-_layouts: dict = {}
-_MAX_LAYOUTS = 4096
+# Checks, allocations and the stream of these calls are in csrc/binding.cpp.
 
 
-def _keep(key, value):
-    if len(_layouts) >= _MAX_LAYOUTS:
-        _layouts.clear()
-    _layouts[key] = value
-    return value
-
-
-def _same_device(first: torch.Tensor, *ts):
-    dev = first.device
-    if dev.type != "cuda":
-        raise ValueError("expected CUDA tensors")
-    for t in ts:
-        if t.device != dev:
-            raise ValueError(f"expected tensors on one device, got {dev} and {t.device}")
-    return dev
-
-
-def _i32(name: str, t: torch.Tensor, n: Optional[int] = None):
-    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous 1-D int32 tensor")
-    if n is not None and t.numel() != n:
-        raise ValueError(f"{name} must have {n} entries, got {t.numel()}")
-
-
-def _dense_rows(name: str, t: torch.Tensor) -> int:
-    """The stride of the first axis in elements, 0 where the tensor is contiguous; what an entry of the
-    first axis holds must be contiguous."""
-    if t.is_contiguous():
-        return 0
-    if t.dim() < 2 or not t[0].is_contiguous() or t.stride(0) < t[0].numel():
-        raise ValueError(f"{name}: only the first axis may be strided")
-    return t.stride(0)
-
-
-def _cache_dims(k_cache: torch.Tensor, v_cache: torch.Tensor) -> UspCacheDims:
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
-        raise ValueError("k_cache and v_cache must be (num_pages, hkv, page_size, hd), of one shape and dtype")
-    pages, hkv, ps, hd = k_cache.shape
-    return UspCacheDims(pages, _dense_rows("k_cache", k_cache), _dense_rows("v_cache", v_cache), ps, hkv, hd,
-                        _dtype_code(k_cache))
-
-
-def _block_table(t: torch.Tensor, nreq: int) -> int:
-    """The table's row stride; its rows must be contiguous."""
-    if t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] != nreq:
-        raise ValueError(f"block_table must be an int32 tensor of {nreq} rows")
-    return _dense_rows("block_table", t) or t.shape[1]
-
-
-# the raw handle of a device's current stream, without the Stream object where torch has the call
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
-_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-
-
-def _with_stream(index: int, stream, call):
-    """call(raw stream) with the tensors' device current and, where ``stream`` is given, with it as the
-    current stream, so that what the call allocates is ordered on the stream that uses it."""
+def _on_stream(fn: str, t, stream, call, *args):
+    """The binding's ``call`` with ``stream`` current where it is given, so that what the call allocates is
+    ordered on the stream that uses it."""
     if stream is None:
-        if _current_device() == index:
-            return call(_raw_stream(index))
-        with torch.cuda.device(index):
-            return call(_raw_stream(index))
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=index) if stream else torch.cuda.default_stream(index)
-    _need(stream.device.index == index, "the stream belongs to another device than the tensors")
-    with torch.cuda.stream(stream):
-        return call(stream.cuda_stream)
+        r = call(*args)
+    else:
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError("expected CUDA tensors")
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=t.device) if stream else \
+                torch.cuda.default_stream(t.device)
+        _need(stream.device == t.device, "the stream belongs to another device than the tensors")
+        with torch.cuda.stream(stream):
+            r = call(*args)
+    if r.__class__ is int:
+        _abi.check(fn, r)
+    return r
 
 
 def usp_page_plan(ctx_lens, new_lens, free_pages, free_head, block_table, page_size: int, num_pages: int,
@@ -606,88 +552,21 @@ def usp_page_plan(ctx_lens, new_lens, free_pages, free_head, block_table, page_s
     ``max_tokens`` new tokens (-1: none), cumulative new lengths, keys per request, and (new tokens, the
     next free head, tokens left without a slot, largest kv length). The next step passes kv_lens as
     ctx_lens and counts[1:2] as free_head, with other output tensors than its inputs."""
-    key = (ctx_lens.shape, ctx_lens.stride(), ctx_lens.dtype, ctx_lens.device, new_lens.shape, new_lens.stride(),
-           new_lens.dtype, new_lens.device, free_pages.shape, free_pages.stride(), free_pages.dtype, free_pages.device,
-           free_head.shape, free_head.stride(), free_head.dtype, free_head.device, block_table.shape,
-           block_table.stride(), block_table.dtype, block_table.device, page_size, num_pages, max_tokens)
-    d = _layouts.get(key)
-    if d is None:
-        nreq = ctx_lens.numel()
-        for name, t in (("ctx_lens", ctx_lens), ("new_lens", new_lens)):
-            _i32(name, t, nreq)
-        _i32("free_pages", free_pages)
-        _i32("free_head", free_head, 1)
-        _need(max_tokens >= 0, "max_tokens must not be negative")
-        stride = _block_table(block_table, nreq)
-        _same_device(ctx_lens, new_lens, free_pages, free_head, block_table)
-        d = _keep(key, UspPlanDims(num_pages, stride, free_pages.numel(), max_tokens, nreq, block_table.shape[1],
-                                   page_size))
-    dev = ctx_lens.device
-
-    def call(raw):
-        nreq = d.nreq
-        if slot_map is None and cu_new is None and kv_lens is None and counts is None:
-            # one allocation, in four parts
-            cnt, slots, cu, kv = torch.empty(max_tokens + 2 * nreq + 5, dtype=torch.int32, device=dev) \
-                .unsafe_split_with_sizes((4, max_tokens, nreq + 1, nreq))
-        else:
-            def output(name, t, n):
-                if t is None:
-                    return torch.empty(n, dtype=torch.int32, device=dev)
-                _i32(name, t, n)
-                _same_device(ctx_lens, t)
-                return t
-            slots, cu = output("slot_map", slot_map, max_tokens), output("cu_new", cu_new, nreq + 1)
-            kv, cnt = output("kv_lens", kv_lens, nreq), output("counts", counts, 4)
-        rc = _abi.load().usp_page_plan(
-            ctx_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), free_head.data_ptr(),
-            block_table.data_ptr(), slots.data_ptr(), cu.data_ptr(), kv.data_ptr(), cnt.data_ptr(), d, raw)
-        if rc:
-            _abi.check("usp_page_plan", rc)
-        return slots, cu, kv, cnt
-
-    return _with_stream(dev.index, stream, call)
+    return _on_stream("usp_page_plan", ctx_lens, stream, _abi.binding().page_plan, ctx_lens, new_lens, free_pages,
+                      free_head, block_table, page_size, num_pages, max_tokens, slot_map, cu_new, kv_lens, counts)
 
 
 def usp_cache_append(k, v, k_cache, v_cache, slot_map, stream=None):
     """Write the rows of k and v (tokens, hkv, hd) into their slots of the caches
     (num_pages, hkv, page_size, hd), in place; a token with slot -1 is skipped. The first axis of every
     tensor may be strided (slices of a fused projection, a cache that interleaves K and V)."""
-    key = (k.shape, k.stride(), k.dtype, k.device, v.shape, v.stride(), v.dtype, v.device, k_cache.shape,
-           k_cache.stride(), k_cache.dtype, k_cache.device, v_cache.shape, v_cache.stride(), v_cache.dtype,
-           v_cache.device, slot_map.shape, slot_map.stride(), slot_map.dtype, slot_map.device)
-    spec = _layouts.get(key)
-    if spec is None:
-        d = _cache_dims(k_cache, v_cache)
-        if k.dim() != 3 or k.shape[1] != d.hkv or k.shape[2] != d.hd or v.shape != k.shape:
-            raise ValueError("k and v must be (tokens, hkv, hd) like the cache")
-        if k.dtype != k_cache.dtype or v.dtype != k_cache.dtype:
-            raise ValueError("dtype mismatch")
-        _i32("slot_map", slot_map, k.shape[0])
-        strides = _dense_rows("k", k), _dense_rows("v", v)
-        _same_device(k, v, k_cache, v_cache, slot_map)
-        spec = _keep(key, (k.shape[0], *strides, d))
-    _with_stream(k.get_device(), stream, lambda raw: _abi.check("usp_cache_append", _abi.load().usp_cache_append(
-        k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), slot_map.data_ptr(), *spec, raw)))
+    _on_stream("usp_cache_append", k, stream, _abi.binding().cache_append, k, v, k_cache, v_cache, slot_map)
     return k_cache, v_cache
-
-
-def _paged_desc(q, k_cache, v_cache, block_table, nreq, max_new, causal, scale, out_stride):
-    d = _cache_dims(k_cache, v_cache)
-    if q.dim() != 3 or q.shape[2] != d.hd or q.dtype != k_cache.dtype:
-        raise ValueError("q must be (tokens, hq, hd), of the cache's head dim and dtype")
-    stride = _block_table(block_table, nreq)
-    return UspPagedDesc(d, q.shape[0], _dense_rows("q", q), out_stride, stride, nreq, block_table.shape[1], q.shape[1],
-                        q.shape[0] if max_new is None else max_new, int(bool(causal)), 0.0 if scale is None else scale)
 
 
 def usp_paged_attn_workspace_size(q, k_cache, block_table, max_new: Optional[int] = None) -> int:
     """Workspace bytes usp_paged_attn needs for these shapes (on q's device)."""
-    d = _paged_desc(q, k_cache, k_cache, block_table, block_table.shape[0], max_new, True, None, 0)
-    with torch.cuda.device(q.device):
-        n = _abi.load().usp_paged_attn_workspace_size(d)
-    _need(n > 0, "invalid paged attention shapes")
-    return int(n)
+    return _abi.binding().paged_attn_workspace_size(q, k_cache, block_table, max_new)
 
 
 def usp_paged_attn(q, k_cache, v_cache, block_table, cu_new, kv_lens, max_new: Optional[int] = None,
@@ -700,49 +579,8 @@ def usp_paged_attn(q, k_cache, v_cache, block_table, cu_new, kv_lens, max_new: O
     were (unset where the call allocates them). ``max_new``: the most new tokens of one request, where
     the host knows it (1 for a decode step); it saves launches and does not change what is computed.
     ``workspace``: at least usp_paged_attn_workspace_size bytes (allocated per call where not given)."""
-    out_stride = 0
-    if out is not None:
-        if out.shape != q.shape or out.dtype != q.dtype:
-            raise ValueError("out must match q")
-        out_stride = _dense_rows("out", out)
-        _same_device(q, out)
-    dev = q.device
-    key = (q.shape, q.stride(), q.dtype, dev, k_cache.shape, k_cache.stride(), k_cache.dtype, k_cache.device,
-           v_cache.shape, v_cache.stride(), v_cache.dtype, v_cache.device, block_table.shape, block_table.stride(),
-           block_table.dtype, block_table.device, cu_new.shape, cu_new.stride(), cu_new.dtype, cu_new.device,
-           kv_lens.shape, kv_lens.stride(), kv_lens.dtype, kv_lens.device, max_new, causal, scale, out_stride)
-    d = _layouts.get(key)
-    if d is None:
-        nreq = kv_lens.numel()
-        _i32("cu_new", cu_new, nreq + 1)
-        _i32("kv_lens", kv_lens)
-        d = _paged_desc(q, k_cache, v_cache, block_table, nreq, max_new, causal, scale, out_stride)
-        _same_device(q, k_cache, v_cache, block_table, cu_new, kv_lens)
-        _keep(key, d)
-
-    def call(raw):
-        lib = _abi.load()
-        o, l, w = out, lse, workspace
-        if o is None:
-            o = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        if l is None:
-            l = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
-        else:
-            _need(l.shape == q.shape[:2] and l.dtype == torch.float32 and l.is_contiguous(),
-                  "lse must be contiguous fp32 (tokens, hq)")
-            _same_device(q, l)
-        if w is None:
-            w = torch.empty(max(lib.usp_paged_attn_workspace_size(d), 1), dtype=torch.uint8, device=dev)
-        elif w.device != dev or not w.is_contiguous():
-            raise ValueError("workspace must be contiguous, on the tensors' device")
-        rc = lib.usp_paged_attn(
-            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), cu_new.data_ptr(),
-            kv_lens.data_ptr(), o.data_ptr(), l.data_ptr(), d, w.data_ptr(), w.nbytes, raw)
-        if rc:
-            _abi.check("usp_paged_attn", rc)
-        return o, l
-
-    return _with_stream(dev.index, stream, call)
+    return _on_stream("usp_paged_attn", q, stream, _abi.binding().paged_attn, q, k_cache, v_cache, block_table, cu_new,
+                      kv_lens, max_new, causal, scale, out, lse, workspace)
 
 
 def default_scale(hd: int) -> float:

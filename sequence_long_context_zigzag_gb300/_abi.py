@@ -135,6 +135,32 @@ def load():
     return lib
 
 
+_binding = None
+
+
+def binding():
+    """The C++ binding of the paged cache's calls (csrc/binding.cpp), built first if it is absent, with the
+    library's functions bound to it."""
+    global _binding
+    if _binding is not None:
+        return _binding
+    import importlib.machinery
+    import importlib.util
+
+    from . import build as _build
+    lib = load()
+    path = _build.binding_path()
+    if not os.path.exists(path):
+        _build.build_binding()
+    loader = importlib.machinery.ExtensionFileLoader("_usp_binding", path)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_usp_binding", loader))
+    loader.exec_module(module)
+    module.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in
+                  (lib.usp_page_plan, lib.usp_cache_append, lib.usp_paged_attn, lib.usp_paged_attn_workspace_size)])
+    _binding = module
+    return module
+
+
 def strerror(status: int) -> str:
     return load().usp_strerror(int(status)).decode()
 

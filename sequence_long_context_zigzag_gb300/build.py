@@ -3,6 +3,9 @@
 Each .cu file compiles to an object in parallel (``-gencode arch=compute_103a,code=sm_103a``), then
 the objects link into one shared library with the CUDA runtime linked statically, so the library has
 no load-time dependency on libcudart or libcuda (driver entry points are fetched at run time).
+
+Beside them the C++ binding of the paged cache's calls (csrc/binding.cpp), a CPython module against the
+installed torch, compiles with g++ (a few seconds; its file name carries the torch version).
 """
 from __future__ import annotations
 
@@ -19,6 +22,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libusp.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -45,6 +49,40 @@ def _compile(src, obj, extra):
     return r.stderr
 
 
+def binding_path() -> str:
+    import torch
+    return os.path.join(PKG, "_usp_binding_torch" + "".join(c if c.isalnum() else "_" for c in torch.__version__) + ".so")
+
+
+def _build_binding(path: str) -> str:
+    import inspect
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    def dirs(f):  # the argument's name differs between torch versions
+        return f("cuda") if "device_type" in inspect.signature(f).parameters else f(True)
+    tmp = f"{path}.{os.getpid()}.tmp"
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", BINDING_SRC, "-o", tmp, "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"], *[f"-I{d}" for d in dirs(cpp_extension.include_paths)],
+           *[f"-L{d}" for d in dirs(cpp_extension.library_paths)], "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, path)
+    return r.stderr
+
+
+def build_binding(force: bool = False) -> str:
+    path = binding_path()
+    newest = max(os.path.getmtime(BINDING_SRC), os.path.getmtime(os.path.join(INCLUDE, "usp.h")))
+    if force or not os.path.exists(path) or os.path.getmtime(path) < newest:
+        _build_binding(path)
+    return path
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
@@ -56,6 +94,14 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         objs.append(o)
         if force or not os.path.exists(o) or os.path.getmtime(o) < max(os.path.getmtime(s), hdr_t):
             jobs.append((s, o))
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:  # beside nvcc
+        binding = ex.submit(build_binding, force)
+        lib = _build_lib(jobs, objs, force, verbose, extra_flags)
+        binding.result()
+    return lib
+
+
+def _build_lib(jobs, objs, force, verbose, extra_flags) -> str:
     if jobs:
         with cf.ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
             futs = {ex.submit(_compile, s, o, list(extra_flags)): s for s, o in jobs}
