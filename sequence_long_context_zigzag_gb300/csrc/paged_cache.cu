@@ -69,6 +69,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
     __shared__ int32_t ctx_s[kTile];
     __shared__ int64_t red[kPlanThreads / 32];
     __shared__ int32_t red_max[kPlanThreads / 32];
+    wait_grid_before();
     const int tid = threadIdx.x, ps = 1 << p.log_ps;
     const int64_t t0 = (int64_t)blockIdx.x * p.slice, t1 = min(t0 + p.slice, p.max_tokens);
     const bool writer = blockIdx.x == 0;  // CTA 0 walks all requests and writes the per-request outputs
@@ -186,6 +187,7 @@ struct AppendArgs {
 };
 
 __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const AppendArgs p) {
+    wait_grid_before();
     uint4 k[kUnroll], v[kUnroll];
     int64_t kd[kUnroll], vd[kUnroll];
     bool ok[kUnroll];
@@ -287,8 +289,8 @@ int usp_page_plan(const int32_t *ctx_lens, const int32_t *new_lens, const int32_
     const int64_t ctas = std::max<int64_t>(
         1, std::min<int64_t>((d.max_tokens + kPlanThreads - 1) / kPlanThreads, 2 * (int64_t)di->sm_count));
     a.slice = (d.max_tokens + ctas - 1) / ctas;
-    page_plan_kernel<<<(unsigned)ctas, kPlanThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
-    return cudaGetLastError() == cudaSuccess ? USP_OK : USP_ERR_CUDA;
+    return launch_overlapped(page_plan_kernel, dim3((unsigned)ctas), kPlanThreads, 0,
+                             reinterpret_cast<cudaStream_t>(stream), a);
 }
 
 int usp_cache_append(const void *k, const void *v, void *k_cache, void *v_cache, const int32_t *slot_map,
@@ -323,8 +325,7 @@ int usp_cache_append(const void *k, const void *v, void *k_cache, void *v_cache,
     a.log_row = log2_of((int64_t)d.hd * es / 16);
     a.per_token = FastDiv((uint32_t)per_token);
     const unsigned grid = (a.pieces + (unsigned)(kAppendThreads * kUnroll) - 1) / (kAppendThreads * kUnroll);
-    cache_append_kernel<<<grid, kAppendThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
-    return cudaGetLastError() == cudaSuccess ? USP_OK : USP_ERR_CUDA;
+    return launch_overlapped(cache_append_kernel, dim3(grid), kAppendThreads, 0, reinterpret_cast<cudaStream_t>(stream), a);
 }
 
 }  // extern "C"

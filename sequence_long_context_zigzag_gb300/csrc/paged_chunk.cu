@@ -668,14 +668,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kSlot);
     volatile uint32_t *skip_flag = tmem_slot + 1;
     const int warp = threadIdx.x >> 5;
-    // the next kernels of the call may take their places as SMs come free
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
         tc::prefetch_tmap(&p.tq);
         tc::prefetch_tmap(&p.tk);
         tc::prefetch_tmap(&p.tv);
-        // a bounded wait of an earlier kernel ran out: do no work until usp_check clears it
-        *skip_flag = (*reinterpret_cast<volatile int *>(p.status) != 0) ? 1u : 0u;
         for (int s = 0; s < C::kStages; ++s) {
             tc::mbar_init(bar0 + 8u * (C::K_FULL + s), 1);
             tc::mbar_init(bar0 + 8u * (C::K_EMPTY + s), 2);
@@ -703,7 +699,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         tc::tmem_alloc(tc::smem_u32(tmem_slot), 512);
         tc::tmem_relinquish();
     }
+    wait_grid_before();
+    // a bounded wait of an earlier kernel ran out: do no work until usp_check clears it
+    const int status = *reinterpret_cast<volatile int *>(p.status);
+    let_next_start();
     const bool work = sched_scan<kThreads, kN>(p.s, sh);  // the same for every thread
+    if (threadIdx.x == 0) *skip_flag = status != 0;
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -756,8 +757,7 @@ int launch_typed(const ChunkParams &p, int grid, cudaStream_t s) {
             attr_set[dev] = true;
         }
     }
-    paged_chunk_kernel<HD><<<grid, kThreads, kSmem, s>>>(p);
-    return cudaGetLastError() == cudaSuccess ? USP_OK : USP_ERR_CUDA;
+    return launch_overlapped(paged_chunk_kernel<HD>, dim3((unsigned)grid), kThreads, kSmem, s, p);
 }
 
 }  // namespace

@@ -71,6 +71,7 @@ struct DecodeParams {
     int64_t q_stride, out_stride, table_stride;
     int32_t num_pages, log_ps, hq;
     float scale_log2;
+    bool second;  // the call's other kernel is in the stream before this one
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -415,13 +416,9 @@ __global__ void __launch_bounds__(Cfg<HD, RT>::kThreads, RT == 1 ? 2 : 1)
     const uint32_t sbase = raw + pad;
     __shared__ SchedShared sh;
     __shared__ uint32_t skip;
-    // the combine may take its place on the SMs already; it waits for this kernel's end before it reads
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
         tc::prefetch_tmap(&p.tk);
         tc::prefetch_tmap(&p.tv);
-        // a bounded wait of an earlier kernel ran out: do no work until usp_check clears it
-        skip = *reinterpret_cast<volatile int *>(p.status) != 0;
         const uint32_t bar = sbase + C::kBar;
         for (int i = 0; i < C::kStages; ++i) {
             tc::mbar_init(bar + 8 * (C::FULL + i), 1);
@@ -433,6 +430,9 @@ __global__ void __launch_bounds__(Cfg<HD, RT>::kThreads, RT == 1 ? 2 : 1)
         }
         tc::fence_barrier_init();
     }
+    begin_in_order(p.second);
+    // a bounded wait of an earlier kernel ran out: do no work until usp_check clears it
+    if (threadIdx.x == 0) skip = *reinterpret_cast<volatile int *>(p.status) != 0;
     const bool work = sched_scan<C::kThreads, C::kKT>(p.s, sh);
     __syncthreads();
     if (!work || skip) {
@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(Cfg<HD, RT>::kThreads, RT == 1 ? 2 : 1)
     } else {
         consumer<HD, RT>(p, smem, sbase);
     }
-    follow_grid_before();
+    end_in_order(p.second);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -542,7 +542,7 @@ __device__ __forceinline__ void combine_rows(const CombineArgs &a, const PartSpa
 
 template <typename T, int HD>
 __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const CombineArgs a) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_grid_before();
     const int per0 = (a.w[0].rows + kCombineRows - 1) / kCombineRows;
     const int per1 = (a.w[1].rows + kCombineRows - 1) / kCombineRows;
     const int x = (int)blockIdx.x - a.w[0].ctas * per0;
@@ -551,7 +551,7 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Co
 }
 
 template <int HD, int RT>
-int launch_typed(const DecodeParams &p, int grid, bool second, cudaStream_t s) {
+int launch_typed(const DecodeParams &p, int grid, cudaStream_t s) {
     using C = Cfg<HD, RT>;
     constexpr int kSmem = C::kSmem;
     static_assert(kSmem + 2048 <= (RT == 1 ? 114 : 227) * 1024, "shared memory per CTA");
@@ -569,7 +569,7 @@ int launch_typed(const DecodeParams &p, int grid, bool second, cudaStream_t s) {
             attr_set[dev] = true;
         }
     }
-    return launch_overlapped(paged_decode_kernel<HD, RT>, dim3((unsigned)grid), C::kThreads, kSmem, s, p, second);
+    return launch_overlapped(paged_decode_kernel<HD, RT>, dim3((unsigned)grid), C::kThreads, kSmem, s, p);
 }
 
 }  // namespace
@@ -603,15 +603,16 @@ int launch_paged_decode(const PagedArgs &a, int rows, int n_hi, bool second, con
     p.q_stride = a.q_stride; p.out_stride = a.out_stride; p.table_stride = a.table_stride;
     p.num_pages = (int32_t)a.num_pages; p.log_ps = a.log_ps; p.hq = a.hq;
     p.scale_log2 = a.scale_log2;
+    p.second = second;
     if (rows == 16)
-        return a.hd == 128 ? launch_typed<128, 1>(p, w.ctas, second, s) : launch_typed<64, 1>(p, w.ctas, second, s);
-    return a.hd == 128 ? launch_typed<128, 2>(p, w.ctas, second, s) : launch_typed<64, 2>(p, w.ctas, second, s);
+        return a.hd == 128 ? launch_typed<128, 1>(p, w.ctas, s) : launch_typed<64, 1>(p, w.ctas, s);
+    return a.hd == 128 ? launch_typed<128, 2>(p, w.ctas, s) : launch_typed<64, 2>(p, w.ctas, s);
 }
 
 int launch_paged_combine(const CombineArgs &a, int hd, int dtype, cudaStream_t s) {
     const int per = kCombineRows;
     const dim3 grid((unsigned)(a.w[0].ctas * ((a.w[0].rows + per - 1) / per) + a.w[1].ctas * ((a.w[1].rows + per - 1) / per)));
-    auto go = [&](auto kernel) { return launch_overlapped(kernel, grid, kCombineThreads, 0, s, a, true); };
+    auto go = [&](auto kernel) { return launch_overlapped(kernel, grid, kCombineThreads, 0, s, a); };
     if (dtype == USP_BF16)
         return hd == 128 ? go(paged_combine_kernel<__nv_bfloat16, 128>) : go(paged_combine_kernel<__nv_bfloat16, 64>);
     return hd == 128 ? go(paged_combine_kernel<float, 128>) : go(paged_combine_kernel<float, 64>);

@@ -38,6 +38,7 @@ struct F32Params {
     int64_t q_stride, out_stride, table_stride, k_page, v_page;
     int32_t num_pages, log_ps, hq;
     float scale_log2;
+    bool second;  // the call's other kernel is in the stream before this one
 };
 
 __device__ __forceinline__ float finite_or_0(float m) { return m == -INFINITY ? 0.f : m; }
@@ -68,7 +69,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_f32_few_kernel(const __g
     __shared__ __align__(16) float qs[kFewRows][HD];
     __shared__ float xch[kFewWarps][kFewRows][HD];
     __shared__ float2 ml[kFewWarps][kFewRows];
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    begin_in_order(p.second);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int srow = lane >> 2, skey = lane & 3;  // the score this lane ends up with
     // thread 0 walks the span; its state stays in shared memory, out of the products' registers
@@ -219,7 +220,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_f32_few_kernel(const __g
         }
     }
     if (tid == 0) p.w.head[blockIdx.x] = opened;
-    follow_grid_before();
+    end_in_order(p.second);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -259,7 +260,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) paged_f32_many_kernel(const _
     constexpr int kLd = kManyKT * HD / 4 / kManyThreads;  // 16-byte copies of K (and V) per thread
     extern __shared__ __align__(16) float sm[];
     __shared__ SchedShared sh;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    begin_in_order(false);
     float *qs = sm + C::kQ, *ks = sm + C::kK, *vs = sm + C::kV, *pt = sm + C::kP;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     // thread 0 walks the span; its state stays in shared memory, out of the products' registers
@@ -479,8 +480,7 @@ int launch_many(const F32Params &p, int grid, cudaStream_t s) {
             attr_set[dev] = true;
         }
     }
-    paged_f32_many_kernel<HD><<<grid, kManyThreads, kSmem, s>>>(p);
-    return cudaGetLastError() == cudaSuccess ? USP_OK : USP_ERR_CUDA;
+    return launch_overlapped(paged_f32_many_kernel<HD>, dim3((unsigned)grid), kManyThreads, kSmem, s, p);
 }
 
 }  // namespace
@@ -510,9 +510,10 @@ int launch_paged_f32(const PagedArgs &a, bool many, int n_lo, int n_hi, bool sec
     p.k_page = a.k_page; p.v_page = a.v_page;
     p.num_pages = (int32_t)a.num_pages; p.log_ps = a.log_ps; p.hq = a.hq;
     p.scale_log2 = a.scale_log2;
+    p.second = second;
     if (many) return a.hd == 128 ? launch_many<128>(p, w.ctas, s) : launch_many<64>(p, w.ctas, s);
     return launch_overlapped(a.hd == 128 ? paged_f32_few_kernel<128> : paged_f32_few_kernel<64>, dim3((unsigned)w.ctas),
-                             kFewThreads, 0, s, p, second);
+                             kFewThreads, 0, s, p);
 }
 
 }  // namespace usp

@@ -302,29 +302,6 @@ __device__ __forceinline__ float *part_slot(const PartSpace &w, int hd, int cta,
     return w.data + ((size_t)cta * 2 + slot) * (size_t)w.rows * (hd + 2);
 }
 
-// Launch of a call's later kernels: they may start while the one before still runs (as SMs come free), and
-// order themselves with griddepcontrol.wait where they need its results, at their end at the latest.
-template <typename K, typename P>
-inline int launch_overlapped(K kernel, dim3 grid, int threads, int smem, cudaStream_t s, const P &p, bool overlap) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = overlap ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? USP_OK : USP_ERR_CUDA;
-}
-// the end of a kernel that may have been launched early: the grid before has completed when this one has,
-// so that the combine, which waits for this one only, follows both. One CTA waits for that; the others make
-// room on the SMs.
-__device__ __forceinline__ void follow_grid_before() {
-    if (blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 struct CombineArgs {
     PartSpace w[2];  // one per kernel of the call (ctas == 0: not launched)
     void *out;

@@ -451,3 +451,66 @@ def test_binding_refuses_on_the_gpu():
     assert (o == 3).all()
     usp.usp_paged_attn(q[:0], kc, vc, table, cu * 0, kv)
     usp.usp_check()
+
+
+def test_calls_follow_the_work_before_them():
+    """The kernels may start before the work before them in the stream has ended: inputs that long kernels,
+    copies and other streams are still writing when the calls are made have to be seen, eagerly and in a
+    graph."""
+    hq, hkv, hd, ps = 8, 2, 128, 16
+    for reqs in ([(700, 1), (90, 1)], [(600, 120), (90, 1)]):
+        for dt in (torch.bfloat16, torch.float32):
+            c = Cache(reqs, hq, hkv, hd, ps, dt, seed=60)
+            want = [x.clone() for x in attend(c)]
+            true = [t.clone() for t in c.args()]
+            slow = torch.randn(4096, 4096, device="cuda")
+            buf = [torch.empty_like(t) for t in true]
+            rows = torch.arange(c.T, device="cuda", dtype=torch.int32)
+            side = torch.cuda.Stream()
+            dst = [torch.zeros(64, hkv, ps, hd, dtype=dt, device="cuda") for _ in range(2)]
+            kvrows = [torch.randn(c.T, hkv, hd, device="cuda").to(dt) for _ in range(2)]
+            late = [torch.zeros_like(x) for x in kvrows]
+
+            def work():
+                for d in dst:
+                    d.zero_()
+                for b, x in zip(late, kvrows):
+                    b.zero_()
+                for b, t in zip(buf, true):
+                    b.zero_() if b.dtype == torch.int32 else b.fill_(1)
+                here = torch.cuda.current_stream()
+                side.wait_stream(here)
+                with torch.cuda.stream(side):
+                    (slow @ slow).sum()
+                    buf[2].copy_(true[2])
+                for _ in range(3):
+                    y = slow @ slow
+                y.sum()
+                for i in (0, 1, 3, 4, 5):
+                    buf[i].copy_(true[i])
+                here.wait_stream(side)
+                o1 = usp.usp_paged_attn(*buf)                       # after a copy and another stream
+                for b, x in zip(late, kvrows):
+                    b.copy_(x)
+                usp.usp_cache_append(*late, *dst, rows)             # after a copy kernel
+                p1 = usp.usp_page_plan(buf[5], buf[5], rows, rows[:1], buf[3].clone(), ps, 2 ** 20, 5000)
+                o2 = usp.usp_paged_attn(*buf)                       # after its own kind
+                return o1, p1, o2
+
+            def check(o1, p1, o2):
+                for o in (o1, o2):
+                    assert torch.equal(o[0], want[0]) and torch.equal(o[1], want[1])
+                assert torch.equal(p1[2], true[5] * 2)
+                for d, x in zip(dst, kvrows):
+                    assert torch.equal(d.transpose(1, 2).reshape(-1, hkv, hd)[:c.T], x)
+            for _ in range(3):
+                r = work()
+                torch.cuda.synchronize()
+                check(*r)
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                r = work()
+            for _ in range(3):
+                g.replay()
+                torch.cuda.synchronize()
+                check(*r)
