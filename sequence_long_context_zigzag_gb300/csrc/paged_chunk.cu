@@ -80,7 +80,8 @@ template <int HD> struct Cfg {
     static constexpr int SEG_FULL = O_EMPTY + 2;      // [kSegSlots]
     static constexpr int SEG_EMPTY = SEG_FULL + kSegSlots;
     static constexpr int TAIL = SEG_EMPTY + kSegSlots;  // [2]: V tiles that the walk warp has to clear the end of
-    static constexpr int kNumBars = TAIL + 2;
+    static constexpr int P_HALF = TAIL + 2;             // [2]: the first half of a tile's P
+    static constexpr int kNumBars = P_HALF + 2;
     static constexpr int kSlot = kBar + (kNumBars * 8 + 15) / 16 * 16;  // tensor memory address, skip flag
     static constexpr int kSeg = kSlot + 16;
     // a staging slot per softmax warp for its stores: 32 rows x 128 bytes
@@ -336,12 +337,12 @@ __device__ __forceinline__ void issue_s(uint32_t el, uint32_t d_tmem, uint64_t q
     }
 }
 // V as (N = hd) x (K = keys), MN-major: 64-column blocks kBoxBytes apart, 8-key groups 1024 bytes apart
-template <int HD>
+template <int HD, int kHalf>  // keys [64 kHalf, 64 kHalf + 64)
 __device__ __forceinline__ void issue_pv(uint32_t el, uint32_t d_tmem, uint32_t p_tmem, uint64_t vdesc,
                                          uint32_t accumulate) {
     constexpr uint32_t id = tc::idesc_bf16_f32(kM, HD, 0, 1);
 #pragma unroll
-    for (int k = 0; k < kN / 16; ++k)
+    for (int k = kHalf * 4; k < kHalf * 4 + 4; ++k)
         mma_ts_if(el, d_tmem, p_tmem + k * 8, vdesc + (uint64_t)((k * 2048) >> 4), id, (accumulate || k > 0) ? 1u : 0u);
 }
 
@@ -424,11 +425,14 @@ __device__ void mma_role(const ChunkParams &p, const uint8_t *smem, uint32_t sba
         if (!last && !(ok = wait(C::K_FULL + stn, phn))) break;
         if (cur.act && !started && no > 0 && !(ok = wait(C::O_EMPTY + i, (no - 1) & 1u))) break;
         if (!(ok = wait(my_turn, (turns++) & 1u))) break;
-        if (cur.act && !(ok = wait(C::P_FULL + i, pc & 1u))) break;
+        if (cur.act && !(ok = wait(C::P_HALF + i, pc & 1u))) break;
         if (cur.act) {
+            tc::fence_after_sync();
+            issue_pv<HD, 0>(el, tO, tS, vdesc0 + stage_off(st), started);
+            if (!(ok = wait(C::P_FULL + i, pc & 1u))) break;
             ++pc;
             tc::fence_after_sync();
-            issue_pv<HD>(el, tO, tS, vdesc0 + stage_off(st), started);
+            issue_pv<HD, 1>(el, tO, tS, vdesc0 + stage_off(st), 1);
             started = 1;
         }
         commit_if(el, BAR(C::V_EMPTY + st));
@@ -563,6 +567,13 @@ __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegM
                 pk[e] = float2_to_bf16x2(p0, p1);
             }
             tc::tmem_st16(tS + c * 16, pk);
+            if (c == 1) {
+                // the products of the first 64 keys run under the exponentials of the others (1% at all lengths)
+                tc::tmem_st_wait();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(bar0 + 8u * (C::P_HALF + i));
+            }
         }
         float s0, s1;
         tc::unpack2(sum, s0, s1);
@@ -687,6 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(bar0 + 8u * (C::S_FULL + i), 1);
             tc::mbar_init(bar0 + 8u * (C::P_FULL + i), 4);
+            tc::mbar_init(bar0 + 8u * (C::P_HALF + i), 4);
             tc::mbar_init(bar0 + 8u * (C::O_FULL + i), 1);
             tc::mbar_init(bar0 + 8u * (C::O_EMPTY + i), 4);
             tc::mbar_init(bar0 + 8u * (C::DONE + i), 1);
