@@ -592,7 +592,7 @@ __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegM
     float *slot = part_slot(p.w, HD, blockIdx.x, g.t0 == 0 ? 1 : 0);
     const int head = g.head * p.s.G + (int)rh;
     __nv_bfloat16 *orow = p.out + (g.tok0 + tok) * p.out_stride + (int64_t)head * HD;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
     if (any) {
         ok = tc::mbar_wait(bar0 + 8u * (C::O_FULL + i), no & 1u, p.status, USP_ERR_TIMEOUT, kWaitLimitNs);
         ok = __all_sync(0xffffffffu, ok);
@@ -656,7 +656,7 @@ __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegM
     }
     if (row_ok) {
         if (whole) {
-            p.lse[(g.tok0 + tok) * p.hq + head] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+            p.lse[(g.tok0 + tok) * p.hq + head] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
         } else {
             // a part without a visible key has m = -inf: the combine gives its (unwritten) o no weight
             slot[(size_t)p.w.rows * HD + r] = m;

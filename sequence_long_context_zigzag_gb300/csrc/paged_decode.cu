@@ -362,7 +362,7 @@ __device__ void consumer(const DecodeParams &p, uint8_t *smem, uint32_t sbase) {
             for (int w = 0; w < 4; ++w) mm = fmaxf(mm, ml[w * 16 + qr + h * 8].x);
             a[h] = mm == -INFINITY ? 0.f : tc::ex2(m[h] - mm);
         }
-        const float inv = whole ? (L > 0.f ? 1.f / L : 0.f) : 1.f;
+        const float inv = whole && L != 0.f ? 1.f / L : 1.f;
         uint32_t tok, hr;
         p.s.by_G.divmod((uint32_t)(group * 16 + orow), tok, hr);
         const int head = g.head * p.s.G + (int)hr;
@@ -394,7 +394,7 @@ __device__ void consumer(const DecodeParams &p, uint8_t *smem, uint32_t sbase) {
         }
         if (orow < rows && (tid & 7) == 0) {
             if (whole) {
-                p.lse[(g.tok0 + tok) * p.hq + head] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
+                p.lse[(g.tok0 + tok) * p.hq + head] = L == 0.f ? -INFINITY : (M + __log2f(L)) * kLn2;
             } else {
                 float *st = part_slot(p.w, HD, blockIdx.x, g.t0 == 0 ? 1 : 0) + (size_t)p.w.rows * HD + group * 16 + orow;
                 st[0] = M;
@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(Cfg<HD, RT>::kThreads, RT == 1 ? 2 : 1)
 // parts), so a thread fetches the maxima, sums and rows of 8 (row, part) pairs at once: 8 parts of a row in
 // the few-row kernels' units, which long sequences cut into many, 2 parts of 4 rows in the others' (prompts
 // of 16334 tokens: 16 us with a row at a time). A part whose rows saw nothing has m = -inf, and its o
-// (perhaps unwritten) is not used. Small CTAs: some fit beside the decode kernel's and are in place when it
+// (perhaps unwritten) is not used; a NaN score leaves l NaN, which is kept. Small CTAs: some fit beside the decode kernel's and are in place when it
 // ends.
 constexpr int kCombineThreads = 128;
 constexpr int kCombineRows = 16;  // rows per CTA
@@ -507,7 +507,7 @@ __device__ __forceinline__ void combine_rows(const CombineArgs &a, const PartSpa
 #pragma unroll
                 for (int i = 0; i < NP; ++i) {
                     const float g = tc::ex2(m[j][i] - mb);
-                    if (g > 0.f) {
+                    if (g > 0.f || l[j][i] != l[j][i]) {
                         L[j] = fmaf(g, l[j][i], L[j]);
                         acc[j].x = fmaf(g, o[j][i].x, acc[j].x);
                         acc[j].y = fmaf(g, o[j][i].y, acc[j].y);
@@ -521,7 +521,7 @@ __device__ __forceinline__ void combine_rows(const CombineArgs &a, const PartSpa
         for (int j = 0; j < NR; ++j) {
             const int r = first + j * kStep;
             if (r >= end) break;
-            const float inv = L[j] > 0.f ? 1.f / L[j] : 0.f;
+            const float inv = L[j] == 0.f ? 0.f : 1.f / L[j];
             uint32_t tok, hr;
             a.by_G.divmod((uint32_t)r, tok, hr);
             const int head = h.head * a.G + (int)hr;
@@ -535,7 +535,7 @@ __device__ __forceinline__ void combine_rows(const CombineArgs &a, const PartSpa
             }
             if (col == 0)
                 a.lse[(h.tok0 + tok) * a.hq + head] =
-                    L[j] > 0.f ? (M[j] + (kExact ? log2f(L[j]) : __log2f(L[j]))) * kLn2 : -INFINITY;
+                    L[j] == 0.f ? -INFINITY : (M[j] + (kExact ? log2f(L[j]) : __log2f(L[j]))) * kLn2;
         }
     }
 }

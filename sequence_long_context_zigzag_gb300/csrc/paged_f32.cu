@@ -207,8 +207,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_f32_few_kernel(const __g
                 p.s.by_G.divmod((uint32_t)r, tok, h);
                 const int head = g.head * p.s.G + (int)h;
                 if (whole) {
-                    p.out[(g.tok0 + tok) * p.out_stride + (int64_t)head * HD + c] = L > 0.f ? acc / L : 0.f;
-                    if (c == 0) p.lse[(g.tok0 + tok) * p.hq + head] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+                    p.out[(g.tok0 + tok) * p.out_stride + (int64_t)head * HD + c] = L == 0.f ? 0.f : acc / L;
+                    if (c == 0) p.lse[(g.tok0 + tok) * p.hq + head] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
                 } else {
                     slot[(size_t)r * HD + c] = acc;
                     if (c == 0) {
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) paged_f32_many_kernel(const _
                 uint32_t tok, h;
                 p.s.by_G.divmod((uint32_t)r, tok, h);
                 const int head = g.head * p.s.G + (int)h;
-                const float inv = whole ? (l[i] > 0.f ? 1.f / l[i] : 0.f) : 1.f;
+                const float inv = whole && l[i] != 0.f ? 1.f / l[i] : 1.f;
                 float *dst = whole ? p.out + (g.tok0 + tok) * p.out_stride + (int64_t)head * HD : slot + (size_t)r * HD;
 #pragma unroll
                 for (int c = 0; c < kCols; ++c) {
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) paged_f32_many_kernel(const _
                 }
                 if (tx == 0) {
                     if (whole) {
-                        p.lse[(g.tok0 + tok) * p.hq + head] = l[i] > 0.f ? (m[i] + log2f(l[i])) * kLn2 : -INFINITY;
+                        p.lse[(g.tok0 + tok) * p.hq + head] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * kLn2;
                     } else {
                         slot[(size_t)p.w.rows * HD + r] = m[i];
                         slot[(size_t)p.w.rows * (HD + 1) + r] = l[i];

@@ -214,6 +214,27 @@ def test_attention_peaked_and_large_scores():
 
 
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("reqs", [[(500, 1), (64, 1), (9000, 1)], [(300, 150), (2000, 70), (80, 80)]], ids=["decode", "chunks"])
+def test_attention_a_nan_query_row_is_nan_and_stays_alone(reqs, dt):
+    """A query row that holds a NaN gets NaN in out and lse, in units that one CTA finishes and in cut ones;
+    every other row stays what it is. (Not to the bit: rows of a unit rescale together when the maximum of one
+    of them grows, so a row's rounding depends on its neighbours' scores; the bounds count any such order.)"""
+    c = Cache(reqs, 8, 2, 64, 32, dt, seed=8)
+    q = c.q.clone()
+    want = [x.clone() for x in attend(c)]
+    rows = [(0, 3), (c.T // 2, 6), (c.T - 1, 0)]
+    for t, h in rows:
+        c.q[t, h, 5] = float("nan")
+    out, lse = attend(c)
+    hit = torch.zeros(c.T, c.hq, dtype=torch.bool, device="cuda")
+    for t, h in rows:
+        hit[t, h] = True
+    assert torch.isnan(out[hit]).all() and torch.isnan(lse[hit]).all()
+    out[hit], lse[hit], c.q = want[0][hit], want[1][hit], q
+    check_attention(c, out, lse)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
 def test_attention_same_bits_on_every_run(dt):
     c = Cache([(5000, 1), (3000, 300), (40, 40), (2500, 1)], 8, 2, 128, 16, dt, seed=6)
     a = [x.clone() for x in attend(c)]
