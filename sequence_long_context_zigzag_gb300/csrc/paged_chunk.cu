@@ -369,15 +369,17 @@ __device__ void mma_role(const ChunkParams &p, const uint8_t *smem, uint32_t sba
     const int my_turn = C::TURN + i, other_turn = C::TURN + (1 - i);
     uint32_t turns = 0, nseg = 0;
     bool ok = true;
-    // the tiles of all segments as one stream (segments without a tile are passed over): the next tile is
-    // kt of [kt, t1); this issuer's Q tile needs those below act_end
+    // the tiles of all segments as one stream: the next tile is kt of [kt, t1); this issuer's Q tile needs
+    // those below act_end. A segment without a tile is an element of the stream too: passed over at once, it
+    // would take the issuers up to a ring of segments ahead of the softmax warps, which wait for the O of the
+    // last tile while the ring has no place for the segment that the issuers wait for.
     struct Tile {
-        bool have, first, act;  // there is one; it opens a segment; the Q tile needs it
+        bool have, first, act, none;  // there is one; it opens a segment; the Q tile needs it; no tile
     };
     int kt = 0, t1 = 0, act_end = 0;
     auto next_tile = [&]() {
-        Tile t{true, false, false};
-        while (kt >= t1) {
+        Tile t{true, false, false, false};
+        if (kt >= t1) {
             SegMsg g;
             ok = next_segment<HD>(p, smem, bar0, nseg, g);
             if (!ok || __reduce_max_sync(0xffffffffu, g.ntok) == 0) {
@@ -389,6 +391,10 @@ __device__ void mma_role(const ChunkParams &p, const uint8_t *smem, uint32_t sba
             t1 = __reduce_max_sync(0xffffffffu, g.t1);
             act_end = __reduce_max_sync(0xffffffffu, i ? g.act[1] : g.act[0]);
             t.first = true;
+            if (kt >= t1) {
+                t.none = true;
+                return t;
+            }
         }
         t.act = kt < act_end;
         ++kt;
@@ -405,6 +411,7 @@ __device__ void mma_role(const ChunkParams &p, const uint8_t *smem, uint32_t sba
     uint32_t nq = 0, no = 0;       // Q loads consumed; O_i read-outs handed to the softmax
     uint32_t j = 0;                // tiles of the stream
     Tile cur = next_tile();
+    while (ok && cur.have && cur.none) cur = next_tile();  // nothing waits for this warp yet
     if (ok && cur.have) {
         ok = wait(C::Q_FULL, 0) && wait(C::K_FULL, 0);
         nq = 1;
@@ -417,7 +424,7 @@ __device__ void mma_role(const ChunkParams &p, const uint8_t *smem, uint32_t sba
     while (ok && cur.have) {
         const Tile nxt = next_tile();
         if (!ok) break;
-        const bool last = !nxt.have || nxt.first, boundary = nxt.have && nxt.first;
+        const bool last = !nxt.have || nxt.first, boundary = nxt.have && nxt.first && !nxt.none;
         const uint32_t st = j % C::kStages, ph = (j / C::kStages) & 1u;
         const uint32_t stn = (j + 1) % C::kStages, phn = ((j + 1) / C::kStages) & 1u;
         if (last) commit_if(el, BAR(C::Q_EMPTY));  // this issuer's S products of the segment are issued
@@ -454,6 +461,15 @@ __device__ void mma_role(const ChunkParams &p, const uint8_t *smem, uint32_t sba
         }
         cur = nxt;
         ++j;
+        // over segments without a tile, one at a time: all that the softmax warps need is issued
+        if (cur.none) {
+            while (ok && cur.have && cur.none) cur = next_tile();
+            if (!ok || !cur.have) break;
+            if (!(ok = wait(C::Q_FULL, nq & 1u))) break;
+            ++nq;
+            if (!(ok = wait(C::K_FULL + j % C::kStages, (j / C::kStages) & 1u))) break;
+            s_burst(cur.act, j % C::kStages);
+        }
     }
     if (!ok) arrive_if(el, BAR(other_turn));  // let the other issuer reach its own bounded exit
     commit_if(el, BAR(C::DONE + i));           // every MMA of this issuer ends before tensor memory is freed

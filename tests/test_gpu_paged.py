@@ -214,6 +214,19 @@ def test_attention_peaked_and_large_scores():
 
 
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("reqs", [[(200, 2000)], [(300, 40)] + [(0, 40)] * 30 + [(300, 40)], [(0, 90)] * 9,
+                                  [(1, 500), (900, 40), (2, 700), (0, 50), (40, 1)]],
+                         ids=["one-request", "between", "only", "mixed"])
+def test_attention_runs_of_units_without_a_key(reqs, dt):
+    """Many blocks of tokens in a row that see no key (more new tokens than keys), before, between and behind
+    blocks that do."""
+    c = Cache(reqs, 8, 2, 64, 32, dt, seed=9)
+    for kw in (dict(max_new=c.max_new), dict(max_new=1), dict(max_new=c.max_new, causal=False)):
+        out, lse = attend(c, **kw)
+        check_attention(c, out, lse, causal=kw.get("causal", True))
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("reqs", [[(500, 1), (64, 1), (9000, 1)], [(300, 150), (2000, 70), (80, 80)]], ids=["decode", "chunks"])
 def test_attention_a_nan_query_row_is_nan_and_stays_alone(reqs, dt):
     """A query row that holds a NaN gets NaN in out and lse, in units that one CTA finishes and in cut ones;
