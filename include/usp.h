@@ -392,7 +392,7 @@ typedef struct {
     int64_t table_stride; /* entries between consecutive rows of block_table (>= max_pages) */
     int64_t free_count;   /* entries of free_pages */
     int64_t max_tokens;   /* entries of slot_map, < 2^31 */
-    int32_t nreq;         /* requests */
+    int32_t nreq;         /* requests, at most 2^30 */
     int32_t max_pages;    /* columns of block_table */
     int32_t page_size;    /* 16, 32, 64, 128 or 256 */
 } usp_plan_dims;
@@ -428,7 +428,8 @@ USP_API int usp_page_plan(const int32_t *ctx_lens, const int32_t *new_lens, cons
  *                slices of a fused projection; strides a multiple of 16 bytes
  *   slot_map   : int32 [tokens]; a token whose slot is not in [0, num_pages * page_size) is skipped
  * Bit-exact copy; nothing else of the cache changes. Slots must be distinct (where two tokens share
- * one, its row may hold parts of both). k, v, k_cache, v_cache 16-byte aligned; sources must not
+ * one, its row may hold parts of both): requests that share pages share full ones, and a page that is
+ * to be continued by two requests is copied first. k, v, k_cache, v_cache 16-byte aligned; sources must not
  * overlap the cache.
  */
 USP_API int usp_cache_append(const void *k, const void *v, void *k_cache, void *v_cache, const int32_t *slot_map,
@@ -441,7 +442,7 @@ typedef struct {
     int64_t q_stride;     /* elements between consecutive tokens of q (0: hq * hd); a multiple of 16 bytes */
     int64_t out_stride;   /* the same for out */
     int64_t table_stride; /* entries between consecutive rows of block_table (>= max_pages) */
-    int32_t nreq;         /* requests */
+    int32_t nreq;         /* requests, at most 2^30 */
     int32_t max_pages;    /* columns of block_table */
     int32_t hq;           /* query heads; head h reads KV head h / (hq / hkv); hq / hkv <= 128 */
     int32_t max_new;      /* the most new tokens of one request, as far as the host knows (at most
@@ -460,10 +461,10 @@ typedef struct {
  * New token j of n_i has position kv_i - n_i + j and sees keys 0 .. that position (0 .. kv_i - 1
  * without the causal mask). A row without a visible key gets o = 0, lse = -inf. Rows outside
  * [cu_new[0], cu_new[nreq]) are left as they were. Cache rows behind kv_i may hold anything (NaN
- * among it); rows a request has must be finite where some query of the call sees them: in the bf16
- * kernels a non-finite V row reaches every query of its 128-key tile. Partials over parts of
- * a sequence (e.g. one ring rank's keys each) merge with usp_lse_merge. Requests may share pages. out and
- * lse must not overlap each other or the inputs.
+ * among it); a request's own rows must be finite: a non-finite V row may reach queries that do not see
+ * it (its weight is zero there, and 0 x NaN is NaN). A query row with a NaN gets NaN, it alone. Partials
+ * over parts of a sequence (e.g. one ring rank's keys each) merge with usp_lse_merge. Requests may share
+ * pages. out and lse must not overlap each other or the inputs.
  *   workspace : DEVICE buffer, 256-byte aligned, at least usp_paged_attn_workspace_size(d) bytes,
  *               clobbered; calls that share it must be ordered on one stream (two captured graphs
  *               that may run at the same time need one each). It needs no initialisation.

@@ -7,6 +7,9 @@ namespace usp {
 
 inline bool valid_page_size(int32_t ps) { return ps >= 16 && ps <= 256 && (ps & (ps - 1)) == 0; }
 
+// requests of a call: loops step over them by up to 1024 in 32 bits
+constexpr int32_t kMaxRequests = 1 << 30;
+
 int check_cache_dims(const usp_cache_dims &d);
 
 // usp_paged_attn's arguments, checked and with the defaults filled in (strides in elements)

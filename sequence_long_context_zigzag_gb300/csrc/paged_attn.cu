@@ -21,10 +21,10 @@ int check_paged_desc(const usp_paged_desc &d) {
     const int64_t row = (int64_t)d.hq * d.cache.hd;
     for (int64_t st : {d.q_stride, d.out_stride}) {
         if (st != 0 && st < row) return USP_ERR_SHAPE;
-        if (st * elem_size(d.cache.dtype) % 16 != 0) return USP_ERR_ALIGN;
         if (st >= (int64_t(1) << 38)) return USP_ERR_UNSUPPORTED;
+        if (st * elem_size(d.cache.dtype) % 16 != 0) return USP_ERR_ALIGN;
     }
-    if (d.tokens >= (int64_t(1) << 31) / d.hq) return USP_ERR_UNSUPPORTED;
+    if (d.tokens >= (int64_t(1) << 31) / d.hq || d.nreq > kMaxRequests) return USP_ERR_UNSUPPORTED;
     return USP_OK;
 }
 

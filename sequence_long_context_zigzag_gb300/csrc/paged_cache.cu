@@ -236,8 +236,8 @@ int check_cache_dims(const usp_cache_dims &d) {
     const int64_t dense = (int64_t)d.hkv * d.page_size * d.hd;
     for (int64_t st : {d.k_page_stride, d.v_page_stride}) {
         if (st != 0 && st < dense) return USP_ERR_SHAPE;
-        if (st * es % 16 != 0) return USP_ERR_ALIGN;
         if (st >= (int64_t(1) << 38)) return USP_ERR_UNSUPPORTED;  // the tensor maps' strides end at 2^40 bytes
+        if (st * es % 16 != 0) return USP_ERR_ALIGN;
     }
     return USP_OK;
 }
@@ -256,7 +256,7 @@ int usp_page_plan(const int32_t *ctx_lens, const int32_t *new_lens, const int32_
     if (!valid_page_size(d.page_size)) return USP_ERR_UNSUPPORTED;
     if (d.table_stride < d.max_pages) return USP_ERR_SHAPE;
     if (d.num_pages >= (int64_t(1) << 31) / d.page_size || d.max_tokens >= (int64_t(1) << 31) ||
-        d.free_count >= (int64_t(1) << 31))
+        d.free_count >= (int64_t(1) << 31) || d.nreq > kMaxRequests)
         return USP_ERR_UNSUPPORTED;
     // empty arrays may be null: no request, no free page, no column, no token
     if (!free_head || !cu_new || !counts || (d.nreq > 0 && (!ctx_lens || !new_lens || !kv_lens)) ||
@@ -302,6 +302,7 @@ int usp_cache_append(const void *k, const void *v, void *k_cache, void *v_cache,
     const int64_t row = (int64_t)d.hkv * d.hd;
     for (int64_t st : {k_stride, v_stride}) {
         if (st != 0 && st < row) return USP_ERR_SHAPE;
+        if (st >= (int64_t(1) << 38)) return USP_ERR_UNSUPPORTED;
         if (st * es % 16 != 0) return USP_ERR_ALIGN;
     }
     if (tokens == 0 || d.num_pages == 0) return USP_OK;

@@ -181,7 +181,8 @@ __device__ bool sched_scan(const SchedIn &s, SchedShared &sh) {
         }
         return x;
     };
-    if (tid == 0) sh.end = UnitPos{s.nreq, 0, 0, 0};
+    // (also where it begins, for sums past 64 bits: 2^13 requests that all claim the same 2^30 tokens)
+    if (tid == 0) sh.at = sh.end = UnitPos{s.nreq, 0, 0, 0};
     int64_t mine = 0, W;
     ReqUnits r{};
     for (int32_t i = tid; i < s.nreq; i += NT) {

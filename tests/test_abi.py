@@ -377,3 +377,14 @@ def test_paged_binding_rejects():
         usp.usp_page_plan(i.long(), i, i, i[:1], t, 16, 8, 4)
     with pytest.raises(ValueError, match="CUDA"):
         usp.usp_page_plan(i[:2], i[:2], i, i[:1], t, 16, 8, 4)
+
+
+def test_paged_calls_reject_what_32_bit_walks_cannot_hold():
+    lib = _abi.load()
+    nine = [GOOD + (i << 34) for i in range(9)]
+    assert lib.usp_page_plan(*nine, plan(nreq=2 ** 30 + 1), None) == _abi.USP_ERR_UNSUPPORTED
+    assert lib.usp_page_plan(*nine, plan(nreq=2 ** 31 - 1), None) == _abi.USP_ERR_UNSUPPORTED
+    assert lib.usp_paged_attn(*([GOOD] * 8), paged(nreq=2 ** 30 + 1), GOOD, 2 ** 30, None) == _abi.USP_ERR_UNSUPPORTED
+    assert lib.usp_cache_append(GOOD, GOOD, GOOD, GOOD, GOOD, 4, 2 ** 62, 0, cache(), None) == _abi.USP_ERR_UNSUPPORTED
+    assert lib.usp_cache_append(GOOD, GOOD, GOOD, GOOD, GOOD, 4, 0, 2 ** 38, cache(), None) == _abi.USP_ERR_UNSUPPORTED
+    assert lib.usp_paged_attn(*([GOOD] * 8), paged(q_stride=2 ** 62), GOOD, 2 ** 30, None) == _abi.USP_ERR_UNSUPPORTED
