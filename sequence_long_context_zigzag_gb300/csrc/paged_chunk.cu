@@ -367,39 +367,8 @@ __device__ void mma_role(const ChunkParams &p, const uint8_t *smem, uint32_t sba
     auto stage_off = [](uint32_t st) { return (uint64_t)((st * C::kTileBytes) >> 4); };
     const uint32_t tS = tmem + 128u * i, tO = tmem + 256u + (uint32_t)(HD * i);
     const int my_turn = C::TURN + i, other_turn = C::TURN + (1 - i);
-    uint32_t turns = 0, nseg = 0;
-    bool ok = true;
-    // the tiles of all segments as one stream: the next tile is kt of [kt, t1); this issuer's Q tile needs
-    // those below act_end. A segment without a tile is an element of the stream too: passed over at once, it
-    // would take the issuers up to a ring of segments ahead of the softmax warps, which wait for the O of the
-    // last tile while the ring has no place for the segment that the issuers wait for.
-    struct Tile {
-        bool have, first, act, none;  // there is one; it opens a segment; the Q tile needs it; no tile
-    };
+    // the current segment's tiles: kt of [., t1); this issuer's Q tile needs those below act_end
     int kt = 0, t1 = 0, act_end = 0;
-    auto next_tile = [&]() {
-        Tile t{true, false, false, false};
-        if (kt >= t1) {
-            SegMsg g;
-            ok = next_segment<HD>(p, smem, bar0, nseg, g);
-            if (!ok || __reduce_max_sync(0xffffffffu, g.ntok) == 0) {
-                t.have = false;
-                return t;
-            }
-            // (reductions over equal values: the compiler then knows that they are uniform)
-            kt = __reduce_max_sync(0xffffffffu, g.t0);
-            t1 = __reduce_max_sync(0xffffffffu, g.t1);
-            act_end = __reduce_max_sync(0xffffffffu, i ? g.act[1] : g.act[0]);
-            t.first = true;
-            if (kt >= t1) {
-                t.none = true;
-                return t;
-            }
-        }
-        t.act = kt < act_end;
-        ++kt;
-        return t;
-    };
     auto s_burst = [&](bool act, uint32_t st) {
         if (act) {
             issue_s<HD>(el, tS, qdesc, kdesc0 + stage_off(st));
@@ -409,67 +378,64 @@ __device__ void mma_role(const ChunkParams &p, const uint8_t *smem, uint32_t sba
     };
     uint32_t pc = 0, started = 0;  // P waits; a PV of the current segment has been issued
     uint32_t nq = 0, no = 0;       // Q loads consumed; O_i read-outs handed to the softmax
-    uint32_t j = 0;                // tiles of the stream
-    Tile cur = next_tile();
-    while (ok && cur.have && cur.none) cur = next_tile();  // nothing waits for this warp yet
-    if (ok && cur.have) {
-        ok = wait(C::Q_FULL, 0) && wait(C::K_FULL, 0);
-        nq = 1;
-        if (ok && i == 1) ok = wait(my_turn, (turns++) & 1u);
-        if (ok) {
-            s_burst(cur.act, 0);
+    uint32_t turns = 0, nseg = 0;
+    uint32_t j = 0;                // tiles of all segments
+    bool ok = true;
+    for (;;) {
+        // The next segment with a tile. All that the softmax warps need of the one before is issued by now: one
+        // taken earlier, with segments without a tile between, would take the issuers up to a ring of segments
+        // ahead of the softmax warps, which wait for the O of the last tile while the ring has no place for
+        // the segment that the issuers wait for.
+        int ntok;
+        do {
+            SegMsg g;
+            if (!(ok = next_segment<HD>(p, smem, bar0, nseg, g))) break;
+            // (reductions over equal values: the compiler then knows that they are uniform)
+            ntok = __reduce_max_sync(0xffffffffu, g.ntok);
+            kt = __reduce_max_sync(0xffffffffu, g.t0);
+            t1 = __reduce_max_sync(0xffffffffu, g.t1);
+            act_end = __reduce_max_sync(0xffffffffu, i ? g.act[1] : g.act[0]);
+        } while (ntok > 0 && kt >= t1);
+        if (!ok || ntok == 0) break;
+        if (!(ok = wait(C::Q_FULL, nq & 1u))) break;
+        ++nq;
+        if (!(ok = wait(C::K_FULL + j % C::kStages, (j / C::kStages) & 1u))) break;
+        if (j == 0 && i == 1 && !(ok = wait(my_turn, (turns++) & 1u))) break;
+        s_burst(kt < act_end, j % C::kStages);
+        if (j == 0) arrive_if(el, BAR(other_turn));
+        for (;;) {
+            const bool act = kt < act_end, last = kt + 1 >= t1;
+            const uint32_t st = j % C::kStages, ph = (j / C::kStages) & 1u;
+            const uint32_t stn = (j + 1) % C::kStages, phn = ((j + 1) / C::kStages) & 1u;
+            if (last) commit_if(el, BAR(C::Q_EMPTY));  // this issuer's S products of the segment are issued
+            if (!(ok = wait(C::V_FULL + st, ph))) break;
+            if (!last && !(ok = wait(C::K_FULL + stn, phn))) break;
+            if (act && !started && no > 0 && !(ok = wait(C::O_EMPTY + i, (no - 1) & 1u))) break;
+            if (!(ok = wait(my_turn, (turns++) & 1u))) break;
+            if (act) {
+                if (!(ok = wait(C::P_HALF + i, pc & 1u))) break;
+                tc::fence_after_sync();
+                issue_pv<HD, 0>(el, tO, tS, vdesc0 + stage_off(st), started);
+                if (!(ok = wait(C::P_FULL + i, pc & 1u))) break;
+                ++pc;
+                tc::fence_after_sync();
+                issue_pv<HD, 1>(el, tO, tS, vdesc0 + stage_off(st), 1);
+                started = 1;
+            }
+            commit_if(el, BAR(C::V_EMPTY + st));
+            ++j;
+            ++kt;
+            if (last) break;
+            s_burst(kt < act_end, stn);
             arrive_if(el, BAR(other_turn));
         }
-    }
-    while (ok && cur.have) {
-        const Tile nxt = next_tile();
         if (!ok) break;
-        const bool last = !nxt.have || nxt.first, boundary = nxt.have && nxt.first && !nxt.none;
-        const uint32_t st = j % C::kStages, ph = (j / C::kStages) & 1u;
-        const uint32_t stn = (j + 1) % C::kStages, phn = ((j + 1) / C::kStages) & 1u;
-        if (last) commit_if(el, BAR(C::Q_EMPTY));  // this issuer's S products of the segment are issued
-        if (!(ok = wait(C::V_FULL + st, ph))) break;
-        if (!last && !(ok = wait(C::K_FULL + stn, phn))) break;
-        if (cur.act && !started && no > 0 && !(ok = wait(C::O_EMPTY + i, (no - 1) & 1u))) break;
-        if (!(ok = wait(my_turn, (turns++) & 1u))) break;
-        if (cur.act && !(ok = wait(C::P_HALF + i, pc & 1u))) break;
-        if (cur.act) {
-            tc::fence_after_sync();
-            issue_pv<HD, 0>(el, tO, tS, vdesc0 + stage_off(st), started);
-            if (!(ok = wait(C::P_FULL + i, pc & 1u))) break;
-            ++pc;
-            tc::fence_after_sync();
-            issue_pv<HD, 1>(el, tO, tS, vdesc0 + stage_off(st), 1);
-            started = 1;
+        if (started) {
+            commit_if(el, BAR(C::O_FULL + i));
+            ++no;
         }
-        commit_if(el, BAR(C::V_EMPTY + st));
-        if (last) {
-            if (started) {
-                commit_if(el, BAR(C::O_FULL + i));
-                ++no;
-            }
-            started = 0;
-        } else {
-            s_burst(nxt.act, stn);
-        }
+        started = 0;
         arrive_if(el, BAR(other_turn));
-        if (boundary) {
-            if (!(ok = wait(C::Q_FULL, nq & 1u))) break;
-            ++nq;
-            if (!(ok = wait(C::K_FULL + stn, phn))) break;
-            s_burst(nxt.act, stn);
-        }
-        cur = nxt;
-        ++j;
-        // over segments without a tile, one at a time: all that the softmax warps need is issued
-        if (cur.none) {
-            while (ok && cur.have && cur.none) cur = next_tile();
-            if (!ok || !cur.have) break;
-            if (!(ok = wait(C::Q_FULL, nq & 1u))) break;
-            ++nq;
-            if (!(ok = wait(C::K_FULL + j % C::kStages, (j / C::kStages) & 1u))) break;
-            s_burst(cur.act, j % C::kStages);
-        }
     }
     if (!ok) arrive_if(el, BAR(other_turn));  // let the other issuer reach its own bounded exit
     commit_if(el, BAR(C::DONE + i));           // every MMA of this issuer ends before tensor memory is freed
