@@ -33,7 +33,10 @@
 namespace usp {
 namespace {
 
-constexpr int kOver = 64;         // a unit's constant cost, in keys
+// A unit's constant cost, in keys: its start and end take a CTA about 2.5 us, in which the other CTAs read
+// that many keys each. 256 tokens over up to 2000 keys: 64 in its place 101 us, 128 78, 192 and 256 67; 26
+// single tokens and 7 chunks 38, 34.5, 32, 31.
+constexpr int kOver = 256;
 constexpr int kMinSpan = 194;     // keys per CTA below which fewer CTAs work
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr float kRescale = 8.0f;  // log2 units
@@ -48,7 +51,7 @@ template <int HD, int RT> struct Cfg {
     static constexpr int kBoxes = HD / 64;
     static constexpr int kTile = kKT * HD * 2;  // bytes of K (or V) of one tile
     static constexpr int kStages = RT == 1 ? 3 : HD == 128 ? 3 : 5;  // 96 KB per CTA at two per SM, 160-192 KB at one
-    static_assert(kMinSpan > kOver + kKT, "a span holds more than a tile");
+    static_assert(kMinSpan > kKT, "a span holds more than a tile");
     static constexpr int kXRow = 36;            // exchange row: 32 columns + padding
     static constexpr int kXGroup = 4 * 16 * kXRow * 4;
     static constexpr int kX = kStages * 2 * kTile;

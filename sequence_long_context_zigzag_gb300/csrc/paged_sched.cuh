@@ -9,7 +9,8 @@
 // few hundred), which costs less than a planning launch and keeps the call free of host copies.
 // A unit cut by a span's end is finished by paged_combine_kernel: the CTA that opens it writes its
 // partial to its slot 1 with a header, the CTAs that continue it to their slot 0; spans are longer than
-// a tile, so a CTA has at most one of each.
+// a tile, so each of these has a tile, and a CTA has at most one of each. (A span that ends within a unit's
+// constant cost leaves the whole unit to the next one.)
 #pragma once
 
 #include "paged.cuh"
@@ -24,7 +25,7 @@ struct SchedIn {
     int32_t causal;
     int32_t n_lo, n_hi;  // the requests of this kernel: n_lo < new tokens <= n_hi
     int32_t over;        // constant cost of a unit, in keys
-    int32_t min_span;    // keys per CTA below which fewer CTAs work (more than over + a key tile)
+    int32_t min_span;    // keys per CTA below which fewer CTAs work (more than a key tile)
     float inv_ctas;      // 1 / CTAs of the launch
     FastDiv by_tb, by_G;
 };
