@@ -120,7 +120,7 @@ __device__ void walk_role(const ChunkParams &p, const SchedShared &sh, uint8_t *
     SegMsg *ring = reinterpret_cast<SegMsg *>(smem + C::kSeg);
     Sched sc;
     sched_begin<kN>(p.s, sh, sc);
-    PartHeader opened{};
+    PartHeader opened = no_part(sh);
     uint32_t tiles = 0, ntail = 0;  // tiles and tails of the segments handed out
     int tail_row = -1;              // first row to clear in the pending tail tile
     uint32_t tail_stage = 0;
@@ -168,9 +168,9 @@ __device__ void walk_role(const ChunkParams &p, const SchedShared &sh, uint8_t *
                 tail_stage = (tiles - 1) % C::kStages;
             }
         }
-        if (more && g.t0 == 0 && g.t1 < g.tiles) opened = part_header(p.s, sc, g);
+        if (more && g.t0 == 0 && g.t1 < g.tiles) opened = part_header(p.s, sh, sc, g);
     }
-    if (!ok) opened = PartHeader{};
+    if (!ok) opened = no_part(sh);
     if (lane == 0) p.w.head[blockIdx.x] = opened;
 }
 
@@ -719,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         while (!skip && next_segment<HD>(p, smem, bar0, nseg, g) && g.ntok > 0)
             if (!softmax_segment<HD>(p, g, smem, bar0, tmem, warp >> 2, ns, no)) break;
     }
-    if (skip && threadIdx.x == 0) p.w.head[blockIdx.x] = PartHeader{};
+    if (skip && threadIdx.x == 0) p.w.head[blockIdx.x] = no_part(sh);
     tc::fence_before_sync();
     __syncthreads();
     if (warp == kMmaWarp) {
@@ -780,7 +780,7 @@ int launch_paged_chunk(const PagedArgs &a, int n_lo, const PartSpace &w, cudaStr
     p.s.nreq = a.nreq; p.s.hkv = a.hkv; p.s.G = a.G;
     p.s.tb = 2 * p.tq_tokens; p.s.causal = a.causal;
     p.s.n_lo = n_lo; p.s.n_hi = INT32_MAX;
-    p.s.over = kOver; p.s.min_span = kMinSpan;
+    p.s.over = kOver; p.s.min_span = kMinSpan; p.s.long_parts = kManyParts;
     p.s.inv_ctas = 1.0f / (float)w.ctas;
     p.s.by_tb = FastDiv((uint32_t)p.s.tb); p.s.by_G = FastDiv((uint32_t)a.G);
     p.w = w;

@@ -128,7 +128,7 @@ __device__ void producer(const DecodeParams &p, const SchedShared &sh, uint8_t *
     const void *map = kv ? &p.tv : &p.tk;
     Sched sc;
     sched_begin<C::kKT>(p.s, sh, sc);
-    PartHeader opened{};
+    PartHeader opened = no_part(sh);
     uint32_t fill = 0, nseg = 0;
     bool ok = true, more = true;
     while (more) {
@@ -168,10 +168,10 @@ __device__ void producer(const DecodeParams &p, const SchedShared &sh, uint8_t *
             page = next;
         }
         if (!ok) break;
-        if (g.t0 == 0 && g.t1 < g.tiles) opened = part_header(p.s, sc, g);
+        if (g.t0 == 0 && g.t1 < g.tiles) opened = part_header(p.s, sh, sc, g);
     }
     if (!ok) {  // drain (bounded): no copy may land after the CTA has gone
-        opened = PartHeader{};
+        opened = no_part(sh);
         for (uint32_t f = fill > C::kStages ? fill - C::kStages : 0; f < fill; ++f)
             wait(C::FULL + f % C::kStages, (f / C::kStages) & 1u);
     }
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(Cfg<HD, RT>::kThreads, RT == 1 ? 2 : 1)
     const bool work = sched_scan<C::kThreads, C::kKT>(p.s, sh);
     __syncthreads();
     if (!work || skip) {
-        if (threadIdx.x == 0) p.w.head[blockIdx.x] = PartHeader{};
+        if (threadIdx.x == 0) p.w.head[blockIdx.x] = no_part(sh);
     } else if ((threadIdx.x >> 5) == C::kConsumers) {
         producer<HD, RT>(p, sh, smem, sbase);
     } else {
@@ -451,94 +451,201 @@ __global__ void __launch_bounds__(Cfg<HD, RT>::kThreads, RT == 1 ? 2 : 1)
 // ------------------------------------------------------------------------------------------------
 // combine: out and lse of the units that spans cut
 // ------------------------------------------------------------------------------------------------
-// A thread computes 4 columns of a row over all parts of its unit: o = sum_i 2^(m_i - M) o_i / l, online,
-// in the parts' order, so the result does not depend on timing. Bound by latency (the header, then the
-// parts), so a thread fetches the maxima, sums and rows of 8 (row, part) pairs at once: 8 parts of a row in
-// the few-row kernels' units, which long sequences cut into many, 2 parts of 4 rows in the others' (prompts
-// of 16334 tokens: 16 us with a row at a time). A part whose rows saw nothing has m = -inf, and its o
-// (perhaps unwritten) is not used; a NaN score leaves l NaN, which is kept. Small CTAs: some fit beside the decode kernel's and are in place when it
-// ends.
+// o = sum_i 2^(m_i - M) o_i / l over a row's parts, online, in an order that depends on their number alone, so the
+// result does not depend on timing. A group of threads, 4 columns each, holds a row. What bounds it is
+// latency: the header, then the parts, so a group fetches 8 (row, part) pairs at once: 8 parts of a row in
+// the few-row kernels' units, 2 parts of 4 rows in the others' (prompts of 16334 tokens: 16 us with a row at a
+// time).
+// A CTA takes 16 rows of the unit that one header names. Units of many parts (a long sequence with few KV heads:
+// up to 304) would leave that to a few CTAs, round after round: where the headers say that there are any, all
+// CTAs then read all headers and share these units' rows evenly, and the groups of a CTA share a row's parts
+// and join through shared memory. One token over 100000 keys, 16 heads on one KV head: 125 us a call with the first
+// way alone, 28 with both; 32 tokens of 8 heads 69, 36.
+// A part whose rows saw nothing has m = -inf, and its o (perhaps unwritten) is not used; a NaN score leaves l
+// NaN, which is kept. Small CTAs: some fit beside the decode kernel's and are in place when it ends.
 constexpr int kCombineThreads = 128;
-constexpr int kCombineRows = 16;  // rows per CTA
+constexpr int kCombineRows = 16;  // rows of a header's unit per CTA
+constexpr int kHeadersPer = 4;    // headers per thread
+constexpr int kMaxHeaders = kCombineThreads * kHeadersPer;
+constexpr int kRowCost = 4;       // a row's constant cost, in parts
+constexpr int kSharing = 608;     // CTAs that share the long units: all that run at once
 
-template <typename T, int HD, int NR, int NP>  // rows and parts fetched at once
-__device__ __forceinline__ void combine_rows(const CombineArgs &a, const PartSpace &w, int c, int r0) {
+// the running combination of a row's parts, 4 columns
+struct RowSum {
+    float M, L;
+    float4 acc;
+    __device__ __forceinline__ void clear() {
+        M = -INFINITY;
+        L = 0.f;
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    __device__ __forceinline__ void rescale(float to, float base) {  // base: to, or 0 for -inf
+        const float g = tc::ex2(M - base);
+        M = to;
+        L *= g;
+        acc.x *= g; acc.y *= g; acc.z *= g; acc.w *= g;
+    }
+    __device__ __forceinline__ void add(float m, float l, const float4 &o, float base) {
+        const float g = tc::ex2(m - base);
+        if (g > 0.f || l != l) {
+            L = fmaf(g, l, L);
+            acc.x = fmaf(g, o.x, acc.x);
+            acc.y = fmaf(g, o.y, acc.y);
+            acc.z = fmaf(g, o.z, acc.z);
+            acc.w = fmaf(g, o.w, acc.w);
+        }
+    }
+};
+
+// The partials of one unit, as a group's thread sees them (its columns start at col).
+struct Parts {
+    const float *open, *cont;  // part 0; parts 1, 2, ... a CTA's slots apart
+    size_t step;
+    int32_t cap, hd, col;      // rows of a slot; head dim
+    __device__ __forceinline__ Parts(const PartSpace &w, int hd_, int c, int col_)
+        : open(part_slot(w, hd_, c, 1)), cont(part_slot(w, hd_, c + 1, 0)), step(2 * (size_t)w.rows * (hd_ + 2)),
+          cap(w.rows), hd(hd_), col(col_) {}
+    // parts [base, base + NP) of the rows first, first + row_step, ..., below `end`, into sum[NR]
+    template <int NR, int NP>
+    __device__ __forceinline__ void fold(int first, int row_step, int end, int base, int parts, RowSum (&sum)[NR]) const {
+        float m[NR][NP], l[NR][NP];
+        float4 o[NR][NP];
+#pragma unroll
+        for (int j = 0; j < NR; ++j)
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                const int r = first + j * row_step;
+                m[j][i] = -INFINITY;
+                l[j][i] = 0.f;
+                o[j][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (base + i < parts && r < end) {
+                    const float *s = base + i == 0 ? open : cont + (base + i - 1) * step;
+                    m[j][i] = s[(size_t)cap * hd + r];
+                    l[j][i] = s[(size_t)cap * (hd + 1) + r];
+                    o[j][i] = *reinterpret_cast<const float4 *>(s + (size_t)r * hd + col);
+                }
+            }
+#pragma unroll
+        for (int j = 0; j < NR; ++j) {
+            float mx = sum[j].M;
+#pragma unroll
+            for (int i = 0; i < NP; ++i) mx = fmaxf(mx, m[j][i]);
+            const float mb = mx == -INFINITY ? 0.f : mx;
+            sum[j].rescale(mx, mb);
+#pragma unroll
+            for (int i = 0; i < NP; ++i) sum[j].add(m[j][i], l[j][i], o[j][i], mb);
+        }
+    }
+};
+
+template <typename T, int HD>
+__device__ __forceinline__ void write_row(const CombineArgs &a, const PartHeader &h, int r, int col, const RowSum &x) {
     constexpr bool kExact = sizeof(T) == 4;  // log2f for the fp32 path
-    constexpr int kStep = kCombineThreads / (HD / 4);
-    const int col = (int)threadIdx.x % (HD / 4) * 4, row = r0 + (int)threadIdx.x / (HD / 4);
-    const PartHeader h = w.head[c];
-    const int parts = h.last - c + 1, end = min(r0 + kCombineRows, h.rows);
-    const size_t step = 2 * (size_t)w.rows * (HD + 2);  // from a CTA's slot to the next CTA's
-    const float *cont = part_slot(w, HD, c + 1, 0);       // parts 1, 2, ...
-    const float *open = part_slot(w, HD, c, 1);           // part 0
-    for (int first = row; first < end; first += NR * kStep) {
-        float M[NR], L[NR];
-        float4 acc[NR];
+    const float inv = x.L == 0.f ? 0.f : 1.f / x.L;
+    uint32_t tok, hr;
+    a.by_G.divmod((uint32_t)r, tok, hr);
+    const int head = h.head * a.G + (int)hr;
+    T *to = static_cast<T *>(a.out) + (h.tok0 + tok) * a.out_stride + (int64_t)head * HD + col;
+    if constexpr (kExact)
+        *reinterpret_cast<float4 *>(to) = make_float4(x.acc.x * inv, x.acc.y * inv, x.acc.z * inv, x.acc.w * inv);
+    else
+        *reinterpret_cast<uint2 *>(to) =
+            make_uint2(float2_to_bf16x2(x.acc.x * inv, x.acc.y * inv), float2_to_bf16x2(x.acc.z * inv, x.acc.w * inv));
+    if (col == 0)
+        a.lse[(h.tok0 + tok) * a.hq + head] =
+            x.L == 0.f ? -INFINITY : (x.M + (kExact ? log2f(x.L) : __log2f(x.L))) * kLn2;
+}
+
+// the rows [r0, end) of the unit that header c names, NR rows and NP parts at a time
+template <typename T, int HD, int NR, int NP>
+__device__ __forceinline__ void combine_rows(const CombineArgs &a, const Parts &p, const PartHeader &h, int parts, int r0,
+                                             int end) {
+    constexpr int kGroups = kCombineThreads / (HD / 4);
+    for (int first = r0 + (int)threadIdx.x / (HD / 4); first < end; first += NR * kGroups) {
+        RowSum x[NR];
 #pragma unroll
-        for (int j = 0; j < NR; ++j) {
-            M[j] = -INFINITY;
-            L[j] = 0.f;
-            acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int j = 0; j < NR; ++j) x[j].clear();
+        for (int base = 0; base < parts; base += NP) p.fold<NR, NP>(first, kGroups, end, base, parts, x);
+#pragma unroll
+        for (int j = 0; j < NR; ++j)
+            if (first + j * kGroups < end) write_row<T, HD>(a, h, first + j * kGroups, p.col, x[j]);
+    }
+}
+
+// CTA x of `ctas`: its share of the rows of all units of more than `limit` parts
+template <typename T, int HD>
+__device__ void combine_long(const CombineArgs &a, const PartSpace &w, int limit, int x, int ctas) {
+    constexpr int kLanes = HD / 4, kGroups = kCombineThreads / kLanes;
+    __shared__ int32_t before[kMaxHeaders + 1];  // cost of the rows before each header's
+    __shared__ int32_t warp_sum[kCombineThreads / 32];
+    __shared__ float4 xo[kGroups][kLanes];
+    __shared__ float2 xml[kGroups];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int32_t cost[kHeadersPer], mine = 0;
+#pragma unroll
+    for (int e = 0; e < kHeadersPer; ++e) {
+        const int c = tid * kHeadersPer + e;
+        cost[e] = 0;
+        if (c < w.ctas) {
+            const int4 h = *reinterpret_cast<const int4 *>(w.head + c);  // rows, head, last
+            if (h.x > 0 && h.z - c + 1 > limit) cost[e] = h.x * (h.z - c + 1 + kRowCost);
         }
-        for (int base = 0; base < parts; base += NP) {
-            float m[NR][NP], l[NR][NP];
-            float4 o[NR][NP];
+        mine += cost[e];
+    }
+    int32_t incl = mine;
 #pragma unroll
-            for (int j = 0; j < NR; ++j)
+    for (int d = 1; d < 32; d <<= 1) {
+        const int32_t y = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += y;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int32_t all = 0, at = incl - mine;
 #pragma unroll
-                for (int i = 0; i < NP; ++i) {
-                    const int r = first + j * kStep;
-                    m[j][i] = -INFINITY;
-                    l[j][i] = 0.f;
-                    o[j][i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (base + i < parts && r < end) {
-                        const float *s = base + i == 0 ? open : cont + (base + i - 1) * step;
-                        m[j][i] = s[(size_t)w.rows * HD + r];
-                        l[j][i] = s[(size_t)w.rows * (HD + 1) + r];
-                        o[j][i] = *reinterpret_cast<const float4 *>(s + (size_t)r * HD + col);
-                    }
-                }
+    for (int i = 0; i < kCombineThreads / 32; ++i) {
+        if (i < warp) at += warp_sum[i];
+        all += warp_sum[i];
+    }
 #pragma unroll
-            for (int j = 0; j < NR; ++j) {
-                float mx = M[j];
+    for (int e = 0; e < kHeadersPer; ++e) {
+        before[tid * kHeadersPer + e] = at;
+        at += cost[e];
+    }
+    if (tid == 0) before[kMaxHeaders] = all;
+    __syncthreads();
+    const int32_t share = (all + ctas - 1) / ctas, x0 = x * share, x1 = min(x0 + share, all);
+    if (x0 >= all) return;
+    int c = 0;  // the last header that begins at or before x0
 #pragma unroll
-                for (int i = 0; i < NP; ++i) mx = fmaxf(mx, m[j][i]);
-                const float mb = mx == -INFINITY ? 0.f : mx, g0 = tc::ex2(M[j] - mb);
-                M[j] = mx;
-                L[j] *= g0;
-                acc[j].x *= g0; acc[j].y *= g0; acc[j].z *= g0; acc[j].w *= g0;
+    for (int d = kMaxHeaders / 2; d > 0; d >>= 1)
+        if (before[c + d] <= x0) c += d;
+    const int group = tid / kLanes, in_group = tid % kLanes;
+    for (; c < w.ctas && before[c] < x1; ++c) {
+        if (before[c + 1] == before[c]) continue;
+        const PartHeader h = w.head[c];
+        const int parts = h.last - c + 1;
+        // the rows whose cost begins in this CTA's share
+        const int32_t per = parts + kRowCost;
+        const int r0 = max(0, (x0 - before[c] + per - 1) / per), r1 = min(h.rows, (x1 - before[c] + per - 1) / per);
+        const Parts p(w, HD, c, in_group * 4);
+        for (int r = r0; r < r1; ++r) {
+            RowSum x[1];
+            x[0].clear();
+            for (int base = group * 8; base < parts; base += kGroups * 8) p.fold<1, 8>(r, 0, r1, base, parts, x);
+            xo[group][in_group] = x[0].acc;
+            if (in_group == 0) xml[group] = make_float2(x[0].M, x[0].L);
+            __syncthreads();
+            if (group == 0) {
+                float mx = x[0].M;
 #pragma unroll
-                for (int i = 0; i < NP; ++i) {
-                    const float g = tc::ex2(m[j][i] - mb);
-                    if (g > 0.f || l[j][i] != l[j][i]) {
-                        L[j] = fmaf(g, l[j][i], L[j]);
-                        acc[j].x = fmaf(g, o[j][i].x, acc[j].x);
-                        acc[j].y = fmaf(g, o[j][i].y, acc[j].y);
-                        acc[j].z = fmaf(g, o[j][i].z, acc[j].z);
-                        acc[j].w = fmaf(g, o[j][i].w, acc[j].w);
-                    }
-                }
+                for (int g = 1; g < kGroups; ++g) mx = fmaxf(mx, xml[g].x);
+                const float mb = mx == -INFINITY ? 0.f : mx;
+                x[0].rescale(mx, mb);
+#pragma unroll
+                for (int g = 1; g < kGroups; ++g) x[0].add(xml[g].x, xml[g].y, xo[g][in_group], mb);
+                write_row<T, HD>(a, h, r, p.col, x[0]);
             }
-        }
-#pragma unroll
-        for (int j = 0; j < NR; ++j) {
-            const int r = first + j * kStep;
-            if (r >= end) break;
-            const float inv = L[j] == 0.f ? 0.f : 1.f / L[j];
-            uint32_t tok, hr;
-            a.by_G.divmod((uint32_t)r, tok, hr);
-            const int head = h.head * a.G + (int)hr;
-            T *to = static_cast<T *>(a.out) + (h.tok0 + tok) * a.out_stride + (int64_t)head * HD + col;
-            if constexpr (kExact) {
-                *reinterpret_cast<float4 *>(to) =
-                    make_float4(acc[j].x * inv, acc[j].y * inv, acc[j].z * inv, acc[j].w * inv);
-            } else {
-                *reinterpret_cast<uint2 *>(to) = make_uint2(float2_to_bf16x2(acc[j].x * inv, acc[j].y * inv),
-                                                            float2_to_bf16x2(acc[j].z * inv, acc[j].w * inv));
-            }
-            if (col == 0)
-                a.lse[(h.tok0 + tok) * a.hq + head] =
-                    L[j] == 0.f ? -INFINITY : (M[j] + (kExact ? log2f(L[j]) : __log2f(L[j]))) * kLn2;
+            __syncthreads();
         }
     }
 }
@@ -548,9 +655,20 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Co
     wait_grid_before();
     const int per0 = (a.w[0].rows + kCombineRows - 1) / kCombineRows;
     const int per1 = (a.w[1].rows + kCombineRows - 1) / kCombineRows;
-    const int x = (int)blockIdx.x - a.w[0].ctas * per0;
-    if (x < 0) combine_rows<T, HD, 4, 2>(a, a.w[0], (int)blockIdx.x / per0, (int)blockIdx.x % per0 * kCombineRows);
-    else combine_rows<T, HD, 1, 8>(a, a.w[1], x / per1, x % per1 * kCombineRows);
+    const int n0 = a.w[0].ctas * per0, n1 = a.w[1].ctas * per1;
+    const bool many = (int)blockIdx.x < n0;
+    const PartSpace &w = many ? a.w[0] : a.w[1];
+    const int x = many ? (int)blockIdx.x : (int)blockIdx.x - n0, per = many ? per0 : per1;
+    const int limit = many ? kManyParts : kFewParts, c = x / per, r0 = x % per * kCombineRows;
+    const PartHeader h = w.head[c];
+    const int parts = h.last - c + 1, end = min(r0 + kCombineRows, h.rows);
+    if (r0 < end && parts <= limit) {
+        const Parts p(w, HD, c, (int)threadIdx.x % (HD / 4) * 4);
+        if (many) combine_rows<T, HD, 4, 2>(a, p, h, parts, r0, end);
+        else combine_rows<T, HD, 1, 8>(a, p, h, parts, r0, end);
+    }
+    const int sharing = min(many ? n0 : n1, kSharing);
+    if (h.any_long && x < sharing) combine_long<T, HD>(a, w, limit, x, sharing);
 }
 
 template <int HD, int RT>
@@ -594,7 +712,7 @@ int launch_paged_decode(const PagedArgs &a, int rows, int n_hi, bool second, con
     p.s.nreq = a.nreq; p.s.hkv = a.hkv; p.s.G = a.G;
     p.s.tb = rows / a.G; p.s.causal = a.causal;
     p.s.n_lo = 0; p.s.n_hi = n_hi;
-    p.s.over = kOver; p.s.min_span = kMinSpan;
+    p.s.over = kOver; p.s.min_span = kMinSpan; p.s.long_parts = kFewParts;
     p.s.inv_ctas = 1.0f / (float)w.ctas;
     p.s.by_tb = FastDiv((uint32_t)p.s.tb); p.s.by_G = FastDiv((uint32_t)a.G);
     p.w = w;
@@ -613,6 +731,7 @@ int launch_paged_decode(const PagedArgs &a, int rows, int n_hi, bool second, con
 }
 
 int launch_paged_combine(const CombineArgs &a, int hd, int dtype, cudaStream_t s) {
+    if (std::max(a.w[0].ctas, a.w[1].ctas) > kMaxHeaders) return USP_ERR_UNSUPPORTED;
     const int per = kCombineRows;
     const dim3 grid((unsigned)(a.w[0].ctas * ((a.w[0].rows + per - 1) / per) + a.w[1].ctas * ((a.w[1].rows + per - 1) / per)));
     auto go = [&](auto kernel) { return launch_overlapped(kernel, grid, kCombineThreads, 0, s, a); };

@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_f32_few_kernel(const __g
         for (;;) {
             if (tid == 0) {
                 if (!sched_next<kFewKT>(p.s, sc, seg)) seg.ntok = 0;
-                else if (seg.t0 == 0 && seg.t1 < seg.tiles) opened = part_header(p.s, sc, seg);
+                else if (seg.t0 == 0 && seg.t1 < seg.tiles) opened = part_header(p.s, sh, sc, seg);
             }
             __syncthreads();
             const Segment g = seg;
@@ -219,7 +219,11 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_f32_few_kernel(const __g
             }
         }
     }
-    if (tid == 0) p.w.head[blockIdx.x] = opened;
+    __syncthreads();  // sh.any_long, also where this CTA has no work
+    if (tid == 0) {
+        opened.any_long = sh.any_long;
+        p.w.head[blockIdx.x] = opened;
+    }
     end_in_order(p.second);
 }
 
@@ -274,7 +278,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) paged_f32_many_kernel(const _
         for (;;) {
             if (tid == 0) {
                 if (!sched_next<kManyKT>(p.s, sc, seg)) seg.ntok = 0;
-                else if (seg.t0 == 0 && seg.t1 < seg.tiles) opened = part_header(p.s, sc, seg);
+                else if (seg.t0 == 0 && seg.t1 < seg.tiles) opened = part_header(p.s, sh, sc, seg);
             }
             __syncthreads();
             const Segment g = seg;
@@ -459,7 +463,11 @@ __global__ void __launch_bounds__(kManyThreads, 1) paged_f32_many_kernel(const _
             }
         }
     }
-    if (tid == 0) p.w.head[blockIdx.x] = opened;
+    __syncthreads();  // sh.any_long, also where this CTA has no work
+    if (tid == 0) {
+        opened.any_long = sh.any_long;
+        p.w.head[blockIdx.x] = opened;
+    }
 }
 
 template <int HD>
@@ -499,6 +507,7 @@ int launch_paged_f32(const PagedArgs &a, bool many, int n_lo, int n_hi, bool sec
     p.s.tb = f32_rows(many) / a.G; p.s.causal = a.causal;
     p.s.n_lo = n_lo; p.s.n_hi = n_hi;
     p.s.over = many ? kManyOver : kFewOver;
+    p.s.long_parts = many ? kManyParts : kFewParts;
     p.s.min_span = many ? kManyMinSpan : kFewMinSpan;
     p.s.inv_ctas = 1.0f / (float)w.ctas;
     p.s.by_tb = FastDiv((uint32_t)p.s.tb); p.s.by_G = FastDiv((uint32_t)a.G);

@@ -26,6 +26,7 @@ struct SchedIn {
     int32_t n_lo, n_hi;  // the requests of this kernel: n_lo < new tokens <= n_hi
     int32_t over;        // constant cost of a unit, in keys
     int32_t min_span;    // keys per CTA below which fewer CTAs work (more than a key tile)
+    int32_t long_parts;  // parts of a unit above which the combine shares it out (kManyParts, kFewParts)
     float inv_ctas;      // 1 / CTAs of the launch
     FastDiv by_tb, by_G;
 };
@@ -73,6 +74,7 @@ struct SchedShared {
     ReqUnits r;       // the request of `at`
     int64_t before;   // cost before that request
     int64_t span;
+    int32_t any_long;  // some unit may have more than long_parts parts
 };
 
 // One stretch of a unit's key tiles [t0, t1), of `tiles` in all, that this CTA computes.
@@ -183,18 +185,25 @@ __device__ bool sched_scan(const SchedIn &s, SchedShared &sh) {
         return x;
     };
     // (also where it begins, for sums past 64 bits: 2^13 requests that all claim the same 2^30 tokens)
-    if (tid == 0) sh.at = sh.end = UnitPos{s.nreq, 0, 0, 0};
+    if (tid == 0) {
+        sh.at = sh.end = UnitPos{s.nreq, 0, 0, 0};
+        sh.any_long = 0;
+    }
     int64_t mine = 0, W;
+    int32_t longest = 0;  // keys
     ReqUnits r{};
     for (int32_t i = tid; i < s.nreq; i += NT) {
         r = req_units(s, i);
         mine += r.head_cost * s.hkv;
+        if (r.n > 0) longest = max(longest, r.kv);
     }
     int64_t incl = scan(mine, W);
     // one length for all spans; the factor covers the estimate's roundings, so that they cover W
     const int64_t span = max((int64_t)s.min_span, (int64_t)((float)W * s.inv_ctas * 1.000001f) + 1);
     const int64_t x0 = blockIdx.x * span, x1 = x0 + span;
     if (tid == 0) sh.span = span;
+    // a unit of cost u has at most u / span + 2 parts
+    if (longest + s.over > (s.long_parts - 2) * span) sh.any_long = 1;
     if (x0 >= W) return false;
     int64_t carry = 0;
     for (int32_t base = 0; base < s.nreq; base += NT) {
@@ -269,18 +278,26 @@ struct SegMsg {
 static_assert(sizeof(SegMsg) == 64, "four 16-byte words");
 
 // What the CTA that opens a unit and does not finish it leaves for the combine.
-struct PartHeader {
-    int64_t tok0;
+struct __align__(16) PartHeader {
     int32_t rows;  // valid rows (ntok * G); 0: this CTA opens no cut unit
     int32_t head;
     int32_t last;  // the CTA that finishes the unit
-    int32_t pad[3];
+    int32_t any_long;  // a unit of the call may have more than long_parts parts
+    int64_t tok0, pad;
 };
+static_assert(sizeof(PartHeader) == 32, "two 16-byte words");
+
+__device__ __forceinline__ PartHeader no_part(const SchedShared &sh) {
+    PartHeader h{};
+    h.any_long = sh.any_long;
+    return h;
+}
 
 // The header of the segment just returned, with t0 == 0 and t1 < tiles: the last one in the order of
 // the units, so `o` still holds its request.
-__device__ __forceinline__ PartHeader part_header(const SchedIn &s, const Sched &o, const Segment &g) {
-    PartHeader h{};
+__device__ __forceinline__ PartHeader part_header(const SchedIn &s, const SchedShared &sh, const Sched &o,
+                                                   const Segment &g) {
+    PartHeader h = no_part(sh);
     h.tok0 = g.tok0;
     h.rows = g.ntok * s.G;
     h.head = g.head;
@@ -289,6 +306,9 @@ __device__ __forceinline__ PartHeader part_header(const SchedIn &s, const Sched 
     h.last = div_small(end - 1, o.span);  // fewer than 2^16 CTAs
     return h;
 }
+
+// parts of a unit up to which the combine leaves its rows to one CTA each 16: units of many rows, of few
+constexpr int kManyParts = 16, kFewParts = 40;
 
 // ---- partials: per CTA two slots of `rows` rows: o (rows x hd, relative to the maximum m), m, l ------
 struct PartSpace {

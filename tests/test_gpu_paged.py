@@ -214,6 +214,17 @@ def test_attention_peaked_and_large_scores():
 
 
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("hq,hkv,hd", [(8, 1, 128), (5, 1, 64), (6, 2, 64)])
+@pytest.mark.parametrize("reqs", [[(60000, 1)], [(30, 1), (25000, 1), (27000, 2), (7, 0), (100, 1)], [(25000, 37), (300, 1)]],
+                         ids=["one", "some", "chunk"])
+def test_attention_units_of_many_parts(reqs, hq, hkv, hd, dt):
+    """Long sequences with few KV heads: a row's keys lie over most of the GPU, in up to 304 parts."""
+    c = Cache(reqs, hq, hkv, hd, 64, dt, seed=10)
+    out, lse = attend(c, max_new=c.max_new)
+    check_attention(c, out, lse)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("reqs", [[(200, 2000)], [(300, 40)] + [(0, 40)] * 30 + [(300, 40)], [(0, 90)] * 9,
                                   [(1, 500), (900, 40), (2, 700), (0, 50), (40, 1)]],
                          ids=["one-request", "between", "only", "mixed"])
