@@ -55,12 +55,15 @@ struct Route {
     int split;  // the most new tokens of a request that the kernel for few rows takes
 };
 
-// Up to 32 rows of a KV head (bf16; 16 in fp32) a call is bound by reading the cache, and the kernels for
-// few rows read it at the HBM rate; above, their re-reading of K/V per unit costs more than the others' idle rows.
+// bf16: up to 32 rows of a KV head a call is bound by reading the cache, and the kernel for few rows reads it
+// at the HBM rate; above, its re-reading of K/V per unit costs more than the other one's idle rows. fp32: the
+// kernel for few rows computes 17 (hd 64) to 25 TFLOP/s at any number of rows, the other one 47 at 128 rows and
+// a row's share of that below (40000 keys, 4 requests: 32 rows of 128 829 against 1785 us, 64 1577 against 1788;
+// 40 rows of 64 741 against 866, 48 883 against 865).
 Route route(const usp_paged_desc &d, int sms) {
     Route r{};
     const bool bf16 = d.cache.dtype == USP_BF16;
-    const int G = d.hq / d.cache.hkv, most = bf16 ? 32 : 16;
+    const int G = d.hq / d.cache.hkv, most = bf16 ? 32 : d.cache.hd == 128 ? 64 : 40;
     const int64_t rows = G * (int64_t)std::max(1, d.max_new);
     r.split = INT_MAX;
     if (rows > most || G > (bf16 ? 32 : f32_rows(false))) {
@@ -68,7 +71,7 @@ Route route(const usp_paged_desc &d, int sms) {
         r.many_rows = bf16 ? kChunkRows : f32_rows(true);
         // beside chunks, the few-row requests are mostly single tokens: the 16-row kernel (two CTAs per SM)
         // takes those, the other one all chunks (33 requests, 26 of one token: 49 -> 40 us)
-        r.split = G > (bf16 ? 32 : f32_rows(false)) ? 0 : (G <= 16 ? 16 : most) / G;
+        r.split = G > (bf16 ? 32 : f32_rows(false)) ? 0 : (bf16 && G <= 16 ? 16 : most) / G;
     }
     if (r.split > 0) {
         r.few_rows = bf16 ? (std::min<int64_t>(rows, (int64_t)r.split * G) <= 16 ? 16 : 32) : f32_rows(false);
