@@ -16,7 +16,8 @@ namespace {
 // places are exclusive prefix sums over the requests. Every CTA owns a slice of the slot map and walks
 // the requests in tiles of kTile with a running carry of both sums until its slice is done, so one
 // launch suffices: repeating the scan costs less than a second launch or a grid-wide wait (64 to 1024
-// requests are one tile, about a microsecond, and the lengths come from L2). A token finds its request
+// requests are one tile, about a microsecond, and the lengths come from L2). 64 requests 6.2 us, 256 with 272576
+// slots 8.3, of which the launch, the two dependent loads and the scan are 6. A token finds its request
 // by binary search in the tile's cumulative lengths in shared memory. A fresh page always begins with
 // a new token of its request (position % ps == 0), so that token's thread writes the table entry.
 // Sums are 64-bit; what is written saturates.
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
 // A pure copy, bound by HBM: 16-byte pieces, kUnroll of K and V each in flight per thread. A token's
 // hkv * hd elements are contiguous in the source and go to hkv runs of hd elements in its page. A CTA takes
 // consecutive pieces, so that the accesses in flight lie close together: 73055 tokens of 8 heads of 128
-// (599 MB) in 91 us, 0.98 of the measured copy rate; with strides of the whole grid between a thread's
+// (599 MB) in 87 us, 1.03 of the measured copy rate; with strides of the whole grid between a thread's
 // pieces 105 us. More pieces per thread gain nothing and cost a small call CTAs.
 constexpr int kAppendThreads = 256;
 constexpr int kUnroll = 2;

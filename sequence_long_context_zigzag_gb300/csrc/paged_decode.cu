@@ -18,6 +18,10 @@
 //    (mma.sync: at 16 rows a product uses an eighth of a tcgen05 tile, and the rate needed is far below
 //    the legacy pipe's); P goes from S's registers straight into the next product;
 //  - the four states merge through shared memory at a unit's end.
+// Measured, a whole call with the combine (8 KV heads of 128, 4 query heads each, L2 cold): 64 requests of 2000 to
+// 16384 keys (1.59 GB) 234 us and 2 of 200000 to 262143 (1.93 GB) 281 us, 1.02 and 1.03 of the measured copy rate; 64
+// of 8000 keys at hd 64 162 us, 0.97; 4 of 300 to 1024 keys 11 us, where 7 are the start (instructions, lengths, table,
+// keys, one after the other) and 2 to 3 the combine.
 // Rows behind the request's last key may hold NaN: scores are replaced, and V's registers of such keys
 // are cleared, since 0 x NaN would spread.
 #include <cuda_bf16.h>
