@@ -68,7 +68,10 @@ template <int HD> struct Cfg {
     static constexpr int kQ = 0;
     static constexpr int kK = kQ + 2 * kTileBytes;
     static constexpr int kV = kK + kStages * kTileBytes;
-    static constexpr int kBar = kV + kStages * kTileBytes;
+    // a staging slot per softmax warp for its stores: 32 rows x 128 bytes (1024-byte aligned: a swizzled box)
+    static constexpr int kStgSlot = 32 * 128;
+    static constexpr int kStg = kV + kStages * kTileBytes;
+    static constexpr int kBar = kStg + kSoftmaxWarps * kStgSlot;
     static constexpr int Q_FULL = 0;
     static constexpr int K_FULL = 1;
     static constexpr int K_EMPTY = K_FULL + kStages;
@@ -88,10 +91,7 @@ template <int HD> struct Cfg {
     static constexpr int kNumBars = P_HALF + 2;
     static constexpr int kSlot = kBar + (kNumBars * 8 + 15) / 16 * 16;  // tensor memory address, skip flag
     static constexpr int kSeg = kSlot + 16;
-    // a staging slot per softmax warp for its stores: 32 rows x 128 bytes
-    static constexpr int kStgSlot = 32 * 128;
-    static constexpr int kStg = kSeg + kSegSlots * (int)sizeof(SegMsg);
-    static constexpr int kSmem = kStg + kSoftmaxWarps * kStgSlot + 1024;  // + slack for the alignment
+    static constexpr int kSmem = kSeg + kSegSlots * (int)sizeof(SegMsg) + 1024;  // + slack for the alignment
 };
 
 struct ChunkParams {
@@ -106,6 +106,7 @@ struct ChunkParams {
     int32_t num_pages, log_ps, hq;
     int32_t tq_tokens;  // tokens per Q tile
     float scale_log2;
+    CUtensorMap to;  // of the launches with boxes
 };
 
 // does key tile t hold rows behind the request's last key? (only a unit's last tile can)
@@ -459,7 +460,7 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
 
 // One segment of the softmax of Q tile i; ns (S tiles) and no (O read-outs) run on across segments. False after
 // a failed wait (the whole warp leaves; the others' waits end by the recorded status).
-template <int HD>
+template <int HD, bool kBox>  // kBox: whole warps of rows of out are stored as boxes
 __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegMsg &g, uint8_t *smem, uint32_t bar0,
                                                 uint32_t tmem, int i, uint32_t &ns, uint32_t &no) {
     using C = Cfg<HD>;
@@ -586,8 +587,8 @@ __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegM
         ++no;
         tc::fence_after_sync();
         // A lane holds a row, and rows lie apart in memory: 128 bytes of each of the 32 rows go through the
-        // warp's staging slot, 16-byte pieces swizzled by row % 8 against bank conflicts, so that a store
-        // instruction writes four whole lines instead of 32 scattered pieces.
+        // warp's staging slot, 16-byte pieces swizzled by row % 8 against bank conflicts. A TMA box of out takes the
+        // slot, or the lanes write it, four whole lines per instruction (see launch_paged_chunk).
         const uint32_t stg = tc::smem_u32(smem) + C::kStg + warp * C::kStgSlot;
         const int sub = lane >> 3, pc = lane & 7;  // row of 4 and piece of 8 that this lane stores
         const uint64_t mine = !row_ok ? 0
@@ -607,6 +608,11 @@ __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegM
             }
             __syncwarp();
         };
+        const bool box = kBox && whole && __all_sync(0xffffffffu, row_ok);
+        if constexpr (kBox) {
+            if (lane == 0) tma_stores_read();  // the unit before may have left one
+            __syncwarp();
+        }
 #pragma unroll 1
         for (uint32_t c = 0; c < HD / 64; ++c) {
             uint32_t o[2][32];
@@ -614,6 +620,10 @@ __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegM
             tc::tmem_ld32(tO + c * 64 + 32, o[1]);
             tc::tmem_ld_wait();
             if (whole) {
+                if (c > 0 && box) {
+                    if (lane == 0) tma_stores_read();
+                    __syncwarp();
+                }
 #pragma unroll
                 for (int c8 = 0; c8 < 8; ++c8) {
                     uint32_t w[4];
@@ -623,7 +633,13 @@ __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegM
                                                 u2f(o[c8 / 4][c8 % 4 * 8 + 2 * e + 1]) * inv);
                     stage_in(c8, w[0], w[1], w[2], w[3]);
                 }
-                stage_out(c * 128);
+                if (box) {
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) tma_store_3d(&p.to, (int32_t)c * 64, head, (int32_t)(g.tok0 + tok), stg);
+                } else {
+                    stage_out(c * 128);
+                }
             } else {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -652,7 +668,7 @@ __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegM
     return true;
 }
 
-template <int HD>
+template <int HD, bool kBox>
 __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_constant__ ChunkParams p) {
     using C = Cfg<HD>;
     extern __shared__ uint8_t smem_raw[];
@@ -721,7 +737,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         uint32_t ns = 0, no = 0, nseg = 0;
         SegMsg g;
         while (!skip && next_segment<HD>(p, smem, bar0, nseg, g) && g.ntok > 0)
-            if (!softmax_segment<HD>(p, g, smem, bar0, tmem, warp >> 2, ns, no)) break;
+            if (!softmax_segment<HD, kBox>(p, g, smem, bar0, tmem, warp >> 2, ns, no)) break;
+        if (kBox && (threadIdx.x & 31) == 0) tma_stores_done();
     }
     if (skip && threadIdx.x == 0) p.w.head[blockIdx.x] = no_part(sh);
     tc::fence_before_sync();
@@ -732,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     }
 }
 
-template <int HD>
+template <int HD, bool kBox>
 int launch_typed(const ChunkParams &p, int grid, cudaStream_t s) {
     constexpr int kSmem = Cfg<HD>::kSmem;
     static_assert(kSmem <= 226 * 1024, "shared memory per CTA");
@@ -747,15 +764,15 @@ int launch_typed(const ChunkParams &p, int grid, cudaStream_t s) {
             // setmaxnreg.inc is granted only from registers the launch holds: never launch a build whose
             // register count would make the split wait forever
             cudaFuncAttributes fa{};
-            if (cudaFuncGetAttributes(&fa, paged_chunk_kernel<HD>) != cudaSuccess) return USP_ERR_CUDA;
+            if (cudaFuncGetAttributes(&fa, paged_chunk_kernel<HD, kBox>) != cudaSuccess) return USP_ERR_CUDA;
             if ((long)fa.numRegs * kThreads < 2L * 128 * kSoftmaxRegs + 128L * kControlRegs) return USP_ERR_UNSUPPORTED;
-            if (cudaFuncSetAttribute(paged_chunk_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
+            if (cudaFuncSetAttribute(paged_chunk_kernel<HD, kBox>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
                 cudaSuccess)
                 return USP_ERR_CUDA;
             attr_set[dev] = true;
         }
     }
-    return launch_overlapped(paged_chunk_kernel<HD>, dim3((unsigned)grid), kThreads, kSmem, s, p);
+    return launch_overlapped(paged_chunk_kernel<HD, kBox>, dim3((unsigned)grid), kThreads, kSmem, s, p);
 }
 
 }  // namespace
@@ -773,9 +790,20 @@ int launch_paged_chunk(const PagedArgs &a, int n_lo, const PartSpace &w, cudaStr
     const cuuint64_t dims[3] = {(cuuint64_t)a.hd, (cuuint64_t)a.hq, (cuuint64_t)a.tokens};
     const cuuint64_t strides[2] = {(cuuint64_t)a.hd * 2, (cuuint64_t)a.q_stride * 2};
     const cuuint32_t qbox[3] = {64, (cuuint32_t)a.G, (cuuint32_t)p.tq_tokens}, estr[3] = {1, 1, 1};
+    // out likewise, in boxes of a softmax warp's 32 rows where these are whole tokens or parts of one token's heads.
+    // With two units per CTA or more a warp goes on while its boxes are written, where its own stores would cost it a
+    // thousand cycles per unit (6 prompts of 1500 to 4100 tokens, 13 units per CTA: 311 us, with boxes 303); with
+    // fewer the CTA would only wait for them (a prompt of 500 tokens 27.5 us, with boxes 28.5).
+    const bool box_out = (32 % a.G == 0 || a.G % 32 == 0) && a.tokens * a.hkv / (2 * p.tq_tokens) >= 2 * (int64_t)w.ctas;
+    const cuuint64_t out_strides[2] = {(cuuint64_t)a.hd * 2, (cuuint64_t)a.out_stride * 2};
+    const cuuint32_t oheads = box_out ? (cuuint32_t)std::min(a.G, 32) : 1u;
+    const cuuint32_t obox[3] = {64, oheads, box_out ? 32 / oheads : 1u};
     if (enc(&p.tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(a.q), dims, strides, qbox, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
+        (box_out && enc(&p.to, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.out, dims, out_strides, obox, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS) ||
         !make_cache_tmap(&p.tk, a.k, a.num_pages, a.k_page, a.hkv, ps, a.hd, box) ||
         !make_cache_tmap(&p.tv, a.v, a.num_pages, a.v_page, a.hkv, ps, a.hd, box))
         return USP_ERR_CUDA;
@@ -795,7 +823,8 @@ int launch_paged_chunk(const PagedArgs &a, int n_lo, const PartSpace &w, cudaStr
     p.out_stride = a.out_stride; p.table_stride = a.table_stride;
     p.num_pages = (int32_t)a.num_pages; p.log_ps = a.log_ps; p.hq = a.hq;
     p.scale_log2 = a.scale_log2;
-    return a.hd == 128 ? launch_typed<128>(p, w.ctas, s) : launch_typed<64>(p, w.ctas, s);
+    if (box_out) return a.hd == 128 ? launch_typed<128, true>(p, w.ctas, s) : launch_typed<64, true>(p, w.ctas, s);
+    return a.hd == 128 ? launch_typed<128, false>(p, w.ctas, s) : launch_typed<64, false>(p, w.ctas, s);
 }
 
 }  // namespace usp

@@ -224,6 +224,32 @@ def test_attention_units_of_many_parts(reqs, hq, hkv, hd, dt):
     check_attention(c, out, lse)
 
 
+@pytest.mark.parametrize("hq,hkv,hd", [(8, 8, 64), (16, 4, 128), (24, 3, 64), (64, 2, 128), (128, 1, 128), (12, 4, 128)])
+def test_attention_long_prompts(hq, hkv, hd):
+    """Enough blocks that out is written in boxes where a warp's rows are whole: every grouping, blocks that end
+    inside a warp's rows, and rows of other requests and columns beside out that stay as they were."""
+    T = 160 * 2 * 256 * hkv // hq // hkv + 700      # more than two units of 256 rows for each of up to 160 SMs
+    c = Cache([(T, T), (333, 129), (65, 65)], hq, hkv, hd, 128, torch.bfloat16, seed=11)
+    wide = torch.full((c.T + 5, hq * hd + 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = wide[:, :hq * hd].unflatten(1, (hq, hd))
+    lse = torch.full((c.T + 5, hq), 7.0, device="cuda")
+    q = torch.cat([c.q.contiguous(), c.q[:5]])
+    usp.usp_paged_attn(q, c.k_cache, c.v_cache, c.table, c.cu, c.kv, out=out, lse=lse)
+    usp.usp_check()
+    assert (wide[:, hq * hd:] == 7).all() and (wide[c.T:] == 7).all() and (lse[c.T:] == 7).all()
+    assert not (out[:c.T] == 7).all(-1).any() and (lse[:c.T] != 7).all()
+    # the long request in the definition's memory: its last rows only, as a chunk of their own
+    n = 300
+    tail = Cache.__new__(Cache)
+    tail.__dict__.update(c.__dict__)
+    tail.reqs, tail.q, tail.T = [(T, n), (333, 129), (65, 65)], c.q[T - n:], c.T - T + n
+    check_attention(tail, out[T - n:c.T], lse[T - n:c.T])
+    head = Cache.__new__(Cache)
+    head.__dict__.update(c.__dict__)
+    head.reqs, head.q, head.T, head.k, head.v = [(n, n)], c.q[:n], n, [c.k[0][:n]], [c.v[0][:n]]
+    check_attention(head, out[:n], lse[:n])
+
+
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("reqs", [[(200, 2000)], [(300, 40)] + [(0, 40)] * 30 + [(300, 40)], [(0, 90)] * 9,
                                   [(1, 500), (900, 40), (2, 700), (0, 50), (40, 1)]],
