@@ -52,7 +52,8 @@ PagedArgs paged_args(const usp_paged_desc &d) {
 // or both, each with the CTAs (0: not launched) and unit rows of its partials.
 struct Route {
     int few_ctas, few_rows, many_ctas, many_rows;
-    int split;  // the most new tokens of a request that the kernel for few rows takes
+    int split;   // the most new tokens of a request that the kernel for few rows takes
+    bool alone;  // the kernel for many rows takes all requests (the other's workspace counts all the same)
 };
 
 // bf16: up to 32 rows of a KV head a call is bound by reading the cache, and the kernel for few rows reads it
@@ -76,6 +77,17 @@ Route route(const usp_paged_desc &d, int sms) {
     if (r.split > 0) {
         r.few_rows = bf16 ? (std::min<int64_t>(rows, (int64_t)r.split * G) <= 16 ? 16 : 32) : f32_rows(false);
         r.few_ctas = bf16 ? decode_ctas(sms, r.few_rows) : f32_ctas(sms, false);
+    }
+    if (r.many_ctas && r.few_ctas) {
+        // A second kernel costs its launch (3 to 5 us), also with nothing to do. The requests for it are at most `few`, as
+        // many as may be short when the rows add up to `tokens`. None, or with hd 128, where a key costs an SM the
+        // same in both bf16 kernels, three units per SM: the kernel for many rows takes them too (one prompt of
+        // 500 tokens 27.5 -> 24.6 us; 2 chunks and 30 single tokens over 500 to 4096 keys 79 -> 67, 46 single tokens
+        // 97 -> 87; with 6 units per SM 70 -> 80). With hd 64 reading is twice as fast in the kernel for few rows (2 chunks
+        // and 14 single tokens over 4000 to 32000 keys 93 -> 98 us), in fp32 several times.
+        const int64_t M = std::min<int64_t>(d.max_new, d.tokens), all = d.nreq * M;
+        const int64_t few = M > r.split ? (all - std::min(d.tokens, all)) / (M - r.split) : d.nreq;
+        r.alone = few * d.cache.hkv <= (bf16 && d.cache.hd == 128 ? 3 * sms : 0);
     }
     return r;
 }
@@ -136,10 +148,11 @@ int usp_paged_attn(const void *q, const void *k_cache, const void *v_cache, cons
     c.G = a.G; c.hq = a.hq; c.by_G = FastDiv((uint32_t)a.G);
     if (r.many_ctas) {
         c.w[0] = part_space(at, r.many_ctas, r.many_rows, a.hd);
-        rc = bf16 ? launch_paged_chunk(a, r.split, c.w[0], s) : launch_paged_f32(a, true, r.split, INT_MAX, false, c.w[0], s);
+        const int lo = r.alone ? 0 : r.split;
+        rc = bf16 ? launch_paged_chunk(a, lo, c.w[0], s) : launch_paged_f32(a, true, lo, INT_MAX, false, c.w[0], s);
         if (rc) return rc;
     }
-    if (r.few_ctas) {
+    if (r.few_ctas && !r.alone) {
         c.w[1] = part_space(at, r.few_ctas, r.few_rows, a.hd);
         rc = bf16 ? launch_paged_decode(a, r.few_rows, r.split, r.many_ctas > 0, c.w[1], s)
                   : launch_paged_f32(a, false, 0, r.split, r.many_ctas > 0, c.w[1], s);
