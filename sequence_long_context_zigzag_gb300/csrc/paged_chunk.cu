@@ -21,9 +21,9 @@
 //                   behind the request's last key may hold NaN, and 0 x NaN would spread in P V: this warp
 //                   clears them in V's stage before the issuers see it.
 // Measured, whole calls (8 KV heads of 128, 4 query heads each): 900 tokens over 64000 keys 591 us, 1608 TFLOP/s of a
-// measured 1939 for cuBLAS (power-capped: 1748 sustained); 6 prompts of 1500 to 4100 tokens 318 us, 1194; a prompt of
-// 16384 tokens 1315 us, 1672. A pair of tiles takes about 2750 cycles (its products 2050: each Q tile is one chain of
-// products, softmax, products), a unit's end 5600 more (mask, last products, read-out of O).
+// measured 1939 for cuBLAS (power-capped: 1748 sustained); 6 prompts of 1500 to 4100 tokens 314 us, 1210; a prompt of
+// 16384 tokens 1305 us, 1685. A pair of tiles takes about 2750 cycles (its products 2050: each Q tile is one chain of
+// products, softmax, products), a unit's end about 6000 more (last products, read-out of O, both Q tiles in step again).
 //   TMEM: S0 [0,128) S1 [128,256) O0 [256,256+hd) O1 [256+hd,256+2hd); P_i lies over S_i.
 #include <cuda_bf16.h>
 
