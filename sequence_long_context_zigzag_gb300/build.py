@@ -67,7 +67,7 @@ def _build_binding(path: str) -> str:
     cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", BINDING_SRC, "-o", tmp, "-I", INCLUDE,
            "-I", sysconfig.get_paths()["include"], *[f"-I{d}" for d in dirs(cpp_extension.include_paths)],
-           *[f"-L{d}" for d in dirs(cpp_extension.library_paths)], "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+           *[f"-L{d}" for d in dirs(cpp_extension.library_paths)], "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stdout}\n{r.stderr}")

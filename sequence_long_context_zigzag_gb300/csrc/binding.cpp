@@ -9,6 +9,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -114,6 +115,11 @@ usp_stream_t stream_of(int index) {
     return reinterpret_cast<usp_stream_t>(c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)index).stream());
 }
 
+// (without the dispatcher: a page plan allocates four of these; 8.0 -> 6.2 us a call)
+Tensor empty(at::IntArrayRef sizes, at::ScalarType type, int index) {
+    return Tensor(at::detail::empty_cuda(sizes, type, at::Device(at::kCUDA, (c10::DeviceIndex)index), std::nullopt));
+}
+
 // A call's output: the caller's tensor, returned as it came, or a new one.
 struct Output {
     PyObject *given = nullptr;
@@ -128,7 +134,7 @@ template <typename Check>
 Output output(PyObject *o, const char *name, int index, at::IntArrayRef sizes, at::ScalarType type, Check check) {
     Output r;
     if (o == Py_None) {
-        r.t = at::empty(sizes, at::TensorOptions().dtype(type).device(at::kCUDA, (c10::DeviceIndex)index));
+        r.t = empty(sizes, type, index);
         return r;
     }
     r.given = o;
@@ -257,8 +263,7 @@ PyObject *paged_attn(PyObject *const *a) {
     });
     Tensor work;
     if (a[11] == Py_None) {
-        work = at::empty({(int64_t)g_attn_workspace(d)},
-                         at::TensorOptions().dtype(at::kByte).device(at::kCUDA, (c10::DeviceIndex)index));
+        work = empty({(int64_t)g_attn_workspace(d)}, at::kByte, index);
     } else {
         work = tensor(a[11], "workspace");
         need(work.is_cuda() && work.get_device() == index && work.is_contiguous(),
