@@ -17,8 +17,9 @@
 //   its odd elements, so that Q's and K's rows serve as they are, 12 16-byte words for 64 pair products; an
 //   output's pair is two rows, from P written transposed. K and V come by asynchronous copies: V during a tile's scores, the next K during its outputs,
 //   so the copies hold no registers (with register prefetch the loop had none left to run its loads ahead). 2048 tokens
-//   over 8192 keys, 8 heads: 806 us at hd 64, 1663 at 128, 46 to 48 TFLOP/s, 0.6 of what packed multiply-adds
-//   alone reach (79): the operands' shared-memory reads share the issue slots.
+//   over 8192 keys, 8 heads: 755 us at hd 64, 1488 at 128, 51 to 52 TFLOP/s, two thirds of what packed multiply-adds
+//   alone reach (79): the operands' shared-memory reads share the issue slots. The products' loops are unrolled all
+//   the way for their addresses (2 and 4 steps at a time 805 and 1660 us).
 #include <math.h>
 
 #include <algorithm>
@@ -345,7 +346,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) paged_f32_many_kernel(const _
                 for (int i = 0; i < 8; ++i)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) s[i][j] = 0;
-#pragma unroll 2
+#pragma unroll 16
                 for (int d = 0; d < HD; d += 4) {
                     ulonglong2 k2[4];
 #pragma unroll
@@ -418,7 +419,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) paged_f32_many_kernel(const _
                 copies_wait_all();  // V
                 __syncthreads();    // everyone's; and all are done with K
                 if (t + 1 < g.t1) fetch(t + 1, p.k, p.k_page, ks, C::kRow);
-#pragma unroll 4
+#pragma unroll
                 for (int d = 0; d < kManyKT; ++d) {
                     uint64_t p2[4];
                     load_pairs(pt + d * C::kPRow + ty * 8, p2);
