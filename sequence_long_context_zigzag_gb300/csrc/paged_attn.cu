@@ -58,9 +58,9 @@ struct Route {
 
 // bf16: up to 32 rows of a KV head a call is bound by reading the cache, and the kernel for few rows reads it
 // at the HBM rate; above, its re-reading of K/V per unit costs more than the other one's idle rows. fp32: the
-// kernel for few rows computes 17 (hd 64) to 25 TFLOP/s at any number of rows, the other one 47 at 128 rows and
-// a row's share of that below (40000 keys, 4 requests: 32 rows of 128 829 against 1785 us, 64 1577 against 1788;
-// 40 rows of 64 741 against 866, 48 883 against 865).
+// kernel for few rows computes 17 (hd 64) to 25 TFLOP/s at any number of rows, the other one 52 at 128 rows and
+// a row's share of that below (40000 keys, 4 requests: 48 rows of 128 1204 against 1600 us, 64 1577 against 1601;
+// 40 rows of 64 741 against 811, 48 883 against 812).
 Route route(const usp_paged_desc &d, int sms) {
     Route r{};
     const bool bf16 = d.cache.dtype == USP_BF16;
