@@ -336,8 +336,15 @@ __device__ void consumer(const DecodeParams &p, uint8_t *smem, uint32_t sbase) {
                         mma16816(o[c + 1], pf[w], b[2] & keep[w][0], b[3] & keep[w][1]);
                     }
             }
+            // The stage is released only when its rows have arrived in registers: an arrive does not wait for
+            // ldmatrix reads in flight, and beside another kernel's load on the shared memory pipe these came after
+            // the next tile had landed (one call in 10^4: the last columns of a unit a few keys wrong). The arrive's
+            // address depends on a result of every product of V, compared with a NaN that no product gives.
+            bool never = false;
+#pragma unroll
+            for (int c = 0; c < kNT; ++c) never |= __float_as_uint(o[c][0]) == 0x7fa5a5a5u;
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(BAR(C::EMPTY + st));
+            if (lane == 0) tc::mbar_arrive(BAR(C::EMPTY + st) + (never ? 8u : 0u));
         }
         // ---- merge the four warps' states and write the rows ---------------------------------------
 #pragma unroll
