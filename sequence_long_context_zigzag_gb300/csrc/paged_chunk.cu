@@ -181,16 +181,16 @@ __device__ void walk_role(const ChunkParams &p, const SchedShared &sh, uint8_t *
 
 // The next segment, for a whole warp; ntok == 0 at the end. False after a failed wait.
 template <int HD>
-__device__ __forceinline__ bool next_segment(const ChunkParams &p, const uint8_t *smem, uint32_t bar0, uint32_t &n,
-                                             SegMsg &g) {
+__device__ __forceinline__ bool next_segment(const ChunkParams &p, uint32_t bar0, uint32_t &n, SegMsg &g) {
     using C = Cfg<HD>;
     bool ok = tc::mbar_wait(bar0 + 8u * (C::SEG_FULL + n % kSegSlots), (n / kSegSlots) & 1u, p.status, USP_ERR_TIMEOUT,
                             kWaitLimitNs);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) return false;
-    g = reinterpret_cast<const SegMsg *>(smem + C::kSeg)[n % kSegSlots];
+    bool never;
+    g = read_segment(bar0 + (uint32_t)(C::kSeg - C::kBar) + n % kSegSlots * (uint32_t)sizeof(SegMsg), never);
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar0 + 8u * (C::SEG_EMPTY + n % kSegSlots));
+    if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar0 + 8u * (C::SEG_EMPTY + n % kSegSlots) + (never ? 8u : 0u));
     ++n;
     return true;
 }
@@ -198,7 +198,7 @@ __device__ __forceinline__ bool next_segment(const ChunkParams &p, const uint8_t
 // The producer warp. Lane l < boxes loads box l of each K and V tile: column half l / pieces, page piece
 // l % pieces; lane 0 loads Q too.
 template <int HD>
-__device__ void producer_role(const ChunkParams &p, const uint8_t *smem, uint32_t sbase, uint32_t bar0) {
+__device__ void producer_role(const ChunkParams &p, uint32_t sbase, uint32_t bar0) {
     using C = Cfg<HD>;
     const int lane = threadIdx.x & 31;
     auto BAR = [&](int i) { return bar0 + 8u * i; };
@@ -212,7 +212,7 @@ __device__ void producer_role(const ChunkParams &p, const uint8_t *smem, uint32_
     uint32_t kfills = 0, vfills = 0, nq = 0, nseg = 0, ntail = 0;
     bool ok = true;
     SegMsg g;
-    while (ok && (ok = next_segment<HD>(p, smem, bar0, nseg, g)) && g.ntok > 0) {
+    while (ok && (ok = next_segment<HD>(p, bar0, nseg, g)) && g.ntok > 0) {
         if (g.t0 >= g.t1) continue;
         // Q: the first one at once; later ones when the buffer is free, into L2 meanwhile
         auto q_boxes = [&](auto &&f) {
@@ -359,7 +359,7 @@ __device__ __forceinline__ void issue_pv(uint32_t el, uint32_t d_tmem, uint32_t 
 // released by both issuers; each waits for a stage's fill before releasing it, also when its Q tile skips
 // the tile.
 template <int HD>
-__device__ void mma_role(const ChunkParams &p, const uint8_t *smem, uint32_t sbase, uint32_t bar0, uint32_t tmem, int i) {
+__device__ void mma_role(const ChunkParams &p, uint32_t sbase, uint32_t bar0, uint32_t tmem, int i) {
     using C = Cfg<HD>;
     const uint32_t el = elect_one();
     auto BAR = [&](int k) { return bar0 + 8u * k; };
@@ -394,7 +394,7 @@ __device__ void mma_role(const ChunkParams &p, const uint8_t *smem, uint32_t sba
         int ntok;
         do {
             SegMsg g;
-            if (!(ok = next_segment<HD>(p, smem, bar0, nseg, g))) break;
+            if (!(ok = next_segment<HD>(p, bar0, nseg, g))) break;
             // (reductions over equal values: the compiler then knows that they are uniform)
             ntok = __reduce_max_sync(0xffffffffu, g.ntok);
             kt = __reduce_max_sync(0xffffffffu, g.t0);
@@ -727,16 +727,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     if (warp >= kSoftmaxWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
         if (!skip) {
-            if (warp == kProducerWarp) producer_role<HD>(p, smem, sbase, bar0);
+            if (warp == kProducerWarp) producer_role<HD>(p, sbase, bar0);
             else if (warp == kWalkWarp) walk_role<HD>(p, sh, smem, bar0);
-            else mma_role<HD>(p, smem, sbase, bar0, tmem, warp - kMmaWarp);
+            else mma_role<HD>(p, sbase, bar0, tmem, warp - kMmaWarp);
             __syncwarp();
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         uint32_t ns = 0, no = 0, nseg = 0;
         SegMsg g;
-        while (!skip && next_segment<HD>(p, smem, bar0, nseg, g) && g.ntok > 0)
+        while (!skip && next_segment<HD>(p, bar0, nseg, g) && g.ntok > 0)
             if (!softmax_segment<HD, kBox>(p, g, smem, bar0, tmem, warp >> 2, ns, no)) break;
         if (kBox && (threadIdx.x & 31) == 0) tma_stores_done();
     }

@@ -193,7 +193,6 @@ __device__ void consumer(const DecodeParams &p, uint8_t *smem, uint32_t sbase) {
         const bool r = tc::mbar_wait(BAR(bar), parity, p.status, USP_ERR_TIMEOUT, kWaitLimitNs);
         return (bool)__all_sync(0xffffffffu, r);
     };
-    const SegMsg *ring = reinterpret_cast<const SegMsg *>(smem + C::kSeg);
     float *xch = reinterpret_cast<float *>(smem + C::kX + group * C::kXGroup);
     float2 *ml = reinterpret_cast<float2 *>(smem + C::kML) + group * 64;  // [warp][16]
     const int qr = lane >> 2, qc = (lane & 3) * 2;  // fragment row and column of this lane
@@ -211,9 +210,10 @@ __device__ void consumer(const DecodeParams &p, uint8_t *smem, uint32_t sbase) {
         SegMsg g;
         g.ntok = 0;
         if (ok) {
-            g = ring[nseg % kSegSlots];
+            bool never;
+            g = read_segment(sbase + C::kSeg + nseg % kSegSlots * (uint32_t)sizeof(SegMsg), never);
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(BAR(C::SEG_EMPTY + nseg % kSegSlots));
+            if (lane == 0) tc::mbar_arrive(BAR(C::SEG_EMPTY + nseg % kSegSlots) + (never ? 8u : 0u));
         }
         const int rows = g.ntok * p.s.G - group * 16;  // rows of this group's tile
         uint32_t qf[kKS][4];

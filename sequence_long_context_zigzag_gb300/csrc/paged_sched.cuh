@@ -13,6 +13,8 @@
 // constant cost leaves the whole unit to the next one.)
 #pragma once
 
+#include <string.h>
+
 #include "paged.cuh"
 
 namespace usp {
@@ -276,6 +278,22 @@ struct SegMsg {
     int32_t pad[2];
 };
 static_assert(sizeof(SegMsg) == 64, "four 16-byte words");
+
+// Reads the message at shared address `at`. `never` is false, but known only when all words have arrived: an arrive
+// does not wait for loads in flight, so the one that releases the slot takes its address from it.
+__device__ __forceinline__ SegMsg read_segment(uint32_t at, bool &never) {
+    uint4 w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                     : "r"(at + 16u * i)
+                     : "memory");
+    SegMsg m;
+    memcpy(&m, w, sizeof(m));
+    never = (m.ntok | m.t0 | m.t1 | m.full[0]) < 0;  // one of each word
+    return m;
+}
 
 // What the CTA that opens a unit and does not finish it leaves for the combine.
 struct __align__(16) PartHeader {

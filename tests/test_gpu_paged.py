@@ -443,6 +443,35 @@ def test_two_calls_at_once_with_their_own_workspaces():
             assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+def test_calls_on_three_streams_keep_their_bits():
+    """Calls of every kind running beside each other, so that kernels of several calls share an SM: each
+    gives the bits that it gives alone."""
+    r = random.Random(1)
+
+    def make(i):
+        reqs = [[(r.randrange(1, 4000), 1) for _ in range(r.randrange(1, 40))],
+                [(r.randrange(300, 3000), r.randrange(1, 300)) for _ in range(r.randrange(1, 5))],
+                [(r.randrange(100, 2500),) * 2 for _ in range(r.randrange(1, 4))],
+                [(r.randrange(200, 3000), r.choice([1, 1, 1, 200])) for _ in range(20)]][i % 4]
+        hkv = r.choice([1, 2, 4])
+        c = Cache(reqs, hkv * r.choice([1, 2, 4, 5, 8]), hkv, r.choice([64, 128]), r.choice([16, 64, 256]),
+                  torch.float32 if i % 5 == 4 else torch.bfloat16, seed=i)
+        return c, [x.clone() for x in attend(c, max_new=c.max_new)]
+    calls, streams = [make(i) for i in range(24)], [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for _ in range(600):
+        wrong = []
+        for _ in range(40):
+            c, want = r.choice(calls)
+            with torch.cuda.stream(r.choice(streams)):
+                out, lse = torch.full_like(want[0], float("nan")), torch.full_like(want[1], float("nan"))
+                usp.usp_paged_attn(*c.args(), max_new=c.max_new, out=out, lse=lse)
+                wrong.append((out != want[0]).sum() + (lse != want[1]).sum())
+        torch.cuda.synchronize()
+        assert sum(int(x) for x in wrong) == 0
+    usp.usp_check()
+
+
 def test_whole_step_in_one_graph():
     """Plan, append and attention captured together and replayed for other lengths, with -1 slots behind
     the last token."""
