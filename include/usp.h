@@ -405,7 +405,9 @@ typedef struct {
  *   free_head          : int32 [1]: the first entry of free_pages not taken yet
  *   block_table        : updated in place: with old_i = ceil(ctx_i / page_size), columns
  *                        [old_i, ceil((ctx_i + new_i) / page_size)) of row i get the next entries of
- *                        free_pages (request by request, in column order); others are left as they are
+ *                        free_pages (request by request, in column order), -1 where these have run out;
+ *                        others are left as they are. So a page is taken and named for every token, also
+ *                        for one behind max_tokens
  *   slot_map           : int32 [max_tokens]: the slot of every new token, request by request; -1
  *                        where there is none: behind the last token, where free_pages or the table's
  *                        columns run out, where the page is not in [0, num_pages)

@@ -19,7 +19,8 @@ namespace {
 // requests are one tile, about a microsecond, and the lengths come from L2). 64 requests 6.2 us, 256 with 272576
 // slots 8.3, of which the launch, the two dependent loads and the scan are 6. A token finds its request
 // by binary search in the tile's cumulative lengths in shared memory. A fresh page always begins with
-// a new token of its request (position % ps == 0), so that token's thread writes the table entry.
+// a new token of its request (position % ps == 0), so that token's thread writes the table entry; the
+// pages of tokens behind max_tokens, which no thread has, are written by CTA 0.
 // Sums are 64-bit; what is written saturates.
 constexpr int kPlanThreads = 256;
 constexpr int kPer = 4;
@@ -135,6 +136,19 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
             }
             const bool ok = page >= 0 && page < p.num_pages;
             p.slots[t] = ok ? (page << p.log_ps) + (int32_t)(pos & (ps - 1)) : -1;
+        }
+        if (writer && carry.a + total.a > p.max_tokens) {
+            // a warp per request, a lane per column, from the first page that a token at max_tokens or behind opens
+            for (int l = tid >> 5; l < kTile && base + l < p.nreq; l += kPlanThreads / 32) {
+                const int64_t ctx0 = ctx_s[l], end = ctx0 + (cu_s[l + 1] - cu_s[l]);
+                const int64_t old = (ctx0 + ps - 1) >> p.log_ps;
+                const int64_t from = ctx0 + max(p.max_tokens - cu_s[l], (int64_t)0);  // its first token without a place
+                const int64_t cols = min((end + ps - 1) >> p.log_ps, (int64_t)p.max_pages);
+                for (int64_t col = ((from + ps - 1) >> p.log_ps) + (tid & 31); col < cols; col += 32) {
+                    const int64_t at = page_s[l] + (col - old);
+                    p.table[(int64_t)(base + l) * p.table_stride + col] = at < p.free_count ? __ldg(p.free_pages + at) : -1;
+                }
+            }
         }
         carry.a += total.a;
         carry.b += total.b;
