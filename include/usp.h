@@ -478,7 +478,9 @@ USP_API int usp_paged_attn(const void *q, const void *k_cache, const void *v_cac
                            const int32_t *cu_new, const int32_t *kv_lens, void *out, float *lse, usp_paged_desc d,
                            void *workspace, size_t workspace_bytes, usp_stream_t stream);
 
-/* Bytes of workspace usp_paged_attn needs on the current device; 0 if the arguments are invalid. */
+/* Bytes of workspace usp_paged_attn needs on the current device; 0 if the arguments are invalid. They depend on
+ * the heads, hd, the dtype and max_new alone, and do not shrink as max_new grows: a workspace for the largest
+ * max_new serves every step of a loop. */
 USP_API size_t usp_paged_attn_workspace_size(usp_paged_desc d);
 
 /* Synchronise `stream`, then report (and clear) the device status word of the current device:

@@ -565,7 +565,8 @@ def usp_cache_append(k, v, k_cache, v_cache, slot_map, stream=None):
 
 
 def usp_paged_attn_workspace_size(q, k_cache, block_table, max_new: Optional[int] = None) -> int:
-    """Workspace bytes usp_paged_attn needs for these shapes (on q's device)."""
+    """Workspace bytes usp_paged_attn needs for these shapes (on q's device). A workspace for the largest
+    ``max_new`` serves every smaller one."""
     return _abi.binding().paged_attn_workspace_size(q, k_cache, block_table, max_new)
 
 

@@ -97,6 +97,16 @@ size_t workspace_bytes_of(const Route &r, int hd) {
            (r.many_ctas ? part_bytes(r.many_ctas, r.many_rows, hd) : 0);
 }
 
+// What the caller provides: what every call with this max_new or a smaller one uses. The one layout that is smaller
+// than that of fewer tokens is the bf16 kernel's for up to 32 rows on its own (half the headers of the 16-row one).
+size_t workspace_bytes_for(const usp_paged_desc &d, int sms) {
+    const Route r = route(d, sms);
+    size_t most = workspace_bytes_of(r, d.cache.hd);
+    if (r.few_rows == 32 && d.hq / d.cache.hkv <= 16)
+        most = std::max(most, part_bytes(decode_ctas(sms, 16), 16, d.cache.hd));
+    return most;
+}
+
 PartSpace part_space(char *&at, int ctas, int rows, int hd) {
     PartSpace w{};
     w.ctas = ctas;
@@ -117,7 +127,7 @@ extern "C" {
 size_t usp_paged_attn_workspace_size(usp_paged_desc d) {
     const DeviceInfo *di = nullptr;
     if (check_paged_desc(d) || !(di = device_info())) return 0;
-    return workspace_bytes_of(route(d, di->sm_count), d.cache.hd);
+    return workspace_bytes_for(d, di->sm_count);
 }
 
 int usp_paged_attn(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_table,
