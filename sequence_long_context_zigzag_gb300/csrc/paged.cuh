@@ -38,6 +38,8 @@ inline int64_t paged_max_keys(const PagedArgs &a) {
 //   completed; it runs beside the first as SMs come free, and ends after it (one CTA waits for that, the
 //   others make room), so that what waits for the second one only follows both.
 //   The combine waits for the kernel before it before it reads.
+//   Inputs are read with plain loads. The read-only path is for data that nothing writes during the kernel's life,
+// and here that begins while the grid that makes them may still be writing.
 template <typename K, typename P>
 inline int launch_overlapped(K kernel, dim3 grid, int threads, int smem, cudaStream_t s, const P &p) {
     cudaLaunchConfig_t cfg{};
@@ -70,9 +72,9 @@ struct Request {
 };
 __device__ __forceinline__ Request paged_request(const int32_t *cu, const int32_t *kv, int32_t i, int64_t tokens,
                                                  int64_t max_keys) {
-    const int64_t a = min(max((int64_t)__ldg(cu + i), (int64_t)0), tokens);
-    const int64_t b = min(max((int64_t)__ldg(cu + i + 1), a), tokens);
-    return Request{a, (int32_t)(b - a), (int32_t)min(max((int64_t)__ldg(kv + i), (int64_t)0), max_keys)};
+    const int64_t a = min(max((int64_t)cu[i], (int64_t)0), tokens);
+    const int64_t b = min(max((int64_t)cu[i + 1], a), tokens);
+    return Request{a, (int32_t)(b - a), (int32_t)min(max((int64_t)kv[i], (int64_t)0), max_keys)};
 }
 
 }  // namespace usp

@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
     const int tid = threadIdx.x, ps = 1 << p.log_ps;
     const int64_t t0 = (int64_t)blockIdx.x * p.slice, t1 = min(t0 + p.slice, p.max_tokens);
     const bool writer = blockIdx.x == 0;  // CTA 0 walks all requests and writes the per-request outputs
-    const int64_t head = max(__ldg(p.free_head), 0);
+    const int64_t head = max(*p.free_head, 0);
     Pair carry{0, head};
     int64_t lost = 0;
     int32_t longest = 0;
@@ -85,8 +85,8 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
 #pragma unroll
         for (int e = 0; e < kPer; ++e) {
             const int i = base + tid * kPer + e;
-            ctx[e] = i < p.nreq ? max(__ldg(p.ctx + i), 0) : 0;
-            len[e] = i < p.nreq ? max(__ldg(p.fresh_len + i), 0) : 0;
+            ctx[e] = i < p.nreq ? max(p.ctx[i], 0) : 0;
+            len[e] = i < p.nreq ? max(p.fresh_len[i], 0) : 0;
             const int64_t end = (int64_t)ctx[e] + len[e];
             mine[e] = sum;  // exclusive within the thread
             sum.a += len[e];
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
                     page = *entry;
                 } else {
                     const int64_t at = page_s[lo] + (col - old);
-                    if (at < p.free_count) page = __ldg(p.free_pages + at);
+                    if (at < p.free_count) page = p.free_pages[at];
                     if ((pos & (ps - 1)) == 0) *entry = page;
                 }
             }
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
                 const int64_t cols = min((end + ps - 1) >> p.log_ps, (int64_t)p.max_pages);
                 for (int64_t col = ((from + ps - 1) >> p.log_ps) + (tid & 31); col < cols; col += 32) {
                     const int64_t at = page_s[l] + (col - old);
-                    p.table[(int64_t)(base + l) * p.table_stride + col] = at < p.free_count ? __ldg(p.free_pages + at) : -1;
+                    p.table[(int64_t)(base + l) * p.table_stride + col] = at < p.free_count ? p.free_pages[at] : -1;
                 }
             }
         }
@@ -213,11 +213,11 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Appe
         if (!ok[e]) continue;
         uint32_t t, r;
         p.per_token.divmod(x, t, r);
-        const uint32_t slot = (uint32_t)__ldg(p.slots + t);
+        const uint32_t slot = (uint32_t)p.slots[t];
         ok[e] = slot < p.nslots;
         if (!ok[e]) continue;
-        k[e] = __ldg(reinterpret_cast<const uint4 *>(p.k + t * p.k_stride) + r);
-        v[e] = __ldg(reinterpret_cast<const uint4 *>(p.v + t * p.v_stride) + r);
+        k[e] = reinterpret_cast<const uint4 *>(p.k + t * p.k_stride)[r];
+        v[e] = reinterpret_cast<const uint4 *>(p.v + t * p.v_stride)[r];
         const uint32_t h = r >> p.log_row, c = r & ((1u << p.log_row) - 1);
         const int64_t page = slot >> p.log_ps;
         const int64_t in = (((int64_t)h << p.log_ps) + (slot & ((1u << p.log_ps) - 1))) << p.log_row;

@@ -235,7 +235,7 @@ __device__ void producer_role(const ChunkParams &p, uint32_t sbase, uint32_t bar
         auto page_of = [&](int t) {
             const int64_t key = (int64_t)t * kN + pc * piece;
             if (lane >= nbox || key >= g.kv) return p.num_pages;
-            const int32_t x = __ldg(row + (key >> p.log_ps));
+            const int32_t x = row[key >> p.log_ps];
             return x >= 0 && x < p.num_pages ? x : p.num_pages;
         };
         int32_t page = page_of(g.t0);

@@ -155,7 +155,7 @@ __device__ void producer(const DecodeParams &p, const SchedShared &sh, uint8_t *
         auto page_of = [&](int t) {
             const int64_t key = (int64_t)t * C::kKT + pc * piece;
             if (lane >= nbox || key >= g.kv) return p.num_pages;
-            const int32_t x = __ldg(row + (key >> p.log_ps));
+            const int32_t x = row[key >> p.log_ps];
             return x >= 0 && x < p.num_pages ? x : p.num_pages;
         };
         int32_t page = page_of(g.t0);
@@ -229,10 +229,10 @@ __device__ void consumer(const DecodeParams &p, uint8_t *smem, uint32_t sbase) {
             const uint32_t *q0 = q_row(qr), *q1 = q_row(qr + 8);
 #pragma unroll
             for (int k = 0; k < kKS; ++k) {
-                qf[k][0] = q0 ? __ldg(q0 + k * 8) : 0u;
-                qf[k][1] = q1 ? __ldg(q1 + k * 8) : 0u;
-                qf[k][2] = q0 ? __ldg(q0 + k * 8 + 4) : 0u;
-                qf[k][3] = q1 ? __ldg(q1 + k * 8 + 4) : 0u;
+                qf[k][0] = q0 ? q0[k * 8] : 0u;
+                qf[k][1] = q1 ? q1[k * 8] : 0u;
+                qf[k][2] = q0 ? q0[k * 8 + 4] : 0u;
+                qf[k][3] = q1 ? q1[k * 8 + 4] : 0u;
             }
         }
 #pragma unroll

@@ -62,7 +62,7 @@ template <int E> struct Vec;
 template <> struct Vec<4> { typedef float4 T; };
 template <> struct Vec<2> { typedef float2 T; };
 template <int E> __device__ __forceinline__ void load_vec(const float *p, float (&x)[E]) {
-    const typename Vec<E>::T t = __ldg(reinterpret_cast<const typename Vec<E>::T *>(p));
+    const typename Vec<E>::T t = *reinterpret_cast<const typename Vec<E>::T *>(p);
     const float *f = reinterpret_cast<const float *>(&t);
 #pragma unroll
     for (int e = 0; e < E; ++e) x[e] = f[e];
@@ -116,12 +116,11 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_f32_few_kernel(const __g
             auto page_of = [&](int t) {
                 const int64_t key = (int64_t)t * kFewKT + warp * 4;
                 if (key >= g.kv) return -1;
-                const int32_t x = __ldg(row + (key >> p.log_ps));
+                const int32_t x = row[key >> p.log_ps];
                 return x < p.num_pages ? x : -1;
             };
             int32_t page = g.t0 < g.t1 ? page_of(g.t0) : -1;
             for (int t = g.t0; t < g.t1; ++t) {
-                const int32_t next = t + 1 < g.t1 ? page_of(t + 1) : -1;
                 const int key0 = t * kFewKT + warp * 4;
                 float k[4][E], v[4][E];
                 const int64_t in = ((int64_t)g.head * ps + (key0 & (ps - 1))) * HD + lane * E;
@@ -137,7 +136,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) paged_f32_few_kernel(const __g
                     if (ok) load_vec<E>(p.v + page * p.v_page + in + j * HD, v[j]);
                     else for (int e = 0; e < E; ++e) v[j][e] = 0.f;
                 }
-                page = next;
+                page = t + 1 < g.t1 ? page_of(t + 1) : -1;  // the next tile's
                 float s[32];
 #pragma unroll
                 for (int r = 0; r < kFewRows; ++r) {
@@ -292,17 +291,26 @@ __global__ void __launch_bounds__(kManyThreads, 1) paged_f32_many_kernel(const _
             if (g.ntok == 0) break;
             const int rows = g.ntok * p.s.G;
             __syncthreads();  // the previous unit's products are done
-            for (int x = tid; x < kManyRows * (HD / 4); x += kManyThreads) {
-                const int r = x / (HD / 4), c = x % (HD / 4) * 4;
-                float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (r < rows) {
-                    uint32_t tok, h;
-                    p.s.by_G.divmod((uint32_t)r, tok, h);
-                    f = __ldg(reinterpret_cast<const float4 *>(p.q + (g.tok0 + tok) * p.q_stride +
-                                                               (int64_t)(g.head * p.s.G + (int)h) * HD + c));
+            constexpr int kQ = HD == 128 ? 8 : 4;  // pieces per thread and round: plain loads stay behind stores
+            for (int x0 = tid; x0 < kManyRows * (HD / 4); x0 += kQ * kManyThreads) {
+                float4 f[kQ];
+#pragma unroll
+                for (int i = 0; i < kQ; ++i) {
+                    const int x = x0 + i * kManyThreads, r = x / (HD / 4), c = x % (HD / 4) * 4;
+                    f[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (r < rows) {
+                        uint32_t tok, h;
+                        p.s.by_G.divmod((uint32_t)r, tok, h);
+                        f[i] = *reinterpret_cast<const float4 *>(p.q + (g.tok0 + tok) * p.q_stride +
+                                                                 (int64_t)(g.head * p.s.G + (int)h) * HD + c);
+                    }
                 }
-                *reinterpret_cast<float4 *>(qs + r * C::kRow + c) =
-                    make_float4(f.x * p.scale_log2, f.y * p.scale_log2, f.z * p.scale_log2, f.w * p.scale_log2);
+#pragma unroll
+                for (int i = 0; i < kQ; ++i) {
+                    const int x = x0 + i * kManyThreads, r = x / (HD / 4), c = x % (HD / 4) * 4;
+                    *reinterpret_cast<float4 *>(qs + r * C::kRow + c) = make_float4(
+                        f[i].x * p.scale_log2, f[i].y * p.scale_log2, f[i].z * p.scale_log2, f[i].w * p.scale_log2);
+                }
             }
             const int32_t *row = p.table + (int64_t)g.req * p.table_stride;
             const int ps = 1 << p.log_ps;
@@ -313,7 +321,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) paged_f32_many_kernel(const _
                     const int x = tid + i * kManyThreads, r = x / (HD / 4), c = x % (HD / 4) * 4;
                     const int key = t * kManyKT + r;
                     int32_t page = -1;
-                    if (key < g.kv) page = __ldg(row + (key >> p.log_ps));
+                    if (key < g.kv) page = row[key >> p.log_ps];
                     const bool ok = page >= 0 && page < p.num_pages;
                     const float *from = ok ? base + page * stride + ((int64_t)g.head * ps + (key & (ps - 1))) * HD + c : base;
                     copy16(tc::smem_u32(to + r * to_row + c), from, ok);
