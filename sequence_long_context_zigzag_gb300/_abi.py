@@ -139,8 +139,8 @@ _binding = None
 
 
 def binding():
-    """The C++ binding of the paged cache's calls (csrc/binding.cpp), built first if it is absent, with the
-    library's functions bound to it."""
+    """The C++ binding of the paged cache's calls (csrc/binding.cpp), built first if there is none from
+    its present sources, with the library's functions bound to it."""
     global _binding
     if _binding is not None:
         return _binding
@@ -149,9 +149,7 @@ def binding():
 
     from . import build as _build
     lib = load()
-    path = _build.binding_path()
-    if not os.path.exists(path):
-        _build.build_binding()
+    path = _build.build_binding()
     loader = importlib.machinery.ExtensionFileLoader("_usp_binding", path)
     module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_usp_binding", loader))
     loader.exec_module(module)

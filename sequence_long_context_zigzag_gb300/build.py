@@ -5,9 +5,9 @@ the objects link into one shared library with the CUDA runtime linked statically
 no load-time dependency on libcudart or libcuda (driver entry points are fetched at run time).
 
 Beside them the C++ binding of the paged cache's calls (csrc/binding.cpp), a CPython module against the
-installed torch, compiles with g++ (a few seconds; its file name carries the torch version). The library does not
-depend on it: where it cannot be built (no torch, no Python headers, no g++), build() warns, and the first call that
-needs the binding raises.
+installed torch, compiles with g++ (a few seconds; its file name carries the torch and Python versions and a
+hash of its sources). The library does not depend on it: where it cannot be built (no torch, no Python
+headers, no g++), build() warns, and the first call that needs the binding raises.
 """
 from __future__ import annotations
 
@@ -53,8 +53,18 @@ def _compile(src, obj, extra):
 
 
 def binding_path() -> str:
+    """The binding for this interpreter and torch, from the sources as they are now: it takes the ABI's structs by value
+    through plain addresses, so one from another usp.h would pass arguments to the wrong places."""
+    import hashlib
+    import sysconfig
+
     import torch
-    return os.path.join(PKG, "_usp_binding_torch" + "".join(c if c.isalnum() else "_" for c in torch.__version__) + ".so")
+    h = hashlib.sha256()
+    for src in (BINDING_SRC, os.path.join(INCLUDE, "usp.h")):
+        with open(src, "rb") as f:
+            h.update(f.read())
+    name = f"torch{torch.__version__}_{sysconfig.get_config_var('SOABI')}_{h.hexdigest()[:12]}"
+    return os.path.join(PKG, "_usp_binding_" + "".join(c if c.isalnum() else "_" for c in name) + ".so")
 
 
 def _build_binding(path: str) -> str:
@@ -80,8 +90,7 @@ def _build_binding(path: str) -> str:
 
 def build_binding(force: bool = False) -> str:
     path = binding_path()
-    newest = max(os.path.getmtime(BINDING_SRC), os.path.getmtime(os.path.join(INCLUDE, "usp.h")))
-    if force or not os.path.exists(path) or os.path.getmtime(path) < newest:
+    if force or not os.path.exists(path):
         _build_binding(path)
     return path
 
