@@ -109,6 +109,16 @@ struct ChunkParams {
     CUtensorMap to;  // of the launches with boxes
 };
 
+// Waits between the roles last a tile or two, those for a segment's place, message or end as long as the segments
+// before: a tile of 128 keys takes a CTA 1.1 to 1.5 us, so 2^31 keys would outlast any one limit. These waits may take
+// ten times the time of the CTA's span.
+constexpr uint64_t kKeyLimitNs = 128;
+__device__ __forceinline__ bool wait_segment(uint32_t bar, uint32_t parity, int *status, const SchedShared &sh) {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    const uint64_t limit = kWaitLimitNs + kKeyLimitNs * (uint64_t)min(sh.span, int64_t(1) << 36);
+    return tc::mbar_wait(bar, parity, status, USP_ERR_TIMEOUT, limit);
+}
+
 // does key tile t hold rows behind the request's last key? (only a unit's last tile can)
 __device__ __forceinline__ bool is_tail(const int32_t t, const int32_t kv) { return (t + 1) * kN > kv; }
 
@@ -119,7 +129,7 @@ __device__ void walk_role(const ChunkParams &p, const SchedShared &sh, uint8_t *
     using C = Cfg<HD>;
     const int lane = threadIdx.x & 31;
     auto wait = [&](int bar, uint32_t parity) {
-        const bool r = tc::mbar_wait(bar0 + 8u * bar, parity, p.status, USP_ERR_TIMEOUT, kWaitLimitNs);
+        const bool r = wait_segment(bar0 + 8u * bar, parity, p.status, sh);
         return (bool)__all_sync(0xffffffffu, r);
     };
     SegMsg *ring = reinterpret_cast<SegMsg *>(smem + C::kSeg);
@@ -181,10 +191,10 @@ __device__ void walk_role(const ChunkParams &p, const SchedShared &sh, uint8_t *
 
 // The next segment, for a whole warp; ntok == 0 at the end. False after a failed wait.
 template <int HD>
-__device__ __forceinline__ bool next_segment(const ChunkParams &p, uint32_t bar0, uint32_t &n, SegMsg &g) {
+__device__ __forceinline__ bool next_segment(const ChunkParams &p, const SchedShared &sh, uint32_t bar0, uint32_t &n,
+                                             SegMsg &g) {
     using C = Cfg<HD>;
-    bool ok = tc::mbar_wait(bar0 + 8u * (C::SEG_FULL + n % kSegSlots), (n / kSegSlots) & 1u, p.status, USP_ERR_TIMEOUT,
-                            kWaitLimitNs);
+    bool ok = wait_segment(bar0 + 8u * (C::SEG_FULL + n % kSegSlots), (n / kSegSlots) & 1u, p.status, sh);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) return false;
     bool never;
@@ -198,7 +208,7 @@ __device__ __forceinline__ bool next_segment(const ChunkParams &p, uint32_t bar0
 // The producer warp. Lane l < boxes loads box l of each K and V tile: column half l / pieces, page piece
 // l % pieces; lane 0 loads Q too.
 template <int HD>
-__device__ void producer_role(const ChunkParams &p, uint32_t sbase, uint32_t bar0) {
+__device__ void producer_role(const ChunkParams &p, const SchedShared &sh, uint32_t sbase, uint32_t bar0) {
     using C = Cfg<HD>;
     const int lane = threadIdx.x & 31;
     auto BAR = [&](int i) { return bar0 + 8u * i; };
@@ -212,7 +222,7 @@ __device__ void producer_role(const ChunkParams &p, uint32_t sbase, uint32_t bar
     uint32_t kfills = 0, vfills = 0, nq = 0, nseg = 0, ntail = 0;
     bool ok = true;
     SegMsg g;
-    while (ok && (ok = next_segment<HD>(p, bar0, nseg, g)) && g.ntok > 0) {
+    while (ok && (ok = next_segment<HD>(p, sh, bar0, nseg, g)) && g.ntok > 0) {
         if (g.t0 >= g.t1) continue;
         // Q: the first one at once; later ones when the buffer is free, into L2 meanwhile
         auto q_boxes = [&](auto &&f) {
@@ -359,7 +369,7 @@ __device__ __forceinline__ void issue_pv(uint32_t el, uint32_t d_tmem, uint32_t 
 // released by both issuers; each waits for a stage's fill before releasing it, also when its Q tile skips
 // the tile.
 template <int HD>
-__device__ void mma_role(const ChunkParams &p, uint32_t sbase, uint32_t bar0, uint32_t tmem, int i) {
+__device__ void mma_role(const ChunkParams &p, const SchedShared &sh, uint32_t sbase, uint32_t bar0, uint32_t tmem, int i) {
     using C = Cfg<HD>;
     const uint32_t el = elect_one();
     auto BAR = [&](int k) { return bar0 + 8u * k; };
@@ -394,7 +404,7 @@ __device__ void mma_role(const ChunkParams &p, uint32_t sbase, uint32_t bar0, ui
         int ntok;
         do {
             SegMsg g;
-            if (!(ok = next_segment<HD>(p, bar0, nseg, g))) break;
+            if (!(ok = next_segment<HD>(p, sh, bar0, nseg, g))) break;
             // (reductions over equal values: the compiler then knows that they are uniform)
             ntok = __reduce_max_sync(0xffffffffu, g.ntok);
             kt = __reduce_max_sync(0xffffffffu, g.t0);
@@ -727,16 +737,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     if (warp >= kSoftmaxWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
         if (!skip) {
-            if (warp == kProducerWarp) producer_role<HD>(p, sbase, bar0);
+            if (warp == kProducerWarp) producer_role<HD>(p, sh, sbase, bar0);
             else if (warp == kWalkWarp) walk_role<HD>(p, sh, smem, bar0);
-            else mma_role<HD>(p, sbase, bar0, tmem, warp - kMmaWarp);
+            else mma_role<HD>(p, sh, sbase, bar0, tmem, warp - kMmaWarp);
             __syncwarp();
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         uint32_t ns = 0, no = 0, nseg = 0;
         SegMsg g;
-        while (!skip && next_segment<HD>(p, bar0, nseg, g) && g.ntok > 0)
+        while (!skip && next_segment<HD>(p, sh, bar0, nseg, g) && g.ntok > 0)
             if (!softmax_segment<HD, kBox>(p, g, smem, bar0, tmem, warp >> 2, ns, no)) break;
         if (kBox && (threadIdx.x & 31) == 0) tma_stores_done();
     }

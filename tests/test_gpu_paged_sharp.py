@@ -132,3 +132,30 @@ def test_both_bf16_kernels_in_one_call_at_head_dim_128(hq, hkv, chunks, singles)
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(got[0], out) and torch.equal(got[1], lse)
+
+
+def test_a_call_of_several_seconds():
+    """One token over 400 million keys on every SM: no wait inside the kernel gives up while the keys before are
+    still being worked on. (The table names one page over and over.)"""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    hkv, G, hd, ps, kv = sms, 33, 64, 256, 400_000_037
+    k = torch.zeros(2, hkv, ps, hd, dtype=torch.bfloat16, device="cuda")
+    v = torch.nn.functional.one_hot(torch.arange(ps) % hd, hd).to(k).expand(2, hkv, -1, -1).contiguous()
+    table = torch.ones(1, -(-kv // ps), dtype=torch.int32, device="cuda")
+    q = torch.randn(1, hkv * G, hd, device="cuda").to(torch.bfloat16)
+    cu, kvs = torch.tensor([0, 1], dtype=torch.int32, device="cuda"), torch.tensor([kv], dtype=torch.int32, device="cuda")
+    ws = torch.empty(usp.usp_paged_attn_workspace_size(q, k, table, 1), dtype=torch.uint8, device="cuda")
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    a.record()
+    out, lse = usp.usp_paged_attn(q, k, v, table, cu, kvs, max_new=1, workspace=ws)
+    b.record()
+    usp.usp_check()
+    assert a.elapsed_time(b) > 2000     # as long as a wait may be that is not for a segment
+    # exact sums: counts per column stay below 2^24, the normaliser is a multiple of 128 below 2^31 until its last tile;
+    # then its rounding, 1 / l, the product (2^-24 each), log2 to 2 units in the last place and the product with ln 2
+    want = torch.full((hd,), kv // hd, dtype=torch.float64, device="cuda")
+    want[:kv % hd] += 1
+    want /= kv
+    err = (out[0].double() - want).abs()
+    assert (err <= want * (HALF_STEP[torch.bfloat16] + 2.0 ** -21)).all()
+    assert ((lse.double() - torch.log(torch.tensor(float(kv), dtype=torch.float64))).abs() <= 20 * 2.0 ** -21).all()
