@@ -415,7 +415,9 @@ typedef struct {
  *   kv_lens            : int32 [nreq]: ctx_i + new_i
  *   counts             : int32 [4]: new tokens; the free head after this plan (above free_count when
  *                        pages ran out); tokens without a slot because free_pages, the table or
- *                        slot_map ended; the largest kv_lens entry
+ *                        slot_map ended; the largest kv_lens entry. Where the third is not 0, kv_lens counts
+ *                        tokens that no append has stored, and where slot_map ended cu_new leaves out what
+ *                        kv_lens counts: attention for these requests is not meaningful, for others it is
  * One launch. Running it again with the same inputs gives the same outputs: to go on, the caller
  * passes counts + 1 (of another buffer) as free_head and kv_lens as ctx_lens. Outputs must not
  * overlap inputs (USP_ERR_INVALID_ARG where counts overlaps free_head). Pointers 4-byte aligned.
@@ -432,7 +434,7 @@ USP_API int usp_page_plan(const int32_t *ctx_lens, const int32_t *new_lens, cons
  * Bit-exact copy; nothing else of the cache changes. Slots must be distinct (where two tokens share
  * one, its row may hold parts of both): requests that share pages share full ones, and a page that is
  * to be continued by two requests is copied first. k, v, k_cache, v_cache 16-byte aligned; sources must not
- * overlap the cache.
+ * overlap the cache. tokens * hkv * hd elements hold fewer than 2^31 16-byte pieces (USP_ERR_UNSUPPORTED).
  */
 USP_API int usp_cache_append(const void *k, const void *v, void *k_cache, void *v_cache, const int32_t *slot_map,
                              int64_t tokens, int64_t k_stride, int64_t v_stride, usp_cache_dims d,

@@ -82,9 +82,10 @@ Route route(const usp_paged_desc &d, int sms) {
         // A second kernel costs its launch (3 to 5 us), also with nothing to do. The requests for it are at most `few`, as
         // many as may be short when the rows add up to `tokens`. None, or with hd 128, where a key costs an SM the
         // same in both bf16 kernels, three units per SM: the kernel for many rows takes them too (one prompt of
-        // 500 tokens 27.5 -> 24.6 us; 2 chunks and 30 single tokens over 500 to 4096 keys 79 -> 67, 46 single tokens
-        // 97 -> 87; with 6 units per SM 70 -> 80). With hd 64 reading is twice as fast in the kernel for few rows (2 chunks
-        // and 14 single tokens over 4000 to 32000 keys 93 -> 98 us), in fp32 several times.
+        // 500 tokens 24.6 -> 21.5 us; 2 chunks and 30 single tokens over 500 to 4096 keys 63.8 -> 59.5, 46 single tokens
+        // 84.5 -> 79.5; 6 prompts 316 -> 313; with 6 units per SM slower, 70 -> 80). With hd 64 reading is twice as fast in
+        // the kernel for few rows (2 chunks and 14 single tokens over 4000 to 32000 keys 101 -> 120 us), in fp32 several
+        // times.
         const int64_t M = std::min<int64_t>(d.max_new, d.tokens), all = d.nreq * M;
         const int64_t few = M > r.split ? (all - std::min(d.tokens, all)) / (M - r.split) : d.nreq;
         r.alone = few * d.cache.hkv <= (bf16 && d.cache.hd == 128 ? 3 * sms : 0);

@@ -16,8 +16,9 @@ namespace {
 // places are exclusive prefix sums over the requests. Every CTA owns a slice of the slot map and walks
 // the requests in tiles of kTile with a running carry of both sums until its slice is done, so one
 // launch suffices: repeating the scan costs less than a second launch or a grid-wide wait (64 to 1024
-// requests are one tile, about a microsecond, and the lengths come from L2). 64 requests 6.2 us, 256 with 272576
-// slots 8.3, of which the launch, the two dependent loads and the scan are 6. A token finds its request
+// requests are one tile, about a microsecond, and the lengths come from L2). Calls one after the other take 6.4 us for
+// 64 requests and 6.2 to 7.1 for 256 with 272576 slots: the launch, the two dependent loads and the scan, and the host
+// side of the call as long. A token finds its request
 // by binary search in the tile's cumulative lengths in shared memory. A fresh page always begins with
 // a new token of its request (position % ps == 0), so that token's thread writes the table entry; the
 // pages of tokens behind max_tokens, which no thread has, are written by CTA 0.
@@ -299,8 +300,8 @@ int usp_page_plan(const int32_t *ctx_lens, const int32_t *new_lens, const int32_
     a.num_pages = d.num_pages; a.table_stride = d.table_stride; a.free_count = d.free_count;
     a.max_tokens = d.max_tokens;
     a.nreq = d.nreq; a.max_pages = d.max_pages; a.log_ps = log2_of(d.page_size);
-    // slices of one slot per thread at least, at most two CTAs per SM (272576 slots of 256 requests: 8.2 us;
-    // with one per SM 10.3, with four, where the repeated scan shows, 9.6, with eight 11.8)
+    // slices of one slot per thread at least, at most two CTAs per SM (272576 slots of 256 requests: 6.0 to
+    // 6.8 us, with one or four per SM the same, with eight, where the repeated scan shows, 8.1)
     const int64_t ctas = std::max<int64_t>(
         1, std::min<int64_t>((d.max_tokens + kPlanThreads - 1) / kPlanThreads, 2 * (int64_t)di->sm_count));
     a.slice = (d.max_tokens + ctas - 1) / ctas;

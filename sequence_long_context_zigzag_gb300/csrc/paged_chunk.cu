@@ -20,9 +20,11 @@
 //                   is the warpgroup that gives registers to the softmax (setmaxnreg). Rows of the last page
 //                   behind the request's last key may hold NaN, and 0 x NaN would spread in P V: this warp
 //                   clears them in V's stage before the issuers see it.
-// Measured, whole calls (8 KV heads of 128, 4 query heads each): 900 tokens over 64000 keys 591 us, 1608 TFLOP/s of a
-// measured 1939 for cuBLAS (power-capped: 1748 sustained); 6 prompts of 1500 to 4100 tokens 314 us, 1210; a prompt of
-// 16384 tokens 1305 us, 1685. A pair of tiles takes about 2750 cycles (its products 2050: each Q tile is one chain of
+// Measured, whole calls (8 KV heads of 128, 4 query heads each): 900 tokens over 64000 keys 587 to 600 us, 1580 to
+// 1617 TFLOP/s of a measured 1939 for cuBLAS (power-capped: 1748 sustained); 6 prompts of 1500 to 4100 tokens 309 to 314 us,
+// 1210 to 1230; a prompt of 16384 tokens 1310 to 1340 us, 1640 to 1680. Below a full tile, 32 requests of 8000 keys (1.06
+// GB): 64 rows per KV head 174 to 176 us, 128 rows 179 to 181, 0.91 and 0.89 of the copy rate; 256 rows 213 to 225, 1200
+// to 1260 TFLOP/s. A pair of tiles takes about 2750 cycles (its products 2050: each Q tile is one chain of
 // products, softmax, products), a unit's end about 6000 more (last products, read-out of O, both Q tiles in step again).
 //   TMEM: S0 [0,128) S1 [128,256) O0 [256,256+hd) O1 [256+hd,256+2hd); P_i lies over S_i.
 #include <cuda_bf16.h>
@@ -561,7 +563,7 @@ __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegM
                 tc::unpack2(y, y0, y1);
                 const float p0 = tc::ex2(y0), p1 = tc::ex2(y1);
                 sum = tc::add2(sum, tc::pack2(p0, p1));
-                pk[e] = float2_to_bf16x2(p0, p1);
+                pk[e] = float2_to_bf16x2(p0, p1);  // (see paged_decode.cu on this rounding)
             }
             tc::tmem_st16(tS + c * 16, pk);
             if (c == 1) {
@@ -802,8 +804,8 @@ int launch_paged_chunk(const PagedArgs &a, int n_lo, const PartSpace &w, cudaStr
     const cuuint32_t qbox[3] = {64, (cuuint32_t)a.G, (cuuint32_t)p.tq_tokens}, estr[3] = {1, 1, 1};
     // out likewise, in boxes of a softmax warp's 32 rows where these are whole tokens or parts of one token's heads.
     // With two units per CTA or more a warp goes on while its boxes are written, where its own stores would cost it a
-    // thousand cycles per unit (6 prompts of 1500 to 4100 tokens, 13 units per CTA: 311 us, with boxes 303); with
-    // fewer the CTA would only wait for them (a prompt of 500 tokens 27.5 us, with boxes 28.5).
+    // thousand cycles per unit (6 prompts of 1500 to 4100 tokens, 13 units per CTA: 320 us, with boxes 313; a
+    // prompt of 16384 1353, 1326); with fewer the CTA would only wait for them (a prompt of 500 tokens 1 us more).
     const bool box_out = (32 % a.G == 0 || a.G % 32 == 0) && a.tokens * a.hkv / (2 * p.tq_tokens) >= 2 * (int64_t)w.ctas;
     const cuuint64_t out_strides[2] = {(cuuint64_t)a.hd * 2, (cuuint64_t)a.out_stride * 2};
     const cuuint32_t oheads = box_out ? (cuuint32_t)std::min(a.G, 32) : 1u;

@@ -3,7 +3,10 @@
 //
 // Mathematics: online softmax over key tiles, o = sum_j 2^(s_j - m) v_j / l with s = scale log2(e) <q, k>,
 // m the running maximum (rescaled only when it grows by more than 2^8: exact, the same stale maximum
-// normalises), l the sum of the unrounded weights in fp32.
+// normalises), l the sum of the unrounded weights in fp32. The weights are rounded to bf16 for the product
+// with V, whose products take both operands in one type: up to 2^-8 of each weight, at random signs, which over
+// the keys adds less to o than o's own rounding to bf16 (whole outputs are 0.0018 to 0.0023 off in the norm against 64
+// bits, the formula with fp32 weights 0.0016 to 0.0017).
 //
 // What bounds it: every K/V row is read once for 2 x rows multiply-adds per element, so HBM is the limit
 // (an SM's share of the copy rate is about 23 bytes per clock). Layout of the work:
@@ -19,8 +22,8 @@
 //    the legacy pipe's); P goes from S's registers straight into the next product;
 //  - the four states merge through shared memory at a unit's end.
 // Measured, a whole call with the combine (8 KV heads of 128, 4 query heads each, L2 cold): 64 requests of 2000 to
-// 16384 keys (1.59 GB) 234 us and 2 of 200000 to 262143 (1.93 GB) 281 us, 1.02 and 1.03 of the measured copy rate; 64
-// of 8000 keys at hd 64 162 us, 0.97; 4 of 300 to 1024 keys 11 us, where 7 are the start (instructions, lengths, table,
+// 16384 keys (1.59 GB) 234 to 238 us and 2 of 200000 to 262143 (1.93 GB) 281 to 286 us, 1.00 to 1.03 of the measured copy
+// rate; 64 of 8000 keys at hd 64 158 to 161 us, 0.98; 4 of 300 to 1024 keys 11 us, where 7 are the start (instructions, lengths, table,
 // keys, one after the other) and 2 to 3 the combine.
 // Rows behind the request's last key may hold NaN: scores are replaced, and V's registers of such keys
 // are cleared, since 0 x NaN would spread.
@@ -38,7 +41,7 @@ namespace usp {
 namespace {
 
 // A unit's constant cost, in keys: its start and end take a CTA about 2.5 us, in which the other CTAs read
-// that many keys each. 256 tokens over up to 2000 keys: 64 in its place 101 us, 128 78, 192 and 256 67; 26
+// that many keys each. 256 tokens over up to 2000 keys: 64 in its place 101 us, 128 78, 192 and 256 67 (61 to 67 over the runs); 26
 // single tokens and 7 chunks 38, 34.5, 32, 31.
 constexpr int kOver = 256;
 constexpr int kMinSpan = 194;     // keys per CTA below which fewer CTAs work
@@ -471,7 +474,7 @@ __global__ void __launch_bounds__(Cfg<HD, RT>::kThreads, RT == 1 ? 2 : 1)
 // up to 304) would leave that to a few CTAs, round after round: where the headers say that there are any, all
 // CTAs then read all headers and share these units' rows evenly, and the groups of a CTA share a row's parts
 // and join through shared memory. One token over 100000 keys, 16 heads on one KV head: 125 us a call with the first
-// way alone, 28 with both; 32 tokens of 8 heads 69, 36.
+// way alone, 25 to 28 with both; 32 tokens of 8 heads 69, 36.
 // A part whose rows saw nothing has m = -inf, and its o (perhaps unwritten) is not used; a NaN score leaves l
 // NaN, which is kept. Small CTAs: some fit beside the decode kernel's and are in place when it ends.
 constexpr int kCombineThreads = 128;

@@ -9,15 +9,15 @@
 //   whole rows per load, no shared memory and no synchronisation inside a unit. The 8 x 4 scores are
 //   reduced over the lanes by a butterfly that halves the values each lane holds, which ends with one
 //   score per lane (row lane / 4, key lane % 4): 31 shuffles for 32 sums. 32 requests of 8000 keys, 8 heads of 128:
-//   363 us, 5.8 TB/s (0.86 of the copy rate); 4 query heads on each of 8 KV heads of 64: 4.1 TB/s, bound by the
-//   shuffles and multiply-adds.
+//   356 us, 5.9 TB/s (0.88 of the copy rate); 4 query heads on each of 8 KV heads of 64: 249 us, 4.2 TB/s (0.63), bound
+//   by the shuffles and multiply-adds.
 // many rows (paged_f32_many_kernel, units of up to 128 query rows): bound by the fp32 pipes
 //   (128 lanes per SM). 256 threads compute 128 x 64 scores, 8 x 4 each, and 128 x hd outputs, 8 x hd / 16
 //   each, from shared memory, with packed fp32 pairs (half the issue slots): a score's pair sums its even and
 //   its odd elements, so that Q's and K's rows serve as they are, 12 16-byte words for 64 pair products; an
 //   output's pair is two rows, from P written transposed. K and V come by asynchronous copies: V during a tile's scores, the next K during its outputs,
 //   so the copies hold no registers (with register prefetch the loop had none left to run its loads ahead). 2048 tokens
-//   over 8192 keys, 8 heads: 755 us at hd 64, 1488 at 128, 51 to 52 TFLOP/s, two thirds of what packed multiply-adds
+//   over 8192 keys, 8 heads: 756 us at hd 64, 1493 at 128, 51 to 52 TFLOP/s, two thirds of what packed multiply-adds
 //   alone reach (79): the operands' shared-memory reads share the issue slots. The products' loops are unrolled all
 //   the way for their addresses (2 and 4 steps at a time 805 and 1660 us).
 #include <math.h>
