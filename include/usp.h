@@ -485,6 +485,132 @@ USP_API int usp_paged_attn(const void *q, const void *k_cache, const void *v_cac
  * max_new serves every step of a loop. */
 USP_API size_t usp_paged_attn_workspace_size(usp_paged_desc d);
 
+/*
+ * Rotary position embedding. The first `rot` elements of a head are rot / 2 pairs: (i, i + rot / 2), or (2 i, 2 i + 1)
+ * where `interleaved`. A pair (u, v) of a token at position p becomes (u c - v s, v c + u s) with c = table[p][i], s =
+ * table[p][rot / 2 + i]; elements from rot on are copied. Products and sums are rounded to fp32 one by one, results once
+ * more to the tensors' type.
+ *   table : fp32 (max_pos, rot): the cosines of a position's angles, then their sines
+ * rot is a multiple of 16, at most hd; hd 64 or 128; tensors and table 16-byte aligned, strides a multiple of 16 bytes.
+ */
+typedef struct {
+    int64_t bs, L;         /* sequences, tokens of each; bs * L * (hq + hkv) < 2^31 */
+    int64_t q_stride;      /* elements between consecutive tokens of q (0: hq * hd; a sequence follows the one */
+    int64_t q_out_stride;  /* before at L times the stride); the same for q_out, */
+    int64_t k_stride;      /* k (0: hkv * hd) */
+    int64_t k_out_stride;  /* and k_out */
+    int64_t max_pos;       /* rows of table, < 2^31 */
+    int32_t hq, hkv;       /* heads of q and k; hkv may be 0 (no k) */
+    int32_t hd, rot;
+    int32_t dtype;         /* usp_dtype */
+    int32_t interleaved;   /* nonzero: pairs of neighbours */
+    int32_t inverse;       /* nonzero: by the negative angles (the gradient) */
+    int32_t nseq;          /* packed samples (0: none) */
+} usp_rope_desc;
+
+/*
+ * usp_rope -- rotate q and k of whole sequences.
+ *   q, k       : (bs, L, hq, hd), (bs, L, hkv, hd); q_out, k_out alike (they may be q and k themselves)
+ *   positions  : int32 [bs * L], or NULL: a token's place in its sequence, or in its packed sample. A token whose
+ *                position is not in [0, max_pos) is copied (padding marked -1). Without it L <= max_pos.
+ *   cu_seqlens : int32 [nseq + 1], cumulative lengths of the samples packed into each sequence (nseq > 0; unused with
+ *                positions)
+ */
+USP_API int usp_rope(const void *q, void *q_out, const void *k, void *k_out, const float *table,
+                     const int32_t *positions, const int32_t *cu_seqlens, usp_rope_desc d, usp_stream_t stream);
+
+typedef struct {
+    int64_t tokens;        /* tokens * (hq + 2 hkv) < 2^31 */
+    int64_t q_stride;      /* elements between consecutive tokens of q (0: hq * hd), */
+    int64_t q_out_stride;  /* q_out, */
+    int64_t k_stride;      /* k (0: hkv * hd) */
+    int64_t v_stride;      /* and v */
+    int64_t max_pos;       /* rows of table, < 2^31 */
+    int32_t nreq;          /* requests, at most 2^30 (unused with positions) */
+    int32_t hq;            /* heads of q; 0: no q */
+    int32_t rot;
+    int32_t interleaved;
+    int32_t dtype;         /* of q, k and v */
+} usp_rope_append_desc;
+
+/*
+ * usp_rope_append -- usp_cache_append with the rotation on the way: q_out = rotated q, the cache gets rotated k, and v.
+ *   q, q_out   : (tokens, hq, hd) (q_out may be q); k, v: (tokens, hkv, hd)
+ *   slot_map   : int32 [tokens] as in usp_cache_append
+ *   positions  : int32 [tokens], or NULL: kv_lens[i] - cu_new[i + 1] + t for token t of request i
+ *   cu_new, kv_lens : as usp_page_plan leaves them, int32 [nreq + 1] and [nreq] (unused with positions)
+ * A token without a position in [0, max_pos) (among them those behind cu_new[nreq]) is skipped: its row of q_out is left
+ * as it was, nothing is stored. One without a slot is rotated in q_out and not stored. The rest as usp_cache_append.
+ */
+USP_API int usp_rope_append(const void *q, void *q_out, const void *k, const void *v, void *k_cache, void *v_cache,
+                            const int32_t *slot_map, const int32_t *positions, const int32_t *cu_new,
+                            const int32_t *kv_lens, const float *table, usp_rope_append_desc d, usp_cache_dims c,
+                            usp_stream_t stream);
+
+/*
+ * A paged cache in 4 bits. A row's hd values are groups of 32, each with a scale byte b that stands for
+ * s = (8 + (b & 7)) 2^((b >> 3) - 23); a code c of -8 .. 7 stands for c s (exact in bf16).
+ *   codes  : k_cache, v_cache uint8 [num_pages][hkv][page_size][hd / 2]: two's complement, 8 codes to a little-endian
+ *            32-bit word, value e of the 8 in bits [4 n, 4 n + 4) with n = e / 2 + 4 (e % 2)
+ *   scales : k_scales, v_scales uint8 [num_pages][hkv][page_size][hd / 32]
+ * Slots and block tables as those of the other caches. All four 16-byte aligned.
+ */
+typedef struct {
+    int64_t num_pages;       /* pages in the cache; num_pages * page_size < 2^31 */
+    int64_t k_page_stride;   /* bytes between consecutive pages of k_cache (0: hkv * page_size * hd / 2); a multiple of */
+    int64_t v_page_stride;   /* 16; the same for v_cache, */
+    int64_t k_scale_stride;  /* k_scales (0: hkv * page_size * hd / 32) */
+    int64_t v_scale_stride;  /* and v_scales */
+    int32_t page_size;       /* 16, 32, 64, 128 or 256 */
+    int32_t hkv;
+    int32_t hd;              /* 64 or 128 */
+} usp_q4_dims;
+
+/*
+ * usp_cache_append_q4 -- quantise the K and V rows of `tokens` tokens into their slots of a 4-bit cache; arguments as
+ * usp_cache_append's. A group's b is the smallest whose 7.5 s reaches its largest magnitude (255, s = 3840, where none
+ * does: larger values saturate), a value's code min(7, max(-8, x / s to the nearest whole number, ties to even)): off by
+ * half a step s / 2 at most. NaN is stored as 0.
+ */
+USP_API int usp_cache_append_q4(const void *k, const void *v, void *k_cache, void *v_cache, uint8_t *k_scales,
+                                uint8_t *v_scales, const int32_t *slot_map, int64_t tokens, int64_t k_stride,
+                                int64_t v_stride, int32_t dtype, usp_q4_dims c, usp_stream_t stream);
+
+/* usp_rope_append into a 4-bit cache: the rotated k is quantised from fp32. rot = 0 (with hq = 0): no rotation. */
+USP_API int usp_rope_append_q4(const void *q, void *q_out, const void *k, const void *v, void *k_cache, void *v_cache,
+                               uint8_t *k_scales, uint8_t *v_scales, const int32_t *slot_map,
+                               const int32_t *positions, const int32_t *cu_new, const int32_t *kv_lens,
+                               const float *table, usp_rope_append_desc d, usp_q4_dims c, usp_stream_t stream);
+
+typedef struct {
+    usp_q4_dims cache;
+    int64_t tokens;       /* rows of q, out and lse; tokens * hq < 2^31 */
+    int64_t q_stride;     /* elements between consecutive tokens of q (0: hq * hd); a multiple of 16 bytes */
+    int64_t out_stride;   /* the same for out */
+    int64_t table_stride; /* entries between consecutive rows of block_table (>= max_pages) */
+    int32_t nreq;         /* requests, at most 2^30 */
+    int32_t max_pages;    /* columns of block_table */
+    int32_t hq;           /* query heads; head h reads KV head h / (hq / hkv); hq / hkv <= 128 */
+    int32_t max_new;      /* as in usp_paged_desc */
+    int32_t causal;
+    float scale;          /* softmax scale; <= 0 means 1/sqrt(hd) */
+    int32_t dtype;        /* of q and out */
+} usp_paged_q4_desc;
+
+/*
+ * usp_paged_attn_q4 -- usp_paged_attn over a 4-bit cache: attention of each request's new tokens over what its cached
+ * rows stand for. Arguments, masks, workspace and empty rows as there; cache rows behind kv_i may hold anything. Products
+ * run on the tensor cores with the cache's values exact; bf16: the weights are rounded to bf16; fp32: q and the weights
+ * enter as three bf16 terms each, which hold 24 bits.
+ */
+USP_API int usp_paged_attn_q4(const void *q, const void *k_cache, const void *v_cache, const uint8_t *k_scales,
+                              const uint8_t *v_scales, const int32_t *block_table, const int32_t *cu_new,
+                              const int32_t *kv_lens, void *out, float *lse, usp_paged_q4_desc d, void *workspace,
+                              size_t workspace_bytes, usp_stream_t stream);
+
+/* Bytes of workspace usp_paged_attn_q4 needs; as usp_paged_attn_workspace_size. */
+USP_API size_t usp_paged_attn_q4_workspace_size(usp_paged_q4_desc d);
+
 /* Synchronise `stream`, then report (and clear) the device status word of the current device:
  * USP_OK, USP_ERR_TIMEOUT, or USP_ERR_CUDA if the synchronisation itself failed. */
 USP_API int usp_check(usp_stream_t stream);

@@ -2,7 +2,7 @@
 
 Thin Python binding of the C ABI in include/usp.h: functions with the ABI's names take torch CUDA
 tensors, check their shapes, and pass raw device pointers and the current CUDA stream to libusp.so
-(through ctypes; the paged cache's calls through a small C++ module).
+(through ctypes; the paged cache's and the rotation's calls through a small C++ module).
 Every step of the path runs in the library's CUDA kernels; torch only allocates memory and supplies
 streams. There is no CPU fallback: if libusp.so cannot be loaded, every call raises.
 
@@ -12,6 +12,7 @@ Layouts (all row-major; see include/usp.h for the index formulas):
   head-sharded       [rd][ud][H/ud][bs][Lr][hd]          after AllToAll4D
   lse (head-sharded) [rd][ud][hq/ud][bs][Lr] fp32; lse (natural) (bs, L, hq)
   paged K/V cache    [num_pages][hkv][page_size][hd]     what a sequence goes on from, token by token
+  in 4 bits          codes uint8 [num_pages][hkv][page_size][hd/2], scales uint8 [..][hd/32]
 """
 from __future__ import annotations
 
@@ -30,6 +31,8 @@ __all__ = ["usp_extract_local", "usp_a2a4d", "usp_a2a4d_multi", "usp_extract_a2a
            "usp_forward_noalloc", "heads_per_rank",
            "usp_attn_bwd_delta", "usp_attn_bwd", "usp_backward", "usp_backward_workspace_size", "UspAttentionFunction",
            "UspAttention", "usp_page_plan", "usp_cache_append", "usp_paged_attn", "usp_paged_attn_workspace_size",
+           "usp_rope_table", "usp_rope", "UspRopeFunction", "usp_rope_append", "usp_cache_append_q4",
+           "usp_paged_attn_q4", "usp_paged_attn_q4_workspace_size",
            "UspError", "USP_MODE_FUSED", "USP_MODE_STEP", "USP_MODE_ACCUM", "lib_path"]
 
 lib_path = _abi.LIB_PATH
@@ -582,6 +585,84 @@ def usp_paged_attn(q, k_cache, v_cache, block_table, cu_new, kv_lens, max_new: O
     ``workspace``: at least usp_paged_attn_workspace_size bytes (allocated per call where not given)."""
     return _on_stream("usp_paged_attn", q, stream, _abi.binding().paged_attn, q, k_cache, v_cache, block_table, cu_new,
                       kv_lens, max_new, causal, scale, out, lse, workspace)
+
+
+# ---- rotary position embedding, 4-bit paged cache --------------------------------------------------
+
+
+def usp_rope_table(max_pos: int, rot: int, base: float = 10000.0, inv_freq=None, device=None) -> torch.Tensor:
+    """The table the rotation reads, fp32 (max_pos, rot): cosines of each position's angles, then their sines.
+    ``inv_freq``: the rot / 2 angles per position (base^(-2 i / rot) where not given; frequencies that are scaled
+    for long contexts go here). Made once per model, in 64 bits: angles of far positions lose what 32 have."""
+    device = torch.device("cuda" if device is None else device)
+    if inv_freq is None:
+        inv_freq = float(base) ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
+    inv_freq = torch.as_tensor(inv_freq, dtype=torch.float64).to(device)
+    _need(rot > 0 and rot % 2 == 0 and inv_freq.shape == (rot // 2,), "inv_freq must hold rot / 2 values")
+    angle = torch.arange(max_pos, dtype=torch.float64, device=device)[:, None] * inv_freq
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
+def usp_rope(q, k, table, positions=None, cu_seqlens=None, interleaved: bool = False, inverse: bool = False, q_out=None,
+             k_out=None, stream=None):
+    """Rotate q (bs, L, hq, hd) and k (bs, L, hkv, hd; or None) of whole sequences by their tokens' positions, before
+    the attention: the place in the sequence, or in its packed sample (``cu_seqlens``), or ``positions`` (int32, one per
+    token; a token whose position is not in the table, e.g. -1 for padding, is copied). ``table``: see
+    :func:`usp_rope_table`; its columns are the elements of a head that are rotated, in pairs (i, i + rot / 2), or
+    (2 i, 2 i + 1) with ``interleaved``. ``inverse`` rotates back. The outputs may be the inputs.
+    Returns (q_out, k_out)."""
+    return _on_stream("usp_rope", q, stream, _abi.binding().rope, q, k, table, positions, cu_seqlens, interleaved, inverse,
+                      q_out, k_out)
+
+
+class UspRopeFunction(torch.autograd.Function):
+    """usp_rope as a differentiable op: (q, k) rotated; the gradients are rotated back, in one launch. (k may be None.)"""
+
+    @staticmethod
+    def forward(ctx, q, k, table, positions=None, cu_seqlens=None, interleaved=False):
+        ctx.save_for_backward(table, positions, cu_seqlens)
+        ctx.interleaved = interleaved
+        return usp_rope(q, k, table, positions, cu_seqlens, interleaved)
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        table, positions, cu_seqlens = ctx.saved_tensors
+        dq, dk = usp_rope(dq.contiguous(), None if dk is None else dk.contiguous(), table, positions, cu_seqlens,
+                          ctx.interleaved, inverse=True)
+        return dq, dk, None, None, None, None
+
+
+def usp_rope_append(q, k, v, k_cache, v_cache, slot_map, table, cu_new=None, kv_lens=None, positions=None, k_scales=None,
+                    v_scales=None, interleaved: bool = False, q_out=None, stream=None):
+    """:func:`usp_cache_append` with the rotation on the way: rotated k, and v, go to their slots, and rotated q
+    (tokens, hq, hd; or None) is returned. Positions follow from ``cu_new`` and ``kv_lens`` as usp_page_plan leaves
+    them, or are given (int32, one per token). A token without a position in the table is skipped (its row of
+    ``q_out`` is left as it was). With ``k_scales`` and ``v_scales`` the caches are 4-bit ones (see
+    :func:`usp_cache_append_q4`)."""
+    return _on_stream("usp_rope_append", k, stream, _abi.binding().rope_append, q, k, v, k_cache, v_cache, k_scales, v_scales,
+                      slot_map, table, cu_new, kv_lens, positions, interleaved, q_out)
+
+
+def usp_cache_append_q4(k, v, k_cache, v_cache, k_scales, v_scales, slot_map, stream=None):
+    """Quantise the rows of k and v (tokens, hkv, hd; bf16 or fp32) into their slots of a 4-bit cache: codes uint8
+    (num_pages, hkv, page_size, hd / 2) and scales uint8 (num_pages, hkv, page_size, hd / 32), in place; the format is
+    described in include/usp.h. Values are off by half a step, at most 1 / 13 of their group's largest."""
+    _on_stream("usp_cache_append_q4", k, stream, _abi.binding().rope_append, None, k, v, k_cache, v_cache, k_scales, v_scales,
+               slot_map, None, None, None, None, False, None)
+    return k_cache, v_cache, k_scales, v_scales
+
+
+def usp_paged_attn_q4_workspace_size(q, k_cache, block_table, max_new: Optional[int] = None) -> int:
+    """Workspace bytes usp_paged_attn_q4 needs for these shapes; as :func:`usp_paged_attn_workspace_size`."""
+    return _abi.binding().paged_attn_q4_workspace_size(q, k_cache, block_table, max_new)
+
+
+def usp_paged_attn_q4(q, k_cache, v_cache, k_scales, v_scales, block_table, cu_new, kv_lens, max_new: Optional[int] = None,
+                      causal: bool = True, scale: Optional[float] = None, out=None, lse=None, workspace=None, stream=None):
+    """:func:`usp_paged_attn` over a 4-bit cache (see :func:`usp_cache_append_q4`), for bf16 or fp32 queries: single
+    tokens, chunks and whole prompts in one call. Arguments and results as there."""
+    return _on_stream("usp_paged_attn_q4", q, stream, _abi.binding().paged_attn_q4, q, k_cache, v_cache, k_scales, v_scales,
+                      block_table, cu_new, kv_lens, max_new, causal, scale, out, lse, workspace)
 
 
 def default_scale(hd: int) -> float:

@@ -64,6 +64,34 @@ class UspPagedDesc(ctypes.Structure):
                 ("causal", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
+class UspRopeDesc(ctypes.Structure):
+    _fields_ = [("bs", ctypes.c_int64), ("L", ctypes.c_int64), ("q_stride", ctypes.c_int64),
+                ("q_out_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("k_out_stride", ctypes.c_int64),
+                ("max_pos", ctypes.c_int64), ("hq", ctypes.c_int32), ("hkv", ctypes.c_int32), ("hd", ctypes.c_int32),
+                ("rot", ctypes.c_int32), ("dtype", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("inverse", ctypes.c_int32), ("nseq", ctypes.c_int32)]
+
+
+class UspRopeAppendDesc(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("q_stride", ctypes.c_int64), ("q_out_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64), ("max_pos", ctypes.c_int64),
+                ("nreq", ctypes.c_int32), ("hq", ctypes.c_int32), ("rot", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class UspQ4Dims(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int64), ("k_page_stride", ctypes.c_int64), ("v_page_stride", ctypes.c_int64),
+                ("k_scale_stride", ctypes.c_int64), ("v_scale_stride", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("hkv", ctypes.c_int32), ("hd", ctypes.c_int32)]
+
+
+class UspPagedQ4Desc(ctypes.Structure):
+    _fields_ = [("cache", UspQ4Dims), ("tokens", ctypes.c_int64), ("q_stride", ctypes.c_int64),
+                ("out_stride", ctypes.c_int64), ("table_stride", ctypes.c_int64), ("nreq", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("hq", ctypes.c_int32), ("max_new", ctypes.c_int32),
+                ("causal", ctypes.c_int32), ("scale", ctypes.c_float), ("dtype", ctypes.c_int32)]
+
+
 class UspError(RuntimeError):
     def __init__(self, fn, status, text):
         super().__init__(f"{fn} failed: {text} (status {status})")
@@ -123,6 +151,18 @@ def load():
     lib.usp_paged_attn.restype = ctypes.c_int
     lib.usp_paged_attn_workspace_size.argtypes = [UspPagedDesc]
     lib.usp_paged_attn_workspace_size.restype = ctypes.c_size_t
+    lib.usp_rope.argtypes = [vp, vp, vp, vp, vp, vp, vp, UspRopeDesc, vp]
+    lib.usp_rope.restype = ctypes.c_int
+    lib.usp_rope_append.argtypes = [vp] * 11 + [UspRopeAppendDesc, UspCacheDims, vp]
+    lib.usp_rope_append.restype = ctypes.c_int
+    lib.usp_cache_append_q4.argtypes = [vp] * 7 + [i64, i64, i64, i32, UspQ4Dims, vp]
+    lib.usp_cache_append_q4.restype = ctypes.c_int
+    lib.usp_rope_append_q4.argtypes = [vp] * 13 + [UspRopeAppendDesc, UspQ4Dims, vp]
+    lib.usp_rope_append_q4.restype = ctypes.c_int
+    lib.usp_paged_attn_q4.argtypes = [vp] * 10 + [UspPagedQ4Desc, vp, ctypes.c_size_t, vp]
+    lib.usp_paged_attn_q4.restype = ctypes.c_int
+    lib.usp_paged_attn_q4_workspace_size.argtypes = [UspPagedQ4Desc]
+    lib.usp_paged_attn_q4_workspace_size.restype = ctypes.c_size_t
     lib.usp_check.argtypes = [vp]
     lib.usp_check.restype = ctypes.c_int
     lib.usp_selftest_timeout.argtypes = [i64, vp]
@@ -139,7 +179,7 @@ _binding = None
 
 
 def binding():
-    """The C++ binding of the paged cache's calls (csrc/binding.cpp), built first if there is none from
+    """The C++ binding of the paged cache's and the rotation's calls (csrc/binding.cpp), built first if there is none from
     its present sources, with the library's functions bound to it."""
     global _binding
     if _binding is not None:
@@ -154,7 +194,9 @@ def binding():
     module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_usp_binding", loader))
     loader.exec_module(module)
     module.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in
-                  (lib.usp_page_plan, lib.usp_cache_append, lib.usp_paged_attn, lib.usp_paged_attn_workspace_size)])
+                  (lib.usp_page_plan, lib.usp_cache_append, lib.usp_paged_attn, lib.usp_paged_attn_workspace_size,
+                   lib.usp_rope, lib.usp_rope_append, lib.usp_rope_append_q4, lib.usp_paged_attn_q4,
+                   lib.usp_paged_attn_q4_workspace_size)])
     _binding = module
     return module
 

@@ -1,4 +1,4 @@
-// binding.cpp -- the Python binding of the paged K/V cache calls: argument checks, output allocation and the
+// binding.cpp -- the Python binding of the paged K/V cache's and the rotation's calls: argument checks, output allocation and the
 // current stream in C++, then the C ABI (include/usp.h).
 //
 // Serving calls these once per layer and token, where a short call's GPU work is about 15 microseconds; in
@@ -27,6 +27,11 @@ decltype(&usp_page_plan) g_plan;
 decltype(&usp_cache_append) g_append;
 decltype(&usp_paged_attn) g_attn;
 decltype(&usp_paged_attn_workspace_size) g_attn_workspace;
+decltype(&usp_rope) g_rope;
+decltype(&usp_rope_append) g_rope_append;
+decltype(&usp_rope_append_q4) g_rope_append_q4;
+decltype(&usp_paged_attn_q4) g_attn_q4;
+decltype(&usp_paged_attn_q4_workspace_size) g_attn_q4_workspace;
 
 struct Refused {
     PyObject *type;
@@ -276,6 +281,262 @@ PyObject *paged_attn(PyObject *const *a) {
     return tuple({&out, &lse});
 }
 
+// ---- rotation ----
+int truth(PyObject *o) {
+    const int x = PyObject_IsTrue(o);
+    if (x < 0) throw PythonError{};
+    return x;
+}
+
+// the rotation's table: rows (max_pos) and rot
+struct RopeTable {
+    const float *data = nullptr;
+    int64_t max_pos = 0;
+    int32_t rot = 0;
+};
+RopeTable rope_table(const Tensor &t) {
+    if (t.scalar_type() != at::kFloat || t.dim() != 2 || !t.is_contiguous())
+        refuse("table must be a contiguous fp32 tensor (positions, rot)");
+    need(t.size(1) > 0, "table must have columns");
+    return {static_cast<const float *>(t.const_data_ptr()), t.size(0), size32(t, 1)};
+}
+
+// the stride of (bs, L, H, hd) over tokens in elements (0: contiguous); sequences follow one another at L times the stride
+int64_t token_stride(const char *name, const Tensor &t) {
+    if (t.is_contiguous()) return 0;
+    const int64_t row = t.size(2) * t.size(3), st = t.stride(1);
+    const bool heads = (t.size(3) == 1 || t.stride(3) == 1) && (t.size(2) == 1 || t.stride(2) == t.size(3));
+    const bool seqs = t.size(0) == 1 || (t.size(1) == 1 ? t.stride(0) >= row : t.stride(0) == t.size(1) * st);
+    if (!heads || !seqs || (t.size(1) > 1 && st < row)) refuse(std::string(name) + ": only the tokens' axis may be strided");
+    return t.size(1) > 1 ? st : t.size(0) > 1 ? t.stride(0) : 0;
+}
+
+// q, k or None, table, positions or None, cu_seqlens or None, interleaved, inverse, q_out, k_out
+PyObject *rope(PyObject *const *a) {
+    const bool has_k = a[1] != Py_None;
+    const Tensor &q = tensor(a[0], "q"), &k = has_k ? tensor(a[1], "k") : q, &table = tensor(a[2], "table");
+    usp_rope_desc d{};
+    if (q.dim() != 4 || k.dim() != 4) refuse("q and k must be (bs, L, heads, hd)");
+    need(k.size(0) == q.size(0) && k.size(1) == q.size(1) && k.size(3) == q.size(3) && k.scalar_type() == q.scalar_type(),
+         "q and k must agree in bs, L, hd and dtype");
+    const RopeTable t = rope_table(table);
+    d.bs = q.size(0);
+    d.L = q.size(1);
+    d.hq = size32(q, 2);
+    d.hkv = has_k ? size32(k, 2) : 0;
+    d.hd = size32(q, 3);
+    d.rot = t.rot;
+    d.max_pos = t.max_pos;
+    d.dtype = dtype_code(q);
+    d.interleaved = truth(a[5]);
+    d.inverse = truth(a[6]);
+    d.q_stride = token_stride("q", q);
+    if (has_k) d.k_stride = token_stride("k", k);
+    const int index = device_of({&q, &k, &table});
+    const int32_t *positions = nullptr, *cu = nullptr;
+    if (a[3] != Py_None) {
+        const Tensor &p = tensor(a[3], "positions");
+        if (p.scalar_type() != at::kInt || p.numel() != d.bs * d.L || !p.is_contiguous())
+            refuse("positions must be a contiguous int32 tensor, one per token");
+        same_device(index, p);
+        positions = ints(p);
+    }
+    if (a[4] != Py_None) {
+        const Tensor &c = tensor(a[4], "cu_seqlens");
+        i32("cu_seqlens", c);
+        need(c.numel() >= 2 && c.numel() <= INT32_MAX, "cu_seqlens must have an entry more than there are samples");
+        same_device(index, c);
+        d.nseq = (int32_t)(c.numel() - 1);
+        cu = ints(c);
+    }
+    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)index);
+    auto out = [&](PyObject *o, const char *name, const Tensor &like, int64_t &stride) {
+        return output(o, name, index, like.sizes(), like.scalar_type(), [&](const Tensor &x) {
+            if (x.sizes() != like.sizes() || x.scalar_type() != like.scalar_type()) refuse(std::string(name) + " must match its input");
+            stride = token_stride(name, x);
+        });
+    };
+    Output qo = out(a[7], "q_out", q, d.q_out_stride), ko;
+    if (has_k) ko = out(a[8], "k_out", k, d.k_out_stride);
+    const int rc = g_rope(q.const_data_ptr(), qo.t.mutable_data_ptr(), has_k ? k.const_data_ptr() : nullptr,
+                          has_k ? ko.t.mutable_data_ptr() : nullptr, t.data, positions, cu, d, stream_of(index));
+    if (rc) return PyLong_FromLong(rc);
+    if (has_k) return tuple({&qo, &ko});
+    Output none;
+    none.given = Py_None;
+    return tuple({&qo, &none});
+}
+
+usp_q4_dims q4_dims(const Tensor &k, const Tensor &v, const Tensor &ks, const Tensor &vs) {
+    if (k.dim() != 4 || v.sizes() != k.sizes() || k.scalar_type() != at::kByte || v.scalar_type() != at::kByte)
+        refuse("k_cache and v_cache must be uint8 (num_pages, hkv, page_size, hd / 2)");
+    if (ks.dim() != 4 || vs.sizes() != ks.sizes() || ks.scalar_type() != at::kByte || vs.scalar_type() != at::kByte ||
+        ks.size(0) != k.size(0) || ks.size(1) != k.size(1) || ks.size(2) != k.size(2) || ks.size(3) * 16 != k.size(3))
+        refuse("k_scales and v_scales must be uint8 (num_pages, hkv, page_size, hd / 32)");
+    usp_q4_dims d{};
+    d.num_pages = k.size(0);
+    d.k_page_stride = dense_rows("k_cache", k);
+    d.v_page_stride = dense_rows("v_cache", v);
+    d.k_scale_stride = dense_rows("k_scales", ks);
+    d.v_scale_stride = dense_rows("v_scales", vs);
+    d.hkv = size32(k, 1);
+    d.page_size = size32(k, 2);
+    d.hd = (int32_t)std::min<int64_t>(2 * k.size(3), INT32_MAX);
+    return d;
+}
+uint8_t *mutable_bytes(const Tensor &t) { return static_cast<uint8_t *>(t.mutable_data_ptr()); }
+const uint8_t *bytes(const Tensor &t) { return static_cast<const uint8_t *>(t.const_data_ptr()); }
+
+// q or None, k, v, k_cache, v_cache, k_scales or None, v_scales or None, slot_map, table or None, cu_new or None, kv_lens or
+// None, positions or None, interleaved, q_out. The result: q_out (None without a q).
+PyObject *rope_append(PyObject *const *a) {
+    const bool has_q = a[0] != Py_None, q4 = a[5] != Py_None || a[6] != Py_None;
+    const Tensor &k = tensor(a[1], "k"), &v = tensor(a[2], "v"), &q = has_q ? tensor(a[0], "q") : k,
+                 &kc = tensor(a[3], "k_cache"), &vc = tensor(a[4], "v_cache"), &slots = tensor(a[7], "slot_map");
+    const Tensor &ks = q4 ? tensor(a[5], "k_scales") : kc, &vs = q4 ? tensor(a[6], "v_scales") : kc;
+    usp_cache_dims c{};
+    usp_q4_dims c4{};
+    if (q4) {
+        c4 = q4_dims(kc, vc, ks, vs);
+    } else {
+        if (kc.scalar_type() == at::kByte) refuse("a 4-bit cache needs k_scales and v_scales");
+        c = cache_dims(kc, vc);
+        need(k.scalar_type() == kc.scalar_type(), "dtype mismatch");
+    }
+    const int64_t hkv = q4 ? c4.hkv : c.hkv, hd = q4 ? c4.hd : c.hd;
+    if (k.dim() != 3 || k.size(1) != hkv || k.size(2) != hd || v.sizes() != k.sizes())
+        refuse("k and v must be (tokens, hkv, hd) like the cache");
+    if (q.dim() != 3 || q.size(0) != k.size(0) || q.size(2) != hd) refuse("q must be (tokens, hq, hd), of k's tokens and head dim");
+    need(v.scalar_type() == k.scalar_type() && q.scalar_type() == k.scalar_type(), "dtype mismatch");
+    usp_rope_append_desc d{};
+    d.tokens = k.size(0);
+    d.dtype = dtype_code(k);
+    d.hq = has_q ? size32(q, 1) : 0;
+    d.q_stride = has_q ? dense_rows("q", q) : 0;
+    d.k_stride = dense_rows("k", k);
+    d.v_stride = dense_rows("v", v);
+    d.interleaved = truth(a[12]);
+    i32("slot_map", slots, d.tokens);
+    const int index = device_of({&k, &v, &q, &kc, &vc, &ks, &vs, &slots});
+    RopeTable t;
+    const int32_t *positions = nullptr, *cu = nullptr, *kv = nullptr;
+    if (a[8] != Py_None) {
+        const Tensor &x = tensor(a[8], "table");
+        t = rope_table(x);
+        same_device(index, x);
+        if (a[11] != Py_None) {
+            const Tensor &p = tensor(a[11], "positions");
+            i32("positions", p, d.tokens);
+            same_device(index, p);
+            positions = ints(p);
+        } else {
+            const Tensor &n = tensor(a[10], "kv_lens"), &u = tensor(a[9], "cu_new");
+            i32("kv_lens", n);
+            i32("cu_new", u, n.numel() + 1);
+            same_device(index, n);
+            same_device(index, u);
+            need(n.numel() <= INT32_MAX, "too many requests");
+            d.nreq = (int32_t)n.numel();
+            cu = ints(u);
+            kv = ints(n);
+        }
+    }
+    d.rot = t.rot;
+    d.max_pos = t.max_pos;
+    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)index);
+    Output qo;
+    if (has_q)
+        qo = output(a[13], "q_out", index, q.sizes(), q.scalar_type(), [&](const Tensor &x) {
+            need(x.sizes() == q.sizes() && x.scalar_type() == q.scalar_type(), "q_out must match q");
+            d.q_out_stride = dense_rows("q_out", x);
+        });
+    const void *qp = has_q ? q.const_data_ptr() : nullptr;
+    void *qop = has_q ? qo.t.mutable_data_ptr() : nullptr;
+    const int rc =
+        q4 ? g_rope_append_q4(qp, qop, k.const_data_ptr(), v.const_data_ptr(), kc.mutable_data_ptr(), vc.mutable_data_ptr(),
+                              mutable_bytes(ks), mutable_bytes(vs), ints(slots), positions, cu, kv, t.data, d, c4, stream_of(index))
+           : g_rope_append(qp, qop, k.const_data_ptr(), v.const_data_ptr(), kc.mutable_data_ptr(), vc.mutable_data_ptr(),
+                           ints(slots), positions, cu, kv, t.data, d, c, stream_of(index));
+    if (rc) return PyLong_FromLong(rc);
+    if (!has_q) Py_RETURN_NONE;
+    PyObject *r = qo.result();
+    if (!r) throw PythonError{};
+    return r;
+}
+
+usp_paged_q4_desc paged_q4_desc(const Tensor &q, const usp_q4_dims &cache, const Tensor &table, int64_t nreq, PyObject *max_new) {
+    usp_paged_q4_desc d{};
+    d.cache = cache;
+    if (q.dim() != 3 || q.size(2) != cache.hd) refuse("q must be (tokens, hq, hd), of the cache's head dim");
+    d.dtype = dtype_code(q);
+    need(nreq <= INT32_MAX, "too many requests");
+    d.tokens = q.size(0);
+    d.q_stride = dense_rows("q", q);
+    d.table_stride = block_table(table, nreq);
+    d.nreq = (int32_t)nreq;
+    d.max_pages = size32(table, 1);
+    d.hq = size32(q, 1);
+    d.max_new = max_new == Py_None ? (int32_t)std::min<int64_t>(d.tokens, INT32_MAX) : integer32(max_new, "max_new");
+    return d;
+}
+
+// q, k_cache, block_table, max_new
+PyObject *paged_attn_q4_workspace_size(PyObject *const *a) {
+    const Tensor &q = tensor(a[0], "q"), &kc = tensor(a[1], "k_cache"), &table = tensor(a[2], "block_table");
+    if (kc.dim() != 4 || kc.scalar_type() != at::kByte) refuse("k_cache must be uint8 (num_pages, hkv, page_size, hd / 2)");
+    usp_q4_dims c{};
+    c.num_pages = kc.size(0);
+    c.hkv = size32(kc, 1);
+    c.page_size = size32(kc, 2);
+    c.hd = (int32_t)std::min<int64_t>(2 * kc.size(3), INT32_MAX);
+    const usp_paged_q4_desc d = paged_q4_desc(q, c, table, table.size(0), a[3]);
+    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)device_of({&q}));
+    const size_t n = g_attn_q4_workspace(d);
+    need(n > 0, "invalid paged attention shapes");
+    return PyLong_FromSize_t(n);
+}
+
+// q, k_cache, v_cache, k_scales, v_scales, block_table, cu_new, kv_lens, max_new, causal, scale, out, lse, workspace
+PyObject *paged_attn_q4(PyObject *const *a) {
+    const Tensor &q = tensor(a[0], "q"), &kc = tensor(a[1], "k_cache"), &vc = tensor(a[2], "v_cache"),
+                 &ks = tensor(a[3], "k_scales"), &vs = tensor(a[4], "v_scales"), &table = tensor(a[5], "block_table"),
+                 &cu = tensor(a[6], "cu_new"), &kv = tensor(a[7], "kv_lens");
+    const int64_t nreq = kv.numel();
+    i32("cu_new", cu, nreq + 1);
+    i32("kv_lens", kv);
+    usp_paged_q4_desc d = paged_q4_desc(q, q4_dims(kc, vc, ks, vs), table, nreq, a[8]);
+    d.causal = truth(a[9]);
+    d.scale = 0.f;
+    if (a[10] != Py_None) {
+        d.scale = (float)PyFloat_AsDouble(a[10]);
+        if (PyErr_Occurred()) throw PythonError{};
+    }
+    const int index = device_of({&q, &kc, &vc, &ks, &vs, &table, &cu, &kv});
+    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)index);
+    Output out = output(a[11], "out", index, q.sizes(), q.scalar_type(), [&](const Tensor &t) {
+        need(t.sizes() == q.sizes() && t.scalar_type() == q.scalar_type(), "out must match q");
+        d.out_stride = dense_rows("out", t);
+    });
+    const int64_t rows[2] = {q.size(0), q.size(1)};
+    Output lse = output(a[12], "lse", index, rows, at::kFloat, [&](const Tensor &t) {
+        need(t.sizes() == at::IntArrayRef(rows) && t.scalar_type() == at::kFloat && t.is_contiguous(),
+             "lse must be contiguous fp32 (tokens, hq)");
+    });
+    Tensor work;
+    if (a[13] == Py_None) {
+        work = empty({(int64_t)g_attn_q4_workspace(d)}, at::kByte, index);
+    } else {
+        work = tensor(a[13], "workspace");
+        need(work.is_cuda() && work.get_device() == index && work.is_contiguous(),
+             "workspace must be contiguous, on the tensors' device");
+    }
+    const int rc = g_attn_q4(q.const_data_ptr(), kc.const_data_ptr(), vc.const_data_ptr(), bytes(ks), bytes(vs), ints(table),
+                             ints(cu), ints(kv), out.t.mutable_data_ptr(), static_cast<float *>(lse.t.mutable_data_ptr()), d,
+                             work.mutable_data_ptr(), work.nbytes(), stream_of(index));
+    if (rc) return PyLong_FromLong(rc);
+    return tuple({&out, &lse});
+}
+
 template <PyObject *(*F)(PyObject *const *), Py_ssize_t kArgs>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
@@ -296,17 +557,26 @@ PyObject *bind(PyObject *const *a) {
     g_append = reinterpret_cast<decltype(g_append)>(integer(a[1]));
     g_attn = reinterpret_cast<decltype(g_attn)>(integer(a[2]));
     g_attn_workspace = reinterpret_cast<decltype(g_attn_workspace)>(integer(a[3]));
+    g_rope = reinterpret_cast<decltype(g_rope)>(integer(a[4]));
+    g_rope_append = reinterpret_cast<decltype(g_rope_append)>(integer(a[5]));
+    g_rope_append_q4 = reinterpret_cast<decltype(g_rope_append_q4)>(integer(a[6]));
+    g_attn_q4 = reinterpret_cast<decltype(g_attn_q4)>(integer(a[7]));
+    g_attn_q4_workspace = reinterpret_cast<decltype(g_attn_q4_workspace)>(integer(a[8]));
     Py_RETURN_NONE;
 }
 
 template <PyObject *(*F)(PyObject *const *), Py_ssize_t kArgs> PyMethodDef method(const char *name) {
     return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<F, kArgs>)), METH_FASTCALL, nullptr};
 }
-PyMethodDef g_methods[] = {method<bind, 4>("bind"),
+PyMethodDef g_methods[] = {method<bind, 9>("bind"),
                            method<page_plan, 12>("page_plan"),
                            method<cache_append, 5>("cache_append"),
                            method<paged_attn, 12>("paged_attn"),
                            method<paged_attn_workspace_size, 4>("paged_attn_workspace_size"),
+                           method<rope, 9>("rope"),
+                           method<rope_append, 14>("rope_append"),
+                           method<paged_attn_q4, 14>("paged_attn_q4"),
+                           method<paged_attn_q4_workspace_size, 4>("paged_attn_q4_workspace_size"),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_usp_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
