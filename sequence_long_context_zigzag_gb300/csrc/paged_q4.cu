@@ -1,18 +1,13 @@
-// paged_q4.cu -- usp_paged_attn_q4: attention over a 4-bit paged cache. Argument checks, and a first kernel.
+// paged_q4.cu -- usp_paged_attn_q4: attention over a 4-bit paged cache: argument checks and dispatch.
 #include <limits.h>
 #include <math.h>
 
 #include <algorithm>
 
-#include "paged.cuh"
-#include "q4.cuh"
-#include "tc_ptx.cuh"
-#include "usp_device.cuh"
+#include "paged_q4.cuh"
 
 namespace usp {
 namespace {
-
-constexpr float kLn2 = 0.69314718055994531f;
 
 int check_paged_q4_desc(const usp_paged_q4_desc &d) {
     int rc = check_q4_dims(d.cache);
@@ -56,80 +51,42 @@ PagedQ4Args paged_q4_args(const usp_paged_q4_desc &d) {
     return a;
 }
 
-// A warp per query row: 32 keys at a time, a key per lane for the scores, hd / 32 columns per lane for the products.
-template <typename T, int HD> __global__ void __launch_bounds__(128) paged_q4_rows_kernel(const PagedQ4Args p) {
-    constexpr int kPer = HD / 32;
-    __shared__ float q_s[4][HD];
-    wait_grid_before();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * 4 + warp;
-    if (row >= p.tokens * p.hq) return;
-    const int64_t t = row / p.hq;
-    const int h = (int)(row % p.hq), head = h / p.G;
-    int lo = 0, hi = p.nreq;  // the last request with cu <= t
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.cu[mid] <= t) lo = mid;
-        else hi = mid;
-    }
-    const Request r = paged_request(p.cu, p.kv, lo, p.tokens, min((int64_t)p.max_pages << p.log_ps, (int64_t)INT_MAX - 1024));
-    if (t < r.t0 || t >= r.t0 + r.n) return;
-    const int64_t pos = (int64_t)r.kv - r.n + (t - r.t0);
-    const int keys = p.causal ? (int)max((int64_t)0, min((int64_t)r.kv, pos + 1)) : r.kv;
-    const T *q = static_cast<const T *>(p.q) + t * p.q_stride + (int64_t)h * HD;
-    for (int e = lane; e < HD; e += 32) q_s[warp][e] = (float)q[e];
-    __syncwarp();
-    float m = -INFINITY, l = 0.f, o[kPer] = {};
-    const int32_t *pages = p.table + lo * p.table_stride;
-    for (int base = 0; base < keys; base += 32) {
-        const int key = base + lane;
-        int32_t page = -1;
-        int64_t in = 0;
-        float s = -INFINITY;
-        if (key < keys) {
-            page = pages[key >> p.log_ps];
-            if (page >= p.num_pages) page = -1;
-            in = ((int64_t)head << p.log_ps) + (key & ((1 << p.log_ps) - 1));
-            s = 0.f;
-            if (page >= 0) {
-                const uint32_t *w = reinterpret_cast<const uint32_t *>(p.k + page * p.k_page + in * q4_code_bytes(HD));
-                const uint8_t *sc = p.ks + page * p.ks_page + in * q4_scale_bytes(HD);
-                for (int x = 0; x < HD / 8; ++x) {
-                    const float f = q4_scale(sc[x / 4]);
-                    for (int e = 0; e < 8; ++e) {
-                        const int n = e / 2 + 4 * (e % 2), c = (int)(w[x] << (28 - 4 * n)) >> 28;
-                        s = fmaf(q_s[warp][x * 8 + e], (float)c * f, s);
-                    }
-                }
-            }
-            s *= p.scale_log2;
-        }
-        float mx = s;
-        for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-        const float mn = fmaxf(m, mx), mb = mn == -INFINITY ? 0.f : mn, a = exp2f(m - mb);
-        const float w = exp2f(s - mb);
-        l = l * a + w;
-        m = mn;
-        for (int e = 0; e < kPer; ++e) o[e] *= a;
-        for (int j = 0; j < min(32, keys - base); ++j) {
-            const float pj = __shfl_sync(0xffffffffu, w, j);
-            const int32_t pg = __shfl_sync(0xffffffffu, page, j);
-            const int64_t ij = __shfl_sync(0xffffffffu, in, j);
-            if (pg < 0) continue;
-            const uint8_t *b = p.v + pg * p.v_page + ij * q4_code_bytes(HD);
-            const uint8_t *sc = p.vs + pg * p.vs_page + ij * q4_scale_bytes(HD);
-            for (int e = 0; e < kPer; ++e) {
-                const int d = lane + 32 * e, n = (d & 7) / 2 + 4 * (d & 1);
-                const uint32_t w32 = *reinterpret_cast<const uint32_t *>(b + d / 8 * 4);
-                const int c = (int)(w32 << (28 - 4 * n)) >> 28;
-                o[e] = fmaf(pj, (float)c * q4_scale(sc[e]), o[e]);
-            }
-        }
-    }
-    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-    T *out = static_cast<T *>(p.out) + t * p.out_stride + (int64_t)h * HD;
-    for (int e = 0; e < kPer; ++e) out[lane + 32 * e] = (T)(l == 0.f ? 0.f : o[e] / l);
-    if (lane == 0) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+// The heads of a unit: the KV head's G, or where these are more than the kernel for few rows takes, the largest divisor of
+// G that it does.
+int few_heads(int G) {
+    int h = std::min(G, 16);
+    while (G % h != 0) --h;
+    return h;
+}
+
+struct Route {
+    int few_ctas, few_rows, few_G;
+};
+Route route(const usp_paged_q4_desc &d, int sms) {
+    Route r{};
+    r.few_G = few_heads(d.hq / d.cache.hkv);
+    r.few_rows = r.few_G * (int64_t)std::max(1, d.max_new) <= 8 ? 8 : 16;
+    r.few_ctas = q4_few_ctas(sms, r.few_rows);
+    return r;
+}
+
+size_t workspace_bytes_of(const Route &r, int hd) { return part_bytes(r.few_ctas, r.few_rows, hd); }
+
+// What the caller provides: what every call with this max_new or a smaller one uses (the layout of 8 rows has twice the
+// headers of that of 16).
+size_t workspace_bytes_for(const usp_paged_q4_desc &d, int sms) {
+    const Route r = route(d, sms);
+    return std::max(workspace_bytes_of(r, d.cache.hd), part_bytes(q4_few_ctas(sms, 8), 8, d.cache.hd));
+}
+
+PartSpace part_space(char *&at, int ctas, int rows, int hd) {
+    PartSpace w{};
+    w.ctas = ctas;
+    w.rows = rows;
+    w.head = reinterpret_cast<PartHeader *>(at);
+    w.data = reinterpret_cast<float *>(at + (size_t)ctas * sizeof(PartHeader));
+    at += part_bytes(ctas, rows, hd);
+    return w;
 }
 
 }  // namespace
@@ -139,7 +96,11 @@ using namespace usp;
 
 extern "C" {
 
-size_t usp_paged_attn_q4_workspace_size(usp_paged_q4_desc d) { return check_paged_q4_desc(d) ? 0 : 256; }
+size_t usp_paged_attn_q4_workspace_size(usp_paged_q4_desc d) {
+    const DeviceInfo *di = nullptr;
+    if (check_paged_q4_desc(d) || !(di = device_info())) return 0;
+    return workspace_bytes_for(d, di->sm_count);
+}
 
 int usp_paged_attn_q4(const void *q, const void *k_cache, const void *v_cache, const uint8_t *k_scales,
                       const uint8_t *v_scales, const int32_t *block_table, const int32_t *cu_new, const int32_t *kv_lens,
@@ -156,19 +117,25 @@ int usp_paged_attn_q4(const void *q, const void *k_cache, const void *v_cache, c
         !aligned(v_scales, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(block_table, 4) ||
         !aligned(cu_new, 4) || !aligned(kv_lens, 4) || !aligned(workspace, 256))
         return USP_ERR_ALIGN;
-    if (workspace_bytes < 256) return USP_ERR_INVALID_ARG;
+    const DeviceInfo *di = device_info();
+    if (!di) return USP_ERR_CUDA;
+    const Route r = route(d, di->sm_count);
+    if (workspace_bytes < workspace_bytes_of(r, d.cache.hd)) return USP_ERR_INVALID_ARG;
     PagedQ4Args a = paged_q4_args(d);
     a.q = q;
     a.k = static_cast<const uint8_t *>(k_cache); a.v = static_cast<const uint8_t *>(v_cache);
     a.ks = k_scales; a.vs = v_scales;
     a.table = block_table; a.cu = cu_new; a.kv = kv_lens;
     a.out = out; a.lse = lse;
-    const dim3 grid((unsigned)((a.tokens * a.hq + 3) / 4));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    auto go = [&](auto kernel) { return launch_overlapped(kernel, grid, 128, 0, s, a); };
-    if (a.dtype == USP_BF16)
-        return a.hd == 128 ? go(paged_q4_rows_kernel<__nv_bfloat16, 128>) : go(paged_q4_rows_kernel<__nv_bfloat16, 64>);
-    return a.hd == 128 ? go(paged_q4_rows_kernel<float, 128>) : go(paged_q4_rows_kernel<float, 64>);
+    char *at = static_cast<char *>(workspace);
+    CombineArgs c{};
+    c.out = out; c.lse = lse; c.out_stride = a.out_stride;
+    c.G = r.few_G; c.hq = a.hq; c.by_G = FastDiv((uint32_t)r.few_G);
+    c.w[1] = part_space(at, r.few_ctas, r.few_rows, a.hd);
+    rc = launch_paged_q4_few(a, r.few_G, r.few_rows, INT_MAX, false, c.w[1], s);
+    if (rc) return rc;
+    return launch_paged_combine(c, a.hd, a.dtype, s);
 }
 
 }  // extern "C"

@@ -1,0 +1,645 @@
+// paged_q4_few.cu -- attention of few query rows per KV head over the 4-bit paged cache (sm_103a): single tokens and short
+// chunks, up to 16 query rows (tokens x G heads) per unit; fp32 queries at any length.
+//
+// Mathematics: as paged_decode.cu (online softmax over key tiles, lazy rescale, weights rounded to bf16 for the product
+// with V; fp32 queries and weights enter as three bf16 terms each, x = x0 + x1 + x2 to 24 bits). The products run
+// transposed, S^T = K Q^T and O^T = V^T P^T as m16n8k16 (mma.sync), so that the cache is the operand of 16 rows and 8
+// query rows fill the other: a value of the cache is converted once for all rows, and with up to 8 rows no product is idle.
+//   A code pair becomes an operand in registers: (word >> 4 j) has two codes in the low nibbles of its halves; with
+// 0x4308 exclusive-ored in they are the bf16 numbers 136 + c, and one bf16x2 multiply-add gives (136 + c) s - 136 s =
+// c s. It is exact: 136 s = 17 (8 .. 15) 2^e has 8 bits, c s 7.
+//
+// What bounds it: reading the cache (0.53 bytes a value, an SM's share of the copy rate 42 values a clock) and, close to
+// it, the conversion: about 1.5 instructions a value beside some 0.6 of products, loads and softmax, where an SM issues
+// 128 lanes a clock. Layout of the work:
+//  - spans of equal key counts per CTA (paged_sched.cuh); a producer warp walks the span and streams K, V (TMA boxes) and
+//    their scales (bulk copies) of 128 keys a tile through a ring of stages; eight consumer warps, each with 16 keys of
+//    the tile and a softmax state of its own, which merge through shared memory at a unit's end;
+//  - S^T comes out of the product with a key per lane group and rows along lanes; two 8x8 transposes (movmatrix) make
+//    the weights the operand of the second product;
+//  - lane (g, t) converts for K the 32 values of group t of keys g and g + 8, and for V the 16 columns from 16 g on of four
+//    keys: loads of 16 and 8 bytes, a scale byte each. Which key is row k of a product is free: kKeyOf makes both loads
+//    meet all banks (with rows of 64 bytes swizzled as TMA does).
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "paged_q4.cuh"
+#include "paged_tma.cuh"
+#include "tc_ptx.cuh"
+#include "usp_device.cuh"
+
+namespace usp {
+namespace {
+
+constexpr int kOver = 512;     // a unit's constant cost, in keys
+constexpr int kWarps = 8;      // consumers
+constexpr int kThreads = (kWarps + 1) * 32;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr float kRescale = 8.0f;  // log2 units
+constexpr float kLn2 = 0.69314718055994531f;
+
+// NT: tiles of 8 query rows; F32: q, out and the weights in three bf16 terms
+template <int HD, int NT, bool F32> struct Cfg {
+    static constexpr int kTerms = F32 ? 3 : 1;
+    static constexpr int kCtas = NT == 1 ? 2 : 1;         // per SM
+    static constexpr int kKT = 16 * kWarps;               // keys per tile
+    static constexpr int kMinSpan = 192;                  // keys per CTA below which fewer CTAs work
+    static_assert(kMinSpan > kKT, "a span holds more than a tile");
+    static constexpr int kRow = q4_code_bytes(HD), kSRow = q4_scale_bytes(HD);
+    static constexpr int kCodes = kKT * kRow, kScales = kKT * kSRow;
+    static constexpr int kStage = 2 * (kCodes + kScales); // K codes, V codes, K scales, V scales
+    static constexpr int kStages = kCtas == 2 ? (HD == 128 ? 4 : 8) : 8;
+    static constexpr int kXRow = HD + 4;                  // exchange row in floats
+    static constexpr int kX = kStages * kStage;           // [warp][row][kXRow]
+    static constexpr int kML = kX + kWarps * NT * 8 * kXRow * 4;
+    static constexpr int kQ = kML + kWarps * NT * 8 * 8;  // q's terms as operands: [term][step][row tile][lane]
+    static constexpr int kSeg = kQ + (F32 ? kTerms * (HD / 16) * NT * 256 : 0);
+    static constexpr int kBar = kSeg + kSegSlots * (int)sizeof(SegMsg);
+    static constexpr int FULL = 0, EMPTY = kStages, SEG_FULL = 2 * kStages, SEG_EMPTY = SEG_FULL + kSegSlots;
+    static constexpr int kSmem = kBar + (SEG_EMPTY + kSegSlots) * 8 + 1024;  // + slack for the alignment
+    static_assert(kStage % 512 == 0 && kCodes % 512 == 0, "the swizzle's pattern of 512 bytes");
+};
+
+struct FewParams {
+    CUtensorMap tk, tv;
+    SchedIn s;
+    PartSpace w;
+    const void *q;
+    const uint8_t *ks, *vs;
+    void *out;
+    float *lse;
+    const int32_t *table;
+    int *status;
+    int64_t q_stride, out_stride, table_stride, ks_page, vs_page;
+    int32_t num_pages, log_ps, hq;
+    FastDiv by_sub;  // row groups (heads of the walk) per KV head
+    float scale_log2;
+    bool second;  // the call's other kernel is in the stream before this one
+};
+
+// c += a (16x16, row) * b (16x8, column), bf16 in, fp32 out
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t x;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(a) : "memory");
+    return x;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 x;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(a) : "memory");
+    return x;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 x;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(a) : "memory");
+    return x;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+    uint32_t x;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x) : "r"(a) : "memory");
+    return x;
+}
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+// two scale bytes as bf16 numbers: (b << 4) + the exponent field's 107 (see q4_scale)
+__device__ __forceinline__ uint32_t scales2(uint32_t lo, uint32_t hi) { return lo * 0x10u + (hi * 0x100000u + 0x35803580u); }
+__device__ __forceinline__ uint32_t minus136(uint32_t s2) {
+    return fma_bf16x2(s2, 0xc308c308u, 0x80008000u);  // -136 s - 0
+}
+// codes j (low nibbles of the halves of word >> 4 j), as values
+template <int j> __device__ __forceinline__ uint32_t values2(uint32_t word, uint32_t s2, uint32_t off) {
+    return fma_bf16x2(((word >> (4 * j)) & 0x000f000fu) ^ 0x43084308u, s2, off);
+}
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); }
+__device__ __forceinline__ bool consumers_all(bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+        "bar.red.and.pred p, 1, %2, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x), "n"(kWarps * 32)
+        : "memory");
+    return r != 0;
+}
+// x as kTerms bf16 numbers, the first pair of two values (low half: x)
+template <int kTerms> __device__ __forceinline__ void split2(float x, float y, uint32_t (&t)[kTerms]) {
+#pragma unroll
+    for (int i = 0; i < kTerms; ++i) {
+        t[i] = float2_to_bf16x2(x, y);
+        if (i + 1 < kTerms) {
+            const float2 f = bf16x2_to_float2(t[i]);
+            x -= f.x;
+            y -= f.y;
+        }
+    }
+}
+
+// The key of a warp's 16 that is row k of the products (k < 8; row k + 8: 8 further). Rows of 64 bytes (hd 128): the pairs of
+// K's 16-byte loads (k, k + 1) and the quadruples of V's 8-byte loads (k, k + 2, ..) then lie in different banks; rows of 32: the
+// quadruples of K's 8-byte and V's 4-byte loads.
+template <int HD> __device__ __forceinline__ int key_of(int k) {
+    return HD == 128 ? (k & 4) + (((k >> 1) & 1) ^ (3 * (k & 1))) : k ^ ((k >> 2) & 1);
+}
+
+// The producer warp: walks the span; lane b < 4 x pieces loads box b of each tile (K, V, K's scales, V's scales x page piece).
+template <int HD, int NT, bool F32>
+__device__ void producer(const FewParams &p, const SchedShared &sh, uint8_t *smem, uint32_t sbase) {
+    using C = Cfg<HD, NT, F32>;
+    const int lane = threadIdx.x & 31;
+    auto BAR = [&](int i) { return sbase + C::kBar + 8u * i; };
+    auto wait = [&](int bar, uint32_t parity) {
+        const bool r = tc::mbar_wait(BAR(bar), parity, p.status, USP_ERR_TIMEOUT, kWaitLimitNs);
+        return (bool)__all_sync(0xffffffffu, r);
+    };
+    SegMsg *ring = reinterpret_cast<SegMsg *>(smem + C::kSeg);
+    const int ps = 1 << p.log_ps, piece = min(ps, C::kKT), pieces = C::kKT / piece;  // at most 8 pieces
+    const int kind = lane / pieces, pc = lane % pieces;
+    const bool loads = kind < 4, scales = kind >= 2, v = kind & 1;
+    const uint32_t dst0 = sbase + (scales ? 2 * C::kCodes + (v ? C::kScales : 0) + pc * piece * C::kSRow
+                                          : (v ? C::kCodes : 0) + pc * piece * C::kRow);
+    Sched sc;
+    sched_begin<C::kKT>(p.s, sh, sc);
+    PartHeader opened = no_part(sh);
+    uint32_t fill = 0, nseg = 0;
+    bool ok = true, more = true;
+    while (more) {
+        Segment g;
+        more = sched_next<C::kKT>(p.s, sc, g);
+        if (!(ok = wait(C::SEG_EMPTY + nseg % kSegSlots, ((nseg / kSegSlots) & 1u) ^ 1u))) break;
+        if (lane == 0) {
+            SegMsg m{};
+            if (more) {
+                m.tok0 = g.tok0; m.ntok = g.ntok; m.head = g.head; m.req = g.req; m.p0 = g.p0; m.kv = g.kv;
+                m.t0 = g.t0; m.t1 = g.t1; m.tiles = g.tiles;
+            }
+            ring[nseg % kSegSlots] = m;
+            tc::mbar_arrive(BAR(C::SEG_FULL + nseg % kSegSlots));
+        }
+        ++nseg;
+        if (!more) break;
+        const int32_t *row = p.table + (int64_t)g.req * p.table_stride;
+        const int kv_head = (int)p.by_sub.div((uint32_t)g.head);
+        // page of this lane's piece of tile t; num_pages (a box of zeros) behind the request's keys
+        auto page_of = [&](int t) {
+            const int64_t key = (int64_t)t * C::kKT + pc * piece;
+            if (!loads || key >= g.kv) return p.num_pages;
+            const int32_t x = row[key >> p.log_ps];
+            return x >= 0 && x < p.num_pages ? x : p.num_pages;
+        };
+        int32_t page = page_of(g.t0);
+        for (int t = g.t0; t < g.t1; ++t) {
+            const int32_t next = t + 1 < g.t1 ? page_of(t + 1) : 0;
+            const uint32_t st = fill % C::kStages;
+            if (!(ok = wait(C::EMPTY + st, ((fill / C::kStages) & 1u) ^ 1u))) break;
+            if (lane == 0) tc::mbar_arrive_expect_tx(BAR(C::FULL + st), C::kStage);
+            __syncwarp();
+            const int in_page = kv_head * ps + (int)(((int64_t)t * C::kKT + pc * piece) & (ps - 1));
+            if (loads && !scales) {
+                tma_load_3d(dst0 + st * C::kStage, v ? &p.tv : &p.tk, 0, in_page, page, BAR(C::FULL + st));
+            } else if (loads) {
+                // (the scales of a page outside the cache are page 0's: its codes are zeros)
+                const int64_t pg = page < p.num_pages ? page : 0;
+                bulk_load(dst0 + st * C::kStage, (v ? p.vs + pg * p.vs_page : p.ks + pg * p.ks_page) + (int64_t)in_page * C::kSRow,
+                          piece * C::kSRow, BAR(C::FULL + st));
+            }
+            ++fill;
+            page = next;
+        }
+        if (!ok) break;
+        if (g.t0 == 0 && g.t1 < g.tiles) opened = part_header(p.s, sh, sc, g);
+    }
+    if (!ok) {  // drain (bounded): no copy may land after the CTA has gone
+        opened = no_part(sh);
+        for (uint32_t f = fill > C::kStages ? fill - C::kStages : 0; f < fill; ++f)
+            wait(C::FULL + f % C::kStages, (f / C::kStages) & 1u);
+    }
+    if (lane == 0) p.w.head[blockIdx.x] = opened;
+}
+
+template <int HD, int NT, bool F32> __device__ void consumer(const FewParams &p, uint8_t *smem, uint32_t sbase) {
+    using C = Cfg<HD, NT, F32>;
+    using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
+    constexpr int kMT = HD / 16;  // 16-column tiles of O^T; 16-element steps of the head dim
+    constexpr int kT = C::kTerms;
+    constexpr int kWords = HD / 32;  // K's words of a lane and key; a lane converts 8 kWords values of a key
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    auto BAR = [&](int i) { return sbase + C::kBar + 8u * i; };
+    auto wait = [&](int bar, uint32_t parity) {
+        const bool r = tc::mbar_wait(BAR(bar), parity, p.status, USP_ERR_TIMEOUT, kWaitLimitNs);
+        return (bool)__all_sync(0xffffffffu, r);
+    };
+    float *xch = reinterpret_cast<float *>(smem + C::kX);
+    float2 *ml = reinterpret_cast<float2 *>(smem + C::kML);  // [warp][8 NT rows]
+    uint2 *q_s = reinterpret_cast<uint2 *>(smem + C::kQ);
+    // addresses inside a stage: K's row k = g (and + 8), this lane's values; V's rows 2 t, 2 t + 1 (and + 8), its columns
+    const int kkey = warp * 16 + key_of<HD>(g);
+    const uint32_t k_at = kkey * C::kRow + (HD == 128 ? (t ^ ((kkey >> 1) & 3)) * 16 : t * 8);
+    const uint32_t ks_at = 2 * C::kCodes + kkey * C::kSRow + (HD == 128 ? t : t >> 1);
+    uint32_t v_at[2], vs_at[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int key = warp * 16 + key_of<HD>(2 * t + e);
+        v_at[e] = C::kCodes + key * C::kRow + (HD == 128 ? ((g >> 1) ^ ((key >> 1) & 3)) * 16 + (g & 1) * 8 : g * 4);
+        vs_at[e] = 2 * C::kCodes + C::kScales + key * C::kSRow + (HD == 128 ? g >> 1 : g >> 2);
+    }
+    uint32_t fill = 0;
+    for (uint32_t nseg = 0;; ++nseg) {
+        // Every warp reaches exactly one consumers_all per segment, also after a failed wait and at the end, and
+        // leaves only by its result: so no warp waits for one that has gone.
+        bool ok = wait(C::SEG_FULL + nseg % kSegSlots, (nseg / kSegSlots) & 1u);
+        SegMsg s;
+        s.ntok = 0;
+        if (ok) {
+            bool never;
+            s = read_segment(sbase + C::kSeg + nseg % kSegSlots * (uint32_t)sizeof(SegMsg), never);
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(BAR(C::SEG_EMPTY + nseg % kSegSlots) + (never ? 8u : 0u));
+        }
+        const int rows = s.ntok * p.s.G;
+        // q as the products' second operand: row g of each tile, values 4 step .. + 3 of this lane's
+        uint2 qf[F32 ? 1 : kMT][NT];
+        if (s.ntok > 0) {
+            auto q_row = [&](int r) -> const T * {
+                if (r >= rows) return nullptr;
+                uint32_t tok, h;
+                p.s.by_G.divmod((uint32_t)r, tok, h);
+                return static_cast<const T *>(p.q) + (s.tok0 + tok) * p.q_stride + (int64_t)(s.head * p.s.G + (int)h) * HD +
+                       t * (8 * kWords);
+            };
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const T *q = q_row(n * 8 + g);
+                if constexpr (F32) {
+                    if (warp < kMT) {
+                        const float4 x = q ? *reinterpret_cast<const float4 *>(q + warp * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        uint32_t a[kT], b[kT];
+                        split2(x.x, x.y, a);
+                        split2(x.z, x.w, b);
+#pragma unroll
+                        for (int i = 0; i < kT; ++i) q_s[((i * kMT + warp) * NT + n) * 32 + lane] = make_uint2(a[i], b[i]);
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < kMT; ++k)
+                        qf[k][n] = q ? *reinterpret_cast<const uint2 *>(q + k * 4) : make_uint2(0u, 0u);
+                }
+            }
+        }
+        if constexpr (F32) consumers_sync();  // (the end of the segment before has a barrier behind its reads)
+        float o[NT][kMT][4], m[NT][2], l[NT][2];
+        int lim[NT][2];  // keys that this lane's rows 2 t, 2 t + 1 see (rows beyond the valid ones like the last)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int i = 0; i < kMT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                m[n][e] = -INFINITY;
+                l[n][e] = 0.f;
+                const int tok = (int)p.s.by_G.div((uint32_t)max(0, min(n * 8 + 2 * t + e, rows - 1)));
+                lim[n][e] = p.s.causal ? max(0, min(s.kv, s.p0 + tok + 1)) : s.kv;
+            }
+        }
+        const int lim_all = p.s.causal ? max(0, min(s.kv, s.p0 + 1)) : s.kv;  // keys that every row sees
+        for (int kt = s.t0; ok && s.ntok > 0 && kt < s.t1; ++kt, ++fill) {
+            const uint32_t st = fill % C::kStages;
+            if (!(ok = wait(C::FULL + st, (fill / C::kStages) & 1u))) break;
+            const uint32_t base = sbase + st * C::kStage;
+            const int key0 = kt * C::kKT + warp * 16;
+            // ---- S^T = K Q^T ----
+            float sc[NT][2][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[n][c][e] = 0.f;
+            {
+                uint32_t w[2][kWords], s2[2], off[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if constexpr (HD == 128) {
+                        const uint4 x = lds128(base + k_at + e * 8 * C::kRow);
+                        w[e][0] = x.x; w[e][1] = x.y; w[e][2] = x.z; w[e][3] = x.w;
+                    } else {
+                        const uint2 x = lds64(base + k_at + e * 8 * C::kRow);
+                        w[e][0] = x.x; w[e][1] = x.y;
+                    }
+                    const uint32_t b = lds8(base + ks_at + e * 8 * C::kSRow);
+                    s2[e] = b * 0x100010u + 0x35803580u;
+                    off[e] = minus136(s2[e]);
+                }
+#pragma unroll
+                for (int k = 0; k < kMT; ++k) {
+                    uint32_t a[4];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t x = w[e][k / 2];
+                        a[e] = k % 2 ? values2<2>(x, s2[e], off[e]) : values2<0>(x, s2[e], off[e]);
+                        a[2 + e] = k % 2 ? values2<3>(x, s2[e], off[e]) : values2<1>(x, s2[e], off[e]);
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        if constexpr (F32) {
+#pragma unroll
+                            for (int i = kT - 1; i >= 0; --i) {
+                                const uint2 b = lds64(sbase + C::kQ + (((i * kMT + k) * NT + n) * 32 + lane) * 8);
+                                mma16816(sc[n][k & 1], a, b.x, b.y);
+                            }
+                        } else {
+                            mma16816(sc[n][k & 1], a, qf[k][n].x, qf[k][n].y);
+                        }
+                    }
+                }
+            }
+            // V's words and scales, under the softmax
+            uint32_t vw[2][2][kMT / 4], vb[2][2];  // [row k half][pair's element][word]
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if constexpr (HD == 128) {
+                        const uint2 x = lds64(base + v_at[e] + h * 8 * C::kRow);
+                        vw[h][e][0] = x.x; vw[h][e][1] = x.y;
+                    } else {
+                        vw[h][e][0] = lds32(base + v_at[e] + h * 8 * C::kRow);
+                    }
+                    vb[h][e] = lds8(base + vs_at[e] + h * 8 * C::kSRow);
+                }
+            // ---- softmax ----
+            uint32_t pf[NT][kT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float x[4];  // key g rows 2t, 2t+1; key g + 8
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = sc[n][0][e] + sc[n][1][e];
+                if (key0 + 16 > lim_all) {
+                    const int key = key0 + key_of<HD>(g);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (key + (e >> 1) * 8 >= lim[n][e & 1]) x[e] = -INFINITY;
+                }
+                // a row's maximum over its eight lanes is needed only when some lane's own exceeds the bound
+                float mx[2] = {fmaxf(x[0], x[2]) * p.scale_log2, fmaxf(x[1], x[3]) * p.scale_log2};
+                const bool need = mx[0] > m[n][0] + kRescale || mx[1] > m[n][1] + kRescale;
+                if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], d));
+                        const float mn = fmaxf(m[n][e], mx[e]);
+                        const float a = mn == -INFINITY ? 1.f : tc::ex2(m[n][e] - mn);
+                        m[n][e] = mn;
+                        l[n][e] *= a;
+#pragma unroll
+                        for (int i = 0; i < kMT; ++i) {
+                            o[n][i][e] *= a;
+                            o[n][i][2 + e] *= a;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float mb = m[n][e & 1] == -INFINITY ? 0.f : m[n][e & 1];
+                    const float y = fmaf(x[e], p.scale_log2, -mb);
+                    x[e] = F32 ? exp2f(y) : tc::ex2(y);
+                }
+                l[n][0] += x[0] + x[2];
+                l[n][1] += x[1] + x[3];
+                uint32_t lo[kT], hi[kT];
+                split2(x[0], x[1], lo);
+                split2(x[2], x[3], hi);
+#pragma unroll
+                for (int i = 0; i < kT; ++i) {
+                    pf[n][i][0] = transpose8x8(lo[i]);
+                    pf[n][i][1] = transpose8x8(hi[i]);
+                }
+            }
+            // ---- O^T += V^T P^T ----
+            uint32_t s2[2], off[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                s2[h] = scales2(vb[h][0], vb[h][1]);
+                off[h] = minus136(s2[h]);
+            }
+#pragma unroll
+            for (int x = 0; x < kMT / 4; ++x) {
+                uint32_t even[2], odd[2];  // the even and the odd columns of 8, four codes of either key
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    even[h] = __byte_perm(vw[h][0][x], vw[h][1][x], 0x5410);
+                    odd[h] = __byte_perm(vw[h][0][x], vw[h][1][x], 0x7632);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t a[4];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        a[2 * h] = fma_bf16x2(((even[h] >> (4 * j)) & 0x000f000fu) ^ 0x43084308u, s2[h], off[h]);
+                        a[2 * h + 1] = fma_bf16x2(((odd[h] >> (4 * j)) & 0x000f000fu) ^ 0x43084308u, s2[h], off[h]);
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = kT - 1; i >= 0; --i) mma16816(o[n][x * 4 + j], a, pf[n][i][0], pf[n][i][1]);
+                }
+            }
+            // The stage is released only when its rows have arrived in registers (see paged_decode.cu): the arrive's
+            // address depends on a result of every product of V, compared with a NaN that no product gives.
+            bool never = false;
+#pragma unroll
+            for (int i = 0; i < kMT; ++i) never |= __float_as_uint(o[0][i][0]) == 0x7fa5a5a5u;
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(BAR(C::EMPTY + st) + (never ? 8u : 0u));
+        }
+        // ---- merge the eight warps' states and write the rows ----
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], d);
+                if (g == 0) ml[(warp * NT + n) * 8 + 2 * t + e] = make_float2(m[n][e], l[n][e]);
+            }
+        if (!consumers_all(ok) || s.ntok == 0) return;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float mm = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, ml[(w * NT + n) * 8 + 2 * t + e].x);
+                const float a = mm == -INFINITY ? 0.f : tc::ex2(m[n][e] - mm);
+                float *d = xch + ((warp * NT + n) * 8 + 2 * t + e) * C::kXRow + g * (HD / 8);
+#pragma unroll
+                for (int i = 0; i < kMT; i += 2)  // columns 2 i .. 2 i + 3 of the lane's
+                    *reinterpret_cast<float4 *>(d + 2 * i) = make_float4(o[n][i][e] * a, o[n][i][2 + e] * a, o[n][i + 1][e] * a,
+                                                                         o[n][i + 1][2 + e] * a);
+            }
+        consumers_sync();
+        const bool whole = s.t0 == 0 && s.t1 == s.tiles;
+        float *slot = part_slot(p.w, HD, blockIdx.x, s.t0 == 0 ? 1 : 0);
+        constexpr int kLanes = HD / 4, kAtOnce = kWarps * 32 / kLanes;  // threads of a row, 4 columns each
+        const int col = tid % kLanes * 4;
+        for (int r = tid / kLanes; r < rows; r += kAtOnce) {
+            float M = -INFINITY, L = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * NT * 8 + r].x);
+            const float Mb = M == -INFINITY ? 0.f : M;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float2 x = ml[w * NT * 8 + r];
+                L = fmaf(x.y, tc::ex2(x.x - Mb), L);
+                const float4 f = *reinterpret_cast<const float4 *>(xch + (w * NT * 8 + r) * C::kXRow + col);
+                v.x += f.x; v.y += f.y; v.z += f.z; v.w += f.w;
+            }
+            uint32_t tok, h;
+            p.s.by_G.divmod((uint32_t)r, tok, h);
+            const int head = s.head * p.s.G + (int)h;
+            if (whole) {
+                const float inv = L == 0.f ? 1.f : 1.f / L;
+                T *to = static_cast<T *>(p.out) + (s.tok0 + tok) * p.out_stride + (int64_t)head * HD + col;
+                if constexpr (F32)
+                    *reinterpret_cast<float4 *>(to) = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+                else
+                    *reinterpret_cast<uint2 *>(to) =
+                        make_uint2(float2_to_bf16x2(v.x * inv, v.y * inv), float2_to_bf16x2(v.z * inv, v.w * inv));
+                if (col == 0)
+                    p.lse[(s.tok0 + tok) * p.hq + head] =
+                        L == 0.f ? -INFINITY : (M + (F32 ? log2f(L) : __log2f(L))) * kLn2;
+            } else {
+                *reinterpret_cast<float4 *>(slot + (size_t)r * HD + col) = v;
+                if (col == 0) {
+                    slot[(size_t)p.w.rows * HD + r] = M;
+                    slot[(size_t)p.w.rows * (HD + 1) + r] = L;
+                }
+            }
+        }
+        consumers_sync();  // xch, ml and q_s are free for the next segment
+    }
+}
+
+template <int HD, int NT, bool F32>
+__global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, F32>::kCtas)) paged_q4_few_kernel(const __grid_constant__ FewParams p) {
+    using C = Cfg<HD, NT, F32>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t raw = tc::smem_u32(smem_raw);
+    const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
+    uint8_t *smem = smem_raw + pad;
+    const uint32_t sbase = raw + pad;
+    __shared__ SchedShared sh;
+    __shared__ uint32_t skip;
+    if (threadIdx.x == 0) {
+        tc::prefetch_tmap(&p.tk);
+        tc::prefetch_tmap(&p.tv);
+        const uint32_t bar = sbase + C::kBar;
+        for (int i = 0; i < C::kStages; ++i) {
+            tc::mbar_init(bar + 8 * (C::FULL + i), 1);
+            tc::mbar_init(bar + 8 * (C::EMPTY + i), kWarps);
+        }
+        for (int i = 0; i < kSegSlots; ++i) {
+            tc::mbar_init(bar + 8 * (C::SEG_FULL + i), 1);
+            tc::mbar_init(bar + 8 * (C::SEG_EMPTY + i), kWarps);
+        }
+        tc::fence_barrier_init();
+    }
+    begin_in_order(p.second);
+    // a bounded wait of an earlier kernel ran out: do no work until usp_check clears it
+    if (threadIdx.x == 0) skip = *reinterpret_cast<volatile int *>(p.status) != 0;
+    const bool work = sched_scan<kThreads, C::kKT>(p.s, sh);
+    __syncthreads();
+    if (!work || skip) {
+        if (threadIdx.x == 0) p.w.head[blockIdx.x] = no_part(sh);
+    } else if ((threadIdx.x >> 5) == kWarps) {
+        producer<HD, NT, F32>(p, sh, smem, sbase);
+    } else {
+        consumer<HD, NT, F32>(p, smem, sbase);
+    }
+    end_in_order(p.second);
+}
+
+template <int HD, int NT, bool F32> int launch_typed(FewParams &p, cudaStream_t s) {
+    using C = Cfg<HD, NT, F32>;
+    static_assert(C::kSmem + 2048 <= (C::kCtas == 2 ? 114 : 227) * 1024, "shared memory per CTA");
+    static std::mutex mu;
+    static bool attr_set[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return USP_ERR_CUDA;
+    {
+        std::lock_guard<std::mutex> lk(mu);
+        if (dev < 0 || dev >= 64) return USP_ERR_UNSUPPORTED;
+        if (!attr_set[dev]) {
+            if (cudaFuncSetAttribute(paged_q4_few_kernel<HD, NT, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) !=
+                cudaSuccess)
+                return USP_ERR_CUDA;
+            attr_set[dev] = true;
+        }
+    }
+    p.s.min_span = C::kMinSpan;
+    return launch_overlapped(paged_q4_few_kernel<HD, NT, F32>, dim3((unsigned)p.w.ctas), kThreads, C::kSmem, s, p);
+}
+
+}  // namespace
+
+int q4_few_ctas(int sms, int rows) { return rows == 8 ? 2 * sms : sms; }
+
+int launch_paged_q4_few(const PagedQ4Args &a, int G, int rows, int n_hi, bool second, const PartSpace &w, cudaStream_t s) {
+    const DeviceInfo *di = device_info();
+    if (!di) return USP_ERR_CUDA;
+    FewParams p{};
+    const int ps = 1 << a.log_ps;
+    const uint32_t box = (uint32_t)std::min(ps, 16 * kWarps);
+    if (!make_codes_tmap(&p.tk, a.k, a.num_pages, a.k_page, a.hkv, ps, a.hd, box) ||
+        !make_codes_tmap(&p.tv, a.v, a.num_pages, a.v_page, a.hkv, ps, a.hd, box))
+        return USP_ERR_CUDA;
+    p.s.cu = a.cu; p.s.kv = a.kv;
+    p.s.tokens = a.tokens; p.s.max_keys = q4_max_keys(a);
+    p.s.nreq = a.nreq; p.s.hkv = a.hq / G; p.s.G = G;
+    p.s.tb = rows / G; p.s.causal = a.causal;
+    p.s.n_lo = 0; p.s.n_hi = n_hi;
+    p.s.over = kOver; p.s.long_parts = kFewParts;
+    p.s.inv_ctas = 1.0f / (float)w.ctas;
+    p.s.by_tb = FastDiv((uint32_t)p.s.tb); p.s.by_G = FastDiv((uint32_t)G);
+    p.by_sub = FastDiv((uint32_t)(a.G / G));
+    p.w = w;
+    p.q = a.q; p.out = a.out; p.lse = a.lse;
+    p.ks = a.ks; p.vs = a.vs; p.ks_page = a.ks_page; p.vs_page = a.vs_page;
+    p.table = a.table;
+    p.status = di->status;
+    p.q_stride = a.q_stride; p.out_stride = a.out_stride; p.table_stride = a.table_stride;
+    p.num_pages = (int32_t)a.num_pages; p.log_ps = a.log_ps; p.hq = a.hq;
+    p.scale_log2 = a.scale_log2;
+    p.second = second;
+    auto go = [&](auto hd, auto nt, auto f32) {
+        return launch_typed<decltype(hd)::value, decltype(nt)::value, decltype(f32)::value>(p, s);
+    };
+    auto with = [&](auto hd, auto nt) {
+        return a.dtype == USP_F32 ? go(hd, nt, std::true_type{}) : go(hd, nt, std::false_type{});
+    };
+    using I64 = std::integral_constant<int, 64>;
+    using I128 = std::integral_constant<int, 128>;
+    using One = std::integral_constant<int, 1>;
+    using Two = std::integral_constant<int, 2>;
+    if (rows == 8) return a.hd == 128 ? with(I128{}, One{}) : with(I64{}, One{});
+    return a.hd == 128 ? with(I128{}, Two{}) : with(I64{}, Two{});
+}
+
+}  // namespace usp

@@ -76,17 +76,4 @@ __device__ __forceinline__ uint32_t q4_pack(const float (&x)[8], uint32_t b) {
 
 int check_q4_dims(const usp_q4_dims &d);
 
-// usp_paged_attn_q4's arguments, checked and with the defaults filled in (q's and out's strides in elements, the pages' in
-// bytes)
-struct PagedQ4Args {
-    const void *q;
-    const uint8_t *k, *v, *ks, *vs;
-    const int32_t *table, *cu, *kv;
-    void *out;
-    float *lse;
-    int64_t tokens, q_stride, out_stride, table_stride, num_pages, k_page, v_page, ks_page, vs_page;
-    int32_t nreq, max_pages, max_new, hq, hkv, G, hd, log_ps, causal, dtype;
-    float scale_log2;  // softmax scale * log2(e)
-};
-
 }  // namespace usp
