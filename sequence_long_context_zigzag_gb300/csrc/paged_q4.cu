@@ -66,17 +66,17 @@ Route route(const usp_paged_q4_desc &d, int sms) {
     Route r{};
     r.few_G = few_heads(d.hq / d.cache.hkv);
     r.few_rows = r.few_G * (int64_t)std::max(1, d.max_new) <= 8 ? 8 : 16;
-    r.few_ctas = q4_few_ctas(sms, r.few_rows);
+    r.few_ctas = q4_few_ctas(sms, r.few_rows, d.dtype);
     return r;
 }
 
 size_t workspace_bytes_of(const Route &r, int hd) { return part_bytes(r.few_ctas, r.few_rows, hd); }
 
-// What the caller provides: what every call with this max_new or a smaller one uses (the layout of 8 rows has twice the
-// headers of that of 16).
+// What the caller provides: what every call with this max_new or a smaller one uses (the layout of 8 rows has more
+// headers than that of 16).
 size_t workspace_bytes_for(const usp_paged_q4_desc &d, int sms) {
     const Route r = route(d, sms);
-    return std::max(workspace_bytes_of(r, d.cache.hd), part_bytes(q4_few_ctas(sms, 8), 8, d.cache.hd));
+    return std::max(workspace_bytes_of(r, d.cache.hd), part_bytes(q4_few_ctas(sms, 8, d.dtype), 8, d.cache.hd));
 }
 
 PartSpace part_space(char *&at, int ctas, int rows, int hd) {

@@ -13,7 +13,7 @@
 // it, the conversion: about 1.5 instructions a value beside some 0.6 of products, loads and softmax, where an SM issues
 // 128 lanes a clock. Layout of the work:
 //  - spans of equal key counts per CTA (paged_sched.cuh); a producer warp walks the span and streams K, V (TMA boxes) and
-//    their scales (bulk copies) of 128 keys a tile through a ring of stages; eight consumer warps, each with 16 keys of
+//    their scales (bulk copies) of 128 keys a tile through a ring of stages; four consumer warps, each with 32 keys of
 //    the tile and a softmax state of its own, which merge through shared memory at a unit's end;
 //  - S^T comes out of the product with a key per lane group and rows along lanes; two 8x8 transposes (movmatrix) make
 //    the weights the operand of the second product;
@@ -34,7 +34,8 @@ namespace usp {
 namespace {
 
 constexpr int kOver = 512;     // a unit's constant cost, in keys
-constexpr int kWarps = 8;      // consumers
+constexpr int kWarps = 4;      // consumers
+constexpr int kW = 2;          // 16-key steps per warp and tile
 constexpr int kThreads = (kWarps + 1) * 32;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr float kRescale = 8.0f;  // log2 units
@@ -43,14 +44,14 @@ constexpr float kLn2 = 0.69314718055994531f;
 // NT: tiles of 8 query rows; F32: q, out and the weights in three bf16 terms
 template <int HD, int NT, bool F32> struct Cfg {
     static constexpr int kTerms = F32 ? 3 : 1;
-    static constexpr int kCtas = NT == 1 ? 2 : 1;         // per SM
-    static constexpr int kKT = 16 * kWarps;               // keys per tile
+    static constexpr int kCtas = NT == 1 && !F32 ? 3 : 2; // per SM
+    static constexpr int kKT = 16 * kW * kWarps;          // keys per tile
     static constexpr int kMinSpan = 192;                  // keys per CTA below which fewer CTAs work
     static_assert(kMinSpan > kKT, "a span holds more than a tile");
     static constexpr int kRow = q4_code_bytes(HD), kSRow = q4_scale_bytes(HD);
     static constexpr int kCodes = kKT * kRow, kScales = kKT * kSRow;
     static constexpr int kStage = 2 * (kCodes + kScales); // K codes, V codes, K scales, V scales
-    static constexpr int kStages = kCtas == 2 ? (HD == 128 ? 4 : 8) : 8;
+    static constexpr int kStages = (kCtas == 3 || F32 ? 3 : 4) * (HD == 128 ? 1 : 2);
     static constexpr int kXRow = HD + 4;                  // exchange row in floats
     static constexpr int kX = kStages * kStage;           // [warp][row][kXRow]
     static constexpr int kML = kX + kWarps * NT * 8 * kXRow * 4;
@@ -121,10 +122,21 @@ __device__ __forceinline__ uint32_t scales2(uint32_t lo, uint32_t hi) { return l
 __device__ __forceinline__ uint32_t minus136(uint32_t s2) {
     return fma_bf16x2(s2, 0xc308c308u, 0x80008000u);  // -136 s - 0
 }
-// codes j (low nibbles of the halves of word >> 4 j), as values
-template <int j> __device__ __forceinline__ uint32_t values2(uint32_t word, uint32_t s2, uint32_t off) {
-    return fma_bf16x2(((word >> (4 * j)) & 0x000f000fu) ^ 0x43084308u, s2, off);
-}
+// The two constants of a conversion in registers: an instruction has room for one constant of its own, and with both known
+// the compiler takes two instructions (143 instead of 77 logic operations per 16 keys, a quarter more time).
+struct Nibbles {
+    uint32_t mask, magic;
+    __device__ __forceinline__ Nibbles() {
+        asm volatile("mov.b32 %0, 0x000f000f;" : "=r"(mask));
+        asm volatile("mov.b32 %0, 0x43084308;" : "=r"(magic));
+    }
+    // codes j (the low nibbles of the halves of word >> 4 j) as values
+    __device__ __forceinline__ uint32_t values(uint32_t word, int j, uint32_t s2, uint32_t off) const {
+        uint32_t x;
+        asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(x) : "r"(word >> (4 * j)), "r"(mask), "r"(magic));  // (a & b) ^ c
+        return fma_bf16x2(x, s2, off);
+    }
+};
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); }
 __device__ __forceinline__ bool consumers_all(bool x) {
     uint32_t r;
@@ -149,7 +161,12 @@ template <int kTerms> __device__ __forceinline__ void split2(float x, float y, u
     }
 }
 
-// The key of a warp's 16 that is row k of the products (k < 8; row k + 8: 8 further). Rows of 64 bytes (hd 128): the pairs of
+// a whole warp's wait that did not end at once (out of line: the loop has no registers for it)
+static __device__ __noinline__ bool wait_longer(uint32_t bar, uint32_t parity, int *status) {
+    return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, status, USP_ERR_TIMEOUT, kWaitLimitNs));
+}
+
+// The key of a step's 16 that is row k of the products (k < 8; row k + 8: 8 further). Rows of 64 bytes (hd 128): the pairs of
 // K's 16-byte loads (k, k + 1) and the quadruples of V's 8-byte loads (k, k + 2, ..) then lie in different banks; rows of 32: the
 // quadruples of K's 8-byte and V's 4-byte loads.
 template <int HD> __device__ __forceinline__ int key_of(int k) {
@@ -240,24 +257,25 @@ template <int HD, int NT, bool F32> __device__ void consumer(const FewParams &p,
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     auto BAR = [&](int i) { return sbase + C::kBar + 8u * i; };
     auto wait = [&](int bar, uint32_t parity) {
-        const bool r = tc::mbar_wait(BAR(bar), parity, p.status, USP_ERR_TIMEOUT, kWaitLimitNs);
-        return (bool)__all_sync(0xffffffffu, r);
+        return __all_sync(0xffffffffu, tc::mbar_try_wait(BAR(bar), parity)) || wait_longer(BAR(bar), parity, p.status);
     };
     float *xch = reinterpret_cast<float *>(smem + C::kX);
     float2 *ml = reinterpret_cast<float2 *>(smem + C::kML);  // [warp][8 NT rows]
     uint2 *q_s = reinterpret_cast<uint2 *>(smem + C::kQ);
-    // addresses inside a stage: K's row k = g (and + 8), this lane's values; V's rows 2 t, 2 t + 1 (and + 8), its columns
-    const int kkey = warp * 16 + key_of<HD>(g);
+    const Nibbles nib;
+    // addresses inside a stage: K's row k = g (and + 8), this lane's values; V's rows 2 t, 2 t + 1 (and + 8), its columns; a
+    // step's rows are 16 further
+    const int kkey = warp * 16 * kW + key_of<HD>(g);
     const uint32_t k_at = kkey * C::kRow + (HD == 128 ? (t ^ ((kkey >> 1) & 3)) * 16 : t * 8);
     const uint32_t ks_at = 2 * C::kCodes + kkey * C::kSRow + (HD == 128 ? t : t >> 1);
     uint32_t v_at[2], vs_at[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-        const int key = warp * 16 + key_of<HD>(2 * t + e);
+        const int key = warp * 16 * kW + key_of<HD>(2 * t + e);
         v_at[e] = C::kCodes + key * C::kRow + (HD == 128 ? ((g >> 1) ^ ((key >> 1) & 3)) * 16 + (g & 1) * 8 : g * 4);
         vs_at[e] = 2 * C::kCodes + C::kScales + key * C::kSRow + (HD == 128 ? g >> 1 : g >> 2);
     }
-    uint32_t fill = 0;
+    uint32_t st = 0, st_phase = 0;  // the stage of the next tile, and its fill's parity
     for (uint32_t nseg = 0;; ++nseg) {
         // Every warp reaches exactly one consumers_all per segment, also after a failed wait and at the end, and
         // leaves only by its result: so no warp waits for one that has gone.
@@ -285,13 +303,13 @@ template <int HD, int NT, bool F32> __device__ void consumer(const FewParams &p,
             for (int n = 0; n < NT; ++n) {
                 const T *q = q_row(n * 8 + g);
                 if constexpr (F32) {
-                    if (warp < kMT) {
-                        const float4 x = q ? *reinterpret_cast<const float4 *>(q + warp * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int k = warp; k < kMT; k += kWarps) {
+                        const float4 x = q ? *reinterpret_cast<const float4 *>(q + k * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
                         uint32_t a[kT], b[kT];
                         split2(x.x, x.y, a);
                         split2(x.z, x.w, b);
 #pragma unroll
-                        for (int i = 0; i < kT; ++i) q_s[((i * kMT + warp) * NT + n) * 32 + lane] = make_uint2(a[i], b[i]);
+                        for (int i = 0; i < kT; ++i) q_s[((i * kMT + k) * NT + n) * 32 + lane] = make_uint2(a[i], b[i]);
                     }
                 } else {
 #pragma unroll
@@ -301,7 +319,7 @@ template <int HD, int NT, bool F32> __device__ void consumer(const FewParams &p,
             }
         }
         if constexpr (F32) consumers_sync();  // (the end of the segment before has a barrier behind its reads)
-        float o[NT][kMT][4], m[NT][2], l[NT][2];
+        float o[NT][kMT][4], m[NT][2], l[NT][2], nmb[NT][2];  // nmb: -m, or 0 before the first key
         int lim[NT][2];  // keys that this lane's rows 2 t, 2 t + 1 see (rows beyond the valid ones like the last)
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -312,92 +330,106 @@ template <int HD, int NT, bool F32> __device__ void consumer(const FewParams &p,
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 m[n][e] = -INFINITY;
-                l[n][e] = 0.f;
+                l[n][e] = nmb[n][e] = 0.f;
                 const int tok = (int)p.s.by_G.div((uint32_t)max(0, min(n * 8 + 2 * t + e, rows - 1)));
                 lim[n][e] = p.s.causal ? max(0, min(s.kv, s.p0 + tok + 1)) : s.kv;
             }
         }
         const int lim_all = p.s.causal ? max(0, min(s.kv, s.p0 + 1)) : s.kv;  // keys that every row sees
-        for (int kt = s.t0; ok && s.ntok > 0 && kt < s.t1; ++kt, ++fill) {
-            const uint32_t st = fill % C::kStages;
-            if (!(ok = wait(C::FULL + st, (fill / C::kStages) & 1u))) break;
+        const int t1 = s.ntok > 0 ? s.t1 : s.t0;
+        for (int kt = s.t0; ok && kt < t1; ++kt) {
+            if (!(ok = wait(C::FULL + st, st_phase))) break;
             const uint32_t base = sbase + st * C::kStage;
-            const int key0 = kt * C::kKT + warp * 16;
+            const int key0 = kt * C::kKT + warp * 16 * kW;
             // ---- S^T = K Q^T ----
-            float sc[NT][2][4];
+            float sc[kW][NT][4];
+            uint32_t w[kW][2][kWords], kb[kW][2];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[n][c][e] = 0.f;
-            {
-                uint32_t w[2][kWords], s2[2], off[2];
+            for (int i = 0; i < kW; ++i)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
+                    const uint32_t at = base + k_at + (i * 16 + e * 8) * C::kRow;
                     if constexpr (HD == 128) {
-                        const uint4 x = lds128(base + k_at + e * 8 * C::kRow);
-                        w[e][0] = x.x; w[e][1] = x.y; w[e][2] = x.z; w[e][3] = x.w;
+                        const uint4 x = lds128(at);
+                        w[i][e][0] = x.x; w[i][e][1] = x.y; w[i][e][2] = x.z; w[i][e][3] = x.w;
                     } else {
-                        const uint2 x = lds64(base + k_at + e * 8 * C::kRow);
-                        w[e][0] = x.x; w[e][1] = x.y;
+                        const uint2 x = lds64(at);
+                        w[i][e][0] = x.x; w[i][e][1] = x.y;
                     }
-                    const uint32_t b = lds8(base + ks_at + e * 8 * C::kSRow);
-                    s2[e] = b * 0x100010u + 0x35803580u;
+                    kb[i][e] = lds8(base + ks_at + (i * 16 + e * 8) * C::kSRow);
+                }
+#pragma unroll
+            for (int i = 0; i < kW; ++i) {
+                uint32_t s2[2], off[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    s2[e] = kb[i][e] * 0x100010u + 0x35803580u;
                     off[e] = minus136(s2[e]);
                 }
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[i][n][e] = 0.f;
 #pragma unroll
                 for (int k = 0; k < kMT; ++k) {
                     uint32_t a[4];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const uint32_t x = w[e][k / 2];
-                        a[e] = k % 2 ? values2<2>(x, s2[e], off[e]) : values2<0>(x, s2[e], off[e]);
-                        a[2 + e] = k % 2 ? values2<3>(x, s2[e], off[e]) : values2<1>(x, s2[e], off[e]);
+                        a[e] = nib.values(w[i][e][k / 2], k % 2 * 2, s2[e], off[e]);
+                        a[2 + e] = nib.values(w[i][e][k / 2], k % 2 * 2 + 1, s2[e], off[e]);
                     }
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         if constexpr (F32) {
 #pragma unroll
-                            for (int i = kT - 1; i >= 0; --i) {
-                                const uint2 b = lds64(sbase + C::kQ + (((i * kMT + k) * NT + n) * 32 + lane) * 8);
-                                mma16816(sc[n][k & 1], a, b.x, b.y);
+                            for (int x = kT - 1; x >= 0; --x) {
+                                const uint2 b = lds64(sbase + C::kQ + (((x * kMT + k) * NT + n) * 32 + lane) * 8);
+                                mma16816(sc[i][n], a, b.x, b.y);
                             }
                         } else {
-                            mma16816(sc[n][k & 1], a, qf[k][n].x, qf[k][n].y);
+                            mma16816(sc[i][n], a, qf[k][n].x, qf[k][n].y);
                         }
                     }
                 }
             }
             // V's words and scales, under the softmax
-            uint32_t vw[2][2][kMT / 4], vb[2][2];  // [row k half][pair's element][word]
+            uint32_t vw[kW][2][2][kMT / 4], vb[kW][2][2];  // [step][half of the step's keys][pair's element][word]
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int i = 0; i < kW; ++i)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    if constexpr (HD == 128) {
-                        const uint2 x = lds64(base + v_at[e] + h * 8 * C::kRow);
-                        vw[h][e][0] = x.x; vw[h][e][1] = x.y;
-                    } else {
-                        vw[h][e][0] = lds32(base + v_at[e] + h * 8 * C::kRow);
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        if constexpr (HD == 128) {
+                            const uint2 x = lds64(base + v_at[e] + (i * 16 + h * 8) * C::kRow);
+                            vw[i][h][e][0] = x.x; vw[i][h][e][1] = x.y;
+                        } else {
+                            vw[i][h][e][0] = lds32(base + v_at[e] + (i * 16 + h * 8) * C::kRow);
+                        }
+                        vb[i][h][e] = lds8(base + vs_at[e] + (i * 16 + h * 8) * C::kSRow);
                     }
-                    vb[h][e] = lds8(base + vs_at[e] + h * 8 * C::kSRow);
-                }
             // ---- softmax ----
-            uint32_t pf[NT][kT][2];
+            uint32_t pf[kW][NT][kT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                float x[4];  // key g rows 2t, 2t+1; key g + 8
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] = sc[n][0][e] + sc[n][1][e];
-                if (key0 + 16 > lim_all) {
+                // sc: key g rows 2t, 2t+1; key g + 8
+                if (key0 + 16 * kW > lim_all) {
                     const int key = key0 + key_of<HD>(g);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (key + (e >> 1) * 8 >= lim[n][e & 1]) x[e] = -INFINITY;
+                    for (int i = 0; i < kW; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (key + i * 16 + (e >> 1) * 8 >= lim[n][e & 1]) sc[i][n][e] = -INFINITY;
                 }
                 // a row's maximum over its eight lanes is needed only when some lane's own exceeds the bound
-                float mx[2] = {fmaxf(x[0], x[2]) * p.scale_log2, fmaxf(x[1], x[3]) * p.scale_log2};
+                float mx[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    mx[e] = fmaxf(sc[0][n][e], sc[0][n][2 + e]);
+#pragma unroll
+                    for (int i = 1; i < kW; ++i) mx[e] = tc::max3(mx[e], sc[i][n][e], sc[i][n][2 + e]);
+                    mx[e] *= p.scale_log2;
+                }
                 const bool need = mx[0] > m[n][0] + kRescale || mx[1] > m[n][1] + kRescale;
                 if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
@@ -407,6 +439,7 @@ template <int HD, int NT, bool F32> __device__ void consumer(const FewParams &p,
                         const float mn = fmaxf(m[n][e], mx[e]);
                         const float a = mn == -INFINITY ? 1.f : tc::ex2(m[n][e] - mn);
                         m[n][e] = mn;
+                        nmb[n][e] = mn == -INFINITY ? 0.f : -mn;
                         l[n][e] *= a;
 #pragma unroll
                         for (int i = 0; i < kMT; ++i) {
@@ -416,60 +449,71 @@ template <int HD, int NT, bool F32> __device__ void consumer(const FewParams &p,
                     }
                 }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float mb = m[n][e & 1] == -INFINITY ? 0.f : m[n][e & 1];
-                    const float y = fmaf(x[e], p.scale_log2, -mb);
-                    x[e] = F32 ? exp2f(y) : tc::ex2(y);
-                }
-                l[n][0] += x[0] + x[2];
-                l[n][1] += x[1] + x[3];
-                uint32_t lo[kT], hi[kT];
-                split2(x[0], x[1], lo);
-                split2(x[2], x[3], hi);
+                for (int i = 0; i < kW; ++i) {
+                    float x[4];
 #pragma unroll
-                for (int i = 0; i < kT; ++i) {
-                    pf[n][i][0] = transpose8x8(lo[i]);
-                    pf[n][i][1] = transpose8x8(hi[i]);
+                    for (int e = 0; e < 4; ++e) {
+                        const float y = fmaf(sc[i][n][e], p.scale_log2, nmb[n][e & 1]);
+                        x[e] = F32 ? exp2f(y) : tc::ex2(y);
+                    }
+                    l[n][0] += x[0] + x[2];
+                    l[n][1] += x[1] + x[3];
+                    uint32_t lo[kT], hi[kT];
+                    split2(x[0], x[1], lo);
+                    split2(x[2], x[3], hi);
+#pragma unroll
+                    for (int c = 0; c < kT; ++c) {
+                        pf[i][n][c][0] = transpose8x8(lo[c]);
+                        pf[i][n][c][1] = transpose8x8(hi[c]);
+                    }
                 }
             }
             // ---- O^T += V^T P^T ----
-            uint32_t s2[2], off[2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                s2[h] = scales2(vb[h][0], vb[h][1]);
-                off[h] = minus136(s2[h]);
-            }
-#pragma unroll
-            for (int x = 0; x < kMT / 4; ++x) {
-                uint32_t even[2], odd[2];  // the even and the odd columns of 8, four codes of either key
+            for (int i = 0; i < kW; ++i) {
+                uint32_t s2[2], off[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    even[h] = __byte_perm(vw[h][0][x], vw[h][1][x], 0x5410);
-                    odd[h] = __byte_perm(vw[h][0][x], vw[h][1][x], 0x7632);
+                    s2[h] = scales2(vb[i][h][0], vb[i][h][1]);
+                    off[h] = minus136(s2[h]);
                 }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t a[4];
+                for (int x = 0; x < kMT / 4; ++x) {
+                    uint32_t even[2], odd[2];  // the even and the odd columns of 8, four codes of either key
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        a[2 * h] = fma_bf16x2(((even[h] >> (4 * j)) & 0x000f000fu) ^ 0x43084308u, s2[h], off[h]);
-                        a[2 * h + 1] = fma_bf16x2(((odd[h] >> (4 * j)) & 0x000f000fu) ^ 0x43084308u, s2[h], off[h]);
+                        even[h] = __byte_perm(vw[i][h][0][x], vw[i][h][1][x], 0x5410);
+                        odd[h] = __byte_perm(vw[i][h][0][x], vw[i][h][1][x], 0x7632);
                     }
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t a[4];
 #pragma unroll
-                        for (int i = kT - 1; i >= 0; --i) mma16816(o[n][x * 4 + j], a, pf[n][i][0], pf[n][i][1]);
+                        for (int h = 0; h < 2; ++h) {
+                            a[2 * h] = nib.values(even[h], j, s2[h], off[h]);
+                            a[2 * h + 1] = nib.values(odd[h], j, s2[h], off[h]);
+                        }
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int c = kT - 1; c >= 0; --c) mma16816(o[n][x * 4 + j], a, pf[i][n][c][0], pf[i][n][c][1]);
+                    }
                 }
             }
             // The stage is released only when its rows have arrived in registers (see paged_decode.cu): the arrive's
-            // address depends on a result of every product of V, compared with a NaN that no product gives.
-            bool never = false;
+            // address depends on a result of every product of V. Their bits' conjunction is this NaN only if each is a NaN
+            // and not all the one that products give.
+            uint32_t all = 0xffffffffu;
 #pragma unroll
-            for (int i = 0; i < kMT; ++i) never |= __float_as_uint(o[0][i][0]) == 0x7fa5a5a5u;
+            for (int i = 0; i < kMT; ++i) all &= __float_as_uint(o[0][i][0]);
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(BAR(C::EMPTY + st) + (never ? 8u : 0u));
+            if (lane == 0) tc::mbar_arrive(BAR(C::EMPTY + st) + (all == 0x7fa5a5a5u ? 8u : 0u));
+            if (++st == C::kStages) {
+                st = 0;
+                st_phase ^= 1u;
+            }
         }
-        // ---- merge the eight warps' states and write the rows ----
+        // ---- merge the warps' states and write the rows ----
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -578,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, F32>::kCtas)) paged_q4_
 
 template <int HD, int NT, bool F32> int launch_typed(FewParams &p, cudaStream_t s) {
     using C = Cfg<HD, NT, F32>;
-    static_assert(C::kSmem + 2048 <= (C::kCtas == 2 ? 114 : 227) * 1024, "shared memory per CTA");
+    static_assert(C::kSmem + 2048 <= (228 / C::kCtas - 1) * 1024, "shared memory per CTA");
     static std::mutex mu;
     static bool attr_set[64] = {};
     int dev = 0;
@@ -599,14 +643,16 @@ template <int HD, int NT, bool F32> int launch_typed(FewParams &p, cudaStream_t 
 
 }  // namespace
 
-int q4_few_ctas(int sms, int rows) { return rows == 8 ? 2 * sms : sms; }
+int q4_few_ctas(int sms, int rows, int dtype) {
+    return (rows == 8 && dtype == USP_BF16 ? Cfg<128, 1, false>::kCtas : Cfg<128, 2, false>::kCtas) * sms;
+}
 
 int launch_paged_q4_few(const PagedQ4Args &a, int G, int rows, int n_hi, bool second, const PartSpace &w, cudaStream_t s) {
     const DeviceInfo *di = device_info();
     if (!di) return USP_ERR_CUDA;
     FewParams p{};
     const int ps = 1 << a.log_ps;
-    const uint32_t box = (uint32_t)std::min(ps, 16 * kWarps);
+    const uint32_t box = (uint32_t)std::min(ps, 16 * kW * kWarps);
     if (!make_codes_tmap(&p.tk, a.k, a.num_pages, a.k_page, a.hkv, ps, a.hd, box) ||
         !make_codes_tmap(&p.tv, a.v, a.num_pages, a.v_page, a.hkv, ps, a.hd, box))
         return USP_ERR_CUDA;
