@@ -26,26 +26,36 @@ inline int64_t q4_max_keys(const PagedQ4Args &a) {
     return held < most ? held : most;
 }
 
-// A cache's codes as bytes (hd / 2, hkv * page_size, num_pages), in boxes of whole rows, `rows` of one page; rows of 64
-// bytes in the 64-byte swizzle (16-byte piece c of row r at c ^ ((r >> 1) & 3)), rows of 32 as they are. A page outside the
-// cache is out of bounds in the last dimension: the box reads zeros, codes that stand for 0.
+// A cache's codes as lines of 128 bytes, 2 keys of hd 128 or 4 of hd 64 each: (128, lines of a page, num_pages), in boxes
+// of `rows` keys of one page, 128-byte swizzle: 16-byte piece c of line l lies at c ^ (l % 8). (As rows of a key, 64 bytes,
+// the copies of a page of 16 tokens ran at a bit over half the rate.) A page outside the cache is out of bounds in the last
+// dimension: the box reads zeros, codes that stand for 0.
 inline bool make_codes_tmap(CUtensorMap *m, const void *base, int64_t pages, int64_t page_stride, int32_t hkv, int32_t ps,
                             int32_t hd, uint32_t rows) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return false;
-    const cuuint64_t dims[3] = {(cuuint64_t)q4_code_bytes(hd), (cuuint64_t)hkv * ps, (cuuint64_t)pages};
-    const cuuint64_t strides[2] = {(cuuint64_t)q4_code_bytes(hd), (cuuint64_t)page_stride};
-    const cuuint32_t box[3] = {(cuuint32_t)q4_code_bytes(hd), rows, 1}, estr[3] = {1, 1, 1};
+    const uint32_t keys = 128 / q4_code_bytes(hd);  // of a line
+    const cuuint64_t dims[3] = {128, (cuuint64_t)hkv * ps / keys, (cuuint64_t)pages};
+    const cuuint64_t strides[2] = {128, (cuuint64_t)page_stride};
+    const cuuint32_t box[3] = {128, rows / keys, 1}, estr[3] = {1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, hd == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// where byte b of a key's codes lies in a tile (1024-byte aligned) that the boxes filled
+template <int HD> __device__ __forceinline__ uint32_t codes_at(uint32_t key, uint32_t b) {
+    const uint32_t x = key * q4_code_bytes(HD) + b;
+    return x ^ ((x >> 3) & 0x70u);
 }
 
-// `bytes` (a multiple of 16) from global to shared memory, both 16-byte aligned, completion counted on an mbarrier
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
-                 : "memory");
+// 16 bytes from global to shared memory, asynchronously (the 256 bytes around them come to L2 for the CTAs of the other KV
+// heads: a page's scales are hd / 32 bytes a token and head); and an arrival on an mbarrier when this thread's copies so far
+// have landed
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // Units of up to `rows` (8 or 16) query rows, G query heads each (a divisor of the group's); requests with at most n_hi new

@@ -18,8 +18,8 @@
 //  - S^T comes out of the product with a key per lane group and rows along lanes; two 8x8 transposes (movmatrix) make
 //    the weights the operand of the second product;
 //  - lane (g, t) converts for K the 32 values of group t of keys g and g + 8, and for V the 16 columns from 16 g on of four
-//    keys: loads of 16 and 8 bytes, a scale byte each. Which key is row k of a product is free: kKeyOf makes both loads
-//    meet all banks (with rows of 64 bytes swizzled as TMA does).
+//    keys: loads of 16 and 8 bytes, a scale byte each. Which key is row k of a product is free: key_of makes both loads
+//    meet all banks.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -50,17 +50,17 @@ template <int HD, int NT, bool F32> struct Cfg {
     static_assert(kMinSpan > kKT, "a span holds more than a tile");
     static constexpr int kRow = q4_code_bytes(HD), kSRow = q4_scale_bytes(HD);
     static constexpr int kCodes = kKT * kRow, kScales = kKT * kSRow;
-    static constexpr int kStage = 2 * (kCodes + kScales); // K codes, V codes, K scales, V scales
     static constexpr int kStages = (kCtas == 3 || F32 ? 3 : 4) * (HD == 128 ? 1 : 2);
     static constexpr int kXRow = HD + 4;                  // exchange row in floats
-    static constexpr int kX = kStages * kStage;           // [warp][row][kXRow]
+    static constexpr int kSc = kStages * 2 * kCodes;      // scales, behind all stages' codes (K, V each)
+    static constexpr int kX = kSc + kStages * 2 * kScales;  // [warp][row][kXRow]
     static constexpr int kML = kX + kWarps * NT * 8 * kXRow * 4;
     static constexpr int kQ = kML + kWarps * NT * 8 * 8;  // q's terms as operands: [term][step][row tile][lane]
     static constexpr int kSeg = kQ + (F32 ? kTerms * (HD / 16) * NT * 256 : 0);
     static constexpr int kBar = kSeg + kSegSlots * (int)sizeof(SegMsg);
     static constexpr int FULL = 0, EMPTY = kStages, SEG_FULL = 2 * kStages, SEG_EMPTY = SEG_FULL + kSegSlots;
     static constexpr int kSmem = kBar + (SEG_EMPTY + kSegSlots) * 8 + 1024;  // + slack for the alignment
-    static_assert(kStage % 512 == 0 && kCodes % 512 == 0, "the swizzle's pattern of 512 bytes");
+    static_assert(kCodes % 1024 == 0, "the swizzle's pattern of 1024 bytes");
 };
 
 struct FewParams {
@@ -122,18 +122,15 @@ __device__ __forceinline__ uint32_t scales2(uint32_t lo, uint32_t hi) { return l
 __device__ __forceinline__ uint32_t minus136(uint32_t s2) {
     return fma_bf16x2(s2, 0xc308c308u, 0x80008000u);  // -136 s - 0
 }
-// The two constants of a conversion in registers: an instruction has room for one constant of its own, and with both known
-// the compiler takes two instructions (143 instead of 77 logic operations per 16 keys, a quarter more time).
+// The codes j of a word (the low nibbles of the halves of word >> 4 j) as values. One of the conversion's two constants is
+// held in a register: an instruction has room for one of its own, and with both known the compiler takes two
+// instructions (143 instead of 72 logic operations per 16 keys).
 struct Nibbles {
-    uint32_t mask, magic;
-    __device__ __forceinline__ Nibbles() {
-        asm volatile("mov.b32 %0, 0x000f000f;" : "=r"(mask));
-        asm volatile("mov.b32 %0, 0x43084308;" : "=r"(magic));
-    }
-    // codes j (the low nibbles of the halves of word >> 4 j) as values
+    uint32_t magic;
+    __device__ __forceinline__ Nibbles() { asm volatile("mov.b32 %0, 0x43084308;" : "=r"(magic)); }
     __device__ __forceinline__ uint32_t values(uint32_t word, int j, uint32_t s2, uint32_t off) const {
         uint32_t x;
-        asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(x) : "r"(word >> (4 * j)), "r"(mask), "r"(magic));  // (a & b) ^ c
+        asm("lop3.b32 %0, %1, 0x000f000f, %2, 0x6a;" : "=r"(x) : "r"(word >> (4 * j)), "r"(magic));  // (a & b) ^ c
         return fma_bf16x2(x, s2, off);
     }
 };
@@ -166,14 +163,16 @@ static __device__ __noinline__ bool wait_longer(uint32_t bar, uint32_t parity, i
     return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, status, USP_ERR_TIMEOUT, kWaitLimitNs));
 }
 
-// The key of a step's 16 that is row k of the products (k < 8; row k + 8: 8 further). Rows of 64 bytes (hd 128): the pairs of
-// K's 16-byte loads (k, k + 1) and the quadruples of V's 8-byte loads (k, k + 2, ..) then lie in different banks; rows of 32: the
-// quadruples of K's 8-byte and V's 4-byte loads.
+// The key of a step's 16 that is row k of the products (k < 8; row k + 8: 8 further). hd 128: the keys of K's 16-byte loads
+// that meet, rows (k, k + 1), and of V's 8-byte loads, rows (k, k + 2, k + 4, k + 6) with k even, then lie in different banks
+// of the swizzled lines; hd 64: rows (k, .., k + 3) of K's 8-byte loads and the same rows of V's 4-byte loads.
 template <int HD> __device__ __forceinline__ int key_of(int k) {
     return HD == 128 ? (k & 4) + (((k >> 1) & 1) ^ (3 * (k & 1))) : k ^ ((k >> 2) & 1);
 }
 
-// The producer warp: walks the span; lane b < 4 x pieces loads box b of each tile (K, V, K's scales, V's scales x page piece).
+// The producer warp: walks the span. Lane b < 2 x pieces loads box b of each tile's codes (K, then V; a page piece each) by
+// TMA, and every lane 16-byte pieces of the scales with asynchronous copies: as bulk copies of a page piece each (64 bytes
+// where a page has 16 tokens) they took as long to issue as the boxes.
 template <int HD, int NT, bool F32>
 __device__ void producer(const FewParams &p, const SchedShared &sh, uint8_t *smem, uint32_t sbase) {
     using C = Cfg<HD, NT, F32>;
@@ -185,10 +184,13 @@ __device__ void producer(const FewParams &p, const SchedShared &sh, uint8_t *sme
     };
     SegMsg *ring = reinterpret_cast<SegMsg *>(smem + C::kSeg);
     const int ps = 1 << p.log_ps, piece = min(ps, C::kKT), pieces = C::kKT / piece;  // at most 8 pieces
-    const int kind = lane / pieces, pc = lane % pieces;
-    const bool loads = kind < 4, scales = kind >= 2, v = kind & 1;
-    const uint32_t dst0 = sbase + (scales ? 2 * C::kCodes + (v ? C::kScales : 0) + pc * piece * C::kSRow
-                                          : (v ? C::kCodes : 0) + pc * piece * C::kRow);
+    const bool v = lane >= pieces, loads = lane < 2 * pieces;
+    const int pc = v ? lane - pieces : lane;
+    const uint32_t dst0 = sbase + (v ? C::kCodes : 0) + pc * piece * C::kRow;
+    // this lane's 16 bytes of K's and V's scales: kCopyKeys keys from its key on
+    constexpr int kCopyKeys = 16 / C::kSRow;
+    const int skey = lane * kCopyKeys;
+    const bool copies = lane < C::kScales / 16;
     Sched sc;
     sched_begin<C::kKT>(p.s, sh, sc);
     PartHeader opened = no_part(sh);
@@ -211,31 +213,37 @@ __device__ void producer(const FewParams &p, const SchedShared &sh, uint8_t *sme
         if (!more) break;
         const int32_t *row = p.table + (int64_t)g.req * p.table_stride;
         const int kv_head = (int)p.by_sub.div((uint32_t)g.head);
-        // page of this lane's piece of tile t; num_pages (a box of zeros) behind the request's keys
-        auto page_of = [&](int t) {
-            const int64_t key = (int64_t)t * C::kKT + pc * piece;
-            if (!loads || key >= g.kv) return p.num_pages;
+        // page of the tile's key `in`; num_pages (a box of zeros) behind the request's keys
+        auto page_of = [&](int t, int in) {
+            const int64_t key = (int64_t)t * C::kKT + in;
+            if (key >= g.kv) return p.num_pages;
             const int32_t x = row[key >> p.log_ps];
             return x >= 0 && x < p.num_pages ? x : p.num_pages;
         };
-        int32_t page = page_of(g.t0);
+        int32_t page = loads ? page_of(g.t0, pc * piece) : 0, spage = copies ? page_of(g.t0, skey) : 0;
         for (int t = g.t0; t < g.t1; ++t) {
-            const int32_t next = t + 1 < g.t1 ? page_of(t + 1) : 0;
+            const bool more_tiles = t + 1 < g.t1;
+            const int32_t next = loads && more_tiles ? page_of(t + 1, pc * piece) : 0;
+            const int32_t snext = copies && more_tiles ? page_of(t + 1, skey) : 0;
             const uint32_t st = fill % C::kStages;
             if (!(ok = wait(C::EMPTY + st, ((fill / C::kStages) & 1u) ^ 1u))) break;
-            if (lane == 0) tc::mbar_arrive_expect_tx(BAR(C::FULL + st), C::kStage);
+            if (lane == 0) tc::mbar_arrive_expect_tx(BAR(C::FULL + st), 2 * C::kCodes);
             __syncwarp();
-            const int in_page = kv_head * ps + (int)(((int64_t)t * C::kKT + pc * piece) & (ps - 1));
-            if (loads && !scales) {
-                tma_load_3d(dst0 + st * C::kStage, v ? &p.tv : &p.tk, 0, in_page, page, BAR(C::FULL + st));
-            } else if (loads) {
+            const int mask = ps - 1, row0 = kv_head * ps, tile0 = (int)(((int64_t)t * C::kKT) & mask);
+            if (loads)
+                tma_load_3d(dst0 + st * 2 * C::kCodes, v ? &p.tv : &p.tk, 0, (row0 + ((tile0 + pc * piece) & mask)) / (128 / C::kRow), page,
+                            BAR(C::FULL + st));
+            if (copies) {
                 // (the scales of a page outside the cache are page 0's: its codes are zeros)
-                const int64_t pg = page < p.num_pages ? page : 0;
-                bulk_load(dst0 + st * C::kStage, (v ? p.vs + pg * p.vs_page : p.ks + pg * p.ks_page) + (int64_t)in_page * C::kSRow,
-                          piece * C::kSRow, BAR(C::FULL + st));
+                const int64_t pg = spage < p.num_pages ? spage : 0, at = (int64_t)(row0 + ((tile0 + skey) & mask)) * C::kSRow;
+                const uint32_t dst = sbase + C::kSc + st * 2 * C::kScales + lane * 16;
+                copy16(dst, p.ks + pg * p.ks_page + at);
+                copy16(dst + C::kScales, p.vs + pg * p.vs_page + at);
             }
+            copies_arrive(BAR(C::FULL + st));
             ++fill;
             page = next;
+            spage = snext;
         }
         if (!ok) break;
         if (g.t0 == 0 && g.t1 < g.tiles) opened = part_header(p.s, sh, sc, g);
@@ -266,14 +274,16 @@ template <int HD, int NT, bool F32> __device__ void consumer(const FewParams &p,
     // addresses inside a stage: K's row k = g (and + 8), this lane's values; V's rows 2 t, 2 t + 1 (and + 8), its columns; a
     // step's rows are 16 further
     const int kkey = warp * 16 * kW + key_of<HD>(g);
-    const uint32_t k_at = kkey * C::kRow + (HD == 128 ? (t ^ ((kkey >> 1) & 3)) * 16 : t * 8);
-    const uint32_t ks_at = 2 * C::kCodes + kkey * C::kSRow + (HD == 128 ? t : t >> 1);
+    const uint32_t k_at = codes_at<HD>(kkey, t * (C::kRow / 4));
+    const uint32_t ks_at = kkey * C::kSRow + (HD == 128 ? t : t >> 1);
+    // the address of the same codes n keys further (a multiple of 8; no carry reaches the swizzled bits)
+    auto further = [](uint32_t at, int n) { return (at ^ ((n * C::kRow >> 3) & 0x70)) + n * C::kRow; };
     uint32_t v_at[2], vs_at[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const int key = warp * 16 * kW + key_of<HD>(2 * t + e);
-        v_at[e] = C::kCodes + key * C::kRow + (HD == 128 ? ((g >> 1) ^ ((key >> 1) & 3)) * 16 + (g & 1) * 8 : g * 4);
-        vs_at[e] = 2 * C::kCodes + C::kScales + key * C::kSRow + (HD == 128 ? g >> 1 : g >> 2);
+        v_at[e] = C::kCodes + codes_at<HD>(key, g * (C::kRow / 8));
+        vs_at[e] = C::kScales + key * C::kSRow + (HD == 128 ? g >> 1 : g >> 2);
     }
     uint32_t st = 0, st_phase = 0;  // the stage of the next tile, and its fill's parity
     for (uint32_t nseg = 0;; ++nseg) {
@@ -339,31 +349,24 @@ template <int HD, int NT, bool F32> __device__ void consumer(const FewParams &p,
         const int t1 = s.ntok > 0 ? s.t1 : s.t0;
         for (int kt = s.t0; ok && kt < t1; ++kt) {
             if (!(ok = wait(C::FULL + st, st_phase))) break;
-            const uint32_t base = sbase + st * C::kStage;
+            const uint32_t base = sbase + st * 2 * C::kCodes, sbs = sbase + C::kSc + st * 2 * C::kScales;
             const int key0 = kt * C::kKT + warp * 16 * kW;
             // ---- S^T = K Q^T ----
             float sc[kW][NT][4];
-            uint32_t w[kW][2][kWords], kb[kW][2];
-#pragma unroll
-            for (int i = 0; i < kW; ++i)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint32_t at = base + k_at + (i * 16 + e * 8) * C::kRow;
-                    if constexpr (HD == 128) {
-                        const uint4 x = lds128(at);
-                        w[i][e][0] = x.x; w[i][e][1] = x.y; w[i][e][2] = x.z; w[i][e][3] = x.w;
-                    } else {
-                        const uint2 x = lds64(at);
-                        w[i][e][0] = x.x; w[i][e][1] = x.y;
-                    }
-                    kb[i][e] = lds8(base + ks_at + (i * 16 + e * 8) * C::kSRow);
-                }
 #pragma unroll
             for (int i = 0; i < kW; ++i) {
-                uint32_t s2[2], off[2];
+                uint32_t w[2][kWords], s2[2], off[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    s2[e] = kb[i][e] * 0x100010u + 0x35803580u;
+                    const uint32_t at = base + further(k_at, i * 16 + e * 8);
+                    if constexpr (HD == 128) {
+                        const uint4 x = lds128(at);
+                        w[e][0] = x.x; w[e][1] = x.y; w[e][2] = x.z; w[e][3] = x.w;
+                    } else {
+                        const uint2 x = lds64(at);
+                        w[e][0] = x.x; w[e][1] = x.y;
+                    }
+                    s2[e] = lds8(sbs + ks_at + (i * 16 + e * 8) * C::kSRow) * 0x100010u + 0x35803580u;
                     off[e] = minus136(s2[e]);
                 }
 #pragma unroll
@@ -375,8 +378,8 @@ template <int HD, int NT, bool F32> __device__ void consumer(const FewParams &p,
                     uint32_t a[4];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        a[e] = nib.values(w[i][e][k / 2], k % 2 * 2, s2[e], off[e]);
-                        a[2 + e] = nib.values(w[i][e][k / 2], k % 2 * 2 + 1, s2[e], off[e]);
+                        a[e] = nib.values(w[e][k / 2], k % 2 * 2, s2[e], off[e]);
+                        a[2 + e] = nib.values(w[e][k / 2], k % 2 * 2 + 1, s2[e], off[e]);
                     }
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
@@ -392,22 +395,6 @@ template <int HD, int NT, bool F32> __device__ void consumer(const FewParams &p,
                     }
                 }
             }
-            // V's words and scales, under the softmax
-            uint32_t vw[kW][2][2][kMT / 4], vb[kW][2][2];  // [step][half of the step's keys][pair's element][word]
-#pragma unroll
-            for (int i = 0; i < kW; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        if constexpr (HD == 128) {
-                            const uint2 x = lds64(base + v_at[e] + (i * 16 + h * 8) * C::kRow);
-                            vw[i][h][e][0] = x.x; vw[i][h][e][1] = x.y;
-                        } else {
-                            vw[i][h][e][0] = lds32(base + v_at[e] + (i * 16 + h * 8) * C::kRow);
-                        }
-                        vb[i][h][e] = lds8(base + vs_at[e] + (i * 16 + h * 8) * C::kSRow);
-                    }
             // ---- softmax ----
             uint32_t pf[kW][NT][kT][2];
 #pragma unroll
@@ -471,10 +458,21 @@ template <int HD, int NT, bool F32> __device__ void consumer(const FewParams &p,
             // ---- O^T += V^T P^T ----
 #pragma unroll
             for (int i = 0; i < kW; ++i) {
-                uint32_t s2[2], off[2];
+                uint32_t vw[2][2][kMT / 4], s2[2], off[2];  // [half of the step's keys][pair's element][word]
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    s2[h] = scales2(vb[i][h][0], vb[i][h][1]);
+                    uint32_t b[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        if constexpr (HD == 128) {
+                            const uint2 x = lds64(base + further(v_at[e], i * 16 + h * 8));
+                            vw[h][e][0] = x.x; vw[h][e][1] = x.y;
+                        } else {
+                            vw[h][e][0] = lds32(base + further(v_at[e], i * 16 + h * 8));
+                        }
+                        b[e] = lds8(sbs + vs_at[e] + (i * 16 + h * 8) * C::kSRow);
+                    }
+                    s2[h] = scales2(b[0], b[1]);
                     off[h] = minus136(s2[h]);
                 }
 #pragma unroll
@@ -482,8 +480,8 @@ template <int HD, int NT, bool F32> __device__ void consumer(const FewParams &p,
                     uint32_t even[2], odd[2];  // the even and the odd columns of 8, four codes of either key
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        even[h] = __byte_perm(vw[i][h][0][x], vw[i][h][1][x], 0x5410);
-                        odd[h] = __byte_perm(vw[i][h][0][x], vw[i][h][1][x], 0x7632);
+                        even[h] = __byte_perm(vw[h][0][x], vw[h][1][x], 0x5410);
+                        odd[h] = __byte_perm(vw[h][0][x], vw[h][1][x], 0x7632);
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -596,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, F32>::kCtas)) paged_q4_
         tc::prefetch_tmap(&p.tv);
         const uint32_t bar = sbase + C::kBar;
         for (int i = 0; i < C::kStages; ++i) {
-            tc::mbar_init(bar + 8 * (C::FULL + i), 1);
+            tc::mbar_init(bar + 8 * (C::FULL + i), 33);  // the boxes' bytes, and each lane's copies
             tc::mbar_init(bar + 8 * (C::EMPTY + i), kWarps);
         }
         for (int i = 0; i < kSegSlots; ++i) {
