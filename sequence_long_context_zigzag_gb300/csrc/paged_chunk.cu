@@ -1,4 +1,4 @@
-// paged_chunk.cu -- bf16 attention of many query rows per KV head over the paged cache, on the
+// paged_chunk.cu -- bf16 attention of many query rows per KV head over the paged cache, bf16 or 4-bit, on the
 // 5th-generation tensor cores (sm_103a): chunks of a prompt, whole prompts.
 //
 // Mathematics: as paged_decode.cu (online softmax, lazy rescale). A unit is two tiles of up to 128 query
@@ -27,12 +27,18 @@
 // to 1260 TFLOP/s. A pair of tiles takes about 2750 cycles (its products 2050: each Q tile is one chain of
 // products, softmax, products), a unit's end about 6000 more (last products, read-out of O, both Q tiles in step again).
 //   TMEM: S0 [0,128) S1 [128,256) O0 [256,256+hd) O1 [256+hd,256+2hd); P_i lies over S_i.
+//
+// Over a 4-bit cache (Q4) the producer loads codes and scales into a small ring of tiles, and four more warps (12-15), a
+// thread per key, convert them into the stages: c s is exact in bf16, so all else is as for a bf16 cache. A tile is
+// converted anew for every unit that reads it: 400 instructions a thread for K and V in the 2750 cycles that a pair of
+// tiles takes the other roles, where converting the cache once into memory would need that memory, and 13% of the time of
+// a chunk of 900 tokens. Rows behind the last key need no clearing: whatever their bytes, they stand for finite numbers.
 #include <cuda_bf16.h>
 
 #include <algorithm>
 #include <mutex>
 
-#include "paged_sched.cuh"
+#include "paged_q4.cuh"
 #include "paged_tma.cuh"
 #include "tc_ptx.cuh"
 #include "usp_device.cuh"
@@ -43,26 +49,29 @@ namespace {
 constexpr int kM = 128;  // rows of a Q tile
 constexpr int kN = 128;  // keys of a tile
 constexpr int kSoftmaxWarps = 8;
-constexpr int kWarps = kSoftmaxWarps + 4;
-constexpr int kThreads = kWarps * 32;
+template <bool Q4> constexpr int kWarps = kSoftmaxWarps + (Q4 ? 8 : 4);
+template <bool Q4> constexpr int kThreads = kWarps<Q4> * 32;
 constexpr int kProducerWarp = kSoftmaxWarps;
 constexpr int kMmaWarp = kSoftmaxWarps + 1;  // Q tile 0's issuer (tile 1's follows); allocates and frees tensor memory
 constexpr int kWalkWarp = kSoftmaxWarps + 3;
-constexpr int kSegReaders = kSoftmaxWarps + 3;  // the softmax warps, the producer and the issuers
+constexpr int kConvertWarp = kSoftmaxWarps + 4;  // the first of four (Q4)
+template <bool Q4> constexpr int kSegReaders = kSoftmaxWarps + 3 + (Q4 ? 4 : 0);  // the softmax warps, the producer, the issuers, the converters
 // the warpgroups' shares (setmaxnreg) add up to exactly the launch's registers
-constexpr int kLaunchRegs = (65536 / kThreads) / 8 * 8;
-constexpr int kSoftmaxRegs = 208;
-constexpr int kControlRegs = kLaunchRegs * kWarps / 4 - 2 * kSoftmaxRegs;
-static_assert(kControlRegs >= 24 && kControlRegs % 8 == 0 &&
-                  2 * kSoftmaxRegs + kControlRegs == kLaunchRegs * kWarps / 4,
-              "register split must use exactly the launch's registers");
+template <bool Q4> constexpr int kLaunchRegs = (65536 / kThreads<Q4>) / 8 * 8;
+template <bool Q4> constexpr int kSoftmaxRegs = Q4 ? 184 : 208;
+template <bool Q4> constexpr int kConvertRegs = Q4 ? 72 : 0;
+template <bool Q4> constexpr int kControlRegs = kLaunchRegs<Q4> * kWarps<Q4> / 4 - 2 * kSoftmaxRegs<Q4> - kConvertRegs<Q4>;
+template <bool Q4>
+constexpr bool split_ok = kControlRegs<Q4> >= 24 && kControlRegs<Q4> % 8 == 0 &&
+                          2 * kSoftmaxRegs<Q4> + kControlRegs<Q4> + kConvertRegs<Q4> == kLaunchRegs<Q4> * kWarps<Q4> / 4;
+static_assert(split_ok<false> && split_ok<true>, "register split must use exactly the launch's registers");
 constexpr int kOver = 192;     // a unit's constant cost, in keys
 constexpr int kMinSpan = 448;  // keys per CTA below which fewer CTAs work
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr float kRescale = 8.0f;  // log2 units
 constexpr float kLn2 = 0.69314718055994531f;
 
-template <int HD> struct Cfg {
+template <int HD, bool Q4> struct Cfg {
     static constexpr int kBoxes = HD / 64;
     static constexpr int kBoxBytes = kM * 128;
     static constexpr int kTileBytes = kM * HD * 2;
@@ -70,10 +79,18 @@ template <int HD> struct Cfg {
     static constexpr int kQ = 0;
     static constexpr int kK = kQ + 2 * kTileBytes;
     static constexpr int kV = kK + kStages * kTileBytes;
-    // a staging slot per softmax warp for its stores: 32 rows x 128 bytes (1024-byte aligned: a swizzled box)
-    static constexpr int kStgSlot = 32 * 128;
-    static constexpr int kStg = kV + kStages * kTileBytes;
+    // tiles of codes and scales (K, V, K, V, ..), codes 1024-byte aligned
+    static constexpr int kSlots = Q4 ? (HD == 128 ? 2 : 4) : 0;
+    static constexpr int kCodes = kN * q4_code_bytes(HD), kScales = kN * q4_scale_bytes(HD);
+    static constexpr int kQ4 = kV + kStages * kTileBytes;
+    static constexpr int kQ4Scales = kQ4 + kSlots * kCodes;
+    // a staging slot per softmax warp for its stores: 32 rows x 128 bytes (1024-byte aligned: a swizzled box), 32 bytes where
+    // the slots of codes leave no more
+    static constexpr int kStgRow = Q4 && HD == 128 ? 32 : 128;
+    static constexpr int kStgSlot = 32 * kStgRow;
+    static constexpr int kStg = kQ4Scales + kSlots * kScales;
     static constexpr int kBar = kStg + kSoftmaxWarps * kStgSlot;
+    static_assert(kStg % 1024 == 0, "boxes of staged rows");
     static constexpr int Q_FULL = 0;
     static constexpr int K_FULL = 1;
     static constexpr int K_EMPTY = K_FULL + kStages;
@@ -90,7 +107,9 @@ template <int HD> struct Cfg {
     static constexpr int SEG_EMPTY = SEG_FULL + kSegSlots;
     static constexpr int TAIL = SEG_EMPTY + kSegSlots;  // [2]: V tiles that the walk warp has to clear the end of
     static constexpr int P_HALF = TAIL + 2;             // [2]: the first half of a tile's P
-    static constexpr int kNumBars = P_HALF + 2;
+    static constexpr int Q4_FULL = P_HALF + 2;          // [kSlots]
+    static constexpr int Q4_EMPTY = Q4_FULL + kSlots;   // [kSlots]
+    static constexpr int kNumBars = Q4_EMPTY + kSlots;
     static constexpr int kSlot = kBar + (kNumBars * 8 + 15) / 16 * 16;  // tensor memory address, skip flag
     static constexpr int kSeg = kSlot + 16;
     static constexpr int kSmem = kSeg + kSegSlots * (int)sizeof(SegMsg) + 1024;  // + slack for the alignment
@@ -109,6 +128,8 @@ struct ChunkParams {
     int32_t tq_tokens;  // tokens per Q tile
     float scale_log2;
     CUtensorMap to;  // of the launches with boxes
+    const uint8_t *ks, *vs;  // Q4: the scales
+    int64_t ks_page, vs_page;
 };
 
 // Waits between the roles last a tile or two, those for a segment's place, message or end as long as the segments
@@ -126,9 +147,9 @@ __device__ __forceinline__ bool is_tail(const int32_t t, const int32_t kv) { ret
 
 // The walk warp hands out the segments and, at the end, the header of a unit left open. It is a segment
 // ahead when it clears the end of a segment's last V tile.
-template <int HD>
+template <int HD, bool Q4>
 __device__ void walk_role(const ChunkParams &p, const SchedShared &sh, uint8_t *smem, uint32_t bar0) {
-    using C = Cfg<HD>;
+    using C = Cfg<HD, Q4>;
     const int lane = threadIdx.x & 31;
     auto wait = [&](int bar, uint32_t parity) {
         const bool r = wait_segment(bar0 + 8u * bar, parity, p.status, sh);
@@ -180,7 +201,7 @@ __device__ void walk_role(const ChunkParams &p, const SchedShared &sh, uint8_t *
         }
         if (more && g.t0 < g.t1) {
             tiles += (uint32_t)(g.t1 - g.t0);
-            if (is_tail(g.t1 - 1, g.kv)) {
+            if (!Q4 && is_tail(g.t1 - 1, g.kv)) {
                 tail_row = g.kv - (g.t1 - 1) * kN;
                 tail_stage = (tiles - 1) % C::kStages;
             }
@@ -192,10 +213,10 @@ __device__ void walk_role(const ChunkParams &p, const SchedShared &sh, uint8_t *
 }
 
 // The next segment, for a whole warp; ntok == 0 at the end. False after a failed wait.
-template <int HD>
+template <int HD, bool Q4>
 __device__ __forceinline__ bool next_segment(const ChunkParams &p, const SchedShared &sh, uint32_t bar0, uint32_t &n,
                                              SegMsg &g) {
-    using C = Cfg<HD>;
+    using C = Cfg<HD, Q4>;
     bool ok = wait_segment(bar0 + 8u * (C::SEG_FULL + n % kSegSlots), (n / kSegSlots) & 1u, p.status, sh);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) return false;
@@ -209,9 +230,9 @@ __device__ __forceinline__ bool next_segment(const ChunkParams &p, const SchedSh
 
 // The producer warp. Lane l < boxes loads box l of each K and V tile: column half l / pieces, page piece
 // l % pieces; lane 0 loads Q too.
-template <int HD>
+template <int HD, bool Q4>
 __device__ void producer_role(const ChunkParams &p, const SchedShared &sh, uint32_t sbase, uint32_t bar0) {
-    using C = Cfg<HD>;
+    using C = Cfg<HD, Q4>;
     const int lane = threadIdx.x & 31;
     auto BAR = [&](int i) { return bar0 + 8u * i; };
     auto wait = [&](int bar, uint32_t parity) {
@@ -224,7 +245,7 @@ __device__ void producer_role(const ChunkParams &p, const SchedShared &sh, uint3
     uint32_t kfills = 0, vfills = 0, nq = 0, nseg = 0, ntail = 0;
     bool ok = true;
     SegMsg g;
-    while (ok && (ok = next_segment<HD>(p, sh, bar0, nseg, g)) && g.ntok > 0) {
+    while (ok && (ok = next_segment<HD, Q4>(p, sh, bar0, nseg, g)) && g.ntok > 0) {
         if (g.t0 >= g.t1) continue;
         // Q: the first one at once; later ones when the buffer is free, into L2 meanwhile
         auto q_boxes = [&](auto &&f) {
@@ -343,9 +364,9 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int *st
     return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, status, USP_ERR_TIMEOUT, kWaitLimitNs));
 }
 
-template <int HD>
+template <int HD, bool Q4>
 __device__ __forceinline__ void issue_s(uint32_t el, uint32_t d_tmem, uint64_t qdesc, uint64_t kdesc) {
-    using C = Cfg<HD>;
+    using C = Cfg<HD, Q4>;
     constexpr uint32_t id = tc::idesc_bf16_f32(kM, kN, 0, 0);
 #pragma unroll
     for (int k = 0; k < HD / 16; ++k) {
@@ -370,9 +391,9 @@ __device__ __forceinline__ void issue_pv(uint32_t el, uint32_t d_tmem, uint32_t 
 // S_i(j+1) come from one lane, so S_i(j+1) overwrites P_i(j) only after PV_i(j) has read it. Stages are
 // released by both issuers; each waits for a stage's fill before releasing it, also when its Q tile skips
 // the tile.
-template <int HD>
+template <int HD, bool Q4>
 __device__ void mma_role(const ChunkParams &p, const SchedShared &sh, uint32_t sbase, uint32_t bar0, uint32_t tmem, int i) {
-    using C = Cfg<HD>;
+    using C = Cfg<HD, Q4>;
     const uint32_t el = elect_one();
     auto BAR = [&](int k) { return bar0 + 8u * k; };
     auto wait = [&](int bar, uint32_t parity) {
@@ -388,7 +409,7 @@ __device__ void mma_role(const ChunkParams &p, const SchedShared &sh, uint32_t s
     int kt = 0, t1 = 0, act_end = 0;
     auto s_burst = [&](bool act, uint32_t st) {
         if (act) {
-            issue_s<HD>(el, tS, qdesc, kdesc0 + stage_off(st));
+            issue_s<HD, Q4>(el, tS, qdesc, kdesc0 + stage_off(st));
             commit_if(el, BAR(C::S_FULL + i));
         }
         commit_if(el, BAR(C::K_EMPTY + st));
@@ -406,7 +427,7 @@ __device__ void mma_role(const ChunkParams &p, const SchedShared &sh, uint32_t s
         int ntok;
         do {
             SegMsg g;
-            if (!(ok = next_segment<HD>(p, sh, bar0, nseg, g))) break;
+            if (!(ok = next_segment<HD, Q4>(p, sh, bar0, nseg, g))) break;
             // (reductions over equal values: the compiler then knows that they are uniform)
             ntok = __reduce_max_sync(0xffffffffu, g.ntok);
             kt = __reduce_max_sync(0xffffffffu, g.t0);
@@ -470,12 +491,147 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
     return v;
 }
 
+// The producer warp over a 4-bit cache: tiles of codes and scales, K then V, through the ring of slots. Lane l < pieces loads the
+// codes of page piece l (a TMA box), every lane 16 bytes of the scales; lane 0 loads Q as above.
+template <int HD>
+__device__ void producer_q4_role(const ChunkParams &p, const SchedShared &sh, uint32_t sbase, uint32_t bar0) {
+    using C = Cfg<HD, true>;
+    const int lane = threadIdx.x & 31;
+    auto BAR = [&](int i) { return bar0 + 8u * i; };
+    auto wait = [&](int bar, uint32_t parity) {
+        const bool r = tc::mbar_wait(BAR(bar), parity, p.status, USP_ERR_TIMEOUT, kWaitLimitNs);
+        return (bool)__all_sync(0xffffffffu, r);
+    };
+    const int ps = 1 << p.log_ps, mask = ps - 1, piece = min(ps, kN), pieces = kN / piece;
+    constexpr int kCopyKeys = 16 / q4_scale_bytes(HD), kLineKeys = 128 / q4_code_bytes(HD);
+    const int skey = lane * kCopyKeys;
+    const bool loads = lane < pieces, copies = lane < C::kScales / 16;
+    uint32_t fills = 0, nq = 0, nseg = 0;
+    bool ok = true;
+    SegMsg g;
+    while (ok && (ok = next_segment<HD, true>(p, sh, bar0, nseg, g)) && g.ntok > 0) {
+        if (g.t0 >= g.t1) continue;
+        auto q_boxes = [&](auto &&f) {
+            for (int i = 0; i < 2; ++i)
+                for (int bx = 0; bx < C::kBoxes; ++bx)
+                    f(C::kQ + i * C::kTileBytes + bx * C::kBoxBytes, bx * 64, (int32_t)(g.tok0 + i * p.tq_tokens));
+        };
+        auto load_q = [&]() {
+            if (lane != 0) return;
+            tc::mbar_arrive_expect_tx(BAR(C::Q_FULL), 2 * C::kBoxes * (uint32_t)(p.tq_tokens * p.s.G) * 128);
+            q_boxes([&](int dst, int c, int32_t tok) {
+                tma_load_3d(sbase + dst, &p.tq, c, g.head * p.s.G, tok, BAR(C::Q_FULL));
+            });
+        };
+        if (nq == 0) load_q();
+        else if (lane == 0) q_boxes([&](int, int c, int32_t tok) { tma_prefetch_3d(&p.tq, c, g.head * p.s.G, tok); });
+        ++nq;
+        const int32_t *row = p.table + (int64_t)g.req * p.table_stride;
+        // page of the tile's key `in`; num_pages (a box of zeros) behind the request's keys
+        auto page_of = [&](int t, int in) {
+            const int64_t key = (int64_t)t * kN + in;
+            if (key >= g.kv) return p.num_pages;
+            const int32_t x = row[key >> p.log_ps];
+            return x >= 0 && x < p.num_pages ? x : p.num_pages;
+        };
+        int32_t page = loads ? page_of(g.t0, lane * piece) : 0, spage = copies ? page_of(g.t0, skey) : 0;
+        for (int t = g.t0; t < g.t1; ++t) {
+            const bool more = t + 1 < g.t1;
+            const int32_t next = loads && more ? page_of(t + 1, lane * piece) : 0;
+            const int32_t snext = copies && more ? page_of(t + 1, skey) : 0;
+            const int row0 = g.head * ps, tile0 = (int)(((int64_t)t * kN) & mask);
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                const uint32_t slot = fills % C::kSlots;
+                if (!(ok = wait(C::Q4_EMPTY + slot, ((fills / C::kSlots) & 1u) ^ 1u))) break;
+                if (lane == 0) tc::mbar_arrive_expect_tx(BAR(C::Q4_FULL + slot), C::kCodes);
+                __syncwarp();
+                if (loads)
+                    tma_load_3d(sbase + C::kQ4 + slot * C::kCodes + lane * piece * q4_code_bytes(HD), v ? &p.tv : &p.tk, 0,
+                                (row0 + ((tile0 + lane * piece) & mask)) / kLineKeys, page, BAR(C::Q4_FULL + slot));
+                if (copies) {
+                    // (the scales of a page outside the cache are page 0's: its codes are zeros)
+                    const int64_t pg = spage < p.num_pages ? spage : 0;
+                    const int64_t at = (int64_t)(row0 + ((tile0 + skey) & mask)) * q4_scale_bytes(HD);
+                    copy16(sbase + C::kQ4Scales + slot * C::kScales + lane * 16,
+                           (v ? p.vs + pg * p.vs_page : p.ks + pg * p.ks_page) + at);
+                }
+                copies_arrive(BAR(C::Q4_FULL + slot));
+                ++fills;
+                if (v == 0 && t == g.t0 && nq > 1) {
+                    if (!(ok = wait(C::Q_EMPTY, (nq - 2) & 1u))) break;
+                    load_q();
+                }
+            }
+            if (!ok) break;
+            page = next;
+            spage = snext;
+        }
+    }
+    if (!ok) {
+        // drain (bounded), so that no copy lands after the CTA has gone
+        if (nq > 0) wait(C::Q_FULL, (nq - 1) & 1u);  // (a load that was not issued ends by the recorded status)
+        for (uint32_t f = fills > C::kSlots ? fills - C::kSlots : 0; f < fills; ++f)
+            wait(C::Q4_FULL + f % C::kSlots, (f / C::kSlots) & 1u);
+    }
+}
+
+// The converting warps: thread r takes key r of each tile of codes to row r of the K or V stage.
+template <int HD>
+__device__ void convert_role(const ChunkParams &p, const SchedShared &sh, uint32_t sbase, uint32_t bar0) {
+    using C = Cfg<HD, true>;
+    const int lane = threadIdx.x & 31;
+    const uint32_t r = threadIdx.x & 127;
+    auto BAR = [&](int i) { return bar0 + 8u * i; };
+    auto wait = [&](int bar, uint32_t parity) { return warp_wait(BAR(bar), parity, p.status); };
+    const Q4Nibbles nib;
+    const uint32_t codes0 = codes_at<HD>(r, 0);
+    uint32_t fills = 0, nseg = 0;
+    bool ok = true;
+    SegMsg g;
+    while (ok && (ok = next_segment<HD, true>(p, sh, bar0, nseg, g)) && g.ntok > 0) {
+        const int n = 2 * max(g.t1 - g.t0, 0);
+        for (int x = 0; x < n; ++x, ++fills) {
+            const uint32_t slot = fills % C::kSlots, v = fills & 1u, tile = fills >> 1, st = tile % C::kStages;
+            if (!(ok = wait(C::Q4_FULL + slot, (fills / C::kSlots) & 1u))) break;
+            const uint32_t codes = sbase + C::kQ4 + slot * C::kCodes + codes0, scales = sbase + C::kQ4Scales + slot * C::kScales;
+            uint4 w[HD / 32];
+#pragma unroll
+            for (int c = 0; c < HD / 32; ++c) w[c] = ld_shared_v4(codes ^ (c * 16));  // (of one line: swizzled alike)
+            uint32_t sb;
+            if constexpr (HD == 128) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(sb) : "r"(scales + r * 4) : "memory");
+            else asm volatile("ld.shared.u16 %0, [%1];" : "=r"(sb) : "r"(scales + r * 2) : "memory");
+            if (!(ok = wait((v ? C::V_EMPTY : C::K_EMPTY) + st, ((tile / C::kStages) & 1u) ^ 1u))) break;
+            const uint32_t to = sbase + (v ? C::kV : C::kK) + st * C::kTileBytes + r * 128;
+#pragma unroll
+            for (int c = 0; c < HD / 32; ++c) {  // a group of 32 values
+                const uint32_t s2 = q4_scales2((sb >> (8 * c)) & 255u), off = q4_minus136(s2);
+                const uint32_t words[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int c8 = c * 4 + e;
+                    st_shared_v4(to + (c8 >> 3) * C::kBoxBytes + (((uint32_t)(c8 & 7) ^ (r & 7u)) << 4),
+                                 nib.values(words[e], 0, s2, off), nib.values(words[e], 1, s2, off),
+                                 nib.values(words[e], 2, s2, off), nib.values(words[e], 3, s2, off));
+                }
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            // (what was stored depends on all that was loaded: the slot's words have arrived)
+            if (lane == 0) {
+                tc::mbar_arrive(BAR((v ? C::V_FULL : C::K_FULL) + st));
+                tc::mbar_arrive(BAR(C::Q4_EMPTY + slot));
+            }
+        }
+    }
+}
+
 // One segment of the softmax of Q tile i; ns (S tiles) and no (O read-outs) run on across segments. False after
 // a failed wait (the whole warp leaves; the others' waits end by the recorded status).
-template <int HD, bool kBox>  // kBox: whole warps of rows of out are stored as boxes
+template <int HD, bool Q4, bool kBox>  // kBox: whole warps of rows of out are stored as boxes
 __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegMsg &g, uint8_t *smem, uint32_t bar0,
                                                 uint32_t tmem, int i, uint32_t &ns, uint32_t &no) {
-    using C = Cfg<HD>;
+    using C = Cfg<HD, Q4>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wq = warp & 3;
     const int row = wq * 32 + lane;
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
@@ -602,19 +758,21 @@ __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegM
         // warp's staging slot, 16-byte pieces swizzled by row % 8 against bank conflicts. A TMA box of out takes the
         // slot, or the lanes write it, four whole lines per instruction (see launch_paged_chunk).
         const uint32_t stg = tc::smem_u32(smem) + C::kStg + warp * C::kStgSlot;
-        const int sub = lane >> 3, pc = lane & 7;  // row of 4 and piece of 8 that this lane stores
+        constexpr int kP = C::kStgRow / 16, kR = 32 / kP;  // pieces of a staged row; rows per instruction
+        const int sub = lane / kP, pc = lane % kP;         // the row and the piece that this lane stores
+        auto swz = [](uint32_t c, uint32_t r) { return kP == 8 ? c ^ (r & 7u) : c ^ ((r >> 2) & 1u); };
         const uint64_t mine = !row_ok ? 0
                               : whole ? reinterpret_cast<uint64_t>(orow)
                                       : reinterpret_cast<uint64_t>(slot + (size_t)r * HD);
         auto stage_in = [&](int c, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-            st_shared_v4(stg + (uint32_t)lane * 128u + (((uint32_t)c ^ ((uint32_t)lane & 7u)) << 4), x, y, z, w);
+            st_shared_v4(stg + (uint32_t)lane * C::kStgRow + (swz((uint32_t)c, (uint32_t)lane) << 4), x, y, z, w);
         };
-        auto stage_out = [&](uint32_t at) {  // the staged 128 bytes of every row, to byte `at` of the rows
+        auto stage_out = [&](uint32_t at) {  // the staged bytes of every row, to byte `at` of the rows
             __syncwarp();
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                const uint32_t rr = (uint32_t)x * 4u + (uint32_t)sub;
-                const uint4 v = ld_shared_v4(stg + rr * 128u + (((uint32_t)pc ^ (rr & 7u)) << 4));
+            for (int x = 0; x < kP; ++x) {
+                const uint32_t rr = (uint32_t)(x * kR + sub);
+                const uint4 v = ld_shared_v4(stg + rr * C::kStgRow + (swz((uint32_t)pc, rr) << 4));
                 const uint64_t to = __shfl_sync(0xffffffffu, mine, (int)rr);
                 if (to) *reinterpret_cast<uint4 *>(to + at + (uint32_t)pc * 16u) = v;
             }
@@ -643,8 +801,10 @@ __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegM
                     for (int e = 0; e < 4; ++e)
                         w[e] = float2_to_bf16x2(u2f(o[c8 / 4][c8 % 4 * 8 + 2 * e]) * inv,
                                                 u2f(o[c8 / 4][c8 % 4 * 8 + 2 * e + 1]) * inv);
-                    stage_in(c8, w[0], w[1], w[2], w[3]);
+                    stage_in(c8 % kP, w[0], w[1], w[2], w[3]);
+                    if (kP < 8 && c8 % kP == kP - 1) stage_out(c * 128 + c8 / kP * C::kStgRow);
                 }
+                if (kP < 8) continue;
                 if (box) {
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
@@ -656,9 +816,10 @@ __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegM
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                    for (int c8 = 0; c8 < 8; ++c8)
-                        stage_in(c8, o[h][c8 * 4], o[h][c8 * 4 + 1], o[h][c8 * 4 + 2], o[h][c8 * 4 + 3]);
-                    stage_out(c * 256 + h * 128);
+                    for (int c8 = 0; c8 < 8; ++c8) {
+                        stage_in(c8 % kP, o[h][c8 * 4], o[h][c8 * 4 + 1], o[h][c8 * 4 + 2], o[h][c8 * 4 + 3]);
+                        if (c8 % kP == kP - 1) stage_out(c * 256 + h * 128 + c8 / kP * C::kStgRow);
+                    }
                 }
             }
         }
@@ -680,9 +841,9 @@ __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegM
     return true;
 }
 
-template <int HD, bool kBox>
-__global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_constant__ ChunkParams p) {
-    using C = Cfg<HD>;
+template <int HD, bool Q4, bool kBox>
+__global__ void __launch_bounds__(kThreads<Q4>, 1) paged_chunk_kernel(const __grid_constant__ ChunkParams p) {
+    using C = Cfg<HD, Q4>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ SchedShared sh;
     const uint32_t raw = tc::smem_u32(smem_raw);
@@ -698,16 +859,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         tc::prefetch_tmap(&p.tk);
         tc::prefetch_tmap(&p.tv);
         for (int s = 0; s < C::kStages; ++s) {
-            tc::mbar_init(bar0 + 8u * (C::K_FULL + s), 1);
+            tc::mbar_init(bar0 + 8u * (C::K_FULL + s), Q4 ? 4 : 1);
             tc::mbar_init(bar0 + 8u * (C::K_EMPTY + s), 2);
-            tc::mbar_init(bar0 + 8u * (C::V_FULL + s), 1);
+            tc::mbar_init(bar0 + 8u * (C::V_FULL + s), Q4 ? 4 : 1);
             tc::mbar_init(bar0 + 8u * (C::V_EMPTY + s), 2);
         }
         tc::mbar_init(bar0 + 8u * C::Q_FULL, 1);
         tc::mbar_init(bar0 + 8u * C::Q_EMPTY, 2);
         for (int i = 0; i < kSegSlots; ++i) {
             tc::mbar_init(bar0 + 8u * (C::SEG_FULL + i), 1);
-            tc::mbar_init(bar0 + 8u * (C::SEG_EMPTY + i), kSegReaders);
+            tc::mbar_init(bar0 + 8u * (C::SEG_EMPTY + i), kSegReaders<Q4>);
+        }
+        for (int i = 0; i < C::kSlots; ++i) {
+            tc::mbar_init(bar0 + 8u * (C::Q4_FULL + i), 33);  // the boxes' bytes, and each lane's copies
+            tc::mbar_init(bar0 + 8u * (C::Q4_EMPTY + i), 4);
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(bar0 + 8u * (C::S_FULL + i), 1);
@@ -729,27 +894,36 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     // a bounded wait of an earlier kernel ran out: do no work until usp_check clears it
     const int status = *reinterpret_cast<volatile int *>(p.status);
     let_next_start();
-    const bool work = sched_scan<kThreads, kN>(p.s, sh);  // the same for every thread
+    const bool work = sched_scan<kThreads<Q4>, kN>(p.s, sh);  // the same for every thread
     if (threadIdx.x == 0) *skip_flag = status != 0;
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     const bool skip = !work || *skip_flag != 0;
-    if (warp >= kSoftmaxWarps) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
+    if (Q4 && warp >= kConvertWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Q4 ? kConvertRegs<Q4> : 24));
+        if constexpr (Q4)
+            if (!skip) convert_role<HD>(p, sh, sbase, bar0);
+    } else if (warp >= kSoftmaxWarps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs<Q4>));
         if (!skip) {
-            if (warp == kProducerWarp) producer_role<HD>(p, sh, sbase, bar0);
-            else if (warp == kWalkWarp) walk_role<HD>(p, sh, smem, bar0);
-            else mma_role<HD>(p, sh, sbase, bar0, tmem, warp - kMmaWarp);
+            if (warp == kProducerWarp) {
+                if constexpr (Q4) producer_q4_role<HD>(p, sh, sbase, bar0);
+                else producer_role<HD, Q4>(p, sh, sbase, bar0);
+            } else if (warp == kWalkWarp) {
+                walk_role<HD, Q4>(p, sh, smem, bar0);
+            } else {
+                mma_role<HD, Q4>(p, sh, sbase, bar0, tmem, warp - kMmaWarp);
+            }
             __syncwarp();
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs<Q4>));
         uint32_t ns = 0, no = 0, nseg = 0;
         SegMsg g;
-        while (!skip && next_segment<HD>(p, sh, bar0, nseg, g) && g.ntok > 0)
-            if (!softmax_segment<HD, kBox>(p, g, smem, bar0, tmem, warp >> 2, ns, no)) break;
+        while (!skip && next_segment<HD, Q4>(p, sh, bar0, nseg, g) && g.ntok > 0)
+            if (!softmax_segment<HD, Q4, kBox>(p, g, smem, bar0, tmem, warp >> 2, ns, no)) break;
         if (kBox && (threadIdx.x & 31) == 0) tma_stores_done();
     }
     if (skip && threadIdx.x == 0) p.w.head[blockIdx.x] = no_part(sh);
@@ -761,9 +935,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     }
 }
 
-template <int HD, bool kBox>
+template <int HD, bool Q4, bool kBox>
 int launch_typed(const ChunkParams &p, int grid, cudaStream_t s) {
-    constexpr int kSmem = Cfg<HD>::kSmem;
+    constexpr int kSmem = Cfg<HD, Q4>::kSmem;
     static_assert(kSmem <= 226 * 1024, "shared memory per CTA");
     static std::mutex mu;
     static bool attr_set[64] = {};
@@ -776,15 +950,15 @@ int launch_typed(const ChunkParams &p, int grid, cudaStream_t s) {
             // setmaxnreg.inc is granted only from registers the launch holds: never launch a build whose
             // register count would make the split wait forever
             cudaFuncAttributes fa{};
-            if (cudaFuncGetAttributes(&fa, paged_chunk_kernel<HD, kBox>) != cudaSuccess) return USP_ERR_CUDA;
-            if ((long)fa.numRegs * kThreads < 2L * 128 * kSoftmaxRegs + 128L * kControlRegs) return USP_ERR_UNSUPPORTED;
-            if (cudaFuncSetAttribute(paged_chunk_kernel<HD, kBox>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
+            if (cudaFuncGetAttributes(&fa, paged_chunk_kernel<HD, Q4, kBox>) != cudaSuccess) return USP_ERR_CUDA;
+            if ((long)fa.numRegs * kThreads<Q4> < 128L * (2 * kSoftmaxRegs<Q4> + kControlRegs<Q4> + kConvertRegs<Q4>)) return USP_ERR_UNSUPPORTED;
+            if (cudaFuncSetAttribute(paged_chunk_kernel<HD, Q4, kBox>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
                 cudaSuccess)
                 return USP_ERR_CUDA;
             attr_set[dev] = true;
         }
     }
-    return launch_overlapped(paged_chunk_kernel<HD, kBox>, dim3((unsigned)grid), kThreads, kSmem, s, p);
+    return launch_overlapped(paged_chunk_kernel<HD, Q4, kBox>, dim3((unsigned)grid), kThreads<Q4>, kSmem, s, p);
 }
 
 }  // namespace
@@ -835,8 +1009,46 @@ int launch_paged_chunk(const PagedArgs &a, int n_lo, const PartSpace &w, cudaStr
     p.out_stride = a.out_stride; p.table_stride = a.table_stride;
     p.num_pages = (int32_t)a.num_pages; p.log_ps = a.log_ps; p.hq = a.hq;
     p.scale_log2 = a.scale_log2;
-    if (box_out) return a.hd == 128 ? launch_typed<128, true>(p, w.ctas, s) : launch_typed<64, true>(p, w.ctas, s);
-    return a.hd == 128 ? launch_typed<128, false>(p, w.ctas, s) : launch_typed<64, false>(p, w.ctas, s);
+    if (box_out) return a.hd == 128 ? launch_typed<128, false, true>(p, w.ctas, s) : launch_typed<64, false, true>(p, w.ctas, s);
+    return a.hd == 128 ? launch_typed<128, false, false>(p, w.ctas, s) : launch_typed<64, false, false>(p, w.ctas, s);
+}
+
+int launch_paged_q4_chunk(const PagedQ4Args &a, int n_lo, const PartSpace &w, cudaStream_t s) {
+    const DeviceInfo *di = device_info();
+    if (!di) return USP_ERR_CUDA;
+    ChunkParams p{};
+    const int ps = 1 << a.log_ps;
+    const uint32_t box = (uint32_t)std::min(ps, kN);
+    p.tq_tokens = kM / a.G;
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return USP_ERR_CUDA;
+    const cuuint64_t dims[3] = {(cuuint64_t)a.hd, (cuuint64_t)a.hq, (cuuint64_t)a.tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)a.hd * 2, (cuuint64_t)a.q_stride * 2};
+    const cuuint32_t qbox[3] = {64, (cuuint32_t)a.G, (cuuint32_t)p.tq_tokens}, estr[3] = {1, 1, 1};
+    if (enc(&p.tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(a.q), dims, strides, qbox, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
+        !make_codes_tmap(&p.tk, a.k, a.num_pages, a.k_page, a.hkv, ps, a.hd, box) ||
+        !make_codes_tmap(&p.tv, a.v, a.num_pages, a.v_page, a.hkv, ps, a.hd, box))
+        return USP_ERR_CUDA;
+    p.ks = a.ks; p.vs = a.vs; p.ks_page = a.ks_page; p.vs_page = a.vs_page;
+    p.s.cu = a.cu; p.s.kv = a.kv;
+    p.s.tokens = a.tokens; p.s.max_keys = q4_max_keys(a);
+    p.s.nreq = a.nreq; p.s.hkv = a.hkv; p.s.G = a.G;
+    p.s.tb = 2 * p.tq_tokens; p.s.causal = a.causal;
+    p.s.n_lo = n_lo; p.s.n_hi = INT32_MAX;
+    p.s.over = kOver; p.s.min_span = kMinSpan; p.s.long_parts = kManyParts;
+    p.s.inv_ctas = 1.0f / (float)w.ctas;
+    p.s.by_tb = FastDiv((uint32_t)p.s.tb); p.s.by_G = FastDiv((uint32_t)a.G);
+    p.w = w;
+    p.out = static_cast<__nv_bfloat16 *>(a.out);
+    p.lse = a.lse;
+    p.table = a.table;
+    p.status = di->status;
+    p.out_stride = a.out_stride; p.table_stride = a.table_stride;
+    p.num_pages = (int32_t)a.num_pages; p.log_ps = a.log_ps; p.hq = a.hq;
+    p.scale_log2 = a.scale_log2;
+    return a.hd == 128 ? launch_typed<128, true, false>(p, w.ctas, s) : launch_typed<64, true, false>(p, w.ctas, s);
 }
 
 }  // namespace usp

@@ -59,24 +59,49 @@ int few_heads(int G) {
     return h;
 }
 
+// Which kernels run: one for units of few query rows (a request's new tokens x G), one for units of many (bf16), or both,
+// each with the CTAs (0: not launched) and unit rows of its partials.
 struct Route {
-    int few_ctas, few_rows, few_G;
+    int few_ctas, few_rows, few_G, many_ctas;
+    int split;   // the most new tokens of a request that the kernel for few rows takes
+    bool alone;  // the kernel for many rows takes all requests (the other's workspace counts all the same)
 };
 Route route(const usp_paged_q4_desc &d, int sms) {
     Route r{};
-    r.few_G = few_heads(d.hq / d.cache.hkv);
-    r.few_rows = r.few_G * (int64_t)std::max(1, d.max_new) <= 8 ? 8 : 16;
-    r.few_ctas = q4_few_ctas(sms, r.few_rows, d.dtype);
+    const int G = d.hq / d.cache.hkv, most = 16;
+    const int64_t rows = G * (int64_t)std::max(1, d.max_new);
+    r.few_G = few_heads(G);
+    r.split = INT_MAX;
+    if (d.dtype == USP_BF16 && (rows > most || G > most)) {
+        r.many_ctas = sms;
+        // beside chunks, the few-row requests are mostly single tokens: the kernel of 8 rows takes those where it can
+        r.split = G > most ? 0 : (G > 8 ? most : 8) / G;
+    }
+    if (r.split > 0) {
+        r.few_rows = r.few_G * std::min<int64_t>(std::max(1, d.max_new), r.split) <= 8 ? 8 : 16;
+        r.few_ctas = q4_few_ctas(sms, r.few_rows, d.dtype);
+    }
+    if (r.many_ctas && r.few_ctas) {
+        // The requests for the second kernel are at most `few`, as many as may be short when the rows add up to `tokens`.
+        const int64_t M = std::min<int64_t>(d.max_new, d.tokens), all = d.nreq * M;
+        const int64_t few = M > r.split ? (all - std::min(d.tokens, all)) / (M - r.split) : d.nreq;
+        r.alone = few * d.cache.hkv <= sms;
+    }
     return r;
 }
 
-size_t workspace_bytes_of(const Route &r, int hd) { return part_bytes(r.few_ctas, r.few_rows, hd); }
+size_t workspace_bytes_of(const Route &r, int hd) {
+    return (r.few_ctas ? part_bytes(r.few_ctas, r.few_rows, hd) : 0) + (r.many_ctas ? part_bytes(r.many_ctas, kChunkRows, hd) : 0);
+}
 
-// What the caller provides: what every call with this max_new or a smaller one uses (the layout of 8 rows has more
-// headers than that of 16).
+// What the caller provides: what every call with this max_new or a smaller one uses. The layouts of few rows alone are
+// larger than those of more rows (in headers) or beside chunks.
 size_t workspace_bytes_for(const usp_paged_q4_desc &d, int sms) {
     const Route r = route(d, sms);
-    return std::max(workspace_bytes_of(r, d.cache.hd), part_bytes(q4_few_ctas(sms, 8, d.dtype), 8, d.cache.hd));
+    size_t most = workspace_bytes_of(r, d.cache.hd);
+    if (r.few_ctas)
+        for (int rows : {8, 16}) most = std::max(most, part_bytes(q4_few_ctas(sms, rows, d.dtype), rows, d.cache.hd));
+    return most;
 }
 
 PartSpace part_space(char *&at, int ctas, int rows, int hd) {
@@ -131,10 +156,19 @@ int usp_paged_attn_q4(const void *q, const void *k_cache, const void *v_cache, c
     char *at = static_cast<char *>(workspace);
     CombineArgs c{};
     c.out = out; c.lse = lse; c.out_stride = a.out_stride;
-    c.G = r.few_G; c.hq = a.hq; c.by_G = FastDiv((uint32_t)r.few_G);
-    c.w[1] = part_space(at, r.few_ctas, r.few_rows, a.hd);
-    rc = launch_paged_q4_few(a, r.few_G, r.few_rows, INT_MAX, false, c.w[1], s);
-    if (rc) return rc;
+    // (a unit's heads: the KV head's, or fewer in the kernel for few rows, which then runs alone)
+    const int G = r.many_ctas ? a.G : r.few_G;
+    c.G = G; c.hq = a.hq; c.by_G = FastDiv((uint32_t)G);
+    if (r.many_ctas) {
+        c.w[0] = part_space(at, r.many_ctas, kChunkRows, a.hd);
+        rc = launch_paged_q4_chunk(a, r.alone ? 0 : r.split, c.w[0], s);
+        if (rc) return rc;
+    }
+    if (r.few_ctas && !r.alone) {
+        c.w[1] = part_space(at, r.few_ctas, r.few_rows, a.hd);
+        rc = launch_paged_q4_few(a, r.few_G, r.few_rows, r.split, r.many_ctas > 0, c.w[1], s);
+        if (rc) return rc;
+    }
     return launch_paged_combine(c, a.hd, a.dtype, s);
 }
 

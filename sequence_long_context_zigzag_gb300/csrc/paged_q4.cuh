@@ -58,9 +58,37 @@ __device__ __forceinline__ void copies_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
+// ---- codes to operands: (136 + c) s - 136 s in bf16, exact (see paged_q4_few.cu) ----
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+// two scale bytes as bf16 numbers: (b << 4) + the exponent field's 107 (see q4_scale)
+__device__ __forceinline__ uint32_t q4_scales2(uint32_t lo, uint32_t hi) { return lo * 0x10u + (hi * 0x100000u + 0x35803580u); }
+__device__ __forceinline__ uint32_t q4_scales2(uint32_t b) { return b * 0x100010u + 0x35803580u; }
+__device__ __forceinline__ uint32_t q4_minus136(uint32_t s2) {
+    return fma_bf16x2(s2, 0xc308c308u, 0x80008000u);  // -136 s - 0
+}
+// The codes j of a word (the low nibbles of the halves of word >> 4 j) as values. One of the conversion's two constants is
+// held in a register: an instruction has room for one of its own, and with both known the compiler takes two
+// instructions (143 instead of 72 logic operations per 16 keys).
+struct Q4Nibbles {
+    uint32_t magic;
+    __device__ __forceinline__ Q4Nibbles() { asm volatile("mov.b32 %0, 0x43084308;" : "=r"(magic)); }
+    __device__ __forceinline__ uint32_t values(uint32_t word, int j, uint32_t s2, uint32_t off) const {
+        uint32_t x;
+        asm("lop3.b32 %0, %1, 0x000f000f, %2, 0x6a;" : "=r"(x) : "r"(word >> (4 * j)), "r"(magic));  // (a & b) ^ c
+        return fma_bf16x2(x, s2, off);
+    }
+};
+
 // Units of up to `rows` (8 or 16) query rows, G query heads each (a divisor of the group's); requests with at most n_hi new
 // tokens. `second`: the call's other kernel is in the stream before it.
 int launch_paged_q4_few(const PagedQ4Args &a, int G, int rows, int n_hi, bool second, const PartSpace &w, cudaStream_t s);
 int q4_few_ctas(int sms, int rows, int dtype);
+
+// bf16, units of up to kChunkRows query rows, one CTA per SM; requests with more than n_lo new tokens (paged_chunk.cu)
+int launch_paged_q4_chunk(const PagedQ4Args &a, int n_lo, const PartSpace &w, cudaStream_t s);
 
 }  // namespace usp

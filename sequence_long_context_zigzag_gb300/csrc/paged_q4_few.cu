@@ -112,28 +112,6 @@ __device__ __forceinline__ uint32_t lds8(uint32_t a) {
     asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x) : "r"(a) : "memory");
     return x;
 }
-__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
-    uint32_t d;
-    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-    return d;
-}
-// two scale bytes as bf16 numbers: (b << 4) + the exponent field's 107 (see q4_scale)
-__device__ __forceinline__ uint32_t scales2(uint32_t lo, uint32_t hi) { return lo * 0x10u + (hi * 0x100000u + 0x35803580u); }
-__device__ __forceinline__ uint32_t minus136(uint32_t s2) {
-    return fma_bf16x2(s2, 0xc308c308u, 0x80008000u);  // -136 s - 0
-}
-// The codes j of a word (the low nibbles of the halves of word >> 4 j) as values. One of the conversion's two constants is
-// held in a register: an instruction has room for one of its own, and with both known the compiler takes two
-// instructions (143 instead of 72 logic operations per 16 keys).
-struct Nibbles {
-    uint32_t magic;
-    __device__ __forceinline__ Nibbles() { asm volatile("mov.b32 %0, 0x43084308;" : "=r"(magic)); }
-    __device__ __forceinline__ uint32_t values(uint32_t word, int j, uint32_t s2, uint32_t off) const {
-        uint32_t x;
-        asm("lop3.b32 %0, %1, 0x000f000f, %2, 0x6a;" : "=r"(x) : "r"(word >> (4 * j)), "r"(magic));  // (a & b) ^ c
-        return fma_bf16x2(x, s2, off);
-    }
-};
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); }
 __device__ __forceinline__ bool consumers_all(bool x) {
     uint32_t r;
@@ -270,7 +248,7 @@ template <int HD, int NT, bool F32> __device__ void consumer(const FewParams &p,
     float *xch = reinterpret_cast<float *>(smem + C::kX);
     float2 *ml = reinterpret_cast<float2 *>(smem + C::kML);  // [warp][8 NT rows]
     uint2 *q_s = reinterpret_cast<uint2 *>(smem + C::kQ);
-    const Nibbles nib;
+    const Q4Nibbles nib;
     // addresses inside a stage: K's row k = g (and + 8), this lane's values; V's rows 2 t, 2 t + 1 (and + 8), its columns; a
     // step's rows are 16 further
     const int kkey = warp * 16 * kW + key_of<HD>(g);
@@ -366,8 +344,8 @@ template <int HD, int NT, bool F32> __device__ void consumer(const FewParams &p,
                         const uint2 x = lds64(at);
                         w[e][0] = x.x; w[e][1] = x.y;
                     }
-                    s2[e] = lds8(sbs + ks_at + (i * 16 + e * 8) * C::kSRow) * 0x100010u + 0x35803580u;
-                    off[e] = minus136(s2[e]);
+                    s2[e] = q4_scales2(lds8(sbs + ks_at + (i * 16 + e * 8) * C::kSRow));
+                    off[e] = q4_minus136(s2[e]);
                 }
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
@@ -472,8 +450,8 @@ template <int HD, int NT, bool F32> __device__ void consumer(const FewParams &p,
                         }
                         b[e] = lds8(sbs + vs_at[e] + (i * 16 + h * 8) * C::kSRow);
                     }
-                    s2[h] = scales2(b[0], b[1]);
-                    off[h] = minus136(s2[h]);
+                    s2[h] = q4_scales2(b[0], b[1]);
+                    off[h] = q4_minus136(s2[h]);
                 }
 #pragma unroll
                 for (int x = 0; x < kMT / 4; ++x) {
