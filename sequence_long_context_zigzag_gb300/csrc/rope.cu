@@ -7,8 +7,11 @@
 // formula alone, and not on how a compiler contracts it.
 //
 // What bounds it: HBM for long sequences (each element is read and written once for 3 operations), latency for a decode
-// step. A row (one head of one token) has hd / 16 threads, 16 elements each: 8 of either half of its pairs. Rows of q, K and V
-// of a token lie one after the other in a CTA's range, so the accesses in flight are close together.
+// step. A row (one head of one token) has hd / 16 threads, 16 elements each: 8 of either half of its pairs. A thread stays
+// with its token, whose cosines and sines it holds, and walks the heads of q, K and V, the next row's loads in flight; the
+// threads of a token side by side read a few KB in a row.
+#include <string.h>
+
 #include <algorithm>
 
 #include "paged.cuh"
@@ -19,7 +22,6 @@ namespace usp {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMostPasses = 4;
 constexpr int kSearch = 1024;  // entries of cu that a CTA searches in shared memory
 
 enum RopeMode { ROPE_PLAIN = 0, ROPE_CACHE = 1, ROPE_Q4 = 2 };
@@ -33,41 +35,20 @@ struct RopeArgs {
     int64_t q_stride, k_stride, v_stride, qo_stride, ko_stride;  // bytes between tokens
     int64_t k_page, v_page, ks_page, vs_page;                    // bytes between pages
     int64_t max_pos;
-    uint32_t rows, tokens, per_cta, nslots;
+    uint32_t tokens, nslots;
     int32_t nreq;                                                // entries of kv, or packed samples
-    int32_t hq, hkv, per_token;                                  // per_token: heads of q, K and V together
+    int32_t hq, hkv, heads;                                      // heads: of q, K and V together
+    int32_t log_side;                                            // rows of a token side by side: 1 << log_side
     int32_t rot, log_ps;
     bool interleaved, inverse, quads;                            // quads: see group_max
-    FastDiv by_heads, by_L;
-    uint32_t L;
+    FastDiv by_L;
 };
 
-template <typename T> __device__ __forceinline__ void load8(const char *p, float (&x)[8]) {
-    if constexpr (sizeof(T) == 2) {
-        const uint4 w = *reinterpret_cast<const uint4 *>(p);
-        const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+__device__ __forceinline__ void load8(const char *p, float (&x)[8]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = bf16x2_to_float2(a[i]);
-            x[2 * i] = f.x;
-            x[2 * i + 1] = f.y;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float4 f = reinterpret_cast<const float4 *>(p)[i];
-            x[4 * i] = f.x; x[4 * i + 1] = f.y; x[4 * i + 2] = f.z; x[4 * i + 3] = f.w;
-        }
-    }
-}
-template <typename T> __device__ __forceinline__ void store8(char *p, const float (&x)[8]) {
-    if constexpr (sizeof(T) == 2) {
-        *reinterpret_cast<uint4 *>(p) = make_uint4(float2_to_bf16x2(x[0], x[1]), float2_to_bf16x2(x[2], x[3]),
-                                                   float2_to_bf16x2(x[4], x[5]), float2_to_bf16x2(x[6], x[7]));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            reinterpret_cast<float4 *>(p)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    for (int i = 0; i < 2; ++i) {
+        const float4 f = reinterpret_cast<const float4 *>(p)[i];
+        x[4 * i] = f.x; x[4 * i + 1] = f.y; x[4 * i + 2] = f.z; x[4 * i + 3] = f.w;
     }
 }
 
@@ -77,10 +58,11 @@ __device__ __forceinline__ void turn(float &u, float &v, float c, float s) {
     u = a;
 }
 
+// the largest magnitude; NaN if there is one
 __device__ __forceinline__ float max8(const float (&x)[8]) {
-    float m = 0.f;  // a NaN is left out
+    float m = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));
+    for (int e = 0; e < 8; ++e) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(x[e])));
     return m;
 }
 
@@ -88,7 +70,13 @@ __device__ __forceinline__ float max8(const float (&x)[8]) {
 // call it. A row's lane c holds runs c and R + c for c < R, 2 c and 2 c + 1 behind that (R: the lanes of its row that hold the
 // halves of pairs). Where R is a multiple of 4 a group is a run of four lanes or both runs of two; else each member
 // is fetched from its lane.
-template <int kLanes> __device__ __forceinline__ void group_max(float a, float b, int c, int R, bool quads, float &ga, float &gb) {
+template <int kLanes> __device__ __forceinline__ void group_max(float a, float b, int c, int R, bool none, bool quads,
+                                                                        float &ga, float &gb) {
+    if (none) {  // no row of the call has halves
+        ga = fmaxf(a, b);
+        ga = gb = fmaxf(ga, __shfl_xor_sync(0xffffffffu, ga, 1));
+        return;
+    }
     if (quads) {
         const bool split = c < R;
         float x = split ? a : fmaxf(a, b), y = b;
@@ -132,73 +120,159 @@ __device__ __forceinline__ int find_sample(const int32_t *cu, int n, const int32
     return lo;
 }
 
-template <typename T, int HD, int kMode> __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs p) {
-    constexpr int kLanes = HD / 16, kRows = kThreads / kLanes;  // lanes of a row; rows of a pass
-    constexpr int kMostTokens = kMostPasses * kRows + 1;
+// 8 elements as they lie in memory
+template <typename T> struct Raw8 {
+    uint4 w[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const char *p) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = reinterpret_cast<const uint4 *>(p)[i];
+    }
+    __device__ __forceinline__ void store(char *p) const {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4 *>(p)[i] = w[i];
+    }
+    __device__ __forceinline__ void values(float (&x)[8]) const {
+        if constexpr (sizeof(T) == 2) {
+            const uint32_t a[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = bf16x2_to_float2(a[i]);
+                x[2 * i] = f.x;
+                x[2 * i + 1] = f.y;
+            }
+        } else {
+            memcpy(x, w, sizeof(x));
+        }
+    }
+    __device__ __forceinline__ void set(const float (&x)[8]) {
+        if constexpr (sizeof(T) == 2)
+            w[0] = make_uint4(float2_to_bf16x2(x[0], x[1]), float2_to_bf16x2(x[2], x[3]), float2_to_bf16x2(x[4], x[5]),
+                              float2_to_bf16x2(x[6], x[7]));
+        else
+            memcpy(w, x, sizeof(x));
+    }
+};
+
+// rows of a thread whose loads are in flight at once, at three CTAs per SM
+template <typename T> constexpr int rope_batch(int mode) {
+    const int n = mode == ROPE_PLAIN ? 4 : mode == ROPE_CACHE ? 3 : 2;
+    return sizeof(T) == 2 ? n : (n + 1) / 2;
+}
+
+template <typename T, int HD, int kMode> __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeArgs p) {
+    constexpr int kLanes = HD / 16, kRows = kThreads / kLanes;  // lanes of a row; rows side by side in a CTA
+    constexpr int kRowBytes = HD * (int)sizeof(T), kStored = kMode == ROPE_Q4 ? q4_code_bytes(HD) : kRowBytes;
+    constexpr int kBatch = rope_batch<T>(kMode);
     __shared__ int32_t part[kSearch];
-    __shared__ int32_t pos_s[kMostTokens], slot_s[kMostTokens];
+    __shared__ int32_t pos_s[kRows], slot_s[kRows];
     wait_grid_before();
-    const uint32_t r0 = blockIdx.x * p.per_cta, r1 = min(r0 + p.per_cta, p.rows);
-    const uint32_t t0 = p.by_heads.div(r0), ntok = p.by_heads.div(r1 - 1) + 1 - t0;
-    // ---- positions (-1: none) and slots of the CTA's tokens ----
+    // ---- this thread's token, and its part of the token's rows ----
+    const int side = 1 << p.log_side;
+    const uint32_t t0 = blockIdx.x * (kRows >> p.log_side), ntok = min((uint32_t)(kRows >> p.log_side), p.tokens - t0);
+    const int c = threadIdx.x % kLanes, row = threadIdx.x / kLanes, h0 = row & (side - 1);
+    const uint32_t tl = (uint32_t)row >> p.log_side, t = t0 + tl;
+    const bool live = tl < ntok;
+    // runs of 8: one of either half of the pairs, or neighbours (V, what is not rotated, interleaved pairs)
+    const int R = p.interleaved ? 0 : p.rot / 16;
+    struct Row {
+        int head, d0, d1;
+        bool q, k, ok;
+    };
+    auto row_of = [&](int h) {
+        Row r;
+        r.q = h < p.hq;
+        r.k = !r.q && h < p.hq + p.hkv;
+        r.head = r.q ? h : r.k ? h - p.hq : h - p.hq - p.hkv;
+        r.ok = live && h < p.heads;
+        const bool halves = (r.q || r.k) && c < R;
+        r.d0 = halves ? 8 * c : 16 * c;
+        r.d1 = halves ? p.rot / 2 + 8 * c : 16 * c + 8;
+        return r;
+    };
+    Raw8<T> a[kBatch], b[kBatch];
+    // (also of tokens that turn out to have no place: their rows are there)
+    auto fetch = [&](int first) {
+        const char *q = p.q + t * p.q_stride, *k = p.k + t * p.k_stride, *v = p.v + t * p.v_stride;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const Row r = row_of(first + i * side + h0);
+            if (!r.ok) continue;
+            const char *src = (r.q ? q : r.k ? k : v) + r.head * kRowBytes;
+            a[i].load(src + r.d0 * sizeof(T));
+            b[i].load(src + r.d1 * sizeof(T));
+        }
+    };
+    fetch(0);
+    // ---- positions (-1: none) and slots of the CTA's tokens, under the first loads ----
     const bool search = p.rot > 0 && !p.positions && p.cu && p.nreq > 0;
     const int step = (p.nreq + kSearch - 1) / kSearch;
     if (search) {
-        for (int i = threadIdx.x; i * step < p.nreq; i += kThreads) part[i] = p.cu[i * step];
+        for (int i = threadIdx.x; (int64_t)i * step < p.nreq; i += kThreads) part[i] = p.cu[i * step];
         __syncthreads();
     }
-    for (uint32_t i = threadIdx.x; i < ntok; i += kThreads) {
-        const uint32_t t = t0 + i;
+    if (threadIdx.x < ntok) {
+        const uint32_t u = t0 + threadIdx.x;
+        const uint32_t slot = kMode != ROPE_PLAIN ? (uint32_t)p.slots[u] : 0;
         int64_t pos = -1;
         if (p.rot > 0) {
             if (p.positions) {
-                pos = p.positions[t];
+                pos = p.positions[u];
             } else if constexpr (kMode == ROPE_PLAIN) {
-                uint32_t b, l;
-                p.by_L.divmod(t, b, l);
+                uint32_t s, l;
+                p.by_L.divmod(u, s, l);
                 pos = l;
                 if (search && part[0] <= (int)l) pos = (int64_t)l - p.cu[find_sample(p.cu, p.nreq, part, step, l)];
-            } else if (search && part[0] <= (int)t) {
-                const int r = find_sample(p.cu, p.nreq, part, step, t);
+            } else if (search && part[0] <= (int)u) {
+                const int r = find_sample(p.cu, p.nreq, part, step, u);
                 const int64_t end = p.cu[r + 1];  // a token behind the last request has no position
-                if (t < end) pos = (int64_t)p.kv[r] - end + t;
+                if (u < end) pos = (int64_t)p.kv[r] - end + u;
             }
             if (pos >= p.max_pos) pos = -1;
         }
-        pos_s[i] = (int32_t)max(pos, (int64_t)-1);
-        if (kMode != ROPE_PLAIN) {
-            const uint32_t slot = (uint32_t)p.slots[t];
-            slot_s[i] = slot < p.nslots && (p.rot == 0 || pos >= 0) ? (int32_t)slot : -1;
-        }
+        pos_s[threadIdx.x] = (int32_t)max(pos, (int64_t)-1);
+        if (kMode != ROPE_PLAIN) slot_s[threadIdx.x] = slot < p.nslots && (p.rot == 0 || pos >= 0) ? (int32_t)slot : -1;
     }
     __syncthreads();
-    // ---- rows ----
-    const int c = threadIdx.x % kLanes;
-    for (uint32_t first = r0; first < r1; first += kRows) {
-        const uint32_t r = first + threadIdx.x / kLanes;
-        uint32_t t, h;
-        p.by_heads.divmod(min(r, r1 - 1), t, h);
-        const int32_t pos = pos_s[t - t0], slot = kMode != ROPE_PLAIN ? slot_s[t - t0] : 0;
-        const bool is_q = (int)h < p.hq, is_k = !is_q && (int)h < p.hq + p.hkv, is_v = !is_q && !is_k;
-        const int head = is_q ? (int)h : is_k ? (int)h - p.hq : (int)h - p.hq - p.hkv;
-        const bool turned = !is_v && p.rot > 0;
-        const int R = turned && !p.interleaved ? p.rot / 16 : 0;
-        const bool ok = r < r1 && (kMode == ROPE_PLAIN || (is_q ? pos >= 0 : slot >= 0));
-        const int d0 = c < R ? 8 * c : 16 * c, d1 = c < R ? p.rot / 2 + 8 * c : 16 * c + 8;
-        float x[8] = {}, y[8] = {};
-        if (ok) {
-            const char *src = (is_q ? p.q + t * p.q_stride : is_k ? p.k + t * p.k_stride : p.v + t * p.v_stride) +
-                              (int64_t)head * HD * sizeof(T);
-            load8<T>(src + d0 * sizeof(T), x);
-            load8<T>(src + d1 * sizeof(T), y);
-            if (turned && 16 * c < p.rot && pos >= 0) {
-                float cs[8], sn[8];
-                const char *row = reinterpret_cast<const char *>(p.table + (int64_t)pos * p.rot + 8 * c);
-                load8<float>(row, cs);
-                load8<float>(row + p.rot * 2, sn);
+    const int32_t pos = live ? pos_s[tl] : -1, slot = live && kMode != ROPE_PLAIN ? slot_s[tl] : -1;
+    const bool angles = 16 * c < p.rot && pos >= 0;
+    float cs[8], sn[8];
+    if (angles) {
+        const char *at = reinterpret_cast<const char *>(p.table + (int64_t)pos * p.rot + 8 * c);
+        load8(at, cs);
+        load8(at + p.rot * 2, sn);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (p.inverse) sn[e] = -sn[e];
+        for (int e = 0; e < 8; ++e)
+            if (p.inverse) sn[e] = -sn[e];
+    }
+    // ---- rows: head h's is h rows (of the page: h << log_ps rows) from the token's first ----
+    char *q_out = p.q_out + t * p.qo_stride, *k_out, *v_out = nullptr;
+    uint8_t *k_sc = nullptr, *v_sc = nullptr;
+    int k_step = kRowBytes;
+    if constexpr (kMode == ROPE_PLAIN) {
+        k_out = p.k_out + t * p.ko_stride;
+    } else {
+        const int64_t page = slot >> p.log_ps;
+        const int in_page = slot & ((1 << p.log_ps) - 1);
+        k_out = p.k_out + page * p.k_page + in_page * kStored;
+        v_out = p.v_out + page * p.v_page + in_page * kStored;
+        k_step = kStored << p.log_ps;
+        if constexpr (kMode == ROPE_Q4) {
+            k_sc = p.k_scales + page * p.ks_page + in_page * q4_scale_bytes(HD);
+            v_sc = p.v_scales + page * p.vs_page + in_page * q4_scale_bytes(HD);
+        }
+    }
+    for (int first = 0;;) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (i > 0 && first + i * side >= p.heads) break;
+            const Row r = row_of(first + i * side + h0);
+            const bool turned = (r.q || r.k) && angles, ok = r.ok && (kMode == ROPE_PLAIN || (r.q ? pos >= 0 : slot >= 0));
+            float x[8], y[8];
+            if (turned || kMode == ROPE_Q4) {
+                a[i].values(x);
+                b[i].values(y);
+            }
+            if (turned) {
                 if (p.interleaved) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -210,44 +284,67 @@ template <typename T, int HD, int kMode> __global__ void __launch_bounds__(kThre
                     for (int e = 0; e < 8; ++e) turn(x[e], y[e], cs[e], sn[e]);
                 }
             }
-        }
-        const int64_t page = slot >> p.log_ps;
-        const int64_t in_page = ((int64_t)head << p.log_ps) + (slot & ((1 << p.log_ps) - 1));  // row of the page
-        if (kMode == ROPE_Q4) {
-            float ga, gb;
-            group_max<kLanes>(max8(x), max8(y), c, R, p.quads, ga, gb);
-            if (ok && !is_q) {
-                const uint32_t ba = q4_scale_for(ga), bb = q4_scale_for(gb);
-                char *row = (is_k ? p.k_out + page * p.k_page : p.v_out + page * p.v_page) + in_page * q4_code_bytes(HD);
-                *reinterpret_cast<uint32_t *>(row + d0 / 2) = q4_pack(x, ba);
-                *reinterpret_cast<uint32_t *>(row + d1 / 2) = q4_pack(y, bb);
-                uint8_t *sc = (is_k ? p.k_scales + page * p.ks_page : p.v_scales + page * p.vs_page) + in_page * q4_scale_bytes(HD);
-                if (d0 % kQ4Group == 0) sc[d0 / kQ4Group] = (uint8_t)ba;
-                if (d1 % kQ4Group == 0) sc[d1 / kQ4Group] = (uint8_t)bb;
+            if constexpr (kMode == ROPE_Q4) {
+                const int split = r.k ? R : 0;
+                float ma = max8(x), mb = max8(y), ga, gb;
+                if (__any_sync(0xffffffffu, ma != ma || mb != mb)) {  // NaN is stored as 0
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        x[e] = x[e] == x[e] || r.q ? x[e] : 0.f;
+                        y[e] = y[e] == y[e] || r.q ? y[e] : 0.f;
+                    }
+                    ma = max8(x);
+                    mb = max8(y);
+                }
+                group_max<kLanes>(ma, mb, c, split, R == 0, p.quads, ga, gb);
+                if (ok && !r.q) {
+                    const Q4Scale sa(ga), sb = R == 0 ? sa : Q4Scale(gb);
+                    uint32_t wa, wb;
+                    if (sizeof(T) == 2 && !(r.k && p.rot > 0)) {
+                        wa = q4_pack<true>(x, sa);
+                        wb = q4_pack<true>(y, sb);
+                    } else {
+                        wa = q4_pack<false>(x, sa);
+                        wb = q4_pack<false>(y, sb);
+                    }
+                    char *to = (r.k ? k_out : v_out) + (int64_t)r.head * k_step;
+                    *reinterpret_cast<uint32_t *>(to + r.d0 / 2) = wa;
+                    *reinterpret_cast<uint32_t *>(to + r.d1 / 2) = wb;
+                    uint8_t *sc = (r.k ? k_sc : v_sc) + ((int64_t)r.head << p.log_ps) * q4_scale_bytes(HD);
+                    if (r.d0 % kQ4Group == 0) sc[r.d0 / kQ4Group] = (uint8_t)sa.b;
+                    if (r.d1 % kQ4Group == 0) sc[r.d1 / kQ4Group] = (uint8_t)sb.b;
+                }
+            }
+            if (ok && (kMode != ROPE_Q4 || r.q)) {
+                if (turned) {
+                    a[i].set(x);
+                    b[i].set(y);
+                }
+                char *to = r.q ? q_out + r.head * kRowBytes : (r.k ? k_out : v_out) + (int64_t)r.head * k_step;
+                a[i].store(to + r.d0 * sizeof(T));
+                b[i].store(to + r.d1 * sizeof(T));
             }
         }
-        if (ok && (kMode != ROPE_Q4 || is_q)) {
-            char *dst;
-            if (is_q) dst = p.q_out + t * p.qo_stride + (int64_t)head * HD * sizeof(T);
-            else if (kMode == ROPE_PLAIN) dst = p.k_out + t * p.ko_stride + (int64_t)head * HD * sizeof(T);
-            else dst = (is_k ? p.k_out + page * p.k_page : p.v_out + page * p.v_page) + in_page * (HD * (int64_t)sizeof(T));
-            store8<T>(dst + d0 * sizeof(T), x);
-            store8<T>(dst + d1 * sizeof(T), y);
-        }
+        first += side * kBatch;
+        if (first >= p.heads) break;
+        fetch(first);
     }
 }
 
 template <int kMode> int launch_rope(RopeArgs a, int hd, int dtype, cudaStream_t s) {
     const DeviceInfo *di = device_info();
     if (!di) return USP_ERR_CUDA;
-    a.by_heads = FastDiv((uint32_t)a.per_token);
-    a.rows = a.tokens * (uint32_t)a.per_token;
     a.quads = a.interleaved || a.rot % 64 == 0;
-    // passes per CTA: as many as leave every SM eight CTAs
-    const uint32_t pass = (uint32_t)(kThreads / (hd / 16));
-    const uint32_t passes = std::max(1u, std::min((uint32_t)kMostPasses, a.rows / (pass * 8u * (uint32_t)di->sm_count)));
-    a.per_cta = pass * passes;
-    const dim3 grid((a.rows + a.per_cta - 1) / a.per_cta);
+    // Rows of a token side by side: all, as far as a CTA has place, where there are few; in large calls eight, or four where
+    // the rows go to pages (40 heads of 128 of 32768 tokens: 2, 4, 8, 16, 32 of them 126, 114, 107, 119, 174 us; 48 heads of 46000
+    // into a cache 172, 169, 176, 211, 307).
+    const int rows = kThreads / (hd / 16);
+    int log_side = 0;
+    const int most = (int64_t)a.tokens * a.heads < (int64_t)rows * 8 * di->sm_count ? 30 : kMode == ROPE_PLAIN ? 3 : 2;
+    while (log_side < most && (1 << log_side) < a.heads && (2 << log_side) <= rows) ++log_side;
+    a.log_side = log_side;
+    const uint32_t per_cta = (uint32_t)rows >> log_side;
+    const dim3 grid((a.tokens + per_cta - 1) / per_cta);
     auto go = [&](auto kernel) { return launch_overlapped(kernel, grid, kThreads, 0, s, a); };
     if (dtype == USP_BF16)
         return hd == 128 ? go(rope_kernel<__nv_bfloat16, 128, kMode>) : go(rope_kernel<__nv_bfloat16, 64, kMode>);
@@ -318,7 +415,7 @@ RopeArgs append_args(const void *q, void *q_out, const void *k, const void *v, c
     a.tokens = (uint32_t)d.tokens;
     a.nslots = (uint32_t)(num_pages * page_size);
     a.nreq = d.nreq;
-    a.hq = d.hq; a.hkv = hkv; a.per_token = d.hq + 2 * hkv;
+    a.hq = d.hq; a.hkv = hkv; a.heads = d.hq + 2 * hkv;
     a.rot = d.rot; a.log_ps = log2_of(page_size);
     a.interleaved = d.interleaved != 0;
     return a;
@@ -384,10 +481,10 @@ int usp_rope(const void *q, void *q_out, const void *k, void *k_out, const float
     a.max_pos = d.max_pos;
     a.tokens = (uint32_t)(d.bs * d.L);
     a.nreq = d.nseq;
-    a.hq = d.hq; a.hkv = d.hkv; a.per_token = d.hq + d.hkv;
+    a.hq = d.hq; a.hkv = d.hkv; a.heads = d.hq + d.hkv;
     a.rot = d.rot;
     a.interleaved = d.interleaved != 0; a.inverse = d.inverse != 0;
-    a.by_L = FastDiv((uint32_t)d.L); a.L = (uint32_t)d.L;
+    a.by_L = FastDiv((uint32_t)d.L);
     return launch_rope<ROPE_PLAIN>(a, d.hd, d.dtype, reinterpret_cast<cudaStream_t>(stream));
 }
 
