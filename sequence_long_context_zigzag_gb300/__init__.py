@@ -615,21 +615,13 @@ def usp_rope(q, k, table, positions=None, cu_seqlens=None, interleaved: bool = F
                       q_out, k_out)
 
 
-class UspRopeFunction(torch.autograd.Function):
-    """usp_rope as a differentiable op: (q, k) rotated; the gradients are rotated back, in one launch. (k may be None.)"""
+class UspRopeFunction:
+    """usp_rope as a differentiable op: (q, k) rotated; the gradients are rotated back, in one launch, and are
+    differentiable in turn. (k may be None. The op itself is in csrc/binding.cpp.)"""
 
     @staticmethod
-    def forward(ctx, q, k, table, positions=None, cu_seqlens=None, interleaved=False):
-        ctx.save_for_backward(table, positions, cu_seqlens)
-        ctx.interleaved = interleaved
-        return usp_rope(q, k, table, positions, cu_seqlens, interleaved)
-
-    @staticmethod
-    def backward(ctx, dq, dk):
-        table, positions, cu_seqlens = ctx.saved_tensors
-        dq, dk = usp_rope(dq.contiguous(), None if dk is None else dk.contiguous(), table, positions, cu_seqlens,
-                          ctx.interleaved, inverse=True)
-        return dq, dk, None, None, None, None
+    def apply(q, k, table, positions=None, cu_seqlens=None, interleaved=False):
+        return _on_stream("usp_rope", q, None, _abi.binding().rope_grad, q, k, table, positions, cu_seqlens, interleaved)
 
 
 def usp_rope_append(q, k, v, k_cache, v_cache, slot_map, table, cu_new=None, kv_lens=None, positions=None, k_scales=None,

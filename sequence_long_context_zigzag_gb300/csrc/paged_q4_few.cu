@@ -331,6 +331,7 @@ template <int HD, int NT, bool F32> __device__ void consumer(const FewParams &p,
             const int key0 = kt * C::kKT + warp * 16 * kW;
             // ---- S^T = K Q^T ----
             float sc[kW][NT][4];
+            float low[kW][NT][4];  // F32: of q's second and third terms
 #pragma unroll
             for (int i = 0; i < kW; ++i) {
                 uint32_t w[2][kWords], s2[2], off[2];
@@ -350,7 +351,7 @@ template <int HD, int NT, bool F32> __device__ void consumer(const FewParams &p,
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[i][n][e] = 0.f;
+                    for (int e = 0; e < 4; ++e) sc[i][n][e] = low[i][n][e] = 0.f;
 #pragma unroll
                 for (int k = 0; k < kMT; ++k) {
                     uint32_t a[4];
@@ -365,7 +366,7 @@ template <int HD, int NT, bool F32> __device__ void consumer(const FewParams &p,
 #pragma unroll
                             for (int x = kT - 1; x >= 0; --x) {
                                 const uint2 b = lds64(sbase + C::kQ + (((x * kMT + k) * NT + n) * 32 + lane) * 8);
-                                mma16816(sc[i][n], a, b.x, b.y);
+                                mma16816(x ? low[i][n] : sc[i][n], a, b.x, b.y);
                             }
                         } else {
                             mma16816(sc[i][n], a, qf[k][n].x, qf[k][n].y);
@@ -378,6 +379,11 @@ template <int HD, int NT, bool F32> __device__ void consumer(const FewParams &p,
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 // sc: key g rows 2t, 2t+1; key g + 8
+                if constexpr (F32)
+#pragma unroll
+                    for (int i = 0; i < kW; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sc[i][n][e] += low[i][n][e];
                 if (key0 + 16 * kW > lim_all) {
                     const int key = key0 + key_of<HD>(g);
 #pragma unroll
@@ -434,9 +440,10 @@ template <int HD, int NT, bool F32> __device__ void consumer(const FewParams &p,
                 }
             }
             // ---- O^T += V^T P^T ----
-#pragma unroll
-            for (int i = 0; i < kW; ++i) {
-                uint32_t vw[2][2][kMT / 4], s2[2], off[2];  // [half of the step's keys][pair's element][word]
+            struct VRows {
+                uint32_t w[2][2][kMT / 4], s2[2], off[2];  // [half of the step's keys][pair's element][word]
+            };
+            auto load_v = [&](int i, VRows &v) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     uint32_t b[2];
@@ -444,35 +451,57 @@ template <int HD, int NT, bool F32> __device__ void consumer(const FewParams &p,
                     for (int e = 0; e < 2; ++e) {
                         if constexpr (HD == 128) {
                             const uint2 x = lds64(base + further(v_at[e], i * 16 + h * 8));
-                            vw[h][e][0] = x.x; vw[h][e][1] = x.y;
+                            v.w[h][e][0] = x.x; v.w[h][e][1] = x.y;
                         } else {
-                            vw[h][e][0] = lds32(base + further(v_at[e], i * 16 + h * 8));
+                            v.w[h][e][0] = lds32(base + further(v_at[e], i * 16 + h * 8));
                         }
                         b[e] = lds8(sbs + vs_at[e] + (i * 16 + h * 8) * C::kSRow);
                     }
-                    s2[h] = q4_scales2(b[0], b[1]);
-                    off[h] = q4_minus136(s2[h]);
+                    v.s2[h] = q4_scales2(b[0], b[1]);
+                    v.off[h] = q4_minus136(v.s2[h]);
                 }
+            };
+            // columns 2 j, 2 j + 1 of word x: the even and the odd columns of 8 are four codes of either key of a pair
+            auto operand = [&](const VRows &v, int x, int j, uint32_t (&a)[4]) {
 #pragma unroll
-                for (int x = 0; x < kMT / 4; ++x) {
-                    uint32_t even[2], odd[2];  // the even and the odd columns of 8, four codes of either key
+                for (int h = 0; h < 2; ++h) {
+                    a[2 * h] = nib.values(__byte_perm(v.w[h][0][x], v.w[h][1][x], 0x5410), j, v.s2[h], v.off[h]);
+                    a[2 * h + 1] = nib.values(__byte_perm(v.w[h][0][x], v.w[h][1][x], 0x7632), j, v.s2[h], v.off[h]);
+                }
+            };
+            if constexpr (F32) {
+                // a tile's sum on its own: the products' accumulation truncates, which over a thousand tiles would show
+                VRows v[kW];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        even[h] = __byte_perm(vw[h][0][x], vw[h][1][x], 0x5410);
-                        odd[h] = __byte_perm(vw[h][0][x], vw[h][1][x], 0x7632);
-                    }
+                for (int i = 0; i < kW; ++i) load_v(i, v[i]);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
+                for (int x = 0; x < kMT; ++x) {
+                    float sum[NT][4] = {};
+#pragma unroll
+                    for (int i = 0; i < kW; ++i) {
                         uint32_t a[4];
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            a[2 * h] = nib.values(even[h], j, s2[h], off[h]);
-                            a[2 * h + 1] = nib.values(odd[h], j, s2[h], off[h]);
-                        }
+                        operand(v[i], x / 4, x % 4, a);
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
 #pragma unroll
-                            for (int c = kT - 1; c >= 0; --c) mma16816(o[n][x * 4 + j], a, pf[i][n][c][0], pf[i][n][c][1]);
+                            for (int c = kT - 1; c >= 0; --c) mma16816(sum[n], a, pf[i][n][c][0], pf[i][n][c][1]);
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[n][x][e] += sum[n][e];
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < kW; ++i) {
+                    VRows v;
+                    load_v(i, v);
+#pragma unroll
+                    for (int x = 0; x < kMT; ++x) {
+                        uint32_t a[4];
+                        operand(v, x / 4, x % 4, a);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma16816(o[n][x], a, pf[i][n][0][0], pf[i][n][0][1]);
                     }
                 }
             }

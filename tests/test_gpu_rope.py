@@ -105,6 +105,49 @@ def test_rope_gradient(interleaved, dt):
     assert none is None and torch.equal(torch.autograd.grad(y, q, gq)[0], dq)
 
 
+def test_rope_second_gradient():
+    """The gradient is differentiable in turn: of <rotate back(g), u> with respect to g it is the rotation of u."""
+    table, cu = usp.usp_rope_table(30, 64), i32([0, 11, 30])
+    q, k = (torch.randn(1, 30, h, 64, device="cuda", requires_grad=True) for h in (3, 2))
+    gq, gk = (torch.randn_like(x, requires_grad=True) for x in (q, k))
+    uq, uk = torch.randn_like(q), torch.randn_like(k)
+    dq, dk = torch.autograd.grad(usp.UspRopeFunction.apply(q, k, table, None, cu, True), (q, k), (gq, gk), create_graph=True)
+    second = torch.autograd.grad((dq, dk), (gq, gk), (uq, uk))
+    want = usp.usp_rope(uq, uk, table, cu_seqlens=cu, interleaved=True)
+    assert all(torch.equal(a, b) for a, b in zip(second, want))
+
+
+def test_rope_gradients_in_a_graph():
+    """Forward and backward through the op, captured and replayed on other values; strided leaves."""
+    table = usp.usp_rope_table(24, 128)
+    base = torch.randn(2, 24, 8, 128, device="cuda").bfloat16()
+    both = base.clone().requires_grad_()
+    gq, gk = (torch.randn(2, 24, h, 128, device="cuda").bfloat16() for h in (5, 3))
+
+    def step():
+        y = usp.UspRopeFunction.apply(both[:, :, :5], both[:, :, 5:], table)
+        return (*y, torch.autograd.grad(y, both, (gq, gk))[0])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    with torch.no_grad():
+        both.copy_(base.flip(0))
+        gq.neg_()
+    graph.replay()
+    torch.cuda.synchronize()
+    want = step()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    pos = torch.arange(24).repeat(2)
+    for d, up in ((want[2][:, :, :5], gq), (want[2][:, :, 5:], gk)):
+        _, w, bound = rotate(up.flatten(0, 1), table.cpu(), pos, False, True)
+        near(d.flatten(0, 1), w, bound)
+
+
 def test_rotated_attention_step():
     """Rotation and attention as a training step uses them: forward and gradients of the two ops together agree with
     the formula's, differentiated by torch in 64 bits."""
