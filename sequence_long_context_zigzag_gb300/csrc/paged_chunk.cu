@@ -58,8 +58,8 @@ constexpr int kConvertWarp = kSoftmaxWarps + 4;  // the first of four (Q4)
 template <bool Q4> constexpr int kSegReaders = kSoftmaxWarps + 3 + (Q4 ? 4 : 0);  // the softmax warps, the producer, the issuers, the converters
 // the warpgroups' shares (setmaxnreg) add up to exactly the launch's registers
 template <bool Q4> constexpr int kLaunchRegs = (65536 / kThreads<Q4>) / 8 * 8;
-template <bool Q4> constexpr int kSoftmaxRegs = Q4 ? 184 : 208;
-template <bool Q4> constexpr int kConvertRegs = Q4 ? 72 : 0;
+template <bool Q4> constexpr int kSoftmaxRegs = Q4 ? 200 : 208;
+template <bool Q4> constexpr int kConvertRegs = Q4 ? 56 : 0;
 template <bool Q4> constexpr int kControlRegs = kLaunchRegs<Q4> * kWarps<Q4> / 4 - 2 * kSoftmaxRegs<Q4> - kConvertRegs<Q4>;
 template <bool Q4>
 constexpr bool split_ok = kControlRegs<Q4> >= 24 && kControlRegs<Q4> % 8 == 0 &&

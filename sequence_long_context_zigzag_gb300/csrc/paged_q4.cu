@@ -82,10 +82,11 @@ Route route(const usp_paged_q4_desc &d, int sms) {
         r.few_ctas = q4_few_ctas(sms, r.few_rows, d.dtype);
     }
     if (r.many_ctas && r.few_ctas) {
-        // The requests for the second kernel are at most `few`, as many as may be short when the rows add up to `tokens`.
-        const int64_t M = std::min<int64_t>(d.max_new, d.tokens), all = d.nreq * M;
-        const int64_t few = M > r.split ? (all - std::min(d.tokens, all)) / (M - r.split) : d.nreq;
-        r.alone = few * d.cache.hkv <= sms;
+        // A second kernel costs its launch, but a key of a short request costs the kernel for many rows half as much again
+        // and more (26 single tokens beside 7 chunks, hd 64: 27.4 us, all in one kernel 30.7; 14 of 4000 to 32000 keys
+        // 164, 226). Only where the tokens' number tells that no request is short does that kernel run alone.
+        const int64_t M = std::min<int64_t>(d.max_new, d.tokens);
+        r.alone = M > r.split && (d.nreq * M - std::min(d.tokens, d.nreq * M)) / (M - r.split) == 0;
     }
     return r;
 }

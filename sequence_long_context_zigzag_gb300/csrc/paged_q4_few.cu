@@ -35,7 +35,6 @@ namespace {
 
 constexpr int kOver = 512;     // a unit's constant cost, in keys
 constexpr int kWarps = 4;      // consumers
-constexpr int kW = 2;          // 16-key steps per warp and tile
 constexpr int kThreads = (kWarps + 1) * 32;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr float kRescale = 8.0f;  // log2 units
@@ -45,12 +44,13 @@ constexpr float kLn2 = 0.69314718055994531f;
 template <int HD, int NT, bool F32> struct Cfg {
     static constexpr int kTerms = F32 ? 3 : 1;
     static constexpr int kCtas = NT == 1 && !F32 ? 3 : 2; // per SM
+    static constexpr int kW = HD == 64 && NT == 1 && !F32 ? 4 : 2;  // 16-key steps per warp and tile
     static constexpr int kKT = 16 * kW * kWarps;          // keys per tile
-    static constexpr int kMinSpan = 192;                  // keys per CTA below which fewer CTAs work
+    static constexpr int kMinSpan = kKT + 64;             // keys per CTA below which fewer CTAs work
     static_assert(kMinSpan > kKT, "a span holds more than a tile");
     static constexpr int kRow = q4_code_bytes(HD), kSRow = q4_scale_bytes(HD);
     static constexpr int kCodes = kKT * kRow, kScales = kKT * kSRow;
-    static constexpr int kStages = (kCtas == 3 || F32 ? 3 : 4) * (HD == 128 ? 1 : 2);
+    static constexpr int kStages = (kCtas == 3 || F32 ? 3 : 4) * (kKT * HD == 128 * 128 ? 1 : 2);
     static constexpr int kXRow = HD + 4;                  // exchange row in floats
     static constexpr int kSc = kStages * 2 * kCodes;      // scales, behind all stages' codes (K, V each)
     static constexpr int kX = kSc + kStages * 2 * kScales;  // [warp][row][kXRow]
@@ -161,7 +161,7 @@ __device__ void producer(const FewParams &p, const SchedShared &sh, uint8_t *sme
         return (bool)__all_sync(0xffffffffu, r);
     };
     SegMsg *ring = reinterpret_cast<SegMsg *>(smem + C::kSeg);
-    const int ps = 1 << p.log_ps, piece = min(ps, C::kKT), pieces = C::kKT / piece;  // at most 8 pieces
+    const int ps = 1 << p.log_ps, piece = min(ps, C::kKT), pieces = C::kKT / piece;  // at most 16 pieces
     const bool v = lane >= pieces, loads = lane < 2 * pieces;
     const int pc = v ? lane - pieces : lane;
     const uint32_t dst0 = sbase + (v ? C::kCodes : 0) + pc * piece * C::kRow;
@@ -239,7 +239,7 @@ template <int HD, int NT, bool F32> __device__ void consumer(const FewParams &p,
     using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
     constexpr int kMT = HD / 16;  // 16-column tiles of O^T; 16-element steps of the head dim
     constexpr int kT = C::kTerms;
-    constexpr int kWords = HD / 32;  // K's words of a lane and key; a lane converts 8 kWords values of a key
+    constexpr int kW = C::kW, kWords = HD / 32;  // K's words of a lane and key; a lane converts 8 kWords values of a key
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     auto BAR = [&](int i) { return sbase + C::kBar + 8u * i; };
     auto wait = [&](int bar, uint32_t parity) {
@@ -657,7 +657,9 @@ int launch_paged_q4_few(const PagedQ4Args &a, int G, int rows, int n_hi, bool se
     if (!di) return USP_ERR_CUDA;
     FewParams p{};
     const int ps = 1 << a.log_ps;
-    const uint32_t box = (uint32_t)std::min(ps, 16 * kW * kWarps);
+    const bool f32 = a.dtype == USP_F32;
+    const int tile = a.hd == 128 || rows == 16 || f32 ? Cfg<128, 1, false>::kKT : Cfg<64, 1, false>::kKT;
+    const uint32_t box = (uint32_t)std::min(ps, tile);
     if (!make_codes_tmap(&p.tk, a.k, a.num_pages, a.k_page, a.hkv, ps, a.hd, box) ||
         !make_codes_tmap(&p.tv, a.v, a.num_pages, a.v_page, a.hkv, ps, a.hd, box))
         return USP_ERR_CUDA;
