@@ -33,6 +33,10 @@
 // converted anew for every unit that reads it: 400 instructions a thread for K and V in the 2750 cycles that a pair of
 // tiles takes the other roles, where converting the cache once into memory would need that memory, and 13% of the time of
 // a chunk of 900 tokens. Rows behind the last key need no clearing: whatever their bytes, they stand for finite numbers.
+//   Where a unit's rows fit one Q tile, reading is four times as fast as over a bf16 cache, and one chain of products,
+// softmax, products per key tile would bound the kernel: such a segment is split, both Q tiles being the same rows, each
+// for every other key tile. At its end the second one's state goes through a scratch in the workspace to the first one's
+// threads, which join the two (32 requests of 6000 keys, 20 rows: see launch_paged_q4_chunk).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -58,8 +62,8 @@ constexpr int kConvertWarp = kSoftmaxWarps + 4;  // the first of four (Q4)
 template <bool Q4> constexpr int kSegReaders = kSoftmaxWarps + 3 + (Q4 ? 4 : 0);  // the softmax warps, the producer, the issuers, the converters
 // the warpgroups' shares (setmaxnreg) add up to exactly the launch's registers
 template <bool Q4> constexpr int kLaunchRegs = (65536 / kThreads<Q4>) / 8 * 8;
-template <bool Q4> constexpr int kSoftmaxRegs = Q4 ? 200 : 208;
-template <bool Q4> constexpr int kConvertRegs = Q4 ? 56 : 0;
+template <bool Q4> constexpr int kSoftmaxRegs = Q4 ? 192 : 208;
+template <bool Q4> constexpr int kConvertRegs = Q4 ? 64 : 0;
 template <bool Q4> constexpr int kControlRegs = kLaunchRegs<Q4> * kWarps<Q4> / 4 - 2 * kSoftmaxRegs<Q4> - kConvertRegs<Q4>;
 template <bool Q4>
 constexpr bool split_ok = kControlRegs<Q4> >= 24 && kControlRegs<Q4> % 8 == 0 &&
@@ -80,17 +84,16 @@ template <int HD, bool Q4> struct Cfg {
     static constexpr int kK = kQ + 2 * kTileBytes;
     static constexpr int kV = kK + kStages * kTileBytes;
     // tiles of codes and scales (K, V, K, V, ..), codes 1024-byte aligned
-    static constexpr int kSlots = Q4 ? (HD == 128 ? 2 : 4) : 0;
+    static constexpr int kSlots = Q4 ? (HD == 128 ? 2 : 6) : 0;
     static constexpr int kCodes = kN * q4_code_bytes(HD), kScales = kN * q4_scale_bytes(HD);
     static constexpr int kQ4 = kV + kStages * kTileBytes;
     static constexpr int kQ4Scales = kQ4 + kSlots * kCodes;
     // a staging slot per softmax warp for its stores: 32 rows x 128 bytes (1024-byte aligned: a swizzled box), 32 bytes where
-    // the slots of codes leave no more
+    // the slots of codes leave no more (16-byte stores straight from registers cost a unit's end 7 us)
     static constexpr int kStgRow = Q4 && HD == 128 ? 32 : 128;
     static constexpr int kStgSlot = 32 * kStgRow;
-    static constexpr int kStg = kQ4Scales + kSlots * kScales;
+    static constexpr int kStg = (kQ4Scales + kSlots * kScales + 1023) / 1024 * 1024;
     static constexpr int kBar = kStg + kSoftmaxWarps * kStgSlot;
-    static_assert(kStg % 1024 == 0, "boxes of staged rows");
     static constexpr int Q_FULL = 0;
     static constexpr int K_FULL = 1;
     static constexpr int K_EMPTY = K_FULL + kStages;
@@ -109,7 +112,9 @@ template <int HD, bool Q4> struct Cfg {
     static constexpr int P_HALF = TAIL + 2;             // [2]: the first half of a tile's P
     static constexpr int Q4_FULL = P_HALF + 2;          // [kSlots]
     static constexpr int Q4_EMPTY = Q4_FULL + kSlots;   // [kSlots]
-    static constexpr int kNumBars = Q4_EMPTY + kSlots;
+    static constexpr int JOIN_FULL = Q4_EMPTY + kSlots;  // Q4: a split segment's second state is in the scratch; is read
+    static constexpr int JOIN_EMPTY = JOIN_FULL + 1;
+    static constexpr int kNumBars = JOIN_EMPTY + 1;
     static constexpr int kSlot = kBar + (kNumBars * 8 + 15) / 16 * 16;  // tensor memory address, skip flag
     static constexpr int kSeg = kSlot + 16;
     static constexpr int kSmem = kSeg + kSegSlots * (int)sizeof(SegMsg) + 1024;  // + slack for the alignment
@@ -130,6 +135,7 @@ struct ChunkParams {
     CUtensorMap to;  // of the launches with boxes
     const uint8_t *ks, *vs;  // Q4: the scales
     int64_t ks_page, vs_page;
+    float *join;  // Q4: per CTA the state of a tile of rows: o in columns of four ([hd / 4][kM][4]), m, l
 };
 
 // Waits between the roles last a tile or two, those for a segment's place, message or end as long as the segments
@@ -179,6 +185,11 @@ __device__ void walk_role(const ChunkParams &p, const SchedShared &sh, uint8_t *
                     const int all = p.s.causal ? max(0, min(g.kv, g.p0 + a + 1)) : g.kv;
                     m.act[i] = (last + kN - 1) / kN;
                     m.full[i] = all / kN;
+                }
+                if (Q4 && g.ntok <= p.tq_tokens) {
+                    m.split = 1;
+                    m.act[1] = m.act[0];
+                    m.full[1] = m.full[0];
                 }
             }
             ring[n % kSegSlots] = m;
@@ -407,6 +418,10 @@ __device__ void mma_role(const ChunkParams &p, const SchedShared &sh, uint32_t s
     const int my_turn = C::TURN + i, other_turn = C::TURN + (1 - i);
     // the current segment's tiles: kt of [., t1); this issuer's Q tile needs those below act_end
     int kt = 0, t1 = 0, act_end = 0;
+    // a split segment (Q4): this issuer takes every other key tile, and the two go on without turns
+    bool split = false, begun = false;
+    int t0 = 0;  // the segment's first tile
+    auto acts = [&](int t) { return t < act_end && (!split || ((t - t0) & 1) == i); };
     auto s_burst = [&](bool act, uint32_t st) {
         if (act) {
             issue_s<HD, Q4>(el, tS, qdesc, kdesc0 + stage_off(st));
@@ -430,26 +445,29 @@ __device__ void mma_role(const ChunkParams &p, const SchedShared &sh, uint32_t s
             if (!(ok = next_segment<HD, Q4>(p, sh, bar0, nseg, g))) break;
             // (reductions over equal values: the compiler then knows that they are uniform)
             ntok = __reduce_max_sync(0xffffffffu, g.ntok);
-            kt = __reduce_max_sync(0xffffffffu, g.t0);
+            kt = t0 = __reduce_max_sync(0xffffffffu, g.t0);
             t1 = __reduce_max_sync(0xffffffffu, g.t1);
             act_end = __reduce_max_sync(0xffffffffu, i ? g.act[1] : g.act[0]);
+            if (Q4) split = __reduce_max_sync(0xffffffffu, g.split) != 0;
         } while (ntok > 0 && kt >= t1);
         if (!ok || ntok == 0) break;
         if (!(ok = wait(C::Q_FULL, nq & 1u))) break;
         ++nq;
         if (!(ok = wait(C::K_FULL + j % C::kStages, (j / C::kStages) & 1u))) break;
-        if (j == 0 && i == 1 && !(ok = wait(my_turn, (turns++) & 1u))) break;
-        s_burst(kt < act_end, j % C::kStages);
-        if (j == 0) arrive_if(el, BAR(other_turn));
+        const bool first = !begun && !split;
+        begun |= !split;
+        if (first && i == 1 && !(ok = wait(my_turn, (turns++) & 1u))) break;
+        s_burst(acts(kt), j % C::kStages);
+        if (first) arrive_if(el, BAR(other_turn));
         for (;;) {
-            const bool act = kt < act_end, last = kt + 1 >= t1;
+            const bool act = acts(kt), last = kt + 1 >= t1;
             const uint32_t st = j % C::kStages, ph = (j / C::kStages) & 1u;
             const uint32_t stn = (j + 1) % C::kStages, phn = ((j + 1) / C::kStages) & 1u;
             if (last) commit_if(el, BAR(C::Q_EMPTY));  // this issuer's S products of the segment are issued
             if (!(ok = wait(C::V_FULL + st, ph))) break;
             if (!last && !(ok = wait(C::K_FULL + stn, phn))) break;
             if (act && !started && no > 0 && !(ok = wait(C::O_EMPTY + i, (no - 1) & 1u))) break;
-            if (!(ok = wait(my_turn, (turns++) & 1u))) break;
+            if (!split && !(ok = wait(my_turn, (turns++) & 1u))) break;
             if (act) {
                 if (!(ok = wait(C::P_HALF + i, pc & 1u))) break;
                 tc::fence_after_sync();
@@ -464,8 +482,8 @@ __device__ void mma_role(const ChunkParams &p, const SchedShared &sh, uint32_t s
             ++j;
             ++kt;
             if (last) break;
-            s_burst(kt < act_end, stn);
-            arrive_if(el, BAR(other_turn));
+            s_burst(acts(kt), stn);
+            if (!split) arrive_if(el, BAR(other_turn));
         }
         if (!ok) break;
         if (started) {
@@ -473,7 +491,7 @@ __device__ void mma_role(const ChunkParams &p, const SchedShared &sh, uint32_t s
             ++no;
         }
         started = 0;
-        arrive_if(el, BAR(other_turn));
+        if (!split) arrive_if(el, BAR(other_turn));
     }
     if (!ok) arrive_if(el, BAR(other_turn));  // let the other issuer reach its own bounded exit
     commit_if(el, BAR(C::DONE + i));           // every MMA of this issuer ends before tensor memory is freed
@@ -498,14 +516,12 @@ __device__ void producer_q4_role(const ChunkParams &p, const SchedShared &sh, ui
     using C = Cfg<HD, true>;
     const int lane = threadIdx.x & 31;
     auto BAR = [&](int i) { return bar0 + 8u * i; };
-    auto wait = [&](int bar, uint32_t parity) {
-        const bool r = tc::mbar_wait(BAR(bar), parity, p.status, USP_ERR_TIMEOUT, kWaitLimitNs);
-        return (bool)__all_sync(0xffffffffu, r);
-    };
+    auto wait = [&](int bar, uint32_t parity) { return warp_wait(BAR(bar), parity, p.status); };
     const int ps = 1 << p.log_ps, mask = ps - 1, piece = min(ps, kN), pieces = kN / piece;
     constexpr int kCopyKeys = 16 / q4_scale_bytes(HD), kLineKeys = 128 / q4_code_bytes(HD);
     const int skey = lane * kCopyKeys;
     const bool loads = lane < pieces, copies = lane < C::kScales / 16;
+    const uint32_t codes0 = sbase + C::kQ4 + lane * piece * q4_code_bytes(HD), scales0 = sbase + C::kQ4Scales + lane * 16;
     uint32_t fills = 0, nq = 0, nseg = 0;
     bool ok = true;
     SegMsg g;
@@ -514,7 +530,7 @@ __device__ void producer_q4_role(const ChunkParams &p, const SchedShared &sh, ui
         auto q_boxes = [&](auto &&f) {
             for (int i = 0; i < 2; ++i)
                 for (int bx = 0; bx < C::kBoxes; ++bx)
-                    f(C::kQ + i * C::kTileBytes + bx * C::kBoxBytes, bx * 64, (int32_t)(g.tok0 + i * p.tq_tokens));
+                    f(C::kQ + i * C::kTileBytes + bx * C::kBoxBytes, bx * 64, (int32_t)(g.tok0 + (g.split ? 0 : i) * p.tq_tokens));
         };
         auto load_q = [&]() {
             if (lane != 0) return;
@@ -526,46 +542,43 @@ __device__ void producer_q4_role(const ChunkParams &p, const SchedShared &sh, ui
         if (nq == 0) load_q();
         else if (lane == 0) q_boxes([&](int, int c, int32_t tok) { tma_prefetch_3d(&p.tq, c, g.head * p.s.G, tok); });
         ++nq;
+        // The next tile's page numbers are read a tile ahead and looked at only when that tile's slot is free: this warp alone
+        // feeds the SM, and a wait for them in every tile (800 cycles) would show. -1: behind the request's keys.
         const int32_t *row = p.table + (int64_t)g.req * p.table_stride;
-        // page of the tile's key `in`; num_pages (a box of zeros) behind the request's keys
-        auto page_of = [&](int t, int in) {
-            const int64_t key = (int64_t)t * kN + in;
-            if (key >= g.kv) return p.num_pages;
-            const int32_t x = row[key >> p.log_ps];
-            return x >= 0 && x < p.num_pages ? x : p.num_pages;
+        auto page_of = [&](int t, int in, bool on) {
+            const int key = t * kN + in;
+            return on && key < g.kv ? row[key >> p.log_ps] : -1;
         };
-        int32_t page = loads ? page_of(g.t0, lane * piece) : 0, spage = copies ? page_of(g.t0, skey) : 0;
+        const int row0 = g.head * ps;
+        int32_t raw = page_of(g.t0, lane * piece, loads), sraw = page_of(g.t0, skey, copies);
         for (int t = g.t0; t < g.t1; ++t) {
-            const bool more = t + 1 < g.t1;
-            const int32_t next = loads && more ? page_of(t + 1, lane * piece) : 0;
-            const int32_t snext = copies && more ? page_of(t + 1, skey) : 0;
-            const int row0 = g.head * ps, tile0 = (int)(((int64_t)t * kN) & mask);
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                const uint32_t slot = fills % C::kSlots;
-                if (!(ok = wait(C::Q4_EMPTY + slot, ((fills / C::kSlots) & 1u) ^ 1u))) break;
-                if (lane == 0) tc::mbar_arrive_expect_tx(BAR(C::Q4_FULL + slot), C::kCodes);
+            uint32_t slot = fills % C::kSlots;
+            if (!(ok = wait(C::Q4_EMPTY + slot, ((fills / C::kSlots) & 1u) ^ 1u))) break;
+            if (lane == 0) tc::mbar_arrive_expect_tx(BAR(C::Q4_FULL + slot), C::kCodes);
+            // a page outside the cache: a box of zeros, and page 0's scales
+            const int32_t page = (uint32_t)raw < (uint32_t)p.num_pages ? raw : p.num_pages;
+            const int64_t spage = (uint32_t)sraw < (uint32_t)p.num_pages ? sraw : 0;
+            const int line = (row0 + ((t * kN + lane * piece) & mask)) / kLineKeys;
+            const int in = (row0 + ((t * kN + skey) & mask)) * q4_scale_bytes(HD);
+            const uint8_t *ks = p.ks + spage * p.ks_page + in, *vs = p.vs + spage * p.vs_page + in;
+            auto load = [&](const CUtensorMap *map, const uint8_t *scales) {
                 __syncwarp();
-                if (loads)
-                    tma_load_3d(sbase + C::kQ4 + slot * C::kCodes + lane * piece * q4_code_bytes(HD), v ? &p.tv : &p.tk, 0,
-                                (row0 + ((tile0 + lane * piece) & mask)) / kLineKeys, page, BAR(C::Q4_FULL + slot));
-                if (copies) {
-                    // (the scales of a page outside the cache are page 0's: its codes are zeros)
-                    const int64_t pg = spage < p.num_pages ? spage : 0;
-                    const int64_t at = (int64_t)(row0 + ((tile0 + skey) & mask)) * q4_scale_bytes(HD);
-                    copy16(sbase + C::kQ4Scales + slot * C::kScales + lane * 16,
-                           (v ? p.vs + pg * p.vs_page : p.ks + pg * p.ks_page) + at);
-                }
+                if (loads) tma_load_3d(codes0 + slot * C::kCodes, map, 0, line, page, BAR(C::Q4_FULL + slot));
+                if (copies) copy16(scales0 + slot * C::kScales, scales);
                 copies_arrive(BAR(C::Q4_FULL + slot));
                 ++fills;
-                if (v == 0 && t == g.t0 && nq > 1) {
-                    if (!(ok = wait(C::Q_EMPTY, (nq - 2) & 1u))) break;
-                    load_q();
-                }
+            };
+            load(&p.tk, ks);
+            raw = page_of(t + 1, lane * piece, loads);
+            sraw = page_of(t + 1, skey, copies);
+            if (t == g.t0 && nq > 1) {
+                if (!(ok = wait(C::Q_EMPTY, (nq - 2) & 1u))) break;
+                load_q();
             }
-            if (!ok) break;
-            page = next;
-            spage = snext;
+            slot = fills % C::kSlots;
+            if (!(ok = wait(C::Q4_EMPTY + slot, ((fills / C::kSlots) & 1u) ^ 1u))) break;
+            if (lane == 0) tc::mbar_arrive_expect_tx(BAR(C::Q4_FULL + slot), C::kCodes);
+            load(&p.tv, vs);
         }
     }
     if (!ok) {
@@ -601,6 +614,17 @@ __device__ void convert_role(const ChunkParams &p, const SchedShared &sh, uint32
             uint32_t sb;
             if constexpr (HD == 128) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(sb) : "r"(scales + r * 4) : "memory");
             else asm volatile("ld.shared.u16 %0, [%1];" : "=r"(sb) : "r"(scales + r * 2) : "memory");
+            // The slot goes back at once, so that all slots are loads in flight; but only when its words are here: an arrive does
+            // not wait for loads. The store before it does, for its predicate, which is a word of each load (the word it
+            // may write is nobody's).
+            uint32_t all = sb;
+#pragma unroll
+            for (int c = 0; c < HD / 32; ++c) all ^= w[c].x;
+            asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.u32 p, %0, 0x9e3779b9;\n\t@p st.shared.b32 [%1], %0;\n\t}" ::"r"(all),
+                         "r"(sbase + C::kSlot + 8)
+                         : "memory");
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(BAR(C::Q4_EMPTY + slot));
             if (!(ok = wait((v ? C::V_EMPTY : C::K_EMPTY) + st, ((tile / C::kStages) & 1u) ^ 1u))) break;
             const uint32_t to = sbase + (v ? C::kV : C::kK) + st * C::kTileBytes + r * 128;
 #pragma unroll
@@ -617,20 +641,16 @@ __device__ void convert_role(const ChunkParams &p, const SchedShared &sh, uint32
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            // (what was stored depends on all that was loaded: the slot's words have arrived)
-            if (lane == 0) {
-                tc::mbar_arrive(BAR((v ? C::V_FULL : C::K_FULL) + st));
-                tc::mbar_arrive(BAR(C::Q4_EMPTY + slot));
-            }
+            if (lane == 0) tc::mbar_arrive(BAR((v ? C::V_FULL : C::K_FULL) + st));
         }
     }
 }
 
-// One segment of the softmax of Q tile i; ns (S tiles) and no (O read-outs) run on across segments. False after
+// One segment of the softmax of Q tile i; ns (S tiles), no (O read-outs) and nj (joined states) run on across segments. False after
 // a failed wait (the whole warp leaves; the others' waits end by the recorded status).
 template <int HD, bool Q4, bool kBox>  // kBox: whole warps of rows of out are stored as boxes
 __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegMsg &g, uint8_t *smem, uint32_t bar0,
-                                                uint32_t tmem, int i, uint32_t &ns, uint32_t &no) {
+                                                uint32_t tmem, int i, uint32_t &ns, uint32_t &no, uint32_t &nj) {
     using C = Cfg<HD, Q4>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wq = warp & 3;
     const int row = wq * 32 + lane;
@@ -639,7 +659,9 @@ __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegM
     const uint32_t tO = tmem + lane_off + 256u + (uint32_t)(HD * i);
     uint32_t rt, rh;
     p.s.by_G.divmod((uint32_t)row, rt, rh);
-    const int tok = i * p.tq_tokens + (int)rt;  // token of the segment's block
+    const bool split = Q4 && g.split != 0;
+    const int tile = split ? 0 : i;                // of the unit's rows
+    const int tok = tile * p.tq_tokens + (int)rt;  // token of the segment's block
     const bool row_ok = row < p.tq_tokens * p.s.G && tok < g.ntok;
     const int lim = p.s.causal ? max(0, min(g.kv, g.p0 + min(tok, g.ntok - 1) + 1)) : g.kv;
     const float sl2 = p.scale_log2;
@@ -647,7 +669,7 @@ __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegM
     float m = -INFINITY, l = 0.f;
     bool any = false, ok = true;
     const int act_end = min(g.t1, i ? g.act[1] : g.act[0]), full_end = i ? g.full[1] : g.full[0];
-    for (int kt = g.t0; kt < act_end; ++kt) {
+    for (int kt = split ? g.t0 + i : g.t0; kt < act_end; kt += split ? 2 : 1) {
         const bool full = kt < full_end;
         ok = tc::mbar_wait(bar0 + 8u * (C::S_FULL + i), ns & 1u, p.status, USP_ERR_TIMEOUT, kWaitLimitNs);
         ok = __all_sync(0xffffffffu, ok);
@@ -743,11 +765,64 @@ __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegM
     if (!ok) return false;
     // ---- end of the segment -----------------------------------------------------------------------
     const bool whole = g.t0 == 0 && g.t1 == g.tiles;
-    const int r = i * p.tq_tokens * p.s.G + row;  // row of the unit
+    const int r = tile * p.tq_tokens * p.s.G + row;  // row of the unit
     float *slot = part_slot(p.w, HD, blockIdx.x, g.t0 == 0 ? 1 : 0);
     const int head = g.head * p.s.G + (int)rh;
     __nv_bfloat16 *orow = p.out + (g.tok0 + tok) * p.out_stride + (int64_t)head * HD;
+    // A split segment: the second tile's state to the scratch, column by column of four, so that a warp's lanes, a row each,
+    // write and read whole lines; the first tile's threads scale both to the common maximum.
+    float mine_by = 1.f, other_by = 0.f;
+    const float *join = nullptr;
+    if constexpr (Q4) {
+        if (split && g.t0 + 1 < min(g.t1, g.act[1])) {  // (then the first tile of rows has a key tile too)
+            float *at = p.join + (size_t)blockIdx.x * (kM * (HD + 2)), *stats = at + kM * HD;
+            if (i == 1) {
+                ok = tc::mbar_wait(bar0 + 8u * (C::O_FULL + 1), no & 1u, p.status, USP_ERR_TIMEOUT, kWaitLimitNs) &&
+                     (nj == 0 || tc::mbar_wait(bar0 + 8u * C::JOIN_EMPTY, (nj - 1) & 1u, p.status, USP_ERR_TIMEOUT, kWaitLimitNs));
+                if (!__all_sync(0xffffffffu, ok)) return false;
+                ++no;
+                tc::fence_after_sync();
+#pragma unroll 1
+                for (int c = 0; c < HD / 32; ++c) {
+                    uint32_t o[32];
+                    tc::tmem_ld32(tO + c * 32, o);
+                    tc::tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        *reinterpret_cast<uint4 *>(at + ((c * 8 + e) * kM + row) * 4) =
+                            make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                }
+                stats[row] = m;
+                stats[kM + row] = l;
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    tc::mbar_arrive(bar0 + 8u * (C::O_EMPTY + 1));
+                    tc::mbar_arrive(bar0 + 8u * C::JOIN_FULL);
+                }
+                ++nj;
+                return true;
+            }
+            ok = tc::mbar_wait(bar0 + 8u * C::JOIN_FULL, nj & 1u, p.status, USP_ERR_TIMEOUT, kWaitLimitNs);
+            if (!__all_sync(0xffffffffu, ok)) return false;
+            ++nj;
+            const float m1 = stats[row], l1 = stats[kM + row], both = fmaxf(m, m1), base = both == -INFINITY ? 0.f : both;
+            mine_by = tc::ex2(m - base);
+            other_by = tc::ex2(m1 - base);
+            l = l * mine_by + l1 * other_by;
+            m = both;
+            join = at;
+        } else if (split && i == 1) {
+            return true;
+        }
+    }
     const float inv = l == 0.f ? 0.f : 1.f / l;
+    auto released = [&]() {  // the scratch is read
+        if (Q4 && join) {
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(bar0 + 8u * C::JOIN_EMPTY);
+        }
+    };
     if (any) {
         ok = tc::mbar_wait(bar0 + 8u * (C::O_FULL + i), no & 1u, p.status, USP_ERR_TIMEOUT, kWaitLimitNs);
         ok = __all_sync(0xffffffffu, ok);
@@ -789,6 +864,18 @@ __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegM
             tc::tmem_ld32(tO + c * 64, o[0]);
             tc::tmem_ld32(tO + c * 64 + 32, o[1]);
             tc::tmem_ld_wait();
+            if (Q4 && join) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float4 x = *reinterpret_cast<const float4 *>(join + ((c * 16 + e) * kM + row) * 4);
+                    const float y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int f = 0; f < 4; ++f) {
+                        uint32_t &w = o[e / 8][e % 8 * 4 + f];
+                        w = __float_as_uint(fmaf(y[f], other_by, u2f(w) * mine_by));
+                    }
+                }
+            }
             if (whole) {
                 if (c > 0 && box) {
                     if (lane == 0) tma_stores_read();
@@ -826,6 +913,7 @@ __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegM
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar0 + 8u * (C::O_EMPTY + i));
+        released();
     } else if (row_ok && whole) {
         for (int e = 0; e < HD; e += 8) *reinterpret_cast<uint4 *>(orow + e) = make_uint4(0, 0, 0, 0);
     }
@@ -874,6 +962,8 @@ __global__ void __launch_bounds__(kThreads<Q4>, 1) paged_chunk_kernel(const __gr
             tc::mbar_init(bar0 + 8u * (C::Q4_FULL + i), 33);  // the boxes' bytes, and each lane's copies
             tc::mbar_init(bar0 + 8u * (C::Q4_EMPTY + i), 4);
         }
+        tc::mbar_init(bar0 + 8u * C::JOIN_FULL, 4);
+        tc::mbar_init(bar0 + 8u * C::JOIN_EMPTY, 4);
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(bar0 + 8u * (C::S_FULL + i), 1);
             tc::mbar_init(bar0 + 8u * (C::P_FULL + i), 4);
@@ -920,10 +1010,10 @@ __global__ void __launch_bounds__(kThreads<Q4>, 1) paged_chunk_kernel(const __gr
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs<Q4>));
-        uint32_t ns = 0, no = 0, nseg = 0;
+        uint32_t ns = 0, no = 0, nj = 0, nseg = 0;
         SegMsg g;
         while (!skip && next_segment<HD, Q4>(p, sh, bar0, nseg, g) && g.ntok > 0)
-            if (!softmax_segment<HD, Q4, kBox>(p, g, smem, bar0, tmem, warp >> 2, ns, no)) break;
+            if (!softmax_segment<HD, Q4, kBox>(p, g, smem, bar0, tmem, warp >> 2, ns, no, nj)) break;
         if (kBox && (threadIdx.x & 31) == 0) tma_stores_done();
     }
     if (skip && threadIdx.x == 0) p.w.head[blockIdx.x] = no_part(sh);
@@ -1013,7 +1103,9 @@ int launch_paged_chunk(const PagedArgs &a, int n_lo, const PartSpace &w, cudaStr
     return a.hd == 128 ? launch_typed<128, false, false>(p, w.ctas, s) : launch_typed<64, false, false>(p, w.ctas, s);
 }
 
-int launch_paged_q4_chunk(const PagedQ4Args &a, int n_lo, const PartSpace &w, cudaStream_t s) {
+size_t q4_join_bytes(int ctas, int hd) { return (size_t)ctas * kM * (hd + 2) * 4; }
+
+int launch_paged_q4_chunk(const PagedQ4Args &a, int n_lo, const PartSpace &w, float *join, cudaStream_t s) {
     const DeviceInfo *di = device_info();
     if (!di) return USP_ERR_CUDA;
     ChunkParams p{};
@@ -1032,6 +1124,7 @@ int launch_paged_q4_chunk(const PagedQ4Args &a, int n_lo, const PartSpace &w, cu
         !make_codes_tmap(&p.tv, a.v, a.num_pages, a.v_page, a.hkv, ps, a.hd, box))
         return USP_ERR_CUDA;
     p.ks = a.ks; p.vs = a.vs; p.ks_page = a.ks_page; p.vs_page = a.vs_page;
+    p.join = join;
     p.s.cu = a.cu; p.s.kv = a.kv;
     p.s.tokens = a.tokens; p.s.max_keys = q4_max_keys(a);
     p.s.nreq = a.nreq; p.s.hkv = a.hkv; p.s.G = a.G;

@@ -92,7 +92,7 @@ Route route(const usp_paged_q4_desc &d, int sms) {
 }
 
 size_t workspace_bytes_of(const Route &r, int hd) {
-    return (r.few_ctas ? part_bytes(r.few_ctas, r.few_rows, hd) : 0) + (r.many_ctas ? part_bytes(r.many_ctas, kChunkRows, hd) : 0);
+    return (r.few_ctas ? part_bytes(r.few_ctas, r.few_rows, hd) : 0) + (r.many_ctas ? part_bytes(r.many_ctas, kChunkRows, hd) + q4_join_bytes(r.many_ctas, hd) : 0);
 }
 
 // What the caller provides: what every call with this max_new or a smaller one uses. The layouts of few rows alone are
@@ -162,7 +162,9 @@ int usp_paged_attn_q4(const void *q, const void *k_cache, const void *v_cache, c
     c.G = G; c.hq = a.hq; c.by_G = FastDiv((uint32_t)G);
     if (r.many_ctas) {
         c.w[0] = part_space(at, r.many_ctas, kChunkRows, a.hd);
-        rc = launch_paged_q4_chunk(a, r.alone ? 0 : r.split, c.w[0], s);
+        float *join = reinterpret_cast<float *>(at);
+        at += q4_join_bytes(r.many_ctas, a.hd);
+        rc = launch_paged_q4_chunk(a, r.alone ? 0 : r.split, c.w[0], join, s);
         if (rc) return rc;
     }
     if (r.few_ctas && !r.alone) {

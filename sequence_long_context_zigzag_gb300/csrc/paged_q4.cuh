@@ -88,7 +88,9 @@ struct Q4Nibbles {
 int launch_paged_q4_few(const PagedQ4Args &a, int G, int rows, int n_hi, bool second, const PartSpace &w, cudaStream_t s);
 int q4_few_ctas(int sms, int rows, int dtype);
 
-// bf16, units of up to kChunkRows query rows, one CTA per SM; requests with more than n_lo new tokens (paged_chunk.cu)
-int launch_paged_q4_chunk(const PagedQ4Args &a, int n_lo, const PartSpace &w, cudaStream_t s);
+// bf16, units of up to kChunkRows query rows, one CTA per SM; requests with more than n_lo new tokens (paged_chunk.cu). join:
+// a scratch of q4_join_bytes.
+int launch_paged_q4_chunk(const PagedQ4Args &a, int n_lo, const PartSpace &w, float *join, cudaStream_t s);
+size_t q4_join_bytes(int ctas, int hd);
 
 }  // namespace usp

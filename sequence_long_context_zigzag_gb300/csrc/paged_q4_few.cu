@@ -157,8 +157,7 @@ __device__ void producer(const FewParams &p, const SchedShared &sh, uint8_t *sme
     const int lane = threadIdx.x & 31;
     auto BAR = [&](int i) { return sbase + C::kBar + 8u * i; };
     auto wait = [&](int bar, uint32_t parity) {
-        const bool r = tc::mbar_wait(BAR(bar), parity, p.status, USP_ERR_TIMEOUT, kWaitLimitNs);
-        return (bool)__all_sync(0xffffffffu, r);
+        return __all_sync(0xffffffffu, tc::mbar_try_wait(BAR(bar), parity)) || wait_longer(BAR(bar), parity, p.status);
     };
     SegMsg *ring = reinterpret_cast<SegMsg *>(smem + C::kSeg);
     const int ps = 1 << p.log_ps, piece = min(ps, C::kKT), pieces = C::kKT / piece;  // at most 16 pieces
@@ -191,37 +190,35 @@ __device__ void producer(const FewParams &p, const SchedShared &sh, uint8_t *sme
         if (!more) break;
         const int32_t *row = p.table + (int64_t)g.req * p.table_stride;
         const int kv_head = (int)p.by_sub.div((uint32_t)g.head);
-        // page of the tile's key `in`; num_pages (a box of zeros) behind the request's keys
-        auto page_of = [&](int t, int in) {
-            const int64_t key = (int64_t)t * C::kKT + in;
-            if (key >= g.kv) return p.num_pages;
-            const int32_t x = row[key >> p.log_ps];
-            return x >= 0 && x < p.num_pages ? x : p.num_pages;
+        // The next tile's page numbers are read a tile ahead and looked at only when that tile's stage is free. -1: behind the
+        // request's keys.
+        auto page_of = [&](int t, int in, bool on) {
+            const int key = t * C::kKT + in;
+            return on && key < g.kv ? row[key >> p.log_ps] : -1;
         };
-        int32_t page = loads ? page_of(g.t0, pc * piece) : 0, spage = copies ? page_of(g.t0, skey) : 0;
+        const int mask = ps - 1, row0 = kv_head * ps;
+        int32_t raw = page_of(g.t0, pc * piece, loads), sraw = page_of(g.t0, skey, copies);
         for (int t = g.t0; t < g.t1; ++t) {
-            const bool more_tiles = t + 1 < g.t1;
-            const int32_t next = loads && more_tiles ? page_of(t + 1, pc * piece) : 0;
-            const int32_t snext = copies && more_tiles ? page_of(t + 1, skey) : 0;
             const uint32_t st = fill % C::kStages;
             if (!(ok = wait(C::EMPTY + st, ((fill / C::kStages) & 1u) ^ 1u))) break;
             if (lane == 0) tc::mbar_arrive_expect_tx(BAR(C::FULL + st), 2 * C::kCodes);
             __syncwarp();
-            const int mask = ps - 1, row0 = kv_head * ps, tile0 = (int)(((int64_t)t * C::kKT) & mask);
+            // a page outside the cache: a box of zeros, and page 0's scales
+            const int32_t page = (uint32_t)raw < (uint32_t)p.num_pages ? raw : p.num_pages;
+            const int64_t spage = (uint32_t)sraw < (uint32_t)p.num_pages ? sraw : 0;
             if (loads)
-                tma_load_3d(dst0 + st * 2 * C::kCodes, v ? &p.tv : &p.tk, 0, (row0 + ((tile0 + pc * piece) & mask)) / (128 / C::kRow), page,
-                            BAR(C::FULL + st));
+                tma_load_3d(dst0 + st * 2 * C::kCodes, v ? &p.tv : &p.tk, 0,
+                            (row0 + ((t * C::kKT + pc * piece) & mask)) / (128 / C::kRow), page, BAR(C::FULL + st));
             if (copies) {
-                // (the scales of a page outside the cache are page 0's: its codes are zeros)
-                const int64_t pg = spage < p.num_pages ? spage : 0, at = (int64_t)(row0 + ((tile0 + skey) & mask)) * C::kSRow;
+                const int at = (row0 + ((t * C::kKT + skey) & mask)) * C::kSRow;
                 const uint32_t dst = sbase + C::kSc + st * 2 * C::kScales + lane * 16;
-                copy16(dst, p.ks + pg * p.ks_page + at);
-                copy16(dst + C::kScales, p.vs + pg * p.vs_page + at);
+                copy16(dst, p.ks + spage * p.ks_page + at);
+                copy16(dst + C::kScales, p.vs + spage * p.vs_page + at);
             }
             copies_arrive(BAR(C::FULL + st));
+            raw = page_of(t + 1, pc * piece, loads);
+            sraw = page_of(t + 1, skey, copies);
             ++fill;
-            page = next;
-            spage = snext;
         }
         if (!ok) break;
         if (g.t0 == 0 && g.t1 < g.tiles) opened = part_header(p.s, sh, sc, g);
