@@ -380,7 +380,10 @@ PyObject *rope(PyObject *const *a) {
     Output qo = out(a[7], "q_out", q, call.d.q_out_stride), ko;
     if (k.defined()) ko = out(a[8], "k_out", k, call.d.k_out_stride);
     if (const int rc = call.run(q, k, qo.t, ko.t)) return PyLong_FromLong(rc);
-    if (!k.defined()) ko.given = Py_None;
+    if (!k.defined()) {
+        need(a[8] == Py_None, "k_out without k");
+        ko.given = Py_None;
+    }
     return tuple({&qo, &ko});
 }
 
@@ -407,14 +410,19 @@ struct RopeFunction : torch::autograd::Function<RopeFunction> {
         ctx->saved_data["inverse"] = inverse;
         return k.defined() ? torch::autograd::variable_list{qo, ko} : torch::autograd::variable_list{qo};
     }
+    // a gradient as the rotation takes it; it may come expanded, or as part of another tensor at any address
+    static Tensor dense(const Tensor &g) {
+        const Tensor c = g.contiguous();
+        return reinterpret_cast<uintptr_t>(c.const_data_ptr()) % 16 == 0 ? c : c.clone();
+    }
     static torch::autograd::variable_list backward(torch::autograd::AutogradContext *ctx, torch::autograd::variable_list g) {
         const auto saved = ctx->get_saved_variables();
         const bool has_k = g.size() > 1;
         try {
             const bool has_pos = ctx->saved_data["positions"].toBool();
-            const Optional k = has_k ? Optional(g[1].contiguous()) : std::nullopt, pos = has_pos ? Optional(saved[1]) : std::nullopt,
+            const Optional k = has_k ? Optional(dense(g[1])) : std::nullopt, pos = has_pos ? Optional(saved[1]) : std::nullopt,
                            cu = saved.size() > 1u + has_pos ? Optional(saved.back()) : std::nullopt;
-            auto d = apply(g[0].contiguous(), k, saved[0], pos, cu, ctx->saved_data["interleaved"].toBool(),
+            auto d = apply(dense(g[0]), k, saved[0], pos, cu, ctx->saved_data["interleaved"].toBool(),
                            !ctx->saved_data["inverse"].toBool());
             return {d[0], has_k ? d[1] : Tensor(), Tensor(), Tensor(), Tensor(), Tensor(), Tensor()};
         } catch (const Refused &r) {

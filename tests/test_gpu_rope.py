@@ -117,6 +117,22 @@ def test_rope_second_gradient():
     assert all(torch.equal(a, b) for a, b in zip(second, want))
 
 
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_rope_gradients_that_lie_anywhere(dt):
+    """Gradients that come expanded, and as parts of a tensor that start at no 16-byte boundary."""
+    table = usp.usp_rope_table(9, 64)
+    q, k = (torch.randn(2, 9, h, 64, device="cuda").to(dt).requires_grad_() for h in (3, 1))
+    yq, yk = usp.UspRopeFunction.apply(q, k, table)
+    one = torch.ones_like
+    want = usp.usp_rope(one(q), one(k), table, inverse=True)
+    got = torch.autograd.grad(yq.sum() + yk.sum(), (q, k), retain_graph=True)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    up = torch.randn(1 + q.numel() + k.numel(), device="cuda").to(dt)
+    got = torch.autograd.grad(torch.cat([up.new_zeros(1), yq.flatten(), yk.flatten()]), (q, k), up)
+    want = usp.usp_rope(up[1:q.numel() + 1].clone().view_as(q), up[q.numel() + 1:].clone().view_as(k), table, inverse=True)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_rope_gradients_in_a_graph():
     """Forward and backward through the op, captured and replayed on other values; strided leaves."""
     table = usp.usp_rope_table(24, 128)
@@ -314,6 +330,8 @@ def test_binding_refuses():
     for args in ((q, k, t[:7]), (q, k, usp.usp_rope_table(8, 24)), (q, k, usp.usp_rope_table(8, 128))):
         with pytest.raises(usp.UspError):
             usp.usp_rope(*args)
+    with pytest.raises(ValueError):
+        usp.usp_rope(q, None, t, k_out=torch.empty_like(k))
     kc = torch.zeros(4, 2, 16, 64, device="cuda")
     slots, cu, kv = i32([0] * 8), i32([0, 8]), i32([8])
     q, k = q[0], k[0]
