@@ -188,6 +188,21 @@ def test_a_very_large_or_small_query(dt):
         check_attention(c, out, lse, scale=0.125 / f)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("hq,hkv,hd,ps", [(8, 2, 128, 64), (8, 1, 64, 16), (5, 1, 128, 128), (40, 1, 64, 32)])
+@pytest.mark.parametrize("reqs", [
+    [(30000, 9)], [(26000, 12), (200, 6), (15, 12), (129, 5), (0, 5), (128, 11), (1, 7), (31000, 10)],
+    [(500 + 130 * i, 5 + i) for i in range(12)], [(6, 12), (300, 12), (2, 9)]], ids=["one", "mixed", "twelve", "few keys"])
+def test_units_of_one_tile_of_rows(reqs, hq, hkv, hd, ps, causal):
+    """More rows than the kernel for few takes, and no more than a tile: the key tiles go to two states, which are joined;
+    odd numbers of tiles, one tile, none, units cut between CTAs; rows without a key in either."""
+    c = Q4Cache(reqs, hq, hkv, hd, ps, torch.bfloat16, seed=80, wide=True)
+    out, lse = attend(c, max_new=c.max_new, causal=causal)
+    check_attention(c, out, lse, causal)
+    again = attend(c, max_new=c.max_new, causal=causal)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
 def test_same_bits_on_every_run(dt):
     c = Q4Cache([(5000, 1), (3000, 300), (40, 40), (2500, 1)], 8, 2, 128, 16, dt, seed=6)
