@@ -9,10 +9,13 @@
 // What bounds it: HBM for long sequences (each element is read and written once for 3 operations), latency for a decode
 // step. A row (one head of one token) has hd / 16 threads, 16 elements each: 8 of either half of its pairs. A thread stays
 // with its token, whose cosines and sines it holds, and walks the heads of q, K and V, the next row's loads in flight; the
-// threads of a token side by side read a few KB in a row.
+// threads of a token side by side read a few KB in a row. Measured: 32768 tokens of 40 heads of 128 rotated 107 us, 0.95 of the
+// copy rate; 48 heads of 46000 tokens rotated and appended 169 us, 1.01. What goes to a 4-bit cache has its own rows
+// (quant_rows). A call of 64 tokens takes 3.7 us, quantising 5.1: launch and latency.
 #include <string.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "paged.cuh"
 #include "q4.cuh"
@@ -24,7 +27,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kSearch = 1024;  // entries of cu that a CTA searches in shared memory
 
-enum RopeMode { ROPE_PLAIN = 0, ROPE_CACHE = 1, ROPE_Q4 = 2 };
+enum RopeMode { ROPE_PLAIN, ROPE_CACHE, ROPE_Q4 };  // whole sequences; into the pages; q of an append to a 4-bit cache
 
 struct RopeArgs {
     const char *q, *k, *v;
@@ -38,7 +41,8 @@ struct RopeArgs {
     uint32_t tokens, nslots;
     int32_t nreq;                                                // entries of kv, or packed samples
     int32_t hq, hkv, heads;                                      // heads: of q, K and V together
-    int32_t log_side;                                            // rows of a token side by side: 1 << log_side
+    int32_t log_side, log_side_kv;                               // rows of a token side by side: 1 << log_side; in quant_rows
+    uint32_t kv_blocks;                                          // CTAs of quant_rows
     int32_t rot, log_ps;
     bool interleaved, inverse, quads;                            // quads: see group_max
     FastDiv by_L;
@@ -155,20 +159,54 @@ template <typename T> struct Raw8 {
 
 // rows of a thread whose loads are in flight at once, at three CTAs per SM
 template <typename T> constexpr int rope_batch(int mode) {
-    const int n = mode == ROPE_PLAIN ? 4 : mode == ROPE_CACHE ? 3 : 2;
+    const int n = mode == ROPE_CACHE ? 3 : 4;
     return sizeof(T) == 2 ? n : (n + 1) / 2;
 }
 
-template <typename T, int HD, int kMode> __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeArgs p) {
+struct Places {
+    int32_t part[kSearch], pos[kThreads / 4], slot[kThreads / 4];  // (4: the fewest lanes of a row)
+};
+// The positions (-1: none) and slots of a CTA's ntok tokens from t0 on; all of its threads call it.
+template <int kMode> __device__ __forceinline__ void find_places(const RopeArgs &p, uint32_t t0, uint32_t ntok, Places &sh) {
+    const bool search = p.rot > 0 && !p.positions && p.cu && p.nreq > 0;
+    const int step = (p.nreq + kSearch - 1) / kSearch;
+    if (search) {
+        for (int i = threadIdx.x; (int64_t)i * step < p.nreq; i += kThreads) sh.part[i] = p.cu[i * step];
+        __syncthreads();
+    }
+    if (threadIdx.x < ntok) {
+        const uint32_t u = t0 + threadIdx.x;
+        const uint32_t slot = kMode != ROPE_PLAIN ? (uint32_t)p.slots[u] : 0;
+        int64_t pos = -1;
+        if (p.rot > 0) {
+            if (p.positions) {
+                pos = p.positions[u];
+            } else if constexpr (kMode == ROPE_PLAIN) {
+                uint32_t s, l;
+                p.by_L.divmod(u, s, l);
+                pos = l;
+                if (search && sh.part[0] <= (int)l) pos = (int64_t)l - p.cu[find_sample(p.cu, p.nreq, sh.part, step, l)];
+            } else if (search && sh.part[0] <= (int)u) {
+                const int r = find_sample(p.cu, p.nreq, sh.part, step, u);
+                const int64_t end = p.cu[r + 1];  // a token behind the last request has no position
+                if (u < end) pos = (int64_t)p.kv[r] - end + u;
+            }
+            if (pos >= p.max_pos) pos = -1;
+        }
+        sh.pos[threadIdx.x] = (int32_t)max(pos, (int64_t)-1);
+        if (kMode != ROPE_PLAIN) sh.slot[threadIdx.x] = slot < p.nslots && (p.rot == 0 || pos >= 0) ? (int32_t)slot : -1;
+    }
+    __syncthreads();
+}
+
+// Rows rotated and copied: the CTA's share of the tokens, q (and K and V, except for ROPE_Q4) of each; all threads call it.
+template <typename T, int HD, int kMode> __device__ __forceinline__ void rope_rows(const RopeArgs &p, uint32_t block, Places &sh) {
     constexpr int kLanes = HD / 16, kRows = kThreads / kLanes;  // lanes of a row; rows side by side in a CTA
-    constexpr int kRowBytes = HD * (int)sizeof(T), kStored = kMode == ROPE_Q4 ? q4_code_bytes(HD) : kRowBytes;
+    constexpr int kRowBytes = HD * (int)sizeof(T);
     constexpr int kBatch = rope_batch<T>(kMode);
-    __shared__ int32_t part[kSearch];
-    __shared__ int32_t pos_s[kRows], slot_s[kRows];
-    wait_grid_before();
     // ---- this thread's token, and its part of the token's rows ----
     const int side = 1 << p.log_side;
-    const uint32_t t0 = blockIdx.x * (kRows >> p.log_side), ntok = min((uint32_t)(kRows >> p.log_side), p.tokens - t0);
+    const uint32_t t0 = block * (kRows >> p.log_side), ntok = min((uint32_t)(kRows >> p.log_side), p.tokens - t0);
     const int c = threadIdx.x % kLanes, row = threadIdx.x / kLanes, h0 = row & (side - 1);
     const uint32_t tl = (uint32_t)row >> p.log_side, t = t0 + tl;
     const bool live = tl < ntok;
@@ -180,7 +218,7 @@ template <typename T, int HD, int kMode> __global__ void __launch_bounds__(kThre
     };
     auto row_of = [&](int h) {
         Row r;
-        r.q = h < p.hq;
+        r.q = kMode == ROPE_Q4 || h < p.hq;
         r.k = !r.q && h < p.hq + p.hkv;
         r.head = r.q ? h : r.k ? h - p.hq : h - p.hq - p.hkv;
         r.ok = live && h < p.heads;
@@ -203,37 +241,8 @@ template <typename T, int HD, int kMode> __global__ void __launch_bounds__(kThre
         }
     };
     fetch(0);
-    // ---- positions (-1: none) and slots of the CTA's tokens, under the first loads ----
-    const bool search = p.rot > 0 && !p.positions && p.cu && p.nreq > 0;
-    const int step = (p.nreq + kSearch - 1) / kSearch;
-    if (search) {
-        for (int i = threadIdx.x; (int64_t)i * step < p.nreq; i += kThreads) part[i] = p.cu[i * step];
-        __syncthreads();
-    }
-    if (threadIdx.x < ntok) {
-        const uint32_t u = t0 + threadIdx.x;
-        const uint32_t slot = kMode != ROPE_PLAIN ? (uint32_t)p.slots[u] : 0;
-        int64_t pos = -1;
-        if (p.rot > 0) {
-            if (p.positions) {
-                pos = p.positions[u];
-            } else if constexpr (kMode == ROPE_PLAIN) {
-                uint32_t s, l;
-                p.by_L.divmod(u, s, l);
-                pos = l;
-                if (search && part[0] <= (int)l) pos = (int64_t)l - p.cu[find_sample(p.cu, p.nreq, part, step, l)];
-            } else if (search && part[0] <= (int)u) {
-                const int r = find_sample(p.cu, p.nreq, part, step, u);
-                const int64_t end = p.cu[r + 1];  // a token behind the last request has no position
-                if (u < end) pos = (int64_t)p.kv[r] - end + u;
-            }
-            if (pos >= p.max_pos) pos = -1;
-        }
-        pos_s[threadIdx.x] = (int32_t)max(pos, (int64_t)-1);
-        if (kMode != ROPE_PLAIN) slot_s[threadIdx.x] = slot < p.nslots && (p.rot == 0 || pos >= 0) ? (int32_t)slot : -1;
-    }
-    __syncthreads();
-    const int32_t pos = live ? pos_s[tl] : -1, slot = live && kMode != ROPE_PLAIN ? slot_s[tl] : -1;
+    find_places<kMode>(p, t0, ntok, sh);  // under the first loads
+    const int32_t pos = live ? sh.pos[tl] : -1, slot = live && kMode != ROPE_PLAIN ? sh.slot[tl] : -1;
     const bool angles = 16 * c < p.rot && pos >= 0;
     float cs[8], sn[8];
     if (angles) {
@@ -246,20 +255,15 @@ template <typename T, int HD, int kMode> __global__ void __launch_bounds__(kThre
     }
     // ---- rows: head h's is h rows (of the page: h << log_ps rows) from the token's first ----
     char *q_out = p.q_out + t * p.qo_stride, *k_out, *v_out = nullptr;
-    uint8_t *k_sc = nullptr, *v_sc = nullptr;
     int k_step = kRowBytes;
     if constexpr (kMode == ROPE_PLAIN) {
         k_out = p.k_out + t * p.ko_stride;
     } else {
         const int64_t page = slot >> p.log_ps;
         const int in_page = slot & ((1 << p.log_ps) - 1);
-        k_out = p.k_out + page * p.k_page + in_page * kStored;
-        v_out = p.v_out + page * p.v_page + in_page * kStored;
-        k_step = kStored << p.log_ps;
-        if constexpr (kMode == ROPE_Q4) {
-            k_sc = p.k_scales + page * p.ks_page + in_page * q4_scale_bytes(HD);
-            v_sc = p.v_scales + page * p.vs_page + in_page * q4_scale_bytes(HD);
-        }
+        k_out = p.k_out + page * p.k_page + in_page * kRowBytes;
+        v_out = p.v_out + page * p.v_page + in_page * kRowBytes;
+        k_step = kRowBytes << p.log_ps;
     }
     for (int first = 0;;) {
 #pragma unroll
@@ -268,11 +272,9 @@ template <typename T, int HD, int kMode> __global__ void __launch_bounds__(kThre
             const Row r = row_of(first + i * side + h0);
             const bool turned = (r.q || r.k) && angles, ok = r.ok && (kMode == ROPE_PLAIN || (r.q ? pos >= 0 : slot >= 0));
             float x[8], y[8];
-            if (turned || kMode == ROPE_Q4) {
+            if (turned) {
                 a[i].values(x);
                 b[i].values(y);
-            }
-            if (turned) {
                 if (p.interleaved) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -284,38 +286,7 @@ template <typename T, int HD, int kMode> __global__ void __launch_bounds__(kThre
                     for (int e = 0; e < 8; ++e) turn(x[e], y[e], cs[e], sn[e]);
                 }
             }
-            if constexpr (kMode == ROPE_Q4) {
-                const int split = r.k ? R : 0;
-                float ma = max8(x), mb = max8(y), ga, gb;
-                if (__any_sync(0xffffffffu, ma != ma || mb != mb)) {  // NaN is stored as 0
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        x[e] = x[e] == x[e] || r.q ? x[e] : 0.f;
-                        y[e] = y[e] == y[e] || r.q ? y[e] : 0.f;
-                    }
-                    ma = max8(x);
-                    mb = max8(y);
-                }
-                group_max<kLanes>(ma, mb, c, split, R == 0, p.quads, ga, gb);
-                if (ok && !r.q) {
-                    const Q4Scale sa(ga), sb = R == 0 ? sa : Q4Scale(gb);
-                    uint32_t wa, wb;
-                    if (sizeof(T) == 2 && !(r.k && p.rot > 0)) {
-                        wa = q4_pack<true>(x, sa);
-                        wb = q4_pack<true>(y, sb);
-                    } else {
-                        wa = q4_pack<false>(x, sa);
-                        wb = q4_pack<false>(y, sb);
-                    }
-                    char *to = (r.k ? k_out : v_out) + (int64_t)r.head * k_step;
-                    *reinterpret_cast<uint32_t *>(to + r.d0 / 2) = wa;
-                    *reinterpret_cast<uint32_t *>(to + r.d1 / 2) = wb;
-                    uint8_t *sc = (r.k ? k_sc : v_sc) + ((int64_t)r.head << p.log_ps) * q4_scale_bytes(HD);
-                    if (r.d0 % kQ4Group == 0) sc[r.d0 / kQ4Group] = (uint8_t)sa.b;
-                    if (r.d1 % kQ4Group == 0) sc[r.d1 / kQ4Group] = (uint8_t)sb.b;
-                }
-            }
-            if (ok && (kMode != ROPE_Q4 || r.q)) {
+            if (ok) {
                 if (turned) {
                     a[i].set(x);
                     b[i].set(y);
@@ -331,24 +302,175 @@ template <typename T, int HD, int kMode> __global__ void __launch_bounds__(kThre
     }
 }
 
+// K and V rows quantised. A thread has 16 elements of the K and of the V row of a head at a time, the next head's loads under
+// the arithmetic. Without a rotation it is about 100 operations a row and thread, which leave the kernel 0.94 of the copy
+// rate (73000 tokens of 8 heads of 128 59 us; with 32 heads of q, rotated, 265 us, 0.90). One walk over q's, K's and V's
+// rows alike, as rope_rows does it, took three times the operations (120 and 351 us).
+enum Turn { TURN_NONE, TURN_NEIGHBOURS, TURN_HALVES };  // how K is rotated on the way
+
+template <typename T> struct QuantRow {
+    Raw8<T> a, b;
+    __device__ __forceinline__ void load(const char *p, int d0, int d1) {
+        a.load(p + d0 * sizeof(T));
+        b.load(p + d1 * sizeof(T));
+    }
+};
+
+template <typename T, int HD, int kTurn> __device__ __forceinline__ void quant_rows(const RopeArgs &p, uint32_t block, Places &sh) {
+    constexpr int kLanes = HD / 16, kRows = kThreads / kLanes, kRowBytes = HD * (int)sizeof(T);
+    constexpr int kCode = q4_code_bytes(HD), kScale = q4_scale_bytes(HD);
+    const int side = 1 << p.log_side_kv;
+    const uint32_t t0 = block * (kRows >> p.log_side_kv), ntok = min((uint32_t)(kRows >> p.log_side_kv), p.tokens - t0);
+    const int c = threadIdx.x % kLanes, row = threadIdx.x / kLanes, h0 = row & (side - 1);
+    const uint32_t tl = (uint32_t)row >> p.log_side_kv, t = t0 + tl;
+    const bool live = tl < ntok;
+    const int R = kTurn == TURN_HALVES ? p.rot / 16 : 0;
+    const bool halves = c < R;
+    const int d0 = halves ? 8 * c : 16 * c, d1 = halves ? p.rot / 2 + 8 * c : 16 * c + 8;
+    const char *k = p.k + t * p.k_stride + h0 * kRowBytes, *v = p.v + t * p.v_stride + h0 * kRowBytes;
+    QuantRow<T> kr, vr;
+    if (live && h0 < p.hkv) {
+        kr.load(k, d0, d1);
+        vr.load(v, 16 * c, 16 * c + 8);
+    }
+    int32_t pos = -1, slot = -1;
+    if constexpr (kTurn == TURN_NONE) {
+        if (live && (uint32_t)p.slots[t] < p.nslots) slot = p.slots[t];
+    } else {
+        find_places<ROPE_Q4>(p, t0, ntok, sh);
+        if (live) pos = sh.pos[tl], slot = sh.slot[tl];
+    }
+    float cs[8], sn[8];
+    const bool angles = kTurn != TURN_NONE && 16 * c < p.rot && pos >= 0;
+    if (angles) {
+        const char *at = reinterpret_cast<const char *>(p.table + (int64_t)pos * p.rot + 8 * c);
+        load8(at, cs);
+        load8(at + p.rot * 2, sn);
+    }
+    const int64_t page = slot >> p.log_ps;
+    const int at = (h0 << p.log_ps) + (slot & ((1 << p.log_ps) - 1));  // the row in its page
+    char *ko = p.k_out + page * p.k_page + (int64_t)at * kCode, *vo = p.v_out + page * p.v_page + (int64_t)at * kCode;
+    uint8_t *ks = p.k_scales + page * p.ks_page + (int64_t)at * kScale, *vs = p.v_scales + page * p.vs_page + (int64_t)at * kScale;
+    // x, y: the lane's runs at e0 and e1 of a row
+    auto store = [&](auto turned, float (&x)[8], float (&y)[8], char *to, uint8_t *sc, bool ok, int e0, int e1) {
+        constexpr bool kHalves = decltype(turned)::value && kTurn == TURN_HALVES;
+        constexpr bool kExact = sizeof(T) == 2 && !(decltype(turned)::value && kTurn != TURN_NONE);
+        float ma = max8(x), mb = max8(y), ga, gb;
+        if (__any_sync(0xffffffffu, ma != ma || mb != mb)) {  // NaN is stored as 0
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                x[e] = x[e] == x[e] ? x[e] : 0.f;
+                y[e] = y[e] == y[e] ? y[e] : 0.f;
+            }
+            ma = max8(x);
+            mb = max8(y);
+        }
+        group_max<kLanes>(ma, mb, c, R, !kHalves, p.quads, ga, gb);
+        if (!ok) return;
+        const Q4Scale sa(ga), sb = kHalves ? Q4Scale(gb) : sa;
+        const uint32_t wa = q4_pack<kExact>(x, sa), wb = q4_pack<kExact>(y, sb);
+        if (kHalves) {
+            *reinterpret_cast<uint32_t *>(to + e0 / 2) = wa;
+            *reinterpret_cast<uint32_t *>(to + e1 / 2) = wb;
+            if (e0 % kQ4Group == 0) sc[e0 / kQ4Group] = (uint8_t)sa.b;
+            if (e1 % kQ4Group == 0) sc[e1 / kQ4Group] = (uint8_t)sb.b;
+        } else {
+            *reinterpret_cast<uint2 *>(to + 8 * c) = make_uint2(wa, wb);
+            if (c % 2 == 0) sc[c / 2] = (uint8_t)sa.b;
+        }
+    };
+    for (int first = 0;;) {
+        const bool ok = slot >= 0 && first + h0 < p.hkv;
+        float x[8], y[8];
+        kr.a.values(x);
+        kr.b.values(y);
+        if (angles) {
+            if (kTurn == TURN_NEIGHBOURS) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    turn(x[2 * e], x[2 * e + 1], cs[e], sn[e]);
+                    turn(y[2 * e], y[2 * e + 1], cs[4 + e], sn[4 + e]);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) turn(x[e], y[e], cs[e], sn[e]);
+            }
+        }
+        first += side;
+        const bool more = live && first + h0 < p.hkv;
+        k += side * kRowBytes;
+        v += side * kRowBytes;
+        if (more) kr.load(k, d0, d1);  // the next head's K under this one's
+        store(std::true_type{}, x, y, ko, ks, ok, d0, d1);
+        vr.a.values(x);
+        vr.b.values(y);
+        if (more) vr.load(v, 16 * c, 16 * c + 8);
+        store(std::false_type{}, x, y, vo, vs, ok, 16 * c, 16 * c + 8);
+        if (first >= p.hkv) break;
+        ko += (int64_t)(side * kCode) << p.log_ps;
+        vo += (int64_t)(side * kCode) << p.log_ps;
+        ks += (int64_t)(side * kScale) << p.log_ps;
+        vs += (int64_t)(side * kScale) << p.log_ps;
+    }
+}
+
+template <typename T, int HD, int kMode> __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeArgs p) {
+    __shared__ Places sh;
+    wait_grid_before();
+    rope_rows<T, HD, kMode>(p, blockIdx.x, sh);
+}
+
+// CTAs per SM: as many as their registers allow without a spill, nearly (a fourth costs the rotating kinds 20 to 30%)
+template <typename T> constexpr int quant_ctas(int turn) { return turn == TURN_NONE && sizeof(T) == 2 ? 4 : 3; }
+
+// K and V, and q's rows (the last blocks)
+template <typename T, int HD, int kTurn> __global__ void __launch_bounds__(kThreads, quant_ctas<T>(kTurn)) quant_kernel(const RopeArgs p) {
+    __shared__ Places sh;
+    wait_grid_before();
+    if (blockIdx.x < p.kv_blocks) quant_rows<T, HD, kTurn>(p, blockIdx.x, sh);
+    else if constexpr (kTurn != TURN_NONE) rope_rows<T, HD, ROPE_Q4>(p, blockIdx.x - p.kv_blocks, sh);
+}
+
+// Rows of a token side by side: all, as far as a CTA has place, where there are few; in large calls 1 << large.
+int side_by_side(int64_t tokens, int heads, int rows, int large, int sms) {
+    const int most = tokens * heads < (int64_t)rows * 8 * sms ? 30 : large;
+    int log_side = 0;
+    while (log_side < most && (1 << log_side) < heads && (2 << log_side) <= rows) ++log_side;
+    return log_side;
+}
+uint32_t blocks_of(uint32_t tokens, int rows, int log_side) {
+    const uint32_t per_cta = (uint32_t)rows >> log_side;
+    return (tokens + per_cta - 1) / per_cta;
+}
+
 template <int kMode> int launch_rope(RopeArgs a, int hd, int dtype, cudaStream_t s) {
     const DeviceInfo *di = device_info();
     if (!di) return USP_ERR_CUDA;
-    a.quads = a.interleaved || a.rot % 64 == 0;
-    // Rows of a token side by side: all, as far as a CTA has place, where there are few; in large calls eight, or four where
-    // the rows go to pages (40 heads of 128 of 32768 tokens: 2, 4, 8, 16, 32 of them 126, 114, 107, 119, 174 us; 48 heads of 46000
-    // into a cache 172, 169, 176, 211, 307).
+    // In large calls eight, or four where the rows go to pages (40 heads of 128 of 32768 tokens: 2, 4, 8, 16, 32 of them 126,
+    // 114, 107, 119, 174 us; 48 heads of 46000 into a cache 172, 169, 176, 211, 307).
     const int rows = kThreads / (hd / 16);
-    int log_side = 0;
-    const int most = (int64_t)a.tokens * a.heads < (int64_t)rows * 8 * di->sm_count ? 30 : kMode == ROPE_PLAIN ? 3 : 2;
-    while (log_side < most && (1 << log_side) < a.heads && (2 << log_side) <= rows) ++log_side;
-    a.log_side = log_side;
-    const uint32_t per_cta = (uint32_t)rows >> log_side;
-    const dim3 grid((a.tokens + per_cta - 1) / per_cta);
+    a.log_side = side_by_side(a.tokens, a.heads, rows, kMode == ROPE_PLAIN ? 3 : 2, di->sm_count);
+    const dim3 grid(blocks_of(a.tokens, rows, a.log_side));
     auto go = [&](auto kernel) { return launch_overlapped(kernel, grid, kThreads, 0, s, a); };
     if (dtype == USP_BF16)
         return hd == 128 ? go(rope_kernel<__nv_bfloat16, 128, kMode>) : go(rope_kernel<__nv_bfloat16, 64, kMode>);
     return hd == 128 ? go(rope_kernel<float, 128, kMode>) : go(rope_kernel<float, 64, kMode>);
+}
+
+template <typename T, int HD> int launch_quant(RopeArgs a, cudaStream_t s) {
+    const DeviceInfo *di = device_info();
+    if (!di) return USP_ERR_CUDA;
+    const int rows = kThreads / (HD / 16);
+    a.quads = a.rot % 64 == 0;
+    a.heads = a.hq;  // (of rope_rows)
+    a.log_side = side_by_side(a.tokens, a.hq, rows, 3, di->sm_count);
+    // (73000 tokens, 8 heads: 1, 2, 4, 8 of them side by side 66.1, 65.2, 65.7, 69.0 us; rotated, with 32 of q, 278, 283, 294, 317)
+    a.log_side_kv = side_by_side(a.tokens, a.hkv, rows, a.rot == 0 ? 1 : 0, di->sm_count);
+    a.kv_blocks = blocks_of(a.tokens, rows, a.log_side_kv);
+    const dim3 grid(a.kv_blocks + (a.hq > 0 ? blocks_of(a.tokens, rows, a.log_side) : 0));
+    auto go = [&](auto kernel) { return launch_overlapped(kernel, grid, kThreads, 0, s, a); };
+    return a.rot == 0 ? go(quant_kernel<T, HD, TURN_NONE>)
+           : a.interleaved ? go(quant_kernel<T, HD, TURN_NEIGHBOURS>) : go(quant_kernel<T, HD, TURN_HALVES>);
 }
 
 int log2_of(int64_t x) {
@@ -530,7 +652,9 @@ int usp_rope_append_q4(const void *q, void *q_out, const void *k, const void *v,
     a.v_page = c.v_page_stride ? c.v_page_stride : rows * q4_code_bytes(c.hd);
     a.ks_page = c.k_scale_stride ? c.k_scale_stride : rows * q4_scale_bytes(c.hd);
     a.vs_page = c.v_scale_stride ? c.v_scale_stride : rows * q4_scale_bytes(c.hd);
-    return launch_rope<ROPE_Q4>(a, c.hd, d.dtype, reinterpret_cast<cudaStream_t>(stream));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (d.dtype == USP_BF16) return c.hd == 128 ? launch_quant<__nv_bfloat16, 128>(a, st) : launch_quant<__nv_bfloat16, 64>(a, st);
+    return c.hd == 128 ? launch_quant<float, 128>(a, st) : launch_quant<float, 64>(a, st);
 }
 
 int usp_cache_append_q4(const void *k, const void *v, void *k_cache, void *v_cache, uint8_t *k_scales, uint8_t *v_scales,
