@@ -4,7 +4,7 @@ Each .cu file compiles to an object in parallel (``-gencode arch=compute_103a,co
 the objects link into one shared library with the CUDA runtime linked statically, so the library has
 no load-time dependency on libcudart or libcuda (driver entry points are fetched at run time).
 
-Beside them the C++ binding of the paged cache's calls (csrc/binding.cpp), a CPython module against the
+Beside them the C++ binding of the paged cache's and the rotation's calls (csrc/binding.cpp), a CPython module against the
 installed torch, compiles with g++ (a few seconds; its file name carries the torch and Python versions and a
 hash of its sources). The library does not depend on it: where it cannot be built (no torch, no Python
 headers, no g++), build() warns, and the first call that needs the binding raises.

@@ -13,13 +13,21 @@
 // it, the conversion: about 1.5 instructions a value beside some 0.6 of products, loads and softmax, where an SM issues
 // 128 lanes a clock. Layout of the work:
 //  - spans of equal key counts per CTA (paged_sched.cuh); a producer warp walks the span and streams K, V (TMA boxes) and
-//    their scales (bulk copies) of 128 keys a tile through a ring of stages; four consumer warps, each with 32 keys of
-//    the tile and a softmax state of its own, which merge through shared memory at a unit's end;
+//    their scales (16-byte asynchronous copies) of 128 keys a tile (256 of hd 64) through a ring of stages; four consumer
+//    warps, each with a quarter of the tile and a softmax state of its own, which merge through shared memory at a unit's
+//    end;
 //  - S^T comes out of the product with a key per lane group and rows along lanes; two 8x8 transposes (movmatrix) make
 //    the weights the operand of the second product;
 //  - lane (g, t) converts for K the 32 values of group t of keys g and g + 8, and for V the 16 columns from 16 g on of four
 //    keys: loads of 16 and 8 bytes, a scale byte each. Which key is row k of a product is free: key_of makes both loads
 //    meet all banks.
+// Measured (8 KV heads of 128, 4 query heads each, pages of 64): 64 requests of 11000 keys 157 us, 0.72 of the copy rate; with
+// pages of 16 tokens 176, hd 64 90 (0.63), two requests of 230000 keys 107 (0.69); up to 16 rows 230 us. Loading alone runs
+// at 0.95 to 1.05 of the copy rate. Per 16 keys a warp issues 306 instructions; 16 operands of four shifts, four logic
+// operations, four bf16x2 multiply-adds and a product take 22 to 24 cycles each of a scheduler, as the logic pipe takes one
+// instruction in two cycles and the multiply-adds do not quite hide under them: 486 cycles, where HBM would take 372. More
+// warps do not change that (7 consumers in each of 2 CTAs 164 us, 15 in one 177), nor do shifts as products on the other
+// pipe. Up to four requests of 1000 keys take 10 us a call, start-up of two kernels and the chain over a tile.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -33,7 +41,9 @@
 namespace usp {
 namespace {
 
-constexpr int kOver = 512;     // a unit's constant cost, in keys
+// a unit's constant cost, in keys (64 requests of 2000 to 32768 keys with 128, 256, 512, 1024: 155, 154, 156, 161 us; 26 single
+// tokens beside chunks 27.4, 25.5, 25.1, 25.1)
+constexpr int kOver = 256;
 constexpr int kWarps = 4;      // consumers
 constexpr int kThreads = (kWarps + 1) * 32;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
@@ -46,7 +56,9 @@ template <int HD, int NT, bool F32> struct Cfg {
     static constexpr int kCtas = NT == 1 && !F32 ? 3 : 2; // per SM
     static constexpr int kW = HD == 64 && NT == 1 && !F32 ? 4 : 2;  // 16-key steps per warp and tile
     static constexpr int kKT = 16 * kW * kWarps;          // keys per tile
-    static constexpr int kMinSpan = kKT + 64;             // keys per CTA below which fewer CTAs work
+    // keys per CTA below which fewer CTAs work (one request of 8000 keys with kKT + 1, 64, 128, 320: 17.6, 13.7, 12.3, 12.4 us; four
+    // of 2000 11.4, 11.2, 11.7, 11.7)
+    static constexpr int kMinSpan = kKT + 128;
     static_assert(kMinSpan > kKT, "a span holds more than a tile");
     static constexpr int kRow = q4_code_bytes(HD), kSRow = q4_scale_bytes(HD);
     static constexpr int kCodes = kKT * kRow, kScales = kKT * kSRow;
