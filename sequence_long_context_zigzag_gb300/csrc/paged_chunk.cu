@@ -36,12 +36,12 @@
 //   Where a unit's rows fit one Q tile, reading is four times as fast as over a bf16 cache, and one chain of products,
 // softmax, products per key tile would bound the kernel: such a segment is split, both Q tiles being the same rows, each
 // for every other key tile. At its end the second one's state goes through a scratch in the workspace to the first one's
-// threads, which join the two (32 requests of 8000 keys, 20 rows: 178 us, split 150).
+// threads, which join the two (32 requests of 8000 keys, 20 rows by this kernel: 178 us, split 150).
 //   Measured (8 KV heads of 128, 4 query heads each): 1000 tokens over 48000 keys 495 to 525 us (1510 to 1600 TFLOP/s; over a bf16
-// cache 437), a prompt of 16384 tokens 1437 to 1450 (1182 to 1266); 32 requests of 8000 keys with 5, 16, 64 tokens each 150,
+// cache 437), a prompt of 16384 tokens 1437 to 1450 (1182 to 1266); 32 requests of 8000 keys with 9, 16, 64 tokens each 153,
 // 155, 199 us. The converting warps take a tenth of a long chunk. Below a tile of rows both the chain of a tile and
-// the conversion, which waits for its own loads and stores, take about as long (without any conversion 142 us, 121 with
-// five slots of codes instead of two).
+// the conversion, which waits for its own loads and stores, take about as long (20 rows without any conversion 142 us, 121
+// with five slots of codes instead of two).
 #include <cuda_bf16.h>
 
 #include <algorithm>

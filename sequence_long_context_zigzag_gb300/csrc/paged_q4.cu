@@ -53,8 +53,8 @@ PagedQ4Args paged_q4_args(const usp_paged_q4_desc &d) {
 
 // The heads of a unit: the KV head's G, or where these are more than the kernel for few rows takes, the largest divisor of
 // G that it does.
-int few_heads(int G) {
-    int h = std::min(G, 16);
+int few_heads(int G, int most) {
+    int h = std::min(G, most);
     while (G % h != 0) --h;
     return h;
 }
@@ -68,17 +68,21 @@ struct Route {
 };
 Route route(const usp_paged_q4_desc &d, int sms) {
     Route r{};
-    const int G = d.hq / d.cache.hkv, most = 16;
+    // bf16: the kernel for few rows against the one for many, 32 requests of 8000 keys, 20, 24, 32 rows 118, 119, 145 us against
+    // 150, 150, 150; 16 requests of 2000 28, 29, 35 against 39, 39, 40; 36 rows would take two units
+    const int G = d.hq / d.cache.hkv, most = d.dtype == USP_BF16 ? 32 : 16;
     const int64_t rows = G * (int64_t)std::max(1, d.max_new);
-    r.few_G = few_heads(G);
+    r.few_G = few_heads(G, most);
     r.split = INT_MAX;
     if (d.dtype == USP_BF16 && (rows > most || G > most)) {
         r.many_ctas = sms;
-        // beside chunks, the few-row requests are mostly single tokens: the kernel of 8 rows takes those where it can
-        r.split = G > most ? 0 : (G > 8 ? most : 8) / G;
+        // beside chunks, the few-row requests are mostly single tokens: the kernel of 8 rows takes those where it can, else that of
+        // as few tiles of rows as a token's heads need
+        r.split = G > most ? 0 : G > 16 ? 1 : (G > 8 ? 16 : 8) / G;
     }
     if (r.split > 0) {
-        r.few_rows = r.few_G * std::min<int64_t>(std::max(1, d.max_new), r.split) <= 8 ? 8 : 16;
+        // (a multiple of 8; a request of more rows than the host knows of has several units)
+        r.few_rows = (int)std::min<int64_t>(most, (r.few_G * std::min<int64_t>(std::max(1, d.max_new), r.split) + 7) / 8 * 8);
         r.few_ctas = q4_few_ctas(sms, r.few_rows, d.dtype);
     }
     if (r.many_ctas && r.few_ctas) {
@@ -101,7 +105,8 @@ size_t workspace_bytes_for(const usp_paged_q4_desc &d, int sms) {
     const Route r = route(d, sms);
     size_t most = workspace_bytes_of(r, d.cache.hd);
     if (r.few_ctas)
-        for (int rows : {8, 16}) most = std::max(most, part_bytes(q4_few_ctas(sms, rows, d.dtype), rows, d.cache.hd));
+        for (int rows = 8; rows <= (d.dtype == USP_BF16 ? 32 : 16); rows += 8)
+            most = std::max(most, part_bytes(q4_few_ctas(sms, rows, d.dtype), rows, d.cache.hd));
     return most;
 }
 

@@ -83,7 +83,7 @@ struct Q4Nibbles {
     }
 };
 
-// Units of up to `rows` (8 or 16) query rows, G query heads each (a divisor of the group's); requests with at most n_hi new
+// Units of up to `rows` (a multiple of 8, at most 32; fp32: 16) query rows, G query heads each (a divisor of the group's); requests with at most n_hi new
 // tokens. `second`: the call's other kernel is in the stream before it.
 int launch_paged_q4_few(const PagedQ4Args &a, int G, int rows, int n_hi, bool second, const PartSpace &w, cudaStream_t s);
 int q4_few_ctas(int sms, int rows, int dtype);

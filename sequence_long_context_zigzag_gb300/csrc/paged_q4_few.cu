@@ -1,5 +1,5 @@
 // paged_q4_few.cu -- attention of few query rows per KV head over the 4-bit paged cache (sm_103a): single tokens and short
-// chunks, up to 16 query rows (tokens x G heads) per unit; fp32 queries at any length.
+// chunks, up to 32 query rows (tokens x G heads; fp32: 16) per unit; fp32 queries at any length.
 //
 // Mathematics: as paged_decode.cu (online softmax over key tiles, lazy rescale, weights rounded to bf16 for the product
 // with V; fp32 queries and weights enter as three bf16 terms each, x = x0 + x1 + x2 to 24 bits). The products run
@@ -22,8 +22,8 @@
 //    keys: loads of 16 and 8 bytes, a scale byte each. Which key is row k of a product is free: key_of makes both loads
 //    meet all banks.
 // Measured (8 KV heads of 128, 4 query heads each, pages of 64): 64 requests of 11000 keys 157 us, 0.72 of the copy rate; with
-// pages of 16 tokens 176, hd 64 90 (0.63), two requests of 230000 keys 107 (0.69); up to 16 rows 230 us. Loading alone runs
-// at 0.95 to 1.05 of the copy rate. Per 16 keys a warp issues 306 instructions; 16 operands of four shifts, four logic
+// pages of 16 tokens 176, hd 64 90 (0.63), two requests of 230000 keys 107 (0.69); 16 rows 215, 32 rows 351. Loading alone
+// runs at 0.95 to 1.05 of the copy rate. Per 16 keys a warp issues 306 instructions; 16 operands of four shifts, four logic
 // operations, four bf16x2 multiply-adds and a product take 22 to 24 cycles each of a scheduler, as the logic pipe takes one
 // instruction in two cycles and the multiply-adds do not quite hide under them: 486 cycles, where HBM would take 372. More
 // warps do not change that (7 consumers in each of 2 CTAs 164 us, 15 in one 177), nor do shifts as products on the other
@@ -53,7 +53,8 @@ constexpr float kLn2 = 0.69314718055994531f;
 // NT: tiles of 8 query rows; F32: q, out and the weights in three bf16 terms
 template <int HD, int NT, bool F32> struct Cfg {
     static constexpr int kTerms = F32 ? 3 : 1;
-    static constexpr int kCtas = NT == 1 && !F32 ? 3 : 2; // per SM
+    static constexpr bool kWide = NT > 1 && !F32;         // see consumer_wide
+    static constexpr int kCtas = F32 ? 2 : 3;             // per SM
     static constexpr int kW = HD == 64 && NT == 1 && !F32 ? 4 : 2;  // 16-key steps per warp and tile
     static constexpr int kKT = 16 * kW * kWarps;          // keys per tile
     // keys per CTA below which fewer CTAs work (one request of 8000 keys with kKT + 1, 64, 128, 320: 17.6, 13.7, 12.3, 12.4 us; four
@@ -62,13 +63,14 @@ template <int HD, int NT, bool F32> struct Cfg {
     static_assert(kMinSpan > kKT, "a span holds more than a tile");
     static constexpr int kRow = q4_code_bytes(HD), kSRow = q4_scale_bytes(HD);
     static constexpr int kCodes = kKT * kRow, kScales = kKT * kSRow;
-    static constexpr int kStages = (kCtas == 3 || F32 ? 3 : 4) * (kKT * HD == 128 * 128 ? 1 : 2);
+    static constexpr int kStages = 3 * (kKT * HD == 128 * 128 ? 1 : 2);
     static constexpr int kXRow = HD + 4;                  // exchange row in floats
     static constexpr int kSc = kStages * 2 * kCodes;      // scales, behind all stages' codes (K, V each)
     static constexpr int kX = kSc + kStages * 2 * kScales;  // [warp][row][kXRow]
-    static constexpr int kML = kX + kWarps * NT * 8 * kXRow * 4;
+    static constexpr int kML = kX + (kWide ? 0 : kWarps * NT * 8 * kXRow * 4);
     static constexpr int kQ = kML + kWarps * NT * 8 * 8;  // q's terms as operands: [term][step][row tile][lane]
-    static constexpr int kSeg = kQ + (F32 ? kTerms * (HD / 16) * NT * 256 : 0);
+    static constexpr int kP = kQ + (F32 || kWide ? kTerms * (HD / 16) * NT * 256 : 0);  // kWide: P: [step][row tile][lane]
+    static constexpr int kSeg = kP + (kWide ? kKT / 16 * NT * 256 : 0);
     static constexpr int kBar = kSeg + kSegSlots * (int)sizeof(SegMsg);
     static constexpr int FULL = 0, EMPTY = kStages, SEG_FULL = 2 * kStages, SEG_EMPTY = SEG_FULL + kSegSlots;
     static constexpr int kSmem = kBar + (SEG_EMPTY + kSegSlots) * 8 + 1024;  // + slack for the alignment
@@ -118,6 +120,9 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 x;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(a) : "memory");
     return x;
+}
+__device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
 }
 __device__ __forceinline__ uint32_t lds8(uint32_t a) {
     uint32_t x;
@@ -595,6 +600,290 @@ template <int HD, int NT, bool F32> __device__ void consumer(const FewParams &p,
     }
 }
 
+// Units of 9 to 32 rows (bf16). A warp takes a quarter of the tile's keys for S^T, as above, but a quarter of the head's
+// columns, over all of the tile's keys, for O^T: so it holds O of 32 rows in the registers of one row tile, no value of the cache
+// is converted twice, and there is one softmax state: the weights go through shared memory. Two barriers a tile: where a
+// maximum has to move (one for all warps), and before the weights are read. Measured: 32 requests of 8000 keys, 16, 24, 32 rows 90, 119,
+// 145 us (with the division above 16 rows take 97 and spill); for 8 rows the barriers cost more than the smaller O
+// gives (64 requests of 11000 keys 173 us, the division above 156).
+template <int HD, int NT> __device__ void consumer_wide(const FewParams &p, uint8_t *smem, uint32_t sbase) {
+    using C = Cfg<HD, NT, false>;
+    constexpr int kMT = HD / 16, kX = HD / 64;  // 16-element steps of the head dim; this warp's 16-column tiles of O^T
+    constexpr int kW = C::kW, kWords = HD / 32;
+    static_assert(kW == 2, "four score pairs a row tile");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    auto BAR = [&](int i) { return sbase + C::kBar + 8u * i; };
+    auto wait = [&](int bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, tc::mbar_try_wait(BAR(bar), parity)) || wait_longer(BAR(bar), parity, p.status);
+    };
+    float *wm = reinterpret_cast<float *>(smem + C::kML), *wl = wm + kWarps * NT * 8;  // [warp][row]: maxima, sums
+    const Q4Nibbles nib;
+    const int kkey = warp * 16 * kW + key_of<HD>(g);
+    const uint32_t k_at = codes_at<HD>(kkey, t * (C::kRow / 4));
+    const uint32_t ks_at = kkey * C::kSRow + (HD == 128 ? t : t >> 1);
+    auto further = [](uint32_t at, int n) { return (at ^ ((n * C::kRow >> 3) & 0x70)) + n * C::kRow; };
+    // V's rows 2 t, 2 t + 1 (and + 8) of a step: the word with this lane's columns. Of the 8 columns of a word it has the even
+    // or the odd ones (hd 64: two of these)
+    uint32_t v_at[2], vs_at[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int key = key_of<HD>(2 * t + e);
+        v_at[e] = C::kCodes + codes_at<HD>(key, warp * (C::kRow / 4) + (HD == 128 ? g >> 1 : g >> 2) * 4);
+        vs_at[e] = C::kScales + key * C::kSRow + (HD == 128 ? warp : warp >> 1);
+    }
+    const uint32_t half = g & 1 ? 0x7632u : 0x5410u;
+    const int v_shift = HD == 128 ? 0 : (g >> 1 & 1) * 8;
+    uint32_t st = 0, st_phase = 0;  // the stage of the next tile, and its fill's parity
+    for (uint32_t nseg = 0;; ++nseg) {
+        bool ok = wait(C::SEG_FULL + nseg % kSegSlots, (nseg / kSegSlots) & 1u);
+        SegMsg s;
+        s.ntok = 0;
+        if (ok) {
+            bool never;
+            s = read_segment(sbase + C::kSeg + nseg % kSegSlots * (uint32_t)sizeof(SegMsg), never);
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(BAR(C::SEG_EMPTY + nseg % kSegSlots) + (never ? 8u : 0u));
+        }
+        const int rows = s.ntok * p.s.G;
+        if (s.ntok > 0) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const int r = n * 8 + g;
+                const __nv_bfloat16 *q = nullptr;
+                if (r < rows) {
+                    uint32_t tok, h;
+                    p.s.by_G.divmod((uint32_t)r, tok, h);
+                    q = static_cast<const __nv_bfloat16 *>(p.q) + (s.tok0 + tok) * p.q_stride +
+                        (int64_t)(s.head * p.s.G + (int)h) * HD + t * (8 * kWords);
+                }
+                for (int k = warp; k < kMT; k += kWarps) {
+                    const uint2 x = q ? *reinterpret_cast<const uint2 *>(q + k * 4) : make_uint2(0u, 0u);
+                    sts64(sbase + C::kQ + ((k * NT + n) * 32 + lane) * 8, x.x, x.y);
+                }
+            }
+        }
+        // The barriers of the tiles need all warps: a failed wait ends the segment for all of them here or at a tile's first
+        ok = consumers_all(ok);
+        float o[NT][kX][4], m[NT][2], l[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int x = 0; x < kX; ++x)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[n][x][e] = 0.f;
+            m[n][0] = m[n][1] = -INFINITY;
+            l[n][0] = l[n][1] = 0.f;
+        }
+        const int lim_all = p.s.causal ? max(0, min(s.kv, s.p0 + 1)) : s.kv;  // keys that every row sees
+        const int t1 = s.ntok > 0 ? s.t1 : s.t0;
+        for (int kt = s.t0; ok && kt < t1; ++kt) {
+            ok = wait(C::FULL + st, st_phase);
+            const uint32_t base = sbase + st * 2 * C::kCodes, sbs = sbase + C::kSc + st * 2 * C::kScales;
+            const int key0 = kt * C::kKT + warp * 16 * kW;
+            // ---- S^T = K Q^T ----
+            float sc[kW][NT][4];
+            uint32_t w[kW][2][kWords], s2[kW][2], off[kW][2];
+#pragma unroll
+            for (int i = 0; i < kW; ++i) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t at = base + further(k_at, i * 16 + e * 8);
+                    if constexpr (HD == 128) {
+                        const uint4 x = lds128(at);
+                        w[i][e][0] = x.x; w[i][e][1] = x.y; w[i][e][2] = x.z; w[i][e][3] = x.w;
+                    } else {
+                        const uint2 x = lds64(at);
+                        w[i][e][0] = x.x; w[i][e][1] = x.y;
+                    }
+                    s2[i][e] = q4_scales2(lds8(sbs + ks_at + (i * 16 + e * 8) * C::kSRow));
+                    off[i][e] = q4_minus136(s2[i][e]);
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[i][n][e] = 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < kMT; ++k) {
+                uint32_t a[kW][4];
+#pragma unroll
+                for (int i = 0; i < kW; ++i)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        a[i][e] = nib.values(w[i][e][k / 2], k % 2 * 2, s2[i][e], off[i][e]);
+                        a[i][2 + e] = nib.values(w[i][e][k / 2], k % 2 * 2 + 1, s2[i][e], off[i][e]);
+                    }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const uint2 b = lds64(sbase + C::kQ + ((k * NT + n) * 32 + lane) * 8);
+#pragma unroll
+                    for (int i = 0; i < kW; ++i) mma16816(sc[i][n], a[i], b.x, b.y);
+                }
+            }
+            // ---- softmax ----
+            bool need = !ok;
+            float mx[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                if (key0 + 16 * kW > lim_all) {
+                    const int key = key0 + key_of<HD>(g);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int tok = (int)p.s.by_G.div((uint32_t)max(0, min(n * 8 + 2 * t + e, rows - 1)));
+                        const int lim = p.s.causal ? max(0, min(s.kv, s.p0 + tok + 1)) : s.kv;
+#pragma unroll
+                        for (int i = 0; i < kW; ++i)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                if (key + i * 16 + h * 8 >= lim) sc[i][n][2 * h + e] = -INFINITY;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    mx[n][e] = fmaxf(tc::max3(sc[0][n][e], sc[0][n][2 + e], sc[1][n][e]), sc[1][n][2 + e]) * p.scale_log2;
+                    need |= mx[n][e] > m[n][e] + kRescale;
+                }
+            }
+            if (!consumers_all(!need)) {  // (the same for all warps)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) mx[n][e] = fmaxf(mx[n][e], __shfl_xor_sync(0xffffffffu, mx[n][e], d));
+                        if (g == 0) wm[(warp * NT + n) * 8 + 2 * t + e] = mx[n][e];
+                    }
+                if (!(ok = consumers_all(ok))) break;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float mn = m[n][e];
+#pragma unroll
+                        for (int x = 0; x < kWarps; ++x) mn = fmaxf(mn, wm[(x * NT + n) * 8 + 2 * t + e]);
+                        const float a = mn == -INFINITY ? 1.f : tc::ex2(m[n][e] - mn);
+                        m[n][e] = mn;
+                        l[n][e] *= a;
+#pragma unroll
+                        for (int x = 0; x < kX; ++x) {
+                            o[n][x][e] *= a;
+                            o[n][x][2 + e] *= a;
+                        }
+                    }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float nmb[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) nmb[e] = m[n][e] == -INFINITY ? 0.f : -m[n][e];
+#pragma unroll
+                for (int i = 0; i < kW; ++i) {
+                    float x[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[e] = tc::ex2(fmaf(sc[i][n][e], p.scale_log2, nmb[e & 1]));
+                    l[n][0] += x[0] + x[2];
+                    l[n][1] += x[1] + x[3];
+                    sts64(sbase + C::kP + (((warp * kW + i) * NT + n) * 32 + lane) * 8, transpose8x8(float2_to_bf16x2(x[0], x[1])),
+                          transpose8x8(float2_to_bf16x2(x[2], x[3])));
+                }
+            }
+            consumers_sync();
+            // ---- O^T += V^T P^T ----
+#pragma unroll
+            for (int i = 0; i < C::kKT / 16; ++i) {
+                uint32_t a[kX][4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t v[2], b[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        v[e] = lds32(base + further(v_at[e], i * 16 + h * 8));
+                        b[e] = lds8(sbs + vs_at[e] + (i * 16 + h * 8) * C::kSRow);
+                    }
+                    const uint32_t v2 = q4_scales2(b[0], b[1]), voff = q4_minus136(v2);
+                    const uint32_t word = __byte_perm(v[0], v[1], half) >> v_shift;
+#pragma unroll
+                    for (int x = 0; x < kX; ++x) {
+                        a[x][2 * h] = nib.values(word, 2 * x, v2, voff);
+                        a[x][2 * h + 1] = nib.values(word, 2 * x + 1, v2, voff);
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const uint2 b = lds64(sbase + C::kP + ((i * NT + n) * 32 + lane) * 8);
+#pragma unroll
+                    for (int x = 0; x < kX; ++x) mma16816(o[n][x], a[x], b.x, b.y);
+                }
+            }
+            // (as above)
+            uint32_t all = 0xffffffffu;
+#pragma unroll
+            for (int x = 0; x < kX; ++x) all &= __float_as_uint(o[0][x][0]);
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(BAR(C::EMPTY + st) + (all == 0x7fa5a5a5u ? 8u : 0u));
+            if (++st == C::kStages) {
+                st = 0;
+                st_phase ^= 1u;
+            }
+        }
+        // ---- the rows' sums, and the rows ----
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], d);
+                if (g == 0) wl[(warp * NT + n) * 8 + 2 * t + e] = l[n][e];
+            }
+        if (!consumers_all(ok) || s.ntok == 0) return;
+        const bool whole = s.t0 == 0 && s.t1 == s.tiles;
+        float *slot = part_slot(p.w, HD, blockIdx.x, s.t0 == 0 ? 1 : 0);
+        // the lane's columns after the exchange of even and odd ones with its neighbour: 2 kX in a row
+        const int col = warp * (HD / 4) + (HD == 128 ? (g >> 1) * 8 + (g & 1) * 4 : (g >> 2) * 8 + (g >> 1 & 1) * 4 + (g & 1) * 2);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = n * 8 + 2 * t + e;
+                float L = 0.f;
+#pragma unroll
+                for (int x = 0; x < kWarps; ++x) L += wl[(x * NT + n) * 8 + 2 * t + e];
+                float v[2 * kX], y[2 * kX];
+#pragma unroll
+                for (int x = 0; x < kX; ++x) v[2 * x] = o[n][x][e], v[2 * x + 1] = o[n][x][2 + e];
+#pragma unroll
+                for (int j = 0; j < kX; ++j) {  // an even lane gives its upper half for the other's lower one
+                    const float got = __shfl_xor_sync(0xffffffffu, g & 1 ? v[j] : v[kX + j], 4);
+                    y[2 * j] = g & 1 ? got : v[j];
+                    y[2 * j + 1] = g & 1 ? v[kX + j] : got;
+                }
+                if (r >= rows) continue;
+                uint32_t tok, h;
+                p.s.by_G.divmod((uint32_t)r, tok, h);
+                const int head = s.head * p.s.G + (int)h;
+                if (whole) {
+                    const float inv = L == 0.f ? 1.f : 1.f / L;
+                    __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(p.out) + (s.tok0 + tok) * p.out_stride + (int64_t)head * HD + col;
+                    uint32_t z[kX];
+#pragma unroll
+                    for (int j = 0; j < kX; ++j) z[j] = float2_to_bf16x2(y[2 * j] * inv, y[2 * j + 1] * inv);
+                    if constexpr (kX == 2) *reinterpret_cast<uint2 *>(to) = make_uint2(z[0], z[1]);
+                    else *reinterpret_cast<uint32_t *>(to) = z[0];
+                    if (warp == 0 && g == 0)
+                        p.lse[(s.tok0 + tok) * p.hq + head] = L == 0.f ? -INFINITY : (m[n][e] + __log2f(L)) * kLn2;
+                } else {
+                    float *to = slot + (size_t)r * HD + col;
+                    if constexpr (kX == 2) *reinterpret_cast<float4 *>(to) = make_float4(y[0], y[1], y[2], y[3]);
+                    else *reinterpret_cast<float2 *>(to) = make_float2(y[0], y[1]);
+                    if (warp == 0 && g == 0) {
+                        slot[(size_t)p.w.rows * HD + r] = m[n][e];
+                        slot[(size_t)p.w.rows * (HD + 1) + r] = L;
+                    }
+                }
+            }
+    }
+}
+
 template <int HD, int NT, bool F32>
 __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, F32>::kCtas)) paged_q4_few_kernel(const __grid_constant__ FewParams p) {
     using C = Cfg<HD, NT, F32>;
@@ -629,7 +918,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, F32>::kCtas)) paged_q4_
     } else if ((threadIdx.x >> 5) == kWarps) {
         producer<HD, NT, F32>(p, sh, smem, sbase);
     } else {
-        consumer<HD, NT, F32>(p, smem, sbase);
+        if constexpr (C::kWide) consumer_wide<HD, NT>(p, smem, sbase);
+        else consumer<HD, NT, F32>(p, smem, sbase);
     }
     end_in_order(p.second);
 }
@@ -658,7 +948,7 @@ template <int HD, int NT, bool F32> int launch_typed(FewParams &p, cudaStream_t 
 }  // namespace
 
 int q4_few_ctas(int sms, int rows, int dtype) {
-    return (rows == 8 && dtype == USP_BF16 ? Cfg<128, 1, false>::kCtas : Cfg<128, 2, false>::kCtas) * sms;
+    return (dtype == USP_BF16 ? Cfg<128, 1, false>::kCtas : Cfg<128, 1, true>::kCtas) * sms;
 }
 
 int launch_paged_q4_few(const PagedQ4Args &a, int G, int rows, int n_hi, bool second, const PartSpace &w, cudaStream_t s) {
@@ -667,7 +957,7 @@ int launch_paged_q4_few(const PagedQ4Args &a, int G, int rows, int n_hi, bool se
     FewParams p{};
     const int ps = 1 << a.log_ps;
     const bool f32 = a.dtype == USP_F32;
-    const int tile = a.hd == 128 || rows == 16 || f32 ? Cfg<128, 1, false>::kKT : Cfg<64, 1, false>::kKT;
+    const int tile = a.hd == 128 || rows > 8 || f32 ? Cfg<128, 1, false>::kKT : Cfg<64, 1, false>::kKT;
     const uint32_t box = (uint32_t)std::min(ps, tile);
     if (!make_codes_tmap(&p.tk, a.k, a.num_pages, a.k_page, a.hkv, ps, a.hd, box) ||
         !make_codes_tmap(&p.tv, a.v, a.num_pages, a.v_page, a.hkv, ps, a.hd, box))
@@ -693,15 +983,16 @@ int launch_paged_q4_few(const PagedQ4Args &a, int G, int rows, int n_hi, bool se
     auto go = [&](auto hd, auto nt, auto f32) {
         return launch_typed<decltype(hd)::value, decltype(nt)::value, decltype(f32)::value>(p, s);
     };
-    auto with = [&](auto hd, auto nt) {
-        return a.dtype == USP_F32 ? go(hd, nt, std::true_type{}) : go(hd, nt, std::false_type{});
+    auto with = [&](auto hd) {
+        using One = std::integral_constant<int, 1>;
+        using Two = std::integral_constant<int, 2>;
+        using Three = std::integral_constant<int, 3>;
+        using Four = std::integral_constant<int, 4>;
+        if (f32) return rows == 8 ? go(hd, One{}, std::true_type{}) : go(hd, Two{}, std::true_type{});
+        return rows == 8 ? go(hd, One{}, std::false_type{}) : rows == 16 ? go(hd, Two{}, std::false_type{})
+               : rows == 24 ? go(hd, Three{}, std::false_type{}) : go(hd, Four{}, std::false_type{});
     };
-    using I64 = std::integral_constant<int, 64>;
-    using I128 = std::integral_constant<int, 128>;
-    using One = std::integral_constant<int, 1>;
-    using Two = std::integral_constant<int, 2>;
-    if (rows == 8) return a.hd == 128 ? with(I128{}, One{}) : with(I64{}, One{});
-    return a.hd == 128 ? with(I128{}, Two{}) : with(I64{}, Two{});
+    return a.hd == 128 ? with(std::integral_constant<int, 128>{}) : with(std::integral_constant<int, 64>{});
 }
 
 }  // namespace usp

@@ -189,6 +189,35 @@ def test_a_very_large_or_small_query(dt):
 
 
 @pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("hd,ps", [(128, 64), (64, 16), (128, 16), (64, 256)])
+@pytest.mark.parametrize("hq,hkv,most", [(12, 1, 1), (10, 2, 3), (8, 2, 5), (8, 1, 3), (24, 1, 1), (8, 2, 8), (31, 1, 1), (6, 2, 10)])
+def test_units_of_nine_to_thirty_two_rows(hq, hkv, most, hd, ps, causal):
+    """Two to four tiles of 8 rows, the last one in part: units cut between CTAs, without a key, with fewer keys than new
+    tokens; also where a request has more new tokens than the host says."""
+    reqs = [(26000, most), (200, most), (15, 1), (129, max(1, most - 1)), (0, most), (128, most), (1, most), (31000, 1), (7, 0)]
+    c = Q4Cache(reqs + [(450 + 130 * i, most) for i in range(6)], hq, hkv, hd, ps, torch.bfloat16, seed=81, wide=True)
+    out, lse = attend(c, max_new=c.max_new, causal=causal)
+    check_attention(c, out, lse, causal)
+    again = attend(c, max_new=c.max_new, causal=causal)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    c = Q4Cache([(300, 40), (5000, most)], hq, hkv, hd, ps, torch.bfloat16, seed=82)
+    out, lse = attend(c, max_new=most, causal=causal)
+    check_attention(c, out, lse, causal)
+
+
+def test_a_nan_query_row_among_twenty(hd=128):
+    c = Q4Cache([(900, 5), (64, 5), (20000, 5)], 8, 2, hd, 64, torch.bfloat16, seed=83)
+    c.q[7, 3] = float("nan")
+    out, lse = attend(c, max_new=5)
+    assert torch.isnan(out[7, 3]).all() and torch.isnan(lse[7, 3])
+    c.q[7, 3] = 0
+    out2, lse2 = attend(c, max_new=5)
+    keep = torch.ones(c.T, 8, dtype=torch.bool, device="cuda")
+    keep[7, 3] = False
+    assert torch.equal(out[keep], out2[keep]) and torch.equal(lse[keep], lse2[keep])
+
+
+@pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("hq,hkv,hd,ps", [(8, 2, 128, 64), (8, 1, 64, 16), (5, 1, 128, 128), (40, 1, 64, 32)])
 @pytest.mark.parametrize("reqs", [
     [(30000, 9)], [(26000, 12), (200, 6), (15, 12), (129, 5), (0, 5), (128, 11), (1, 7), (31000, 10)],
