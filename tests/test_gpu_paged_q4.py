@@ -396,6 +396,32 @@ def test_calls_on_three_streams_keep_their_bits():
     usp.usp_check()
 
 
+def test_short_chunks_on_three_streams_keep_their_bits():
+    """As above, units of 9 to 128 rows: several tiles of 8 rows with one state, and one tile of 128 with two."""
+    r = random.Random(2)
+
+    def make(i):
+        G, rows = r.choice([1, 2, 4, 5, 8, 12, 16]), [16, 24, 32, 100][i % 4]
+        most = max(1, rows // G)
+        reqs = [(r.randrange(most, 6000), r.randrange(max(1, most - 1), most + 1)) for _ in range(r.randrange(1, 20))]
+        hkv = r.choice([1, 2, 4])
+        c = Q4Cache(reqs, hkv * G, hkv, r.choice([64, 128]), r.choice([16, 64, 256]), torch.bfloat16, seed=100 + i)
+        return c, [x.clone() for x in attend(c, max_new=most)], most
+    calls, streams = [make(i) for i in range(20)], [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for _ in range(200):
+        wrong = []
+        for _ in range(40):
+            c, want, most = r.choice(calls)
+            with torch.cuda.stream(r.choice(streams)):
+                out, lse = torch.full_like(want[0], float("nan")), torch.full_like(want[1], float("nan"))
+                usp.usp_paged_attn_q4(*c.args(), max_new=most, out=out, lse=lse)
+                wrong.append((out != want[0]).sum() + (lse != want[1]).sum())
+        torch.cuda.synchronize()
+        assert sum(int(x) for x in wrong) == 0
+    usp.usp_check()
+
+
 @pytest.mark.parametrize("hq,hkv,hd,dt", [(8, 1, 128, torch.bfloat16), (16, 4, 128, torch.bfloat16), (5, 5, 64, torch.bfloat16),
                                           (20, 1, 128, torch.bfloat16), (64, 1, 64, torch.bfloat16), (8, 2, 64, torch.float32),
                                           (32, 1, 128, torch.float32)])
