@@ -21,7 +21,7 @@
 //  - lane (g, t) converts for K the 32 values of group t of keys g and g + 8, and for V the 16 columns from 16 g on of four
 //    keys: loads of 16 and 8 bytes, a scale byte each. Which key is row k of a product is free: key_of makes both loads
 //    meet all banks.
-// Measured (8 KV heads of 128, 4 query heads each, pages of 64): 64 requests of 11000 keys 157 us, 0.72 of the copy rate; with
+// Measured (8 KV heads of 128, 4 query heads each, pages of 64): 64 requests of 11000 keys 155 us, 0.73 of the copy rate; with
 // pages of 16 tokens 176, hd 64 90 (0.63), two requests of 230000 keys 107 (0.69); 16 rows 215, 32 rows 351. Loading alone
 // runs at 0.95 to 1.05 of the copy rate. Per 16 keys a warp issues 306 instructions; 16 operands of four shifts, four logic
 // operations, four bf16x2 multiply-adds and a product take 22 to 24 cycles each of a scheduler, as the logic pipe takes one
@@ -347,43 +347,50 @@ template <int HD, int NT, bool F32> __device__ void consumer(const FewParams &p,
             float sc[kW][NT][4];
             float low[kW][NT][4];  // F32: of q's second and third terms
 #pragma unroll
-            for (int i = 0; i < kW; ++i) {
-                uint32_t w[2][kWords], s2[2], off[2];
+            for (int i0 = 0; i0 < kW; i0 += 2) {  // two steps at a time: products of two chains in turn, q's terms loaded once
+                uint32_t w[2][2][kWords], s2[2][2], off[2][2];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint32_t at = base + further(k_at, i * 16 + e * 8);
-                    if constexpr (HD == 128) {
-                        const uint4 x = lds128(at);
-                        w[e][0] = x.x; w[e][1] = x.y; w[e][2] = x.z; w[e][3] = x.w;
-                    } else {
-                        const uint2 x = lds64(at);
-                        w[e][0] = x.x; w[e][1] = x.y;
-                    }
-                    s2[e] = q4_scales2(lds8(sbs + ks_at + (i * 16 + e * 8) * C::kSRow));
-                    off[e] = q4_minus136(s2[e]);
-                }
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[i][n][e] = low[i][n][e] = 0.f;
-#pragma unroll
-                for (int k = 0; k < kMT; ++k) {
-                    uint32_t a[4];
+                for (int i = 0; i < 2; ++i) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        a[e] = nib.values(w[e][k / 2], k % 2 * 2, s2[e], off[e]);
-                        a[2 + e] = nib.values(w[e][k / 2], k % 2 * 2 + 1, s2[e], off[e]);
+                        const uint32_t at = base + further(k_at, (i0 + i) * 16 + e * 8);
+                        if constexpr (HD == 128) {
+                            const uint4 x = lds128(at);
+                            w[i][e][0] = x.x; w[i][e][1] = x.y; w[i][e][2] = x.z; w[i][e][3] = x.w;
+                        } else {
+                            const uint2 x = lds64(at);
+                            w[i][e][0] = x.x; w[i][e][1] = x.y;
+                        }
+                        s2[i][e] = q4_scales2(lds8(sbs + ks_at + ((i0 + i) * 16 + e * 8) * C::kSRow));
+                        off[i][e] = q4_minus136(s2[i][e]);
                     }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sc[i0 + i][n][e] = low[i0 + i][n][e] = 0.f;
+                }
+#pragma unroll
+                for (int k = 0; k < kMT; ++k) {
+                    uint32_t a[2][4];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            a[i][e] = nib.values(w[i][e][k / 2], k % 2 * 2, s2[i][e], off[i][e]);
+                            a[i][2 + e] = nib.values(w[i][e][k / 2], k % 2 * 2 + 1, s2[i][e], off[i][e]);
+                        }
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         if constexpr (F32) {
 #pragma unroll
                             for (int x = kT - 1; x >= 0; --x) {
                                 const uint2 b = lds64(sbase + C::kQ + (((x * kMT + k) * NT + n) * 32 + lane) * 8);
-                                mma16816(x ? low[i][n] : sc[i][n], a, b.x, b.y);
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) mma16816(x ? low[i0 + i][n] : sc[i0 + i][n], a[i], b.x, b.y);
                             }
                         } else {
-                            mma16816(sc[i][n], a, qf[k][n].x, qf[k][n].y);
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) mma16816(sc[i0 + i][n], a[i], qf[k][n].x, qf[k][n].y);
                         }
                     }
                 }
