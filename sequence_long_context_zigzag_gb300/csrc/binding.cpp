@@ -395,19 +395,21 @@ struct RopeFunction : torch::autograd::Function<RopeFunction> {
     static torch::autograd::variable_list forward(torch::autograd::AutogradContext *ctx, const Tensor &q, const Optional &opt_k,
                                                   const Tensor &table, const Optional &positions, const Optional &cu,
                                                   bool interleaved, bool inverse) {
-        const Tensor k = opt_k.value_or(Tensor());
-        const RopeCall call(q, k, table, positions.value_or(Tensor()), cu.value_or(Tensor()), interleaved, inverse);
-        const c10::cuda::CUDAGuard guard((c10::DeviceIndex)call.index);
-        const Tensor qo = empty(q.sizes(), q.scalar_type(), call.index),
-                     ko = k.defined() ? empty(k.sizes(), k.scalar_type(), call.index) : Tensor();
-        if (const int rc = call.run(q, k, qo, ko)) throw Status{rc};
         torch::autograd::variable_list saved{table};
         if (positions) saved.push_back(*positions);
         if (cu) saved.push_back(*cu);
         ctx->save_for_backward(std::move(saved));
-        ctx->saved_data["positions"] = positions.has_value();
-        ctx->saved_data["interleaved"] = interleaved;
-        ctx->saved_data["inverse"] = inverse;
+        ctx->saved_data["flags"] = int64_t(positions ? POSITIONS : 0) | (interleaved ? INTERLEAVED : 0) | (inverse ? INVERSE : 0);
+        return rotated(q, opt_k.value_or(Tensor()), table, positions.value_or(Tensor()), cu.value_or(Tensor()), interleaved, inverse);
+    }
+    enum Flags { POSITIONS = 1, INTERLEAVED = 2, INVERSE = 4 };
+    static torch::autograd::variable_list rotated(const Tensor &q, const Tensor &k, const Tensor &table, const Tensor &positions,
+                                                  const Tensor &cu, bool interleaved, bool inverse) {
+        const RopeCall call(q, k, table, positions, cu, interleaved, inverse);
+        const c10::cuda::CUDAGuard guard((c10::DeviceIndex)call.index);
+        const Tensor qo = empty(q.sizes(), q.scalar_type(), call.index),
+                     ko = k.defined() ? empty(k.sizes(), k.scalar_type(), call.index) : Tensor();
+        if (const int rc = call.run(q, k, qo, ko)) throw Status{rc};
         return k.defined() ? torch::autograd::variable_list{qo, ko} : torch::autograd::variable_list{qo};
     }
     // a gradient as the rotation takes it; it may come expanded, or as part of another tensor at any address
@@ -419,11 +421,16 @@ struct RopeFunction : torch::autograd::Function<RopeFunction> {
         const auto saved = ctx->get_saved_variables();
         const bool has_k = g.size() > 1;
         try {
-            const bool has_pos = ctx->saved_data["positions"].toBool();
-            const Optional k = has_k ? Optional(dense(g[1])) : std::nullopt, pos = has_pos ? Optional(saved[1]) : std::nullopt,
-                           cu = saved.size() > 1u + has_pos ? Optional(saved.back()) : std::nullopt;
-            auto d = apply(dense(g[0]), k, saved[0], pos, cu, ctx->saved_data["interleaved"].toBool(),
-                           !ctx->saved_data["inverse"].toBool());
+            const int64_t flags = ctx->saved_data["flags"].toInt();
+            const bool has_pos = flags & POSITIONS, has_cu = saved.size() > 1u + has_pos;
+            const bool interleaved = flags & INTERLEAVED, inverse = !(flags & INVERSE);
+            const Tensor q = dense(g[0]), k = has_k ? dense(g[1]) : Tensor();
+            torch::autograd::variable_list d;
+            if (at::GradMode::is_enabled())  // the gradient is to be differentiated in turn
+                d = apply(q, has_k ? Optional(k) : std::nullopt, saved[0], has_pos ? Optional(saved[1]) : std::nullopt,
+                          has_cu ? Optional(saved.back()) : std::nullopt, interleaved, inverse);
+            else
+                d = rotated(q, k, saved[0], has_pos ? saved[1] : Tensor(), has_cu ? saved.back() : Tensor(), interleaved, inverse);
             return {d[0], has_k ? d[1] : Tensor(), Tensor(), Tensor(), Tensor(), Tensor(), Tensor()};
         } catch (const Refused &r) {
             TORCH_CHECK(false, r.what);
