@@ -617,7 +617,9 @@ def usp_rope(q, k, table, positions=None, cu_seqlens=None, interleaved: bool = F
 
 class UspRopeFunction:
     """usp_rope as a differentiable op: (q, k) rotated; the gradients are rotated back, in one launch, and are
-    differentiable in turn. (k may be None. The op itself is in csrc/binding.cpp.)"""
+    differentiable in turn. (k may be None. The op itself is in csrc/binding.cpp.) A backward pass that accumulates into
+    .grad can be captured into a graph only while no eager graph of the same leaves is held: torch keeps one accumulating
+    node per leaf, on the stream where it was made."""
 
     @staticmethod
     def apply(q, k, table, positions=None, cu_seqlens=None, interleaved=False):
