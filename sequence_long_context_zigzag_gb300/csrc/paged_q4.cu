@@ -68,8 +68,8 @@ struct Route {
 };
 Route route(const usp_paged_q4_desc &d, int sms) {
     Route r{};
-    // bf16: the kernel for few rows against the one for many, 32 requests of 8000 keys, 20, 24, 32 rows 118, 119, 145 us against
-    // 150, 150, 150; 16 requests of 2000 28, 29, 35 against 39, 39, 40; 36 rows would take two units
+    // bf16: the kernel for few rows against the one for many, 32 requests of 8000 keys, 20 to 24 and 32 rows 107 and 133 us against
+    // 150; 100 requests of 1000 61 and 76 against 98; 36 rows would take two units
     const int G = d.hq / d.cache.hkv, most = d.dtype == USP_BF16 ? 32 : 16;
     const int64_t rows = G * (int64_t)std::max(1, d.max_new);
     r.few_G = few_heads(G, most);

@@ -22,7 +22,7 @@
 //    keys: loads of 16 and 8 bytes, a scale byte each. Which key is row k of a product is free: key_of makes both loads
 //    meet all banks.
 // Measured (8 KV heads of 128, 4 query heads each, pages of 64): 64 requests of 11000 keys 155 us, 0.73 of the copy rate; with
-// pages of 16 tokens 176, hd 64 90 (0.63), two requests of 230000 keys 107 (0.69); 16 rows 215, 32 rows 351. Loading alone
+// pages of 16 tokens 176, hd 64 90 (0.63), two requests of 230000 keys 107 (0.69); 16 rows 209. Loading alone
 // runs at 0.95 to 1.05 of the copy rate. Per 16 keys a warp issues 306 instructions; 16 operands of four shifts, four logic
 // operations, four bf16x2 multiply-adds and a product take 22 to 24 cycles each of a scheduler, as the logic pipe takes one
 // instruction in two cycles and the multiply-adds do not quite hide under them: 486 cycles, where HBM would take 372. More
@@ -54,7 +54,7 @@ constexpr float kLn2 = 0.69314718055994531f;
 template <int HD, int NT, bool F32> struct Cfg {
     static constexpr int kTerms = F32 ? 3 : 1;
     static constexpr bool kWide = NT > 1 && !F32;         // see consumer_wide
-    static constexpr int kCtas = F32 ? 2 : 3;             // per SM
+    static constexpr int kCtas = F32 || NT >= 3 ? 2 : 3;  // per SM, as registers allow (24, 32 rows in three: 117, 146 us for 107, 133)
     static constexpr int kW = HD == 64 && NT == 1 && !F32 ? 4 : 2;  // 16-key steps per warp and tile
     static constexpr int kKT = 16 * kW * kWarps;          // keys per tile
     // keys per CTA below which fewer CTAs work (one request of 8000 keys with kKT + 1, 64, 128, 320: 17.6, 13.7, 12.3, 12.4 us; four
@@ -63,14 +63,15 @@ template <int HD, int NT, bool F32> struct Cfg {
     static_assert(kMinSpan > kKT, "a span holds more than a tile");
     static constexpr int kRow = q4_code_bytes(HD), kSRow = q4_scale_bytes(HD);
     static constexpr int kCodes = kKT * kRow, kScales = kKT * kSRow;
-    static constexpr int kStages = 3 * (kKT * HD == 128 * 128 ? 1 : 2);
+    static constexpr int kStages = (NT >= 3 ? 4 : 3) * (kKT * HD == 128 * 128 ? 1 : 2);
     static constexpr int kXRow = HD + 4;                  // exchange row in floats
     static constexpr int kSc = kStages * 2 * kCodes;      // scales, behind all stages' codes (K, V each)
     static constexpr int kX = kSc + kStages * 2 * kScales;  // [warp][row][kXRow]
     static constexpr int kML = kX + (kWide ? 0 : kWarps * NT * 8 * kXRow * 4);
     static constexpr int kQ = kML + kWarps * NT * 8 * 8;  // q's terms as operands: [term][step][row tile][lane]
-    static constexpr int kP = kQ + (F32 || kWide ? kTerms * (HD / 16) * NT * 256 : 0);  // kWide: P: [step][row tile][lane]
-    static constexpr int kSeg = kP + (kWide ? kKT / 16 * NT * 256 : 0);
+    static constexpr int kP = kQ + (F32 || kWide ? kTerms * (HD / 16) * NT * 256 : 0);  // kWide: P: [two steps][row tile][lane]
+    static constexpr int kVS = kP + (kWide ? kKT / 16 * NT * 256 : 0);  // kWide: V's scales as operands: [warp][step, t]
+    static constexpr int kSeg = kVS + (kWide ? kWarps * 256 : 0);
     static constexpr int kBar = kSeg + kSegSlots * (int)sizeof(SegMsg);
     static constexpr int FULL = 0, EMPTY = kStages, SEG_FULL = 2 * kStages, SEG_EMPTY = SEG_FULL + kSegSlots;
     static constexpr int kSmem = kBar + (SEG_EMPTY + kSegSlots) * 8 + 1024;  // + slack for the alignment
@@ -123,6 +124,9 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 }
 __device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
     asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint4 x) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
 }
 __device__ __forceinline__ uint32_t lds8(uint32_t a) {
     uint32_t x;
@@ -610,9 +614,9 @@ template <int HD, int NT, bool F32> __device__ void consumer(const FewParams &p,
 // Units of 9 to 32 rows (bf16). A warp takes a quarter of the tile's keys for S^T, as above, but a quarter of the head's
 // columns, over all of the tile's keys, for O^T: so it holds O of 32 rows in the registers of one row tile, no value of the cache
 // is converted twice, and there is one softmax state: the weights go through shared memory. Two barriers a tile: where a
-// maximum has to move (one for all warps), and before the weights are read. Measured: 32 requests of 8000 keys, 16, 24, 32 rows 90, 119,
-// 145 us (with the division above 16 rows take 97 and spill); for 8 rows the barriers cost more than the smaller O
-// gives (64 requests of 11000 keys 173 us, the division above 156).
+// maximum has to move (one for all warps), and before the weights are read. Measured: 32 requests of 8000 keys, 16, 24, 32 rows 87, 107,
+// 133 us, hd 64 61, 78, 91 (with the division above 16 rows take 97 and spill); for 8 rows the barriers cost more than the
+// smaller O gives (64 requests of 11000 keys 173 us, the division above 155).
 template <int HD, int NT> __device__ void consumer_wide(const FewParams &p, uint8_t *smem, uint32_t sbase) {
     using C = Cfg<HD, NT, false>;
     constexpr int kMT = HD / 16, kX = HD / 64;  // 16-element steps of the head dim; this warp's 16-column tiles of O^T
@@ -631,13 +635,17 @@ template <int HD, int NT> __device__ void consumer_wide(const FewParams &p, uint
     auto further = [](uint32_t at, int n) { return (at ^ ((n * C::kRow >> 3) & 0x70)) + n * C::kRow; };
     // V's rows 2 t, 2 t + 1 (and + 8) of a step: the word with this lane's columns. Of the 8 columns of a word it has the even
     // or the odd ones (hd 64: two of these)
-    uint32_t v_at[2], vs_at[2];
+    uint32_t v_at[2];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const int key = key_of<HD>(2 * t + e);
-        v_at[e] = C::kCodes + codes_at<HD>(key, warp * (C::kRow / 4) + (HD == 128 ? g >> 1 : g >> 2) * 4);
-        vs_at[e] = C::kScales + key * C::kSRow + (HD == 128 ? warp : warp >> 1);
-    }
+    for (int e = 0; e < 2; ++e)
+        v_at[e] = C::kCodes + codes_at<HD>(key_of<HD>(2 * t + e), warp * (C::kRow / 4) + (HD == 128 ? g >> 1 : g >> 2) * 4);
+    // V's scales: the warp's columns are of one group, so a pair of keys has one operand; lane 4 i + t makes those of step i's
+    // rows 2 t, 2 t + 1 (and + 8)
+    const uint32_t my_vs = sbase + C::kVS + warp * 256;
+    uint32_t vs_at[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+        vs_at[e] = C::kScales + (g * 16 + key_of<HD>(2 * t + e)) * C::kSRow + (HD == 128 ? warp : warp >> 1);
     const uint32_t half = g & 1 ? 0x7632u : 0x5410u;
     const int v_shift = HD == 128 ? 0 : (g >> 1 & 1) * 8;
     uint32_t st = 0, st_phase = 0;  // the stage of the next tile, and its fill's parity
@@ -663,10 +671,9 @@ template <int HD, int NT> __device__ void consumer_wide(const FewParams &p, uint
                     q = static_cast<const __nv_bfloat16 *>(p.q) + (s.tok0 + tok) * p.q_stride +
                         (int64_t)(s.head * p.s.G + (int)h) * HD + t * (8 * kWords);
                 }
-                for (int k = warp; k < kMT; k += kWarps) {
-                    const uint2 x = q ? *reinterpret_cast<const uint2 *>(q + k * 4) : make_uint2(0u, 0u);
-                    sts64(sbase + C::kQ + ((k * NT + n) * 32 + lane) * 8, x.x, x.y);
-                }
+                for (int k = warp; k < kMT / 2; k += kWarps)  // two steps of the head dim
+                    sts128(sbase + C::kQ + ((k * NT + n) * 32 + lane) * 16,
+                           q ? *reinterpret_cast<const uint4 *>(q + k * 8) : make_uint4(0u, 0u, 0u, 0u));
             }
         }
         // The barriers of the tiles need all warps: a failed wait ends the segment for all of them here or at a tile's first
@@ -687,6 +694,14 @@ template <int HD, int NT> __device__ void consumer_wide(const FewParams &p, uint
             ok = wait(C::FULL + st, st_phase);
             const uint32_t base = sbase + st * 2 * C::kCodes, sbs = sbase + C::kSc + st * 2 * C::kScales;
             const int key0 = kt * C::kKT + warp * 16 * kW;
+            {
+                uint32_t b[2][2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) b[h][e] = lds8(sbs + vs_at[e] + h * 8 * C::kSRow);
+                sts64(my_vs + lane * 8, q4_scales2(b[0][0], b[0][1]), q4_scales2(b[1][0], b[1][1]));
+            }
             // ---- S^T = K Q^T ----
             float sc[kW][NT][4];
             uint32_t w[kW][2][kWords], s2[kW][2], off[kW][2];
@@ -711,20 +726,24 @@ template <int HD, int NT> __device__ void consumer_wide(const FewParams &p, uint
                     for (int e = 0; e < 4; ++e) sc[i][n][e] = 0.f;
             }
 #pragma unroll
-            for (int k = 0; k < kMT; ++k) {
-                uint32_t a[kW][4];
+            for (int k = 0; k < kMT / 2; ++k) {
+                uint32_t a[2][kW][4];
 #pragma unroll
-                for (int i = 0; i < kW; ++i)
+                for (int j = 0; j < 2; ++j)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        a[i][e] = nib.values(w[i][e][k / 2], k % 2 * 2, s2[i][e], off[i][e]);
-                        a[i][2 + e] = nib.values(w[i][e][k / 2], k % 2 * 2 + 1, s2[i][e], off[i][e]);
-                    }
+                    for (int i = 0; i < kW; ++i)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            a[j][i][e] = nib.values(w[i][e][k], 2 * j, s2[i][e], off[i][e]);
+                            a[j][i][2 + e] = nib.values(w[i][e][k], 2 * j + 1, s2[i][e], off[i][e]);
+                        }
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    const uint2 b = lds64(sbase + C::kQ + ((k * NT + n) * 32 + lane) * 8);
+                    const uint4 b = lds128(sbase + C::kQ + ((k * NT + n) * 32 + lane) * 16);
 #pragma unroll
-                    for (int i = 0; i < kW; ++i) mma16816(sc[i][n], a[i], b.x, b.y);
+                    for (int i = 0; i < kW; ++i) mma16816(sc[i][n], a[0][i], b.x, b.y);
+#pragma unroll
+                    for (int i = 0; i < kW; ++i) mma16816(sc[i][n], a[1][i], b.z, b.w);
                 }
             }
             // ---- softmax ----
@@ -783,6 +802,7 @@ template <int HD, int NT> __device__ void consumer_wide(const FewParams &p, uint
                 float nmb[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) nmb[e] = m[n][e] == -INFINITY ? 0.f : -m[n][e];
+                uint32_t pt[kW][2];
 #pragma unroll
                 for (int i = 0; i < kW; ++i) {
                     float x[4];
@@ -790,36 +810,40 @@ template <int HD, int NT> __device__ void consumer_wide(const FewParams &p, uint
                     for (int e = 0; e < 4; ++e) x[e] = tc::ex2(fmaf(sc[i][n][e], p.scale_log2, nmb[e & 1]));
                     l[n][0] += x[0] + x[2];
                     l[n][1] += x[1] + x[3];
-                    sts64(sbase + C::kP + (((warp * kW + i) * NT + n) * 32 + lane) * 8, transpose8x8(float2_to_bf16x2(x[0], x[1])),
-                          transpose8x8(float2_to_bf16x2(x[2], x[3])));
+                    pt[i][0] = transpose8x8(float2_to_bf16x2(x[0], x[1]));
+                    pt[i][1] = transpose8x8(float2_to_bf16x2(x[2], x[3]));
                 }
+                sts128(sbase + C::kP + ((warp * NT + n) * 32 + lane) * 16, make_uint4(pt[0][0], pt[0][1], pt[1][0], pt[1][1]));
             }
             consumers_sync();
             // ---- O^T += V^T P^T ----
 #pragma unroll
-            for (int i = 0; i < C::kKT / 16; ++i) {
-                uint32_t a[kX][4];
+            for (int j = 0; j < C::kKT / 32; ++j) {
+                uint32_t a[2][kX][4];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t v[2], b[2];
+                for (int i = 0; i < 2; ++i) {
+                    const uint2 v2 = lds64(my_vs + (2 * j + i) * 32 + t * 8);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        v[e] = lds32(base + further(v_at[e], i * 16 + h * 8));
-                        b[e] = lds8(sbs + vs_at[e] + (i * 16 + h * 8) * C::kSRow);
-                    }
-                    const uint32_t v2 = q4_scales2(b[0], b[1]), voff = q4_minus136(v2);
-                    const uint32_t word = __byte_perm(v[0], v[1], half) >> v_shift;
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t v[2];
 #pragma unroll
-                    for (int x = 0; x < kX; ++x) {
-                        a[x][2 * h] = nib.values(word, 2 * x, v2, voff);
-                        a[x][2 * h + 1] = nib.values(word, 2 * x + 1, v2, voff);
+                        for (int e = 0; e < 2; ++e) v[e] = lds32(base + further(v_at[e], (2 * j + i) * 16 + h * 8));
+                        const uint32_t vs2 = h ? v2.y : v2.x, voff = q4_minus136(vs2);
+                        const uint32_t word = __byte_perm(v[0], v[1], half) >> v_shift;
+#pragma unroll
+                        for (int x = 0; x < kX; ++x) {
+                            a[i][x][2 * h] = nib.values(word, 2 * x, vs2, voff);
+                            a[i][x][2 * h + 1] = nib.values(word, 2 * x + 1, vs2, voff);
+                        }
                     }
                 }
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    const uint2 b = lds64(sbase + C::kP + ((i * NT + n) * 32 + lane) * 8);
+                    const uint4 b = lds128(sbase + C::kP + ((j * NT + n) * 32 + lane) * 16);
 #pragma unroll
-                    for (int x = 0; x < kX; ++x) mma16816(o[n][x], a[x], b.x, b.y);
+                    for (int x = 0; x < kX; ++x) mma16816(o[n][x], a[0][x], b.x, b.y);
+#pragma unroll
+                    for (int x = 0; x < kX; ++x) mma16816(o[n][x], a[1][x], b.z, b.w);
                 }
             }
             // (as above)
@@ -955,7 +979,7 @@ template <int HD, int NT, bool F32> int launch_typed(FewParams &p, cudaStream_t 
 }  // namespace
 
 int q4_few_ctas(int sms, int rows, int dtype) {
-    return (dtype == USP_BF16 ? Cfg<128, 1, false>::kCtas : Cfg<128, 1, true>::kCtas) * sms;
+    return (dtype == USP_BF16 ? rows > 16 ? Cfg<128, 3, false>::kCtas : Cfg<128, 1, false>::kCtas : Cfg<128, 1, true>::kCtas) * sms;
 }
 
 int launch_paged_q4_few(const PagedQ4Args &a, int G, int rows, int n_hi, bool second, const PartSpace &w, cudaStream_t s) {
