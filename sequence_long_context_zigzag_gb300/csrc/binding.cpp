@@ -377,13 +377,11 @@ PyObject *rope(PyObject *const *a) {
             stride = token_stride(name, x);
         });
     };
+    need(k.defined() || a[8] == Py_None, "k_out without k");
     Output qo = out(a[7], "q_out", q, call.d.q_out_stride), ko;
     if (k.defined()) ko = out(a[8], "k_out", k, call.d.k_out_stride);
+    else ko.given = Py_None;
     if (const int rc = call.run(q, k, qo.t, ko.t)) return PyLong_FromLong(rc);
-    if (!k.defined()) {
-        need(a[8] == Py_None, "k_out without k");
-        ko.given = Py_None;
-    }
     return tuple({&qo, &ko});
 }
 
