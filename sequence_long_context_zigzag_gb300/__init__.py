@@ -609,8 +609,9 @@ def usp_rope(q, k, table, positions=None, cu_seqlens=None, interleaved: bool = F
     the attention: the place in the sequence, or in its packed sample (``cu_seqlens``), or ``positions`` (int32, one per
     token; a token whose position is not in the table, e.g. -1 for padding, is copied). ``table``: see
     :func:`usp_rope_table`; its columns are the elements of a head that are rotated, in pairs (i, i + rot / 2), or
-    (2 i, 2 i + 1) with ``interleaved``. ``inverse`` rotates back. The outputs may be the inputs.
-    Returns (q_out, k_out)."""
+    (2 i, 2 i + 1) with ``interleaved``. ``inverse`` rotates back. The outputs may be the inputs
+    (not tensors that require grad, unless in no_grad: :class:`UspRopeFunction` is what autograd records). Returns
+    (q_out, k_out)."""
     return _on_stream("usp_rope", q, stream, _abi.binding().rope, q, k, table, positions, cu_seqlens, interleaved, inverse,
                       q_out, k_out)
 

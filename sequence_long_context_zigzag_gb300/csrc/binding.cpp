@@ -126,12 +126,24 @@ Tensor empty(at::IntArrayRef sizes, at::ScalarType type, int index) {
     return Tensor(at::detail::empty_cuda(sizes, type, at::Device(at::kCUDA, (c10::DeviceIndex)index), std::nullopt));
 }
 
+// The call wrote t: a node of autograd that saved it notices. (Inference tensors count no versions.)
+void written(const Tensor &t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+// Autograd would follow t past a call that it does not see.
+void unrecorded(const char *name, const Tensor &t) {
+    if (at::GradMode::is_enabled() && t.requires_grad())
+        refuse(std::string(name) + " requires grad, which a rotation that is not recorded would leave wrong (UspRopeFunction is "
+                                   "the differentiable form)");
+}
+
 // A call's output: the caller's tensor, returned as it came, or a new one.
 struct Output {
     PyObject *given = nullptr;
     Tensor t;
     PyObject *result() {
         if (!given) return THPVariable_Wrap(std::move(t));
+        if (t.defined()) written(t);
         Py_INCREF(given);
         return given;
     }
@@ -194,6 +206,7 @@ PyObject *page_plan(PyObject *const *a) {
     const int rc = g_plan(ints(ctx), ints(fresh), ints(pages), ints(head), mutable_ints(table), mutable_ints(slots.t),
                           mutable_ints(cu.t), mutable_ints(kv.t), mutable_ints(counts.t), d, stream_of(index));
     if (rc) return PyLong_FromLong(rc);
+    written(table);
     return tuple({&slots, &cu, &kv, &counts});
 }
 
@@ -209,8 +222,13 @@ PyObject *cache_append(PyObject *const *a) {
     const int64_t ks = dense_rows("k", k), vs = dense_rows("v", v);
     const int index = device_of({&k, &v, &kc, &vc, &slots});
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)index);
-    return PyLong_FromLong(g_append(k.const_data_ptr(), v.const_data_ptr(), kc.mutable_data_ptr(), vc.mutable_data_ptr(),
-                                    ints(slots), k.size(0), ks, vs, d, stream_of(index)));
+    const int rc = g_append(k.const_data_ptr(), v.const_data_ptr(), kc.mutable_data_ptr(), vc.mutable_data_ptr(), ints(slots),
+                            k.size(0), ks, vs, d, stream_of(index));
+    if (rc == USP_OK) {
+        written(kc);
+        written(vc);
+    }
+    return PyLong_FromLong(rc);
 }
 
 usp_paged_desc paged_desc(const Tensor &q, const Tensor &kc, const Tensor &vc, const Tensor &table, int64_t nreq,
@@ -374,6 +392,7 @@ PyObject *rope(PyObject *const *a) {
     auto out = [&](PyObject *o, const char *name, const Tensor &like, int64_t &stride) {
         return output(o, name, call.index, like.sizes(), like.scalar_type(), [&](const Tensor &x) {
             if (x.sizes() != like.sizes() || x.scalar_type() != like.scalar_type()) refuse(std::string(name) + " must match its input");
+            unrecorded(name, x);
             stride = token_stride(name, x);
         });
     };
@@ -537,6 +556,7 @@ PyObject *rope_append(PyObject *const *a) {
     if (has_q)
         qo = output(a[13], "q_out", index, q.sizes(), q.scalar_type(), [&](const Tensor &x) {
             need(x.sizes() == q.sizes() && x.scalar_type() == q.scalar_type(), "q_out must match q");
+            unrecorded("q_out", x);
             d.q_out_stride = dense_rows("q_out", x);
         });
     const void *qp = has_q ? q.const_data_ptr() : nullptr;
@@ -547,6 +567,12 @@ PyObject *rope_append(PyObject *const *a) {
            : g_rope_append(qp, qop, k.const_data_ptr(), v.const_data_ptr(), kc.mutable_data_ptr(), vc.mutable_data_ptr(),
                            ints(slots), positions, cu, kv, t.data, d, c, stream_of(index));
     if (rc) return PyLong_FromLong(rc);
+    written(kc);
+    written(vc);
+    if (q4) {
+        written(ks);
+        written(vs);
+    }
     if (!has_q) Py_RETURN_NONE;
     PyObject *r = qo.result();
     if (!r) throw PythonError{};
