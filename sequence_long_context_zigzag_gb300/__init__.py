@@ -609,18 +609,17 @@ def usp_rope(q, k, table, positions=None, cu_seqlens=None, interleaved: bool = F
     the attention: the place in the sequence, or in its packed sample (``cu_seqlens``), or ``positions`` (int32, one per
     token; a token whose position is not in the table, e.g. -1 for padding, is copied). ``table``: see
     :func:`usp_rope_table`; its columns are the elements of a head that are rotated, in pairs (i, i + rot / 2), or
-    (2 i, 2 i + 1) with ``interleaved``. ``inverse`` rotates back. The outputs may be the inputs
-    (not tensors that require grad, unless in no_grad: :class:`UspRopeFunction` is what autograd records). Returns
-    (q_out, k_out)."""
+    (2 i, 2 i + 1) with ``interleaved``. ``inverse`` rotates back. The outputs may be the inputs (not tensors that
+    require grad, unless in no_grad: :class:`UspRopeFunction` is what autograd records). Returns (q_out, k_out)."""
     return _on_stream("usp_rope", q, stream, _abi.binding().rope, q, k, table, positions, cu_seqlens, interleaved, inverse,
                       q_out, k_out)
 
 
 class UspRopeFunction:
     """usp_rope as a differentiable op: (q, k) rotated; the gradients are rotated back, in one launch, and are
-    differentiable in turn. (k may be None. The op itself is in csrc/binding.cpp.) A backward pass that accumulates into
-    .grad can be captured into a graph only while no eager graph of the same leaves is held: torch keeps one accumulating
-    node per leaf, on the stream where it was made."""
+    differentiable in turn. (k may be None. The op itself is in csrc/binding.cpp.) The table has no gradient: one that
+    requires grad is refused. A backward pass that accumulates into .grad can be captured into a graph only while no eager
+    graph of the same leaves is held: torch keeps one accumulating node per leaf, on the stream where it was made."""
 
     @staticmethod
     def apply(q, k, table, positions=None, cu_seqlens=None, interleaved=False):

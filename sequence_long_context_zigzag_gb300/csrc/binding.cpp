@@ -462,8 +462,10 @@ PyObject *rope_grad(PyObject *const *a) {
     auto given = [&](int i, const char *name) {
         return a[i] == Py_None ? RopeFunction::Optional() : RopeFunction::Optional(tensor(a[i], name));
     };
+    const Tensor &table = tensor(a[2], "table");
+    if (at::GradMode::is_enabled() && table.requires_grad()) refuse("the rotation has no gradient for its table, which requires grad");
     try {
-        auto r = RopeFunction::apply(tensor(a[0], "q"), given(1, "k"), tensor(a[2], "table"), given(3, "positions"),
+        auto r = RopeFunction::apply(tensor(a[0], "q"), given(1, "k"), table, given(3, "positions"),
                                      given(4, "cu_seqlens"), (bool)truth(a[5]), false);
         Output qo, ko;
         qo.t = r[0];

@@ -74,6 +74,21 @@ def test_outputs_in_inference_mode():
     torch.cuda.synchronize()
 
 
+def test_a_table_that_wants_a_gradient_is_refused():
+    """The op has no gradient for its table: it is refused instead of left out."""
+    q, k = leaves()
+    f = (10000.0 ** (-torch.arange(0, HD, 2, device="cuda") / HD)).requires_grad_()
+    angle = torch.arange(L, device="cuda")[:, None] * f
+    table = torch.cat([angle.cos(), angle.sin()], 1)
+    for x, y in ((q, k), (q.detach(), None)):
+        with pytest.raises(ValueError, match="table"):
+            usp.UspRopeFunction.apply(x, y, table)
+    with torch.no_grad():
+        got = usp.UspRopeFunction.apply(q, k, table)
+    want = usp.UspRopeFunction.apply(q, k, table.detach())
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_k_out_without_k_leaves_q_alone():
     """Refused before anything is launched: a caller who mends the call and tries again rotates q once."""
     q = torch.randn(1, L, HQ, HD, device="cuda")
