@@ -2,8 +2,10 @@
 backward pass, and the kinds of differentiation that the op does not have."""
 import pytest
 import torch
+import torch.autograd.forward_ad as fwd
 
 import sequence_long_context_zigzag_gb300 as usp
+from q4_ref import rope_table, rotate
 
 pytestmark = pytest.mark.gpu
 HQ, HKV, HD, L = 4, 2, 64, 24
@@ -97,3 +99,40 @@ def test_k_out_without_k_leaves_q_alone():
         usp.usp_rope(q, None, usp.usp_rope_table(L, HD), q_out=q, k_out=torch.empty(1, L, HKV, HD, device="cuda"))
     torch.cuda.synchronize()
     assert torch.equal(q, before)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("both", [False, True])   # with cu_seqlens beside the positions, which then count
+def test_gradient_at_given_positions(dt, interleaved, both):
+    table = rope_table(L + 3, 48)
+    g = torch.Generator().manual_seed(2)
+    given = torch.randint(-2, L + 6, (1, L), generator=g, dtype=torch.int32)   # some of no row of the table
+    pos = torch.where((given < 0) | (given >= L + 3), -1, given).flatten()
+    cu = torch.tensor([0, 5, L], dtype=torch.int32, device="cuda") if both else None
+    q, k = leaves(dt)
+    up = [torch.randn_like(x, requires_grad=True) for x in (q, k)]
+    y = usp.UspRopeFunction.apply(q, k, table.cuda(), given.cuda(), cu, interleaved)
+    for a, x in zip(y, (q, k)):
+        assert torch.equal(a.flatten(0, 1), rotate(x.detach().flatten(0, 1), table, pos, interleaved)[0].to(dt))
+    d = torch.autograd.grad(y, (q, k), up, create_graph=True)
+    for a, x in zip(d, up):
+        assert torch.equal(a.flatten(0, 1), rotate(x.detach().flatten(0, 1), table, pos, interleaved, True)[0].to(dt))
+    # and their gradient in turn
+    w = [torch.randn_like(x) for x in (q, k)]
+    for a, x in zip(torch.autograd.grad(d, up, w), w):
+        assert torch.equal(a.flatten(0, 1), rotate(x.flatten(0, 1), table, pos, interleaved)[0].to(dt))
+
+
+def test_other_kinds_of_differentiation_are_refused():
+    """Forward mode and torch.func end in an error, never in a result without its derivative."""
+    table = usp.usp_rope_table(L, HD)
+    q, k = (x.detach() for x in leaves())
+    with fwd.dual_level():
+        dual = fwd.make_dual(q, torch.ones_like(q))
+        with pytest.raises(RuntimeError):
+            usp.UspRopeFunction.apply(dual, k, table)
+    with pytest.raises(RuntimeError):
+        torch.func.grad(lambda x: usp.UspRopeFunction.apply(x, k, table)[0].sum())(q)
+    with pytest.raises(RuntimeError):
+        torch.func.vmap(lambda x: usp.UspRopeFunction.apply(x, None, table)[0])(torch.stack([q, q]))
