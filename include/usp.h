@@ -467,8 +467,9 @@ typedef struct {
  * [cu_new[0], cu_new[nreq]) are left as they were. Cache rows behind kv_i may hold anything (NaN
  * among it); a request's own rows must be finite: a non-finite V row may reach queries that do not see
  * it (its weight is zero there, and 0 x NaN is NaN). A query row with a NaN gets NaN, it alone; one with an infinite value
- * too, or, where all its scores are -inf, what a row without a visible key gets. Partials over parts of a sequence (e.g. one ring rank's keys each) merge with usp_lse_merge. Requests may share
- * pages. out and lse must not overlap each other or the inputs.
+ * too, or, where all its scores are -inf, what a row without a visible key gets. Partials over parts of
+ * a sequence (e.g. one ring rank's keys each) merge with usp_lse_merge. Requests may share pages. out and
+ * lse must not overlap each other or the inputs.
  *   workspace : DEVICE buffer, 256-byte aligned, at least usp_paged_attn_workspace_size(d) bytes,
  *               clobbered; calls that share it must be ordered on one stream (two captured graphs
  *               that may run at the same time need one each). It needs no initialisation.

@@ -57,6 +57,11 @@ template <int HD, int NT, bool F32> struct Cfg {
     static constexpr int kCtas = F32 || NT >= 3 ? 2 : 3;  // per SM, as registers allow (24, 32 rows in three: 117, 146 us for 107, 133)
     static constexpr int kW = HD == 64 && NT == 1 && !F32 ? 4 : 2;  // 16-key steps per warp and tile
     static constexpr int kKT = 16 * kW * kWarps;          // keys per tile
+    // Tiles of a segment that O's accumulator takes, a piece, before it is added to a sum in the workspace: 512 products, kWide
+    // 1024. They cut their sum to fp32, by half a unit in the last place each on average, always towards zero; the sum of the pieces is
+    // rounded. (In one piece, a unit of 2^20 keys in one CTA was off by 0.35% with 8 rows and by 0.6% with 16, where bf16's half
+    // step is 0.4%. Pieces of 512 instead of 1024 cost 64 requests of 200000 keys with 16 rows 1.2%.) fp32 adds every tile.
+    static constexpr int kPiece = F32 ? 1 << 30 : kWide ? 1024 / (kKT / 16) : 512 / kW;
     // keys per CTA below which fewer CTAs work (one request of 8000 keys with kKT + 1, 64, 128, 320: 17.6, 13.7, 12.3, 12.4 us; four
     // of 2000 11.4, 11.2, 11.7, 11.7)
     static constexpr int kMinSpan = kKT + 128;
@@ -162,6 +167,17 @@ static __device__ __noinline__ bool wait_longer(uint32_t bar, uint32_t parity, i
     return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, status, USP_ERR_TIMEOUT, kWaitLimitNs));
 }
 
+// The state of a row that the pieces before left in this CTA's slot (m, l and O's N columns from col on) with that of the last
+// one (M, L, v).
+template <int N>
+__device__ __forceinline__ void add_piece(float m, float l, const float *o, float &M, float &L, float (&v)[N]) {
+    const float to = fmaxf(M, m), base = to == -INFINITY ? 0.f : to, now = tc::ex2(M - base), was = tc::ex2(m - base);
+    M = to;
+    L = fmaf(l, was, L * now);
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = fmaf(o[i], was, v[i] * now);
+}
+
 // The key of a step's 16 that is row k of the products (k < 8; row k + 8: 8 further). hd 128: the keys of K's 16-byte loads
 // that meet, rows (k, k + 1), and of V's 8-byte loads, rows (k, k + 2, k + 4, k + 6) with k even, then lie in different banks
 // of the swizzled lines; hd 64: rows (k, .., k + 3) of K's 8-byte loads and the same rows of V's 4-byte loads.
@@ -195,20 +211,8 @@ __device__ void producer(const FewParams &p, const SchedShared &sh, uint8_t *sme
     uint32_t fill = 0, nseg = 0;
     bool ok = true, more = true;
     while (more) {
-        Segment g;
+        Segment g{};
         more = sched_next<C::kKT>(p.s, sc, g);
-        if (!(ok = wait(C::SEG_EMPTY + nseg % kSegSlots, ((nseg / kSegSlots) & 1u) ^ 1u))) break;
-        if (lane == 0) {
-            SegMsg m{};
-            if (more) {
-                m.tok0 = g.tok0; m.ntok = g.ntok; m.head = g.head; m.req = g.req; m.p0 = g.p0; m.kv = g.kv;
-                m.t0 = g.t0; m.t1 = g.t1; m.tiles = g.tiles;
-            }
-            ring[nseg % kSegSlots] = m;
-            tc::mbar_arrive(BAR(C::SEG_FULL + nseg % kSegSlots));
-        }
-        ++nseg;
-        if (!more) break;
         const int32_t *row = p.table + (int64_t)g.req * p.table_stride;
         const int kv_head = (int)p.by_sub.div((uint32_t)g.head);
         // The next tile's page numbers are read a tile ahead and looked at only when that tile's stage is free. -1: behind the
@@ -218,30 +222,47 @@ __device__ void producer(const FewParams &p, const SchedShared &sh, uint8_t *sme
             return on && key < g.kv ? row[key >> p.log_ps] : -1;
         };
         const int mask = ps - 1, row0 = kv_head * ps;
-        int32_t raw = page_of(g.t0, pc * piece, loads), sraw = page_of(g.t0, skey, copies);
-        for (int t = g.t0; t < g.t1; ++t) {
-            const uint32_t st = fill % C::kStages;
-            if (!(ok = wait(C::EMPTY + st, ((fill / C::kStages) & 1u) ^ 1u))) break;
-            if (lane == 0) tc::mbar_arrive_expect_tx(BAR(C::FULL + st), 2 * C::kCodes);
-            __syncwarp();
-            // a page outside the cache: a box of zeros, and page 0's scales
-            const int32_t page = (uint32_t)raw < (uint32_t)p.num_pages ? raw : p.num_pages;
-            const int64_t spage = (uint32_t)sraw < (uint32_t)p.num_pages ? sraw : 0;
-            if (loads)
-                tma_load_3d(dst0 + st * 2 * C::kCodes, v ? &p.tv : &p.tk, 0,
-                            (row0 + ((t * C::kKT + pc * piece) & mask)) / (128 / C::kRow), page, BAR(C::FULL + st));
-            if (copies) {
-                const int at = (row0 + ((t * C::kKT + skey) & mask)) * C::kSRow;
-                const uint32_t dst = sbase + C::kSc + st * 2 * C::kScales + lane * 16;
-                copy16(dst, p.ks + spage * p.ks_page + at);
-                copy16(dst + C::kScales, p.vs + spage * p.vs_page + at);
+        int32_t raw = -1, sraw = -1;
+        if (more) raw = page_of(g.t0, pc * piece, loads), sraw = page_of(g.t0, skey, copies);
+        int t = g.t0;
+        do {  // a piece
+            const int t1 = min(g.t1, t + C::kPiece);
+            if (!(ok = wait(C::SEG_EMPTY + nseg % kSegSlots, ((nseg / kSegSlots) & 1u) ^ 1u))) break;
+            if (lane == 0) {
+                SegMsg m{};
+                if (more) {
+                    m.tok0 = g.tok0; m.ntok = g.ntok; m.head = g.head; m.req = g.req; m.p0 = g.p0; m.kv = g.kv;
+                    m.t0 = t; m.t1 = t1; m.tiles = g.tiles; m.first = g.t0;
+                }
+                ring[nseg % kSegSlots] = m;
+                tc::mbar_arrive(BAR(C::SEG_FULL + nseg % kSegSlots));
             }
-            copies_arrive(BAR(C::FULL + st));
-            raw = page_of(t + 1, pc * piece, loads);
-            sraw = page_of(t + 1, skey, copies);
-            ++fill;
-        }
-        if (!ok) break;
+            ++nseg;
+            if (!more) break;
+            for (; t < t1; ++t) {
+                const uint32_t st = fill % C::kStages;
+                if (!(ok = wait(C::EMPTY + st, ((fill / C::kStages) & 1u) ^ 1u))) break;
+                if (lane == 0) tc::mbar_arrive_expect_tx(BAR(C::FULL + st), 2 * C::kCodes);
+                __syncwarp();
+                // a page outside the cache: a box of zeros, and page 0's scales
+                const int32_t page = (uint32_t)raw < (uint32_t)p.num_pages ? raw : p.num_pages;
+                const int64_t spage = (uint32_t)sraw < (uint32_t)p.num_pages ? sraw : 0;
+                if (loads)
+                    tma_load_3d(dst0 + st * 2 * C::kCodes, v ? &p.tv : &p.tk, 0,
+                                (row0 + ((t * C::kKT + pc * piece) & mask)) / (128 / C::kRow), page, BAR(C::FULL + st));
+                if (copies) {
+                    const int at = (row0 + ((t * C::kKT + skey) & mask)) * C::kSRow;
+                    const uint32_t dst = sbase + C::kSc + st * 2 * C::kScales + lane * 16;
+                    copy16(dst, p.ks + spage * p.ks_page + at);
+                    copy16(dst + C::kScales, p.vs + spage * p.vs_page + at);
+                }
+                copies_arrive(BAR(C::FULL + st));
+                raw = page_of(t + 1, pc * piece, loads);
+                sraw = page_of(t + 1, skey, copies);
+                ++fill;
+            }
+        } while (ok && t < g.t1);
+        if (!ok || !more) break;
         if (g.t0 == 0 && g.t1 < g.tiles) opened = part_header(p.s, sh, sc, g);
     }
     if (!ok) {  // drain (bounded): no copy may land after the CTA has gone
@@ -568,8 +589,8 @@ template <int HD, int NT, bool F32> __device__ void consumer(const FewParams &p,
                                                                          o[n][i + 1][2 + e] * a);
             }
         consumers_sync();
-        const bool whole = s.t0 == 0 && s.t1 == s.tiles;
-        float *slot = part_slot(p.w, HD, blockIdx.x, s.t0 == 0 ? 1 : 0);
+        const bool whole = s.first == 0 && s.t1 == s.tiles;
+        float *slot = part_slot(p.w, HD, blockIdx.x, s.first == 0 ? 1 : 0);
         constexpr int kLanes = HD / 4, kAtOnce = kWarps * 32 / kLanes;  // threads of a row, 4 columns each
         const int col = tid % kLanes * 4;
         for (int r = tid / kLanes; r < rows; r += kAtOnce) {
@@ -584,6 +605,13 @@ template <int HD, int NT, bool F32> __device__ void consumer(const FewParams &p,
                 L = fmaf(x.y, tc::ex2(x.x - Mb), L);
                 const float4 f = *reinterpret_cast<const float4 *>(xch + (w * NT * 8 + r) * C::kXRow + col);
                 v.x += f.x; v.y += f.y; v.z += f.z; v.w += f.w;
+            }
+            if (!F32 && s.t0 != s.first) {
+                const float was_m = slot[(size_t)p.w.rows * HD + r], was_l = slot[(size_t)p.w.rows * (HD + 1) + r];
+                __syncwarp(kLanes == 32 ? 0xffffffffu : 0xffffu << (lane & 16));  // (the row's threads, one of which writes these anew)
+                float x[4] = {v.x, v.y, v.z, v.w};
+                add_piece(was_m, was_l, slot + (size_t)r * HD + col, M, L, x);
+                v = make_float4(x[0], x[1], x[2], x[3]);
             }
             uint32_t tok, h;
             p.s.by_G.divmod((uint32_t)r, tok, h);
@@ -867,8 +895,13 @@ template <int HD, int NT> __device__ void consumer_wide(const FewParams &p, uint
                 if (g == 0) wl[(warp * NT + n) * 8 + 2 * t + e] = l[n][e];
             }
         if (!consumers_all(ok) || s.ntok == 0) return;
-        const bool whole = s.t0 == 0 && s.t1 == s.tiles;
-        float *slot = part_slot(p.w, HD, blockIdx.x, s.t0 == 0 ? 1 : 0);
+        const bool whole = s.first == 0 && s.t1 == s.tiles;
+        float *slot = part_slot(p.w, HD, blockIdx.x, s.first == 0 ? 1 : 0);
+        const bool more = s.t0 != s.first;  // pieces before: their m and l, which warp 0 writes anew
+        if (more) {
+            for (int i = tid; i < 2 * p.w.rows; i += kWarps * 32) wm[i] = slot[(size_t)p.w.rows * HD + i];
+            consumers_sync();
+        }
         // the lane's columns after the exchange of even and odd ones with its neighbour: 2 kX in a row
         const int col = warp * (HD / 4) + (HD == 128 ? (g >> 1) * 8 + (g & 1) * 4 : (g >> 2) * 8 + (g >> 1 & 1) * 4 + (g & 1) * 2);
 #pragma unroll
@@ -889,6 +922,8 @@ template <int HD, int NT> __device__ void consumer_wide(const FewParams &p, uint
                     y[2 * j + 1] = g & 1 ? v[kX + j] : got;
                 }
                 if (r >= rows) continue;
+                float M = m[n][e];
+                if (more) add_piece(wm[r], wm[p.w.rows + r], slot + (size_t)r * HD + col, M, L, y);
                 uint32_t tok, h;
                 p.s.by_G.divmod((uint32_t)r, tok, h);
                 const int head = s.head * p.s.G + (int)h;
@@ -901,13 +936,13 @@ template <int HD, int NT> __device__ void consumer_wide(const FewParams &p, uint
                     if constexpr (kX == 2) *reinterpret_cast<uint2 *>(to) = make_uint2(z[0], z[1]);
                     else *reinterpret_cast<uint32_t *>(to) = z[0];
                     if (warp == 0 && g == 0)
-                        p.lse[(s.tok0 + tok) * p.hq + head] = L == 0.f ? -INFINITY : (m[n][e] + __log2f(L)) * kLn2;
+                        p.lse[(s.tok0 + tok) * p.hq + head] = L == 0.f ? -INFINITY : (M + __log2f(L)) * kLn2;
                 } else {
                     float *to = slot + (size_t)r * HD + col;
                     if constexpr (kX == 2) *reinterpret_cast<float4 *>(to) = make_float4(y[0], y[1], y[2], y[3]);
                     else *reinterpret_cast<float2 *>(to) = make_float2(y[0], y[1]);
                     if (warp == 0 && g == 0) {
-                        slot[(size_t)p.w.rows * HD + r] = m[n][e];
+                        slot[(size_t)p.w.rows * HD + r] = M;
                         slot[(size_t)p.w.rows * (HD + 1) + r] = L;
                     }
                 }

@@ -275,7 +275,8 @@ struct SegMsg {
     int32_t req, p0, kv, t0;
     int32_t t1, tiles;
     int32_t act[2], full[2];  // per tile of rows (paged_chunk.cu): key tiles needed; key tiles without a mask
-    int32_t split, pad;       // (paged_chunk.cu, Q4) both tiles of rows are the first one's, for alternate key tiles
+    int32_t split;            // (paged_chunk.cu, Q4) both tiles of rows are the first one's, for alternate key tiles
+    int32_t first;            // a segment in pieces [t0, t1): the first one's t0
 };
 static_assert(sizeof(SegMsg) == 64, "four 16-byte words");
 
