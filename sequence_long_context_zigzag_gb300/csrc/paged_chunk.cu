@@ -78,6 +78,11 @@ constexpr int kOver = 192;     // a unit's constant cost, in keys
 constexpr int kMinSpan = 448;  // keys per CTA below which fewer CTAs work
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr float kRescale = 8.0f;  // log2 units
+// Tiles of a segment that O takes in tensor memory, a piece, before it is added to a sum in the workspace (the slot that a cut
+// unit's part goes to). The products cut their sums to fp32, always towards zero; the sum of the pieces is rounded. (In one piece,
+// 2^20 keys of a unit in one CTA were off by 0.45%, over a 4-bit cache by 0.26%, where bf16's half step is 0.4%. 60 requests of
+// 300000 keys with 9 tokens each take 2% longer so, 64 tokens 1%.)
+constexpr int kPiece = 512;
 constexpr float kLn2 = 0.69314718055994531f;
 
 template <int HD, bool Q4> struct Cfg {
@@ -241,6 +246,32 @@ __device__ __forceinline__ bool next_segment(const ChunkParams &p, const SchedSh
     __syncwarp();
     if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar0 + 8u * (C::SEG_EMPTY + n % kSegSlots) + (never ? 8u : 0u));
     ++n;
+    return true;
+}
+
+// The next piece of a segment, for a warp of the softmax. n: twice the segments taken, and 1 in a segment with more pieces, whose
+// message stays where it is; the next piece begins at the last one's end, g.t1. (A register more, and long prompts over a 4-bit
+// cache take 3% longer.)
+template <int HD, bool Q4>
+__device__ __forceinline__ bool next_piece(const ChunkParams &p, const SchedShared &sh, uint32_t bar0, uint32_t &n, SegMsg &g) {
+    using C = Cfg<HD, Q4>;
+    const uint32_t at = n / 2 % kSegSlots;
+    bool ok = wait_segment(bar0 + 8u * (C::SEG_FULL + at), (n / (2 * kSegSlots)) & 1u, p.status, sh);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) return false;
+    bool never;
+    SegMsg x = read_segment(bar0 + (uint32_t)(C::kSeg - C::kBar) + at * (uint32_t)sizeof(SegMsg), never);
+    __syncwarp();
+    x.first = x.t0;
+    if (n & 1) x.t0 = g.t1;
+    if (x.t1 - x.t0 > kPiece) {
+        x.t1 = x.t0 + kPiece;
+        n |= 1;
+    } else {
+        if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar0 + 8u * (C::SEG_EMPTY + at) + (never ? 8u : 0u));
+        n = (n | 1) + 1;
+    }
+    g = x;
     return true;
 }
 
@@ -421,8 +452,8 @@ __device__ void mma_role(const ChunkParams &p, const SchedShared &sh, uint32_t s
     auto stage_off = [](uint32_t st) { return (uint64_t)((st * C::kTileBytes) >> 4); };
     const uint32_t tS = tmem + 128u * i, tO = tmem + 256u + (uint32_t)(HD * i);
     const int my_turn = C::TURN + i, other_turn = C::TURN + (1 - i);
-    // the current segment's tiles: kt of [., t1); this issuer's Q tile needs those below act_end
-    int kt = 0, t1 = 0, act_end = 0;
+    // the current segment's tiles: kt of [., end), in pieces of [., t1); this issuer's Q tile needs those below act_end
+    int kt = 0, t1 = 0, end = 0, act_end = 0;
     // a split segment (Q4): this issuer takes every other key tile, and the two go on without turns
     bool split = false, begun = false;
     int t0 = 0;  // the segment's first tile
@@ -440,24 +471,27 @@ __device__ void mma_role(const ChunkParams &p, const SchedShared &sh, uint32_t s
     uint32_t j = 0;                // tiles of all segments
     bool ok = true;
     for (;;) {
-        // The next segment with a tile. All that the softmax warps need of the one before is issued by now: one
+        // The next piece, or the next segment with a tile. All that the softmax warps need of the one before is issued by now: one
         // taken earlier, with segments without a tile between, would take the issuers up to a ring of segments
         // ahead of the softmax warps, which wait for the O of the last tile while the ring has no place for
         // the segment that the issuers wait for.
-        int ntok;
-        do {
-            SegMsg g;
-            if (!(ok = next_segment<HD, Q4>(p, sh, bar0, nseg, g))) break;
-            // (reductions over equal values: the compiler then knows that they are uniform)
-            ntok = __reduce_max_sync(0xffffffffu, g.ntok);
-            kt = t0 = __reduce_max_sync(0xffffffffu, g.t0);
-            t1 = __reduce_max_sync(0xffffffffu, g.t1);
-            act_end = __reduce_max_sync(0xffffffffu, i ? g.act[1] : g.act[0]);
-            if (Q4) split = __reduce_max_sync(0xffffffffu, g.split) != 0;
-        } while (ntok > 0 && kt >= t1);
-        if (!ok || ntok == 0) break;
-        if (!(ok = wait(C::Q_FULL, nq & 1u))) break;
-        ++nq;
+        if (kt >= end) {
+            int ntok;
+            do {
+                SegMsg g;
+                if (!(ok = next_segment<HD, Q4>(p, sh, bar0, nseg, g))) break;
+                // (reductions over equal values: the compiler then knows that they are uniform)
+                ntok = __reduce_max_sync(0xffffffffu, g.ntok);
+                kt = t0 = __reduce_max_sync(0xffffffffu, g.t0);
+                end = __reduce_max_sync(0xffffffffu, g.t1);
+                act_end = __reduce_max_sync(0xffffffffu, i ? g.act[1] : g.act[0]);
+                if (Q4) split = __reduce_max_sync(0xffffffffu, g.split) != 0;
+            } while (ntok > 0 && kt >= end);
+            if (!ok || ntok == 0) break;
+            if (!(ok = wait(C::Q_FULL, nq & 1u))) break;
+            ++nq;
+        }
+        t1 = min(end, kt + kPiece);
         if (!(ok = wait(C::K_FULL + j % C::kStages, (j / C::kStages) & 1u))) break;
         const bool first = !begun && !split;
         begun |= !split;
@@ -468,7 +502,7 @@ __device__ void mma_role(const ChunkParams &p, const SchedShared &sh, uint32_t s
             const bool act = acts(kt), last = kt + 1 >= t1;
             const uint32_t st = j % C::kStages, ph = (j / C::kStages) & 1u;
             const uint32_t stn = (j + 1) % C::kStages, phn = ((j + 1) / C::kStages) & 1u;
-            if (last) commit_if(el, BAR(C::Q_EMPTY));  // this issuer's S products of the segment are issued
+            if (last && t1 == end) commit_if(el, BAR(C::Q_EMPTY));  // this issuer's S products of the segment are issued
             if (!(ok = wait(C::V_FULL + st, ph))) break;
             if (!last && !(ok = wait(C::K_FULL + stn, phn))) break;
             if (act && !started && no > 0 && !(ok = wait(C::O_EMPTY + i, (no - 1) & 1u))) break;
@@ -651,8 +685,8 @@ __device__ void convert_role(const ChunkParams &p, const SchedShared &sh, uint32
     }
 }
 
-// One segment of the softmax of Q tile i; ns (S tiles), no (O read-outs) and nj (joined states) run on across segments. False after
-// a failed wait (the whole warp leaves; the others' waits end by the recorded status).
+// One piece of a segment of the softmax of Q tile i; ns (S tiles), no (O read-outs) and nj (joined states) run on across these.
+// False after a failed wait (the whole warp leaves; the others' waits end by the recorded status).
 template <int HD, bool Q4, bool kBox>  // kBox: whole warps of rows of out are stored as boxes
 __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegMsg &g, uint8_t *smem, uint32_t bar0,
                                                 uint32_t tmem, int i, uint32_t &ns, uint32_t &no, uint32_t &nj) {
@@ -768,12 +802,25 @@ __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegM
         ++ns;
     }
     if (!ok) return false;
-    // ---- end of the segment -----------------------------------------------------------------------
-    const bool whole = g.t0 == 0 && g.t1 == g.tiles;
+    // ---- end of the piece -------------------------------------------------------------------------
+    const bool whole = g.first == 0 && g.t1 == g.tiles, more = g.t0 != g.first;  // more: pieces before this one
     const int r = tile * p.tq_tokens * p.s.G + row;  // row of the unit
-    float *slot = part_slot(p.w, HD, blockIdx.x, g.t0 == 0 ? 1 : 0);
+    float *slot = part_slot(p.w, HD, blockIdx.x, g.first == 0 ? 1 : 0);
     const int head = g.head * p.s.G + (int)rh;
     __nv_bfloat16 *orow = p.out + (g.tok0 + tok) * p.out_stride + (int64_t)head * HD;
+    // What the slot holds of the pieces before (o is unwritten where they saw no key: then without weight)
+    float now = 1.f, was = 0.f;
+    if (more && (!split || i == 0)) {
+        const float m0 = slot[(size_t)p.w.rows * HD + r], l0 = slot[(size_t)p.w.rows * (HD + 1) + r], both = fmaxf(m, m0),
+                    base = both == -INFINITY ? 0.f : both;
+        now = tc::ex2(m - base);
+        was = tc::ex2(m0 - base);
+        l = fmaf(l0, was, l * now);
+        m = both;
+    }
+    auto before = [&](int at) {
+        return was > 0.f ? *reinterpret_cast<const float4 *>(slot + (size_t)r * HD + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
     // A split segment: the second tile's state to the scratch, column by column of four, so that a warp's lanes, a row each,
     // write and read whole lines; the first tile's threads scale both to the common maximum.
     float mine_by = 1.f, other_by = 0.f;
@@ -858,6 +905,23 @@ __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegM
             }
             __syncwarp();
         };
+        if (more) {
+#pragma unroll 1
+            for (int c = 0; c < HD / 32; ++c) {
+                uint32_t o[32];
+                tc::tmem_ld32(tO + c * 32, o);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float4 x = before(c * 32 + e * 4);
+                    const float y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int f = 0; f < 4; ++f) o[e * 4 + f] = __float_as_uint(fmaf(y[f], was, u2f(o[e * 4 + f]) * now));
+                }
+                tc::tmem_st32(tO + c * 32, o);
+            }
+            tc::tmem_st_wait();
+        }
         const bool box = kBox && whole && __all_sync(0xffffffffu, row_ok);
         if constexpr (kBox) {
             if (lane == 0) tma_stores_read();  // the unit before may have left one
@@ -920,7 +984,12 @@ __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegM
         if (lane == 0) tc::mbar_arrive(bar0 + 8u * (C::O_EMPTY + i));
         released();
     } else if (row_ok && whole) {
-        for (int e = 0; e < HD; e += 8) *reinterpret_cast<uint4 *>(orow + e) = make_uint4(0, 0, 0, 0);
+        for (int e = 0; e < HD; e += 4) {
+            const float4 x = before(e);
+            const float by = was * inv;
+            *reinterpret_cast<uint2 *>(orow + e) =
+                make_uint2(float2_to_bf16x2(x.x * by, x.y * by), float2_to_bf16x2(x.z * by, x.w * by));
+        }
     }
     if (row_ok) {
         if (whole) {
@@ -1016,8 +1085,8 @@ __global__ void __launch_bounds__(kThreads<Q4>, 1) paged_chunk_kernel(const __gr
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs<Q4>));
         uint32_t ns = 0, no = 0, nj = 0, nseg = 0;
-        SegMsg g;
-        while (!skip && next_segment<HD, Q4>(p, sh, bar0, nseg, g) && g.ntok > 0)
+        SegMsg g{};
+        while (!skip && next_piece<HD, Q4>(p, sh, bar0, nseg, g) && g.ntok > 0)
             if (!softmax_segment<HD, Q4, kBox>(p, g, smem, bar0, tmem, warp >> 2, ns, no, nj)) break;
         if (kBox && (threadIdx.x & 31) == 0) tma_stores_done();
     }
