@@ -640,7 +640,9 @@ def usp_rope_append(q, k, v, k_cache, v_cache, slot_map, table, cu_new=None, kv_
 def usp_cache_append_q4(k, v, k_cache, v_cache, k_scales, v_scales, slot_map, stream=None):
     """Quantise the rows of k and v (tokens, hkv, hd; bf16 or fp32) into their slots of a 4-bit cache: codes uint8
     (num_pages, hkv, page_size, hd / 2) and scales uint8 (num_pages, hkv, page_size, hd / 32), in place; the format is
-    described in include/usp.h. Values are off by half a step, at most 1 / 13 of their group's largest."""
+    described in include/usp.h. Values are off by half a step, at most 1 / 13 of their group's largest magnitude where that lies
+    between 7.5 * 2**-20 and 28800; in smaller groups by up to 2**-21 (a group of 4e-7 becomes zeros); larger values saturate
+    at 7 and -8 times 3840."""
     _on_stream("usp_cache_append_q4", k, stream, _abi.binding().rope_append, None, k, v, k_cache, v_cache, k_scales, v_scales,
                slot_map, None, None, None, None, False, None)
     return k_cache, v_cache, k_scales, v_scales
