@@ -474,7 +474,8 @@ typedef struct {
  *               clobbered; calls that share it must be ordered on one stream (two captured graphs
  *               that may run at the same time need one each). It needs no initialisation.
  * q, out, the caches 16-byte aligned. Arithmetic: fp32 softmax statistics and sums; bf16: products on
- * the tensor cores with the weights rounded to bf16; fp32: fp32 throughout. The result of a call does
+ * the tensor cores with the weights rounded to bf16, which cut their sums to fp32 towards zero (long ones are taken
+ * in pieces whose sum is rounded: below 2^-11 in all); fp32: fp32 throughout. The result of a call does
  * not depend on timing: the same inputs give the same bits.
  */
 USP_API int usp_paged_attn(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_table,
@@ -621,8 +622,8 @@ USP_API int usp_check(usp_stream_t stream);
  * fault: one CTA waits, through the same bounded mbarrier wait every kernel of this library uses, on
  * a barrier nothing ever arrives on, for at most limit_us microseconds. The wait runs out, the kernel
  * records USP_ERR_TIMEOUT in the device status word and returns; the context stays usable.
- * usp_check then reports USP_ERR_TIMEOUT and clears the word; the tensor-core (bf16) attention
- * kernels, the ones with device-side waits, do no work when launched while the word is set
+ * usp_check then reports USP_ERR_TIMEOUT and clears the word; the tensor-core attention kernels
+ * (bf16, and those over a 4-bit cache), the ones with device-side waits, do no work when launched while the word is set
  * (usp_check reports the timeout for them too).
  *   limit_us : 1 .. 1000000, else USP_ERR_INVALID_ARG.
  */
