@@ -474,8 +474,8 @@ typedef struct {
  *               clobbered; calls that share it must be ordered on one stream (two captured graphs
  *               that may run at the same time need one each). It needs no initialisation.
  * q, out, the caches 16-byte aligned. Arithmetic: fp32 softmax statistics and sums; bf16: products on
- * the tensor cores with the weights rounded to bf16, which cut their sums to fp32 towards zero (long ones are taken
- * in pieces whose sum is rounded: below 2^-11 in all); fp32: fp32 throughout. The result of a call does
+ * the tensor cores with the weights rounded to bf16, which cut their sums to fp32 towards zero (taken in pieces
+ * whose sum is rounded: below 2^-11 over 2^20 keys); fp32: fp32 throughout. The result of a call does
  * not depend on timing: the same inputs give the same bits.
  */
 USP_API int usp_paged_attn(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_table,
