@@ -148,8 +148,8 @@ struct ChunkParams {
     float *join;  // Q4: per CTA the state of a tile of rows: o in columns of four ([hd / 4][kM][4]), m, l
 };
 
-// Waits between the roles last a tile or two, those for a segment's place, message or end as long as the segments
-// before: a tile of 128 keys takes a CTA 1.1 to 1.5 us, so 2^31 keys would outlast any one limit. These waits may take
+// Waits between the roles last a tile or two, those for a segment's place, message, first scores or end as long as the
+// segments before: a tile of 128 keys takes a CTA 1.1 to 1.5 us, so 2^31 keys would outlast any one limit. These waits may take
 // ten times the time of the CTA's span.
 constexpr uint64_t kKeyLimitNs = 128;
 __device__ __forceinline__ bool wait_segment(uint32_t bar, uint32_t parity, int *status, const SchedShared &sh) {
@@ -688,7 +688,7 @@ __device__ void convert_role(const ChunkParams &p, const SchedShared &sh, uint32
 // One piece of a segment of the softmax of Q tile i; ns (S tiles), no (O read-outs) and nj (joined states) run on across these.
 // False after a failed wait (the whole warp leaves; the others' waits end by the recorded status).
 template <int HD, bool Q4, bool kBox>  // kBox: whole warps of rows of out are stored as boxes
-__device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegMsg &g, uint8_t *smem, uint32_t bar0,
+__device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SchedShared &sh, const SegMsg &g, uint8_t *smem, uint32_t bar0,
                                                 uint32_t tmem, int i, uint32_t &ns, uint32_t &no, uint32_t &nj) {
     using C = Cfg<HD, Q4>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wq = warp & 3;
@@ -710,7 +710,9 @@ __device__ __forceinline__ bool softmax_segment(const ChunkParams &p, const SegM
     const int act_end = min(g.t1, i ? g.act[1] : g.act[0]), full_end = i ? g.full[1] : g.full[0];
     for (int kt = split ? g.t0 + i : g.t0; kt < act_end; kt += split ? 2 : 1) {
         const bool full = kt < full_end;
-        ok = tc::mbar_wait(bar0 + 8u * (C::S_FULL + i), ns & 1u, p.status, USP_ERR_TIMEOUT, kWaitLimitNs);
+        // (over a bf16 cache this tile of rows may have skipped segments that the issuers are still in)
+        const uint32_t s_full = bar0 + 8u * (C::S_FULL + i);
+        ok = Q4 ? tc::mbar_wait(s_full, ns & 1u, p.status, USP_ERR_TIMEOUT, kWaitLimitNs) : wait_segment(s_full, ns & 1u, p.status, sh);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc::fence_after_sync();
@@ -1087,7 +1089,7 @@ __global__ void __launch_bounds__(kThreads<Q4>, 1) paged_chunk_kernel(const __gr
         uint32_t ns = 0, no = 0, nj = 0, nseg = 0;
         SegMsg g{};
         while (!skip && next_piece<HD, Q4>(p, sh, bar0, nseg, g) && g.ntok > 0)
-            if (!softmax_segment<HD, Q4, kBox>(p, g, smem, bar0, tmem, warp >> 2, ns, no, nj)) break;
+            if (!softmax_segment<HD, Q4, kBox>(p, sh, g, smem, bar0, tmem, warp >> 2, ns, no, nj)) break;
         if (kBox && (threadIdx.x & 31) == 0) tma_stores_done();
     }
     if (skip && threadIdx.x == 0) p.w.head[blockIdx.x] = no_part(sh);
